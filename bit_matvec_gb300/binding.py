@@ -28,6 +28,8 @@ TQ_ERR_CUDA = -4
 TQ_ERR_TIMEOUT = -5
 TQ_ERR_ALIAS = -6
 TQ_ERR_WORKSPACE = -7
+TQ_ERR_INDEX = -8
+TQ_ERR_TYPE = -9
 
 QK_K = 256
 GROUP = 128
@@ -37,6 +39,9 @@ Q8K_BYTES = 292
 TILE_ROWS = 32
 TILE_BYTES = 1088
 STATIC_WS_BYTES = 8 << 20   # TQ_STATIC_WS_BYTES: fixed workspace of tq_matmul_static_ws
+
+TQ_F32, TQ_F16, TQ_BF16 = 0, 1, 2
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_RAMP, ROPE_BANDS = range(5)
 
 _lock = threading.Lock()
 _lib = None
@@ -72,6 +77,7 @@ def _load():
                 "(python -m bit_matvec_gb300.build, or __graft_entry__.build())")
         lib = ctypes.CDLL(LIB_PATH)
         P, I64, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        F, D = ctypes.c_float, ctypes.c_double
         sig = {
             "tq_quantize_q8K": ([P, P, I64, I64, P], I),
             "tq_repacked_bytes": ([I64, I64], I64),
@@ -97,6 +103,14 @@ def _load():
             "tq_repack_ptq1_0_stream": ([P, P, I64, I64, P], I),
             "tq_matmul_ptq1_0_stream": ([P, P, P, I64, I64, I64, P], I),
             "tq_matmul_ptq1_0_stream_groupsums": ([P, P, P, I64, I64, I64, P], I),
+            "tq_rope_turns": ([I64, D, I, D, D, D, D, P, P], I),
+            "tq_qk_norm_rope": ([P, I64, P, I64, I, P, I64, P, I64, I, I64, I64, I64, I64, P, P,
+                                 F, P, P, P], I),
+            "tq_kv_append": ([P, I64, P, I64, P, I64, I, P, I64, P, P, P, I64, I64, P, P, F, P,
+                              P], I),
+            "tq_paged_attention": ([P, I64, P, P, P, P, I64, I, P, I64, I64, I64, I64, F, I64, P,
+                                    I64, P], I),
+            "tq_paged_attention_workspace_bytes": ([I64] * 8, I64),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -286,6 +300,173 @@ def tq_matmul_host(Wtq: torch.Tensor, X_host: torch.Tensor, X: torch.Tensor, Xq:
     _call("tq_matmul_host", Wtq.device, _ptr(Wtq), _host_ptr(X_host), _ptr(X), _ptr(Xq), _ptr(Y),
           _host_ptr(Y_host), rows, cols, ntok, _ptr(workspace), workspace.numel(),
           _stream(stream, Wtq.device))
+
+
+# ---------------------------------------------------------------- norm, rotation, cache, attention
+
+_TYPES = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+
+
+def _type(t: torch.Tensor) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TQError(TQ_ERR_TYPE, str(t.dtype))
+    return code
+
+
+def _heads(t: torch.Tensor):
+    """(address, token stride) of a [tokens][heads][head_dim] tensor whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    n, h, d = t.shape
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError("the heads of a token must be contiguous")
+    return t.data_ptr(), s[0] if n > 1 else h * d
+
+
+def _of(t: torch.Tensor, dtype, what: str):
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    return _ptr(t)
+
+
+class Rope:
+    """A rotation for tq_qk_norm_rope and tq_kv_append: turns is an int64 CUDA tensor of the
+    rot_dim/2 entries tq_rope_turns gives (the bits of its unsigned fractions)."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int64),
+                    ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+
+    def __init__(self, turns: torch.Tensor, interleaved: bool = False, amplitude: float = 1.0):
+        self.turns = turns   # kept alive: the struct holds its address
+        self.struct = Rope._Struct(_of(turns, torch.int64, "turns"), 2 * turns.numel(),
+                                   1 if interleaved else 0, amplitude)
+        self.ref = ctypes.addressof(self.struct)
+
+
+class PagedKV:
+    """A paged key/value cache: k and v of shape [pages][heads][page_size][head_dim], of any strides
+    but a unit last one (a [pages][page_size][heads][head_dim] cache is passed transposed), and
+    block_table int32 [sequences][pages of a sequence], whose rows may be longer than they are
+    wide here. The tensors are used in place: update block_table and the cache freely between
+    calls."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                    ("block_table", ctypes.c_void_p)] + [
+                        (n, ctypes.c_int64) for n in
+                        ("nseq", "table_width", "table_stride", "pages", "page_size", "heads",
+                         "head_dim", "page_stride", "head_stride", "slot_stride")] + [
+                        ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor):
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
+            raise ValueError("k and v must be alike: [pages][heads][page_size][head_dim]")
+        if not (k.is_cuda and v.is_cuda and block_table.is_cuda):
+            raise ValueError("tensor must live on a CUDA device")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("the last dimension must be contiguous")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or (
+                block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be int32 [sequences][pages] with contiguous rows")
+        self.k, self.v, self.block_table = k, v, block_table
+        nseq, width = block_table.shape
+        pages, heads, page_size, dim = k.shape
+        self.struct = PagedKV._Struct(
+            k.data_ptr(), v.data_ptr(), block_table.data_ptr(), nseq, width,
+            block_table.stride(0) if nseq > 1 else width, pages, page_size, heads, dim,
+            k.stride(0), k.stride(1), k.stride(2), _type(k), 0)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def tq_rope_turns(rot_dim: int, base: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
+                  original_len: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """(turns, amplitude): the int64 CPU tensor that Rope takes (moved to the GPU), for a plain or a
+    long-context rotation."""
+    turns = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
+    amplitude = ctypes.c_float()
+    rc = _load().tq_rope_turns(rot_dim, base, kind, factor, original_len, low, high,
+                               turns.data_ptr(), ctypes.addressof(amplitude))
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_rope_turns")
+    return turns, amplitude.value
+
+
+def tq_qk_norm_rope(Xq, Xk, Yq, Yk, positions=None, rope: Rope | None = None, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, stream=None):
+    """Norm and rotation of the heads of Xq and Xk [tokens][heads][head_dim] (views of a fused
+    projection's rows are fine) into Yq and Yk; Xk and Yk may be None."""
+    ntok, q_heads, dim = Xq.shape
+    k_heads = 0 if Xk is None else Xk.shape[1]
+    if Yq.shape != Xq.shape or (k_heads and (Xk.shape != (ntok, k_heads, dim) or
+                                             Yk.shape != Xk.shape)):
+        raise TQError(TQ_ERR_SHAPE, "tq_qk_norm_rope")
+    if k_heads and (Xk.dtype != Xq.dtype or Yk.dtype != Yq.dtype):
+        raise TQError(TQ_ERR_TYPE, "tq_qk_norm_rope")
+    _check_rows("tq_qk_norm_rope", dim, ntok, q_weight, k_weight, positions)
+    xk, yk = (_heads(Xk), _heads(Yk)) if k_heads else ((None, 0), (None, 0))
+    _call("tq_qk_norm_rope", Xq.device, *_heads(Xq), *xk, _type(Xq), *_heads(Yq), *yk, _type(Yq),
+          ntok, q_heads, k_heads, dim, _ptr(q_weight), _ptr(k_weight), eps,
+          None if rope is None else rope.ref, _ptr(positions), _stream(stream, Xq.device))
+
+
+def tq_kv_append(Xq, Xk, Xv, Yq, kv: PagedKV, seq_ids, positions, rope: Rope | None = None,
+                 q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
+    """The same, with the keys and the values Xv written to kv at positions[t] of sequence
+    seq_ids[t]; Yq is of the cache's type. Xq and Yq may be None."""
+    st = kv.struct
+    ntok = Xk.shape[0]
+    q_heads = 0 if Xq is None else Xq.shape[1]
+    kshape = (ntok, st.heads, st.head_dim)
+    if Xk.shape != kshape or Xv.shape != kshape or (
+            q_heads and (Xq.shape != (ntok, q_heads, st.head_dim) or Yq.shape != Xq.shape)):
+        raise TQError(TQ_ERR_SHAPE, "tq_kv_append")
+    if Xv.dtype != Xk.dtype or (q_heads and (Xq.dtype != Xk.dtype or Yq.dtype != kv.k.dtype)):
+        raise TQError(TQ_ERR_TYPE, "tq_kv_append")
+    _check_rows("tq_kv_append", st.head_dim, ntok, q_weight, k_weight, positions, seq_ids)
+    xq, yq = (_heads(Xq), _heads(Yq)) if q_heads else ((None, 0), (None, 0))
+    _call("tq_kv_append", Xk.device, *xq, *_heads(Xk), *_heads(Xv), _type(Xk), *yq, kv.ref,
+          _ptr(seq_ids), _ptr(positions), ntok, q_heads, _ptr(q_weight), _ptr(k_weight), eps,
+          None if rope is None else rope.ref, _stream(stream, Xk.device))
+
+
+def _check_rows(where, dim, ntok, q_weight, k_weight, *per_token):
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.numel() != dim):
+            raise TQError(TQ_ERR_SHAPE, where + ": a weight is float32 [head_dim]")
+    for t in per_token:
+        if t is not None and (t.dtype != torch.int32 or t.numel() != ntok):
+            raise TQError(TQ_ERR_SHAPE, where + ": positions and seq_ids are int32 [tokens]")
+
+
+def tq_paged_attention_workspace_bytes(nseq: int, ntok: int, q_heads: int, kv_heads: int,
+                                       head_dim: int, max_q: int, max_kv: int,
+                                       window: int = 0) -> int:
+    n = _load().tq_paged_attention_workspace_bytes(nseq, ntok, q_heads, kv_heads, head_dim, max_q,
+                                                   max_kv, window)
+    if n < 0:
+        raise TQError(TQ_ERR_SHAPE, "tq_paged_attention_workspace_bytes")
+    return int(n)
+
+
+def tq_paged_attention(Q, kv: PagedKV, q_start, kv_len, O, max_q: int, max_kv: int, scale: float,
+                       workspace=None, window: int = 0, lse=None, stream=None):
+    """Causal attention of the new tokens Q [tokens][q_heads][head_dim], those of sequence b at
+    q_start[b] .. q_start[b+1] - 1 and last of its kv_len[b] positions, over kv; O of any type."""
+    st = kv.struct
+    ntok, q_heads, dim = Q.shape
+    if dim != st.head_dim or O.shape != Q.shape or q_start.numel() != st.nseq + 1 or \
+            kv_len.numel() != st.nseq or (lse is not None and lse.shape != (ntok, q_heads)):
+        raise TQError(TQ_ERR_SHAPE, "tq_paged_attention")
+    if Q.dtype != kv.k.dtype or q_start.dtype != torch.int32 or kv_len.dtype != torch.int32 or (
+            lse is not None and lse.dtype != torch.float32):
+        raise TQError(TQ_ERR_TYPE, "tq_paged_attention")
+    _call("tq_paged_attention", Q.device, *_heads(Q), kv.ref, _ptr(q_start), _ptr(kv_len),
+          *_heads(O), _type(O), _ptr(lse), ntok, q_heads, max_q, max_kv, scale, window,
+          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+          _stream(stream, Q.device))
 
 
 def tq_strerror(code: int) -> str:

@@ -8,6 +8,7 @@
 #include <unordered_map>
 #include <utility>
 
+#include "tq_attn.cuh"
 #include "tq_internal.cuh"
 
 namespace tq {
@@ -302,6 +303,9 @@ int matmul_impl(const void* Wtq, const void* Xq, float* Y, int32_t* S, int64_t r
 }  // namespace
 
 void record_cuda_error(cudaError_t e) { g_last_cuda_error = (int)e; }
+
+void note_other_kernel(cudaStream_t s) { note_op(s, kOpOther); }
+cudaError_t status_word(int** out) { return device_status_ptr(out); }
 
 int ws_gemv_max_tokens() { return kWsGemvMaxTok; }
 
@@ -660,13 +664,15 @@ int tq_matmul_host(const void* Wtq, const float* X_host, float* X, void* Xq, flo
 const char* tq_strerror(int code) {
   switch (code) {
     case TQ_OK: return "ok";
-    case TQ_ERR_SHAPE: return "bad shape (cols must be a multiple of 256, sizes >= 0)";
+    case TQ_ERR_SHAPE: return "bad shape (a size is negative or not a multiple the call asks for, as cols of 256)";
     case TQ_ERR_NULL: return "null pointer";
     case TQ_ERR_ALIGN: return "misaligned buffer";
     case TQ_ERR_CUDA: return "CUDA error (see tq_last_cuda_error)";
     case TQ_ERR_TIMEOUT: return "a kernel gave up a bounded wait";
     case TQ_ERR_ALIAS: return "output buffer overlaps an input";
     case TQ_ERR_WORKSPACE: return "workspace smaller than tq_matmul_workspace_bytes";
+    case TQ_ERR_INDEX: return "a kernel met a page, sequence or length out of range";
+    case TQ_ERR_TYPE: return "element type not taken by this call";
     default: return "unknown error";
   }
 }
@@ -685,7 +691,7 @@ int tq_device_status(void) {
     e = cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return fail_cuda(e);
   }
-  return v == kDevTimeout ? TQ_ERR_TIMEOUT : TQ_OK;
+  return v == kDevTimeout ? TQ_ERR_TIMEOUT : v == kDevIndex ? TQ_ERR_INDEX : TQ_OK;
 }
 
 int tq_probe_read_sum(const void* buf, int64_t bytes, uint32_t* out, int early, void* stream) {

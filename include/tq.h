@@ -47,6 +47,8 @@ extern "C" {
 #define TQ_ERR_TIMEOUT  -5  /* a kernel gave up a bounded wait (tq_device_status) */
 #define TQ_ERR_ALIAS    -6  /* an output buffer overlaps an input buffer */
 #define TQ_ERR_WORKSPACE -7 /* workspace smaller than tq_matmul_workspace_bytes */
+#define TQ_ERR_INDEX    -8  /* a kernel met a page, sequence or length out of range */
+#define TQ_ERR_TYPE     -9  /* an element type this call does not take */
 
 #define TQ_QK_K 256          /* activations per q8_K block */
 #define TQ_GROUP 128         /* weights per pq2_0 scale */
@@ -383,6 +385,167 @@ int tq_matmul_host(const void *Wtq, const float *X_host, float *X, void *Xq, flo
  */
 int tq_matmul_static_ws(const void *Wtq, const void *Xq, float *Y, int64_t rows, int64_t cols,
                         int64_t ntok, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Between the query/key/value product and the output product of a block:
+ * norm and rotation of the heads, the paged key/value cache, attention.
+ *
+ * Element types of the buffers marked "typed". Sums, norms, angles, softmax
+ * statistics and accumulators are 32-bit floats whatever the types.
+ */
+#define TQ_F32  0
+#define TQ_F16  1
+#define TQ_BF16 2
+
+/*
+ * Rotary position: the first rot_dim values of a head are rotated in pairs by
+ * the angle position * f_i, pair i = 0 .. rot_dim/2 - 1; the others pass.
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * Pair i is values (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved.
+ * The frequencies are given as 64-bit fractions of a turn per position,
+ * turns[i] = round(2^64 * f_i / 2 pi): the product with an integer position
+ * wraps at whole turns, so the angle is exact to 2^-24 of a turn at every
+ * position, where position * f_i in 32 bits is off by position * 2^-24.
+ */
+typedef struct {
+    const uint64_t *turns; /* device, [rot_dim / 2], 8-byte aligned */
+    int64_t rot_dim;       /* even, 0 (no rotation) .. head_dim */
+    int32_t interleaved;   /* 0: pairs (i, i + rot_dim/2); else (2i, 2i + 1) */
+    float amplitude;       /* factor of the rotated values (1 for plain rotation) */
+} tq_rope;
+
+#define TQ_ROPE_PLAIN  0  /* f_i = base^(-2i / rot_dim) */
+#define TQ_ROPE_LINEAR 1  /* f_i / factor: positions compressed */
+#define TQ_ROPE_BASE   2  /* base * factor^(rot_dim / (rot_dim - 2)) as the base */
+#define TQ_ROPE_RAMP   3  /* low frequencies divided by factor, high ones kept, a
+                             ramp over the pair index between; amplitude 0.1 ln(factor) + 1 */
+#define TQ_ROPE_BANDS  4  /* the same with a ramp over the frequency; amplitude 1 */
+
+/*
+ * tq_rope_turns -- turns (HOST memory, [rot_dim / 2]) and amplitude (HOST, may
+ * be NULL) of a rotation, for contexts `factor` times original_len. The number
+ * of turns that pair i makes over original_len positions is
+ * n_i = original_len f_i / 2 pi; with the bounds low < high:
+ *   RAMP:  pairs of n_i >= high are kept, of n_i <= low divided by factor;
+ *          between, linear in i from floor(i at n = high), at least 0, to
+ *          ceil(i at n = low), at most rot_dim - 1.
+ *   BANDS: the share kept is clamp((n_i - low) / (high - low), 0, 1).
+ * Host only; enqueues nothing. Errors: TQ_ERR_SHAPE for an odd or negative
+ * rot_dim, base <= 0, factor < 1, an unknown kind, or (RAMP, BANDS)
+ * original_len <= 0 or low >= high or low <= 0, or (BASE) rot_dim == 2.
+ */
+int tq_rope_turns(int64_t rot_dim, double base, int kind, double factor, double original_len,
+                  double low, double high, uint64_t *turns, float *amplitude);
+
+/*
+ * A paged key/value cache: pages of page_size token slots, and for each
+ * sequence a row of the block table with the page of each run of page_size
+ * positions. Position p of sequence b, key/value head h is at
+ *   k + page * page_stride + h * head_stride + (p % page_size) * slot_stride
+ * (elements, and alike for v), page = block_table[b * table_stride + p / page_size].
+ * Any order of pages, heads and slots is a choice of strides.
+ */
+typedef struct {
+    void *k;                     /* device, typed, 16-byte aligned */
+    void *v;                     /* device, typed, 16-byte aligned, same strides */
+    const int32_t *block_table;  /* device, [nseq][table_width], row stride table_stride */
+    int64_t nseq, table_width, table_stride;
+    int64_t pages;               /* pages of the cache */
+    int64_t page_size;           /* slots of a page: a multiple of 8 */
+    int64_t heads;               /* key/value heads */
+    int64_t head_dim;            /* a multiple of 8, at most 128 */
+    int64_t page_stride, head_stride, slot_stride;  /* elements, multiples of 8 */
+    int32_t type;                /* TQ_F16 or TQ_BF16 */
+    int32_t reserved;            /* 0 */
+} tq_paged_kv;
+
+/*
+ * tq_qk_norm_rope -- queries and keys of each token: RMS norm of each head,
+ * x * w / sqrt(mean(x^2) + eps), then the rotation, in one pass.
+ *   Xq, Xk  typed x_type: head h of token t starts at X + t * x_stride + h * head_dim
+ *           (strides in elements; the rows of a fused projection are taken as
+ *           they are).
+ *   Yq, Yk  typed y_type, laid out alike with their own strides; Y may be X
+ *           (same pointer, stride and type), but must not overlap it otherwise.
+ *   q_weight, k_weight  f32 [head_dim], 4-byte aligned; NULL: no norm.
+ *   rope        HOST struct; NULL or rot_dim 0: no rotation.
+ *   positions   int32 [ntok], any value; may be NULL without rotation.
+ * head_dim: even, at most 256. q_heads or k_heads may be 0.
+ * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN (a pointer not
+ * aligned to its element), TQ_ERR_ALIAS.
+ */
+int tq_qk_norm_rope(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_stride,
+                    int x_type, void *Yq, int64_t yq_stride, void *Yk, int64_t yk_stride,
+                    int y_type, int64_t ntok, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                    const float *q_weight, const float *k_weight, float eps, const tq_rope *rope,
+                    const int32_t *positions, void *stream);
+
+/*
+ * tq_kv_append -- the same for queries and keys, with the keys and the (plain)
+ * values written to the cache, in the cache's type: token t to position
+ * positions[t] of sequence seq_ids[t].
+ *   Xq, Xk, Xv, strides, weights, rope: as tq_qk_norm_rope; Xk and Xv hold
+ *           kv->heads heads of kv->head_dim.
+ *   Yq      typed kv->type, [ntok][q_heads][head_dim] with stride yq_stride.
+ *           q_heads may be 0 (keys and values only; Xq and Yq unused).
+ *   seq_ids, positions  int32 [ntok]. A token of negative position is padding:
+ *           nothing of it is written.
+ * Two tokens of one call must not have the same sequence and position. A
+ * token whose sequence, position or page is outside the table or the cache is
+ * not written to it, and tq_device_status() then returns TQ_ERR_INDEX.
+ * Errors: as tq_qk_norm_rope, and those of the cache's description.
+ */
+int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_stride,
+                 const void *Xv, int64_t xv_stride, int x_type, void *Yq, int64_t yq_stride,
+                 const tq_paged_kv *kv, const int32_t *seq_ids, const int32_t *positions,
+                 int64_t ntok, int64_t q_heads, const float *q_weight, const float *k_weight,
+                 float eps, const tq_rope *rope, void *stream);
+
+/*
+ * tq_paged_attention -- causal attention of each sequence's new tokens over
+ * its cached keys and values, from single tokens (decode) to long chunks
+ * (prefill), the new tokens' own keys and values already in the cache.
+ * Sequence b has the tokens q_start[b] .. q_start[b+1] - 1 of Q, the last of
+ * its kv_len[b] positions: token i of the sequence's n is at position
+ * p = kv_len[b] - n + i and sees the positions j <= p, with window > 0 only
+ * those > p - window. Query head h reads key/value head h / (q_heads / heads).
+ *   o = sum_j exp(s_j) v_j / sum_j exp(s_j),  s_j = scale * q . k_j
+ * A token that sees nothing (p < 0) gets zeros, and minus infinity as its lse.
+ *   Q   typed kv->type, head h of token t at Q + t * q_stride + h * head_dim;
+ *       16-byte aligned, q_stride a multiple of 8.
+ *   q_start int32 [nseq + 1], from 0, non-decreasing, at most ntok; kv_len int32 [nseq].
+ *   O   typed o_type, [ntok][q_heads][head_dim] with stride o_stride; rows of
+ *       tokens from q_start[nseq] on are not written.
+ *   lse f32 [ntok][q_heads]: log of the sum of exp(s_j); NULL: not written.
+ *   max_q, max_kv  upper bounds of the new tokens and of kv_len of any
+ *       sequence, which choose kernels and splits. A sequence of more than
+ *       max_q new tokens, a kv_len beyond the table or a visible position
+ *       whose page is outside the cache gives TQ_ERR_INDEX in
+ *       tq_device_status(), and the sequence's rows are undefined; a kv_len
+ *       beyond max_kv only costs speed.
+ *   workspace  tq_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
+ *       contents overwritten and meaningless after the call; calls that share
+ *       it must be ordered.
+ * The weights exp(s_j) are rounded to the cache's type for their product with
+ * the values; everything else is 32-bit. Slots that no new token sees (past
+ * kv_len, or before the window) may hold anything, NaN included, and their
+ * pages are not read. Keys and values that some token of the sequence sees
+ * must be finite.
+ * Errors: TQ_ERR_SHAPE (also q_heads not a multiple of kv->heads, scale not
+ * finite, window < 0), TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
+ * TQ_ERR_WORKSPACE.
+ */
+int tq_paged_attention(const void *Q, int64_t q_stride, const tq_paged_kv *kv,
+                       const int32_t *q_start, const int32_t *kv_len, void *O, int64_t o_stride,
+                       int o_type, float *lse, int64_t ntok, int64_t q_heads, int64_t max_q,
+                       int64_t max_kv, float scale, int64_t window, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Scratch of tq_paged_attention: partial results where the keys are split over
+ * thread blocks. A function of the sizes alone; -1 for sizes it refuses. */
+int64_t tq_paged_attention_workspace_bytes(int64_t nseq, int64_t ntok, int64_t q_heads,
+                                           int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                                           int64_t max_kv, int64_t window);
 
 /* Human-readable name of a TQ_* code. */
 const char *tq_strerror(int code);

@@ -1,0 +1,291 @@
+"""Paged attention on the GPU against the 64-bit form: single tokens to long chunks, ragged batches,
+shared heads, windows, rows that see nothing, pages that end inside tiles, strides, splits."""
+import math
+
+import pytest
+import torch
+
+from attn_util import assert_within, attention
+
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def tq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_matvec_gb300 import build
+    build.build()
+    import bit_matvec_gb300
+    yield bit_matvec_gb300
+    assert bit_matvec_gb300.tq_device_status() == bit_matvec_gb300.TQ_OK
+
+
+def problem(lens, hq, hk, dim, page, dtype, seed=0, order="hnd", peak=2.0, poison=True, window=0):
+    """Inputs on the CPU and the GPU for sequences of (total, new) tokens. Every slot that no new
+    token sees holds NaN, and table entries of pages no token sees are out of range."""
+    g = torch.Generator().manual_seed(seed + 31 * len(lens) + dim)
+    need = [-(-n // page) for n, _ in lens]
+    pages = sum(need) + 3
+    perm = torch.randperm(pages, generator=g).tolist()
+    table = torch.full((len(lens), max(need + [1]) + 2), -1, dtype=torch.int32)
+    k = torch.randn(pages, hk, page, dim, generator=g).to(dtype)
+    v = torch.randn(pages, hk, page, dim, generator=g).to(dtype)
+    seen = torch.zeros(pages, page, dtype=torch.bool)
+    for b, (n, q) in enumerate(lens):
+        lo = max(0, n - q - window + 1) if window else 0
+        for i in range(need[b]):
+            table[b, i] = perm.pop()
+            at = i * page
+            seen[table[b, i], max(0, lo - at):max(0, n - at)] = q > 0
+            if at + page <= lo:
+                table[b, i] = 10**8    # a page before the window: freed
+    if poison:
+        for c in (k, v):
+            c.transpose(1, 2)[~seen] = float("nan")
+    ntok = sum(q for _, q in lens)
+    Q = (torch.randn(ntok, hq, dim, generator=g) * peak).to(dtype)
+    q_start = torch.tensor([0] + [q for _, q in lens], dtype=torch.int32).cumsum(0).to(torch.int32)
+    kv_len = torch.tensor([n for n, _ in lens], dtype=torch.int32)
+    kd, vd = k.cuda(), v.cuda()
+    if order == "nhd":
+        kd, vd = (c.transpose(1, 2).contiguous().transpose(1, 2) for c in (kd, vd))
+    elif order == "both":
+        both = torch.stack([kd, vd], 1)
+        kd, vd = both[:, 0], both[:, 1]
+    return Q, k, v, table, q_start, kv_len, kd, vd
+
+
+def call(tq, prob, out, window=0, scale=None, max_q=None, max_kv=None, lse=True):
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    ntok, hq, dim = Q.shape
+    nseq = len(kv_len)
+    mq = max_q if max_q is not None else int((q_start[1:] - q_start[:-1]).max())
+    mk = max_kv if max_kv is not None else int(kv_len.max())
+    O = torch.full((ntok, hq, dim), float("nan"), dtype=out, device="cuda")
+    L = torch.full((ntok, hq), float("nan"), device="cuda") if lse else None
+    need = tq.tq_paged_attention_workspace_bytes(nseq, ntok, hq, k.shape[1], dim, mq, mk, window)
+    ws = torch.full((max(need, 16),), 0xA5, dtype=torch.uint8, device="cuda")
+    tq.tq_paged_attention(Q.cuda(), tq.PagedKV(kd, vd, table.cuda()), q_start.cuda(), kv_len.cuda(),
+                          O, mq, mk, scale if scale is not None else dim ** -0.5, ws, window, L)
+    return O, L
+
+
+def check(tq, prob, out, window=0, **kw):
+    Q, k, v, table, q_start, kv_len, _, _ = prob
+    scale = kw.get("scale", Q.shape[2] ** -0.5)
+    o, lse, tol, tol_lse = attention(Q, k, v, table, q_start, kv_len, scale, window, out)
+    O, L = call(tq, prob, out, window, **kw)
+    assert_within(O, o, tol, "o")
+    L = L.double().cpu()
+    none = torch.isinf(lse)
+    assert torch.equal(L[none], lse[none])
+    assert (O.cpu()[none] == 0).all()
+    assert_within(L[~none], lse[~none], tol_lse[~none], "lse")
+    return O
+
+
+CASES = [
+    # (total, new) of each sequence, q heads, kv heads, dim, page, type, out, window, order
+    ([(1, 1)], 1, 1, 128, 16, F16, F16, 0, "hnd"),
+    ([(333, 1)], 40, 40, 128, 16, F16, F16, 0, "hnd"),
+    ([(64, 1), (65, 1), (1, 1), (63, 1), (129, 1)], 10, 2, 128, 16, BF16, BF16, 0, "nhd"),
+    ([(5000, 1)], 8, 1, 128, 64, BF16, F32, 0, "hnd"),
+    ([(5000, 1), (17, 1), (2500, 1)], 6, 2, 64, 32, F16, F32, 0, "both"),
+    ([(700, 5), (0, 0), (5, 5), (90, 1)], 8, 4, 64, 8, F16, F16, 0, "hnd"),
+    ([(400, 5), (31, 5), (300, 3)], 15, 3, 80, 48, BF16, BF16, 100, "nhd"),
+    ([(3000, 1), (20, 1)], 8, 2, 96, 24, F16, F16, 256, "hnd"),
+    ([(3000, 7)], 4, 4, 128, 256, BF16, BF16, 1, "hnd"),
+    ([(17, 17)], 2, 2, 8, 8, F16, F32, 0, "hnd"),
+    ([(40, 40), (33, 2)], 3, 1, 40, 16, BF16, BF16, 7, "hnd"),
+    ([(300, 300)], 5, 1, 128, 16, BF16, BF16, 0, "hnd"),
+    ([(513, 200), (100, 100), (1, 1)], 4, 2, 128, 32, F16, F16, 0, "nhd"),
+    ([(1500, 129), (140, 128)], 8, 8, 64, 64, BF16, BF16, 64, "both"),
+    ([(900, 260), (2100, 1), (64, 64)], 12, 4, 96, 48, BF16, F32, 0, "hnd"),
+    ([(700, 333)], 16, 2, 80, 40, F16, F16, 500, "hnd"),
+    ([(4100, 40)], 8, 2, 128, 128, BF16, BF16, 0, "hnd"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attention(tq, case):
+    lens, hq, hk, dim, page, dtype, out, window, order = case
+    check(tq, problem(lens, hq, hk, dim, page, dtype, order=order, window=window), out, window)
+
+
+@pytest.mark.parametrize("new", [1, 3, 300])
+def test_tokens_that_see_nothing(tq, new):
+    """A kv_len below the number of new tokens: the first ones stand before position 0."""
+    prob = problem([(50, 50), (40, 40)], 4, 2, 64, 16, F16)
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    g = torch.Generator().manual_seed(1)
+    Q = torch.randn(new + 2, 4, 64, generator=g).to(F16)
+    q_start, kv_len = torch.tensor([0, new, new + 2]).int(), torch.tensor([new // 2, 40]).int()
+    if new // 2 > 50:
+        prob = problem([(150, 150), (40, 40)], 4, 2, 64, 16, F16)
+        k, v, table, kd, vd = prob[1], prob[2], prob[3], prob[6], prob[7]
+    check(tq, (Q, k, v, table, q_start, kv_len, kd, vd), F32)
+
+
+def test_rows_past_the_last_sequence_are_not_written(tq):
+    for n, max_q in ((200, 1), (40, 300)):    # one split or several, both kernels
+        prob = list(problem([(n, 1), (n, 2)], 4, 2, 64, 16, F16))
+        prob[0] = torch.cat([prob[0], prob[0]])
+        O, L = call(tq, tuple(prob), F16, max_q=max(max_q, 2), max_kv=100 * n)
+        assert torch.isnan(O[3:]).all() and torch.isnan(L[3:]).all()
+        assert not torch.isnan(O[:3]).any()
+
+
+@pytest.mark.parametrize("new", [1, 40, 300])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_large_scores(tq, new, dtype):
+    """Scores of hundreds, growing and falling along the keys: the running maximum moves every tile,
+    and weights far below it vanish without a NaN."""
+    prob = problem([(1300, new)], 4, 1, 128, 16, dtype, poison=False)
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    up = torch.linspace(0.2, 4.0, 1300).to(dtype)
+    for j in range(1300):
+        k[table[0, j // 16], 0, j % 16] = up[j if new != 40 else 1299 - j] * (1 if j % 7 else -1)
+    Q = (torch.ones_like(Q) * (torch.arange(4)[None, :, None] - 1.5)).to(dtype)
+    check(tq, (Q, k, v, table, q_start, kv_len, k.cuda(), v.cuda()), F32)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.7, 3.0])
+def test_scale(tq, scale):
+    for new in (2, 200):
+        check(tq, problem([(400, new)], 4, 2, 64, 16, F16, peak=1.0), F32, scale=scale)
+
+
+def test_constant_values_come_back(tq):
+    """With every value 1 the output is the sum of the weights over itself, whatever the scores."""
+    for new in (1, 150):
+        prob = problem([(1000, new)], 8, 2, 128, 16, BF16, poison=False)
+        Q, k, v, table, q_start, kv_len, kd, vd = prob
+        vd.fill_(1.0)
+        O, _ = call(tq, prob, F32)
+        assert (O - 1).abs().max().item() <= 2.0**-8 + 2.0**-12
+
+
+@pytest.mark.parametrize("max_kv,new", [(100, 1), (64, 1), (3000, 1), (100000, 1), (1, 200), (10**6, 200)])
+def test_bounds_that_are_not_tight(tq, max_kv, new):
+    """max_kv only plans: too large or too small, the result is that of the exact one."""
+    check(tq, problem([(1900, new), (300, min(new, 100))], 4, 2, 64, 16, F16), F32, max_kv=max_kv)
+
+
+def test_split_count_changes_only_roundings(tq):
+    prob = problem([(8000, 1)], 8, 1, 128, 16, BF16)
+    a, la = call(tq, prob, F32)
+    b, lb = call(tq, prob, F32, max_kv=64)     # planned as one split
+    assert (a - b).abs().max().item() <= 2 * 2.0**-8 * 1.0
+    assert (la - lb).abs().max().item() <= 1e-5
+
+
+def test_same_inputs_same_bits(tq):
+    for lens in ([(3000, 1)] * 3, [(700, 300), (200, 5)]):
+        prob = problem(lens, 8, 2, 128, 16, BF16)
+        a, la = call(tq, prob, BF16)
+        for _ in range(3):
+            b, lb = call(tq, prob, BF16)
+            assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_bad_pages_and_lengths_are_reported(tq):
+    for new in (1, 200):
+        prob = list(problem([(300, new)], 4, 2, 64, 16, F16))
+        for entry in (-1, prob[1].shape[0], 2**31 - 1):
+            bad = prob[3].clone()
+            bad[0, 5] = entry
+            call(tq, tuple(prob[:3] + [bad] + prob[4:]), F16)
+            assert tq.tq_device_status() == tq.TQ_ERR_INDEX, (new, entry)
+        long = prob[:5] + [torch.tensor([100000]).int()] + prob[6:]
+        call(tq, tuple(long), F16, max_kv=300)
+        assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+        call(tq, tuple(prob), F16, max_q=1 if new > 1 else 0)
+        assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+        call(tq, tuple(prob), F16)
+        assert tq.tq_device_status() == tq.TQ_OK
+
+
+def test_strided_queries_and_output(tq):
+    prob = problem([(300, 3), (64, 1)], 4, 2, 64, 16, F16)
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    want, _ = call(tq, prob, F16)
+    wide = torch.zeros(4, 4 * 64 + 24, dtype=F16, device="cuda")
+    Qs = torch.as_strided(wide, (4, 4, 64), (4 * 64 + 24, 64, 1), 8)
+    Qs.copy_(Q)
+    out = torch.zeros(4, 4 * 64 + 3, device="cuda", dtype=F16)
+    O = torch.as_strided(out, (4, 4, 64), (4 * 64 + 3, 64, 1), 1)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    tq.tq_paged_attention(Qs, tq.PagedKV(kd, vd, table.cuda()), q_start.cuda(), kv_len.cuda(), O, 3,
+                          300, 64 ** -0.5, ws)
+    assert torch.equal(O, want)
+    assert (out[:, :1] == 0).all() and (out[:, 257:] == 0).all()
+
+
+def test_long_cache_offsets_pass_32_bits(tq):
+    """Pages whose byte and element offsets pass 2^32, in a cache of which only those are used."""
+    heads, page, dim = 8, 64, 128
+    pages = (1 << 32) // (heads * page * dim) + 9       # 2^32 elements and a little more
+    k = torch.empty(pages, heads, page, dim, dtype=F16, device="cuda")
+    v = torch.empty_like(k)
+    for new in (1, 150):
+        n = 5 * page - 3
+        table = torch.tensor([[pages - 1, pages - 3, 0, pages - 2, pages // 2 + 1]], dtype=torch.int32)
+        g = torch.Generator().manual_seed(9)
+        kc, vc = torch.zeros(5, heads, page, dim, dtype=F16), torch.zeros(5, heads, page, dim, dtype=F16)
+        small = torch.arange(5, dtype=torch.int32)[None]
+        for i in range(5):
+            kc[i] = torch.randn(heads, page, dim, generator=g)
+            vc[i] = torch.randn(heads, page, dim, generator=g)
+            k[table[0, i]], v[table[0, i]] = kc[i].cuda(), vc[i].cuda()
+        Q = torch.randn(new, 16, dim, generator=g).to(F16)
+        q_start, kv_len = torch.tensor([0, new]).int(), torch.tensor([n]).int()
+        o, _, tol, _ = attention(Q, kc, vc, small, q_start, kv_len, dim ** -0.5, 0, F16)
+        O, _ = call(tq, (Q, k, v, table, q_start, kv_len, k, v), F16)
+        assert_within(O, o, tol, "o")
+        # and the append to them
+        X = torch.randn(1, 2 * heads, dim, device="cuda")
+        tq.tq_kv_append(None, X[:, :heads], X[:, heads:], None, tq.PagedKV(k, v, table.cuda()),
+                        torch.zeros(1, dtype=torch.int32, device="cuda"),
+                        torch.full((1,), 5 * page - 3, dtype=torch.int32, device="cuda"))
+        assert torch.equal(v[pages // 2 + 1, :, page - 3], X[0, heads:].half())
+
+
+def test_append_then_attend(tq):
+    """The two calls in a row, in a graph, as a decode step runs them: the second sees what the
+    first wrote."""
+    from attn_util import frequencies, norm_rope
+    g = torch.Generator().manual_seed(4)
+    hq, hk, dim, page, lens = 8, 2, 128, 16, [200, 33, 1]
+    Q, k, v, table, q_start, kv_len, kd, vd = problem([(n, 1) for n in lens], hq, hk, dim, page, BF16)
+    X = torch.randn(3, hq + 2 * hk, dim, generator=g)
+    w = torch.rand(dim, generator=g) + 0.5
+    pos = torch.tensor([n - 1 for n in lens], dtype=torch.int32)
+    turns, _ = tq.tq_rope_turns(dim, 1e4)
+    rope, kv = tq.Rope(turns.cuda()), tq.PagedKV(kd, vd, table.cuda())
+    Xd, Yq = X.cuda(), torch.empty(3, hq, dim, dtype=BF16, device="cuda")
+    O = torch.empty(3, hq, dim, device="cuda")
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    dev = [t.cuda() for t in (torch.arange(3, dtype=torch.int32), pos, q_start, kv_len, w)]
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            tq.tq_kv_append(Xd[:, :hq], Xd[:, hq:hq + hk], Xd[:, hq + hk:], Yq, kv, dev[0], dev[1],
+                            rope, dev[4], dev[4])
+            tq.tq_paged_attention(Yq, kv, dev[2], dev[3], O, 1, 256, dim ** -0.5, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    # the queries and keys as the call rounded them, within its own bound of the definition
+    wantq, boundq = norm_rope(X[:, :hq], w, 1e-6, frequencies(dim), False, 1.0, pos, BF16)
+    assert_within(Yq, wantq, boundq, "q")
+    o, _, tol, _ = attention(Yq.cpu(), kd.cpu(), vd.cpu(), table, q_start, kv_len, dim ** -0.5, 0, F32)
+    assert_within(O, o, tol, "o")
+
+
+def test_no_work(tq):
+    prob = problem([(0, 0), (20, 0)], 2, 2, 64, 16, F16)
+    O, L = call(tq, prob, F16, max_q=1)
+    assert O.numel() == 0
+    assert math.isfinite(float(tq.tq_device_status()))
