@@ -1,0 +1,130 @@
+// tq_attn.cu -- paged attention: the launch (parameters, maps of the cache,
+// which kernel) and the join of partial results.
+#include "tq_attn_dev.cuh"
+
+namespace tq {
+namespace {
+
+// Joins the partial results of the splits: o = sum_s 2^(lse_s - M) o_s /
+// sum_s 2^(lse_s - M), one warp per row of one query head. Reads
+// nsplit * (dim + 1) * 4 bytes a row, a few percent of the keys' bytes.
+__global__ void __launch_bounds__(128)
+attn_join_kernel(const __grid_constant__ AttnParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int64_t rows = p.ntok * p.q_heads;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int64_t tok = row / p.q_heads;
+  // tokens past the last sequence's are not written
+  if (tok >= p.q_start[p.nseq]) return;
+  float top = -INFINITY;
+  for (int s = lane; s < p.nsplit; s += 32) top = fmaxf(top, p.part_lse[s * rows + row]);
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float sum = 0.0f, acc[kMaxKvDim / 32] = {};
+  if (top != -INFINITY)
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float f = exp2_approx(p.part_lse[s * rows + row] - top);
+      if (f == 0.0f) continue;
+      sum += f;
+#pragma unroll
+      for (int i = 0; i < kMaxKvDim / 32; ++i)
+        if (lane + 32 * i < p.dim)
+          acc[i] += f * p.part_o[(s * rows + row) * p.dim + lane + 32 * i];
+    }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxKvDim / 32; ++i)
+    if (lane + 32 * i < p.dim)
+      store_out(p.o, p.o_type, tok * p.o_stride + (row - tok * p.q_heads) * p.dim + lane + 32 * i,
+                acc[i] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn* out) {
+  static EncodeFn fn = nullptr;   // the driver's entry point: the same for every call
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    fn = reinterpret_cast<EncodeFn>(f);
+  }
+  *out = fn;
+  return cudaSuccess;
+}
+
+// The cache as {dim, slot, head, page}, in boxes of 64 values of box_rows slots.
+cudaError_t cache_map(CUtensorMap* map, const tq_paged_kv& c, void* p, int box_rows) {
+  EncodeFn fn;
+  const cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.heads, (cuuint64_t)c.pages};
+  // a stride of a dimension of size 1 is never used, but has to be encodable
+  const cuuint64_t one = (cuuint64_t)c.slot_stride * 2;
+  const cuuint64_t strides[3] = {one, c.heads > 1 ? (cuuint64_t)c.head_stride * 2 : one,
+                                 c.pages > 1 ? (cuuint64_t)c.page_stride * 2 : one};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, c.type == TQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+         4, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
+  AttnParams p = {};
+  p.q = c.q;
+  p.o = c.o;
+  p.lse = c.lse;
+  p.part_o = c.part_o;
+  p.part_lse = c.part_lse;
+  p.q_start = c.q_start;
+  p.kv_len = c.kv_len;
+  p.table = c.kv.block_table;
+  p.q_stride = c.q_stride;
+  p.o_stride = c.o_stride;
+  p.table_stride = c.kv.table_stride;
+  p.table_width = c.kv.table_width;
+  p.ntok = c.ntok;
+  p.status = c.status;
+  p.q_heads = (int)c.q_heads;
+  p.group = (int)(c.q_heads / c.kv.heads);
+  p.dim = (int)c.kv.head_dim;
+  p.page_size = (int)c.kv.page_size;
+  p.pages = (int)c.kv.pages;
+  // boxes are pieces of a page and of a key tile
+  p.box_rows = (int)(c.kv.page_size & -c.kv.page_size);
+  if (p.box_rows > c.plan.key_tile) p.box_rows = c.plan.key_tile;
+  p.nseq = (int)c.kv.nseq;
+  p.tiles_x = (int)c.plan.tiles_x;
+  p.nsplit = c.plan.nsplit;
+  p.chunk_tiles = c.plan.chunk_tiles;
+  p.max_q = (int)c.max_q;
+  p.o_type = c.o_type;
+  p.window = c.window;
+  p.scale_log2 = c.scale * kLog2e;
+  CUtensorMap kmap, vmap;
+  cudaError_t e = cache_map(&kmap, c.kv, c.kv.k, p.box_rows);
+  if (e == cudaSuccess) e = cache_map(&vmap, c.kv, c.kv.v, p.box_rows);
+  if (e != cudaSuccess) return e;
+  e = c.plan.chunk ? launch_attn_chunk(p, c, kmap, vmap, s) : launch_attn_decode(p, c, kmap, vmap, s);
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  const int64_t grid = (c.ntok * c.q_heads + 3) / 4;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_pdl(attn_join_kernel, dim3((unsigned)grid), dim3(128), 0, s, p);
+}
+
+}  // namespace tq

@@ -53,8 +53,10 @@ cudaError_t launch_norm_rope(const RopeCall& c, cudaStream_t s);
 // How a paged attention call is cut: a function of its sizes alone, so that
 // the workspace size is too.
 struct AttnPlan {
+  bool chunk;           // the kernel for many rows
   int tile_rows;        // rows (token, query head) of a thread block
-  int64_t tiles_x;      // row tiles of the grid
+  int key_tile;         // keys of a tile
+  int64_t tiles_x;      // row tiles of a sequence (few rows) or of all (many)
   int nsplit;           // key ranges per row tile
   int chunk_tiles;      // key tiles of a range
   int64_t ws_bytes;

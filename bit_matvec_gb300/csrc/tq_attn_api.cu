@@ -103,10 +103,10 @@ int take_rope(RopeCall& c, const float* qw, const float* kw, float eps, const tq
   return TQ_OK;
 }
 
-// Key tiles are 64 keys in the planner, whatever the kernel.
-constexpr int64_t kPlanKeys = 64;
-// The planner's idea of the GPU: 152 SMs of two thread blocks each.
-constexpr int64_t kPlanSlots = 304;
+// The planner's idea of the GPU.
+constexpr int64_t kPlanSms = 152;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
@@ -115,25 +115,35 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   AttnPlan p = {};
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
-  p.tile_rows = 16;
-  p.tiles_x = (max_q * group + p.tile_rows - 1) / p.tile_rows;
-  if (p.tiles_x < 1) p.tiles_x = 1;
+  // one 16-row tile reads the keys once; from two on the kernel for many rows
+  p.chunk = max_q * group > 16;
+  p.tile_rows = p.chunk ? 256 : 16;
+  p.key_tile = p.chunk ? 128 : 64;
+  const int64_t slots = p.chunk ? kPlanSms : 2 * kPlanSms;
+  int64_t units;
+  if (p.chunk) {
+    p.tiles_x = ntok * group / p.tile_rows + nseq;
+    units = kv_heads * (ceil_div(max_q * group, p.tile_rows) == 1 ? nseq
+                                                                  : ceil_div(ntok * group, p.tile_rows));
+  } else {
+    p.tiles_x = 1;
+    units = kv_heads * nseq;
+  }
   // keys that a row tile sees at most, in tiles (one more where the window
   // does not start on a tile)
   int64_t span = max_kv;
   if (window > 0 && window + max_q < span) span = window + max_q;
-  int64_t tiles = (span + kPlanKeys - 1) / kPlanKeys + (span < max_kv ? 1 : 0);
+  int64_t tiles = ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0);
   if (tiles < 1) tiles = 1;
-  // Few blocks: split the keys until every slot has one. Many: ranges of
-  // 2048 keys or more, so that ragged lengths spread evenly.
-  const int64_t units = nseq * kv_heads * p.tiles_x;
-  int64_t split = units > 0 ? kPlanSlots / units : 1;
-  if (split < tiles / 32) split = units >= 16 * kPlanSlots ? 1 : tiles / 32;
-  if (split > tiles / 4) split = tiles / 4;   // ranges of at least 256 keys
+  // Few blocks: split the keys until every slot has one. Many of the small
+  // ones: ranges of 2048 keys or more, so that ragged lengths spread evenly.
+  int64_t split = slots / units;
+  if (!p.chunk && split < tiles / 32) split = units >= 16 * slots ? 1 : tiles / 32;
+  if (split > tiles * p.key_tile / 256) split = tiles * p.key_tile / 256;   // 256 keys or more
   if (split > 128) split = 128;
   if (split < 1) split = 1;
-  p.chunk_tiles = (int)((tiles + split - 1) / split);
-  p.nsplit = (int)((tiles + p.chunk_tiles - 1) / p.chunk_tiles);
+  p.chunk_tiles = (int)ceil_div(tiles, split);
+  p.nsplit = (int)ceil_div(tiles, p.chunk_tiles);
   p.ws_bytes = p.nsplit > 1 ? (p.nsplit * ntok * q_heads * (head_dim + 1) * 4 + 15) / 16 * 16 : 0;
   return p;
 }

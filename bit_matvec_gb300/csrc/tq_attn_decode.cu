@@ -17,9 +17,7 @@
 // and registers give the softmax its operands without a trip through TMEM.
 // The keys of a row tile are split over thread blocks where there are few of
 // them; partial results are joined by a second kernel.
-#include <cuda.h>
-
-#include "tq_attn.cuh"
+#include "tq_attn_dev.cuh"
 
 namespace tq {
 namespace {
@@ -28,27 +26,6 @@ constexpr int kRows = 16;
 constexpr int kKeys = 64;             // keys of a stage
 constexpr int kWarps = 4;             // compute warps, 16 keys of a stage each
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint64_t kWaitNs = 1000000000ull;
-
-struct Params {
-  const void* q;
-  void* o;
-  float* lse;
-  float* part_o;
-  float* part_lse;
-  const int32_t* q_start;
-  const int32_t* kv_len;
-  const int32_t* table;
-  int64_t q_stride, o_stride, table_stride, table_width;
-  int64_t ntok;
-  int* status;
-  int q_heads, group, dim, page_size, pages, box_rows;
-  int nseq, tiles_x, nsplit, chunk_tiles, max_q;
-  int o_type;
-  int64_t window;
-  float scale_log2;
-};
 
 template <int DP> struct Smem {
   static constexpr int kStages = DP == 128 ? 3 : 6;
@@ -87,47 +64,9 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 4-D tiled TMA load {64 values, box_rows slots, 1 head, 1 page}.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int slot,
-                                        int head, int page, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
-      : "memory");
-}
-
-// Byte offset of 16-byte chunk j of row r in a 64-value-wide tile of 128-byte
-// rows with the 128-byte swizzle (tile 1024-byte aligned).
-__device__ __forceinline__ uint32_t swz(int r, int j) {
-  return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void store_out(void* o, int type, int64_t at, float x) {
-  if (type == TQ_F32) static_cast<float*>(o)[at] = x;
-  else if (type == TQ_F16) static_cast<__half*>(o)[at] = __float2half_rn(x);
-  else static_cast<__nv_bfloat16*>(o)[at] = __float2bfloat16_rn(x);
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 2)
-attn_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
+attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<DP>;
   constexpr int kStages = S::kStages, kSub = DP / 64;
@@ -402,7 +341,7 @@ attn_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
           if (d == 0) p.part_lse[at] = lse;
         } else {
           store_out(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, val);
-          if (d == 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * 0.6931471805599453f;
+          if (d == 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
         }
       }
     }
@@ -416,87 +355,10 @@ attn_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUt
   }
 }
 
-// Joins the partial results of the splits: o = sum_s 2^(lse_s - M) o_s /
-// sum_s 2^(lse_s - M), one warp per row of one query head. Reads
-// nsplit * (dim + 1) * 4 bytes a row, a few percent of the keys' bytes.
-__global__ void __launch_bounds__(128)
-attn_join_kernel(const __grid_constant__ Params p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int64_t rows = p.ntok * p.q_heads;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int64_t tok = row / p.q_heads;
-  // tokens past the last sequence's are not written
-  if (tok >= p.q_start[p.nseq]) return;
-  float top = -INFINITY;
-  for (int s = lane; s < p.nsplit; s += 32) top = fmaxf(top, p.part_lse[s * rows + row]);
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float sum = 0.0f, acc[kMaxKvDim / 32] = {};
-  if (top != -INFINITY)
-    for (int s = 0; s < p.nsplit; ++s) {
-      const float f = exp2_approx(p.part_lse[s * rows + row] - top);
-      if (f == 0.0f) continue;
-      sum += f;
-#pragma unroll
-      for (int i = 0; i < kMaxKvDim / 32; ++i)
-        if (lane + 32 * i < p.dim)
-          acc[i] += f * p.part_o[(s * rows + row) * p.dim + lane + 32 * i];
-    }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kMaxKvDim / 32; ++i)
-    if (lane + 32 * i < p.dim)
-      store_out(p.o, p.o_type, tok * p.o_stride + (row - tok * p.q_heads) * p.dim + lane + 32 * i,
-                acc[i] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-}
-
 // ---------------------------------------------------------------- host
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encode_fn(EncodeFn* out) {
-  static EncodeFn fn = nullptr;   // the driver's entry point: the same for every call
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const cudaError_t e =
-        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
-    if (e != cudaSuccess) return e;
-    if (q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-    fn = reinterpret_cast<EncodeFn>(f);
-  }
-  *out = fn;
-  return cudaSuccess;
-}
-
-// The cache as {dim, slot, head, page}, in boxes of 64 values of box_rows slots.
-cudaError_t cache_map(CUtensorMap* map, const tq_paged_kv& c, void* p, int box_rows) {
-  EncodeFn fn;
-  const cudaError_t e = encode_fn(&fn);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
-                              (cuuint64_t)c.heads, (cuuint64_t)c.pages};
-  // a stride of a dimension of size 1 is never used, but has to be encodable
-  const cuuint64_t one = (cuuint64_t)c.slot_stride * 2;
-  const cuuint64_t strides[3] = {one, c.heads > 1 ? (cuuint64_t)c.head_stride * 2 : one,
-                                 c.pages > 1 ? (cuuint64_t)c.page_stride * 2 : one};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, c.type == TQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-         4, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <typename T, int DP>
-cudaError_t launch_decode(const Params& p, const AttnCall& c, const CUtensorMap& kmap,
+cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, cudaStream_t s) {
   auto kernel = attn_decode_kernel<T, DP>;
   const cudaError_t e = ensure_dynamic_smem((const void*)kernel, Smem<DP>::kBytes);
@@ -508,7 +370,7 @@ cudaError_t launch_decode(const Params& p, const AttnCall& c, const CUtensorMap&
 }
 
 template <typename T>
-cudaError_t launch_decode(const Params& p, const AttnCall& c, const CUtensorMap& kmap,
+cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, cudaStream_t s) {
   return c.kv.head_dim <= 64 ? launch_decode<T, 64>(p, c, kmap, vmap, s)
                              : launch_decode<T, 128>(p, c, kmap, vmap, s);
@@ -516,48 +378,10 @@ cudaError_t launch_decode(const Params& p, const AttnCall& c, const CUtensorMap&
 
 }  // namespace
 
-cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
-  Params p = {};
-  p.q = c.q;
-  p.o = c.o;
-  p.lse = c.lse;
-  p.part_o = c.part_o;
-  p.part_lse = c.part_lse;
-  p.q_start = c.q_start;
-  p.kv_len = c.kv_len;
-  p.table = c.kv.block_table;
-  p.q_stride = c.q_stride;
-  p.o_stride = c.o_stride;
-  p.table_stride = c.kv.table_stride;
-  p.table_width = c.kv.table_width;
-  p.ntok = c.ntok;
-  p.status = c.status;
-  p.q_heads = (int)c.q_heads;
-  p.group = (int)(c.q_heads / c.kv.heads);
-  p.dim = (int)c.kv.head_dim;
-  p.page_size = (int)c.kv.page_size;
-  p.pages = (int)c.kv.pages;
-  // boxes are pieces of a page and of a 64-key tile
-  p.box_rows = (int)(c.kv.page_size & -c.kv.page_size);
-  if (p.box_rows > kKeys) p.box_rows = kKeys;
-  p.nseq = (int)c.kv.nseq;
-  p.tiles_x = (int)c.plan.tiles_x;
-  p.nsplit = c.plan.nsplit;
-  p.chunk_tiles = c.plan.chunk_tiles;
-  p.max_q = (int)c.max_q;
-  p.o_type = c.o_type;
-  p.window = c.window;
-  p.scale_log2 = c.scale * kLog2e;
-  CUtensorMap kmap, vmap;
-  cudaError_t e = cache_map(&kmap, c.kv, c.kv.k, p.box_rows);
-  if (e == cudaSuccess) e = cache_map(&vmap, c.kv, c.kv.v, p.box_rows);
-  if (e != cudaSuccess) return e;
-  e = c.kv.type == TQ_F16 ? launch_decode<__half>(p, c, kmap, vmap, s)
-                          : launch_decode<__nv_bfloat16>(p, c, kmap, vmap, s);
-  if (e != cudaSuccess || p.nsplit == 1) return e;
-  const int64_t grid = (c.ntok * c.q_heads + 3) / 4;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(attn_join_kernel, dim3((unsigned)grid), dim3(128), 0, s, p);
+cudaError_t launch_attn_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, cudaStream_t s) {
+  return c.kv.type == TQ_F16 ? launch_decode<__half>(p, c, kmap, vmap, s)
+                             : launch_decode<__nv_bfloat16>(p, c, kmap, vmap, s);
 }
 
 }  // namespace tq

@@ -1,0 +1,100 @@
+// tq_attn_dev.cuh -- what the two attention kernels and the join of their
+// partial results share: parameters, TMA boxes of the paged cache, stores.
+#pragma once
+
+#include <cuda.h>
+
+#include "tq_attn.cuh"
+
+namespace tq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint64_t kWaitNs = 1000000000ull;   // limit of every wait in the attention kernels
+
+struct AttnParams {
+  const void* q;
+  void* o;
+  float* lse;
+  float* part_o;
+  float* part_lse;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t q_stride, o_stride, table_stride, table_width;
+  int64_t ntok;
+  int* status;
+  int q_heads, group, dim, page_size, pages, box_rows;
+  int nseq, tiles_x, nsplit, chunk_tiles, max_q;
+  int o_type;
+  int64_t window;
+  float scale_log2;
+};
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 4-D tiled TMA load {64 values, box_rows slots, 1 head, 1 page}.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int slot,
+                                        int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// Byte offset of 16-byte chunk j of row r in a 64-value-wide tile of 128-byte
+// rows with the 128-byte swizzle (tile 1024-byte aligned).
+__device__ __forceinline__ uint32_t swz(int r, int j) {
+  return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void store_out(void* o, int type, int64_t at, float x) {
+  if (type == TQ_F32) static_cast<float*>(o)[at] = x;
+  else if (type == TQ_F16) static_cast<__half*>(o)[at] = __float2half_rn(x);
+  else static_cast<__nv_bfloat16*>(o)[at] = __float2bfloat16_rn(x);
+}
+
+// Four consecutive values from a multiple of 4 on: one store where the address
+// allows it.
+__device__ __forceinline__ void store_out4(void* o, int type, int64_t at, const float (&x)[4]) {
+  if (type == TQ_F32) {
+    float* y = static_cast<float*>(o) + at;
+    if (((uintptr_t)y & 15u) == 0) {
+      *reinterpret_cast<float4*>(y) = make_float4(x[0], x[1], x[2], x[3]);
+      return;
+    }
+  } else {
+    uint16_t* y = static_cast<uint16_t*>(o) + at;
+    if (((uintptr_t)y & 7u) == 0) {
+      *reinterpret_cast<uint2*>(y) =
+          type == TQ_F16
+              ? make_uint2(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]))
+              : make_uint2(pack2<__nv_bfloat16>(x[0], x[1]), pack2<__nv_bfloat16>(x[2], x[3]));
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_out(o, type, at + e, x[e]);
+}
+
+cudaError_t launch_attn_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, cudaStream_t s);
+cudaError_t launch_attn_chunk(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
+                              const CUtensorMap& vmap, cudaStream_t s);
+
+}  // namespace tq
