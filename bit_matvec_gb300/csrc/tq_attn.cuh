@@ -50,6 +50,8 @@ struct RopeCall {
 
 cudaError_t launch_norm_rope(const RopeCall& c, cudaStream_t s);
 
+constexpr int kMaxSplits = 128;    // key ranges of a row tile
+
 // How a paged attention call is cut: a function of its sizes alone, so that
 // the workspace size is too.
 struct AttnPlan {

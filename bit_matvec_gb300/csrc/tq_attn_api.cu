@@ -140,7 +140,7 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   int64_t split = slots / units;
   if (!p.chunk && split < tiles / 32) split = units >= 16 * slots ? 1 : tiles / 32;
   if (split > tiles * p.key_tile / 256) split = tiles * p.key_tile / 256;   // 256 keys or more
-  if (split > 128) split = 128;
+  if (split > kMaxSplits) split = kMaxSplits;
   if (split < 1) split = 1;
   p.chunk_tiles = (int)ceil_div(tiles, split);
   p.nsplit = (int)ceil_div(tiles, p.chunk_tiles);
