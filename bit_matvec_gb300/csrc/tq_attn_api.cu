@@ -115,10 +115,11 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   AttnPlan p = {};
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
-  // one 16-row tile reads the keys once; from two on the kernel for many rows
-  p.chunk = max_q * group > 16;
-  p.tile_rows = p.chunk ? 256 : 16;
-  p.key_tile = p.chunk ? 128 : 64;
+  // up to 64 rows stay in one block of the kernel for few rows
+  const int64_t rows = max_q * group;
+  p.chunk = rows > 64;
+  p.tile_rows = p.chunk ? 256 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+  p.key_tile = p.chunk || head_dim <= 64 ? 128 : 64;
   const int64_t slots = p.chunk ? kPlanSms : 2 * kPlanSms;
   int64_t units;
   if (p.chunk) {
@@ -138,7 +139,8 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   // Few blocks: split the keys until every slot has one. Many of the small
   // ones: ranges of 2048 keys or more, so that ragged lengths spread evenly.
   int64_t split = slots / units;
-  if (!p.chunk && split < tiles / 32) split = units >= 16 * slots ? 1 : tiles / 32;
+  const int64_t spread = tiles * p.key_tile / 2048;
+  if (!p.chunk && split < spread) split = units >= 16 * slots ? 1 : spread;
   if (split > tiles * p.key_tile / 256) split = tiles * p.key_tile / 256;   // 256 keys or more
   if (split > kMaxSplits) split = kMaxSplits;
   if (split < 1) split = 1;

@@ -5,16 +5,17 @@
 // o = sum_j 2^(c s_j - M) v_j / sum_j 2^(c s_j - M), c = log2(e), with the
 // running maximum M and sum kept in 32 bits (one pass over the keys).
 //
-// Bound by the bytes of the keys and values: a thread block takes the 16 rows
-// of a 16-row matrix fragment (all query heads that share a key/value head,
-// times a few tokens) and reads every key once for all of them. One producer
-// warp streams 64-key tiles of K and V through a ring of shared-memory stages
-// with TMA boxes, one per page piece, 128-byte swizzled so that the fragment
-// loads are free of bank conflicts. Each of the four other warps owns 16 of a
-// tile's 64 keys with its own maximum, sum and output accumulators, so the
-// warps never wait for one another until the merge at the end. mma.sync, not
-// tcgen05: at 16 rows the tensor work is 16 flop per byte, far from any rate,
-// and registers give the softmax its operands without a trip through TMEM.
+// Bound by the bytes of the keys and values: a thread block takes 16 RW rows
+// (all query heads that share a key/value head, times a few tokens) and reads
+// every key once for all of them. One producer warp streams tiles of K
+// and V through a ring of shared-memory stages with TMA boxes, one per page
+// piece, 128-byte swizzled so that the fragment loads are free of bank
+// conflicts. The four other warps split a tile RW ways by rows (16 rows, one
+// matrix fragment, each) and 4 / RW ways by keys, each with its own maximum,
+// sum and output accumulators, so that they never wait for one another until
+// the merge at the end. mma.sync, not tcgen05: at 16 rows the tensor work is
+// 16 flop per byte, far from any rate, and registers give the softmax its
+// operands without a trip through TMEM.
 // The keys of a row tile are split over thread blocks where there are few of
 // them; partial results are joined by a second kernel.
 #include "tq_attn_dev.cuh"
@@ -22,14 +23,15 @@
 namespace tq {
 namespace {
 
-constexpr int kRows = 16;
-constexpr int kKeys = 64;             // keys of a stage
-constexpr int kWarps = 4;             // compute warps, 16 keys of a stage each
+constexpr int kWarps = 4;             // compute warps
 constexpr int kThreads = (kWarps + 1) * 32;
 
+// A stage is 16 KB of keys and 16 KB of values whatever the head's size; three
+// of them leave room for two blocks on an SM.
 template <int DP> struct Smem {
-  static constexpr int kStages = DP == 128 ? 3 : 6;
-  static constexpr int kTile = kKeys * DP * 2;      // bytes of a K or V tile
+  static constexpr int kKeys = DP == 128 ? 64 : 128;   // keys of a tile
+  static constexpr int kStages = 3;
+  static constexpr int kTile = kKeys * DP * 2;         // bytes of a K or V tile
   static constexpr int kBytes = kStages * 2 * kTile + 1024 + 256;   // + alignment + barriers
 };
 
@@ -64,11 +66,16 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int RW>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<DP>;
+  constexpr int kRows = 16 * RW;        // rows of the block
+  constexpr int KW = kWarps / RW;       // warps along the keys
+  constexpr int kKeys = S::kKeys;
+  constexpr int kMine = kKeys / KW;     // keys of a tile that a warp takes,
+  constexpr int NK = kMine / 16 < 4 ? kMine / 16 : 4;   // in steps of NK x 16
   constexpr int kStages = S::kStages, kSub = DP / 64;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -114,7 +121,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
   if (warp == kWarps) {
     // ------------------------------------------------ producer
-    const int boxes = kKeys / p.box_rows;    // 1 .. 8, one lane each
+    const int boxes = kKeys / p.box_rows;    // 1 .. 16, one lane each
     const int off = lane * p.box_rows;
     int page = p.pages, slot = 0;
     bool bad = false;
@@ -164,12 +171,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   } else {
     // ------------------------------------------------ compute warps
     const int g = lane >> 2, tq = lane & 3;
+    const int rw = warp / KW, kw = warp % KW;   // the warp's 16 rows and its share of the keys
+    const bool busy = rw * 16 < rows;
     // this thread's rows g and g + 8: query fragments and positions
     uint32_t qf[DP / 16][4];
     int pos[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = min(g + 8 * h, rows - 1);   // rows past the end repeat the last
+      const int r = min(rw * 16 + g + 8 * h, rows - 1);   // rows past the end repeat the last
       const int i = (row0 + r) / p.group, hh = (row0 + r) % p.group;
       pos[h] = kv - qn + i;
       const T* q = static_cast<const T*>(p.q) + (int64_t)(q0 + i) * p.q_stride +
@@ -189,8 +198,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
     // ldmatrix addresses: matrix mi = lane / 8, row lane % 8 of it
     const int mi = lane >> 3, mr = lane & 7;
-    const int krow = warp * 16 + (mi >> 1) * 8 + mr, kchunk = mi & 1;
-    const int vrow = warp * 16 + (mi & 1) * 8 + mr, vchunk = mi >> 1;
+    const int krow = kw * kMine + (mi >> 1) * 8 + mr, kchunk = mi & 1;
+    const int vrow = kw * kMine + (mi & 1) * 8 + mr, vchunk = mi >> 1;
 
     int stage = 0, phase = 0;
     bool ok = true;
@@ -200,45 +209,58 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         break;
       }
       const uint32_t ks = base + stage * 2 * S::kTile, vs = ks + S::kTile;
-      const int key0 = t * kKeys + warp * 16;
-      if (key0 < hi && key0 + 16 > lo) {
-        float s[2][4] = {};
+      const int first = t * kKeys + kw * kMine;   // the warp's first key of the tile
+      // values of keys that no row sees may be anything: zero them (their
+      // weights are zero, but zero times NaN is not)
+      if (busy && (first + kMine > hi || first < lo)) {
+        for (int i = lane; i < kMine * DP / 8; i += 32) {
+          const int r = kw * kMine + i % kMine, c = i / kMine;
+          const int key = t * kKeys + r;
+          if (key >= hi || key < lo)
+            *reinterpret_cast<uint4*>(basep + (vs - base) + (c >> 3) * kKeys * 128 +
+                                      swz(r, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-          uint32_t b[4];
-          ldmatrix4(ks + (d >> 2) * kKeys * 128 + swz(krow, (d & 3) * 2 + kchunk), b);
-          mma16816<T>(s[0], qf[d], b[0], b[1]);
-          mma16816<T>(s[1], qf[d], b[2], b[3]);
-        }
-        // values of keys that no row sees may be anything: zero them (their
-        // weights are zero, but zero times NaN is not)
-        if (key0 + 16 > hi || key0 < lo) {
-          for (int i = lane; i < 16 * DP / 8; i += 32) {
-            const int r = warp * 16 + i % 16, c = i / 16;
-            const int key = t * kKeys + r;
-            if (key >= hi || key < lo)
-              *reinterpret_cast<uint4*>(basep + (vs - base) + (c >> 3) * kKeys * 128 +
-                                        swz(r, c & 7)) = make_uint4(0, 0, 0, 0);
+      for (int st = 0; st < kMine; st += 16 * NK) {
+        const int key0 = first + st;
+        if (!busy || key0 >= hi || key0 + 16 * NK <= lo) continue;
+        // scores of NK x 16 keys: 2 NK independent accumulators
+        float s[2 * NK][4] = {};
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+          for (int n = 0; n < NK; ++n) {
+            uint32_t b[4];
+            ldmatrix4(ks + (d >> 2) * kKeys * 128 + swz(krow + st + n * 16, (d & 3) * 2 + kchunk), b);
+            mma16816<T>(s[2 * n], qf[d], b[0], b[1]);
+            mma16816<T>(s[2 * n + 1], qf[d], b[2], b[3]);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        // scores in base-2 logarithms; masked ones to minus infinity
+        // in base-2 logarithms; masked ones to minus infinity
         float mx[2] = {-INFINITY, -INFINITY};
-        const bool masked = key0 + 15 > pos_first ||
+        const bool masked = key0 + 16 * NK - 1 > pos_first ||
                             (p.window > 0 && (int64_t)key0 <= (int64_t)pos_last - p.window);
+        if (masked) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2 * NK; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = e >> 1, key = key0 + n * 8 + 2 * tq + (e & 1);
-            float x = s[n][e] * p.scale_log2;
-            if (masked && (key > pos[h] ||
-                           (p.window > 0 && (int64_t)key <= (int64_t)pos[h] - p.window)))
-              x = -INFINITY;
-            s[n][e] = x;
-            mx[h] = fmaxf(mx[h], x);
-          }
+            for (int e = 0; e < 4; ++e) {
+              const int h = e >> 1, key = key0 + n * 8 + 2 * tq + (e & 1);
+              s[n][e] = key > pos[h] || (p.window > 0 && (int64_t)key <= (int64_t)pos[h] - p.window)
+                            ? -INFINITY : s[n][e] * p.scale_log2;
+              mx[h] = fmaxf(mx[h], s[n][e]);
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2 * NK; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[n][e] *= p.scale_log2;
+              mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+            }
+        }
         float corr[2], ref[2];
         bool grow = false;
 #pragma unroll
@@ -262,24 +284,27 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           l[0] *= corr[0];
           l[1] *= corr[1];
         }
-        uint32_t a[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float w[4];
+        for (int n = 0; n < NK; ++n) {
+          uint32_t a[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = exp2_approx(s[n][e] - ref[e >> 1]);
-            l[e >> 1] += w[e];
+          for (int q = 0; q < 2; ++q) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[e] = exp2_approx(s[2 * n + q][e] - ref[e >> 1]);
+              l[e >> 1] += w[e];
+            }
+            a[2 * q] = pack2<T>(w[0], w[1]);
+            a[2 * q + 1] = pack2<T>(w[2], w[3]);
           }
-          a[2 * n] = pack2<T>(w[0], w[1]);
-          a[2 * n + 1] = pack2<T>(w[2], w[3]);
-        }
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-          uint32_t b[4];
-          ldmatrix4_trans(vs + (d >> 2) * kKeys * 128 + swz(vrow, (d & 3) * 2 + vchunk), b);
-          mma16816<T>(o[2 * d], a, b[0], b[1]);
-          mma16816<T>(o[2 * d + 1], a, b[2], b[3]);
+          for (int d = 0; d < DP / 16; ++d) {
+            uint32_t b[4];
+            ldmatrix4_trans(vs + (d >> 2) * kKeys * 128 + swz(vrow + st + n * 16, (d & 3) * 2 + vchunk), b);
+            mma16816<T>(o[2 * d], a, b[0], b[1]);
+            mma16816<T>(o[2 * d + 1], a, b[2], b[3]);
+          }
         }
       }
       __syncwarp();
@@ -301,20 +326,21 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     if (*failed) {
       if (threadIdx.x == 0) *p.status = kDevTimeout;
     } else {
-      float* const mo = reinterpret_cast<float*>(basep);          // [warp][row][DP + 4]
+      float* const mo = reinterpret_cast<float*>(basep);          // [kw][row][DP + 4]
       constexpr int kLd = DP + 4;
-      float* const ml = mo + kWarps * kRows * kLd;                // [warp][row][2]
+      float* const ml = mo + KW * kRows * kLd;                    // [kw][row][2]
+      const int mine = kw * kRows + rw * 16 + g;
 #pragma unroll
       for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(mo + (warp * kRows + g + 8 * h) * kLd + n * 8 + 2 * tq) =
+          *reinterpret_cast<float2*>(mo + (mine + 8 * h) * kLd + n * 8 + 2 * tq) =
               make_float2(o[n][2 * h], o[n][2 * h + 1]);
       if (tq == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ml[(warp * kRows + g + 8 * h) * 2] = m[h];
-          ml[(warp * kRows + g + 8 * h) * 2 + 1] = l[h];
+          ml[(mine + 8 * h) * 2] = m[h];
+          ml[(mine + 8 * h) * 2 + 1] = l[h];
         }
       }
       named_barrier_sync(1, kWarps * 32);
@@ -323,10 +349,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (d >= p.dim) continue;
         float top = -INFINITY, sum = 0.0f, acc = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
+        for (int w = 0; w < KW; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
         const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < KW; ++w) {
           const float f = exp2_approx(ml[(w * kRows + r) * 2] - ref);
           sum += f * ml[(w * kRows + r) * 2 + 1];
           acc += f * mo[(w * kRows + r) * kLd + d];
@@ -357,16 +383,26 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // ---------------------------------------------------------------- host
 
-template <typename T, int DP>
+template <typename T, int DP, int RW>
 cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, cudaStream_t s) {
-  auto kernel = attn_decode_kernel<T, DP>;
+  auto kernel = attn_decode_kernel<T, DP, RW>;
   const cudaError_t e = ensure_dynamic_smem((const void*)kernel, Smem<DP>::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t x = c.kv.nseq * p.tiles_x * p.nsplit;
   if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
   return launch_pdl(kernel, dim3((unsigned)x, (unsigned)c.kv.heads), dim3(kThreads),
                     Smem<DP>::kBytes, s, p, kmap, vmap);
+}
+
+template <typename T, int DP>
+cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, cudaStream_t s) {
+  switch (c.plan.tile_rows) {
+    case 16: return launch_decode<T, DP, 1>(p, c, kmap, vmap, s);
+    case 32: return launch_decode<T, DP, 2>(p, c, kmap, vmap, s);
+    default: return launch_decode<T, DP, 4>(p, c, kmap, vmap, s);
+  }
 }
 
 template <typename T>

@@ -10,9 +10,14 @@
 // Bound by the bytes of the heads, read once and written once. A group of
 // lanes holds whole heads in registers: a lane owns `VEC` pairs (two vectors
 // of VEC values, at i and i + rot_dim/2, or side by side when interleaved), so
-// a rotation needs no exchange and the norm one shuffle sum. The lane's pairs
-// are the same in every head, so one sine and cosine per pair serves the
-// group's RPG heads of a token; their loads are all issued before any is used.
+// a rotation needs no exchange and the norm one shuffle sum. A group takes
+// HEADS heads of one token and issues all their loads before it uses any. The
+// sines and cosines of a block's tokens are computed once for all its groups,
+// into shared memory, while those loads are under way (by every group for
+// itself they were half of the instructions, and those the limit: 77 us for
+// 8192 tokens of 48 heads of 128, where the bytes take 44). A block serves one
+// of the sets (queries, keys, values), so that nothing but the data differs
+// between its threads.
 #include <cmath>
 #include <cstring>
 
@@ -23,151 +28,164 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename TI, typename TO, int VEC, int NU, int RPG>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_kernel(const __grid_constant__ RopeCall c, int lanes, int rows, int chunks,
-                 int64_t items) {
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* y, const float (&x)[N]) {
+  Vec<T, N> v;
+#pragma unroll
+  for (int e = 0; e < N; ++e) v.v[e] = Elem<T>::down(x[e]);
+  *reinterpret_cast<Vec<T, N>*>(y) = v;
+}
+
+struct Cut {            // how the sets are dealt to blocks
+  int lanes;            // of a group, a power of two
+  int first[4];         // first block of each set, and the end
+  int chunks[3];        // groups of a token
+};
+
+template <typename TI, typename TO, int VEC, int NU, int HEADS>
+__global__ void __launch_bounds__(kThreads, 4)
+norm_rope_kernel(const __grid_constant__ RopeCall c, const __grid_constant__ Cut cut) {
+  // (cos, sin) of the block's tokens: groups * pairs of a head at most, which
+  // is kThreads * NU * VEC
+  __shared__ float2 turn[kThreads * NU * VEC];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+  const int k = blockIdx.x < cut.first[1] ? 0 : blockIdx.x < cut.first[2] ? 1 : 2;
+  const HeadSet& hs = c.set[k];
+  const int lanes = cut.lanes, chunks = cut.chunks[k];
+  const int groups = kThreads / lanes;
+  const int64_t items = c.ntok * chunks;
+  const int64_t item0 = (int64_t)(blockIdx.x - cut.first[k]) * groups;
   // groups past the end shadow the last one up to their stores: the shuffles
   // below want whole warps
-  const bool live = item < items;
-  const int64_t it = live ? item : items - 1;
-  const int64_t tok =
-      items <= 0x7fffffff ? (int64_t)((uint32_t)it / (uint32_t)chunks) : it / chunks;
+  const int64_t mine = item0 + threadIdx.x / lanes;
+  const bool live = mine < items;
+  auto token_of = [&](int64_t i) {
+    return items <= 0x7fffffff ? (int64_t)((uint32_t)i / (uint32_t)chunks) : i / chunks;
+  };
+  const int64_t it = live ? mine : items - 1;
+  const int64_t tok = token_of(it), tok0 = token_of(item0);
   const int first = (int)(it - tok * chunks);
   const int lane = threadIdx.x & (lanes - 1);
-  const int units = c.head_dim / (2 * VEC), runits = c.half / VEC;
+  const int units = c.head_dim / (2 * VEC), runits = hs.rotate ? c.half / VEC : 0;
 
-  // this lane's pairs: where their two vectors start in a head, and whether
-  // they are rotated
+  // this lane's pairs: where their two vectors start in a head
   int o0[NU], o1[NU];
-  bool have[NU], rot[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = lane + i * lanes;
-    have[i] = u < units;
-    rot[i] = u < runits;
     o0[i] = 2 * u * VEC;
     o1[i] = o0[i] + VEC;
-    if (rot[i] && !c.interleaved) {
+    if (u < runits && !c.interleaved) {
       o0[i] = u * VEC;
       o1[i] = c.half + u * VEC;
     }
   }
 
-  // loads of all heads of the group
-  Vec<TI, VEC> xa[RPG][NU], xb[RPG][NU];
-  int set[RPG], head[RPG];
+  // the group's heads: first, first + chunks, ...
+  Vec<TI, VEC> xa[HEADS][NU], xb[HEADS][NU];
+  const TI* x = static_cast<const TI*>(hs.x) + tok * hs.x_stride + first * c.head_dim;
 #pragma unroll
-  for (int j = 0; j < RPG; ++j) {
-    int r = first + j * chunks;
-    set[j] = -1;
-    head[j] = 0;
-    if (r < rows) {
-      int k = 0;
-      if (r >= c.set[0].heads) {
-        r -= c.set[0].heads;
-        k = 1;
-        if (r >= c.set[1].heads) {
-          r -= c.set[1].heads;
-          k = 2;
-        }
-      }
-      set[j] = k;
-      head[j] = r;
-      const TI* x = static_cast<const TI*>(c.set[k].x) + tok * c.set[k].x_stride +
-                    (int64_t)r * c.head_dim;
+  for (int j = 0; j < HEADS; ++j)
+    if (first + j * chunks < hs.heads) {
 #pragma unroll
       for (int i = 0; i < NU; ++i)
-        if (have[i]) {
-          xa[j][i] = *reinterpret_cast<const Vec<TI, VEC>*>(x + o0[i]);
-          xb[j][i] = *reinterpret_cast<const Vec<TI, VEC>*>(x + o1[i]);
+        if (lane + i * lanes < units) {
+          xa[j][i] = *reinterpret_cast<const Vec<TI, VEC>*>(x + j * chunks * c.head_dim + o0[i]);
+          xb[j][i] = *reinterpret_cast<const Vec<TI, VEC>*>(x + j * chunks * c.head_dim + o1[i]);
         }
     }
-  }
 
-  const int pos = c.positions ? c.positions[tok] : 0;
-  float cs[NU][VEC], sn[NU][VEC];
-#pragma unroll
-  for (int i = 0; i < NU; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      cs[i][e] = 1.0f;
-      sn[i][e] = 0.0f;
-      if (rot[i]) {
-        const uint64_t f = c.turns[(lane + i * lanes) * VEC + e];
-        // signed fraction of a turn in [-1/2, 1/2); sincospif wants half turns
-        const float t = (float)(int64_t)((uint64_t)(int64_t)pos * f) * 0x1p-63f;
-        sincospif(t, &sn[i][e], &cs[i][e]);
-        cs[i][e] *= c.amplitude;
-        sn[i][e] *= c.amplitude;
-      }
+  if (runits > 0) {
+    const int n = ((int)(token_of(min(item0 + groups, items) - 1) - tok0) + 1) * c.half;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int t = i / c.half;
+      const int pos = c.positions[tok0 + t];
+      // the upper half of the 64-bit fraction, a signed 32-bit one of a turn
+      const uint64_t frac = (uint64_t)(int64_t)pos * c.turns[i - t * c.half];
+      float s, co;
+      sincospif((float)(int32_t)(frac >> 32) * 0x1p-31f, &s, &co);
+      turn[i] = make_float2(co * c.amplitude, s * c.amplitude);
     }
+    __syncthreads();
+  }
 
   // where the token goes in the cache
   int64_t slot = -1;
   bool write = live;
   if (c.append) {
+    const int pos = c.positions[tok];
     if (pos < 0) {
       write = false;   // padding
-    } else {
+    } else if (k > 0) {
       const int seq = c.seq_ids[tok];
       const int lp = pos / (int)c.kv.page_size;
       int page = -1;
       if (seq >= 0 && seq < c.kv.nseq && lp < c.kv.table_width)
         page = c.kv.block_table[seq * c.kv.table_stride + lp];
-      if (page >= 0 && page < c.kv.pages)
+      if (page >= 0 && page < c.kv.pages) {
         slot = page * c.kv.page_stride + (pos - lp * (int)c.kv.page_size) * c.kv.slot_stride;
-      else if (lane == 0 && live)
-        *c.status = kDevIndex;
+      } else {
+        if (lane == 0 && live) *c.status = kDevIndex;
+        write = false;
+      }
     }
   }
+  TO* y = hs.y ? static_cast<TO*>(hs.y) + tok * hs.y_stride
+               : static_cast<TO*>(k == 1 ? c.kv.k : c.kv.v) + slot;
+  const int64_t y_head = hs.y ? c.head_dim : c.kv.head_stride;
+
+  float wa[NU][VEC], wb[NU][VEC];
+  if (hs.w) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const bool have = lane + i * lanes < units;
+        wa[i][e] = have ? __ldg(hs.w + o0[i] + e) : 0.0f;
+        wb[i][e] = have ? __ldg(hs.w + o1[i] + e) : 0.0f;
+      }
+  }
+  const float2* const cs = turn + (tok - tok0) * c.half;
 
 #pragma unroll
-  for (int j = 0; j < RPG; ++j) {
-    const int k = set[j];
+  for (int j = 0; j < HEADS; ++j) {
+    const int head = first + j * chunks;
+    const bool there = head < hs.heads;
     float a[NU][VEC], b[NU][VEC], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        a[i][e] = b[i][e] = 0.0f;
-        if (k >= 0 && have[i]) {
-          a[i][e] = Elem<TI>::up(xa[j][i].v[e]);
-          b[i][e] = Elem<TI>::up(xb[j][i].v[e]);
-          sum += a[i][e] * a[i][e] + b[i][e] * b[i][e];
-        }
+        const bool have = there && lane + i * lanes < units;
+        a[i][e] = have ? Elem<TI>::up(xa[j][i].v[e]) : 0.0f;
+        b[i][e] = have ? Elem<TI>::up(xb[j][i].v[e]) : 0.0f;
+        sum = fmaf(a[i][e], a[i][e], fmaf(b[i][e], b[i][e], sum));
       }
-    for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (k < 0 || !write) continue;
-    const HeadSet& hs = c.set[k];
-    TO* y;
-    if (hs.y) {
-      y = static_cast<TO*>(hs.y) + tok * hs.y_stride + (int64_t)head[j] * c.head_dim;
-    } else {
-      if (slot < 0) continue;
-      y = static_cast<TO*>(k == 1 ? c.kv.k : c.kv.v) + slot + (int64_t)head[j] * c.kv.head_stride;
-    }
-    const float r = hs.w ? 1.0f / sqrtf(sum / (float)c.head_dim + c.eps) : 1.0f;
+    if (hs.w) {
+      for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const float r = rsqrtf(sum / (float)c.head_dim + c.eps);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (!have[i]) continue;
-      if (hs.w) {
+      for (int i = 0; i < NU; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          a[i][e] = a[i][e] * r * __ldg(hs.w + o0[i] + e);
-          b[i][e] = b[i][e] * r * __ldg(hs.w + o1[i] + e);
+          a[i][e] *= r * wa[i][e];
+          b[i][e] *= r * wb[i][e];
         }
-      }
-      if (hs.rotate && rot[i]) {
+    }
+    if (!there || !write) continue;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = lane + i * lanes;
+      if (u >= units) continue;
+      if (u < runits) {
         if (!c.interleaved) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
+            const float2 t = cs[u * VEC + e];
             const float p = a[i][e], q = b[i][e];
-            a[i][e] = p * cs[i][e] - q * sn[i][e];
-            b[i][e] = q * cs[i][e] + p * sn[i][e];
+            a[i][e] = p * t.x - q * t.y;
+            b[i][e] = q * t.x + p * t.y;
           }
         } else {
           // the unit's 2 VEC values are consecutive: pair n is values 2n, 2n + 1
@@ -179,9 +197,10 @@ norm_rope_kernel(const __grid_constant__ RopeCall c, int lanes, int rows, int ch
           }
 #pragma unroll
           for (int n = 0; n < VEC; ++n) {
+            const float2 t = cs[u * VEC + n];
             const float p = z[2 * n], q = z[2 * n + 1];
-            z[2 * n] = p * cs[i][n] - q * sn[i][n];
-            z[2 * n + 1] = q * cs[i][n] + p * sn[i][n];
+            z[2 * n] = p * t.x - q * t.y;
+            z[2 * n + 1] = q * t.x + p * t.y;
           }
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
@@ -190,31 +209,29 @@ norm_rope_kernel(const __grid_constant__ RopeCall c, int lanes, int rows, int ch
           }
         }
       }
-      Vec<TO, VEC> ya, yb;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        ya.v[e] = Elem<TO>::down(a[i][e]);
-        yb.v[e] = Elem<TO>::down(b[i][e]);
-      }
-      *reinterpret_cast<Vec<TO, VEC>*>(y + o0[i]) = ya;
-      *reinterpret_cast<Vec<TO, VEC>*>(y + o1[i]) = yb;
+      store_vec<TO, VEC>(y + head * y_head + o0[i], a[i]);
+      store_vec<TO, VEC>(y + head * y_head + o1[i], b[i]);
     }
   }
 }
 
-template <typename TI, typename TO, int VEC, int NU, int RPG>
+template <typename TI, typename TO, int VEC, int NU, int HEADS>
 cudaError_t launch_as(const RopeCall& c, cudaStream_t s) {
   const int units = c.head_dim / (2 * VEC);
-  int lanes = 1;
-  while (lanes < 32 && lanes < units) lanes *= 2;
-  const int rows = c.set[0].heads + c.set[1].heads + c.set[2].heads;
-  const int chunks = (rows + RPG - 1) / RPG;
-  const int64_t items = c.ntok * chunks;
-  const int per_cta = kThreads / lanes;
-  const int64_t grid = (items + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(norm_rope_kernel<TI, TO, VEC, NU, RPG>, dim3((unsigned)grid), dim3(kThreads),
-                    0, s, c, lanes, rows, chunks, items);
+  Cut cut = {};
+  cut.lanes = 1;
+  while (cut.lanes < 32 && cut.lanes < units) cut.lanes *= 2;
+  const int groups = kThreads / cut.lanes;
+  int64_t grid = 0;
+  for (int k = 0; k < 3; ++k) {
+    cut.first[k] = (int)grid;
+    cut.chunks[k] = (c.set[k].heads + HEADS - 1) / HEADS;
+    grid += (c.ntok * cut.chunks[k] + groups - 1) / groups;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  }
+  cut.first[3] = (int)grid;
+  return launch_pdl(norm_rope_kernel<TI, TO, VEC, NU, HEADS>, dim3((unsigned)grid),
+                    dim3(kThreads), 0, s, c, cut);
 }
 
 // Widest vectors that the sizes, strides and addresses allow.
@@ -238,7 +255,7 @@ cudaError_t launch_types(const RopeCall& c, cudaStream_t s) {
   const int64_t rows = c.set[0].heads + c.set[1].heads + c.set[2].heads;
   switch (vector_width(c)) {
     case 4:
-      // one head per group where heads are few, so that all SMs get some
+      // one head a group where heads are few, so that all SMs get some
       if (c.ntok * rows < 8192) return launch_as<TI, TO, 4, 1, 1>(c, s);
       return launch_as<TI, TO, 4, 1, 4>(c, s);
     case 2: return launch_as<TI, TO, 2, 2, 2>(c, s);
