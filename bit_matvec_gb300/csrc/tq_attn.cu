@@ -113,6 +113,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.lse = c.lse;
   p.part_o = c.part_o;
   p.part_lse = c.part_lse;
+  p.cuts = c.cuts;
   p.q_start = c.q_start;
   p.kv_len = c.kv_len;
   p.table = c.kv.block_table;
@@ -142,7 +143,8 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   cudaError_t e = cache_map(&kmap, c.kv, c.kv.k, p.box_rows);
   if (e == cudaSuccess) e = cache_map(&vmap, c.kv, c.kv.v, p.box_rows);
   if (e != cudaSuccess) return e;
-  e = c.plan.chunk ? launch_attn_chunk(p, c, kmap, vmap, s) : launch_attn_decode(p, c, kmap, vmap, s);
+  if (c.plan.chunk) return launch_attn_chunk(p, c, kmap, vmap, s);
+  e = launch_attn_decode(p, c, kmap, vmap, s);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   const int64_t grid = c.ntok * c.q_heads;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;

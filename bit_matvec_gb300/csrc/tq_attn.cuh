@@ -56,11 +56,13 @@ constexpr int kMaxSplits = 128;    // key ranges of a row tile
 // the workspace size is too.
 struct AttnPlan {
   bool chunk;           // the kernel for many rows
-  int tile_rows;        // rows (token, query head) of a thread block
+  int tile_rows;        // rows (token, query head) of a row tile
   int key_tile;         // keys of a tile
-  int64_t tiles_x;      // row tiles of a sequence (few rows) or of all (many)
-  int nsplit;           // key ranges per row tile
-  int chunk_tiles;      // key tiles of a range
+  int64_t tiles_x;      // row tiles: of a sequence (few rows), numbers for all (many)
+  int nsplit;           // few rows: key ranges of a row tile,
+  int chunk_tiles;      // and key tiles of a range
+  int blocks;           // many rows: thread blocks
+  int64_t part_rows;    // rows of partial results
   int64_t ws_bytes;
 };
 AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads,
@@ -79,8 +81,11 @@ struct AttnCall {
   int64_t ntok, q_heads, max_q, max_kv;
   float scale;
   int64_t window;
-  float* part_o;        // [nsplit][ntok][q_heads][head_dim] (nsplit > 1)
-  float* part_lse;      // [nsplit][ntok][q_heads], base-2 logarithms
+  // partial results: few rows [nsplit][ntok][q_heads] rows (nsplit > 1), many
+  // rows two row tiles a block
+  float* part_o;        // [part_rows][head_dim]
+  float* part_lse;      // [part_rows], base-2 logarithms
+  void* cuts;
   int* status;
   AttnPlan plan;
 };

@@ -105,6 +105,7 @@ int take_rope(RopeCall& c, const float* qw, const float* kw, float eps, const tq
 
 // The planner's idea of the GPU.
 constexpr int64_t kPlanSms = 152;
+constexpr int64_t kCutBytes = 32;   // a CutTile of the kernel for many rows
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -115,38 +116,40 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   AttnPlan p = {};
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
-  // up to 64 rows stay in one block of the kernel for few rows
+  // up to 32 rows stay in one block of the kernel for few rows, which runs at
+  // the memory's rate there; from about 64 on the rate of mma.sync limits it
   const int64_t rows = max_q * group;
-  p.chunk = rows > 64;
-  p.tile_rows = p.chunk ? 256 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+  p.chunk = rows > 32;
+  p.tile_rows = p.chunk ? 256 : rows > 16 ? 32 : 16;
   p.key_tile = p.chunk || head_dim <= 64 ? 128 : 64;
-  const int64_t slots = p.chunk ? kPlanSms : 2 * kPlanSms;
-  int64_t units;
   if (p.chunk) {
     p.tiles_x = ntok * group / p.tile_rows + nseq;
-    units = kv_heads * (ceil_div(max_q * group, p.tile_rows) == 1 ? nseq
-                                                                  : ceil_div(ntok * group, p.tile_rows));
-  } else {
-    p.tiles_x = 1;
-    units = kv_heads * nseq;
+    p.blocks = (int)kPlanSms;
+    p.nsplit = 1;
+    p.part_rows = 2 * kPlanSms * p.tile_rows;
+    p.ws_bytes = ceil_div(p.part_rows * (head_dim + 1) * 4, 16) * 16 + kPlanSms * kCutBytes;
+    return p;
   }
+  p.tiles_x = 1;
+  const int64_t units = kv_heads * nseq, slots = 2 * kPlanSms;
   // keys that a row tile sees at most, in tiles (one more where the window
   // does not start on a tile)
   int64_t span = max_kv;
   if (window > 0 && window + max_q < span) span = window + max_q;
   int64_t tiles = ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0);
   if (tiles < 1) tiles = 1;
-  // Few blocks: split the keys until every slot has one. Many of the small
-  // ones: ranges of 2048 keys or more, so that ragged lengths spread evenly.
+  // Few blocks: split the keys until every slot has one. Many: ranges of 2048
+  // keys or more, so that ragged lengths spread evenly.
   int64_t split = slots / units;
   const int64_t spread = tiles * p.key_tile / 2048;
-  if (!p.chunk && split < spread) split = units >= 16 * slots ? 1 : spread;
+  if (split < spread) split = units >= 16 * slots ? 1 : spread;
   if (split > tiles * p.key_tile / 256) split = tiles * p.key_tile / 256;   // 256 keys or more
   if (split > kMaxSplits) split = kMaxSplits;
   if (split < 1) split = 1;
   p.chunk_tiles = (int)ceil_div(tiles, split);
   p.nsplit = (int)ceil_div(tiles, p.chunk_tiles);
-  p.ws_bytes = p.nsplit > 1 ? (p.nsplit * ntok * q_heads * (head_dim + 1) * 4 + 15) / 16 * 16 : 0;
+  p.part_rows = p.nsplit > 1 ? p.nsplit * ntok * q_heads : 0;
+  p.ws_bytes = ceil_div(p.part_rows * (head_dim + 1) * 4, 16) * 16;
   return p;
 }
 
@@ -358,7 +361,8 @@ int tq_paged_attention(const void* Q, int64_t q_stride, const tq_paged_kv* kv,
   c.window = window;
   if (need > 0) {
     c.part_o = static_cast<float*>(workspace);
-    c.part_lse = c.part_o + (int64_t)c.plan.nsplit * ntok * q_heads * dim;
+    c.part_lse = c.part_o + c.plan.part_rows * dim;
+    if (c.plan.chunk) c.cuts = static_cast<char*>(workspace) + (need - c.plan.blocks * kCutBytes);
   }
   cudaError_t e = status_word(&c.status);
   if (e != cudaSuccess) return fail_cuda(e);

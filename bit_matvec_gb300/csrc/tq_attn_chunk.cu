@@ -2,19 +2,28 @@
 // time over the paged cache, on the tcgen05 tensor cores.
 //
 // The formulas are those of tq_attn_decode.cu. Bound by the tensor rate: 4 D
-// flop for each row and key it sees. A thread block takes 256 rows that share
-// a key/value head (all its query heads, consecutive tokens) as two halves of
-// 128, and streams 128-key tiles of K and V through a ring of shared-memory
-// slots (TMA boxes, one per page piece). For each tile and half:
+// flop for each row and key it sees. A row tile is up to 256 rows that share a
+// key/value head (all its query heads, consecutive tokens). A thread block
+// streams 128-key tiles of K and V through a ring of shared-memory slots (TMA
+// boxes, one per page piece) and keeps two softmaxes of 128 rows going:
 //   S = Q K^T     tcgen05.mma, both operands in shared memory, S in TMEM;
 //   P = 2^(c S - M) one thread per row: no exchange between threads; M moves
 //                 only when a row's maximum exceeds it by 2^8 (the quotient at
 //                 the end makes any M right), and then O is rescaled in TMEM;
 //   O += P V      P as the A operand from TMEM, written over S; V is read
 //                 as stored, its 64-value rows being the N-major order.
-// While one half's softmax runs, the tensor cores work on the other half.
-// Two halves to a block, and not a block each, because K and V then cross
-// from L2 once for both: at 128 rows a block they would need about 16 TB/s.
+// While one softmax runs, the tensor cores work for the other. With more than
+// 128 rows the two are the halves of the row tile, on the same keys: K and V
+// then cross from L2 once for both (at 128 rows a block they would need about
+// 16 TB/s). With up to 128 rows both take the same rows, on alternate key
+// tiles, and are merged at the end.
+//
+// The work, every key tile of every row tile of every head, is laid in one
+// line (head, sequence, row tile, key tile) and cut into equal pieces, one for
+// each block: lengths, causality and the number of SMs then leave no SM idle,
+// and a row tile is cut at most where a piece ends. Blocks find their piece
+// from q_start and kv_len on the device. Cut row tiles leave partial results,
+// which a second kernel joins.
 #include <type_traits>
 
 #include "tq_attn_dev.cuh"
@@ -25,17 +34,42 @@ namespace {
 
 using namespace tc;
 
-constexpr int kHalf = 128;            // rows of a half: one warpgroup, one row a thread
-constexpr int kRows = 2 * kHalf;
+constexpr int kHalf = 128;            // rows of a softmax: one warpgroup, one row a thread
+constexpr int kRows = 2 * kHalf;      // rows of a tile
 constexpr int kKeys = 128;            // keys of a tile
-constexpr int kThreads = 2 * kHalf + 64;   // two softmax warpgroups, an MMA and a TMA warp
+constexpr int kThreads = 384;         // two softmax warpgroups; MMA, TMA and scheduling warps
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
+constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
+// Cost of a row tile in units of half a key tile of 256 rows: what starting
+// and ending it takes, and the least work worth a block of its own.
+constexpr int kTileCost = 4, kLeastWork = 6;
+
+// A block's share of one row tile.
+struct Segment {
+  int n;              // key tiles; -1: no more segments
+  int t0;             // first key tile
+  int tok;            // token of the tile's first row
+  int off;            // query head of that row within the group
+  int rows;
+  int pos;            // position of that token
+  int lo, hi;         // keys [lo, hi) are seen by some row
+  int head, seq;
+  int part;           // where the partial result goes, -1: whole, to the output
+};
 
 template <int DP> struct Smem {
   static constexpr int kSlots = DP == 128 ? 5 : 8;
   static constexpr int kTile = kKeys * DP * 2;      // bytes of a K or V tile, and of half the queries
   static constexpr int kBars = (2 + kSlots) * kTile;
-  static constexpr int kBytes = kBars + 256 + 1024; // + barriers and flags + alignment
+  // barriers: two a slot, then queries 2, scores 2, weights 4, queue, drain
+  static constexpr int kBarBytes = 8 * (2 * kSlots + 8 + 2 * kQueue + 1);
+  static constexpr int kFlags = kBars + (kBarBytes + 63) / 64 * 64;
+  static constexpr int kSegs = kFlags + 64;
+  static constexpr int kScan = kSegs + kQueue * 64;
+  static constexpr int kStats = kScan + 192;        // maxima and sums of 128 rows
+  static constexpr int kBytes = kStats + 1024 + 1024;   // with room to align
+  static_assert(kBytes <= 232448, "227 KB a block");
+  static_assert(kQueue * sizeof(Segment) <= 256 && kFlags % 16 == 0, "regions");
 };
 
 // K-major operand in 128-byte-swizzled rows of 64 values: 8-row groups 1024
@@ -58,31 +92,102 @@ template <typename T, int DP> struct Desc {
   static constexpr uint32_t kOut = idesc_f16(kHalf, DP) | kType | (1u << 16);
 };
 
-// 64 columns of this thread's TMEM lane -> registers.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&r)[64]) {
+// One lane of the (converged) warp, the same every time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t is;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
+// The MMAs and commits of one warp: every lane computes the operands, so that
+// they stay in uniform registers, and the elected one (`lead`) issues. (Issued
+// from a branch of one lane, an MMA measured 80 to 115 cycles of its thread,
+// more than the 64 it runs.)
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(bar), "r"(lead)
+      : "memory");
+}
+
+// 128 columns of this thread's TMEM lane -> registers.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&a)[64], float (&b)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
       "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+      "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%129];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-        "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]),
-        "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
-        "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]), "=f"(r[33]), "=f"(r[34]),
-        "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]), "=f"(r[41]),
-        "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]),
-        "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]),
-        "=f"(r[56]), "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]),
-        "=f"(r[63])
-      : "r"(taddr)
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]),
+        "=f"(a[7]), "=f"(a[8]), "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]),
+        "=f"(a[14]), "=f"(a[15]), "=f"(a[16]), "=f"(a[17]), "=f"(a[18]), "=f"(a[19]), "=f"(a[20]),
+        "=f"(a[21]), "=f"(a[22]), "=f"(a[23]), "=f"(a[24]), "=f"(a[25]), "=f"(a[26]), "=f"(a[27]),
+        "=f"(a[28]), "=f"(a[29]), "=f"(a[30]), "=f"(a[31]), "=f"(a[32]), "=f"(a[33]), "=f"(a[34]),
+        "=f"(a[35]), "=f"(a[36]), "=f"(a[37]), "=f"(a[38]), "=f"(a[39]), "=f"(a[40]), "=f"(a[41]),
+        "=f"(a[42]), "=f"(a[43]), "=f"(a[44]), "=f"(a[45]), "=f"(a[46]), "=f"(a[47]), "=f"(a[48]),
+        "=f"(a[49]), "=f"(a[50]), "=f"(a[51]), "=f"(a[52]), "=f"(a[53]), "=f"(a[54]), "=f"(a[55]),
+        "=f"(a[56]), "=f"(a[57]), "=f"(a[58]), "=f"(a[59]), "=f"(a[60]), "=f"(a[61]), "=f"(a[62]),
+        "=f"(a[63]), "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]),
+        "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]),
+        "=f"(b[13]), "=f"(b[14]), "=f"(b[15]), "=f"(b[16]), "=f"(b[17]), "=f"(b[18]), "=f"(b[19]),
+        "=f"(b[20]), "=f"(b[21]), "=f"(b[22]), "=f"(b[23]), "=f"(b[24]), "=f"(b[25]), "=f"(b[26]),
+        "=f"(b[27]), "=f"(b[28]), "=f"(b[29]), "=f"(b[30]), "=f"(b[31]), "=f"(b[32]), "=f"(b[33]),
+        "=f"(b[34]), "=f"(b[35]), "=f"(b[36]), "=f"(b[37]), "=f"(b[38]), "=f"(b[39]), "=f"(b[40]),
+        "=f"(b[41]), "=f"(b[42]), "=f"(b[43]), "=f"(b[44]), "=f"(b[45]), "=f"(b[46]), "=f"(b[47]),
+        "=f"(b[48]), "=f"(b[49]), "=f"(b[50]), "=f"(b[51]), "=f"(b[52]), "=f"(b[53]), "=f"(b[54]),
+        "=f"(b[55]), "=f"(b[56]), "=f"(b[57]), "=f"(b[58]), "=f"(b[59]), "=f"(b[60]), "=f"(b[61]),
+        "=f"(b[62]), "=f"(b[63])
+      : "r"(taddr), "r"(taddr + 64)
       : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Registers a thread: the softmax warpgroups take what the third one leaves
+// (2 x 224 + 56 = 3 x 168, what the block was launched with).
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+}
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+}
+
+// 16 bytes from global to shared memory, in the background; zeros if !use.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool use) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Minus infinity into the scores n of a 64-key piece outside (lo, hi].
@@ -121,22 +226,90 @@ __device__ __forceinline__ void weights64(const float (&s)[64], uint64_t scale2,
   tmem_st32(taddr, w);
 }
 
+// The row tiles of sequence b are numbered from f(b) = floor(q_start[b] * group
+// / kRows) + b, which leaves each sequence room for all of its own (and some
+// numbers empty).
+struct Tiles {
+  const AttnParams& p;
+  __device__ __forceinline__ int start(int b) const {
+    return min(max(p.q_start[b], 0), (int)p.ntok);
+  }
+  __device__ __forceinline__ int64_t first(int b) const {
+    return (int64_t)start(b) * p.group / kRows + b;
+  }
+  // the sequence that tile number s belongs to
+  __device__ __forceinline__ int find(int64_t s) const {
+    int lo = 0, hi = p.nseq;   // f(lo) <= s < f(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first(mid) <= s) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
+// Row tile `s` of sequence `b`, whole; n = -1 if the number is an empty one.
+__device__ __forceinline__ Segment row_tile(const AttnParams& p, int64_t s, int b) {
+  const Tiles tiles{p};
+  Segment g = {};
+  g.n = -1;
+  const int q0 = tiles.start(b), qn = max(tiles.start(b + 1) - q0, 0);
+  const int64_t row0 = (s - tiles.first(b)) * kRows;
+  if (row0 >= (int64_t)qn * p.group) return g;
+  const int kv = max(p.kv_len[b], 0);
+  const int t = (int)(row0 / p.group);
+  g.seq = b;
+  g.off = (int)(row0 - (int64_t)t * p.group);
+  g.rows = (int)min((int64_t)kRows, (int64_t)qn * p.group - row0);
+  g.tok = q0 + t;
+  g.pos = kv - qn + t;
+  g.hi = max(g.pos + (g.off + g.rows - 1) / p.group + 1, 0);
+  g.lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)g.pos - p.window + 1) : 0;
+  g.t0 = g.lo / kKeys;
+  g.n = max((g.hi + kKeys - 1) / kKeys - g.t0, 0);
+  return g;
+}
+__device__ __forceinline__ int unit_cost(const Segment& g) { return g.rows > kHalf ? 2 : 1; }
+__device__ __forceinline__ int64_t tile_cost(const Segment& g) {
+  return g.n < 0 ? 0 : kTileCost + (int64_t)g.n * unit_cost(g);
+}
+
+__device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// A row tile that was cut: its rows, and where its partial results are.
+struct CutTile {
+  int n;              // pieces; 0: none here
+  int part0;          // the first, then 2 (block + 1), 2 (block + 2), ...
+  int tok, off, rows, head;
+  int pad[2];
+};
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap) {
+                  const __grid_constant__ CUtensorMap vmap, int64_t numbers) {
   using S = Smem<DP>;
   constexpr int kSlots = S::kSlots, kSub = DP / 64;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const basep = smem_raw + (base - smem_u32(smem_raw));
-  // queries of the two halves, then the ring, then the barriers
+  // queries of the two softmaxes, then the ring, then the barriers
   const uint32_t ring = base + 2 * S::kTile;
-  const uint32_t bars = base + S::kBars;
-  const uint32_t full = bars, empty = bars + 8 * kSlots, q_full = empty + 8 * kSlots;
-  const uint32_t s_full = q_full + 8, p_ready = s_full + 16, drain = p_ready + 16;
-  volatile uint32_t* const shared = reinterpret_cast<volatile uint32_t*>(basep + S::kBars + 192);
-  volatile uint32_t* const failed = shared + 1;   // shared[0]: TMEM address, [2]: sequence
+  const uint32_t full = base + S::kBars, empty = full + 8 * kSlots, q_full = empty + 8 * kSlots;
+  const uint32_t s_full = q_full + 16, p_ready = s_full + 16, seg_full = p_ready + 32;
+  const uint32_t seg_empty = seg_full + 8 * kQueue, drain = seg_empty + 8 * kQueue;
+  static_assert(S::kBarBytes == 8 * (2 * kSlots) + 16 + 16 + 32 + 16 * kQueue + 8, "barriers");
+  volatile uint32_t* const flags = reinterpret_cast<volatile uint32_t*>(basep + S::kFlags);
+  volatile uint32_t* const failed = flags + 1;   // flags[0]: TMEM address
+  Segment* const queue = reinterpret_cast<Segment*>(basep + S::kSegs);
+  int64_t* const scan = reinterpret_cast<int64_t*>(basep + S::kScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -144,241 +317,156 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       mbarrier_init(full + 8 * i, 1);
       mbarrier_init(empty + 8 * i, 1);
     }
-    mbarrier_init(q_full, 2 * kHalf);
     for (int i = 0; i < 2; ++i) {
+      mbarrier_init(q_full + 8 * i, kHalf);
       mbarrier_init(s_full + 8 * i, 1);
-      mbarrier_init(p_ready + 8 * i, 4);
+      mbarrier_init(p_ready + 16 * i, 4);       // weights of the first 64 keys
+      mbarrier_init(p_ready + 16 * i + 8, 4);   // and of the others
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbarrier_init(seg_full + 8 * i, 1);
+      mbarrier_init(seg_empty + 8 * i, 10);   // MMA, TMA and softmax warps
     }
     mbarrier_init(drain, 1);
     *failed = 0;
+    flags[2] = 0;
     mbarrier_init_fence();
   }
   if (warp == 8) {
-    tmem_alloc<1>(smem_u32(const_cast<uint32_t*>(shared)), 512);
+    tmem_alloc<1>(smem_u32(const_cast<uint32_t*>(flags)), 512);
     tmem_relinquish<1>();
   }
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  // The block's row tile. The tiles of sequence b are numbered from
-  // f(b) = floor(q_start[b] * group / kRows) + b, which leaves each sequence
-  // room for all of its own; the last (longest) tiles start first.
-  const int head = blockIdx.y;
-  const int split = blockIdx.x % p.nsplit;
-  const int64_t slot = p.tiles_x - 1 - (int64_t)(blockIdx.x / p.nsplit);
-  const int ntok = (int)p.ntok;
-  auto first_slot = [&](int b) {
-    const int64_t q = min(max(p.q_start[b], 0), ntok);
-    return q * p.group / kRows + b;
-  };
-  if (warp == 9) {
-    int lo = 0, hi = p.nseq;   // f(lo) <= slot < f(hi): 32 probes a step
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + lane * step;
-      const uint32_t below = __ballot_sync(0xffffffffu, at < hi && first_slot(at) <= slot);
-      const int n = max(__popc(below), 1);
-      lo += (n - 1) * step;
-      hi = min(lo + step, hi);
-    }
-    if (lane == 0) shared[2] = (uint32_t)lo;
+  // The block's piece [x0, x1) of the line of work: each thread adds up the
+  // cost of some consecutive row tiles of a head, a scan gives the totals.
+  const Tiles tiles{p};
+  const int64_t per = (numbers + kThreads - 1) / kThreads;
+  const int64_t i0 = min((int64_t)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
+  int64_t mine = 0;
+  const int b0 = i0 < i1 ? tiles.find(i0) : 0;
+  for (int64_t s = i0, b = b0; s < i1; ++s) {
+    while (b + 1 < p.nseq && tiles.first((int)b + 1) <= s) ++b;
+    mine += tile_cost(row_tile(p, s, (int)b));
   }
+  int64_t before = scan_warp(mine, lane);
+  if (lane == 31) scan[warp] = before;
+  before -= mine;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = shared[0];
-  const int seq = (int)shared[2];
-  const int q0 = min(max(p.q_start[seq], 0), ntok);
-  const int qn = min(max(p.q_start[seq + 1], q0), ntok) - q0;
-  const int kv = max(p.kv_len[seq], 0);
-  const int64_t tile = slot - first_slot(seq);
-  const int64_t row0 = tile * kRows;
-  const int rows = (int)min((int64_t)kRows, (int64_t)qn * p.group - row0);
-  if (tile == 0 && split == 0 && head == 0 && threadIdx.x == 0 &&
-      (qn > p.max_q || (int64_t)kv > p.table_width * p.page_size))
-    *p.status = kDevIndex;
-  const int tok0 = rows > 0 ? (int)(row0 / p.group) : 0;      // the tile's first token
-  const int off0 = rows > 0 ? (int)(row0 - (int64_t)tok0 * p.group) : 0;
-  // keys [lo, hi) are seen by some row
-  const int pos_first = kv - qn + tok0;
-  const int pos_last = rows > 0 ? kv - qn + tok0 + (off0 + rows - 1) / p.group : -1;
-  const int hi = max(pos_last + 1, 0);
-  const int lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos_first - p.window + 1) : 0;
-  const int t_lo = lo / kKeys, t_hi = (hi + kKeys - 1) / kKeys;
-  const int t0 = min(t_lo + split * p.chunk_tiles, t_hi);
-  const int t1 = rows <= 0 ? t0 : split == p.nsplit - 1 ? t_hi : min(t0 + p.chunk_tiles, t_hi);
-  const int nt = t1 - t0;
-  const bool two = rows > kHalf;
-
-  if (nt > 0) {
-    if (warp == 9) {
-      // ------------------------------------------------ TMA producer
-      const int boxes = kKeys / p.box_rows;   // 1 .. 16, one lane each
-      const int off = lane * p.box_rows;
-      bool bad = false;
-      int page = p.pages, pslot = 0;
-      // page and slot of this lane's box of tile t; the page one past the
-      // cache (zeros, nothing read) where no row sees the box
-      auto locate = [&](int t) {
-        const int key = t * kKeys + off;
-        page = p.pages;
-        pslot = 0;
-        if (lane < boxes && t < t1 && key < hi && key + p.box_rows > lo) {
-          const int lp = key / p.page_size;
-          pslot = key - lp * p.page_size;
-          int pg = -1;
-          if (lp < p.table_width) pg = p.table[seq * p.table_stride + lp];
-          if (pg >= 0 && pg < p.pages) page = pg;
-          else bad = true;
-        }
-      };
-      locate(t0);
-      int it = 0;
-      for (int j = 0; j < nt && !*failed; ++j) {
-        const int pg = page, sl = pslot;
-        locate(t0 + j + 1);
-        for (int v = 0; v < 2; ++v, ++it) {
-          const int sidx = it % kSlots;
-          if (it >= kSlots && !mbarrier_wait_bounded(empty + 8 * sidx, (it / kSlots - 1) & 1, kWaitNs)) {
-            *failed = 1;
-            break;
-          }
-          if (lane == 0) mbarrier_arrive_expect_tx(full + 8 * sidx, S::kTile);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = ring + sidx * S::kTile + off * 128;
-#pragma unroll
-            for (int c = 0; c < kSub; ++c)
-              tma_box(dst + c * kKeys * 128, v ? &vmap : &kmap, c * 64, sl, head, pg, full + 8 * sidx);
-          }
-        }
-      }
-      if (bad) *p.status = kDevIndex;
-      __syncwarp();
-      // no block leaves before its copies have landed
-      if (*failed && lane < kSlots && it > lane)
-        mbarrier_wait_bounded(full + 8 * lane, ((it - 1 - lane) / kSlots) & 1, kWaitNs / 10);
-    } else if (warp == 8) {
-      // ------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = Desc<T, DP>::kScores, idesc_o = Desc<T, DP>::kOut;
-        auto qk = [&](int h, int item) {
-          const uint32_t a = base + h * S::kTile, b = ring + (item % kSlots) * S::kTile;
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d) {
-            const uint32_t o = (d >> 2) * kKeys * 128 + (d & 3) * 32;
-            mma_f16_ss(tmem + h * kKeys, desc_k(a + o), desc_k(b + o), idesc_s, d > 0);
-          }
-        };
-        auto pv = [&](int h, int item, bool first) {
-          const uint32_t b = ring + (item % kSlots) * S::kTile;
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_f16_tmem_a(tmem + 256 + h * DP, tmem + h * kKeys + k * 8, desc_n(b + k * 2048), idesc_o,
-                           !(first && k == 0));
-        };
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (*failed || !mbarrier_wait_bounded(bar, parity, kWaitNs)) {
-            *failed = 1;
-            return false;
-          }
-          return true;
-        };
-        auto wait_item = [&](int item) { return wait(full + 8 * (item % kSlots), (item / kSlots) & 1); };
-        bool ok = wait(q_full, 0) && wait_item(0);
-        if (ok) {
-          tc_fence_after();
-          qk(0, 0);
-          mma_commit(s_full);
-          if (two) {
-            qk(1, 0);
-            mma_commit(s_full + 8);
-          }
-          mma_commit(empty);
-        }
-        for (int j = 0; j < nt && ok; ++j) {
-          const int vi = 2 * j + 1, ki = 2 * j + 2;
-          const bool more = j + 1 < nt;
-          ok = wait_item(vi) && wait(p_ready, j & 1);
-          if (!ok) break;
-          tc_fence_after();
-          pv(0, vi, j == 0);
-          if (more) {
-            ok = wait_item(ki);
-            if (!ok) break;
-            qk(0, ki);
-          }
-          mma_commit(s_full);
-          if (two) {
-            ok = wait(p_ready + 8, j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            pv(1, vi, j == 0);
-            mma_commit(empty + 8 * (vi % kSlots));
-            if (more) qk(1, ki);
-            mma_commit(s_full + 8);
-          } else {
-            mma_commit(empty + 8 * (vi % kSlots));
-          }
-          if (more) mma_commit(empty + 8 * (ki % kSlots));
-        }
-        if (*failed) {   // the MMAs issued end before TMEM is freed
-          mma_commit(drain);
-          mbarrier_wait_bounded(drain, 0, kWaitNs / 10);
-        }
-      }
-      __syncwarp();
-    }
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) before += total;
+    total += scan[w];
   }
+  const uint32_t tmem = flags[0];
+  const int heads = p.q_heads / p.group;
+  const int64_t all = total * heads;
+  const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, all / kLeastWork));
+  const int64_t x0 = blockIdx.x < blocks ? all * blockIdx.x / blocks : all;
+  const int64_t x1 = blockIdx.x < blocks ? all * (blockIdx.x + 1) / blocks : all;
+  const int64_t y0 = total > 0 ? x0 % total : 0;   // within its head
+  if (mine > 0 && before <= y0 && y0 < before + mine) {
+    scan[16] = i0;
+    scan[17] = b0;
+    scan[18] = before;
+  }
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < p.nseq; b += kThreads)
+      if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
+          (int64_t)p.kv_len[b] > p.table_width * p.page_size)
+        *p.status = kDevIndex;
+  __syncthreads();
 
-  if (warp < 8) {
-    // -------------------------------------------------- softmax, one row a thread
-    const int h = warp >> 2;                          // half
-    const int r = threadIdx.x;                        // row of the tile
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lane_base + h * kKeys, to = lane_base + 256 + h * DP;
-    // a negative scale turns the queries, so that the maximum is one of S; a
-    // zero one takes zero queries
-    const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
-    if (nt > 0) {
-      const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      for (int i = threadIdx.x; i < kRows * (DP / 8); i += 2 * kHalf) {
-        const int row = i / (DP / 8), c = i % (DP / 8);
-        uint4 x = zero;
-        if (row < rows && c * 8 < p.dim && p.scale_log2 != 0.0f) {
-          const int t = (off0 + row) / p.group, hh = (off0 + row) - t * p.group;
-          const T* q = static_cast<const T*>(p.q) + (int64_t)(q0 + tok0 + t) * p.q_stride +
-                       (int64_t)(head * p.group + hh) * p.dim + c * 8;
-          x = *reinterpret_cast<const uint4*>(q);
-          x.x ^= flip;
-          x.y ^= flip;
-          x.z ^= flip;
-          x.w ^= flip;
-        }
-        *reinterpret_cast<uint4*>(basep + (row / kHalf) * S::kTile + (c >> 3) * kHalf * 128 +
-                                  swz(row % kHalf, c & 7)) = x;
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbarrier_arrive(q_full);
+  // Bounded; a wait that gave up ends the waits of all other warps too.
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (mbarrier_try_wait(bar, parity)) return true;
+    const uint64_t t = global_timer_ns();
+    for (uint32_t i = 0; i < (1u << 28) && !*failed; ++i) {
+      if (mbarrier_try_wait(bar, parity)) return true;
+      if ((i & 15u) == 15u && global_timer_ns() - t > kWaitNs) break;
     }
-    const int trow = (off0 + min(r, max(rows, 1) - 1)) / p.group;
-    const int pos = kv - qn + tok0 + trow;
-    float m = -INFINITY;
-    uint64_t l0 = 0, l1 = 0;
-    const uint64_t scale2 = f2_packf(scale, scale);
-    bool ok = true;
-    if (h == 0 || two) {
-      for (int j = 0; j < nt; ++j) {
-        if (*failed || !mbarrier_wait_bounded(s_full + 8 * h, j & 1, kWaitNs)) {
-          ok = false;
-          break;
-        }
+    *failed = 1;
+    return false;
+  };
+  auto wait_item = [&](int item) { return wait(full + 8 * (item % kSlots), (item / kSlots) & 1); };
+  // The next segment of the queue, for a warp; false at the end.
+  auto next_segment = [&](int sg, Segment& g) {
+    const bool ok = wait(seg_full + 8 * (sg % kQueue), (sg / kQueue) & 1);
+    if (__any_sync(0xffffffffu, !ok)) return false;
+    g = queue[sg % kQueue];
+    __syncwarp();
+    if (lane == 0) mbarrier_arrive(seg_empty + 8 * (sg % kQueue));
+    return g.n >= 0;
+  };
+  // Each role is a loop of its own over the segments (the items of a segment
+  // in the ring: K of key tile j is base_item + 2 j, V the one after).
+  if (warp < 8) {
+    registers_up();
+    // This softmax's 128 rows of queries of segment s, in the background: rows
+    // past the end and values past the head are zeros, and all of them with a
+    // scale of zero.
+    auto load_queries = [&](const Segment& s, int h, int r) {
+      const bool alt = s.rows <= kHalf;
+      if (s.n < 0 || (alt ? (s.n - h + 1) / 2 : s.n) == 0) return;
+#pragma unroll 4
+      for (int i = r; i < kHalf * (DP / 8); i += kHalf) {
+        const int qr = i / (DP / 8), c = i % (DP / 8), tr = alt ? qr : h * kHalf + qr;
+        const int t = (s.off + tr) / p.group, hh = (s.off + tr) - t * p.group;
+        const bool use = tr < s.rows && c * 8 < p.dim && p.scale_log2 != 0.0f;
+        const T* q = static_cast<const T*>(p.q);
+        if (use)
+          q += (int64_t)(s.tok + t) * p.q_stride + (int64_t)(s.head * p.group + hh) * p.dim + c * 8;
+        copy16(base + h * S::kTile + (c >> 3) * kHalf * 128 + swz(qr, c & 7), q, use);
+      }
+    };
+    auto queries_loaded = [&](const Segment& s, int h) {
+      const bool alt = s.rows <= kHalf;
+      if (s.n < 0 || (alt ? (s.n - h + 1) / 2 : s.n) == 0) return;
+      copy16_wait();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbarrier_arrive(q_full + 8 * h);
+    };
+    int base_item = 0;
+    uint32_t ss = 0;                          // scores seen so far
+    Segment g;
+    for (int sg = 0; next_segment(sg, g); ++sg) {
+      // alternate key tiles of the same rows, or the same key tiles of two halves
+      const bool alt = g.rows <= kHalf;
+      // ---------------------------------------------- softmax, one row a thread
+      const int h = warp >> 2, r = threadIdx.x & (kHalf - 1);
+      const int row = alt ? r : h * kHalf + r;        // of the row tile
+      const int n = alt ? (g.n - h + 1) / 2 : g.n;    // key tiles
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t ts = lane_base + h * kKeys, to = lane_base + 256 + h * DP;
+      const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+      if (sg == 0) {
+        load_queries(g, h, r);
+        queries_loaded(g, h);
+      }
+      // the next segment's queries, as soon as this one's are done with
+      auto next_queries = [&]() {
+        if (!wait(seg_full + 8 * ((sg + 1) % kQueue), ((sg + 1) / kQueue) & 1)) return;
+        load_queries(queue[(sg + 1) % kQueue], h, r);
+      };
+      const int trow = (g.off + min(row, g.rows - 1)) / p.group;
+      const int pos = g.pos + trow;
+      float m = -INFINITY;
+      uint64_t l0 = 0, l1 = 0;
+      const uint64_t scale2 = f2_packf(scale, scale);
+      bool ok = true;
+      for (int k = 0; k < n; ++k) {
+        ok = wait(s_full + 8 * h, ss & 1);
+        if (!ok) break;
+        ++ss;
+        if (k == n - 1) next_queries();
         tc_fence_after();
-        const int key0 = (t0 + j) * kKeys;
+        const int j = alt ? 2 * k + h : k;
+        const int key0 = (g.t0 + j) * kKeys;
         float a[64], b[64];
-        tmem_ld64(ts, a);
-        tmem_ld64(ts + 64, b);
+        tmem_ld128(ts, a, b);
         // the row sees the keys (pos - window, pos]
         const int see = pos - key0;
         const int64_t from = p.window > 0 ? (int64_t)pos - p.window - key0 : -1;
@@ -395,31 +483,25 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           const uint64_t c2 = f2_packf(corr, corr);
           l0 = f2_mul(l0, c2);
           l1 = f2_mul(l1, c2);
-          if (j > 0) {
+          if (k > 0) {
 #pragma unroll
             for (int c = 0; c < DP; c += 32) {
               uint32_t o[32];
               tmem_ld32(to + c, o);
 #pragma unroll
-              for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * corr);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
               tmem_st32(to + c, o);
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.0f : -m;
-        const uint64_t ref2 = f2_packf(ref, ref);
-        weights64<T>(a, scale2, ref2, l0, l1, ts);
-        weights64<T>(b, scale2, ref2, l0, l1, ts + 32);
         // values of keys that no row sees may be anything: zero them (their
         // weights are zero, but zero times NaN is not)
-        if (h == 0 && (key0 + kKeys > hi || key0 < lo)) {
-          const int item = 2 * j + 1;
-          if (!mbarrier_wait_bounded(full + 8 * (item % kSlots), (item / kSlots) & 1, kWaitNs)) {
-            ok = false;
-            break;
-          }
+        if ((alt || h == 0) && (key0 + kKeys > g.hi || key0 < g.lo)) {
+          const int item = base_item + 2 * j + 1;
+          ok = wait_item(item);
+          if (!ok) break;
           const int key = key0 + r;
-          if (key >= hi || key < lo) {
+          if (key >= g.hi || key < g.lo) {
             uint8_t* v = basep + (2 + item % kSlots) * S::kTile;
 #pragma unroll
             for (int c = 0; c < DP / 8; ++c)
@@ -428,50 +510,291 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbarrier_arrive(p_ready + 8 * h);
+        const float ref = m == -INFINITY ? 0.0f : -m;
+        const uint64_t ref2 = f2_packf(ref, ref);
+        auto signal = [&](uint32_t bar) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbarrier_arrive(bar);
+        };
+        weights64<T>(a, scale2, ref2, l0, l1, ts);
+        signal(p_ready + 16 * h);
+        weights64<T>(b, scale2, ref2, l0, l1, ts + 32);
+        signal(p_ready + 16 * h + 8);
       }
-      if (ok && nt > 0 && !mbarrier_wait_bounded(s_full + 8 * h, nt & 1, kWaitNs)) ok = false;
+      if (ok && n > 0) {   // the last product
+        ok = wait(s_full + 8 * h, ss & 1);
+        ++ss;
+      }
+      base_item += 2 * g.n;
       if (!ok) *failed = 1;
       tc_fence_after();
-      __syncwarp();
-      if (ok && !*failed) {
-        // ---------------------------------------------- output rows
-        const float2 la = f2_unpack(f2_add(l0, l1));
-        const float l = la.x + la.y;
+      if (n == 0) next_queries();
+      if (!*failed) queries_loaded(queue[(sg + 1) % kQueue], h);
+      const float2 la = f2_unpack(f2_add(l0, l1));
+      float l = la.x + la.y, keep = 1.0f, other = 0.0f;
+      const bool merge = alt && g.n > 1;
+      if (merge) {
+        // the first softmax takes the second one's result from TMEM: the two
+        // warpgroups reach the same lanes
+        float* const stats = reinterpret_cast<float*>(basep + S::kStats);
+        if (h == 1) {
+          stats[r] = m;
+          stats[kHalf + r] = l;
+        }
+        tc_fence_before();
+        named_barrier_sync(1, 2 * kHalf);
+        tc_fence_after();
+        if (h == 0) {
+          const float m1 = stats[r], mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
+          keep = exp2_approx(m - ref);
+          other = exp2_approx(m1 - ref);
+          l = l * keep + stats[kHalf + r] * other;
+          m = mn;
+        }
+      }
+      if (ok && !(alt && h == 1)) {
+        // -------------------------------------------- output rows
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const float lse = l > 0.0f ? m + log2f(l) : -INFINITY;
-        const bool live = r < rows;
-        const int64_t tok = q0 + tok0 + trow;
-        const int qh = head * p.group + (off0 + r) % p.group;
-        const int64_t at = p.nsplit > 1 ? ((int64_t)split * p.ntok + tok) * p.q_heads + qh : 0;
-        if (live && p.nsplit > 1) p.part_lse[at] = lse;
-        if (live && p.nsplit == 1 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
-        const int64_t obase = tok * p.o_stride + (int64_t)qh * p.dim;
+        const bool live = row < g.rows;
+        const int64_t tok = g.tok + trow;
+        const int qh = g.head * p.group + (g.off + row) % p.group;
+        const int64_t at = (int64_t)g.part * kRows + row;
+        if (live && g.part >= 0) p.part_lse[at] = lse;
+        if (live && g.part < 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
+        void* const out = g.part >= 0 ? static_cast<void*>(p.part_o) : p.o;
+        const int type = g.part >= 0 ? TQ_F32 : p.o_type;
+        const int64_t obase =
+            g.part >= 0 ? at * p.dim : tok * p.o_stride + (int64_t)qh * p.dim;
+        keep *= inv;
+        other *= inv;
 #pragma unroll
         for (int c = 0; c < DP; c += 32) {
-          uint32_t o[32] = {};
-          if (nt > 0) tmem_ld32(to + c, o);
-          if (!live) continue;
+          uint32_t o[32] = {}, o1[32] = {};
+          if (n > 0) tmem_ld32(to + c, o);
+          if (merge) tmem_ld32(to + DP + c, o1);
+          if (!live || c >= p.dim) continue;
+          float x[32];
 #pragma unroll
-          for (int n = 0; n < 32; n += 4) {
-            if (c + n >= p.dim) continue;
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = nt > 0 ? __uint_as_float(o[n + e]) * inv : 0.0f;
-            if (p.nsplit > 1)
-              *reinterpret_cast<float4*>(p.part_o + at * p.dim + c + n) =
-                  make_float4(x[0], x[1], x[2], x[3]);
-            else
-              store_out4(p.o, p.o_type, obase + c + n, x);
+          for (int e = 0; e < 32; ++e) {
+            x[e] = __uint_as_float(o[e]) * keep;
+            if (merge) x[e] = fmaf(__uint_as_float(o1[e]), other, x[e]);
+          }
+          store_out32(out, type, obase + c, x, p.dim - c);
+        }
+      }
+      tc_fence_before();
+      if (merge) named_barrier_sync(1, 2 * kHalf);
+      if (__any_sync(0xffffffffu, *failed)) break;
+    }
+  } else {
+    registers_down();
+    if (warp == 10) {
+      // ------------------------------------------------ scheduling
+      if (lane == 0) {
+        CutTile cut = {};
+        int queued = 0;
+        auto push = [&](const Segment& g) {
+          const int i = queued % kQueue;
+          if (queued >= kQueue &&
+              !mbarrier_wait_bounded(seg_empty + 8 * i, (queued / kQueue - 1) & 1, kWaitNs))
+            *failed = 1;
+          queue[i] = g;
+          mbarrier_arrive(seg_full + 8 * i);
+          ++queued;
+        };
+        if (x0 < x1) {
+          int head = (int)(x0 / total), b = (int)scan[17];
+          int64_t s = scan[16], at = head * total + scan[18];   // number and start of the row tile
+          while (at < x1 && !*failed) {
+            while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
+            Segment g = row_tile(p, s, b);
+            const int64_t cost = tile_cost(g);
+            if (cost > 0 && at + cost > x0) {
+              // key tiles [from, to) of the row tile fall into the piece
+              const int w = unit_cost(g), n = g.n;
+              const int64_t u0 = max(x0 - at, (int64_t)0), u1 = min(x1 - at, cost);
+              const int from = (int)max((int64_t)0, min((u0 - kTileCost) / w, (int64_t)n));
+              const int to = u1 < kTileCost ? 0 : (int)min((u1 - kTileCost) / w, (int64_t)n);
+              if (n == 0 ? u0 == 0 : from < to) {
+                g.head = head;
+                g.part = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (queued > 0);
+                if (g.part >= 0 && from == 0) {
+                  // the piece with the row tile's end, and so how many pieces
+                  const int64_t last = ((at + cost) * blocks + all - 1) / all - 1;
+                  cut.n = (int)(last - blockIdx.x) + 1;
+                  cut.part0 = g.part;
+                  cut.tok = g.tok;
+                  cut.off = g.off;
+                  cut.rows = g.rows;
+                  cut.head = head;
+                }
+                g.t0 += from;
+                g.n = to - from;
+                push(g);
+              }
+            }
+            at += cost;
+            if (++s == numbers) {
+              s = 0;
+              b = 0;
+              ++head;
+            }
           }
         }
+        Segment end = {};
+        end.n = -1;
+        push(end);
+        static_cast<CutTile*>(p.cuts)[blockIdx.x] = cut;
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      int base_item = 0;
+      Segment g;
+      for (int sg = 0; next_segment(sg, g); ++sg) {
+        // ---------------------------------------------- TMA
+        const int boxes = kKeys / p.box_rows;   // 1 .. 16, one lane each
+        const int off = lane * p.box_rows;
+        bool bad = false;
+        int page = p.pages, pslot = 0;
+        // page and slot of this lane's box of tile t; the page one past the
+        // cache (zeros, nothing read) where no row sees the box
+        auto locate = [&](int t) {
+          const int key = t * kKeys + off;
+          page = p.pages;
+          pslot = 0;
+          if (lane < boxes && t < g.t0 + g.n && key < g.hi && key + p.box_rows > g.lo) {
+            const int lp = key / p.page_size;
+            pslot = key - lp * p.page_size;
+            int pg = -1;
+            if (lp < p.table_width) pg = p.table[g.seq * p.table_stride + lp];
+            if (pg >= 0 && pg < p.pages) page = pg;
+            else bad = true;
+          }
+        };
+        locate(g.t0);
+        for (int j = 0; j < g.n; ++j) {
+          const int pg = page, sl = pslot;
+          locate(g.t0 + j + 1);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int it = base_item + 2 * j + v, sidx = it % kSlots;
+            if (it >= kSlots && !wait(empty + 8 * sidx, (it / kSlots - 1) & 1)) break;
+            if (lane == 0) mbarrier_arrive_expect_tx(full + 8 * sidx, S::kTile);
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = ring + sidx * S::kTile + off * 128;
+#pragma unroll
+              for (int c = 0; c < kSub; ++c)
+                tma_box(dst + c * kKeys * 128, v ? &vmap : &kmap, c * 64, sl, g.head, pg,
+                        full + 8 * sidx);
+            }
+            if (lane == 0) flags[2] = it + 1;   // copies issued, for the failure path
+          }
+          if (__any_sync(0xffffffffu, *failed)) break;
+        }
+        if (bad) *p.status = kDevIndex;
+        base_item += 2 * g.n;
+        if (__any_sync(0xffffffffu, *failed)) break;
+      }
+    } else if (warp == 8) {
+      int base_item = 0;
+      uint32_t qs[2] = {0, 0}, ps[2] = {0, 0};   // queries and weights seen so far
+      const uint32_t mtmem = __shfl_sync(0xffffffffu, tmem, 0), lead = elect_one();
+      // a negative scale turns S (bit 13 negates A), so that the maximum of S
+      // is that of the scores
+      const uint32_t idesc_s = Desc<T, DP>::kScores | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      constexpr uint32_t idesc_o = Desc<T, DP>::kOut;
+      Segment g;
+      for (int sg = 0; next_segment(sg, g); ++sg) {
+        // ---------------------------------------------- MMA
+        const int n = __shfl_sync(0xffffffffu, g.n, 0);
+        const bool alt = __shfl_sync(0xffffffffu, g.rows, 0) <= kHalf;
+        auto qk = [&](int h, int item) {
+          const uint64_t a = desc_k(base + h * S::kTile), b = desc_k(ring + (item % kSlots) * S::kTile);
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d) {
+            const uint64_t o = ((d >> 2) * kKeys * 128 + (d & 3) * 32) >> 4;
+            mma_ss(lead, mtmem + h * kKeys, a + o, b + o, idesc_s, d > 0);
+          }
+        };
+        auto pv = [&](int h, int item, int part, bool first) {
+          const uint64_t b = desc_n(ring + (item % kSlots) * S::kTile);
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) {
+            const int k = part * (kKeys / 32) + i;
+            mma_ts(lead, mtmem + 256 + h * DP, mtmem + h * kKeys + k * 8, b + k * (2048 >> 4), idesc_o,
+                   !(first && k == 0));
+          }
+        };
+        auto free_slot = [&](int item) { commit(lead, empty + 8 * (item % kSlots)); };
+        // all lanes wait; one that gave up ends it for all
+        auto ready = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+        // key tiles of softmax h, and its k-th one
+        auto count = [&](int h) { return alt ? (n - h + 1) / 2 : n; };
+        auto tile_of = [&](int h, int k) { return alt ? 2 * k + h : k; };
+        bool ok = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (count(h) == 0 || !ok) continue;
+          const int ki = base_item + 2 * tile_of(h, 0);
+          ok = ready(wait(q_full + 8 * h, qs[h] & 1) && wait_item(ki));
+          if (!ok) continue;
+          ++qs[h];
+          tc_fence_after();
+          qk(h, ki);
+          commit(lead, s_full + 8 * h);
+          if (alt || h == 1) free_slot(ki);
+        }
+        for (int k = 0; k < count(0) && ok; ++k) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (k >= count(h) || !ok) continue;
+            const int vi = base_item + 2 * tile_of(h, k) + 1;
+            const int ki = base_item + 2 * tile_of(h, k + 1);
+            const bool more = k + 1 < count(h);
+            ok = ready(wait_item(vi) && wait(p_ready + 16 * h, ps[h] & 1));
+            if (!ok) continue;
+            tc_fence_after();
+            pv(h, vi, 0, k == 0);
+            ok = ready(wait(p_ready + 16 * h + 8, ps[h] & 1));
+            if (!ok) continue;
+            ++ps[h];
+            tc_fence_after();
+            pv(h, vi, 1, k == 0);
+            if (more) {
+              ok = ready(wait_item(ki));
+              if (!ok) continue;
+              qk(h, ki);
+            }
+            commit(lead, s_full + 8 * h);
+            if (alt || h == 1) {
+              free_slot(vi);
+              if (more) free_slot(ki);
+            }
+          }
+        }
+        base_item += 2 * n;
+        if (__any_sync(0xffffffffu, *failed)) break;
       }
     }
   }
   __syncwarp();
+  if (*failed) {
+    // no block leaves before its copies have landed and its MMAs have ended
+    if (warp == 9) {
+      const int issued = (int)flags[2];
+      if (lane < kSlots && issued > lane)
+        mbarrier_wait_bounded(full + 8 * lane, ((issued - 1 - lane) / kSlots) & 1, kWaitNs / 10);
+    }
+    if (warp == 8) {
+      commit(elect_one(), drain);
+      mbarrier_wait_bounded(drain, 0, kWaitNs / 10);
+    }
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   if (*failed && threadIdx.x == 0) *p.status = kDevTimeout;
@@ -481,16 +804,65 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   }
 }
 
+constexpr int kJoinRows = 8;   // rows of a block of the join, one a warp
+
+// Joins the pieces of the row tiles that were cut: o = sum_s 2^(lse_s - M) o_s
+// / sum_s 2^(lse_s - M), a warp per row.
+__global__ void __launch_bounds__(kJoinRows * 32)
+attn_chunk_join_kernel(const __grid_constant__ AttnParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const CutTile cut = static_cast<const CutTile*>(p.cuts)[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  if (r >= (cut.n > 0 ? cut.rows : 0)) return;
+  auto row_of = [&](int i) {
+    return (int64_t)(i == 0 ? cut.part0 : 2 * ((int)blockIdx.x + i)) * kRows + r;
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < cut.n; i += 32) top = fmaxf(top, p.part_lse[row_of(i)]);
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int i = 0; i < cut.n; ++i) {
+      const int64_t at = row_of(i);
+      const float f = exp2_approx(p.part_lse[at] - top);
+      sum += f;
+      if (lane * 4 < p.dim) {
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at * p.dim + lane * 4);
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const int t = (cut.off + r) / p.group;
+  const int64_t tok = cut.tok + t, qh = cut.head * p.group + (cut.off + r - t * p.group);
+  const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  if (lane * 4 < p.dim) store_out4(p.o, p.o_type, tok * p.o_stride + qh * p.dim + lane * 4, x);
+  if (lane == 0 && p.lse)
+    p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
 template <typename T, int DP>
 cudaError_t launch_chunk(const AttnParams& p, const AttnCall& c, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, cudaStream_t s) {
   auto kernel = attn_chunk_kernel<T, DP>;
   const cudaError_t e = ensure_dynamic_smem((const void*)kernel, Smem<DP>::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t x = c.plan.tiles_x * p.nsplit;
-  if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kernel, dim3((unsigned)x, (unsigned)c.kv.heads), dim3(kThreads),
-                    Smem<DP>::kBytes, s, p, kmap, vmap);
+  DeviceLimits lim;
+  cudaError_t r = device_limits(&lim);
+  if (r != cudaSuccess) return r;
+  const int grid = lim.sms < c.plan.blocks ? lim.sms : c.plan.blocks;
+  r = launch_pdl(kernel, dim3(grid), dim3(kThreads), Smem<DP>::kBytes, s, p, kmap, vmap,
+                 c.plan.tiles_x);
+  if (r != cudaSuccess) return r;
+  return launch_pdl(attn_chunk_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinRows * 32), 0,
+                    s, p);
 }
 
 template <typename T>

@@ -400,8 +400,7 @@ cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensor
                           const CUtensorMap& vmap, cudaStream_t s) {
   switch (c.plan.tile_rows) {
     case 16: return launch_decode<T, DP, 1>(p, c, kmap, vmap, s);
-    case 32: return launch_decode<T, DP, 2>(p, c, kmap, vmap, s);
-    default: return launch_decode<T, DP, 4>(p, c, kmap, vmap, s);
+    default: return launch_decode<T, DP, 2>(p, c, kmap, vmap, s);
   }
 }
 
