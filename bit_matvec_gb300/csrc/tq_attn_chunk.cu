@@ -7,9 +7,11 @@
 // streams 128-key tiles of K and V through a ring of shared-memory slots (TMA
 // boxes, one per page piece) and keeps two softmaxes of 128 rows going:
 //   S = Q K^T     tcgen05.mma, both operands in shared memory, S in TMEM;
-//   P = 2^(c S - M) one thread per row: no exchange between threads; M moves
-//                 only when a row's maximum exceeds it by 2^8 (the quotient at
-//                 the end makes any M right), and then O is rescaled in TMEM;
+//   P = 2^(c S - M) one thread a row: no exchange between threads (two a row
+//                 measured 1.4 times slower: the fixed work of a step
+//                 doubles); M moves only when a row's maximum exceeds it by
+//                 2^8 (the quotient at the end makes any M right), and then O
+//                 is rescaled in TMEM;
 //   O += P V      P as the A operand from TMEM, written over S; V is read
 //                 as stored, its 64-value rows being the N-major order.
 // While one softmax runs, the tensor cores work for the other. With more than
@@ -34,10 +36,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kHalf = 128;            // rows of a softmax: one warpgroup, one row a thread
+constexpr int kHalf = 128;            // rows of a softmax
 constexpr int kRows = 2 * kHalf;      // rows of a tile
 constexpr int kKeys = 128;            // keys of a tile
-constexpr int kThreads = 384;         // two softmax warpgroups; MMA, TMA and scheduling warps
+constexpr int kSoft = 256;            // softmax threads, one a row
+constexpr int kThreads = kSoft + 128; // and an MMA, a TMA and a scheduling warp (and one that idles)
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
 constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
 // Cost of a row tile in units of half a key tile of 256 rows: what starting
@@ -65,9 +68,10 @@ template <int DP> struct Smem {
   static constexpr int kBarBytes = 8 * (2 * kSlots + 8 + 2 * kQueue + 1);
   static constexpr int kFlags = kBars + (kBarBytes + 63) / 64 * 64;
   static constexpr int kSegs = kFlags + 64;
-  static constexpr int kScan = kSegs + kQueue * 64;
-  static constexpr int kStats = kScan + 192;        // maxima and sums of 128 rows
-  static constexpr int kBytes = kStats + 1024 + 1024;   // with room to align
+  // the second softmax's maxima and sums; before the first segment, the scan
+  // of the work
+  static constexpr int kStats = kSegs + kQueue * 64;
+  static constexpr int kBytes = kStats + 1024;
   static_assert(kBytes <= 232448, "227 KB a block");
   static_assert(kQueue * sizeof(Segment) <= 256 && kFlags % 16 == 0, "regions");
 };
@@ -147,33 +151,44 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&a)[64], float
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]),
         "=f"(a[7]), "=f"(a[8]), "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]),
-        "=f"(a[14]), "=f"(a[15]), "=f"(a[16]), "=f"(a[17]), "=f"(a[18]), "=f"(a[19]), "=f"(a[20]),
-        "=f"(a[21]), "=f"(a[22]), "=f"(a[23]), "=f"(a[24]), "=f"(a[25]), "=f"(a[26]), "=f"(a[27]),
-        "=f"(a[28]), "=f"(a[29]), "=f"(a[30]), "=f"(a[31]), "=f"(a[32]), "=f"(a[33]), "=f"(a[34]),
-        "=f"(a[35]), "=f"(a[36]), "=f"(a[37]), "=f"(a[38]), "=f"(a[39]), "=f"(a[40]), "=f"(a[41]),
-        "=f"(a[42]), "=f"(a[43]), "=f"(a[44]), "=f"(a[45]), "=f"(a[46]), "=f"(a[47]), "=f"(a[48]),
-        "=f"(a[49]), "=f"(a[50]), "=f"(a[51]), "=f"(a[52]), "=f"(a[53]), "=f"(a[54]), "=f"(a[55]),
-        "=f"(a[56]), "=f"(a[57]), "=f"(a[58]), "=f"(a[59]), "=f"(a[60]), "=f"(a[61]), "=f"(a[62]),
-        "=f"(a[63]), "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]),
-        "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]),
-        "=f"(b[13]), "=f"(b[14]), "=f"(b[15]), "=f"(b[16]), "=f"(b[17]), "=f"(b[18]), "=f"(b[19]),
-        "=f"(b[20]), "=f"(b[21]), "=f"(b[22]), "=f"(b[23]), "=f"(b[24]), "=f"(b[25]), "=f"(b[26]),
-        "=f"(b[27]), "=f"(b[28]), "=f"(b[29]), "=f"(b[30]), "=f"(b[31]), "=f"(b[32]), "=f"(b[33]),
-        "=f"(b[34]), "=f"(b[35]), "=f"(b[36]), "=f"(b[37]), "=f"(b[38]), "=f"(b[39]), "=f"(b[40]),
-        "=f"(b[41]), "=f"(b[42]), "=f"(b[43]), "=f"(b[44]), "=f"(b[45]), "=f"(b[46]), "=f"(b[47]),
-        "=f"(b[48]), "=f"(b[49]), "=f"(b[50]), "=f"(b[51]), "=f"(b[52]), "=f"(b[53]), "=f"(b[54]),
-        "=f"(b[55]), "=f"(b[56]), "=f"(b[57]), "=f"(b[58]), "=f"(b[59]), "=f"(b[60]), "=f"(b[61]),
-        "=f"(b[62]), "=f"(b[63])
+        "=f"(a[14]), "=f"(a[15]), "=f"(a[16]), "=f"(a[17]), "=f"(a[18]), "=f"(a[19]),
+        "=f"(a[20]), "=f"(a[21]), "=f"(a[22]), "=f"(a[23]), "=f"(a[24]), "=f"(a[25]),
+        "=f"(a[26]), "=f"(a[27]), "=f"(a[28]), "=f"(a[29]), "=f"(a[30]), "=f"(a[31]),
+        "=f"(a[32]), "=f"(a[33]), "=f"(a[34]), "=f"(a[35]), "=f"(a[36]), "=f"(a[37]),
+        "=f"(a[38]), "=f"(a[39]), "=f"(a[40]), "=f"(a[41]), "=f"(a[42]), "=f"(a[43]),
+        "=f"(a[44]), "=f"(a[45]), "=f"(a[46]), "=f"(a[47]), "=f"(a[48]), "=f"(a[49]),
+        "=f"(a[50]), "=f"(a[51]), "=f"(a[52]), "=f"(a[53]), "=f"(a[54]), "=f"(a[55]),
+        "=f"(a[56]), "=f"(a[57]), "=f"(a[58]), "=f"(a[59]), "=f"(a[60]), "=f"(a[61]),
+        "=f"(a[62]), "=f"(a[63]), "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]),
+        "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]),
+        "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15]), "=f"(b[16]), "=f"(b[17]),
+        "=f"(b[18]), "=f"(b[19]), "=f"(b[20]), "=f"(b[21]), "=f"(b[22]), "=f"(b[23]),
+        "=f"(b[24]), "=f"(b[25]), "=f"(b[26]), "=f"(b[27]), "=f"(b[28]), "=f"(b[29]),
+        "=f"(b[30]), "=f"(b[31]), "=f"(b[32]), "=f"(b[33]), "=f"(b[34]), "=f"(b[35]),
+        "=f"(b[36]), "=f"(b[37]), "=f"(b[38]), "=f"(b[39]), "=f"(b[40]), "=f"(b[41]),
+        "=f"(b[42]), "=f"(b[43]), "=f"(b[44]), "=f"(b[45]), "=f"(b[46]), "=f"(b[47]),
+        "=f"(b[48]), "=f"(b[49]), "=f"(b[50]), "=f"(b[51]), "=f"(b[52]), "=f"(b[53]),
+        "=f"(b[54]), "=f"(b[55]), "=f"(b[56]), "=f"(b[57]), "=f"(b[58]), "=f"(b[59]),
+        "=f"(b[60]), "=f"(b[61]), "=f"(b[62]), "=f"(b[63])
       : "r"(taddr), "r"(taddr + 64)
       : "memory");
+}
+
+// Waits for the loads, and keeps the use of r behind the wait.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Registers a thread: the softmax warpgroups take what the third one leaves
-// (2 x 224 + 56 = 3 x 168, what the block was launched with).
+// Registers a thread: the two softmax warpgroups take what the third one
+// leaves (2 x 224 + 56 = 3 x 168, what the block was launched with).
 __device__ __forceinline__ void registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
 }
@@ -197,16 +212,23 @@ __device__ __forceinline__ void mask64(float (&s)[64], int lo, int hi) {
     if (n > hi || n <= lo) s[n] = -INFINITY;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
 __device__ __forceinline__ float max64(const float (&s)[64]) {
   float a = s[0], b = s[1], c = s[2], d = s[3];
 #pragma unroll
-  for (int n = 4; n < 64; n += 4) {
-    a = fmaxf(a, s[n]);
-    b = fmaxf(b, s[n + 1]);
-    c = fmaxf(c, s[n + 2]);
-    d = fmaxf(d, s[n + 3]);
+  for (int n = 4; n + 8 <= 60; n += 8) {
+    a = max3(a, s[n], s[n + 1]);
+    b = max3(b, s[n + 2], s[n + 3]);
+    c = max3(c, s[n + 4], s[n + 5]);
+    d = max3(d, s[n + 6], s[n + 7]);
   }
-  return fmaxf(fmaxf(a, b), fmaxf(c, d));
+  a = max3(a, s[60], s[61]);
+  b = max3(b, s[62], s[63]);
+  return fmaxf(max3(a, b, c), d);
 }
 
 // Weights of 64 scores, 2^(scale s - ref), packed in pairs of T into TMEM;
@@ -297,9 +319,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                   const __grid_constant__ CUtensorMap vmap, int64_t numbers) {
   using S = Smem<DP>;
   constexpr int kSlots = S::kSlots, kSub = DP / 64;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const basep = smem_raw + (base - smem_u32(smem_raw));
+  extern __shared__ __align__(1024) uint8_t basep[];
+  const uint32_t base = smem_u32(basep);
+  if (base & 1023u) {   // the swizzled tiles need it, and there is no room to align
+    if (threadIdx.x == 0) *p.status = kDevTimeout;
+    return;
+  }
   // queries of the two softmaxes, then the ring, then the barriers
   const uint32_t ring = base + 2 * S::kTile;
   const uint32_t full = base + S::kBars, empty = full + 8 * kSlots, q_full = empty + 8 * kSlots;
@@ -309,7 +334,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   volatile uint32_t* const flags = reinterpret_cast<volatile uint32_t*>(basep + S::kFlags);
   volatile uint32_t* const failed = flags + 1;   // flags[0]: TMEM address
   Segment* const queue = reinterpret_cast<Segment*>(basep + S::kSegs);
-  int64_t* const scan = reinterpret_cast<int64_t*>(basep + S::kScan);
+  int64_t* const scan = reinterpret_cast<int64_t*>(basep + S::kStats);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -318,14 +343,14 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       mbarrier_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbarrier_init(q_full + 8 * i, kHalf);
+      mbarrier_init(q_full + 8 * i, kSoft / 2);
       mbarrier_init(s_full + 8 * i, 1);
       mbarrier_init(p_ready + 16 * i, 4);       // weights of the first 64 keys
       mbarrier_init(p_ready + 16 * i + 8, 4);   // and of the others
     }
     for (int i = 0; i < kQueue; ++i) {
       mbarrier_init(seg_full + 8 * i, 1);
-      mbarrier_init(seg_empty + 8 * i, 10);   // MMA, TMA and softmax warps
+      mbarrier_init(seg_empty + 8 * i, kSoft / 32 + 2);   // softmax, MMA and TMA warps
     }
     mbarrier_init(drain, 1);
     *failed = 0;
@@ -369,9 +394,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   const int64_t x1 = blockIdx.x < blocks ? all * (blockIdx.x + 1) / blocks : all;
   const int64_t y0 = total > 0 ? x0 % total : 0;   // within its head
   if (mine > 0 && before <= y0 && y0 < before + mine) {
-    scan[16] = i0;
-    scan[17] = b0;
-    scan[18] = before;
+    scan[20] = i0;
+    scan[21] = b0;
+    scan[22] = before;
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
@@ -380,37 +405,54 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         *p.status = kDevIndex;
   __syncthreads();
 
-  // Bounded; a wait that gave up ends the waits of all other warps too.
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (mbarrier_try_wait(bar, parity)) return true;
+  // Every wait has a limit. One that gave up sets `failed`, which ends the
+  // other waits too; the warps then run through the rest without waiting (the
+  // softmax warps still meet at their barriers), results are undefined and the
+  // status word says so. The waits for the segment queue are apart: they only
+  // depend on warps that always get there, and all warps see every segment.
+  auto wait_for = [&](uint32_t bar, uint32_t parity, uint64_t limit, bool heed) {
+    if (mbarrier_test_wait(bar, parity)) return true;
     const uint64_t t = global_timer_ns();
-    for (uint32_t i = 0; i < (1u << 28) && !*failed; ++i) {
+    for (uint32_t i = 0; i < (1u << 28) && !(heed && *failed); ++i) {
       if (mbarrier_try_wait(bar, parity)) return true;
-      if ((i & 15u) == 15u && global_timer_ns() - t > kWaitNs) break;
+      if ((i & 15u) == 15u && global_timer_ns() - t > limit) break;
     }
     *failed = 1;
     return false;
   };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_for(bar, parity, kWaitNs, true); };
   auto wait_item = [&](int item) { return wait(full + 8 * (item % kSlots), (item / kSlots) & 1); };
   // The next segment of the queue, for a warp; false at the end.
   auto next_segment = [&](int sg, Segment& g) {
-    const bool ok = wait(seg_full + 8 * (sg % kQueue), (sg / kQueue) & 1);
+    const bool ok = wait_for(seg_full + 8 * (sg % kQueue), (sg / kQueue) & 1, 20 * kWaitNs, false);
     if (__any_sync(0xffffffffu, !ok)) return false;
     g = queue[sg % kQueue];
     __syncwarp();
     if (lane == 0) mbarrier_arrive(seg_empty + 8 * (sg % kQueue));
     return g.n >= 0;
   };
+
   // Each role is a loop of its own over the segments (the items of a segment
   // in the ring: K of key tile j is base_item + 2 j, V the one after).
-  if (warp < 8) {
+  if (warp < kSoft / 32) {
     registers_up();
+    // -------------------------------------------------- softmax
+    const int h = warp >> 2, r = threadIdx.x & (kHalf - 1);        // softmax h, row r
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + h * kKeys;            // scores; the weights go over their first half
+    const uint32_t to = lanes + 256 + h * DP;         // output
+    const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+    const uint64_t scale2 = f2_packf(scale, scale);
+    // Key tiles of segment s for this softmax.
+    auto tiles_of = [&](const Segment& s) {
+      return s.n < 0 ? 0 : s.rows <= kHalf ? (s.n - h + 1) / 2 : s.n;
+    };
     // This softmax's 128 rows of queries of segment s, in the background: rows
     // past the end and values past the head are zeros, and all of them with a
     // scale of zero.
-    auto load_queries = [&](const Segment& s, int h, int r) {
+    auto load_queries = [&](const Segment& s) {
+      if (tiles_of(s) == 0) return;
       const bool alt = s.rows <= kHalf;
-      if (s.n < 0 || (alt ? (s.n - h + 1) / 2 : s.n) == 0) return;
 #pragma unroll 4
       for (int i = r; i < kHalf * (DP / 8); i += kHalf) {
         const int qr = i / (DP / 8), c = i % (DP / 8), tr = alt ? qr : h * kHalf + qr;
@@ -422,44 +464,35 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         copy16(base + h * S::kTile + (c >> 3) * kHalf * 128 + swz(qr, c & 7), q, use);
       }
     };
-    auto queries_loaded = [&](const Segment& s, int h) {
-      const bool alt = s.rows <= kHalf;
-      if (s.n < 0 || (alt ? (s.n - h + 1) / 2 : s.n) == 0) return;
+    auto queries_loaded = [&](const Segment& s) {
+      if (tiles_of(s) == 0) return;
       copy16_wait();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbarrier_arrive(q_full + 8 * h);
     };
     int base_item = 0;
-    uint32_t ss = 0;                          // scores seen so far
+    uint32_t ss = 0;                                  // scores seen so far
     Segment g;
     for (int sg = 0; next_segment(sg, g); ++sg) {
       // alternate key tiles of the same rows, or the same key tiles of two halves
       const bool alt = g.rows <= kHalf;
-      // ---------------------------------------------- softmax, one row a thread
-      const int h = warp >> 2, r = threadIdx.x & (kHalf - 1);
       const int row = alt ? r : h * kHalf + r;        // of the row tile
-      const int n = alt ? (g.n - h + 1) / 2 : g.n;    // key tiles
-      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t ts = lane_base + h * kKeys, to = lane_base + 256 + h * DP;
-      const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+      const int n = tiles_of(g);
       if (sg == 0) {
-        load_queries(g, h, r);
-        queries_loaded(g, h);
+        load_queries(g);
+        queries_loaded(g);
       }
       // the next segment's queries, as soon as this one's are done with
       auto next_queries = [&]() {
-        if (!wait(seg_full + 8 * ((sg + 1) % kQueue), ((sg + 1) / kQueue) & 1)) return;
-        load_queries(queue[(sg + 1) % kQueue], h, r);
+        if (wait_for(seg_full + 8 * ((sg + 1) % kQueue), ((sg + 1) / kQueue) & 1, 20 * kWaitNs, false))
+          load_queries(queue[(sg + 1) % kQueue]);
       };
       const int trow = (g.off + min(row, g.rows - 1)) / p.group;
       const int pos = g.pos + trow;
       float m = -INFINITY;
       uint64_t l0 = 0, l1 = 0;
-      const uint64_t scale2 = f2_packf(scale, scale);
-      bool ok = true;
       for (int k = 0; k < n; ++k) {
-        ok = wait(s_full + 8 * h, ss & 1);
-        if (!ok) break;
+        wait(s_full + 8 * h, ss & 1);
         ++ss;
         if (k == n - 1) next_queries();
         tc_fence_after();
@@ -467,13 +500,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int key0 = (g.t0 + j) * kKeys;
         float a[64], b[64];
         tmem_ld128(ts, a, b);
-        // the row sees the keys (pos - window, pos]
-        const int see = pos - key0;
-        const int64_t from = p.window > 0 ? (int64_t)pos - p.window - key0 : -1;
-        if (__any_sync(0xffffffffu, see < kKeys - 1 || from >= 0)) {
+        // some row of the tile does not see some key
+        if (key0 + kKeys - 1 > g.pos || (p.window > 0 && key0 < g.lo + (g.hi - 1 - g.pos))) {
+          // the row sees the keys (pos - window, pos]
+          const int64_t from = p.window > 0 ? (int64_t)pos - p.window - key0 : -1;
           const int f = (int)max(from, (int64_t)-1);
-          mask64(a, f, see);
-          mask64(b, f - 64, see - 64);
+          mask64(a, f, pos - key0);
+          mask64(b, f - 64, pos - key0 - 64);
         }
         const float top = fmaxf(max64(a), max64(b)) * scale;
         if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
@@ -495,11 +528,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           }
         }
         // values of keys that no row sees may be anything: zero them (their
-        // weights are zero, but zero times NaN is not)
-        if ((alt || h == 0) && (key0 + kKeys > g.hi || key0 < g.lo)) {
+        // weights are zero, but zero times NaN is not); both softmaxes do, as
+        // neither's product waits for the other
+        if (key0 + kKeys > g.hi || key0 < g.lo) {
           const int item = base_item + 2 * j + 1;
-          ok = wait_item(item);
-          if (!ok) break;
+          wait_item(item);
           const int key = key0 + r;
           if (key >= g.hi || key < g.lo) {
             uint8_t* v = basep + (2 + item % kSlots) * S::kTile;
@@ -509,6 +542,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                   make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          named_barrier_sync(2 + h, kHalf);   // all rows, before the first product
         }
         const float ref = m == -INFINITY ? 0.0f : -m;
         const uint64_t ref2 = f2_packf(ref, ref);
@@ -523,38 +557,39 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         weights64<T>(b, scale2, ref2, l0, l1, ts + 32);
         signal(p_ready + 16 * h + 8);
       }
-      if (ok && n > 0) {   // the last product
-        ok = wait(s_full + 8 * h, ss & 1);
+      if (n > 0) {   // the last product
+        wait(s_full + 8 * h, ss & 1);
         ++ss;
       }
       base_item += 2 * g.n;
-      if (!ok) *failed = 1;
-      tc_fence_after();
       if (n == 0) next_queries();
-      if (!*failed) queries_loaded(queue[(sg + 1) % kQueue], h);
+      tc_fence_after();
+      queries_loaded(queue[(sg + 1) % kQueue]);
       const float2 la = f2_unpack(f2_add(l0, l1));
-      float l = la.x + la.y, keep = 1.0f, other = 0.0f;
+      float l = la.x + la.y;
+      float keep = 1.0f, other = 0.0f;
       const bool merge = alt && g.n > 1;
       if (merge) {
-        // the first softmax takes the second one's result from TMEM: the two
-        // warpgroups reach the same lanes
+        // the first softmax takes the second one's result from TMEM: warps of
+        // the same quadrant reach the same lanes
         float* const stats = reinterpret_cast<float*>(basep + S::kStats);
         if (h == 1) {
           stats[r] = m;
           stats[kHalf + r] = l;
         }
         tc_fence_before();
-        named_barrier_sync(1, 2 * kHalf);
+        named_barrier_sync(1, kSoft);
         tc_fence_after();
         if (h == 0) {
-          const float m1 = stats[r], mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
+          const float m1 = stats[r], l1 = stats[kHalf + r];
+          const float mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
           keep = exp2_approx(m - ref);
           other = exp2_approx(m1 - ref);
-          l = l * keep + stats[kHalf + r] * other;
+          l = l * keep + l1 * other;
           m = mn;
         }
       }
-      if (ok && !(alt && h == 1)) {
+      if (!(alt && h == 1)) {
         // -------------------------------------------- output rows
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const float lse = l > 0.0f ? m + log2f(l) : -INFINITY;
@@ -566,48 +601,52 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         if (live && g.part < 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
         void* const out = g.part >= 0 ? static_cast<void*>(p.part_o) : p.o;
         const int type = g.part >= 0 ? TQ_F32 : p.o_type;
-        const int64_t obase =
-            g.part >= 0 ? at * p.dim : tok * p.o_stride + (int64_t)qh * p.dim;
+        const int64_t obase = g.part >= 0 ? at * p.dim : tok * p.o_stride + (int64_t)qh * p.dim;
         keep *= inv;
         other *= inv;
 #pragma unroll
-        for (int c = 0; c < DP; c += 32) {
-          uint32_t o[32] = {}, o1[32] = {};
-          if (n > 0) tmem_ld32(to + c, o);
-          if (merge) tmem_ld32(to + DP + c, o1);
-          if (!live || c >= p.dim) continue;
-          float x[32];
+        for (int c = 0; c < DP; c += 16) {
+          uint32_t o[16] = {}, o1[16] = {};
+          if (n > 0) {
+            tmem_ld16_nowait(to + c, o);
+            tmem_wait_ld16(o);
+          }
+          if (merge) {
+            tmem_ld16_nowait(to + DP + c, o1);
+            tmem_wait_ld16(o1);
+          }
+          const int left = p.dim - c;
+          if (!live || left <= 0) continue;
+          float x[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 16; ++e) {
             x[e] = __uint_as_float(o[e]) * keep;
             if (merge) x[e] = fmaf(__uint_as_float(o1[e]), other, x[e]);
           }
-          store_out32(out, type, obase + c, x, p.dim - c);
+          store_out16(out, type, obase + c, x, left);
         }
       }
       tc_fence_before();
-      if (merge) named_barrier_sync(1, 2 * kHalf);
-      if (__any_sync(0xffffffffu, *failed)) break;
+      if (merge) named_barrier_sync(1, kSoft);
     }
   } else {
     registers_down();
-    if (warp == 10) {
+    if (warp == 11) {
       // ------------------------------------------------ scheduling
       if (lane == 0) {
         CutTile cut = {};
         int queued = 0;
         auto push = [&](const Segment& g) {
           const int i = queued % kQueue;
-          if (queued >= kQueue &&
-              !mbarrier_wait_bounded(seg_empty + 8 * i, (queued / kQueue - 1) & 1, kWaitNs))
-            *failed = 1;
+          if (queued >= kQueue)
+            wait_for(seg_empty + 8 * i, (queued / kQueue - 1) & 1, 20 * kWaitNs, false);
           queue[i] = g;
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
         if (x0 < x1) {
-          int head = (int)(x0 / total), b = (int)scan[17];
-          int64_t s = scan[16], at = head * total + scan[18];   // number and start of the row tile
+          int head = (int)(x0 / total), b = (int)scan[21];
+          int64_t s = scan[20], at = head * total + scan[22];   // number and start of the row tile
           while (at < x1 && !*failed) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(p, s, b);
@@ -650,11 +689,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         static_cast<CutTile*>(p.cuts)[blockIdx.x] = cut;
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 10) {
       int base_item = 0;
       Segment g;
       for (int sg = 0; next_segment(sg, g); ++sg) {
         // ---------------------------------------------- TMA
+        if (__any_sync(0xffffffffu, *failed)) continue;
         const int boxes = kKeys / p.box_rows;   // 1 .. 16, one lane each
         const int off = lane * p.box_rows;
         bool bad = false;
@@ -697,7 +737,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         }
         if (bad) *p.status = kDevIndex;
         base_item += 2 * g.n;
-        if (__any_sync(0xffffffffu, *failed)) break;
       }
     } else if (warp == 8) {
       int base_item = 0;
@@ -710,6 +749,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       Segment g;
       for (int sg = 0; next_segment(sg, g); ++sg) {
         // ---------------------------------------------- MMA
+        // One warp for both softmaxes, in turn: with a warp for each, the two
+        // fall into step, both computing weights and then both waiting for
+        // products (1372 us where this order takes 1150).
         const int n = __shfl_sync(0xffffffffu, g.n, 0);
         const bool alt = __shfl_sync(0xffffffffu, g.rows, 0) <= kHalf;
         auto qk = [&](int h, int item) {
@@ -735,7 +777,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         // key tiles of softmax h, and its k-th one
         auto count = [&](int h) { return alt ? (n - h + 1) / 2 : n; };
         auto tile_of = [&](int h, int k) { return alt ? 2 * k + h : k; };
-        bool ok = true;
+        bool ok = !__any_sync(0xffffffffu, *failed);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (count(h) == 0 || !ok) continue;
@@ -754,8 +796,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             if (k >= count(h) || !ok) continue;
             const int vi = base_item + 2 * tile_of(h, k) + 1;
             const int ki = base_item + 2 * tile_of(h, k + 1);
-            const bool more = k + 1 < count(h);
-            ok = ready(wait_item(vi) && wait(p_ready + 16 * h, ps[h] & 1));
+            // the second half's tiles are there: the first one waited for them
+            const bool own = alt || h == 0;
+            ok = ready((!own || wait_item(vi)) && wait(p_ready + 16 * h, ps[h] & 1));
             if (!ok) continue;
             tc_fence_after();
             pv(h, vi, 0, k == 0);
@@ -764,27 +807,26 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             ++ps[h];
             tc_fence_after();
             pv(h, vi, 1, k == 0);
-            if (more) {
-              ok = ready(wait_item(ki));
+            if (k + 1 < count(h)) {
+              if (own) ok = ready(wait_item(ki));
               if (!ok) continue;
               qk(h, ki);
             }
             commit(lead, s_full + 8 * h);
             if (alt || h == 1) {
               free_slot(vi);
-              if (more) free_slot(ki);
+              if (k + 1 < count(h)) free_slot(ki);
             }
           }
         }
         base_item += 2 * n;
-        if (__any_sync(0xffffffffu, *failed)) break;
       }
     }
   }
   __syncwarp();
   if (*failed) {
     // no block leaves before its copies have landed and its MMAs have ended
-    if (warp == 9) {
+    if (warp == 10) {
       const int issued = (int)flags[2];
       if (lane < kSlots && issued > lane)
         mbarrier_wait_bounded(full + 8 * lane, ((issued - 1 - lane) / kSlots) & 1, kWaitNs / 10);

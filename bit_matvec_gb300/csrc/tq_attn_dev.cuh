@@ -93,39 +93,35 @@ __device__ __forceinline__ void store_out4(void* o, int type, int64_t at, const 
   for (int e = 0; e < 4; ++e) store_out(o, type, at + e, x[e]);
 }
 
-// The first n (a multiple of 8, at least 8) of 32 consecutive values: whole
+// The first n (a multiple of 8, at least 8) of 16 consecutive values: whole
 // 32-byte sectors a store where the address allows it.
 __device__ __forceinline__ void store32(void* y, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                ::"l"(y), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
                "r"(w[7]) : "memory");
 }
-__device__ __forceinline__ void store_out32(void* o, int type, int64_t at, const float (&x)[32], int n) {
-  const int size = type == TQ_F32 ? 4 : 2;
-  char* const y = static_cast<char*>(o) + at * size;
-  if (n >= 32 && ((uintptr_t)y & 31u) == 0) {
+__device__ __forceinline__ void store_out16(void* o, int type, int64_t at, const float (&x)[16], int n) {
+  char* const y = static_cast<char*>(o) + at * (type == TQ_F32 ? 4 : 2);
+  if (n >= 16 && ((uintptr_t)y & 31u) == 0) {
     uint32_t w[8];
     if (type == TQ_F32) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
+      for (int c = 0; c < 16; c += 8) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(x[c + e]);
         store32(y + c * 4, w);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 32; c += 16) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = type == TQ_F16 ? pack2<__half>(x[c + 2 * e], x[c + 2 * e + 1])
-                                : pack2<__nv_bfloat16>(x[c + 2 * e], x[c + 2 * e + 1]);
-        store32(y + c * 2, w);
-      }
+      for (int e = 0; e < 8; ++e)
+        w[e] = type == TQ_F16 ? pack2<__half>(x[2 * e], x[2 * e + 1])
+                              : pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
+      store32(y, w);
     }
     return;
   }
 #pragma unroll
-  for (int c = 0; c < 32; c += 4) {
+  for (int c = 0; c < 16; c += 4) {
     const float v[4] = {x[c], x[c + 1], x[c + 2], x[c + 3]};
     if (c < n) store_out4(o, type, at + c, v);
   }
