@@ -43,9 +43,11 @@ constexpr int kSoft = 256;            // softmax threads, one a row
 constexpr int kThreads = kSoft + 128; // and an MMA, a TMA and a scheduling warp (and one that idles)
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
 constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
-// Cost of a row tile in units of half a key tile of 256 rows: what starting
-// and ending it takes, and the least work worth a block of its own.
-constexpr int kTileCost = 4, kLeastWork = 6;
+// The cost of work, in units of about 0.45 us: a key tile of two halves, one of
+// up to 128 rows, starting and ending a row tile (1.8, 1.4 and 4.5 us measured
+// at dim 128), and the least work worth a block of its own.
+constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 10, kLeastWork = 16;
+constexpr int kCachedSeqs = 128;      // lengths of so many sequences are kept in shared memory
 
 // A block's share of one row tile.
 struct Segment {
@@ -71,7 +73,8 @@ template <int DP> struct Smem {
   // the second softmax's maxima and sums; before the first segment, the scan
   // of the work
   static constexpr int kStats = kSegs + kQueue * 64;
-  static constexpr int kBytes = kStats + 1024;
+  static constexpr int kSeqs = kStats + 1024;           // q_start, kv_len
+  static constexpr int kBytes = kSeqs + 8 * kCachedSeqs + 16;
   static_assert(kBytes <= 232448, "227 KB a block");
   static_assert(kQueue * sizeof(Segment) <= 256 && kFlags % 16 == 0, "regions");
 };
@@ -253,8 +256,10 @@ __device__ __forceinline__ void weights64(const float (&s)[64], uint64_t scale2,
 // numbers empty).
 struct Tiles {
   const AttnParams& p;
+  const int32_t* q_start;   // of the call, or their copies in shared memory
+  const int32_t* kv_len;
   __device__ __forceinline__ int start(int b) const {
-    return min(max(p.q_start[b], 0), (int)p.ntok);
+    return min(max(q_start[b], 0), (int)p.ntok);
   }
   __device__ __forceinline__ int64_t first(int b) const {
     return (int64_t)start(b) * p.group / kRows + b;
@@ -272,14 +277,14 @@ struct Tiles {
 };
 
 // Row tile `s` of sequence `b`, whole; n = -1 if the number is an empty one.
-__device__ __forceinline__ Segment row_tile(const AttnParams& p, int64_t s, int b) {
-  const Tiles tiles{p};
+__device__ __forceinline__ Segment row_tile(const Tiles& tiles, int64_t s, int b) {
+  const AttnParams& p = tiles.p;
   Segment g = {};
   g.n = -1;
   const int q0 = tiles.start(b), qn = max(tiles.start(b + 1) - q0, 0);
   const int64_t row0 = (s - tiles.first(b)) * kRows;
   if (row0 >= (int64_t)qn * p.group) return g;
-  const int kv = max(p.kv_len[b], 0);
+  const int kv = max(tiles.kv_len[b], 0);
   const int t = (int)(row0 / p.group);
   g.seq = b;
   g.off = (int)(row0 - (int64_t)t * p.group);
@@ -292,7 +297,9 @@ __device__ __forceinline__ Segment row_tile(const AttnParams& p, int64_t s, int 
   g.n = max((g.hi + kKeys - 1) / kKeys - g.t0, 0);
   return g;
 }
-__device__ __forceinline__ int unit_cost(const Segment& g) { return g.rows > kHalf ? 2 : 1; }
+__device__ __forceinline__ int unit_cost(const Segment& g) {
+  return g.rows > kHalf ? kCostTwo : kCostAlt;
+}
 __device__ __forceinline__ int64_t tile_cost(const Segment& g) {
   return g.n < 0 ? 0 : kTileCost + (int64_t)g.n * unit_cost(g);
 }
@@ -366,14 +373,21 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 
   // The block's piece [x0, x1) of the line of work: each thread adds up the
   // cost of some consecutive row tiles of a head, a scan gives the totals.
-  const Tiles tiles{p};
+  int32_t* const seqs = reinterpret_cast<int32_t*>(basep + S::kSeqs);
+  const bool cached = p.nseq <= kCachedSeqs;
+  if (cached) {
+    if ((int)threadIdx.x <= p.nseq) seqs[threadIdx.x] = p.q_start[threadIdx.x];
+    if ((int)threadIdx.x < p.nseq) seqs[kCachedSeqs + 1 + threadIdx.x] = p.kv_len[threadIdx.x];
+    __syncthreads();
+  }
+  const Tiles tiles{p, cached ? seqs : p.q_start, cached ? seqs + kCachedSeqs + 1 : p.kv_len};
   const int64_t per = (numbers + kThreads - 1) / kThreads;
   const int64_t i0 = min((int64_t)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
   int64_t mine = 0;
   const int b0 = i0 < i1 ? tiles.find(i0) : 0;
   for (int64_t s = i0, b = b0; s < i1; ++s) {
     while (b + 1 < p.nseq && tiles.first((int)b + 1) <= s) ++b;
-    mine += tile_cost(row_tile(p, s, (int)b));
+    mine += tile_cost(row_tile(tiles, s, (int)b));
   }
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
@@ -401,7 +415,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
       if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
-          (int64_t)p.kv_len[b] > p.table_width * p.page_size)
+          (int64_t)tiles.kv_len[b] > p.table_width * p.page_size)
         *p.status = kDevIndex;
   __syncthreads();
 
@@ -649,7 +663,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           int64_t s = scan[20], at = head * total + scan[22];   // number and start of the row tile
           while (at < x1 && !*failed) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
-            Segment g = row_tile(p, s, b);
+            Segment g = row_tile(tiles, s, b);
             const int64_t cost = tile_cost(g);
             if (cost > 0 && at + cost > x0) {
               // key tiles [from, to) of the row tile fall into the piece
