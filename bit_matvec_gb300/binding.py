@@ -306,6 +306,9 @@ def tq_matmul_host(Wtq: torch.Tensor, X_host: torch.Tensor, X: torch.Tensor, Xq:
 
 _TYPES = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
 
+# The calls below cost little on the GPU for a few tokens, so their marshalling is kept short: one
+# look at each tensor, and the current stream's handle without a stream object around it.
+
 
 def _type(t: torch.Tensor) -> int:
     code = _TYPES.get(t.dtype)
@@ -314,21 +317,45 @@ def _type(t: torch.Tensor) -> int:
     return code
 
 
-def _heads(t: torch.Tensor):
-    """(address, token stride) of a [tokens][heads][head_dim] tensor whose heads are contiguous."""
+def _rows(t: torch.Tensor, shape, dtype, where: str):
+    """(address, token stride) of a [tokens][heads][head_dim] tensor of this shape and type whose
+    heads are contiguous."""
+    if t.shape != shape:
+        raise TQError(TQ_ERR_SHAPE, where)
+    if t.dtype != dtype:
+        raise TQError(TQ_ERR_TYPE, where)
+    n, h, d = shape
+    s = t.stride()
+    if s[2] != 1 or s[1] != d:
+        if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+            raise ValueError("the heads of a token must be contiguous")
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
-    n, h, d = t.shape
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-        raise ValueError("the heads of a token must be contiguous")
     return t.data_ptr(), s[0] if n > 1 else h * d
 
 
-def _of(t: torch.Tensor, dtype, what: str):
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}")
-    return _ptr(t)
+def _vector(t: torch.Tensor | None, n: int, dtype, where: str):
+    """Address of a contiguous vector of n values, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {n} values of {dtype} expected")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("tensor must be contiguous, on a CUDA device")
+    return t.data_ptr()
+
+
+def _launch(name: str, fn, device: int, stream, *args):
+    """fn(*args, stream) with `device` current; stream None: its current stream."""
+    if device == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
+                else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
+                    else stream.cuda_stream)
+    if rc != TQ_OK:
+        raise TQError(rc, name)
 
 
 class Rope:
@@ -341,8 +368,10 @@ class Rope:
 
     def __init__(self, turns: torch.Tensor, interleaved: bool = False, amplitude: float = 1.0):
         self.turns = turns   # kept alive: the struct holds its address
-        self.struct = Rope._Struct(_of(turns, torch.int64, "turns"), 2 * turns.numel(),
-                                   1 if interleaved else 0, amplitude)
+        if turns.dtype != torch.int64:
+            raise ValueError("turns must be torch.int64")
+        self.struct = Rope._Struct(_ptr(turns), 2 * turns.numel(), 1 if interleaved else 0,
+                                   amplitude)
         self.ref = ctypes.addressof(self.struct)
 
 
@@ -379,6 +408,8 @@ class PagedKV:
             block_table.stride(0) if nseq > 1 else width, pages, page_size, heads, dim,
             k.stride(0), k.stride(1), k.stride(2), _type(k), 0)
         self.ref = ctypes.addressof(self.struct)
+        # what the calls compare their arguments with
+        self.nseq, self.heads, self.head_dim, self.dtype = nseq, heads, dim, k.dtype
 
 
 def tq_rope_turns(rot_dim: int, base: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -398,47 +429,50 @@ def tq_qk_norm_rope(Xq, Xk, Yq, Yk, positions=None, rope: Rope | None = None, q_
                     k_weight=None, eps: float = 1e-6, stream=None):
     """Norm and rotation of the heads of Xq and Xk [tokens][heads][head_dim] (views of a fused
     projection's rows are fine) into Yq and Yk; Xk and Yk may be None."""
-    ntok, q_heads, dim = Xq.shape
-    k_heads = 0 if Xk is None else Xk.shape[1]
-    if Yq.shape != Xq.shape or (k_heads and (Xk.shape != (ntok, k_heads, dim) or
-                                             Yk.shape != Xk.shape)):
-        raise TQError(TQ_ERR_SHAPE, "tq_qk_norm_rope")
-    if k_heads and (Xk.dtype != Xq.dtype or Yk.dtype != Yq.dtype):
-        raise TQError(TQ_ERR_TYPE, "tq_qk_norm_rope")
-    _check_rows("tq_qk_norm_rope", dim, ntok, q_weight, k_weight, positions)
-    xk, yk = (_heads(Xk), _heads(Yk)) if k_heads else ((None, 0), (None, 0))
-    _call("tq_qk_norm_rope", Xq.device, *_heads(Xq), *xk, _type(Xq), *_heads(Yq), *yk, _type(Yq),
-          ntok, q_heads, k_heads, dim, _ptr(q_weight), _ptr(k_weight), eps,
-          None if rope is None else rope.ref, _ptr(positions), _stream(stream, Xq.device))
+    shape = Xq.shape
+    ntok, q_heads, dim = shape
+    tin, tout, where = Xq.dtype, Yq.dtype, "tq_qk_norm_rope"
+    yq, yq_stride = _rows(Yq, shape, tout, where)
+    xq, xq_stride = _rows(Xq, shape, tin, where)
+    xk = yk = None
+    k_heads = xk_stride = yk_stride = 0
+    if Xk is not None:
+        kshape = Xk.shape
+        _, k_heads, _ = kshape
+        if kshape[0] != ntok or kshape[2] != dim:
+            raise TQError(TQ_ERR_SHAPE, where)
+        xk, xk_stride = _rows(Xk, kshape, tin, where)
+        yk, yk_stride = _rows(Yk, kshape, tout, where)
+    f32 = torch.float32
+    _launch(where, _load().tq_qk_norm_rope, Xq.get_device(), stream, xq, xq_stride, xk, xk_stride,
+            _type(Xq), yq, yq_stride, yk, yk_stride, _type(Yq), ntok, q_heads, k_heads, dim,
+            _vector(q_weight, dim, f32, where), _vector(k_weight, dim, f32, where), eps,
+            None if rope is None else rope.ref, _vector(positions, ntok, torch.int32, where))
 
 
 def tq_kv_append(Xq, Xk, Xv, Yq, kv: PagedKV, seq_ids, positions, rope: Rope | None = None,
                  q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
     """The same, with the keys and the values Xv written to kv at positions[t] of sequence
     seq_ids[t]; Yq is of the cache's type. Xq and Yq may be None."""
-    st = kv.struct
-    ntok = Xk.shape[0]
-    q_heads = 0 if Xq is None else Xq.shape[1]
-    kshape = (ntok, st.heads, st.head_dim)
-    if Xk.shape != kshape or Xv.shape != kshape or (
-            q_heads and (Xq.shape != (ntok, q_heads, st.head_dim) or Yq.shape != Xq.shape)):
-        raise TQError(TQ_ERR_SHAPE, "tq_kv_append")
-    if Xv.dtype != Xk.dtype or (q_heads and (Xq.dtype != Xk.dtype or Yq.dtype != kv.k.dtype)):
-        raise TQError(TQ_ERR_TYPE, "tq_kv_append")
-    _check_rows("tq_kv_append", st.head_dim, ntok, q_weight, k_weight, positions, seq_ids)
-    xq, yq = (_heads(Xq), _heads(Yq)) if q_heads else ((None, 0), (None, 0))
-    _call("tq_kv_append", Xk.device, *xq, *_heads(Xk), *_heads(Xv), _type(Xk), *yq, kv.ref,
-          _ptr(seq_ids), _ptr(positions), ntok, q_heads, _ptr(q_weight), _ptr(k_weight), eps,
-          None if rope is None else rope.ref, _stream(stream, Xk.device))
-
-
-def _check_rows(where, dim, ntok, q_weight, k_weight, *per_token):
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != dim):
-            raise TQError(TQ_ERR_SHAPE, where + ": a weight is float32 [head_dim]")
-    for t in per_token:
-        if t is not None and (t.dtype != torch.int32 or t.numel() != ntok):
-            raise TQError(TQ_ERR_SHAPE, where + ": positions and seq_ids are int32 [tokens]")
+    ntok, dim, where, tin = Xk.shape[0], kv.head_dim, "tq_kv_append", Xk.dtype
+    kshape = (ntok, kv.heads, dim)
+    xk, xk_stride = _rows(Xk, kshape, tin, where)
+    xv, xv_stride = _rows(Xv, kshape, tin, where)
+    xq = yq = None
+    q_heads = xq_stride = yq_stride = 0
+    if Xq is not None:
+        qshape = Xq.shape
+        _, q_heads, _ = qshape
+        if qshape[0] != ntok or qshape[2] != dim:
+            raise TQError(TQ_ERR_SHAPE, where)
+        xq, xq_stride = _rows(Xq, qshape, tin, where)
+        yq, yq_stride = _rows(Yq, qshape, kv.dtype, where)
+    f32, i32 = torch.float32, torch.int32
+    _launch(where, _load().tq_kv_append, Xk.get_device(), stream, xq, xq_stride, xk, xk_stride, xv,
+            xv_stride, _type(Xk), yq, yq_stride, kv.ref, _vector(seq_ids, ntok, i32, where),
+            _vector(positions, ntok, i32, where), ntok, q_heads,
+            _vector(q_weight, dim, f32, where), _vector(k_weight, dim, f32, where), eps,
+            None if rope is None else rope.ref)
 
 
 def tq_paged_attention_workspace_bytes(nseq: int, ntok: int, q_heads: int, kv_heads: int,
@@ -455,18 +489,19 @@ def tq_paged_attention(Q, kv: PagedKV, q_start, kv_len, O, max_q: int, max_kv: i
                        workspace=None, window: int = 0, lse=None, stream=None):
     """Causal attention of the new tokens Q [tokens][q_heads][head_dim], those of sequence b at
     q_start[b] .. q_start[b+1] - 1 and last of its kv_len[b] positions, over kv; O of any type."""
-    st = kv.struct
-    ntok, q_heads, dim = Q.shape
-    if dim != st.head_dim or O.shape != Q.shape or q_start.numel() != st.nseq + 1 or \
-            kv_len.numel() != st.nseq or (lse is not None and lse.shape != (ntok, q_heads)):
-        raise TQError(TQ_ERR_SHAPE, "tq_paged_attention")
-    if Q.dtype != kv.k.dtype or q_start.dtype != torch.int32 or kv_len.dtype != torch.int32 or (
-            lse is not None and lse.dtype != torch.float32):
-        raise TQError(TQ_ERR_TYPE, "tq_paged_attention")
-    _call("tq_paged_attention", Q.device, *_heads(Q), kv.ref, _ptr(q_start), _ptr(kv_len),
-          *_heads(O), _type(O), _ptr(lse), ntok, q_heads, max_q, max_kv, scale, window,
-          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-          _stream(stream, Q.device))
+    shape, where, i32 = Q.shape, "tq_paged_attention", torch.int32
+    ntok, q_heads, dim = shape
+    if dim != kv.head_dim:
+        raise TQError(TQ_ERR_SHAPE, where)
+    q, q_stride = _rows(Q, shape, kv.dtype, where)
+    o, o_stride = _rows(O, shape, O.dtype, where)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _launch(where, _load().tq_paged_attention, Q.get_device(), stream, q, q_stride, kv.ref,
+            _vector(q_start, kv.nseq + 1, i32, where), _vector(kv_len, kv.nseq, i32, where), o,
+            o_stride, _type(O), _vector(lse, ntok * q_heads, torch.float32, where), ntok, q_heads,
+            max_q, max_kv, scale, window, ws, ws_bytes)
 
 
 def tq_strerror(code: int) -> str:

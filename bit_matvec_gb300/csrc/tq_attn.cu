@@ -5,60 +5,73 @@
 namespace tq {
 namespace {
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+static_assert(kMaxSplits <= kJoinThreads, "a thread for each split");
 
 // Joins the partial results of the splits: o = sum_s 2^(lse_s - M) o_s /
 // sum_s 2^(lse_s - M), one thread block per row of one query head; a warp
-// takes every fourth split, a lane four values. All loads of a block are
+// takes every eighth split, a lane four values. All loads of a block are
 // independent (walking the splits one load after another measured 70 us for
 // 38 of them).
 __global__ void __launch_bounds__(kJoinThreads)
 attn_join_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ float weight[kMaxSplits];
-  __shared__ float red[4];
+  __shared__ float weight[kJoinThreads];
+  __shared__ float red[2][kJoinWarps];
   __shared__ float4 part[kJoinThreads];
   pdl_wait_primary();
   pdl_launch_dependents();
   const int64_t rows = p.ntok * p.q_heads, row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t tok = row / p.q_heads;
-  // tokens past the last sequence's are not written
-  if (tok >= p.q_start[p.nseq]) return;
   float lse = -INFINITY;
   if (threadIdx.x < p.nsplit) lse = p.part_lse[threadIdx.x * rows + row];
+  // tokens past the last sequence's are not written
+  if (tok >= p.q_start[p.nseq]) return;
   float top = lse;
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (lane == 0) red[warp] = top;
+  if (lane == 0) red[0][warp] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
   const float w = lse == -INFINITY ? 0.0f : exp2_approx(lse - top);
   weight[threadIdx.x] = w;
   float sum = w;
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) red[1][warp] = sum;
   __syncthreads();
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  sum = (red[0] + red[1]) + (red[2] + red[3]);
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) sum += red[1][i];
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (lane * 4 < p.dim) {
+    const float* from = p.part_o + row * p.dim + lane * 4;
 #pragma unroll 4
-    for (int s = warp; s < p.nsplit; s += 4) {
+    for (int s = warp; s < p.nsplit; s += kJoinWarps) {
+      // loaded in any case; nothing was written for an empty range
+      const float4 x = *reinterpret_cast<const float4*>(from + s * rows * p.dim);
       const float f = weight[s];
-      if (f == 0.0f) continue;   // nothing was written for an empty range
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (s * rows + row) * p.dim + lane * 4);
-      acc.x += f * x.x;
-      acc.y += f * x.y;
-      acc.z += f * x.z;
-      acc.w += f * x.w;
+      acc.x = f > 0.0f ? fmaf(f, x.x, acc.x) : acc.x;
+      acc.y = f > 0.0f ? fmaf(f, x.y, acc.y) : acc.y;
+      acc.z = f > 0.0f ? fmaf(f, x.z, acc.z) : acc.z;
+      acc.w = f > 0.0f ? fmaf(f, x.w, acc.w) : acc.w;
     }
   }
   part[threadIdx.x] = acc;
   __syncthreads();
   if (warp == 0 && lane * 4 < p.dim) {
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const float4 a = part[lane], b = part[lane + 32], c = part[lane + 64], d = part[lane + 96];
-    const float x[4] = {((a.x + b.x) + (c.x + d.x)) * inv, ((a.y + b.y) + (c.y + d.y)) * inv,
-                        ((a.z + b.z) + (c.z + d.z)) * inv, ((a.w + b.w) + (c.w + d.w)) * inv};
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+      const float4 a = part[lane + 32 * i];
+      x[0] += a.x;
+      x[1] += a.y;
+      x[2] += a.z;
+      x[3] += a.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= inv;
     store_out4(p.o, p.o_type, tok * p.o_stride + (row - tok * p.q_heads) * p.dim + lane * 4, x);
   }
   if (threadIdx.x == 0 && p.lse)

@@ -1,5 +1,6 @@
 // tq_attn_api.cu -- the C ABI of the norm/rotation, append and attention
 // calls: argument checks, planning, error reporting.
+#include <climits>
 #include <cmath>
 
 #include "tq_attn.cuh"
@@ -138,14 +139,21 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   if (window > 0 && window + max_q < span) span = window + max_q;
   int64_t tiles = ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0);
   if (tiles < 1) tiles = 1;
-  // Few blocks: split the keys until every slot has one. Many: ranges of 2048
-  // keys or more, so that ragged lengths spread evenly.
-  int64_t split = slots / units;
-  const int64_t spread = tiles * p.key_tile / 2048;
-  if (split < spread) split = units >= 16 * slots ? 1 : spread;
-  if (split > tiles * p.key_tile / 256) split = tiles * p.key_tile / 256;   // 256 keys or more
-  if (split > kMaxSplits) split = kMaxSplits;
-  if (split < 1) split = 1;
+  // The split with the least time in rounds of blocks, each the keys of one
+  // range and what starting and ending a block takes (about 192 keys): one
+  // round where blocks are few, several short ones (which ragged lengths fill
+  // better) where they are many. Ranges have 256 keys or more.
+  int64_t most = tiles * p.key_tile / 256;
+  if (most > kMaxSplits) most = kMaxSplits;
+  int64_t split = 1, least = INT64_MAX;
+  for (int64_t s = 1; s <= most || s == 1; ++s) {
+    const int64_t cost = ceil_div(units * s, slots) * (ceil_div(tiles, s) * p.key_tile + 192);
+    if (cost < least) {
+      least = cost;
+      split = s;
+    }
+    if (units * s > 16 * slots) break;
+  }
   p.chunk_tiles = (int)ceil_div(tiles, split);
   p.nsplit = (int)ceil_div(tiles, p.chunk_tiles);
   p.part_rows = p.nsplit > 1 ? p.nsplit * ntok * q_heads : 0;

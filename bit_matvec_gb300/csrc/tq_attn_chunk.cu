@@ -23,9 +23,11 @@
 // The work, every key tile of every row tile of every head, is laid in one
 // line (head, sequence, row tile, key tile) and cut into equal pieces, one for
 // each block: lengths, causality and the number of SMs then leave no SM idle,
-// and a row tile is cut at most where a piece ends. Blocks find their piece
-// from q_start and kv_len on the device. Cut row tiles leave partial results,
-// which a second kernel joins.
+// and a row tile is cut at most where a piece ends. With four blocks or more to
+// a row tile, where starting and ending a second one would weigh, each row
+// tile gets blocks of its own instead, as many as its share of the work. Blocks
+// find their piece from q_start and kv_len on the device. Cut row tiles leave
+// partial results, which a second kernel joins.
 #include <type_traits>
 
 #include "tq_attn_dev.cuh"
@@ -46,8 +48,8 @@ constexpr int kQueue = 4;             // segments the scheduling warp may be ahe
 // The cost of work, in units of about 0.45 us: a key tile of two halves, one of
 // up to 128 rows, starting and ending a row tile (1.8, 1.4 and 4.5 us measured
 // at dim 128), and the least work worth a block of its own.
-constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 10, kLeastWork = 16;
-constexpr int kCachedSeqs = 128;      // lengths of so many sequences are kept in shared memory
+constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 10, kLeastWork = 12;
+constexpr int kCachedSeqs = 48;       // lengths of so many sequences are kept in shared memory
 
 // A block's share of one row tile.
 struct Segment {
@@ -70,10 +72,10 @@ template <int DP> struct Smem {
   static constexpr int kBarBytes = 8 * (2 * kSlots + 8 + 2 * kQueue + 1);
   static constexpr int kFlags = kBars + (kBarBytes + 63) / 64 * 64;
   static constexpr int kSegs = kFlags + 64;
-  // the second softmax's maxima and sums; before the first segment, the scan
+  // the softmaxes' maxima and sums; before the first segment, the scan
   // of the work
   static constexpr int kStats = kSegs + kQueue * 64;
-  static constexpr int kSeqs = kStats + 1024;           // q_start, kv_len
+  static constexpr int kSeqs = kStats + 2048;           // q_start, kv_len
   static constexpr int kBytes = kSeqs + 8 * kCachedSeqs + 16;
   static_assert(kBytes <= 232448, "227 KB a block");
   static_assert(kQueue * sizeof(Segment) <= 256 && kFlags % 16 == 0, "regions");
@@ -276,6 +278,12 @@ struct Tiles {
   }
 };
 
+// a / b for non-negative values: the 64-bit division, some hundred dependent
+// instructions, only where it is needed.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Row tile `s` of sequence `b`, whole; n = -1 if the number is an empty one.
 __device__ __forceinline__ Segment row_tile(const Tiles& tiles, int64_t s, int b) {
   const AttnParams& p = tiles.p;
@@ -285,7 +293,7 @@ __device__ __forceinline__ Segment row_tile(const Tiles& tiles, int64_t s, int b
   const int64_t row0 = (s - tiles.first(b)) * kRows;
   if (row0 >= (int64_t)qn * p.group) return g;
   const int kv = max(tiles.kv_len[b], 0);
-  const int t = (int)(row0 / p.group);
+  const int t = (int)quotient(row0, p.group);
   g.seq = b;
   g.off = (int)(row0 - (int64_t)t * p.group);
   g.rows = (int)min((int64_t)kRows, (int64_t)qn * p.group - row0);
@@ -300,8 +308,9 @@ __device__ __forceinline__ Segment row_tile(const Tiles& tiles, int64_t s, int b
 __device__ __forceinline__ int unit_cost(const Segment& g) {
   return g.rows > kHalf ? kCostTwo : kCostAlt;
 }
-__device__ __forceinline__ int64_t tile_cost(const Segment& g) {
-  return g.n < 0 ? 0 : kTileCost + (int64_t)g.n * unit_cost(g);
+// (a tile without keys still has its rows to write)
+__device__ __forceinline__ int64_t tile_cost(const Segment& g, int tile) {
+  return g.n < 0 ? 0 : tile + max((int64_t)g.n * unit_cost(g), (int64_t)1);
 }
 
 __device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
@@ -383,11 +392,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   const Tiles tiles{p, cached ? seqs : p.q_start, cached ? seqs + kCachedSeqs + 1 : p.kv_len};
   const int64_t per = (numbers + kThreads - 1) / kThreads;
   const int64_t i0 = min((int64_t)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
+  constexpr int kCount = 44;   // the number of row tiles is added up above the cost
   int64_t mine = 0;
   const int b0 = i0 < i1 ? tiles.find(i0) : 0;
   for (int64_t s = i0, b = b0; s < i1; ++s) {
     while (b + 1 < p.nseq && tiles.first((int)b + 1) <= s) ++b;
-    mine += tile_cost(row_tile(tiles, s, (int)b));
+    const int64_t cost = tile_cost(row_tile(tiles, s, (int)b), 0);
+    mine += cost > 0 ? cost + (int64_t(1) << kCount) : 0;
   }
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
@@ -400,17 +411,47 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     if (w == warp) before += total;
     total += scan[w];
   }
-  const uint32_t tmem = flags[0];
   const int heads = p.q_heads / p.group;
+  const bool own = (total >> kCount) * heads * 4 <= gridDim.x;
+  const int tile_fee = own ? 0 : kTileCost;
+  auto cost_of = [&](int64_t sum) {
+    return (sum & ((int64_t(1) << kCount) - 1)) + (sum >> kCount) * tile_fee;
+  };
+  const int64_t tiles_before = before >> kCount, tiles_mine = mine >> kCount;
+  const int64_t head_tiles = total >> kCount;
+  total = cost_of(total);
+  before = cost_of(before);
+  mine = cost_of(mine);
+  const uint32_t tmem = flags[0];
   const int64_t all = total * heads;
-  const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, all / kLeastWork));
-  const int64_t x0 = blockIdx.x < blocks ? all * blockIdx.x / blocks : all;
-  const int64_t x1 = blockIdx.x < blocks ? all * (blockIdx.x + 1) / blocks : all;
-  const int64_t y0 = total > 0 ? x0 % total : 0;   // within its head
-  if (mine > 0 && before <= y0 && y0 < before + mine) {
-    scan[20] = i0;
-    scan[21] = b0;
-    scan[22] = before;
+  // as many blocks as there is work for
+  const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, quotient(all, kLeastWork)));
+  // own: every row tile has blocks of its own, those of the tile number i that
+  // has the cost `sum` before it from first_block(i, sum) on
+  const int64_t spare = max(blocks - head_tiles * heads, (int64_t)0);
+  auto first_block = [&](int64_t i, int64_t sum) { return i + quotient(sum * spare, max(all, (int64_t)1)); };
+  const int64_t block = blockIdx.x;
+  int64_t x0 = all, x1 = all;   // !own: the block's piece of the line
+  int head0 = 0;                // the head its first row tile belongs to
+  if (own) {
+    while (head0 + 1 < heads && first_block((head0 + 1) * head_tiles, (head0 + 1) * total) <= block) ++head0;
+    const int64_t i = head0 * head_tiles + tiles_before, sum = head0 * total + before;
+    if (mine > 0 && first_block(i, sum) <= block && block < first_block(i + tiles_mine, sum + mine)) {
+      scan[20] = i0;
+      scan[21] = b0;
+      scan[22] = before;
+      scan[23] = tiles_before;
+    }
+  } else if (block < blocks) {
+    x0 = quotient(all * block, blocks);
+    x1 = quotient(all * (block + 1), blocks);
+    head0 = (int)quotient(x0, total);
+    const int64_t y0 = x0 - head0 * total;
+    if (mine > 0 && before <= y0 && y0 < before + mine) {
+      scan[20] = i0;
+      scan[21] = b0;
+      scan[22] = before;
+    }
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
@@ -467,15 +508,25 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     auto load_queries = [&](const Segment& s) {
       if (tiles_of(s) == 0) return;
       const bool alt = s.rows <= kHalf;
+      // 16-byte chunk c of every kStep-th row
+      constexpr int kStep = kHalf / (DP / 8);
+      const int c = r % (DP / 8);
+      int qr = r / (DP / 8);
+      int hh = s.off + (alt ? qr : h * kHalf + qr), t = hh / p.group;
+      hh -= t * p.group;
+      const T* const q = static_cast<const T*>(p.q) + (int64_t)s.tok * p.q_stride +
+                         (int64_t)s.head * p.group * p.dim + c * 8;
+      const bool real = c * 8 < p.dim && p.scale_log2 != 0.0f;
 #pragma unroll 4
-      for (int i = r; i < kHalf * (DP / 8); i += kHalf) {
-        const int qr = i / (DP / 8), c = i % (DP / 8), tr = alt ? qr : h * kHalf + qr;
-        const int t = (s.off + tr) / p.group, hh = (s.off + tr) - t * p.group;
-        const bool use = tr < s.rows && c * 8 < p.dim && p.scale_log2 != 0.0f;
-        const T* q = static_cast<const T*>(p.q);
-        if (use)
-          q += (int64_t)(s.tok + t) * p.q_stride + (int64_t)(s.head * p.group + hh) * p.dim + c * 8;
-        copy16(base + h * S::kTile + (c >> 3) * kHalf * 128 + swz(qr, c & 7), q, use);
+      for (; qr < kHalf; qr += kStep) {
+        const bool use = real && (alt ? qr : h * kHalf + qr) < s.rows;
+        copy16(base + h * S::kTile + (c >> 3) * kHalf * 128 + swz(qr, c & 7),
+               use ? q + (int64_t)t * p.q_stride + (int64_t)hh * p.dim : p.q, use);
+        hh += kStep;
+        while (hh >= p.group) {
+          hh -= p.group;
+          ++t;
+        }
       }
     };
     auto queries_loaded = [&](const Segment& s) {
@@ -584,26 +635,22 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       float keep = 1.0f, other = 0.0f;
       const bool merge = alt && g.n > 1;
       if (merge) {
-        // the first softmax takes the second one's result from TMEM: warps of
-        // the same quadrant reach the same lanes
+        // each softmax takes the other one's result from TMEM: warps of the
+        // same quadrant reach the same lanes
         float* const stats = reinterpret_cast<float*>(basep + S::kStats);
-        if (h == 1) {
-          stats[r] = m;
-          stats[kHalf + r] = l;
-        }
+        stats[2 * h * kHalf + r] = m;
+        stats[(2 * h + 1) * kHalf + r] = l;
         tc_fence_before();
         named_barrier_sync(1, kSoft);
         tc_fence_after();
-        if (h == 0) {
-          const float m1 = stats[r], l1 = stats[kHalf + r];
-          const float mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
-          keep = exp2_approx(m - ref);
-          other = exp2_approx(m1 - ref);
-          l = l * keep + l1 * other;
-          m = mn;
-        }
+        const float m1 = stats[(2 - 2 * h) * kHalf + r], l1 = stats[(3 - 2 * h) * kHalf + r];
+        const float mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
+        keep = exp2_approx(m - ref);
+        other = exp2_approx(m1 - ref);
+        l = l * keep + l1 * other;
+        m = mn;
       }
-      if (!(alt && h == 1)) {
+      if (merge || !alt || h == 0) {
         // -------------------------------------------- output rows
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const float lse = l > 0.0f ? m + log2f(l) : -INFINITY;
@@ -611,33 +658,35 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int64_t tok = g.tok + trow;
         const int qh = g.head * p.group + (g.off + row) % p.group;
         const int64_t at = (int64_t)g.part * kRows + row;
-        if (live && g.part >= 0) p.part_lse[at] = lse;
-        if (live && g.part < 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
+        if (live && (h == 0 || !alt)) {
+          if (g.part >= 0) p.part_lse[at] = lse;
+          else if (p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
+        }
         void* const out = g.part >= 0 ? static_cast<void*>(p.part_o) : p.o;
         const int type = g.part >= 0 ? TQ_F32 : p.o_type;
         const int64_t obase = g.part >= 0 ? at * p.dim : tok * p.o_stride + (int64_t)qh * p.dim;
         keep *= inv;
         other *= inv;
+        // of merged rows each softmax writes half of the values
+        const int c0 = merge ? h * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t o[32] = {}, o1[32] = {};
+          if (n > 0) tmem_ld32(to + c, o);
+          if (merge) tmem_ld32(to + (h == 0 ? DP : -DP) + c, o1);
+          if (!live) continue;
 #pragma unroll
-        for (int c = 0; c < DP; c += 16) {
-          uint32_t o[16] = {}, o1[16] = {};
-          if (n > 0) {
-            tmem_ld16_nowait(to + c, o);
-            tmem_wait_ld16(o);
-          }
-          if (merge) {
-            tmem_ld16_nowait(to + DP + c, o1);
-            tmem_wait_ld16(o1);
-          }
-          const int left = p.dim - c;
-          if (!live || left <= 0) continue;
-          float x[16];
+          for (int q = 0; q < 32; q += 16) {
+            const int left = p.dim - c - q;
+            if (left <= 0) continue;
+            float x[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            x[e] = __uint_as_float(o[e]) * keep;
-            if (merge) x[e] = fmaf(__uint_as_float(o1[e]), other, x[e]);
+            for (int e = 0; e < 16; ++e) {
+              x[e] = __uint_as_float(o[q + e]) * keep;
+              if (merge) x[e] = fmaf(__uint_as_float(o1[q + e]), other, x[e]);
+            }
+            store_out16(out, type, obase + c + q, x, left);
           }
-          store_out16(out, type, obase + c, x, left);
         }
       }
       tc_fence_before();
@@ -658,31 +707,53 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
-        if (x0 < x1) {
-          int head = (int)(x0 / total), b = (int)scan[21];
-          int64_t s = scan[20], at = head * total + scan[22];   // number and start of the row tile
+        int b = (int)scan[21];
+        int64_t s = scan[20];   // number of the row tile
+        if (own) {
+          int64_t i = head0 * head_tiles + scan[23], sum = head0 * total + scan[22];
+          for (; all > 0 && block < head_tiles * heads + spare && s < numbers; ++s) {
+            while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
+            Segment g = row_tile(tiles, s, b);
+            const int64_t cost = tile_cost(g, 0);
+            if (cost == 0) continue;
+            const int64_t from = first_block(i, sum), to = first_block(i + 1, sum + cost);
+            ++i;
+            sum += cost;
+            if (block >= to) continue;
+            // piece j of `pieces` (none without a key tile, but for the only one)
+            const int j = (int)(block - from), n = g.n;
+            const int pieces = max(min((int)(to - from), n), 1);
+            if (j < pieces) {
+              const int t0 = (int)quotient((int64_t)n * j, pieces), t1 = (int)quotient((int64_t)n * (j + 1), pieces);
+              g.head = head0;
+              g.part = pieces == 1 ? -1 : 2 * (int)block;
+              if (pieces > 1 && j == 0) cut = {pieces, g.part, g.tok, g.off, g.rows, g.head};
+              g.t0 += t0;
+              g.n = t1 - t0;
+              push(g);
+            }
+            break;
+          }
+        } else if (x0 < x1) {
+          int head = head0;
+          int64_t at = head * total + scan[22];   // start of the row tile
           while (at < x1 && !*failed) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(tiles, s, b);
-            const int64_t cost = tile_cost(g);
+            const int64_t cost = tile_cost(g, tile_fee);
             if (cost > 0 && at + cost > x0) {
               // key tiles [from, to) of the row tile fall into the piece
               const int w = unit_cost(g), n = g.n;
               const int64_t u0 = max(x0 - at, (int64_t)0), u1 = min(x1 - at, cost);
-              const int from = (int)max((int64_t)0, min((u0 - kTileCost) / w, (int64_t)n));
-              const int to = u1 < kTileCost ? 0 : (int)min((u1 - kTileCost) / w, (int64_t)n);
+              const int from = u0 < tile_fee ? 0 : (int)min(quotient(u0 - tile_fee, w), (int64_t)n);
+              const int to = u1 < tile_fee ? 0 : (int)min(quotient(u1 - tile_fee, w), (int64_t)n);
               if (n == 0 ? u0 == 0 : from < to) {
                 g.head = head;
-                g.part = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (queued > 0);
+                g.part = from == 0 && to == n ? -1 : 2 * (int)block + (queued > 0);
                 if (g.part >= 0 && from == 0) {
-                  // the piece with the row tile's end, and so how many pieces
-                  const int64_t last = ((at + cost) * blocks + all - 1) / all - 1;
-                  cut.n = (int)(last - blockIdx.x) + 1;
-                  cut.part0 = g.part;
-                  cut.tok = g.tok;
-                  cut.off = g.off;
-                  cut.rows = g.rows;
-                  cut.head = head;
+                  // up to the piece with the row tile's end
+                  const int64_t last = quotient((at + cost) * blocks + all - 1, all) - 1;
+                  cut = {(int)(last - block) + 1, g.part, g.tok, g.off, g.rows, g.head};
                 }
                 g.t0 += from;
                 g.n = to - from;
@@ -712,25 +783,32 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int boxes = kKeys / p.box_rows;   // 1 .. 16, one lane each
         const int off = lane * p.box_rows;
         bool bad = false;
-        int page = p.pages, pslot = 0;
-        // page and slot of this lane's box of tile t; the page one past the
-        // cache (zeros, nothing read) where no row sees the box
+        // the table's entry for this lane's box of the next tile is loaded a
+        // tile ahead and looked at when its turn comes
+        int entry = -1, pslot = 0;
+        bool seen = false;   // some row sees the box
         auto locate = [&](int t) {
           const int key = t * kKeys + off;
-          page = p.pages;
-          pslot = 0;
-          if (lane < boxes && t < g.t0 + g.n && key < g.hi && key + p.box_rows > g.lo) {
+          seen = lane < boxes && t < g.t0 + g.n && key < g.hi && key + p.box_rows > g.lo;
+          if (seen) {
             const int lp = key / p.page_size;
             pslot = key - lp * p.page_size;
-            int pg = -1;
-            if (lp < p.table_width) pg = p.table[g.seq * p.table_stride + lp];
-            if (pg >= 0 && pg < p.pages) page = pg;
-            else bad = true;
+            entry = lp < p.table_width ? p.table[g.seq * p.table_stride + lp] : -1;
           }
         };
         locate(g.t0);
         for (int j = 0; j < g.n; ++j) {
-          const int pg = page, sl = pslot;
+          // the page one past the cache (zeros, nothing read) for a box that no
+          // row sees
+          int pg = p.pages, sl = 0;
+          if (seen) {
+            if (entry >= 0 && entry < p.pages) {
+              pg = entry;
+              sl = pslot;
+            } else {
+              bad = true;
+            }
+          }
           locate(g.t0 + j + 1);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -860,48 +938,47 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   }
 }
 
-constexpr int kJoinRows = 8;   // rows of a block of the join, one a warp
+constexpr int kJoinWarps = 8, kJoinBlocks = 32;  // warps of a block, blocks of a row tile
 
 // Joins the pieces of the row tiles that were cut: o = sum_s 2^(lse_s - M) o_s
 // / sum_s 2^(lse_s - M), a warp per row.
-__global__ void __launch_bounds__(kJoinRows * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 attn_chunk_join_kernel(const __grid_constant__ AttnParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const CutTile cut = static_cast<const CutTile*>(p.cuts)[blockIdx.x];
+  if (cut.n == 0) return;
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  if (r >= (cut.n > 0 ? cut.rows : 0)) return;
-  auto row_of = [&](int i) {
-    return (int64_t)(i == 0 ? cut.part0 : 2 * ((int)blockIdx.x + i)) * kRows + r;
-  };
-  float top = -INFINITY;
-  for (int i = lane; i < cut.n; i += 32) top = fmaxf(top, p.part_lse[row_of(i)]);
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float sum = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (top != -INFINITY) {
-#pragma unroll 4
+  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < cut.rows; r += kJoinWarps * kJoinBlocks) {
+    auto row_of = [&](int i) {
+      return (int64_t)(i == 0 ? cut.part0 : 2 * ((int)blockIdx.x + i)) * kRows + r;
+    };
+    float top = -INFINITY;
+    for (int i = lane; i < cut.n; i += 32) top = fmaxf(top, p.part_lse[row_of(i)]);
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
     for (int i = 0; i < cut.n; ++i) {
       const int64_t at = row_of(i);
-      const float f = exp2_approx(p.part_lse[at] - top);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (lane * 4 < p.dim) x = *reinterpret_cast<const float4*>(p.part_o + at * p.dim + lane * 4);
+      const float lse = p.part_lse[at];
+      const float f = lse == -INFINITY ? 0.0f : exp2_approx(lse - top);
       sum += f;
-      if (lane * 4 < p.dim) {
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at * p.dim + lane * 4);
-        acc.x += f * x.x;
-        acc.y += f * x.y;
-        acc.z += f * x.z;
-        acc.w += f * x.w;
-      }
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
     }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int t = (cut.off + r) / p.group;
+    const int64_t tok = cut.tok + t, qh = cut.head * p.group + (cut.off + r - t * p.group);
+    const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    if (lane * 4 < p.dim) store_out4(p.o, p.o_type, tok * p.o_stride + qh * p.dim + lane * 4, x);
+    if (lane == 0 && p.lse)
+      p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  const int t = (cut.off + r) / p.group;
-  const int64_t tok = cut.tok + t, qh = cut.head * p.group + (cut.off + r - t * p.group);
-  const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-  if (lane * 4 < p.dim) store_out4(p.o, p.o_type, tok * p.o_stride + qh * p.dim + lane * 4, x);
-  if (lane == 0 && p.lse)
-    p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <typename T, int DP>
@@ -917,8 +994,8 @@ cudaError_t launch_chunk(const AttnParams& p, const AttnCall& c, const CUtensorM
   r = launch_pdl(kernel, dim3(grid), dim3(kThreads), Smem<DP>::kBytes, s, p, kmap, vmap,
                  c.plan.tiles_x);
   if (r != cudaSuccess) return r;
-  return launch_pdl(attn_chunk_join_kernel, dim3(grid, kRows / kJoinRows), dim3(kJoinRows * 32), 0,
-                    s, p);
+  return launch_pdl(attn_chunk_join_kernel, dim3(grid, kJoinBlocks), dim3(kJoinWarps * 32), 0, s,
+                    p);
 }
 
 template <typename T>
