@@ -10,6 +10,8 @@ first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -18,6 +20,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libtq.so")
+CALL_PATH = os.path.join(_HERE, "_lib", "_tq_call.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "tq.h")
 
 TQ_OK = 0
@@ -306,8 +309,39 @@ def tq_matmul_host(Wtq: torch.Tensor, X_host: torch.Tensor, X: torch.Tensor, Xq:
 
 _TYPES = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
 
-# The calls below cost little on the GPU for a few tokens, so their marshalling is kept short: one
-# look at each tensor, and the current stream's handle without a stream object around it.
+# The calls below run for a few microseconds on the GPU for a few tokens, so their arguments are
+# marshalled in C (csrc/tq_call.c).
+
+_call_module = None
+_OTHER_DEVICE = 1   # what its functions return when the tensors are not on the current device
+
+
+def _calls():
+    global _call_module
+    if _call_module is None:
+        lib = _load()
+        if not os.path.exists(CALL_PATH):
+            raise RuntimeError(f"{CALL_PATH} is missing: build the library first "
+                               "(python -m bit_matvec_gb300.build, or __graft_entry__.build())")
+        loader = importlib.machinery.ExtensionFileLoader("_tq_call", CALL_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_tq_call", CALL_PATH, loader=loader))
+        loader.exec_module(module)
+        module.setup((torch.float32, torch.float16, torch.bfloat16, torch.int32),
+                     torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                     tuple(ctypes.cast(f, ctypes.c_void_p).value for f in
+                           (lib.tq_qk_norm_rope, lib.tq_kv_append, lib.tq_paged_attention)))
+        _call_module = module
+    return _call_module
+
+
+def _finish(rc: int, where: str, tensor: torch.Tensor, fn, args):
+    """What a call's status asks for: the same again on the tensors' own device, or an exception."""
+    if rc == _OTHER_DEVICE:
+        with torch.cuda.device(tensor.device):
+            rc = fn(*args)
+    if rc != TQ_OK:
+        raise TQError(rc, where)
 
 
 def _type(t: torch.Tensor) -> int:
@@ -315,47 +349,6 @@ def _type(t: torch.Tensor) -> int:
     if code is None:
         raise TQError(TQ_ERR_TYPE, str(t.dtype))
     return code
-
-
-def _rows(t: torch.Tensor, shape, dtype, where: str):
-    """(address, token stride) of a [tokens][heads][head_dim] tensor of this shape and type whose
-    heads are contiguous."""
-    if t.shape != shape:
-        raise TQError(TQ_ERR_SHAPE, where)
-    if t.dtype != dtype:
-        raise TQError(TQ_ERR_TYPE, where)
-    n, h, d = shape
-    s = t.stride()
-    if s[2] != 1 or s[1] != d:
-        if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-            raise ValueError("the heads of a token must be contiguous")
-    if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    return t.data_ptr(), s[0] if n > 1 else h * d
-
-
-def _vector(t: torch.Tensor | None, n: int, dtype, where: str):
-    """Address of a contiguous vector of n values, or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n:
-        raise TQError(TQ_ERR_SHAPE, f"{where}: {n} values of {dtype} expected")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("tensor must be contiguous, on a CUDA device")
-    return t.data_ptr()
-
-
-def _launch(name: str, fn, device: int, stream, *args):
-    """fn(*args, stream) with `device` current; stream None: its current stream."""
-    if device == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
-                else stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
-                    else stream.cuda_stream)
-    if rc != TQ_OK:
-        raise TQError(rc, name)
 
 
 class Rope:
@@ -408,8 +401,6 @@ class PagedKV:
             block_table.stride(0) if nseq > 1 else width, pages, page_size, heads, dim,
             k.stride(0), k.stride(1), k.stride(2), _type(k), 0)
         self.ref = ctypes.addressof(self.struct)
-        # what the calls compare their arguments with
-        self.nseq, self.heads, self.head_dim, self.dtype = nseq, heads, dim, k.dtype
 
 
 def tq_rope_turns(rot_dim: int, base: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -429,50 +420,24 @@ def tq_qk_norm_rope(Xq, Xk, Yq, Yk, positions=None, rope: Rope | None = None, q_
                     k_weight=None, eps: float = 1e-6, stream=None):
     """Norm and rotation of the heads of Xq and Xk [tokens][heads][head_dim] (views of a fused
     projection's rows are fine) into Yq and Yk; Xk and Yk may be None."""
-    shape = Xq.shape
-    ntok, q_heads, dim = shape
-    tin, tout, where = Xq.dtype, Yq.dtype, "tq_qk_norm_rope"
-    yq, yq_stride = _rows(Yq, shape, tout, where)
-    xq, xq_stride = _rows(Xq, shape, tin, where)
-    xk = yk = None
-    k_heads = xk_stride = yk_stride = 0
-    if Xk is not None:
-        kshape = Xk.shape
-        _, k_heads, _ = kshape
-        if kshape[0] != ntok or kshape[2] != dim:
-            raise TQError(TQ_ERR_SHAPE, where)
-        xk, xk_stride = _rows(Xk, kshape, tin, where)
-        yk, yk_stride = _rows(Yk, kshape, tout, where)
-    f32 = torch.float32
-    _launch(where, _load().tq_qk_norm_rope, Xq.get_device(), stream, xq, xq_stride, xk, xk_stride,
-            _type(Xq), yq, yq_stride, yk, yk_stride, _type(Yq), ntok, q_heads, k_heads, dim,
-            _vector(q_weight, dim, f32, where), _vector(k_weight, dim, f32, where), eps,
-            None if rope is None else rope.ref, _vector(positions, ntok, torch.int32, where))
+    fn = (_call_module or _calls()).qk_norm_rope
+    args = (Xq, Xk, Yq, Yk, positions, None if rope is None else rope.ref, q_weight, k_weight, eps,
+            stream)
+    rc = fn(*args)
+    if rc:
+        _finish(rc, "tq_qk_norm_rope", Xq, fn, args)
 
 
 def tq_kv_append(Xq, Xk, Xv, Yq, kv: PagedKV, seq_ids, positions, rope: Rope | None = None,
                  q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
     """The same, with the keys and the values Xv written to kv at positions[t] of sequence
     seq_ids[t]; Yq is of the cache's type. Xq and Yq may be None."""
-    ntok, dim, where, tin = Xk.shape[0], kv.head_dim, "tq_kv_append", Xk.dtype
-    kshape = (ntok, kv.heads, dim)
-    xk, xk_stride = _rows(Xk, kshape, tin, where)
-    xv, xv_stride = _rows(Xv, kshape, tin, where)
-    xq = yq = None
-    q_heads = xq_stride = yq_stride = 0
-    if Xq is not None:
-        qshape = Xq.shape
-        _, q_heads, _ = qshape
-        if qshape[0] != ntok or qshape[2] != dim:
-            raise TQError(TQ_ERR_SHAPE, where)
-        xq, xq_stride = _rows(Xq, qshape, tin, where)
-        yq, yq_stride = _rows(Yq, qshape, kv.dtype, where)
-    f32, i32 = torch.float32, torch.int32
-    _launch(where, _load().tq_kv_append, Xk.get_device(), stream, xq, xq_stride, xk, xk_stride, xv,
-            xv_stride, _type(Xk), yq, yq_stride, kv.ref, _vector(seq_ids, ntok, i32, where),
-            _vector(positions, ntok, i32, where), ntok, q_heads,
-            _vector(q_weight, dim, f32, where), _vector(k_weight, dim, f32, where), eps,
-            None if rope is None else rope.ref)
+    fn = (_call_module or _calls()).kv_append
+    args = (Xq, Xk, Xv, Yq, kv.ref, seq_ids, positions, None if rope is None else rope.ref, q_weight,
+            k_weight, eps, stream)
+    rc = fn(*args)
+    if rc:
+        _finish(rc, "tq_kv_append", Xk, fn, args)
 
 
 def tq_paged_attention_workspace_bytes(nseq: int, ntok: int, q_heads: int, kv_heads: int,
@@ -489,19 +454,11 @@ def tq_paged_attention(Q, kv: PagedKV, q_start, kv_len, O, max_q: int, max_kv: i
                        workspace=None, window: int = 0, lse=None, stream=None):
     """Causal attention of the new tokens Q [tokens][q_heads][head_dim], those of sequence b at
     q_start[b] .. q_start[b+1] - 1 and last of its kv_len[b] positions, over kv; O of any type."""
-    shape, where, i32 = Q.shape, "tq_paged_attention", torch.int32
-    ntok, q_heads, dim = shape
-    if dim != kv.head_dim:
-        raise TQError(TQ_ERR_SHAPE, where)
-    q, q_stride = _rows(Q, shape, kv.dtype, where)
-    o, o_stride = _rows(O, shape, O.dtype, where)
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _launch(where, _load().tq_paged_attention, Q.get_device(), stream, q, q_stride, kv.ref,
-            _vector(q_start, kv.nseq + 1, i32, where), _vector(kv_len, kv.nseq, i32, where), o,
-            o_stride, _type(O), _vector(lse, ntok * q_heads, torch.float32, where), ntok, q_heads,
-            max_q, max_kv, scale, window, ws, ws_bytes)
+    fn = (_call_module or _calls()).paged_attention
+    args = (Q, kv.ref, q_start, kv_len, O, max_q, max_kv, scale, workspace, window, lse, stream)
+    rc = fn(*args)
+    if rc:
+        _finish(rc, "tq_paged_attention", Q, fn, args)
 
 
 def tq_strerror(code: int) -> str:

@@ -1,4 +1,5 @@
-"""Build libtq.so (the C-ABI library) from csrc/*.cu with nvcc for sm_103a.
+"""Build libtq.so (the C-ABI library) from csrc/*.cu with nvcc for sm_103a, and the Python
+argument marshalling of csrc/tq_call.c with the host compiler.
 
 Each translation unit compiles in parallel; the shared library links the
 CUDA runtime statically, so it loads next to any PyTorch build. The output
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "libtq.so")
+CALL_SRC = os.path.join(CSRC, "tq_call.c")
+CALL = os.path.join(OUT_DIR, "_tq_call.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,6 +56,20 @@ def _run(cmd):
     return p.stdout
 
 
+def build_call(force: bool = False) -> str:
+    """The extension module that marshals the calls made once or more a decode step."""
+    deps = [CALL_SRC, os.path.join(ROOT, "include", "tq.h")]
+    if force or _stale(CALL, deps):
+        cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+        if not cc:
+            raise RuntimeError("no C compiler found (set CC)")
+        tmp = CALL + f".tmp{os.getpid()}"
+        _run([cc, "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-Wextra",
+              "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp])
+        os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     cc = nvcc()
@@ -74,6 +92,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         os.replace(tmp, obj)
         return src, out
 
+    build_call(force)
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 1)) as ex:
             for src, out in ex.map(compile_one, jobs):
