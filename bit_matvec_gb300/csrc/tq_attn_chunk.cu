@@ -45,10 +45,10 @@ constexpr int kSoft = 256;            // softmax threads, one a row
 constexpr int kThreads = kSoft + 128; // and an MMA, a TMA and a scheduling warp (and one that idles)
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
 constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
-// The cost of work, in units of about 0.45 us: a key tile of two halves, one of
-// up to 128 rows, starting and ending a row tile (1.8, 1.4 and 4.5 us measured
-// at dim 128), and the least work worth a block of its own.
-constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 10, kLeastWork = 12;
+// The cost of work, in units of about 0.4 us: a key tile of two halves, one of
+// up to 128 rows, starting and ending a row tile (1.6, 1.2 and 8 us measured at
+// dim 128), and the least work worth a block of its own.
+constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 18, kLeastWork = 12;
 constexpr int kCachedSeqs = 48;       // lengths of so many sequences are kept in shared memory
 
 // A block's share of one row tile.
@@ -210,11 +210,14 @@ __device__ __forceinline__ void copy16_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Minus infinity into the scores n of a 64-key piece outside (lo, hi].
-__device__ __forceinline__ void mask64(float (&s)[64], int lo, int hi) {
+// Minus infinity into the scores n of a 64-key piece above hi, or up to lo.
+__device__ __forceinline__ void mask_above(float (&s)[64], int hi) {
 #pragma unroll
-  for (int n = 0; n < 64; ++n)
-    if (n > hi || n <= lo) s[n] = -INFINITY;
+  for (int n = 0; n < 64; ++n) s[n] = n > hi ? -INFINITY : s[n];
+}
+__device__ __forceinline__ void mask_to(float (&s)[64], int lo) {
+#pragma unroll
+  for (int n = 0; n < 64; ++n) s[n] = n <= lo ? -INFINITY : s[n];
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -565,13 +568,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         const int key0 = (g.t0 + j) * kKeys;
         float a[64], b[64];
         tmem_ld128(ts, a, b);
-        // some row of the tile does not see some key
-        if (key0 + kKeys - 1 > g.pos || (p.window > 0 && key0 < g.lo + (g.hi - 1 - g.pos))) {
-          // the row sees the keys (pos - window, pos]
-          const int64_t from = p.window > 0 ? (int64_t)pos - p.window - key0 : -1;
-          const int f = (int)max(from, (int64_t)-1);
-          mask64(a, f, pos - key0);
-          mask64(b, f - 64, pos - key0 - 64);
+        // the row sees the keys (pos - window, pos]: where the tile has keys past
+        // its first row's, or before its last row's window
+        if (key0 + kKeys - 1 > g.pos) {
+          mask_above(a, pos - key0);
+          mask_above(b, pos - key0 - 64);
+        }
+        if (p.window > 0 && key0 < g.lo + (g.hi - 1 - g.pos)) {
+          const int to_key = (int)max((int64_t)pos - p.window - key0, (int64_t)-1);
+          mask_to(a, to_key);
+          mask_to(b, to_key - 64);
         }
         const float top = fmaxf(max64(a), max64(b)) * scale;
         if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
