@@ -148,6 +148,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.tiles_x = (int)c.plan.tiles_x;
   p.nsplit = c.plan.nsplit;
   p.chunk_tiles = c.plan.chunk_tiles;
+  p.cluster = c.plan.cluster;
   p.max_q = (int)c.max_q;
   p.o_type = c.o_type;
   p.window = c.window;
@@ -158,7 +159,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (c.plan.chunk) return launch_attn_chunk(p, c, kmap, vmap, s);
   e = launch_attn_decode(p, c, kmap, vmap, s);
-  if (e != cudaSuccess || p.nsplit == 1) return e;
+  if (e != cudaSuccess || p.nsplit == p.cluster) return e;
   const int64_t grid = c.ntok * c.q_heads;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   return launch_pdl(attn_join_kernel, dim3((unsigned)grid), dim3(kJoinThreads), 0, s, p);

@@ -51,6 +51,7 @@ struct RopeCall {
 cudaError_t launch_norm_rope(const RopeCall& c, cudaStream_t s);
 
 constexpr int kMaxSplits = 128;    // key ranges of a row tile
+constexpr int kMaxCluster = 8;     // of which so many can be one cluster
 
 // How a paged attention call is cut: a function of its sizes alone, so that
 // the workspace size is too.
@@ -60,7 +61,8 @@ struct AttnPlan {
   int key_tile;         // keys of a tile
   int64_t tiles_x;      // row tiles: of a sequence (few rows), numbers for all (many)
   int nsplit;           // few rows: key ranges of a row tile,
-  int chunk_tiles;      // and key tiles of a range
+  int chunk_tiles;      // and key tiles of a range,
+  int cluster;          // and ranges that join in a cluster (1: none)
   int blocks;           // many rows: thread blocks
   int64_t part_rows;    // rows of partial results
   int64_t ws_bytes;

@@ -17,7 +17,9 @@
 // 16 flop per byte, far from any rate, and registers give the softmax its
 // operands without a trip through TMEM.
 // The keys of a row tile are split over thread blocks where there are few of
-// them; partial results are joined by a second kernel.
+// them. Up to 8 blocks are a cluster and join their results through one
+// another's shared memory; those of more go through the workspace and a second
+// kernel, which costs about 3.5 us where the cluster takes 1.
 #include "tq_attn_dev.cuh"
 
 namespace tq {
@@ -42,6 +44,29 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Values at this block's shared address `a` in block s of the cluster.
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a, int s) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [r];\n\t}"
+      : "=f"(v.x), "=f"(v.y) : "r"(a), "r"(s) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, int s) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a), "r"(s) : "memory");
+  return v;
+}
+// A release-acquire barrier of all threads of the cluster's blocks.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
 }
 
 template <typename T>
@@ -83,6 +108,12 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const uint32_t bars = base + kStages * 2 * S::kTile;   // full[], then empty[]
   volatile int* const failed = reinterpret_cast<volatile int*>(basep + kStages * 2 * S::kTile + 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // of a cluster: this block's result, [row][DP] and (maximum, sum) of a row,
+  // in the last stage, past the warps' partial results
+  float* const mine_o = reinterpret_cast<float*>(basep + (kStages - 1) * 2 * S::kTile);
+  float* const mine_l = mine_o + kRows * DP;
+  static_assert(kWarps * 16 * (DP + 6) * 4 <= (kStages - 1) * 2 * S::kTile &&
+                kRows * (DP + 2) * 4 <= 2 * S::kTile, "merge regions");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -123,27 +154,33 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // ------------------------------------------------ producer
     const int boxes = kKeys / p.box_rows;    // 1 .. 16, one lane each
     const int off = lane * p.box_rows;
-    int page = p.pages, slot = 0;
-    bool bad = false;
-    // page and slot of this lane's box of tile t; the page one past the cache
-    // (zeros, nothing read) where no row sees the box
+    bool bad = false, seen = false;
+    int entry = -1, slot = 0;
+    // the table's entry for this lane's box of tile t is loaded a tile ahead and
+    // looked at when its turn comes; seen: some row sees the box
     auto locate = [&](int t) {
       const int key = t * kKeys + off;
-      page = p.pages;
-      slot = 0;
-      if (lane < boxes && t < t1 && key < hi && key + p.box_rows > lo) {
+      seen = lane < boxes && t < t1 && key < hi && key + p.box_rows > lo;
+      if (seen) {
         const int lp = key / p.page_size;
         slot = key - lp * p.page_size;
-        int pg = -1;
-        if (lp < p.table_width) pg = p.table[seq * p.table_stride + lp];
-        if (pg >= 0 && pg < p.pages) page = pg;
-        else bad = true;
+        entry = lp < p.table_width ? p.table[seq * p.table_stride + lp] : -1;
       }
     };
     locate(t0);
     int stage = 0, phase = 0;
     for (int t = t0; t < t1; ++t) {
-      const int pg = page, sl = slot;
+      // the page one past the cache (zeros, nothing read) for a box that no row
+      // sees
+      int pg = p.pages, sl = 0;
+      if (seen) {
+        if (entry >= 0 && entry < p.pages) {
+          pg = entry;
+          sl = slot;
+        } else {
+          bad = true;
+        }
+      }
       locate(t + 1);
       if (t - t0 >= kStages &&
           !mbarrier_wait_bounded(bars + 8 * (kStages + stage), phase ^ 1, kWaitNs)) {
@@ -357,6 +394,15 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           sum += f * ml[(w * kRows + r) * 2 + 1];
           acc += f * mo[(w * kRows + r) * kLd + d];
         }
+        if (p.cluster > 1) {
+          // this block's result, for the others of the cluster
+          mine_o[r * DP + d] = acc;
+          if (d == 0) {
+            mine_l[2 * r] = top;
+            mine_l[2 * r + 1] = sum;
+          }
+          continue;
+        }
         const float val = sum > 0.0f ? acc / sum : 0.0f;
         const float lse = sum > 0.0f ? ref + log2f(sum) : -INFINITY;
         const int64_t tok = q0 + (row0 + r) / p.group;
@@ -371,6 +417,51 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
     }
+  }
+  if (p.cluster > 1) {
+    __syncwarp();
+    cluster_sync();
+    // four values of a row a thread, dealt to all blocks of the cluster
+    const uint32_t at_o = smem_u32(mine_o), at_l = smem_u32(mine_l);
+    if (!*failed && warp < kWarps)
+      for (int i = split * kWarps * 32 + threadIdx.x; i < rows * (DP / 4); i += p.cluster * kWarps * 32) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d >= p.dim) continue;
+        float2 l[kMaxCluster];
+        float4 x[kMaxCluster];
+        float top = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+          l[s] = make_float2(-INFINITY, 0.0f);
+          x[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (s < p.cluster) {
+            l[s] = ld_cluster2(at_l + 8 * r, s);
+            x[s] = ld_cluster4(at_o + 4 * (r * DP + d), s);
+          }
+          top = fmaxf(top, l[s].x);
+        }
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+          const float f = exp2_approx(l[s].x - ref);
+          sum = fmaf(f, l[s].y, sum);
+          o[0] = fmaf(f, x[s].x, o[0]);
+          o[1] = fmaf(f, x[s].y, o[1]);
+          o[2] = fmaf(f, x[s].z, o[2]);
+          o[3] = fmaf(f, x[s].w, o[3]);
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= inv;
+        const int64_t tok = q0 + (row0 + r) / p.group;
+        const int qh = head * p.group + (row0 + r) % p.group;
+        store_out4(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, o);
+        if (d == 0 && p.lse)
+          p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+      }
+    __syncwarp();
+    cluster_sync();   // no block's shared memory goes before the others have read it
   }
   // after a failed wait the producer's copies are still counted on the full
   // barriers: no block leaves before they have landed
@@ -391,8 +482,21 @@ cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensor
   if (e != cudaSuccess) return e;
   const int64_t x = c.kv.nseq * p.tiles_x * p.nsplit;
   if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kernel, dim3((unsigned)x, (unsigned)c.kv.heads), dim3(kThreads),
-                    Smem<DP>::kBytes, s, p, kmap, vmap);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)x, (unsigned)c.kv.heads);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<DP>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap);
 }
 
 template <typename T, int DP>

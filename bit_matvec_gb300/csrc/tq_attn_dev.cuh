@@ -27,6 +27,7 @@ struct AttnParams {
   int* status;
   int q_heads, group, dim, page_size, pages, box_rows;
   int nseq, tiles_x, nsplit, chunk_tiles, max_q;
+  int cluster;          // few rows: splits that join within a cluster (1: none)
   int o_type;
   int64_t window;
   float scale_log2;
