@@ -151,7 +151,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.cluster = c.plan.cluster;
   p.max_q = (int)c.max_q;
   p.o_type = c.o_type;
-  p.window = c.window;
+  p.window = c.window >= kMaxPositions ? 0 : (int)c.window;
   p.scale_log2 = c.scale * kLog2e;
   CUtensorMap kmap, vmap;
   cudaError_t e = cache_map(&kmap, c.kv, c.kv.k, p.box_rows);

@@ -19,6 +19,7 @@ void note_other_kernel(cudaStream_t s);
 cudaError_t status_word(int** out);
 
 constexpr int kMaxRopeDim = 256;   // largest head of tq_qk_norm_rope
+constexpr int kMaxPositions = 1 << 30;   // of a sequence, and rows of a head of an attention call
 constexpr int kMaxKvDim = 128;     // largest head of the paged cache
 
 // One of the inputs of the norm/rotation kernel: its heads, where they come

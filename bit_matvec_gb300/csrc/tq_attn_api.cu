@@ -108,6 +108,9 @@ int take_rope(RopeCall& c, const float* qw, const float* kw, float eps, const tq
 constexpr int64_t kPlanSms = 152;
 constexpr int64_t kCutBytes = 32;   // a CutTile of the kernel for many rows
 
+// Limit of rows of a head and of positions, so that sums of two stay in 32 bits.
+static_assert(kMaxPositions <= (1 << 30), "32-bit arithmetic of the kernels");
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
@@ -302,7 +305,8 @@ int check_sizes(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads, i
   if (nseq < 0 || nseq > 0x7fffffff || ntok < 0 || ntok > 0x7fffffff || q_heads < 1 ||
       q_heads > 65535 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 8 ||
       head_dim % 8 != 0 || head_dim > kMaxKvDim || max_q < 0 || max_q > 0x7fffffff ||
-      max_kv < 0 || max_kv > 0x7fffffff || window < 0)
+      max_kv < 0 || max_kv > 0x7fffffff || window < 0 ||
+      (ntok + 1) * (q_heads / kv_heads) > kMaxPositions - 1024)
     return TQ_ERR_SHAPE;
   return TQ_OK;
 }

@@ -179,15 +179,6 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&a)[64], float
       : "memory");
 }
 
-// Waits for the loads, and keeps the use of r behind the wait.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :: "memory");
-}
-
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -266,11 +257,9 @@ struct Tiles {
   __device__ __forceinline__ int start(int b) const {
     return min(max(q_start[b], 0), (int)p.ntok);
   }
-  __device__ __forceinline__ int64_t first(int b) const {
-    return (int64_t)start(b) * p.group / kRows + b;
-  }
+  __device__ __forceinline__ int first(int b) const { return start(b) * p.group / kRows + b; }
   // the sequence that tile number s belongs to
-  __device__ __forceinline__ int find(int64_t s) const {
+  __device__ __forceinline__ int find(int s) const {
     int lo = 0, hi = p.nseq;   // f(lo) <= s < f(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -283,27 +272,28 @@ struct Tiles {
 
 // a / b for non-negative values: the 64-bit division, some hundred dependent
 // instructions, only where it is needed.
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : quotient64(a, b);
 }
 
 // Row tile `s` of sequence `b`, whole; n = -1 if the number is an empty one.
-__device__ __forceinline__ Segment row_tile(const Tiles& tiles, int64_t s, int b) {
+__device__ __forceinline__ Segment row_tile(const Tiles& tiles, int s, int b) {
   const AttnParams& p = tiles.p;
   Segment g = {};
   g.n = -1;
   const int q0 = tiles.start(b), qn = max(tiles.start(b + 1) - q0, 0);
-  const int64_t row0 = (s - tiles.first(b)) * kRows;
-  if (row0 >= (int64_t)qn * p.group) return g;
-  const int kv = max(tiles.kv_len[b], 0);
-  const int t = (int)quotient(row0, p.group);
+  const int row0 = (s - tiles.first(b)) * kRows;
+  if (row0 >= qn * p.group) return g;
+  const int kv = min(max(tiles.kv_len[b], 0), kMaxPositions);
+  const int t = row0 / p.group;
   g.seq = b;
-  g.off = (int)(row0 - (int64_t)t * p.group);
-  g.rows = (int)min((int64_t)kRows, (int64_t)qn * p.group - row0);
+  g.off = row0 - t * p.group;
+  g.rows = min(kRows, qn * p.group - row0);
   g.tok = q0 + t;
   g.pos = kv - qn + t;
   g.hi = max(g.pos + (g.off + g.rows - 1) / p.group + 1, 0);
-  g.lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)g.pos - p.window + 1) : 0;
+  g.lo = p.window > 0 ? max(0, g.pos - p.window + 1) : 0;
   g.t0 = g.lo / kKeys;
   g.n = max((g.hi + kKeys - 1) / kKeys - g.t0, 0);
   return g;
@@ -312,8 +302,8 @@ __device__ __forceinline__ int unit_cost(const Segment& g) {
   return g.rows > kHalf ? kCostTwo : kCostAlt;
 }
 // (a tile without keys still has its rows to write)
-__device__ __forceinline__ int64_t tile_cost(const Segment& g, int tile) {
-  return g.n < 0 ? 0 : tile + max((int64_t)g.n * unit_cost(g), (int64_t)1);
+__device__ __forceinline__ int tile_cost(const Segment& g, int tile) {
+  return g.n < 0 ? 0 : tile + max(g.n * unit_cost(g), 1);
 }
 
 __device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
@@ -335,7 +325,7 @@ struct CutTile {
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap, int64_t numbers) {
+                  const __grid_constant__ CUtensorMap vmap, int numbers) {
   using S = Smem<DP>;
   constexpr int kSlots = S::kSlots, kSub = DP / 64;
   extern __shared__ __align__(1024) uint8_t basep[];
@@ -393,14 +383,14 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     __syncthreads();
   }
   const Tiles tiles{p, cached ? seqs : p.q_start, cached ? seqs + kCachedSeqs + 1 : p.kv_len};
-  const int64_t per = (numbers + kThreads - 1) / kThreads;
-  const int64_t i0 = min((int64_t)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
+  const int per = (numbers + kThreads - 1) / kThreads;
+  const int i0 = min((int)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
   constexpr int kCount = 44;   // the number of row tiles is added up above the cost
   int64_t mine = 0;
   const int b0 = i0 < i1 ? tiles.find(i0) : 0;
-  for (int64_t s = i0, b = b0; s < i1; ++s) {
-    while (b + 1 < p.nseq && tiles.first((int)b + 1) <= s) ++b;
-    const int64_t cost = tile_cost(row_tile(tiles, s, (int)b), 0);
+  for (int s = i0, b = b0; s < i1; ++s) {
+    while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
+    const int cost = tile_cost(row_tile(tiles, s, b), 0);
     mine += cost > 0 ? cost + (int64_t(1) << kCount) : 0;
   }
   int64_t before = scan_warp(mine, lane);
@@ -459,7 +449,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
       if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
-          (int64_t)tiles.kv_len[b] > p.table_width * p.page_size)
+          tiles.kv_len[b] > min(p.table_width * p.page_size, (int64_t)kMaxPositions))
         *p.status = kDevIndex;
   __syncthreads();
 
@@ -575,7 +565,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mask_above(b, pos - key0 - 64);
         }
         if (p.window > 0 && key0 < g.lo + (g.hi - 1 - g.pos)) {
-          const int to_key = (int)max((int64_t)pos - p.window - key0, (int64_t)-1);
+          const int to_key = max(pos - p.window - key0, -1);
           mask_to(a, to_key);
           mask_to(b, to_key - 64);
         }
@@ -714,13 +704,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           ++queued;
         };
         int b = (int)scan[21];
-        int64_t s = scan[20];   // number of the row tile
+        int s = (int)scan[20];   // number of the row tile
         if (own) {
           int64_t i = head0 * head_tiles + scan[23], sum = head0 * total + scan[22];
           for (; all > 0 && block < head_tiles * heads + spare && s < numbers; ++s) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(tiles, s, b);
-            const int64_t cost = tile_cost(g, 0);
+            const int cost = tile_cost(g, 0);
             if (cost == 0) continue;
             const int64_t from = first_block(i, sum), to = first_block(i + 1, sum + cost);
             ++i;
@@ -746,13 +736,13 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           while (at < x1 && !*failed) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(tiles, s, b);
-            const int64_t cost = tile_cost(g, tile_fee);
+            const int cost = tile_cost(g, tile_fee);
             if (cost > 0 && at + cost > x0) {
               // key tiles [from, to) of the row tile fall into the piece
               const int w = unit_cost(g), n = g.n;
-              const int64_t u0 = max(x0 - at, (int64_t)0), u1 = min(x1 - at, cost);
-              const int from = u0 < tile_fee ? 0 : (int)min(quotient(u0 - tile_fee, w), (int64_t)n);
-              const int to = u1 < tile_fee ? 0 : (int)min(quotient(u1 - tile_fee, w), (int64_t)n);
+              const int u0 = (int)max(x0 - at, (int64_t)0), u1 = (int)min(x1 - at, (int64_t)cost);
+              const int from = u0 < tile_fee ? 0 : min((u0 - tile_fee) / w, n);
+              const int to = u1 < tile_fee ? 0 : min((u1 - tile_fee) / w, n);
               if (n == 0 ? u0 == 0 : from < to) {
                 g.head = head;
                 g.part = from == 0 && to == n ? -1 : 2 * (int)block + (queued > 0);
@@ -998,7 +988,7 @@ cudaError_t launch_chunk(const AttnParams& p, const AttnCall& c, const CUtensorM
   if (r != cudaSuccess) return r;
   const int grid = lim.sms < c.plan.blocks ? lim.sms : c.plan.blocks;
   r = launch_pdl(kernel, dim3(grid), dim3(kThreads), Smem<DP>::kBytes, s, p, kmap, vmap,
-                 c.plan.tiles_x);
+                 (int)c.plan.tiles_x);
   if (r != cudaSuccess) return r;
   return launch_pdl(attn_chunk_join_kernel, dim3(grid, kJoinBlocks), dim3(kJoinWarps * 32), 0, s,
                     p);

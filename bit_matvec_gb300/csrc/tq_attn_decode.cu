@@ -135,9 +135,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int ntok = (int)p.ntok;
   const int q0 = min(max(p.q_start[seq], 0), ntok);
   const int qn = min(max(p.q_start[seq + 1], q0), ntok) - q0;
-  const int kv = max(p.kv_len[seq], 0);
+  const int kv = min(max(p.kv_len[seq], 0), kMaxPositions);
   if (threadIdx.x == 0 && tile == 0 && split == 0 && head == 0 &&
-      (qn > p.max_q || (int64_t)kv > p.table_width * p.page_size))
+      (qn > p.max_q || p.kv_len[seq] > min(p.table_width * p.page_size, (int64_t)kMaxPositions)))
     *p.status = kDevIndex;
   const int row0 = tile * kRows;
   const int rows = min(kRows, qn * p.group - row0);
@@ -145,7 +145,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   // positions of the tile's first and last row; keys [lo, hi) are seen by some row
   const int pos_first = kv - qn + row0 / p.group, pos_last = kv - qn + (row0 + rows - 1) / p.group;
   const int hi = max(pos_last + 1, 0);
-  const int lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos_first - p.window + 1) : 0;
+  const int lo = p.window > 0 ? max(0, pos_first - p.window + 1) : 0;
   const int t_lo = lo / kKeys, t_hi = (hi + kKeys - 1) / kKeys;
   const int t0 = min(t_lo + split * p.chunk_tiles, t_hi);
   const int t1 = split == p.nsplit - 1 ? t_hi : min(t0 + p.chunk_tiles, t_hi);
@@ -278,14 +278,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         // in base-2 logarithms; masked ones to minus infinity
         float mx[2] = {-INFINITY, -INFINITY};
         const bool masked = key0 + 16 * NK - 1 > pos_first ||
-                            (p.window > 0 && (int64_t)key0 <= (int64_t)pos_last - p.window);
+                            (p.window > 0 && key0 <= pos_last - p.window);
         if (masked) {
 #pragma unroll
           for (int n = 0; n < 2 * NK; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int h = e >> 1, key = key0 + n * 8 + 2 * tq + (e & 1);
-              s[n][e] = key > pos[h] || (p.window > 0 && (int64_t)key <= (int64_t)pos[h] - p.window)
+              s[n][e] = key > pos[h] || (p.window > 0 && key <= pos[h] - p.window)
                             ? -INFINITY : s[n][e] * p.scale_log2;
               mx[h] = fmaxf(mx[h], s[n][e]);
             }

@@ -29,7 +29,7 @@ struct AttnParams {
   int nseq, tiles_x, nsplit, chunk_tiles, max_q;
   int cluster;          // few rows: splits that join within a cluster (1: none)
   int o_type;
-  int64_t window;
+  int window;           // 0: none
   float scale_log2;
 };
 

@@ -519,8 +519,8 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  *   lse f32 [ntok][q_heads]: log of the sum of exp(s_j); NULL: not written.
  *   max_q, max_kv  upper bounds of the new tokens and of kv_len of any
  *       sequence, which choose kernels and splits. A sequence of more than
- *       max_q new tokens, a kv_len beyond the table or a visible position
- *       whose page is outside the cache gives TQ_ERR_INDEX in
+ *       max_q new tokens, a kv_len beyond the table (or 2^30) or a visible
+ *       position whose page is outside the cache gives TQ_ERR_INDEX in
  *       tq_device_status(), and the sequence's rows are undefined; a kv_len
  *       beyond max_kv only costs speed.
  *   workspace  tq_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
@@ -531,8 +531,9 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  * kv_len, or before the window) may hold anything, NaN included, and their
  * pages are not read. Keys and values that some token of the sequence sees
  * must be finite.
- * Errors: TQ_ERR_SHAPE (also q_heads not a multiple of kv->heads, scale not
- * finite, window < 0), TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
+ * Errors: TQ_ERR_SHAPE (also q_heads not a multiple of kv->heads, ntok times
+ * the query heads of a key/value head near 2^30, scale not finite, window <
+ * 0), TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
  * TQ_ERR_WORKSPACE.
  */
 int tq_paged_attention(const void *Q, int64_t q_stride, const tq_paged_kv *kv,
