@@ -152,6 +152,8 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.max_q = (int)c.max_q;
   p.o_type = c.o_type;
   p.window = c.window >= kMaxPositions ? 0 : (int)c.window;
+  const int64_t positions = c.kv.table_width * c.kv.page_size;
+  p.max_positions = positions < kMaxPositions ? (int)positions : kMaxPositions;
   p.scale_log2 = c.scale * kLog2e;
   CUtensorMap kmap, vmap;
   cudaError_t e = cache_map(&kmap, c.kv, c.kv.k, p.box_rows);

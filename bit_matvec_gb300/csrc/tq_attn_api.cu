@@ -120,11 +120,17 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   AttnPlan p = {};
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
-  // up to 32 rows stay in one block of the kernel for few rows, which runs at
-  // the memory's rate there; from about 64 on the rate of mma.sync limits it
   const int64_t rows = max_q * group;
-  p.chunk = rows > 32;
-  p.tile_rows = p.chunk ? 256 : rows > 16 ? 32 : 16;
+  // keys that a row tile sees at most
+  int64_t span = max_kv;
+  if (window > 0 && window + max_q < span) span = window + max_q;
+  // Up to 32 rows go to the kernel for few rows, which runs near the memory's
+  // rate there, and up to 64 with heads of 64 (22 us for 16 drafts of 40 rows
+  // over up to 4096 positions, where the other takes 29) or short contexts
+  // (heads of 128: 22 us against 27 at 2000 positions, but 118 against 85 at
+  // 9000, where the rate of mma.sync limits it).
+  p.chunk = rows > 64 || (rows > 32 && head_dim > 64 && span > 2048);
+  p.tile_rows = p.chunk ? 256 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
   p.key_tile = p.chunk || head_dim <= 64 ? 128 : 64;
   if (p.chunk) {
     p.tiles_x = ntok * group / p.tile_rows + nseq;
@@ -136,10 +142,7 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   }
   p.tiles_x = 1;
   const int64_t units = kv_heads * nseq, slots = 2 * kPlanSms;
-  // keys that a row tile sees at most, in tiles (one more where the window
-  // does not start on a tile)
-  int64_t span = max_kv;
-  if (window > 0 && window + max_q < span) span = window + max_q;
+  // in tiles, one more where the window does not start on one
   int64_t tiles = ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0);
   if (tiles < 1) tiles = 1;
   // The split with the least time in rounds of blocks, in keys (128 take about

@@ -284,8 +284,8 @@ __device__ __forceinline__ Segment row_tile(const Tiles& tiles, int s, int b) {
   g.n = -1;
   const int q0 = tiles.start(b), qn = max(tiles.start(b + 1) - q0, 0);
   const int row0 = (s - tiles.first(b)) * kRows;
-  if (row0 >= qn * p.group) return g;
-  const int kv = min(max(tiles.kv_len[b], 0), kMaxPositions);
+  if (row0 < 0 || row0 >= qn * p.group) return g;   // (below 0: q_start not in order)
+  const int kv = min(max(tiles.kv_len[b], 0), p.max_positions);
   const int t = row0 / p.group;
   g.seq = b;
   g.off = row0 - t * p.group;
@@ -449,7 +449,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
       if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
-          tiles.kv_len[b] > min(p.table_width * p.page_size, (int64_t)kMaxPositions))
+          tiles.kv_len[b] > p.max_positions)
         *p.status = kDevIndex;
   __syncthreads();
 

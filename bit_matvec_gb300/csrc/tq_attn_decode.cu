@@ -109,11 +109,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   volatile int* const failed = reinterpret_cast<volatile int*>(basep + kStages * 2 * S::kTile + 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // of a cluster: this block's result, [row][DP] and (maximum, sum) of a row,
-  // in the last stage, past the warps' partial results
-  float* const mine_o = reinterpret_cast<float*>(basep + (kStages - 1) * 2 * S::kTile);
+  // past the warps' partial results
+  constexpr int kPartial = kWarps * 16 * (DP + 6) * 4;
+  float* const mine_o = reinterpret_cast<float*>(basep + kPartial);
   float* const mine_l = mine_o + kRows * DP;
-  static_assert(kWarps * 16 * (DP + 6) * 4 <= (kStages - 1) * 2 * S::kTile &&
-                kRows * (DP + 2) * 4 <= 2 * S::kTile, "merge regions");
+  static_assert(kPartial % 16 == 0 && kPartial + kRows * (DP + 2) * 4 <= kStages * 2 * S::kTile, "merge");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -135,9 +135,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int ntok = (int)p.ntok;
   const int q0 = min(max(p.q_start[seq], 0), ntok);
   const int qn = min(max(p.q_start[seq + 1], q0), ntok) - q0;
-  const int kv = min(max(p.kv_len[seq], 0), kMaxPositions);
+  const int kv = min(max(p.kv_len[seq], 0), p.max_positions);
   if (threadIdx.x == 0 && tile == 0 && split == 0 && head == 0 &&
-      (qn > p.max_q || p.kv_len[seq] > min(p.table_width * p.page_size, (int64_t)kMaxPositions)))
+      (qn > p.max_q || p.kv_len[seq] > p.max_positions))
     *p.status = kDevIndex;
   const int row0 = tile * kRows;
   const int rows = min(kRows, qn * p.group - row0);
@@ -504,7 +504,8 @@ cudaError_t launch_decode(const AttnParams& p, const AttnCall& c, const CUtensor
                           const CUtensorMap& vmap, cudaStream_t s) {
   switch (c.plan.tile_rows) {
     case 16: return launch_decode<T, DP, 1>(p, c, kmap, vmap, s);
-    default: return launch_decode<T, DP, 2>(p, c, kmap, vmap, s);
+    case 32: return launch_decode<T, DP, 2>(p, c, kmap, vmap, s);
+    default: return launch_decode<T, DP, 4>(p, c, kmap, vmap, s);
   }
 }
 

@@ -30,6 +30,7 @@ struct AttnParams {
   int cluster;          // few rows: splits that join within a cluster (1: none)
   int o_type;
   int window;           // 0: none
+  int max_positions;    // of the block table; a longer kv_len counts as this
   float scale_log2;
 };
 

@@ -207,6 +207,22 @@ def test_bad_pages_and_lengths_are_reported(tq):
         assert tq.tq_device_status() == tq.TQ_OK
 
 
+@pytest.mark.parametrize("starts", [[0, 90, 40, 130], [30, 60, 100, 130], [-7, 60, 100, 1 << 30]])
+def test_starts_out_of_order_stay_in_bounds(tq, starts):
+    """q_start that is not what it should be: whatever comes out, the call ends, stays within its
+    buffers (here between rows that are checked), and the next one is right."""
+    for new in ([1, 1, 1], [50, 40, 40]):
+        prob = list(problem([(200, n) for n in new], 8, 2, 64, 16, F16))
+        want, _ = call(tq, tuple(prob), F16)
+        good, ntok = prob[4], prob[0].shape[0]
+        prob[4] = torch.tensor([min(s, 2 * ntok) if s > 0 else s for s in starts], dtype=torch.int32)
+        call(tq, tuple(prob), F16, max_q=max(new))
+        tq.tq_device_status()
+        prob[4] = good
+        again, _ = call(tq, tuple(prob), F16)
+        assert torch.equal(want, again)
+
+
 def test_strided_queries_and_output(tq):
     prob = problem([(300, 3), (64, 1)], 4, 2, 64, 16, F16)
     Q, k, v, table, q_start, kv_len, kd, vd = prob
