@@ -314,6 +314,15 @@ __device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
   return x;
 }
 
+// Where a block's work starts: a row tile's number and sequence, its head, and
+// the cost before it.
+struct Start {
+  int number, seq, head, own;
+  int64_t x0, x1;     // the block's piece of the line (own: x0 row tiles before)
+  int64_t at;
+  int64_t all, blocks, spare;
+};
+
 // A row tile that was cut: its rows, and where its partial results are.
 struct CutTile {
   int n;              // pieces; 0: none here
@@ -344,6 +353,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   volatile uint32_t* const failed = flags + 1;   // flags[0]: TMEM address
   Segment* const queue = reinterpret_cast<Segment*>(basep + S::kSegs);
   int64_t* const scan = reinterpret_cast<int64_t*>(basep + S::kStats);
+  Start* const start = reinterpret_cast<Start*>(scan + 20);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -364,6 +374,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     mbarrier_init(drain, 1);
     *failed = 0;
     flags[2] = 0;
+    start->number = -1;
     mbarrier_init_fence();
   }
   if (warp == 8) {
@@ -423,29 +434,29 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   // has the cost `sum` before it from first_block(i, sum) on
   const int64_t spare = max(blocks - head_tiles * heads, (int64_t)0);
   auto first_block = [&](int64_t i, int64_t sum) { return i + quotient(sum * spare, max(all, (int64_t)1)); };
+  // What the scheduling warp needs goes through shared memory: held in
+  // registers across the roles it was spilled, and its first segment late.
   const int64_t block = blockIdx.x;
   int64_t x0 = all, x1 = all;   // !own: the block's piece of the line
   int head0 = 0;                // the head its first row tile belongs to
+  bool first_here;
   if (own) {
     while (head0 + 1 < heads && first_block((head0 + 1) * head_tiles, (head0 + 1) * total) <= block) ++head0;
     const int64_t i = head0 * head_tiles + tiles_before, sum = head0 * total + before;
-    if (mine > 0 && first_block(i, sum) <= block && block < first_block(i + tiles_mine, sum + mine)) {
-      scan[20] = i0;
-      scan[21] = b0;
-      scan[22] = before;
-      scan[23] = tiles_before;
+    first_here = mine > 0 && first_block(i, sum) <= block && block < first_block(i + tiles_mine, sum + mine);
+    x0 = i;
+    x1 = sum;
+  } else {
+    if (block < blocks) {
+      x0 = quotient(all * block, blocks);
+      x1 = quotient(all * (block + 1), blocks);
+      head0 = (int)quotient(x0, total);
     }
-  } else if (block < blocks) {
-    x0 = quotient(all * block, blocks);
-    x1 = quotient(all * (block + 1), blocks);
-    head0 = (int)quotient(x0, total);
     const int64_t y0 = x0 - head0 * total;
-    if (mine > 0 && before <= y0 && y0 < before + mine) {
-      scan[20] = i0;
-      scan[21] = b0;
-      scan[22] = before;
-    }
+    first_here = block < blocks && mine > 0 && before <= y0 && y0 < before + mine;
   }
+  if (first_here)
+    *start = {i0, b0, head0, own, x0, x1, own ? x1 : head0 * total + before, all, blocks, spare};
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
       if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
@@ -703,26 +714,27 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
-        int b = (int)scan[21];
-        int s = (int)scan[20];   // number of the row tile
-        if (own) {
-          int64_t i = head0 * head_tiles + scan[23], sum = head0 * total + scan[22];
-          for (; all > 0 && block < head_tiles * heads + spare && s < numbers; ++s) {
+        const Start st = *start;
+        int s = st.number, b = st.seq;   // number of the row tile, its sequence
+        if (s >= 0 && st.own) {
+          int64_t i = st.x0, sum = st.at;
+          for (; s < numbers; ++s) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(tiles, s, b);
             const int cost = tile_cost(g, 0);
             if (cost == 0) continue;
-            const int64_t from = first_block(i, sum), to = first_block(i + 1, sum + cost);
+            const int64_t from = i + quotient(sum * st.spare, st.all);
+            const int64_t to = i + 1 + quotient((sum + cost) * st.spare, st.all);
             ++i;
             sum += cost;
-            if (block >= to) continue;
+            if ((int64_t)blockIdx.x >= to) continue;
             // piece j of `pieces` (none without a key tile, but for the only one)
-            const int j = (int)(block - from), n = g.n;
+            const int j = (int)(blockIdx.x - from), n = g.n;
             const int pieces = max(min((int)(to - from), n), 1);
             if (j < pieces) {
               const int t0 = (int)quotient((int64_t)n * j, pieces), t1 = (int)quotient((int64_t)n * (j + 1), pieces);
-              g.head = head0;
-              g.part = pieces == 1 ? -1 : 2 * (int)block;
+              g.head = st.head;
+              g.part = pieces == 1 ? -1 : 2 * (int)blockIdx.x;
               if (pieces > 1 && j == 0) cut = {pieces, g.part, g.tok, g.off, g.rows, g.head};
               g.t0 += t0;
               g.n = t1 - t0;
@@ -730,26 +742,26 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
             break;
           }
-        } else if (x0 < x1) {
-          int head = head0;
-          int64_t at = head * total + scan[22];   // start of the row tile
-          while (at < x1 && !*failed) {
+        } else if (s >= 0) {
+          int head = st.head;
+          int64_t at = st.at;   // start of the row tile
+          while (at < st.x1 && !*failed) {
             while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
             Segment g = row_tile(tiles, s, b);
-            const int cost = tile_cost(g, tile_fee);
-            if (cost > 0 && at + cost > x0) {
+            const int cost = tile_cost(g, kTileCost);
+            if (cost > 0 && at + cost > st.x0) {
               // key tiles [from, to) of the row tile fall into the piece
               const int w = unit_cost(g), n = g.n;
-              const int u0 = (int)max(x0 - at, (int64_t)0), u1 = (int)min(x1 - at, (int64_t)cost);
-              const int from = u0 < tile_fee ? 0 : min((u0 - tile_fee) / w, n);
-              const int to = u1 < tile_fee ? 0 : min((u1 - tile_fee) / w, n);
+              const int u0 = (int)max(st.x0 - at, (int64_t)0), u1 = (int)min(st.x1 - at, (int64_t)cost);
+              const int from = u0 < kTileCost ? 0 : min((u0 - kTileCost) / w, n);
+              const int to = u1 < kTileCost ? 0 : min((u1 - kTileCost) / w, n);
               if (n == 0 ? u0 == 0 : from < to) {
                 g.head = head;
-                g.part = from == 0 && to == n ? -1 : 2 * (int)block + (queued > 0);
+                g.part = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (queued > 0);
                 if (g.part >= 0 && from == 0) {
                   // up to the piece with the row tile's end
-                  const int64_t last = quotient((at + cost) * blocks + all - 1, all) - 1;
-                  cut = {(int)(last - block) + 1, g.part, g.tok, g.off, g.rows, g.head};
+                  const int64_t last = quotient((at + cost) * st.blocks + st.all - 1, st.all) - 1;
+                  cut = {(int)(last - blockIdx.x) + 1, g.part, g.tok, g.off, g.rows, g.head};
                 }
                 g.t0 += from;
                 g.n = to - from;
@@ -949,23 +961,46 @@ attn_chunk_join_kernel(const __grid_constant__ AttnParams p) {
     auto row_of = [&](int i) {
       return (int64_t)(i == 0 ? cut.part0 : 2 * ((int)blockIdx.x + i)) * kRows + r;
     };
-    float top = -INFINITY;
-    for (int i = lane; i < cut.n; i += 32) top = fmaxf(top, p.part_lse[row_of(i)]);
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float sum = 0.0f;
+    // 32 pieces at a time, a lane's weight for each; their values are loaded
+    // beside the weights
+    float top = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int i = 0; i < cut.n; ++i) {
-      const int64_t at = row_of(i);
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (lane * 4 < p.dim) x = *reinterpret_cast<const float4*>(p.part_o + at * p.dim + lane * 4);
-      const float lse = p.part_lse[at];
-      const float f = lse == -INFINITY ? 0.0f : exp2_approx(lse - top);
-      sum += f;
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+    for (int i0 = 0; i0 < cut.n; i0 += 32) {
+      const int n = min(32, cut.n - i0);
+      const float lse = lane < n ? p.part_lse[row_of(i0 + lane)] : -INFINITY;
+      float4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n && lane * 4 < p.dim)
+          x[i] = *reinterpret_cast<const float4*>(p.part_o + row_of(i0 + i) * p.dim + lane * 4);
+      float m = lse;
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = fmaxf(m, top);
+      const float ref = m == -INFINITY ? 0.0f : m, old = exp2_approx(top - ref);
+      top = m;
+      float w = exp2_approx(lse - ref), all = w;
+      for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+      sum = sum * old + all;
+      acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+      for (int j = 0; j < n; j += 8) {
+        float4 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + 8 + i < n && lane * 4 < p.dim)
+            x[i] = *reinterpret_cast<const float4*>(p.part_o + row_of(i0 + j + 8 + i) * p.dim + lane * 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = __shfl_sync(0xffffffffu, w, (j + i) & 31);
+          if (j + i < n && lane * 4 < p.dim) {
+            acc.x = fmaf(f, y[i].x, acc.x);
+            acc.y = fmaf(f, y[i].y, acc.y);
+            acc.z = fmaf(f, y[i].z, acc.z);
+            acc.w = fmaf(f, y[i].w, acc.w);
+          }
+        }
+      }
     }
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const int t = (cut.off + r) / p.group;
