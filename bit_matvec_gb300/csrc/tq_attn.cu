@@ -138,6 +138,10 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.status = c.status;
   p.q_heads = (int)c.q_heads;
   p.group = (int)(c.q_heads / c.kv.heads);
+  // x * group < 2^32 makes the high product of x and the rounded-up reciprocal
+  // x / group; row numbers of a tile are below group + 256
+  if (p.group > 1 && p.group < (1 << 15))
+    p.group_inv = (uint32_t)(((uint64_t(1) << 32) + p.group - 1) / p.group);
   p.dim = (int)c.kv.head_dim;
   p.page_size = (int)c.kv.page_size;
   p.pages = (int)c.kv.pages;

@@ -506,6 +506,10 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     auto tiles_of = [&](const Segment& s) {
       return s.n < 0 ? 0 : s.rows <= kHalf ? (s.n - h + 1) / 2 : s.n;
     };
+    // x / group for row numbers of a tile, by the reciprocal
+    auto by_group = [&](int x) {
+      return p.group_inv ? (int)__umulhi((uint32_t)x, p.group_inv) : x / p.group;
+    };
     // This softmax's 128 rows of queries of segment s, in the background: rows
     // past the end and values past the head are zeros, and all of them with a
     // scale of zero.
@@ -514,23 +518,18 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       const bool alt = s.rows <= kHalf;
       // 16-byte chunk c of every kStep-th row
       constexpr int kStep = kHalf / (DP / 8);
-      const int c = r % (DP / 8);
-      int qr = r / (DP / 8);
-      int hh = s.off + (alt ? qr : h * kHalf + qr), t = hh / p.group;
-      hh -= t * p.group;
+      const int c = r % (DP / 8), qr0 = r / (DP / 8), half = alt ? 0 : h * kHalf;
       const T* const q = static_cast<const T*>(p.q) + (int64_t)s.tok * p.q_stride +
                          (int64_t)s.head * p.group * p.dim + c * 8;
       const bool real = c * 8 < p.dim && p.scale_log2 != 0.0f;
-#pragma unroll 4
-      for (; qr < kHalf; qr += kStep) {
-        const bool use = real && (alt ? qr : h * kHalf + qr) < s.rows;
+      // (a short loop: its instructions are fetched when the block starts)
+#pragma unroll 2
+      for (int i = 0; i < kHalf / kStep; ++i) {
+        const int qr = qr0 + i * kStep, x = s.off + half + qr;
+        const int t = by_group(x), hh = x - t * p.group;
+        const bool use = real && half + qr < s.rows;
         copy16(base + h * S::kTile + (c >> 3) * kHalf * 128 + swz(qr, c & 7),
-               use ? q + (int64_t)t * p.q_stride + (int64_t)hh * p.dim : p.q, use);
-        hh += kStep;
-        while (hh >= p.group) {
-          hh -= p.group;
-          ++t;
-        }
+               use ? q + (int64_t)t * p.q_stride + hh * p.dim : p.q, use);
       }
     };
     auto queries_loaded = [&](const Segment& s) {
@@ -556,7 +555,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         if (wait_for(seg_full + 8 * ((sg + 1) % kQueue), ((sg + 1) / kQueue) & 1, 20 * kWaitNs, false))
           load_queries(queue[(sg + 1) % kQueue]);
       };
-      const int trow = (g.off + min(row, g.rows - 1)) / p.group;
+      const int trow = by_group(g.off + min(row, g.rows - 1));
       const int pos = g.pos + trow;
       float m = -INFINITY;
       uint64_t l0 = 0, l1 = 0;

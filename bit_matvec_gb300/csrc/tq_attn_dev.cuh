@@ -25,6 +25,7 @@ struct AttnParams {
   int64_t q_stride, o_stride, table_stride, table_width;
   int64_t ntok;
   int* status;
+  uint32_t group_inv;   // ceil(2^32 / group), exact for numbers below 2^16; 0: divide
   int q_heads, group, dim, page_size, pages, box_rows;
   int nseq, tiles_x, nsplit, chunk_tiles, max_q;
   int cluster;          // few rows: splits that join within a cluster (1: none)

@@ -251,12 +251,13 @@ cudaError_t launch_as(const RopeCall& c, cudaStream_t s) {
                     dim3(kThreads), 0, s, c, cut);
 }
 
-// One head a group where heads are few, so that all SMs get some (3.1 us for
-// one token of 80 heads; 8 a group would leave it to 1 block), else up to 8.
+// One head a group where heads are few, so that all SMs get some (200 tokens of
+// 48 heads 3.1 us, 5.8 with 8 a group), else up to 8, which share more (800
+// tokens 7.1 us, 9.0 with one; the two are even near 24,000 heads).
 template <typename TI, typename TO, int LANES>
 cudaError_t launch_wide(const RopeCall& c, cudaStream_t s) {
   const int64_t rows = c.set[0].heads + c.set[1].heads + c.set[2].heads;
-  return c.ntok * rows < 8192 ? launch_as<TI, TO, 4, 1, LANES, 1>(c, s)
+  return c.ntok * rows < 24576 ? launch_as<TI, TO, 4, 1, LANES, 1>(c, s)
                               : launch_as<TI, TO, 4, 1, LANES, 8>(c, s);
 }
 
