@@ -57,7 +57,7 @@ int64_t cache_bytes(const tq_paged_kv& c) {
 
 int check_cache(const tq_paged_kv* c) {
   if (!c) return TQ_ERR_NULL;
-  if (c->nseq < 0 || c->nseq > 0x7fffffff || c->table_width < 0 || c->table_width > 0x7fffffff ||
+  if (c->nseq < 0 || c->nseq > kMaxPositions || c->table_width < 0 || c->table_width > 0x7fffffff ||
       !size_ok(c->table_stride) || c->table_stride < c->table_width || c->pages < 1 ||
       c->pages > 0x7ffffffe || c->page_size < 8 || c->page_size % 8 != 0 ||
       c->page_size > (1 << 24) || c->heads < 1 || c->heads > 65535 || c->head_dim < 8 ||
@@ -305,7 +305,7 @@ int tq_kv_append(const void* Xq, int64_t xq_stride, const void* Xk, int64_t xk_s
 namespace {
 int check_sizes(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                 int64_t max_q, int64_t max_kv, int64_t window) {
-  if (nseq < 0 || nseq > 0x7fffffff || ntok < 0 || ntok > 0x7fffffff || q_heads < 1 ||
+  if (nseq < 0 || nseq > kMaxPositions || ntok < 0 || ntok > 0x7fffffff || q_heads < 1 ||
       q_heads > 65535 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 8 ||
       head_dim % 8 != 0 || head_dim > kMaxKvDim || max_q < 0 || max_q > 0x7fffffff ||
       max_kv < 0 || max_kv > 0x7fffffff || window < 0 ||

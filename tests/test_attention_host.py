@@ -130,7 +130,7 @@ def append(tq, kv=None, **over):
 
 BAD_CACHES = [(dict(page=12), "SHAPE"), (dict(page=0), "SHAPE"), (dict(dim=60), "SHAPE"),
               (dict(dim=136, hs=4096, ps=8192, ss=136), "SHAPE"), (dict(heads=0), "SHAPE"),
-              (dict(pages=0), "SHAPE"), (dict(nseq=-1), "SHAPE"), (dict(tstride=3), "SHAPE"),
+              (dict(pages=0), "SHAPE"), (dict(nseq=-1), "SHAPE"), (dict(nseq=(1 << 30) + 1), "SHAPE"), (dict(tstride=3), "SHAPE"),
               (dict(ss=68), "SHAPE"), (dict(ss=56), "SHAPE"), (dict(hs=8), "SHAPE"), (dict(ps=-8), "SHAPE"),
               (dict(type=0), "TYPE"), (dict(type=7), "TYPE"), (dict(k=None), "NULL"),
               (dict(table=None), "NULL"), (dict(k=A + 8), "ALIGN"), (dict(table=C + 2), "ALIGN")]
@@ -173,7 +173,7 @@ def attend(tq, kv=None, **over):
     (dict(hq=3), "SHAPE"), (dict(hq=0), "SHAPE"), (dict(n=-1), "SHAPE"), (dict(mq=-1), "SHAPE"),
     (dict(mkv=-1), "SHAPE"), (dict(window=-1), "SHAPE"), (dict(scale=math.nan), "SHAPE"),
     (dict(scale=math.inf), "SHAPE"), (dict(qs=250), "SHAPE"), (dict(qs=260), "SHAPE"), (dict(os=255), "SHAPE"),
-    (dict(ot=4), "TYPE"), (dict(q=None), "NULL"), (dict(o=None), "NULL"), (dict(start=None), "NULL"),
+    (dict(n=1 << 29), "SHAPE"), (dict(ot=4), "TYPE"), (dict(q=None), "NULL"), (dict(o=None), "NULL"), (dict(start=None), "NULL"),
     (dict(lens=None), "NULL"), (dict(q=D + 8), "ALIGN"), (dict(o=E + 2), "ALIGN"), (dict(lse=E + 65537), "ALIGN"),
     (dict(o=D), "ALIAS"), (dict(o=A), "ALIAS"), (dict(lse=G), "ALIAS"), (dict(o=E, lse=E + 64), "ALIAS"),
 ])
@@ -209,3 +209,21 @@ def test_binding_checks(tq):
         tq.Rope(torch.zeros(4))
     with pytest.raises(tq.TQError):
         tq.tq_qk_norm_rope(t, None, torch.zeros(2, 2, 32), None)
+
+
+def test_marshalling_module(tq):
+    """What the C marshalling refuses before it looks for a GPU."""
+    calls = __import__("bit_matvec_gb300.binding", fromlist=["_calls"])._calls()
+    x = torch.zeros(3, 2, 64)
+    for bad in ([], [x] * 3, [None] * 11):
+        with pytest.raises(TypeError):
+            calls.qk_norm_rope(*bad)
+    with pytest.raises(AttributeError):
+        tq.tq_qk_norm_rope(5, None, x, None)
+    for other in (torch.zeros(3, 2, 32), torch.zeros(3, 128), torch.zeros(2, 2, 64)):
+        with pytest.raises(tq.TQError) as e:
+            tq.tq_qk_norm_rope(x, None, other, None)
+        assert e.value.code == tq.TQ_ERR_SHAPE
+    with pytest.raises(tq.TQError) as e:
+        tq.tq_qk_norm_rope(x.double(), None, x, None)
+    assert e.value.code == tq.TQ_ERR_TYPE

@@ -114,6 +114,29 @@ def test_attention(tq, case):
     check(tq, problem(lens, hq, hk, dim, page, dtype, order=order, window=window), out, window)
 
 
+@pytest.mark.parametrize("nseq,most", [(49, 60), (70, 40), (420, 25)])
+def test_many_sequences_of_many_rows(tq, nseq, most):
+    """More sequences than the lengths kept in shared memory, and more row tiles than threads; some
+    sequences empty, some without new tokens, some of one token among chunks."""
+    g = torch.Generator().manual_seed(nseq)
+    lens = []
+    for b in range(nseq):
+        q = int(torch.randint(0, most, (1,), generator=g)) if b % 7 else b % 2
+        lens.append((q + int(torch.randint(0, 200, (1,), generator=g)) if b % 11 else q, q))
+    lens[3] = (150, most)
+    check(tq, problem(lens, 8, 2, 64, 16, BF16), BF16)
+
+
+@pytest.mark.parametrize("lens,hq,hk", [([(257, 256)], 1, 1), ([(3000, 128)], 1, 1), ([(3000, 129)], 1, 1),
+                                        ([(2600, 1), (1300, 300)], 7, 1), ([(128, 128)] * 40, 8, 8),
+                                        ([(6000, 70)], 2, 1), ([(130, 3)] * 3, 64, 1)])
+def test_row_tile_edges(tq, lens, hq, hk):
+    """Row tiles of exactly 128, 129 and 256 rows, groups that do not divide them, a row tile cut
+    into many pieces, several row tiles a block."""
+    for dim in (64, 128):
+        check(tq, problem(lens, hq, hk, dim, 32, F16), F32)
+
+
 @pytest.mark.parametrize("new", [1, 3, 300])
 def test_tokens_that_see_nothing(tq, new):
     """A kv_len below the number of new tokens: the first ones stand before position 0."""
