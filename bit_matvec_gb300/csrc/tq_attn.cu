@@ -136,6 +136,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t s) {
   p.table_width = c.kv.table_width;
   p.ntok = c.ntok;
   p.status = c.status;
+  p.stall_ns = (uint64_t)take_debug_stall();
   p.q_heads = (int)c.q_heads;
   p.group = (int)(c.q_heads / c.kv.heads);
   // x * group < 2^32 makes the high product of x and the rounded-up reciprocal

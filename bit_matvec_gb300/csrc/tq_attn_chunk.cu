@@ -355,6 +355,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   int64_t* const scan = reinterpret_cast<int64_t*>(basep + S::kStats);
   Start* const start = reinterpret_cast<Start*>(scan + 20);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool stalled = p.stall_ns > 0 && blockIdx.x == 0;
+  const uint64_t limit = stalled ? p.stall_ns : kWaitNs;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -469,17 +471,17 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   // softmax warps still meet at their barriers), results are undefined and the
   // status word says so. The waits for the segment queue are apart: they only
   // depend on warps that always get there, and all warps see every segment.
-  auto wait_for = [&](uint32_t bar, uint32_t parity, uint64_t limit, bool heed) {
+  auto wait_for = [&](uint32_t bar, uint32_t parity, uint64_t most, bool heed) {
     if (mbarrier_test_wait(bar, parity)) return true;
     const uint64_t t = global_timer_ns();
     for (uint32_t i = 0; i < (1u << 28) && !(heed && *failed); ++i) {
       if (mbarrier_try_wait(bar, parity)) return true;
-      if ((i & 15u) == 15u && global_timer_ns() - t > limit) break;
+      if ((i & 15u) == 15u && global_timer_ns() - t > most) break;
     }
     *failed = 1;
     return false;
   };
-  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_for(bar, parity, kWaitNs, true); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_for(bar, parity, limit, true); };
   auto wait_item = [&](int item) { return wait(full + 8 * (item % kSlots), (item / kSlots) & 1); };
   // The next segment of the queue, for a warp; false at the end.
   auto next_segment = [&](int sg, Segment& g) {
@@ -786,7 +788,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       Segment g;
       for (int sg = 0; next_segment(sg, g); ++sg) {
         // ---------------------------------------------- TMA
-        if (__any_sync(0xffffffffu, *failed)) continue;
+        if (__any_sync(0xffffffffu, *failed) || stalled) continue;
         const int boxes = kKeys / p.box_rows;   // 1 .. 16, one lane each
         const int off = lane * p.box_rows;
         bool bad = false;
@@ -928,11 +930,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     if (warp == 10) {
       const int issued = (int)flags[2];
       if (lane < kSlots && issued > lane)
-        mbarrier_wait_bounded(full + 8 * lane, ((issued - 1 - lane) / kSlots) & 1, kWaitNs / 10);
+        mbarrier_wait_bounded(full + 8 * lane, ((issued - 1 - lane) / kSlots) & 1, limit / 10);
     }
     if (warp == 8) {
       commit(elect_one(), drain);
-      mbarrier_wait_bounded(drain, 0, kWaitNs / 10);
+      mbarrier_wait_bounded(drain, 0, limit / 10);
     }
     __syncwarp();
   }

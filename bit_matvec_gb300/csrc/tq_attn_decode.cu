@@ -115,6 +115,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   float* const mine_l = mine_o + kRows * DP;
   static_assert(kPartial % 16 == 0 && kPartial + kRows * (DP + 2) * 4 <= kStages * 2 * S::kTile, "merge");
 
+  const bool stalled = p.stall_ns > 0 && blockIdx.x == 0 && blockIdx.y == 0;
+  const uint64_t limit = stalled ? p.stall_ns : kWaitNs;
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbarrier_init(bars + 8 * i, 1);
@@ -169,7 +172,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     };
     locate(t0);
     int stage = 0, phase = 0;
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0; t < t1 && !stalled; ++t) {
       // the page one past the cache (zeros, nothing read) for a box that no row
       // sees
       int pg = p.pages, sl = 0;
@@ -183,7 +186,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       }
       locate(t + 1);
       if (t - t0 >= kStages &&
-          !mbarrier_wait_bounded(bars + 8 * (kStages + stage), phase ^ 1, kWaitNs)) {
+          !mbarrier_wait_bounded(bars + 8 * (kStages + stage), phase ^ 1, limit)) {
         *failed = 1;
         break;
       }
@@ -241,7 +244,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     int stage = 0, phase = 0;
     bool ok = true;
     for (int t = t0; t < t1; ++t) {
-      if (!mbarrier_wait_bounded(bars + 8 * stage, phase, kWaitNs)) {
+      if (!mbarrier_wait_bounded(bars + 8 * stage, phase, limit)) {
         ok = false;
         break;
       }
@@ -466,9 +469,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   // after a failed wait the producer's copies are still counted on the full
   // barriers: no block leaves before they have landed
   __syncthreads();
-  if (*failed && threadIdx.x < kStages) {
+  if (*failed && threadIdx.x < kStages && !stalled) {
     const int issued = (t1 - t0 - (int)threadIdx.x + kStages - 1) / kStages;
-    if (issued > 0) mbarrier_wait_bounded(bars + 8 * threadIdx.x, (issued - 1) & 1, kWaitNs / 10);
+    if (issued > 0) mbarrier_wait_bounded(bars + 8 * threadIdx.x, (issued - 1) & 1, limit / 10);
   }
 }
 

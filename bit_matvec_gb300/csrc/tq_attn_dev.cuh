@@ -10,7 +10,7 @@ namespace tq {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint64_t kWaitNs = 1000000000ull;   // limit of every wait in the attention kernels
+constexpr uint64_t kWaitNs = 1000000000ull;   // limit of the waits in the attention kernels
 
 struct AttnParams {
   const void* q;
@@ -25,6 +25,8 @@ struct AttnParams {
   int64_t q_stride, o_stride, table_stride, table_width;
   int64_t ntok;
   int* status;
+  uint64_t stall_ns;    // test facility, if not 0: the first block requests no tiles,
+                        // and its waits have this limit
   uint32_t group_inv;   // ceil(2^32 / group), exact for numbers below 2^16; 0: divide
   int q_heads, group, dim, page_size, pages, box_rows;
   int nseq, tiles_x, nsplit, chunk_tiles, max_q;

@@ -581,7 +581,7 @@ int tq_probe_read_sum(const void *buf, int64_t bytes, uint32_t *out, int early, 
 
 /*
  * tq_debug_stall_next_launch -- test facility for the timeout path (the pages
- * have no counterpart). The next matmul kernel this library launches, from
+ * have no counterpart). The next such kernel this library launches, from
  * any host thread and on any stream, runs with its first thread block (the
  * first pair of blocks for the tensor-core kernel, which runs on CTA pairs)
  * requesting none of its input copies, as if they never arrived: those
@@ -591,8 +591,9 @@ int tq_probe_read_sum(const void *buf, int64_t bytes, uint32_t *out, int early, 
  * TQ_ERR_TIMEOUT (and clears the word). The block still waits for any copy
  * it did request before it exits, so no copy outlives it. Nothing faults and
  * nothing waits without bound. Kernels that take it: the GEMV (ntok <= 16, or <= 8
- * in the workspace forms) and
- * the tensor-core kernel of the workspace forms. wait_limit_ns = 0 cancels a
+ * in the workspace forms),
+ * the tensor-core kernel of the workspace forms and the kernels of
+ * tq_paged_attention (their usual limit is 1 s). wait_limit_ns = 0 cancels a
  * pending stall.
  * Errors: TQ_ERR_SHAPE if wait_limit_ns < 0.
  */

@@ -323,6 +323,30 @@ def test_append_then_attend(tq):
     assert_within(O, o, tol, "o")
 
 
+@pytest.mark.parametrize("lens,hq,hk", [([(300, 1)], 4, 4), ([(20000, 1)], 2, 1), ([(900, 200)], 4, 1),
+                                        ([(900, 40), (500, 300)] * 5, 8, 8), ([(70, 40)] * 200, 8, 2)])
+def test_timeout_reported_then_cleared(tq, lens, hq, hk):
+    """A first block whose tiles never arrive gives up after a short limit, says so once, and the
+    next call is right: one block of the few-row kernel, a cluster, many splits, the many-row one."""
+    import time
+    for dim in (64, 128):
+        prob = problem(lens, hq, hk, dim, 16, F16)
+        want, _ = call(tq, prob, F16)
+        torch.cuda.synchronize()
+        tq.tq_debug_stall_next_launch(200_000)
+        try:
+            t = time.perf_counter()
+            call(tq, prob, F16)
+            torch.cuda.synchronize()
+            t = time.perf_counter() - t
+        finally:
+            tq.tq_debug_stall_next_launch(0)
+        assert tq.tq_device_status() == tq.TQ_ERR_TIMEOUT
+        assert t < 0.8 and tq.tq_device_status() == tq.TQ_OK
+        again, _ = call(tq, prob, F16)
+        assert torch.equal(want, again)
+
+
 def test_no_work(tq):
     prob = problem([(0, 0), (20, 0)], 2, 2, 64, 16, F16)
     O, L = call(tq, prob, F16, max_q=1)
