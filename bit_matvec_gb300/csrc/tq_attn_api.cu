@@ -1,5 +1,6 @@
 // tq_attn_api.cu -- the C ABI of the norm/rotation, append and attention
 // calls: argument checks, planning, error reporting.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -121,47 +122,55 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
   const int64_t rows = max_q * group;
-  // keys that a row tile sees at most
-  int64_t span = max_kv;
-  if (window > 0 && window + max_q < span) span = window + max_q;
-  // Up to 32 rows go to the kernel for few rows, which runs near the memory's
-  // rate there, and up to 64 with heads of 64 (22 us for 16 drafts of 40 rows
-  // over up to 4096 positions, where the other takes 29) or short contexts
-  // (heads of 128: 22 us against 27 at 2000 positions, but 118 against 85 at
-  // 9000, where the rate of mma.sync limits it).
-  p.chunk = rows > 64 || (rows > 32 && head_dim > 64 && span > 2048);
-  p.tile_rows = p.chunk ? 256 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
-  p.key_tile = p.chunk || head_dim <= 64 ? 128 : 64;
-  if (p.chunk) {
+  // keys that the tokens of `n` rows see at most
+  auto span_of = [&](int64_t n) {
+    const int64_t s = window + std::min(max_q, n / group + 2);
+    return window > 0 && s < max_kv ? s : max_kv;
+  };
+
+  // The kernel for few rows: 16, 32 or 64 of them a block, and the split of the
+  // keys with the least time, in ns: rounds of blocks, each the key tiles of
+  // one range (measured 0.5, 0.8 and 1.8 us a tile) and what starting and
+  // ending a block takes, and the join. One round where blocks are few, several
+  // short ones (which ragged lengths fill better) where they are many. A
+  // cluster joins the ranges of a row tile where all blocks run at once; over
+  // several rounds its blocks would hold their places until the longest ends
+  // (239 us instead of 207 for 64 ragged sequences of up to 8192 positions).
+  p.tile_rows = rows > 32 ? 64 : rows > 16 ? 32 : 16;
+  p.key_tile = head_dim <= 64 ? 128 : 64;
+  p.tiles_x = std::max<int64_t>(ceil_div(rows, p.tile_rows), 1);
+  const int64_t units = kv_heads * nseq * p.tiles_x, slots = 2 * kPlanSms;
+  const int64_t span = span_of(p.tile_rows);
+  // in tiles, one more where the window does not start on one
+  const int64_t tiles = std::max<int64_t>(ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0), 1);
+  const int64_t tile_ns = p.tile_rows == 64 ? 1800 : p.tile_rows == 32 ? 800 : 500;
+  auto clustered = [&](int64_t s) { return s <= kMaxCluster && units * s <= slots; };
+  int64_t split = 1, few_ns = INT64_MAX;
+  for (int64_t s = 1; s <= tiles && s <= kMaxSplits; ++s) {
+    const int64_t join = s == 1 ? 0 : clustered(s) ? 1000 : 3500;
+    const int64_t ns = ceil_div(units * s, slots) * (ceil_div(tiles, s) * tile_ns + 2000) + join + 2000;
+    if (ns < few_ns) {
+      few_ns = ns;
+      split = s;
+    }
+    if (units * s > (p.tile_rows == 64 ? 2 : 16) * slots) break;
+  }
+
+  // The kernel for many rows: its start, ends and join, and the key tiles of
+  // 256 rows (128 rows: alternate ones) dealt evenly to the SMs. With 16 rows
+  // the other is as fast as the memory in any case.
+  const int64_t many_tiles = kv_heads * nseq * ceil_div(rows, 256) * ceil_div(span_of(256), 128);
+  const int64_t many_ns = 16000 + many_tiles * (rows > 128 ? 1600 : 1300) / kPlanSms;
+  if (rows > 16 && many_ns < few_ns) {
+    p.chunk = true;
+    p.tile_rows = 256;
+    p.key_tile = 128;
     p.tiles_x = ntok * group / p.tile_rows + nseq;
     p.blocks = (int)kPlanSms;
     p.nsplit = p.cluster = 1;
     p.part_rows = 2 * kPlanSms * p.tile_rows;
     p.ws_bytes = ceil_div(p.part_rows * (head_dim + 1) * 4, 16) * 16 + kPlanSms * kCutBytes;
     return p;
-  }
-  p.tiles_x = 1;
-  const int64_t units = kv_heads * nseq, slots = 2 * kPlanSms;
-  // in tiles, one more where the window does not start on one
-  int64_t tiles = ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0);
-  if (tiles < 1) tiles = 1;
-  // The split with the least time in rounds of blocks, in keys (128 take about
-  // 1 us): those of one range, what starting and ending a block takes, and the
-  // join. One round where blocks are few, several short ones (which ragged
-  // lengths fill better) where they are many. Ranges have 64 keys or more. A
-  // cluster joins the ranges of a row tile where all blocks run at once; over
-  // several rounds its blocks would hold their places until the longest ends
-  // (239 us instead of 207 for 64 ragged sequences of up to 8192 positions).
-  int64_t split = 1, least = INT64_MAX;
-  auto clustered = [&](int64_t s) { return s <= kMaxCluster && units * s <= slots; };
-  for (int64_t s = 1; s <= tiles && s <= kMaxSplits; ++s) {
-    const int64_t join = s == 1 ? 0 : clustered(s) ? 128 : 448;
-    const int64_t cost = ceil_div(units * s, slots) * (ceil_div(tiles, s) * p.key_tile + 256) + join;
-    if (cost < least) {
-      least = cost;
-      split = s;
-    }
-    if (units * s > 16 * slots) break;
   }
   p.chunk_tiles = (int)ceil_div(tiles, split);
   p.nsplit = (int)ceil_div(tiles, p.chunk_tiles);

@@ -145,8 +145,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int row0 = tile * kRows;
   const int rows = min(kRows, qn * p.group - row0);
   if (rows <= 0) return;
+  // row r of the tile is query head off0 + r of token tok0, running on into the
+  // next tokens
+  const int tok0 = row0 / p.group, off0 = row0 - tok0 * p.group;
+  auto by_group = [&](int x) {
+    return p.group_inv ? (int)__umulhi((uint32_t)x, p.group_inv) : x / p.group;
+  };
   // positions of the tile's first and last row; keys [lo, hi) are seen by some row
-  const int pos_first = kv - qn + row0 / p.group, pos_last = kv - qn + (row0 + rows - 1) / p.group;
+  const int pos_first = kv - qn + tok0, pos_last = pos_first + by_group(off0 + rows - 1);
   const int hi = max(pos_last + 1, 0);
   const int lo = p.window > 0 ? max(0, pos_first - p.window + 1) : 0;
   const int t_lo = lo / kKeys, t_hi = (hi + kKeys - 1) / kKeys;
@@ -219,9 +225,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = min(rw * 16 + g + 8 * h, rows - 1);   // rows past the end repeat the last
-      const int i = (row0 + r) / p.group, hh = (row0 + r) % p.group;
-      pos[h] = kv - qn + i;
-      const T* q = static_cast<const T*>(p.q) + (int64_t)(q0 + i) * p.q_stride +
+      const int i = by_group(off0 + r), hh = off0 + r - i * p.group;
+      pos[h] = pos_first + i;
+      const T* q = static_cast<const T*>(p.q) + (int64_t)(q0 + tok0 + i) * p.q_stride +
                    (int64_t)(head * p.group + hh) * p.dim;
 #pragma unroll
       for (int s = 0; s < DP / 16; ++s)
@@ -384,38 +390,47 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
       named_barrier_sync(1, kWarps * 32);
-      for (int i = threadIdx.x; i < rows * DP; i += kWarps * 32) {
-        const int r = i / DP, d = i % DP;
+      // four values of a row a thread
+#pragma unroll 2
+      for (int i = threadIdx.x; i < rows * (DP / 4); i += kWarps * 32) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
         if (d >= p.dim) continue;
-        float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+        float top = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < KW; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
         const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           const float f = exp2_approx(ml[(w * kRows + r) * 2] - ref);
-          sum += f * ml[(w * kRows + r) * 2 + 1];
-          acc += f * mo[(w * kRows + r) * kLd + d];
+          const float4 x = *reinterpret_cast<const float4*>(mo + (w * kRows + r) * kLd + d);
+          sum = fmaf(f, ml[(w * kRows + r) * 2 + 1], sum);
+          acc.x = fmaf(f, x.x, acc.x);
+          acc.y = fmaf(f, x.y, acc.y);
+          acc.z = fmaf(f, x.z, acc.z);
+          acc.w = fmaf(f, x.w, acc.w);
         }
         if (p.cluster > 1) {
           // this block's result, for the others of the cluster
-          mine_o[r * DP + d] = acc;
+          *reinterpret_cast<float4*>(mine_o + r * DP + d) = acc;
           if (d == 0) {
             mine_l[2 * r] = top;
             mine_l[2 * r + 1] = sum;
           }
           continue;
         }
-        const float val = sum > 0.0f ? acc / sum : 0.0f;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
         const float lse = sum > 0.0f ? ref + log2f(sum) : -INFINITY;
-        const int64_t tok = q0 + (row0 + r) / p.group;
-        const int qh = head * p.group + (row0 + r) % p.group;
+        const int ti = by_group(off0 + r);
+        const int64_t tok = q0 + tok0 + ti;
+        const int qh = head * p.group + off0 + r - ti * p.group;
         if (p.nsplit > 1) {
           const int64_t at = ((int64_t)split * p.ntok + tok) * p.q_heads + qh;
-          p.part_o[at * p.dim + d] = val;
+          *reinterpret_cast<float4*>(p.part_o + at * p.dim + d) = make_float4(x[0], x[1], x[2], x[3]);
           if (d == 0) p.part_lse[at] = lse;
         } else {
-          store_out(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, val);
+          store_out4(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, x);
           if (d == 0 && p.lse) p.lse[tok * p.q_heads + qh] = lse * kLn2;
         }
       }
@@ -457,8 +472,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] *= inv;
-        const int64_t tok = q0 + (row0 + r) / p.group;
-        const int qh = head * p.group + (row0 + r) % p.group;
+        const int ti = by_group(off0 + r);
+        const int64_t tok = q0 + tok0 + ti;
+        const int qh = head * p.group + off0 + r - ti * p.group;
         store_out4(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, o);
         if (d == 0 && p.lse)
           p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
