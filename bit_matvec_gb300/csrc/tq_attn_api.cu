@@ -139,16 +139,18 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   p.tile_rows = rows > 32 ? 64 : rows > 16 ? 32 : 16;
   p.key_tile = head_dim <= 64 ? 128 : 64;
   p.tiles_x = std::max<int64_t>(ceil_div(rows, p.tile_rows), 1);
-  const int64_t units = kv_heads * nseq * p.tiles_x, slots = 2 * kPlanSms;
+  const int64_t slots = 2 * kPlanSms;
+  const double units = (double)(kv_heads * nseq) * p.tiles_x;   // the largest sizes pass 64 bits
   const int64_t span = span_of(p.tile_rows);
   // in tiles, one more where the window does not start on one
   const int64_t tiles = std::max<int64_t>(ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0), 1);
   const int64_t tile_ns = p.tile_rows == 64 ? 1800 : p.tile_rows == 32 ? 800 : 500;
   auto clustered = [&](int64_t s) { return s <= kMaxCluster && units * s <= slots; };
-  int64_t split = 1, few_ns = INT64_MAX;
+  int64_t split = 1;
+  double few_ns = INFINITY;
   for (int64_t s = 1; s <= tiles && s <= kMaxSplits; ++s) {
     const int64_t join = s == 1 ? 0 : clustered(s) ? 1000 : 3500;
-    const int64_t ns = ceil_div(units * s, slots) * (ceil_div(tiles, s) * tile_ns + 2000) + join + 2000;
+    const double ns = std::ceil(units * s / slots) * (ceil_div(tiles, s) * tile_ns + 2000) + join + 2000;
     if (ns < few_ns) {
       few_ns = ns;
       split = s;
@@ -159,8 +161,8 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   // The kernel for many rows: its start, ends and join, and the key tiles of
   // 256 rows (128 rows: alternate ones) dealt evenly to the SMs. With 16 rows
   // the other is as fast as the memory in any case.
-  const int64_t many_tiles = kv_heads * nseq * ceil_div(rows, 256) * ceil_div(span_of(256), 128);
-  const int64_t many_ns = 16000 + many_tiles * (rows > 128 ? 1600 : 1300) / kPlanSms;
+  const double many_tiles = (double)(kv_heads * nseq) * (ceil_div(rows, 256) * ceil_div(span_of(256), 128));
+  const double many_ns = 16000 + many_tiles * (rows > 128 ? 1600 : 1300) / kPlanSms;
   if (rows > 16 && many_ns < few_ns) {
     p.chunk = true;
     p.tile_rows = 256;
