@@ -158,11 +158,19 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
     if (units * s > (p.tile_rows == 64 ? 2 : 16) * slots) break;
   }
 
-  // The kernel for many rows: its start, ends and join, and the key tiles of
-  // 256 rows (128 rows: alternate ones) dealt evenly to the SMs. With 16 rows
-  // the other is as fast as the memory in any case.
-  const double many_tiles = (double)(kv_heads * nseq) * (ceil_div(rows, 256) * ceil_div(span_of(256), 128));
-  const double many_ns = 16000 + many_tiles * (rows > 128 ? 1600 : 1300) / kPlanSms;
+  // The kernel for many rows: its start, end and join (more than 128 rows: twice
+  // the partial results), the key tiles of 256 rows (128 rows: alternate ones)
+  // dealt evenly to the SMs, and row tiles beyond one an SM. With 16 rows the
+  // other is as fast as the memory in any case. Both measured, heads of 128,
+  // few-row kernel first: 64 rows of one sequence over 9001 positions 19 and 23
+  // us, 128 rows 25 and 25, 256 rows 39 and 32; 128 rows of 16 ragged sequences
+  // 220 and 89; 274 tokens of 8 heads on one over 521 positions 12 and 24; 8
+  // ragged sequences of 16 heads on 4 and up to 1000 positions, 64 new tokens
+  // 23 and 29, 200 new tokens 68 and 39.
+  const double row_tiles = (double)(kv_heads * nseq) * ceil_div(rows, 256);
+  const double many_ns = 16000 + (rows > 128 ? 9000 : 0) +
+                         row_tiles * ceil_div(span_of(256), 128) * (rows > 128 ? 1600 : 1300) / kPlanSms +
+                         std::max(row_tiles / kPlanSms - 1, 0.0) * 5000;
   if (rows > 16 && many_ns < few_ns) {
     p.chunk = true;
     p.tile_rows = 256;
