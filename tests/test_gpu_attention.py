@@ -352,3 +352,117 @@ def test_no_work(tq):
     O, L = call(tq, prob, F16, max_q=1)
     assert O.numel() == 0
     assert math.isfinite(float(tq.tq_device_status()))
+
+
+def many_rows(tq, prob, max_kv, window=0):
+    """Whether the plan takes the kernel for many rows: its workspace has a fixed size, the partial
+    results of two row tiles of 256 rows for each of 152 blocks and a few words a block."""
+    Q, k, _, _, q_start, kv_len, _, _ = prob
+    mq = int((q_start[1:] - q_start[:-1]).max())
+    need = tq.tq_paged_attention_workspace_bytes(len(kv_len), Q.shape[0], Q.shape[1], k.shape[1], Q.shape[2],
+                                                 mq, max_kv, window)
+    part = 2 * 152 * 256 * (Q.shape[2] + 1) * 4
+    return part <= need <= part + 152 * 64
+
+
+BOTH = [([(300, 300)], 5, 1, 128, 16, BF16, BF16, "hnd"),
+        ([(513, 200), (100, 100), (1, 1)], 4, 2, 128, 32, F16, F16, "nhd"),
+        ([(900, 260), (2100, 1), (64, 64)], 12, 4, 96, 48, BF16, F32, "hnd"),
+        ([(4100, 40)], 8, 2, 128, 128, BF16, BF16, "hnd"),
+        ([(400, 300), (0, 0), (31, 5), (300, 3)], 15, 3, 80, 8, F16, F16, "both"),
+        ([(257, 256)], 1, 1, 64, 32, F16, F32, "hnd"), ([(3000, 129)], 1, 1, 128, 32, F16, F32, "hnd"),
+        ([(2600, 1), (1300, 300)], 7, 1, 64, 16, BF16, BF16, "nhd"),
+        ([(128, 128)] * 40, 8, 8, 64, 64, F16, F16, "hnd"), ([(6000, 70)], 2, 1, 64, 24, F16, F32, "hnd"),
+        ([(130, 3)] * 3, 64, 1, 128, 16, F16, F16, "hnd"), ([(130, 130), (70, 7)], 24, 3, 40, 40, F16, F16, "hnd"),
+        ([(70, 40)] * 60, 8, 2, 8, 8, BF16, BF16, "hnd")]
+
+
+@pytest.mark.parametrize("case", BOTH, ids=str)
+def test_both_kernels(tq, case):
+    """max_kv only plans: a small one takes the kernel for few rows, a large one that for many, and
+    both are right. A large max_kv also makes splits that no key falls into."""
+    lens, hq, hk, dim, page, dtype, out, order = case
+    prob = problem(lens, hq, hk, dim, page, dtype, order=order)
+    assert not many_rows(tq, prob, 1) and many_rows(tq, prob, 10**8)
+    a = check(tq, prob, out, max_kv=1)
+    b = check(tq, prob, out, max_kv=10**8)
+    assert a.shape == b.shape
+
+
+@pytest.mark.parametrize("lens,hq,hk,dim,page,window", [([(1500, 1000)] * 8, 8, 8, 64, 64, 700),
+                                                        ([(2500, 1000), (40, 40)] * 3, 16, 2, 128, 16, 600),
+                                                        ([(900, 700)] * 12, 12, 4, 80, 48, 65)])
+def test_windows_of_many_rows(tq, lens, hq, hk, dim, page, window):
+    prob = problem(lens, hq, hk, dim, page, BF16, window=window)
+    assert many_rows(tq, prob, max(n for n, _ in lens), window)
+    check(tq, prob, BF16, window)
+
+
+@pytest.mark.parametrize("lens,hq,hk", [([(900, 200)], 4, 1), ([(70, 40)] * 200, 8, 2)])
+@pytest.mark.parametrize("max_kv", [1, 10**8])
+def test_timeout_in_both_kernels(tq, lens, hq, hk, max_kv):
+    for dim in (64, 128):
+        prob = problem(lens, hq, hk, dim, 16, F16)
+        want, _ = call(tq, prob, F16, max_kv=max_kv)
+        torch.cuda.synchronize()
+        tq.tq_debug_stall_next_launch(200_000)
+        try:
+            call(tq, prob, F16, max_kv=max_kv)
+            torch.cuda.synchronize()
+        finally:
+            tq.tq_debug_stall_next_launch(0)
+        assert tq.tq_device_status() == tq.TQ_ERR_TIMEOUT
+        again, _ = call(tq, prob, F16, max_kv=max_kv)
+        assert torch.equal(want, again) and tq.tq_device_status() == tq.TQ_OK
+
+
+@pytest.mark.parametrize("starts", [[0, 90, 40, 130], [30, 60, 100, 130], [-7, 60, 100, 1 << 30]])
+@pytest.mark.parametrize("max_kv", [1, 10**8])
+def test_starts_out_of_order_in_both_kernels(tq, starts, max_kv):
+    prob = list(problem([(200, n) for n in (50, 40, 40)], 8, 2, 64, 16, F16))
+    want, _ = call(tq, tuple(prob), F16, max_kv=max_kv)
+    good, ntok = prob[4], prob[0].shape[0]
+    prob[4] = torch.tensor([min(s, 2 * ntok) for s in starts], dtype=torch.int32)
+    call(tq, tuple(prob), F16, max_q=50, max_kv=max_kv)
+    tq.tq_device_status()
+    prob[4] = good
+    again, _ = call(tq, tuple(prob), F16, max_kv=max_kv)
+    assert torch.equal(want, again)
+
+
+@pytest.mark.parametrize("max_kv", [1, 10**8])
+def test_bad_pages_in_both_kernels(tq, max_kv):
+    prob = list(problem([(300, 200)], 4, 2, 64, 16, F16))
+    for entry in (-1, prob[1].shape[0], 2**31 - 1):
+        bad = prob[3].clone()
+        bad[0, 5] = entry
+        call(tq, tuple(prob[:3] + [bad] + prob[4:]), F16, max_kv=max_kv)
+        assert tq.tq_device_status() == tq.TQ_ERR_INDEX, entry
+    long = prob[:5] + [torch.tensor([100000]).int()] + prob[6:]
+    call(tq, tuple(long), F16, max_kv=max_kv)
+    assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+    call(tq, tuple(prob), F16, max_q=1, max_kv=max_kv)
+    assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+    check(tq, tuple(prob), F16, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("max_kv", [1, 10**8])
+def test_large_scores_and_negative_scales_in_both_kernels(tq, max_kv):
+    prob = problem([(1300, 300)], 4, 1, 128, 16, BF16, poison=False)
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    up = torch.linspace(0.2, 4.0, 1300).to(BF16)
+    for j in range(1300):
+        k[table[0, j // 16], 0, j % 16] = up[j] * (1 if j % 7 else -1)
+    Q = (torch.ones_like(Q) * (torch.arange(4)[None, :, None] - 1.5)).to(BF16)
+    check(tq, (Q, k, v, table, q_start, kv_len, k.cuda(), v.cuda()), F32, max_kv=max_kv)
+    for scale in (0.0, -0.7, 3.0):
+        check(tq, problem([(400, 200)], 4, 2, 64, 16, F16, peak=1.0), F32, scale=scale, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("max_kv", [1, 10**8])
+def test_tokens_that_see_nothing_in_both_kernels(tq, max_kv):
+    prob = problem([(150, 150), (40, 40)], 4, 2, 64, 16, F16)
+    g = torch.Generator().manual_seed(1)
+    Q = torch.randn(302, 4, 64, generator=g).to(F16)
+    q_start, kv_len = torch.tensor([0, 300, 302]).int(), torch.tensor([150, 40]).int()
+    check(tq, (Q,) + prob[1:4] + (q_start, kv_len) + prob[6:], F32, max_kv=max_kv)
