@@ -131,31 +131,45 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   // The kernel for few rows: 16, 32 or 64 of them a block, and the split of the
   // keys with the least time, in ns: rounds of blocks, each the key tiles of
   // one range (measured 0.5, 0.8 and 1.8 us a tile) and what starting and
-  // ending a block takes, and the join. One round where blocks are few, several
+  // ending a block takes (2 us, 5 with 64 rows), blocks of sequences too short
+  // for their row tile, and the join. One round where blocks are few, several
   // short ones (which ragged lengths fill better) where they are many. A
   // cluster joins the ranges of a row tile where all blocks run at once; over
   // several rounds its blocks would hold their places until the longest ends
-  // (239 us instead of 207 for 64 ragged sequences of up to 8192 positions).
+  // (239 us instead of 207 for 64 ragged sequences of up to 8192 positions),
+  // and larger clusters do not fill every last place (40 clusters of 7 took two
+  // rounds: 27 us, where 40 of 6 take 18).
   p.tile_rows = rows > 32 ? 64 : rows > 16 ? 32 : 16;
   p.key_tile = head_dim <= 64 ? 128 : 64;
   p.tiles_x = std::max<int64_t>(ceil_div(rows, p.tile_rows), 1);
   const int64_t slots = 2 * kPlanSms;
-  const double units = (double)(kv_heads * nseq) * p.tiles_x;   // the largest sizes pass 64 bits
+  const double blocks = (double)(kv_heads * nseq) * p.tiles_x;   // the largest sizes pass 64 bits
+  // row tiles of `n` rows that there can be; the rest of the blocks end at once
+  auto row_tiles_of = [&](int64_t n) {
+    return kv_heads * std::min((double)nseq * ceil_div(rows, n), (double)(ntok * group / n) + nseq);
+  };
+  const bool wide = p.tile_rows == 64;
+  const double units = row_tiles_of(p.tile_rows);
   const int64_t span = span_of(p.tile_rows);
   // in tiles, one more where the window does not start on one
   const int64_t tiles = std::max<int64_t>(ceil_div(span, p.key_tile) + (span < max_kv ? 1 : 0), 1);
-  const int64_t tile_ns = p.tile_rows == 64 ? 1800 : p.tile_rows == 32 ? 800 : 500;
-  auto clustered = [&](int64_t s) { return s <= kMaxCluster && units * s <= slots; };
+  const int64_t tile_ns = wide ? 1800 : p.tile_rows == 32 ? 800 : 500;
+  auto clustered = [&](int64_t s) {
+    return s <= kMaxCluster && blocks * s <= (s <= 2 ? slots : slots * 17 / 20);
+  };
   int64_t split = 1;
   double few_ns = INFINITY;
   for (int64_t s = 1; s <= tiles && s <= kMaxSplits; ++s) {
     const int64_t join = s == 1 ? 0 : clustered(s) ? 1000 : 3500;
-    const double ns = std::ceil(units * s / slots) * (ceil_div(tiles, s) * tile_ns + 2000) + join + 2000;
+    const double full = units * s / slots, up = std::ceil(full);
+    const double rounds = wide && full > 1 ? (full + up) / 2 : up;
+    const double ns = rounds * (ceil_div(tiles, s) * tile_ns + (wide ? 5000 : 2000)) + join + 2000 +
+                      (blocks - units) * s / slots * 1500;
     if (ns < few_ns) {
       few_ns = ns;
       split = s;
     }
-    if (units * s > (p.tile_rows == 64 ? 2 : 16) * slots) break;
+    if (blocks * s > (wide ? 2 : 16) * slots) break;
   }
 
   // The kernel for many rows: its start, end and join (more than 128 rows: twice
@@ -164,13 +178,14 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   // other is as fast as the memory in any case. Both measured, heads of 128,
   // few-row kernel first: 64 rows of one sequence over 9001 positions 19 and 23
   // us, 128 rows 25 and 25, 256 rows 39 and 32; 128 rows of 16 ragged sequences
-  // 220 and 89; 274 tokens of 8 heads on one over 521 positions 12 and 24; 8
+  // 163 and 89; 274 tokens of 8 heads on one over 521 positions 12 and 24; 8
   // ragged sequences of 16 heads on 4 and up to 1000 positions, 64 new tokens
-  // 23 and 29, 200 new tokens 68 and 39.
-  const double row_tiles = (double)(kv_heads * nseq) * ceil_div(rows, 256);
-  const double many_ns = 16000 + (rows > 128 ? 9000 : 0) +
+  // 23 and 30, 200 new tokens 42 and 39; 200 single tokens and 2 x 16 over up to
+  // 500 positions 49 and 82.
+  const double row_tiles = row_tiles_of(256);
+  const double many_ns = 18500 + (rows > 128 ? 7500 : 0) +
                          row_tiles * ceil_div(span_of(256), 128) * (rows > 128 ? 1600 : 1300) / kPlanSms +
-                         std::max(row_tiles / kPlanSms - 1, 0.0) * 5000;
+                         std::max(row_tiles / kPlanSms - 1, 0.0) * 8000;
   if (rows > 16 && many_ns < few_ns) {
     p.chunk = true;
     p.tile_rows = 256;
