@@ -543,7 +543,9 @@ int tq_paged_attention(const void *Q, int64_t q_stride, const tq_paged_kv *kv,
                        int64_t workspace_bytes, void *stream);
 
 /* Scratch of tq_paged_attention: partial results where the keys are split over
- * thread blocks. A function of the sizes alone; -1 for sizes it refuses. */
+ * thread blocks. A function of the sizes alone, but not a growing one (fewer
+ * tokens may be split into more ranges): a buffer for calls of several sizes
+ * takes the largest of theirs. -1 for sizes it refuses. */
 int64_t tq_paged_attention_workspace_bytes(int64_t nseq, int64_t ntok, int64_t q_heads,
                                            int64_t kv_heads, int64_t head_dim, int64_t max_q,
                                            int64_t max_kv, int64_t window);
