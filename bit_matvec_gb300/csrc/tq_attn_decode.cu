@@ -222,6 +222,12 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // this thread's rows g and g + 8: query fragments and positions
     uint32_t qf[DP / 16][4];
     int pos[2];
+    // a negative scale turns the queries and one of zero takes zeros for them,
+    // so that the maximum of S is that of the scores and masked ones stay minus
+    // infinity
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+    const int dim = p.scale_log2 == 0.0f ? 0 : p.dim;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = min(rw * 16 + g + 8 * h, rows - 1);   // rows past the end repeat the last
@@ -234,7 +240,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int d = s * 16 + e * 8 + 2 * tq;
-          qf[s][h + 2 * e] = d < p.dim ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+          qf[s][h + 2 * e] = d < dim ? *reinterpret_cast<const uint32_t*>(q + d) ^ flip : 0u;
         }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -284,7 +290,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             mma16816<T>(s[2 * n], qf[d], b[0], b[1]);
             mma16816<T>(s[2 * n + 1], qf[d], b[2], b[3]);
           }
-        // in base-2 logarithms; masked ones to minus infinity
+        // masked ones to minus infinity; maxima, of base-2 logarithms
         float mx[2] = {-INFINITY, -INFINITY};
         const bool masked = key0 + 16 * NK - 1 > pos_first ||
                             (p.window > 0 && key0 <= pos_last - p.window);
@@ -295,17 +301,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int e = 0; e < 4; ++e) {
               const int h = e >> 1, key = key0 + n * 8 + 2 * tq + (e & 1);
               s[n][e] = key > pos[h] || (p.window > 0 && key <= pos[h] - p.window)
-                            ? -INFINITY : s[n][e] * p.scale_log2;
+                            ? -INFINITY : s[n][e];
               mx[h] = fmaxf(mx[h], s[n][e]);
             }
         } else {
 #pragma unroll
           for (int n = 0; n < 2 * NK; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[n][e] *= p.scale_log2;
-              mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-            }
+            for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
         }
         float corr[2], ref[2];
         bool grow = false;
@@ -313,7 +316,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         for (int h = 0; h < 2; ++h) {
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-          const float mn = fmaxf(m[h], mx[h]);
+          const float mn = fmaxf(m[h], mx[h] * scale);
           ref[h] = mn == -INFINITY ? 0.0f : mn;
           corr[h] = exp2_approx(m[h] - ref[h]);
           grow |= mn > m[h];
@@ -338,7 +341,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              w[e] = exp2_approx(s[2 * n + q][e] - ref[e >> 1]);
+              w[e] = exp2_approx(fmaf(s[2 * n + q][e], scale, -ref[e >> 1]));
               l[e >> 1] += w[e];
             }
             a[2 * q] = pack2<T>(w[0], w[1]);
