@@ -20,49 +20,26 @@
 // 16 TB/s). With up to 128 rows both take the same rows, on alternate key
 // tiles, and are merged at the end.
 //
-// The work, every key tile of every row tile of every head, is laid in one
-// line (head, sequence, row tile, key tile) and cut into equal pieces, one for
-// each block: lengths, causality and the number of SMs then leave no SM idle,
-// and a row tile is cut at most where a piece ends. With four blocks or more to
-// a row tile, where starting and ending a second one would weigh, each row
-// tile gets blocks of its own instead, as many as its share of the work. Blocks
-// find their piece from q_start and kv_len on the device. Cut row tiles leave
-// partial results, which a second kernel joins.
+// Blocks find their piece of the work from q_start and kv_len on the device
+// (tq_attn_work.cuh). Cut row tiles leave partial results, which a second
+// kernel joins.
 #include <type_traits>
 
 #include "tq_attn_dev.cuh"
+#include "tq_attn_work.cuh"
 #include "tq_tcgen05.cuh"
 
 namespace tq {
 namespace {
 
 using namespace tc;
+using namespace work;
 
-constexpr int kHalf = 128;            // rows of a softmax
-constexpr int kRows = 2 * kHalf;      // rows of a tile
-constexpr int kKeys = 128;            // keys of a tile
 constexpr int kSoft = 256;            // softmax threads, one a row
 constexpr int kThreads = kSoft + 128; // and an MMA, a TMA and a scheduling warp (and one that idles)
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
 constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
-// The cost of work, in units of about 0.4 us: a key tile of two halves, one of
-// up to 128 rows, starting and ending a row tile (1.6, 1.2 and 8 us measured at
-// dim 128), and the least work worth a block of its own.
-constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 18, kLeastWork = 12;
 constexpr int kCachedSeqs = 48;       // lengths of so many sequences are kept in shared memory
-
-// A block's share of one row tile.
-struct Segment {
-  int n;              // key tiles; -1: no more segments
-  int t0;             // first key tile
-  int tok;            // token of the tile's first row
-  int off;            // query head of that row within the group
-  int rows;
-  int pos;            // position of that token
-  int lo, hi;         // keys [lo, hi) are seen by some row
-  int head, seq;
-  int part;           // where the partial result goes, -1: whole, to the output
-};
 
 template <int DP> struct Smem {
   static constexpr int kSlots = DP == 128 ? 5 : 8;
@@ -247,65 +224,6 @@ __device__ __forceinline__ void weights64(const float (&s)[64], uint64_t scale2,
   tmem_st32(taddr, w);
 }
 
-// The row tiles of sequence b are numbered from f(b) = floor(q_start[b] * group
-// / kRows) + b, which leaves each sequence room for all of its own (and some
-// numbers empty).
-struct Tiles {
-  const AttnParams& p;
-  const int32_t* q_start;   // of the call, or their copies in shared memory
-  const int32_t* kv_len;
-  __device__ __forceinline__ int start(int b) const {
-    return min(max(q_start[b], 0), (int)p.ntok);
-  }
-  __device__ __forceinline__ int first(int b) const { return start(b) * p.group / kRows + b; }
-  // the sequence that tile number s belongs to
-  __device__ __forceinline__ int find(int s) const {
-    int lo = 0, hi = p.nseq;   // f(lo) <= s < f(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first(mid) <= s) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  }
-};
-
-// a / b for non-negative values: the 64-bit division, some hundred dependent
-// instructions, only where it is needed.
-__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : quotient64(a, b);
-}
-
-// Row tile `s` of sequence `b`, whole; n = -1 if the number is an empty one.
-__device__ __forceinline__ Segment row_tile(const Tiles& tiles, int s, int b) {
-  const AttnParams& p = tiles.p;
-  Segment g = {};
-  g.n = -1;
-  const int q0 = tiles.start(b), qn = max(tiles.start(b + 1) - q0, 0);
-  const int row0 = (s - tiles.first(b)) * kRows;
-  if (row0 < 0 || row0 >= qn * p.group) return g;   // (below 0: q_start not in order)
-  const int kv = min(max(tiles.kv_len[b], 0), p.max_positions);
-  const int t = row0 / p.group;
-  g.seq = b;
-  g.off = row0 - t * p.group;
-  g.rows = min(kRows, qn * p.group - row0);
-  g.tok = q0 + t;
-  g.pos = kv - qn + t;
-  g.hi = max(g.pos + (g.off + g.rows - 1) / p.group + 1, 0);
-  g.lo = p.window > 0 ? max(0, g.pos - p.window + 1) : 0;
-  g.t0 = g.lo / kKeys;
-  g.n = max((g.hi + kKeys - 1) / kKeys - g.t0, 0);
-  return g;
-}
-__device__ __forceinline__ int unit_cost(const Segment& g) {
-  return g.rows > kHalf ? kCostTwo : kCostAlt;
-}
-// (a tile without keys still has its rows to write)
-__device__ __forceinline__ int tile_cost(const Segment& g, int tile) {
-  return g.n < 0 ? 0 : tile + max(g.n * unit_cost(g), 1);
-}
-
 __device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
@@ -313,23 +231,6 @@ __device__ __forceinline__ int64_t scan_warp(int64_t x, int lane) {
   }
   return x;
 }
-
-// Where a block's work starts: a row tile's number and sequence, its head, and
-// the cost before it.
-struct Start {
-  int number, seq, head, own;
-  int64_t x0, x1;     // the block's piece of the line (own: x0 row tiles before)
-  int64_t at;
-  int64_t all, blocks, spare;
-};
-
-// A row tile that was cut: its rows, and where its partial results are.
-struct CutTile {
-  int n;              // pieces; 0: none here
-  int part0;          // the first, then 2 (block + 1), 2 (block + 2), ...
-  int tok, off, rows, head;
-  int pad[2];
-};
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -395,17 +296,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     if ((int)threadIdx.x < p.nseq) seqs[kCachedSeqs + 1 + threadIdx.x] = p.kv_len[threadIdx.x];
     __syncthreads();
   }
-  const Tiles tiles{p, cached ? seqs : p.q_start, cached ? seqs + kCachedSeqs + 1 : p.kv_len};
+  const Tiles<AttnParams> tiles{p, cached ? seqs : p.q_start, cached ? seqs + kCachedSeqs + 1 : p.kv_len};
   const int per = (numbers + kThreads - 1) / kThreads;
   const int i0 = min((int)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
-  constexpr int kCount = 44;   // the number of row tiles is added up above the cost
-  int64_t mine = 0;
   const int b0 = i0 < i1 ? tiles.find(i0) : 0;
-  for (int s = i0, b = b0; s < i1; ++s) {
-    while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
-    const int cost = tile_cost(row_tile(tiles, s, b), 0);
-    mine += cost > 0 ? cost + (int64_t(1) << kCount) : 0;
-  }
+  const int64_t mine = sum_tiles(tiles, i0, i1, b0);
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
   before -= mine;
@@ -417,48 +312,11 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     if (w == warp) before += total;
     total += scan[w];
   }
-  const int heads = p.q_heads / p.group;
-  const bool own = (total >> kCount) * heads * 4 <= gridDim.x;
-  const int tile_fee = own ? 0 : kTileCost;
-  auto cost_of = [&](int64_t sum) {
-    return (sum & ((int64_t(1) << kCount) - 1)) + (sum >> kCount) * tile_fee;
-  };
-  const int64_t tiles_before = before >> kCount, tiles_mine = mine >> kCount;
-  const int64_t head_tiles = total >> kCount;
-  total = cost_of(total);
-  before = cost_of(before);
-  mine = cost_of(mine);
   const uint32_t tmem = flags[0];
-  const int64_t all = total * heads;
-  // as many blocks as there is work for
-  const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, quotient(all, kLeastWork)));
-  // own: every row tile has blocks of its own, those of the tile number i that
-  // has the cost `sum` before it from first_block(i, sum) on
-  const int64_t spare = max(blocks - head_tiles * heads, (int64_t)0);
-  auto first_block = [&](int64_t i, int64_t sum) { return i + quotient(sum * spare, max(all, (int64_t)1)); };
   // What the scheduling warp needs goes through shared memory: held in
   // registers across the roles it was spilled, and its first segment late.
-  const int64_t block = blockIdx.x;
-  int64_t x0 = all, x1 = all;   // !own: the block's piece of the line
-  int head0 = 0;                // the head its first row tile belongs to
-  bool first_here;
-  if (own) {
-    while (head0 + 1 < heads && first_block((head0 + 1) * head_tiles, (head0 + 1) * total) <= block) ++head0;
-    const int64_t i = head0 * head_tiles + tiles_before, sum = head0 * total + before;
-    first_here = mine > 0 && first_block(i, sum) <= block && block < first_block(i + tiles_mine, sum + mine);
-    x0 = i;
-    x1 = sum;
-  } else {
-    if (block < blocks) {
-      x0 = quotient(all * block, blocks);
-      x1 = quotient(all * (block + 1), blocks);
-      head0 = (int)quotient(x0, total);
-    }
-    const int64_t y0 = x0 - head0 * total;
-    first_here = block < blocks && mine > 0 && before <= y0 && y0 < before + mine;
-  }
-  if (first_here)
-    *start = {i0, b0, head0, own, x0, x1, own ? x1 : head0 * total + before, all, blocks, spare};
+  Start here;
+  if (find_start(before, mine, total, i0, b0, p.q_heads / p.group, blockIdx.x, gridDim.x, &here)) *start = here;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.nseq; b += kThreads)
       if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
@@ -705,7 +563,6 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     if (warp == 11) {
       // ------------------------------------------------ scheduling
       if (lane == 0) {
-        CutTile cut = {};
         int queued = 0;
         auto push = [&](const Segment& g) {
           const int i = queued % kQueue;
@@ -715,68 +572,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
-        const Start st = *start;
-        int s = st.number, b = st.seq;   // number of the row tile, its sequence
-        if (s >= 0 && st.own) {
-          int64_t i = st.x0, sum = st.at;
-          for (; s < numbers; ++s) {
-            while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
-            Segment g = row_tile(tiles, s, b);
-            const int cost = tile_cost(g, 0);
-            if (cost == 0) continue;
-            const int64_t from = i + quotient(sum * st.spare, st.all);
-            const int64_t to = i + 1 + quotient((sum + cost) * st.spare, st.all);
-            ++i;
-            sum += cost;
-            if ((int64_t)blockIdx.x >= to) continue;
-            // piece j of `pieces` (none without a key tile, but for the only one)
-            const int j = (int)(blockIdx.x - from), n = g.n;
-            const int pieces = max(min((int)(to - from), n), 1);
-            if (j < pieces) {
-              const int t0 = (int)quotient((int64_t)n * j, pieces), t1 = (int)quotient((int64_t)n * (j + 1), pieces);
-              g.head = st.head;
-              g.part = pieces == 1 ? -1 : 2 * (int)blockIdx.x;
-              if (pieces > 1 && j == 0) cut = {pieces, g.part, g.tok, g.off, g.rows, g.head};
-              g.t0 += t0;
-              g.n = t1 - t0;
-              push(g);
-            }
-            break;
-          }
-        } else if (s >= 0) {
-          int head = st.head;
-          int64_t at = st.at;   // start of the row tile
-          while (at < st.x1 && !*failed) {
-            while (b + 1 < p.nseq && tiles.first(b + 1) <= s) ++b;
-            Segment g = row_tile(tiles, s, b);
-            const int cost = tile_cost(g, kTileCost);
-            if (cost > 0 && at + cost > st.x0) {
-              // key tiles [from, to) of the row tile fall into the piece
-              const int w = unit_cost(g), n = g.n;
-              const int u0 = (int)max(st.x0 - at, (int64_t)0), u1 = (int)min(st.x1 - at, (int64_t)cost);
-              const int from = u0 < kTileCost ? 0 : min((u0 - kTileCost) / w, n);
-              const int to = u1 < kTileCost ? 0 : min((u1 - kTileCost) / w, n);
-              if (n == 0 ? u0 == 0 : from < to) {
-                g.head = head;
-                g.part = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (queued > 0);
-                if (g.part >= 0 && from == 0) {
-                  // up to the piece with the row tile's end
-                  const int64_t last = quotient((at + cost) * st.blocks + st.all - 1, st.all) - 1;
-                  cut = {(int)(last - blockIdx.x) + 1, g.part, g.tok, g.off, g.rows, g.head};
-                }
-                g.t0 += from;
-                g.n = to - from;
-                push(g);
-              }
-            }
-            at += cost;
-            if (++s == numbers) {
-              s = 0;
-              b = 0;
-              ++head;
-            }
-          }
-        }
+        const CutTile cut = walk(tiles, numbers, *start, (int)blockIdx.x, push, [&]() { return *failed != 0; });
         Segment end = {};
         end.n = -1;
         push(end);
