@@ -304,8 +304,14 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
   before -= mine;
+  bool disorder = false, index = false;
+  for (int b = threadIdx.x; b < p.nseq; b += kThreads) {
+    disorder |= !tiles.in_order(b);
+    index |= tiles.start(b + 1) - tiles.start(b) > p.max_q || tiles.kv_len[b] > p.max_positions;
+  }
+  if (blockIdx.x == 0 && (disorder || index)) *p.status = kDevIndex;
   tc_fence_before();
-  __syncthreads();
+  disorder = __syncthreads_or(disorder);
   tc_fence_after();
   int64_t total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -316,12 +322,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   // What the scheduling warp needs goes through shared memory: held in
   // registers across the roles it was spilled, and its first segment late.
   Start here;
-  if (find_start(before, mine, total, i0, b0, p.q_heads / p.group, blockIdx.x, gridDim.x, &here)) *start = here;
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < p.nseq; b += kThreads)
-      if (tiles.start(b + 1) - tiles.start(b) > p.max_q ||
-          tiles.kv_len[b] > p.max_positions)
-        *p.status = kDevIndex;
+  const int heads = p.q_heads / p.group;
+  if (!disorder && find_start(before, mine, total, i0, b0, heads, blockIdx.x, gridDim.x, &here)) *start = here;
   __syncthreads();
 
   // Every wait has a limit. One that gave up sets `failed`, which ends the
@@ -572,7 +574,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
-        const CutTile cut = walk(tiles, numbers, *start, (int)blockIdx.x, push, [&]() { return *failed != 0; });
+        const CutTile cut = walk(tiles, numbers, *start, p.q_heads / p.group, (int)gridDim.x, (int)blockIdx.x,
+                                 push, [&]() { return *failed != 0; });
         Segment end = {};
         end.n = -1;
         push(end);

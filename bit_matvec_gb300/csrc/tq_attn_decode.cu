@@ -140,7 +140,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int qn = min(max(p.q_start[seq + 1], q0), ntok) - q0;
   const int kv = min(max(p.kv_len[seq], 0), p.max_positions);
   if (threadIdx.x == 0 && tile == 0 && split == 0 && head == 0 &&
-      (qn > p.max_q || p.kv_len[seq] > p.max_positions))
+      (qn > p.max_q || p.kv_len[seq] > p.max_positions || p.q_start[seq] < 0 ||
+       p.q_start[seq] > p.q_start[seq + 1] || p.q_start[seq + 1] > ntok))
     *p.status = kDevIndex;
   const int row0 = tile * kRows;
   const int rows = min(kRows, qn * p.group - row0);

@@ -64,6 +64,12 @@ template <typename P> struct Tiles {
   const int32_t* q_start;   // of the call, or their copies in shared memory
   const int32_t* kv_len;
   TQ_HD int start(int b) const { return least(most(q_start[b], 0), (int)p.ntok); }
+  // Whether sequence b's tokens lie within the call's, in order. A batch where
+  // one's do not gets no work: the sums below search for a row tile's sequence
+  // where the walk steps through them, which agree in order only.
+  TQ_HD bool in_order(int b) const {
+    return q_start[b] >= 0 && q_start[b] <= q_start[b + 1] && q_start[b + 1] <= p.ntok;
+  }
   TQ_HD int first(int b) const { return start(b) * p.group / kRows + b; }
   // the sequence that tile number s belongs to
   TQ_HD int find(int s) const {
@@ -179,8 +185,10 @@ struct CutTile {
 
 // The block's work from `st` on: push(segment) for each of its row tiles, in
 // order, until stop(); the row tile that was cut and whose first piece is here.
+// Whatever q_start holds, heads and pieces stay within `heads` and `grid`.
 template <typename P, typename Push, typename Stop>
-TQ_HD CutTile walk(const Tiles<P>& tiles, int numbers, const Start& st, int block, Push push, Stop stop) {
+TQ_HD CutTile walk(const Tiles<P>& tiles, int numbers, const Start& st, int heads, int grid, int block,
+                   Push push, Stop stop) {
   CutTile cut = {};
   int pushed = 0;
   int s = st.number, b = st.seq;   // number of the row tile, its sequence
@@ -215,7 +223,7 @@ TQ_HD CutTile walk(const Tiles<P>& tiles, int numbers, const Start& st, int bloc
   }
   int head = st.head;
   int64_t at = st.at;   // start of the row tile
-  while (at < st.x1 && !stop()) {
+  while (at < st.x1 && head < heads && !stop()) {
     while (b + 1 < tiles.p.nseq && tiles.first(b + 1) <= s) ++b;
     Segment g = row_tile(tiles, s, b);
     const int cost = tile_cost(g, kTileCost);
@@ -231,7 +239,7 @@ TQ_HD CutTile walk(const Tiles<P>& tiles, int numbers, const Start& st, int bloc
         if (g.part >= 0 && from == 0) {
           // up to the piece with the row tile's end
           const int64_t last = quotient((at + cost) * st.blocks + st.all - 1, st.all) - 1;
-          cut = {(int)(last - block) + 1, g.part, g.tok, g.off, g.rows, g.head, {}};
+          cut = {least((int)(last - block) + 1, grid - block), g.part, g.tok, g.off, g.rows, g.head, {}};
         }
         g.t0 += from;
         g.n = to - from;

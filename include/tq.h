@@ -521,8 +521,9 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  *       sequence, which choose kernels and splits. A sequence of more than
  *       max_q new tokens, a kv_len beyond the table (or 2^30) or a visible
  *       position whose page is outside the cache gives TQ_ERR_INDEX in
- *       tq_device_status(), and the sequence's rows are undefined; a kv_len
- *       beyond max_kv only costs speed.
+ *       tq_device_status(), and the sequence's rows are undefined; a q_start
+ *       that decreases or leaves 0 .. ntok gives it too, and all rows are
+ *       undefined. A kv_len beyond max_kv only costs speed.
  *   workspace  tq_paged_attention_workspace_bytes(...) bytes, 16-byte aligned;
  *       contents overwritten and meaningless after the call; calls that share
  *       it must be ordered.

@@ -60,7 +60,7 @@ extern "C" int attn_work_check(const int32_t* q_start, const int32_t* kv_len, in
     if (starts > 1) return fails(why, "several starts of block", block, starts);
     int steps = 0;
     const size_t first = pieces.size();
-    cuts[block] = walk(tiles, numbers, st, block,
+    cuts[block] = walk(tiles, numbers, st, heads, grid, block,
                        [&](const Segment& g) { pieces.push_back({g, block}); },
                        [&]() { return ++steps > 100000000; });
     if (steps > 100000000) return fails(why, "no end of the walk of block", block);

@@ -59,3 +59,15 @@ def test_every_key_tile_once(check, seed):
         args = (q_start, kv, int(q_start[-1]) + r.choice((0, 0, 5)), group, heads, r.choice((0, 0, 1, 100, 700)),
                 r.choice((1 << 30, 1024)), r.choice((152, 152, 148, 7)))
         assert check(*args) == "", args
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_starts_out_of_order_stay_in_bounds(check, seed):
+    """Whatever q_start holds: no head, token or partial result past the last one, and an end."""
+    r = random.Random(100 + seed)
+    for _ in range(1500):
+        nseq, ntok = r.randint(1, 9), r.randint(1, 3000)
+        q_start = [r.choice((r.randint(-10, ntok + 10), r.randint(0, ntok), -2**31, 2**31 - 1))
+                   if r.random() < 0.1 else r.randint(0, ntok) for _ in range(nseq + 1)]
+        args = (q_start, [r.randint(0, 4000) for _ in range(nseq)], ntok, r.choice((1, 2, 8)), r.choice((1, 8)))
+        assert check(*args, sound=False) == "", args

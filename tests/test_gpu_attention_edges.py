@@ -1,0 +1,61 @@
+"""Paged attention on the GPU where its inputs are not what they should be, or at the edges of what a
+type holds. max_kv only plans: 1 takes the kernel for few rows, 10^8 that for many."""
+import pytest
+import torch
+
+from test_gpu_attention import BF16, F16, F32, call, check, many_rows, problem
+
+pytestmark = pytest.mark.gpu
+BOTH_KERNELS = pytest.mark.parametrize("max_kv", [1, 10**8])
+
+
+@pytest.fixture(scope="module")
+def tq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_matvec_gb300 import build
+    build.build()
+    import bit_matvec_gb300
+    yield bit_matvec_gb300
+    assert bit_matvec_gb300.tq_device_status() == bit_matvec_gb300.TQ_OK
+
+
+def call_fenced(tq, prob, max_kv, max_q=None, fence=4096):
+    """call() with O, lse and the workspace inside wider buffers; whether what is beside them stayed."""
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    ntok, hq, dim = Q.shape
+    mq = max_q if max_q is not None else int((q_start[1:] - q_start[:-1]).max())
+    need = tq.tq_paged_attention_workspace_bytes(len(kv_len), ntok, hq, k.shape[1], dim, mq, max_kv)
+
+    def fenced(n, dtype, fill):
+        whole = torch.full((n + 2 * fence,), fill, dtype=dtype, device="cuda")
+        return whole, whole[fence:fence + n]
+
+    o, O = fenced(ntok * hq * dim, F32, -3.0)
+    lse, L = fenced(ntok * hq, F32, -3.0)
+    ws, W = fenced(max(need, 16), torch.uint8, 0xA5)
+    O = O.view(ntok, hq, dim)
+    tq.tq_paged_attention(Q.cuda(), tq.PagedKV(kd, vd, table.cuda()), q_start.cuda(), kv_len.cuda(), O,
+                          mq, max_kv, dim ** -0.5, W, 0, L)
+    kept = all(bool((x[:fence] == f).all() and (x[-fence:] == f).all())
+               for x, f in ((o, -3.0), (lse, -3.0), (ws, 0xA5)))
+    return O, L, kept
+
+
+@BOTH_KERNELS
+@pytest.mark.parametrize("starts", [[0, 90, 40, 130], [-1, 60, 100, 130], [0, 60, 100, 131], [0, 0, -5, 130],
+                                    [130, 100, 60, 0], [0, 2**31 - 1, 60, 130]])
+def test_starts_out_of_order_are_reported(tq, starts, max_kv):
+    """A q_start that decreases or leaves the call's tokens is said so, and nothing beside the outputs
+    and the workspace is written; the next call is right."""
+    prob = list(problem([(200, n) for n in (50, 40, 40)], 8, 2, 64, 16, F16))
+    want, _ = call(tq, tuple(prob), F32, max_kv=max_kv)
+    good = prob[4]
+    prob[4] = torch.tensor(starts, dtype=torch.int64).to(torch.int32)
+    _, _, kept = call_fenced(tq, prob, max_kv, max_q=130)
+    assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+    assert kept
+    prob[4] = good
+    again, L, kept = call_fenced(tq, prob, max_kv)
+    assert kept and torch.equal(want, again)
+    assert tq.tq_device_status() == tq.TQ_OK
