@@ -300,7 +300,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   const int per = (numbers + kThreads - 1) / kThreads;
   const int i0 = min((int)threadIdx.x * per, numbers), i1 = min(i0 + per, numbers);
   const int b0 = i0 < i1 ? tiles.find(i0) : 0;
-  const int64_t mine = sum_tiles(tiles, i0, i1, b0);
+  const int64_t mine = sum_tiles(tiles, numbers, i0, i1, b0);
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
   before -= mine;
@@ -323,7 +323,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   // registers across the roles it was spilled, and its first segment late.
   Start here;
   const int heads = p.q_heads / p.group;
-  if (!disorder && find_start(before, mine, total, i0, b0, heads, blockIdx.x, gridDim.x, &here)) *start = here;
+  if (!disorder && find_start(before, mine, total, numbers, i0, b0, heads, blockIdx.x, gridDim.x, &here))
+    *start = here;
   __syncthreads();
 
   // Every wait has a limit. One that gave up sets `failed`, which ends the

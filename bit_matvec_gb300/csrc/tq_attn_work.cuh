@@ -110,14 +110,19 @@ TQ_HD int tile_cost(const Segment& g, int tile) {
   return g.n < 0 ? 0 : tile + most(g.n * unit_cost(g), 1);
 }
 
-// Some consecutive row tiles of a head: their cost, with their number above it.
+// Some consecutive row tiles of a head: their cost, with their number above it,
+// and that of starting and ending them added later. 2^19 row tiles of up to
+// 2^23 key tiles fill the 63 bits; where there can be more, that cost is in the
+// sum instead of the number, which only decides about blocks of their own.
 constexpr int kCount = 44;
-template <typename P> TQ_HD int64_t sum_tiles(const Tiles<P>& tiles, int i0, int i1, int b0) {
+constexpr int kCounted = 1 << 19;     // row tile numbers, of which so many are counted
+template <typename P> TQ_HD int64_t sum_tiles(const Tiles<P>& tiles, int numbers, int i0, int i1, int b0) {
+  const int64_t each = numbers < kCounted ? int64_t(1) << kCount : kTileCost;
   int64_t sum = 0;
   for (int s = i0, b = b0; s < i1; ++s) {
     while (b + 1 < tiles.p.nseq && tiles.first(b + 1) <= s) ++b;
     const int cost = tile_cost(row_tile(tiles, s, b), 0);
-    sum += cost > 0 ? cost + (int64_t(1) << kCount) : 0;
+    sum += cost > 0 ? cost + each : 0;
   }
   return sum;
 }
@@ -134,12 +139,13 @@ struct Start {
 // Whether the work of `block` of `grid` starts in the row tiles [i0, ..) with
 // the sum `mine` (the first of them in sequence b0), `before` those before
 // them and `total` all of a head; and where.
-TQ_HD bool find_start(int64_t before, int64_t mine, int64_t total, int i0, int b0, int heads,
+TQ_HD bool find_start(int64_t before, int64_t mine, int64_t total, int numbers, int i0, int b0, int heads,
                       int64_t block, int64_t grid, Start* start) {
-  const bool own = (total >> kCount) * heads * 4 <= grid;
+  const bool counted = numbers < kCounted;
+  const bool own = total == 0 || (counted && (total >> kCount) * heads * 4 <= grid);
   const int tile_fee = own ? 0 : kTileCost;
   auto cost_of = [&](int64_t sum) {
-    return (sum & ((int64_t(1) << kCount) - 1)) + (sum >> kCount) * tile_fee;
+    return counted ? (sum & ((int64_t(1) << kCount) - 1)) + (sum >> kCount) * tile_fee : sum;
   };
   const int64_t tiles_before = before >> kCount, tiles_mine = mine >> kCount;
   const int64_t head_tiles = total >> kCount;
@@ -151,7 +157,7 @@ TQ_HD bool find_start(int64_t before, int64_t mine, int64_t total, int i0, int b
   const int64_t blocks = most((int64_t)1, least(grid, quotient(all, kLeastWork)));
   // own: every row tile has blocks of its own, those of the tile number i that
   // has the cost `sum` before it from first_block(i, sum) on
-  const int64_t spare = most(blocks - head_tiles * heads, (int64_t)0);
+  const int64_t spare = own ? most(blocks - head_tiles * heads, (int64_t)0) : 0;
   auto first_block = [&](int64_t i, int64_t sum) { return i + quotient(sum * spare, most(all, (int64_t)1)); };
   int64_t x0 = all, x1 = all;   // !own: the block's piece of the line
   int head0 = 0;                // the head its first row tile belongs to

@@ -45,7 +45,7 @@ extern "C" int attn_work_check(const int32_t* q_start, const int32_t* kv_len, in
   for (int t = 0; t < kThreads; ++t) {
     const int i0 = least(t * per, numbers), i1 = least(i0 + per, numbers);
     const int b0 = i0 < i1 ? tiles.find(i0) : 0;
-    const int64_t mine = sum_tiles(tiles, i0, i1, b0);
+    const int64_t mine = sum_tiles(tiles, numbers, i0, i1, b0);
     threads[t] = {i0, b0, total, mine};
     total = total + mine;
   }
@@ -56,7 +56,7 @@ extern "C" int attn_work_check(const int32_t* q_start, const int32_t* kv_len, in
     st.number = -1;
     int starts = 0;
     for (const Mine& m : threads)
-      starts += find_start(m.before, m.mine, total, m.i0, m.b0, heads, block, grid, &st);
+      starts += find_start(m.before, m.mine, total, numbers, m.i0, m.b0, heads, block, grid, &st);
     if (starts > 1) return fails(why, "several starts of block", block, starts);
     int steps = 0;
     const size_t first = pieces.size();

@@ -71,3 +71,21 @@ def test_starts_out_of_order_stay_in_bounds(check, seed):
                    if r.random() < 0.1 else r.randint(0, ntok) for _ in range(nseq + 1)]
         args = (q_start, [r.randint(0, 4000) for _ in range(nseq)], ntok, r.choice((1, 2, 8)), r.choice((1, 8)))
         assert check(*args, sound=False) == "", args
+
+
+@pytest.mark.parametrize("nseq,new,kv,group,heads", [
+    (530000, 1, 1, 200, 1), (4097, 2048, 2048, 16, 1), (2, 1 << 24, 1 << 20, 8, 1), (700000, 1, 300, 130, 3)])
+def test_more_row_tiles_than_19_bits_count(check, nseq, new, kv, group, heads):
+    """Row tiles by the half million, which single tokens of many sequences, or long chunks, can be."""
+    q_start = np.arange(nseq + 1, dtype=np.int64) * new
+    kv_len = np.full(nseq, kv)
+    kv_len[::7] += 129
+    assert nseq * -(-new * group // 256) > 1 << 19
+    assert check(q_start, kv_len, nseq * new, group, heads) == ""
+
+
+def test_no_work(check):
+    """No new tokens at all, in few sequences and in more than are counted."""
+    for nseq in (1, 40, 1 << 19):
+        for ntok in (0, 5):
+            assert check(np.zeros(nseq + 1), np.full(nseq, 100), ntok, 4, 2) == ""

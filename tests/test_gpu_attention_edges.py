@@ -59,3 +59,22 @@ def test_starts_out_of_order_are_reported(tq, starts, max_kv):
     again, L, kept = call_fenced(tq, prob, max_kv)
     assert kept and torch.equal(want, again)
     assert tq.tq_device_status() == tq.TQ_OK
+
+
+def test_more_row_tiles_than_19_bits_count(tq):
+    """A token of each of 530,000 sequences, 200 query heads to a key/value head: with one position
+    each, a row is the value at that position, whatever the query."""
+    nseq, hq, dim = 530000, 200, 8
+    v = torch.randn(64, 1, 8, dim, device="cuda", dtype=F16)
+    table = torch.randint(0, 64, (nseq, 1), device="cuda", dtype=torch.int32)
+    Q = torch.randn(nseq, hq, dim, device="cuda", dtype=F16)
+    O = torch.full_like(Q, float("nan"))
+    need = tq.tq_paged_attention_workspace_bytes(nseq, nseq, hq, 1, dim, 1, 1)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    tq.tq_paged_attention(Q, tq.PagedKV(torch.randn_like(v), v, table),
+                          torch.arange(nseq + 1, device="cuda", dtype=torch.int32),
+                          torch.ones(nseq, device="cuda", dtype=torch.int32), O, 1, 1, 0.3, ws)
+    assert need == 2 * 152 * 256 * (dim + 1) * 4 + 152 * 32      # the kernel for many rows
+    want = v[table[:, 0].long(), 0, 0]
+    assert tq.tq_device_status() == tq.TQ_OK
+    assert torch.equal(O, want[:, None].expand_as(O))
