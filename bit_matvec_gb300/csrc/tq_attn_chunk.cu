@@ -276,7 +276,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     }
     mbarrier_init(drain, 1);
     *failed = 0;
-    flags[2] = 0;
+    flags[2] = flags[3] = 0;
     start->number = -1;
     mbarrier_init_fence();
   }
@@ -304,14 +304,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   int64_t before = scan_warp(mine, lane);
   if (lane == 31) scan[warp] = before;
   before -= mine;
-  bool disorder = false, index = false;
-  for (int b = threadIdx.x; b < p.nseq; b += kThreads) {
-    disorder |= !tiles.in_order(b);
-    index |= tiles.start(b + 1) - tiles.start(b) > p.max_q || tiles.kv_len[b] > p.max_positions;
-  }
-  if (blockIdx.x == 0 && (disorder || index)) *p.status = kDevIndex;
   tc_fence_before();
-  disorder = __syncthreads_or(disorder);
+  __syncthreads();
   tc_fence_after();
   int64_t total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -323,8 +317,16 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   // registers across the roles it was spilled, and its first segment late.
   Start here;
   const int heads = p.q_heads / p.group;
-  if (!disorder && find_start(before, mine, total, numbers, i0, b0, heads, blockIdx.x, gridDim.x, &here))
-    *start = here;
+  if (find_start(before, mine, total, numbers, i0, b0, heads, blockIdx.x, gridDim.x, &here)) *start = here;
+  // Whether the lengths are what they should be, from the last warp on: the
+  // first ones are likelier to find the start.
+  for (int b = kThreads - 1 - (int)threadIdx.x; b < p.nseq; b += kThreads) {
+    const bool disorder = !tiles.in_order(b);
+    if (disorder) flags[3] = 1;   // no work
+    if (blockIdx.x == 0 && (disorder || tiles.start(b + 1) - tiles.start(b) > p.max_q ||
+                            tiles.kv_len[b] > p.max_positions))
+      *p.status = kDevIndex;
+  }
   __syncthreads();
 
   // Every wait has a limit. One that gave up sets `failed`, which ends the
@@ -575,7 +577,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           mbarrier_arrive(seg_full + 8 * i);
           ++queued;
         };
-        const CutTile cut = walk(tiles, numbers, *start, p.q_heads / p.group, (int)gridDim.x, (int)blockIdx.x,
+        Start st = *start;
+        if (flags[3]) st.number = -1;
+        const CutTile cut = walk(tiles, numbers, st, p.q_heads / p.group, (int)gridDim.x, (int)blockIdx.x,
                                  push, [&]() { return *failed != 0; });
         Segment end = {};
         end.n = -1;
