@@ -733,8 +733,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     // no block leaves before its copies have landed and its MMAs have ended
     if (warp == 10) {
       const int issued = (int)flags[2];
-      if (lane < kSlots && issued > lane)
-        mbarrier_wait_bounded(full + 8 * lane, ((issued - 1 - lane) / kSlots) & 1, limit / 10);
+      const int last = lane < kSlots ? last_phase(issued, lane, kSlots) : -1;
+      if (last >= 0) mbarrier_wait_bounded(full + 8 * lane, last, limit / 10);
     }
     if (warp == 8) {
       commit(elect_one(), drain);

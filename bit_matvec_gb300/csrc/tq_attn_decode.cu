@@ -160,6 +160,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int t0 = min(t_lo + split * p.chunk_tiles, t_hi);
   const int t1 = split == p.nsplit - 1 ? t_hi : min(t0 + p.chunk_tiles, t_hi);
 
+  int issued = 0;   // tiles that the producer requested
   if (warp == kWarps) {
     // ------------------------------------------------ producer
     const int boxes = kKeys / p.box_rows;    // 1 .. 16, one lane each
@@ -209,6 +210,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           tma_box(v + c * kKeys * 128, &vmap, c * 64, sl, head, pg, full);
         }
       }
+      ++issued;
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -489,9 +491,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   // after a failed wait the producer's copies are still counted on the full
   // barriers: no block leaves before they have landed
   __syncthreads();
-  if (*failed && threadIdx.x < kStages && !stalled) {
-    const int issued = (t1 - t0 - (int)threadIdx.x + kStages - 1) / kStages;
-    if (issued > 0) mbarrier_wait_bounded(bars + 8 * threadIdx.x, (issued - 1) & 1, limit / 10);
+  if (*failed && warp == kWarps && lane < kStages) {
+    const int last = last_phase(issued, lane, kStages);
+    if (last >= 0) mbarrier_wait_bounded(bars + 8 * lane, last, limit / 10);
   }
 }
 

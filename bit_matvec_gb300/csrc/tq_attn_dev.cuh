@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "tq_attn.cuh"
+#include "tq_ring.cuh"
 
 namespace tq {
 
