@@ -428,6 +428,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         wait(s_full + 8 * h, ss & 1);
         ++ss;
         if (k == n - 1) next_queries();
+        __syncwarp();   // lanes leave a wait apart; tensor memory is read by whole warps
         tc_fence_after();
         const int j = alt ? 2 * k + h : k;
         const int key0 = (g.t0 + j) * kKeys;
@@ -478,6 +479,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                   make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
           named_barrier_sync(2 + h, kHalf);   // all rows, before the first product
         }
         const float ref = m == -INFINITY ? 0.0f : -m;
@@ -499,6 +501,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       }
       base_item += 2 * g.n;
       if (n == 0) next_queries();
+      __syncwarp();
       tc_fence_after();
       queries_loaded(queue[(sg + 1) % kQueue]);
       const float2 la = f2_unpack(f2_add(l0, l1));
@@ -545,19 +548,18 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           uint32_t o[32] = {}, o1[32] = {};
           if (n > 0) tmem_ld32(to + c, o);
           if (merge) tmem_ld32(to + (h == 0 ? DP : -DP) + c, o1);
-          if (!live) continue;
 #pragma unroll
           for (int q = 0; q < 32; q += 16) {
             const int left = p.dim - c - q;
-            if (left <= 0) continue;
             float x[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               x[e] = __uint_as_float(o[q + e]) * keep;
               if (merge) x[e] = fmaf(__uint_as_float(o1[q + e]), other, x[e]);
             }
-            store_out16(out, type, obase + c + q, x, left);
+            if (live && left > 0) store_out16(out, type, obase + c + q, x, left);
           }
+          __syncwarp();   // before the next columns, which the warp reads together
         }
       }
       tc_fence_before();
@@ -626,7 +628,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int it = base_item + 2 * j + v, sidx = it % kSlots;
-            if (it >= kSlots && !wait(empty + 8 * sidx, (it / kSlots - 1) & 1)) break;
+            // (one answer for the warp)
+            if (!__all_sync(0xffffffffu, it < kSlots || wait(empty + 8 * sidx, (it / kSlots - 1) & 1))) break;
             if (lane == 0) mbarrier_arrive_expect_tx(full + 8 * sidx, S::kTile);
             __syncwarp();
             if (lane < boxes) {

@@ -193,12 +193,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
       locate(t + 1);
-      if (t - t0 >= kStages &&
-          !mbarrier_wait_bounded(bars + 8 * (kStages + stage), phase ^ 1, limit)) {
+      // one answer for the warp: lanes whose waits ended apart would part here
+      const bool free = t - t0 < kStages ||
+                        mbarrier_wait_bounded(bars + 8 * (kStages + stage), phase ^ 1, limit);
+      if (!__all_sync(0xffffffffu, free && !*failed)) {
         *failed = 1;
         break;
       }
-      if (*failed) break;
       const uint32_t full = bars + 8 * stage;
       if (lane == 0) mbarrier_arrive_expect_tx(full, 2 * S::kTile);
       __syncwarp();
@@ -259,7 +260,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     int stage = 0, phase = 0;
     bool ok = true;
     for (int t = t0; t < t1; ++t) {
-      if (!mbarrier_wait_bounded(bars + 8 * stage, phase, limit)) {
+      // (and one answer for the warp, whose matrix instructions want all lanes)
+      if (!__all_sync(0xffffffffu, mbarrier_wait_bounded(bars + 8 * stage, phase, limit))) {
         ok = false;
         break;
       }
