@@ -732,6 +732,9 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     }
   }
   __syncwarp();
+  tc_fence_before();
+  __syncthreads();   // no wait of a role runs out after it
+  tc_fence_after();
   if (*failed) {
     // no block leaves before its copies have landed and its MMAs have ended
     if (warp == 10) {
@@ -743,15 +746,10 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       commit(elect_one(), drain);
       mbarrier_wait_bounded(drain, 0, limit / 10);
     }
+    if (threadIdx.x == 0) *p.status = kDevTimeout;
     __syncwarp();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (*failed && threadIdx.x == 0) *p.status = kDevTimeout;
-  if (warp == 8) {
-    tc_fence_after();
-    tmem_dealloc<1>(tmem, 512);
-  }
+  if (warp == 8) tmem_dealloc<1>(tmem, 512);
 }
 
 constexpr int kJoinWarps = 8, kJoinBlocks = 32;  // warps of a block, blocks of a row tile
