@@ -121,6 +121,7 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   AttnPlan p = {};
   const int64_t group = q_heads / kv_heads;
   if (max_q > ntok) max_q = ntok;
+  if (window >= kMaxPositions) window = 0;   // as long as any sequence: none, as for the kernels
   const int64_t rows = max_q * group;
   // keys that the tokens of `n` rows see at most
   auto span_of = [&](int64_t n) {

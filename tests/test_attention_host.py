@@ -227,3 +227,12 @@ def test_marshalling_module(tq):
     with pytest.raises(tq.TQError) as e:
         tq.tq_qk_norm_rope(x.double(), None, x, None)
     assert e.value.code == tq.TQ_ERR_TYPE
+
+
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, 1 << 62, (1 << 63) - 1])
+def test_windows_as_long_as_any_sequence_plan_as_none(tq, window):
+    """The workspace, a function of the plan alone, is that of no window."""
+    for sizes in ((1, 1, 64, 8, 128, 1, 131072), (1, 5, 32, 4, 64, 5, 9001), (16, 80, 32, 4, 64, 5, 9001),
+                  (64, 64, 40, 8, 128, 1, 8192), (8, 2000, 40, 8, 128, 512, 4096), (3, 3, 8, 8, 64, 1, 100)):
+        assert tq.tq_paged_attention_workspace_bytes(*sizes, window) == \
+            tq.tq_paged_attention_workspace_bytes(*sizes, 0), sizes

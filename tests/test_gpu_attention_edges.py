@@ -78,3 +78,12 @@ def test_more_row_tiles_than_19_bits_count(tq):
     want = v[table[:, 0].long(), 0, 0]
     assert tq.tq_device_status() == tq.TQ_OK
     assert torch.equal(O, want[:, None].expand_as(O))
+
+
+@pytest.mark.parametrize("lens,hq,hk", [([(5000, 1)], 8, 1), ([(900, 5)] * 3, 8, 2), ([(900, 300), (40, 40)], 8, 2)])
+def test_windows_as_long_as_any_sequence(tq, lens, hq, hk):
+    prob = problem(lens, hq, hk, 64, 16, BF16)
+    want, want_lse = call(tq, prob, F32)
+    for window in (1 << 30, (1 << 31) - 1, (1 << 63) - 1):
+        got, lse = call(tq, prob, F32, window)
+        assert torch.equal(got, want) and torch.equal(lse, want_lse)
