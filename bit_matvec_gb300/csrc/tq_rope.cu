@@ -38,22 +38,25 @@ extern "C" int tq_rope_turns(int64_t rot_dim, double base, int kind, double fact
   if (amplitude) *amplitude = kind == TQ_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   if (kind == TQ_ROPE_BASE && rot_dim > 2)
     base *= std::pow(factor, (double)rot_dim / (double)(rot_dim - 2));
-  double first = 0, last = 0;
+  // the ramp: pairs up to `kept` make `high` turns or more, those from `divided`
+  // on `low` or fewer (either may lie past the table, at one end or the other)
+  double kept = 0, divided = 0;
   if (kind == TQ_ROPE_RAMP) {
     // the pair index at which a pair makes n turns over original_len positions
     auto index = [&](double n) {
       return 0.5 * rot_dim * std::log(original_len / (n * kTwoPi)) / std::log(base);
     };
-    first = std::fmax(std::floor(index(high)), 0.0);
-    last = std::fmin(std::ceil(index(low)), (double)(rot_dim - 1));
-    if (first == last) last += 0.001;
+    kept = std::floor(index(high));
+    divided = std::ceil(index(low));
   }
   for (int64_t i = 0; i < rot_dim / 2; ++i) {
     double f = std::pow(base, -2.0 * (double)i / (double)rot_dim);
     double keep = 1.0;
     if (kind == TQ_ROPE_LINEAR) keep = 0.0;
-    if (kind == TQ_ROPE_RAMP)
-      keep = 1.0 - std::fmin(std::fmax(((double)i - first) / (last - first), 0.0), 1.0);
+    if (kind == TQ_ROPE_RAMP) {
+      const double first = std::fmax(kept, 0.0), last = std::fmin(divided, (double)(rot_dim - 1));
+      keep = (double)i <= kept ? 1.0 : (double)i >= divided ? 0.0 : 1.0 - ((double)i - first) / (last - first);
+    }
     if (kind == TQ_ROPE_BANDS)
       keep = std::fmin(std::fmax((original_len * f / kTwoPi - low) / (high - low), 0.0), 1.0);
     if (keep < 1.0) f = f * keep + f / factor * (1.0 - keep);

@@ -236,3 +236,39 @@ def test_windows_as_long_as_any_sequence_plan_as_none(tq, window):
                   (64, 64, 40, 8, 128, 1, 8192), (8, 2000, 40, 8, 128, 512, 4096), (3, 3, 8, 8, 64, 1, 100)):
         assert tq.tq_paged_attention_workspace_bytes(*sizes, window) == \
             tq.tq_paged_attention_workspace_bytes(*sizes, 0), sizes
+
+
+def ramp_rule(rot, base, factor, length, low, high):
+    """Frequencies of the ramp from its definition: kept at `high` turns and more over `length`, divided
+    by factor at `low` and fewer, between them linear in the pair's number."""
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    at = [0.5 * rot * math.log(length / (n * 2 * math.pi)) / math.log(base) for n in (high, low)]
+    first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+    out = []
+    for i, x in enumerate(f):
+        n = length * x / (2 * math.pi)
+        keep = 1.0 if n >= high else 0.0 if n <= low else 1 - (i - first) / (last - first)
+        out.append(x * keep + x / factor * (1 - keep))
+    return out
+
+
+@pytest.mark.parametrize("rot,base,length,low,high,what", [
+    (8, 10.0, 65536.0, 1.0, 32.0, "kept"),          # 1854 to 10430 turns, all above high
+    (128, 1e4, 1e9, 1.0, 32.0, "kept"),
+    (64, 1e6, 2.0, 1.0, 32.0, "divided"),           # under a third of a turn
+    (8, 10.0, 3.0, 1.0, 2.0, "divided"),
+    (2, 1e4, 4096.0, 1.0, 32.0, "kept"), (2, 1e4, 5.0, 1.0, 32.0, "divided"), (2, 1e4, 60.0, 1.0, 32.0, "mixed"),
+    (128, 1e4, 4096.0, 1.0, 32.0, "mixed"), (64, 5e5, 8192.0, 1.0, 4.0, "mixed"), (20, 10.0, 300.0, 8.0, 32.0, "mixed"),
+    (128, 1e4, 60.0, 1.0, 32.0, "mixed"),           # the ramp begins before the first pair
+    (16, 3.0, 300.0, 1.0, 32.0, "mixed"),           # and ends past the last one
+])
+def test_ramp_ends(tq, rot, base, length, low, high, what):
+    factor = 4.0
+    got = [turn(x) * 2 * math.pi for x in tq.tq_rope_turns(rot, base, tq.ROPE_RAMP, factor, length, low, high)[0]]
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if what == "kept":
+        assert got == pytest.approx(f, rel=1e-14)
+    elif what == "divided":
+        assert got == pytest.approx([x / factor for x in f], rel=1e-14)
+    else:
+        assert got == pytest.approx(ramp_rule(rot, base, factor, length, low, high), rel=1e-13)
