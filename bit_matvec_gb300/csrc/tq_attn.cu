@@ -48,19 +48,19 @@ attn_join_kernel(const __grid_constant__ AttnParams p) {
     const float* from = p.part_o + row * p.dim + lane * 4;
 #pragma unroll 4
     for (int s = warp; s < p.nsplit; s += kJoinWarps) {
-      // loaded in any case; nothing was written for an empty range
+      // (of a range without keys the row is zeros)
       const float4 x = *reinterpret_cast<const float4*>(from + s * rows * p.dim);
       const float f = weight[s];
-      acc.x = f > 0.0f ? fmaf(f, x.x, acc.x) : acc.x;
-      acc.y = f > 0.0f ? fmaf(f, x.y, acc.y) : acc.y;
-      acc.z = f > 0.0f ? fmaf(f, x.z, acc.z) : acc.z;
-      acc.w = f > 0.0f ? fmaf(f, x.w, acc.w) : acc.w;
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
     }
   }
   part[threadIdx.x] = acc;
   __syncthreads();
   if (warp == 0 && lane * 4 < p.dim) {
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) {
@@ -75,7 +75,7 @@ attn_join_kernel(const __grid_constant__ AttnParams p) {
     store_out4(p.o, p.o_type, tok * p.o_stride + (row - tok * p.q_heads) * p.dim + lane * 4, x);
   }
   if (threadIdx.x == 0 && p.lse)
-    p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

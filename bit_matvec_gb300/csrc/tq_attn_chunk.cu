@@ -526,8 +526,8 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       }
       if (merge || !alt || h == 0) {
         // -------------------------------------------- output rows
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const float lse = l > 0.0f ? m + log2f(l) : -INFINITY;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float lse = l == 0.0f ? -INFINITY : m + log2f(l);
         const bool live = row < g.rows;
         const int64_t tok = g.tok + trow;
         const int qh = g.head * p.group + (g.off + row) % p.group;
@@ -808,13 +808,13 @@ attn_chunk_join_kernel(const __grid_constant__ AttnParams p) {
         }
       }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int t = (cut.off + r) / p.group;
     const int64_t tok = cut.tok + t, qh = cut.head * p.group + (cut.off + r - t * p.group);
     const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
     if (lane * 4 < p.dim) store_out4(p.o, p.o_type, tok * p.o_stride + qh * p.dim + lane * 4, x);
     if (lane == 0 && p.lse)
-      p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      p.lse[tok * p.q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
 }
 

@@ -427,9 +427,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           }
           continue;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-        const float lse = sum > 0.0f ? ref + log2f(sum) : -INFINITY;
+        const float lse = sum == 0.0f ? -INFINITY : ref + log2f(sum);
         const int ti = by_group(off0 + r);
         const int64_t tok = q0 + tok0 + ti;
         const int qh = head * p.group + off0 + r - ti * p.group;
@@ -477,7 +477,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           o[2] = fmaf(f, x[s].z, o[2]);
           o[3] = fmaf(f, x[s].w, o[3]);
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] *= inv;
         const int ti = by_group(off0 + r);
@@ -485,7 +485,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const int qh = head * p.group + off0 + r - ti * p.group;
         store_out4(p.o, p.o_type, tok * p.o_stride + (int64_t)qh * p.dim + d, o);
         if (d == 0 && p.lse)
-          p.lse[tok * p.q_heads + qh] = sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+          p.lse[tok * p.q_heads + qh] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
       }
     __syncwarp();
     cluster_sync();   // no block's shared memory goes before the others have read it

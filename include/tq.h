@@ -510,7 +510,9 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  * p = kv_len[b] - n + i and sees the positions j <= p, with window > 0 only
  * those > p - window. Query head h reads key/value head h / (q_heads / heads).
  *   o = sum_j exp(s_j) v_j / sum_j exp(s_j),  s_j = scale * q . k_j
- * A token that sees nothing (p < 0) gets zeros, and minus infinity as its lse.
+ * A token that sees nothing (p < 0), or whose every score is minus infinity,
+ * gets zeros, and minus infinity as its lse. A query with a NaN gives NaN in its
+ * row and its lse, an infinite one too unless all its scores are minus infinity.
  *   Q   typed kv->type, head h of token t at Q + t * q_stride + h * head_dim;
  *       16-byte aligned, q_stride a multiple of 8.
  *   q_start int32 [nseq + 1], from 0, non-decreasing, at most ntok; kv_len int32 [nseq].

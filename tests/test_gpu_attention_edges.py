@@ -3,6 +3,7 @@ type holds. max_kv only plans: 1 takes the kernel for few rows, 10^8 that for ma
 import pytest
 import torch
 
+from attn_util import assert_within, attention
 from test_gpu_attention import BF16, F16, F32, call, check, many_rows, problem
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,37 @@ def test_windows_as_long_as_any_sequence(tq, lens, hq, hk):
     for window in (1 << 30, (1 << 31) - 1, (1 << 63) - 1):
         got, lse = call(tq, prob, F32, window)
         assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+# a few rows: one block, a cluster, ranges joined through the workspace, rows of several fragments; many
+# rows: whole row tiles, alternate key tiles, cut row tiles
+PLANS = [([(60, 1)], 4, 4, 1), ([(2000, 1)], 8, 8, None), ([(20000, 1)], 2, 1, None), ([(900, 9)] * 40, 8, 2, 1),
+         ([(900, 260), (300, 20)], 4, 1, 10**8), ([(3000, 100)], 2, 2, 10**8), ([(700, 600)] * 6, 8, 8, 10**8)]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("plan", PLANS, ids=str)
+def test_queries_that_are_not_finite_are_not_hidden(tq, plan, dtype, bad):
+    """A NaN in a query is NaN in its row and its lse, an infinity too (it makes scores of both signs),
+    however the keys are split; the other rows are what they were, but for roundings."""
+    lens, hq, hk, max_kv = plan
+    prob = list(problem(lens, hq, hk, 64, 16, dtype))
+    Q, k, v, table, q_start, kv_len, _, _ = prob
+    o, want_lse, tol, tol_lse = attention(Q, k, v, table, q_start, kv_len, 64 ** -0.5, 0, F32)
+    g = torch.Generator().manual_seed(3)
+    Q = prob[0] = prob[0].clone()
+    hit = torch.zeros(Q.shape[:2], dtype=torch.bool)
+    for _ in range(max(1, hit.numel() // 20)):
+        hit.view(-1)[torch.randint(0, hit.numel(), (1,), generator=g)] = True
+    # not the first positions, whose few scores may all have one sign
+    pos = torch.cat([torch.arange(n - q, n) for n, q in lens])
+    hit &= (pos >= 40)[:, None]
+    assert hit.any()
+    Q[..., 7][hit] = bad
+    got, lse = call(tq, tuple(prob), F32, max_kv=max_kv)
+    got, lse = got.cpu(), lse.cpu()
+    assert torch.isnan(got[hit]).all()
+    assert torch.isnan(lse[hit]).all()
+    assert_within(got[~hit], o[~hit], tol[~hit], "o")
+    assert_within(lse[~hit], want_lse[~hit], tol_lse[~hit], "lse")
