@@ -38,6 +38,7 @@ using namespace work;
 constexpr int kSoft = 256;            // softmax threads, one a row
 constexpr int kThreads = kSoft + 128; // and an MMA, a TMA and a scheduling warp (and one that idles)
 constexpr float kGrow = 8.0f;         // a maximum moves when it grew by 2^8
+constexpr int kUp = 7;                // f16 weights are up to 2^(kGrow + kUp)
 constexpr int kQueue = 4;             // segments the scheduling warp may be ahead
 constexpr int kCachedSeqs = 48;       // lengths of so many sequences are kept in shared memory
 
@@ -207,7 +208,7 @@ __device__ __forceinline__ float max64(const float (&s)[64]) {
   return fmaxf(max3(a, b, c), d);
 }
 
-// Weights of 64 scores, 2^(scale s - ref), packed in pairs of T into TMEM;
+// Weights of 64 scores, 2^(scale s + ref), packed in pairs of T into TMEM;
 // their sum into (l0, l1).
 template <typename T>
 __device__ __forceinline__ void weights64(const float (&s)[64], uint64_t scale2, uint64_t ref2,
@@ -482,7 +483,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
           __syncwarp();
           named_barrier_sync(2 + h, kHalf);   // all rows, before the first product
         }
-        const float ref = m == -INFINITY ? 0.0f : -m;
+        const float ref = addend<T, kUp>(m == -INFINITY ? 0.0f : m);
         const uint64_t ref2 = f2_packf(ref, ref);
         auto signal = [&](uint32_t bar) {
           tmem_wait_st();
@@ -506,6 +507,7 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
       queries_loaded(queue[(sg + 1) % kQueue]);
       const float2 la = f2_unpack(f2_add(l0, l1));
       float l = la.x + la.y;
+      m -= Scaled<T, kUp>::kUp;
       float keep = 1.0f, other = 0.0f;
       const bool merge = alt && g.n > 1;
       if (merge) {

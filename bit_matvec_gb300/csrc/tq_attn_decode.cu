@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kWarps = 4;             // compute warps
 constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kUp = 15;               // f16 weights are up to 2^kUp
 
 // A stage is 16 KB of keys and 16 KB of values whatever the head's size; three
 // of them leave room for two blocks on an SM.
@@ -315,15 +316,16 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
         }
-        float corr[2], ref[2];
+        float corr[2], plus[2];
         bool grow = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
           const float mn = fmaxf(m[h], mx[h] * scale);
-          ref[h] = mn == -INFINITY ? 0.0f : mn;
-          corr[h] = exp2_approx(m[h] - ref[h]);
+          const float ref = mn == -INFINITY ? 0.0f : mn;
+          corr[h] = exp2_approx(m[h] - ref);
+          plus[h] = addend<T, kUp>(ref);
           grow |= mn > m[h];
           m[h] = mn;
         }
@@ -346,7 +348,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              w[e] = exp2_approx(fmaf(s[2 * n + q][e], scale, -ref[e >> 1]));
+              w[e] = exp2_approx(fmaf(s[2 * n + q][e], scale, plus[e >> 1]));
               l[e >> 1] += w[e];
             }
             a[2 * q] = pack2<T>(w[0], w[1]);
@@ -369,6 +371,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       }
     }
     if (!ok) *failed = 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) m[h] -= Scaled<T, kUp>::kUp;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);

@@ -38,6 +38,20 @@ struct AttnParams {
   float scale_log2;
 };
 
+// The weights of the keys are rounded to T for their product with the values,
+// which the tensor cores want alike; their sum, the divisor, takes them in 32
+// bits. In f16, where the largest weight were 1, those below 2^-25 would vanish
+// from the product and stay in the sum (20,000 keys with a score 18 below one
+// key's came out as nothing), so weights are 2^Up times that, up to 2^15 of the
+// 2^16 that f16 holds: smaller ones keep all bits to 2^-14 - Up. The power is
+// taken off the maximum at the end. bf16 has the exponents of 32 bits.
+template <typename T, int Up> struct Scaled { static constexpr float kUp = 0.0f; };
+template <int Up> struct Scaled<__half, Up> { static constexpr float kUp = Up; };
+// The exponent's addend for the reference m of a row (finite or 0).
+template <typename T, int Up> __device__ __forceinline__ float addend(float m) {
+  return Scaled<T, Up>::kUp != 0.0f ? Scaled<T, Up>::kUp - m : -m;
+}
+
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);

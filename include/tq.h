@@ -530,7 +530,8 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  *       contents overwritten and meaningless after the call; calls that share
  *       it must be ordered.
  * The weights exp(s_j) are rounded to the cache's type for their product with
- * the values; everything else is 32-bit. Slots that no new token sees (past
+ * the values (in f16 to 11 bits down to 2^-21 of the row's largest weight, to
+ * fewer below, to none below 2^-32); everything else is 32-bit. Slots that no new token sees (past
  * kv_len, or before the window) may hold anything, NaN included, and their
  * pages are not read. Keys and values that some token of the sequence sees
  * must be finite.

@@ -3,7 +3,7 @@ type holds. max_kv only plans: 1 takes the kernel for few rows, 10^8 that for ma
 import pytest
 import torch
 
-from attn_util import assert_within, attention
+from attn_util import U, assert_within, attention, gather
 from test_gpu_attention import BF16, F16, F32, call, check, many_rows, problem
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +122,36 @@ def test_queries_that_are_not_finite_are_not_hidden(tq, plan, dtype, bad):
     assert torch.isnan(lse[hit]).all()
     assert_within(got[~hit], o[~hit], tol[~hit], "o")
     assert_within(lse[~hit], want_lse[~hit], tol_lse[~hit], "lse")
+
+
+@pytest.mark.parametrize("above", [8, 14, 16, 18, 20])
+@pytest.mark.parametrize("every", [128, 20000])
+@pytest.mark.parametrize("new,max_kv", [(1, None), (1, 1), (20, 1), (200, 10**8)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_many_small_weights_beside_a_large_one(tq, dtype, new, max_kv, every, above):
+    """One key `above` the others in its score, with a value of zero, and 20,000 others: what comes out
+    is the others' part alone, which an f16 weight below 2^-25 would not have. With one such key every
+    128, whatever share of the keys a block takes has one.
+
+    The bound is that of the 64-bit form with a weight's subnormal rounding at 2^-32 of the largest
+    weight's instead of 2^-25: f16 weights are kept 2^7 or more above one."""
+    n, dim = 20000, 64
+    Q, k, v, table, q_start, kv_len, _, _ = problem([(n, new)], 2, 1, dim, 16, dtype, poison=False)
+    Q = torch.ones_like(Q)
+    k *= 0.05
+    v = (v * 0.1 + 1).to(dtype)
+    for j in range(0, n, every):
+        k[table[0, j // 16], 0, j % 16] = above / dim ** 0.5   # times dim and the scale dim^-1/2: above
+        v[table[0, j // 16], 0, j % 16] = 0
+    # o in 64 bits; roundings as in attention(): scores, exponentials and sums in 32 bits, weights in dtype
+    kk, vv = gather(k, table[0], n)[0], gather(v, table[0], n)[0]
+    score = torch.einsum("rhd,nd->rhn", Q.double(), kk) * dim ** -0.5
+    size = torch.einsum("rhd,nd->rhn", Q.double().abs(), kk.abs()).amax(-1, keepdim=True) * dim ** -0.5
+    seen = torch.arange(n)[None] <= torch.arange(n - new, n)[:, None]
+    p = torch.exp(score - score.amax(-1, keepdim=True)) * seen[:, None]
+    total = p.sum(-1, keepdim=True)
+    want, mass = p @ vv / total, p @ vv.abs() / total
+    rel = (dim + 2) * 2.0**-23 * size + 2.0**-20 + n * 2.0**-23
+    bound = mass * (2 * rel + U[dtype]) + vv.abs().sum(0) * 2.0**-32 / total
+    O, _ = call(tq, (Q, k, v, table, q_start, kv_len, k.cuda(), v.cuda()), F32, max_kv=max_kv)
+    assert_within(O, want, bound, "o")
