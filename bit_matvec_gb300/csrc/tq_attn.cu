@@ -110,10 +110,22 @@ cudaError_t cache_map(CUtensorMap* map, const tq_paged_kv& c, void* p, int box_r
   const cuuint64_t strides[3] = {one, c.heads > 1 ? (cuuint64_t)c.head_stride * 2 : one,
                                  c.pages > 1 ? (cuuint64_t)c.page_stride * 2 : one};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, c.type == TQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-         4, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&]() {
+    return fn(map, c.type == TQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              4, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r != CUDA_SUCCESS) {
+    // The driver wants the device's context to be current in the calling thread.
+    // A launch sees to that itself, but in a host thread whose first CUDA call
+    // this is there was none yet; setting the device does it.
+    int dev = 0;
+    cudaError_t s = cudaGetDevice(&dev);
+    if (s == cudaSuccess) s = cudaSetDevice(dev);
+    if (s != cudaSuccess) return s;
+    r = encode();
+  }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -155,3 +155,72 @@ def test_many_small_weights_beside_a_large_one(tq, dtype, new, max_kv, every, ab
     bound = mass * (2 * rel + U[dtype]) + vv.abs().sum(0) * 2.0**-32 / total
     O, _ = call(tq, (Q, k, v, table, q_start, kv_len, k.cuda(), v.cuda()), F32, max_kv=max_kv)
     assert_within(O, want, bound, "o")
+
+
+THREADS = """
+import ctypes, threading, torch
+import bit_matvec_gb300 as tq
+lib = tq.library()
+dev = dict(device="cuda")
+k, v = (torch.randn(8, 2, 16, 64, **dev).half() for _ in range(2))
+table = torch.arange(8, dtype=torch.int32, **dev)[None]
+kv = tq.PagedKV(k, v, table)
+q = torch.randn(1, 4, 64, **dev).half()
+starts, lens = torch.tensor([0, 1], dtype=torch.int32, **dev), torch.tensor([100], dtype=torch.int32, **dev)
+out = [torch.zeros(1, 4, 64, **dev) for _ in range(8)]
+streams = [torch.cuda.Stream() for _ in out]
+need = tq.tq_paged_attention_workspace_bytes(1, 1, 4, 2, 64, 1, 100)
+ws = [torch.empty(max(need, 16), dtype=torch.uint8, **dev) for _ in out]
+torch.cuda.synchronize()
+gate, codes = threading.Barrier(len(out)), [None] * len(out)
+def first_call(i):
+    gate.wait()     # ctypes lets go of the interpreter's lock: the calls do run side by side
+    codes[i] = lib.tq_paged_attention(q.data_ptr(), 256, kv.ref, starts.data_ptr(), lens.data_ptr(),
+                                      out[i].data_ptr(), 256, tq.TQ_F32, None, 1, 4, 1, 100, 0.125, 0,
+                                      ws[i].data_ptr(), need, streams[i].cuda_stream)
+threads = [threading.Thread(target=first_call, args=(i,)) for i in range(len(out))]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert codes == [tq.TQ_OK] * len(out), codes
+assert all(torch.equal(o, out[0]) for o in out) and out[0].abs().max() > 0
+assert tq.tq_device_status() == tq.TQ_OK
+"""
+
+
+def test_first_calls_of_several_host_threads(tq):
+    """A fresh process whose first attention calls come from eight threads at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(2):
+        subprocess.run([sys.executable, "-c", THREADS], cwd=root, check=True, timeout=300)
+
+
+@pytest.mark.parametrize("max_kv", [100, 10**8])
+def test_first_cuda_call_of_a_host_thread(tq, max_kv):
+    """A thread that never made a CUDA call, on tensors of another one: both kernels."""
+    import threading
+    prob = problem([(100, 70)], 4, 2, 64, 16, F16)
+    want, want_lse = call(tq, prob, F32, max_kv=max_kv)
+    Q, k, v, table, q_start, kv_len, kd, vd = prob
+    need = tq.tq_paged_attention_workspace_bytes(1, 70, 4, 2, 64, 70, max_kv)
+    args = (Q.cuda(), tq.PagedKV(kd, vd, table.cuda()), q_start.cuda(), kv_len.cuda())
+    O, L = torch.zeros_like(want), torch.zeros_like(want_lse)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    stream, errors = torch.cuda.current_stream(), []
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            tq.tq_paged_attention(*args, O, 70, max_kv, 64 ** -0.5, ws, 0, L, stream=stream)
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert torch.equal(O, want) and torch.equal(L, want_lse)
