@@ -1,5 +1,7 @@
 // tq_attn.cu -- paged attention: the launch (parameters, maps of the cache,
 // which kernel) and the join of partial results.
+#include <atomic>
+
 #include "tq_attn_dev.cuh"
 
 namespace tq {
@@ -84,7 +86,10 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 cudaError_t encode_fn(EncodeFn* out) {
-  static EncodeFn fn = nullptr;   // the driver's entry point: the same for every call
+  // the driver's entry point, the same for every call: host threads that come
+  // first at the same time each look it up
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_relaxed);
   if (!fn) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -93,6 +98,7 @@ cudaError_t encode_fn(EncodeFn* out) {
     if (e != cudaSuccess) return e;
     if (q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
     fn = reinterpret_cast<EncodeFn>(f);
+    known.store(fn, std::memory_order_relaxed);
   }
   *out = fn;
   return cudaSuccess;
