@@ -13,8 +13,12 @@ bool type_ok(int t) { return t == TQ_F32 || t == TQ_F16 || t == TQ_BF16; }
 int64_t type_bytes(int t) { return t == TQ_F32 ? 4 : 2; }
 bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
 
-constexpr int64_t kMaxSize = int64_t(1) << 40;   // of a stride or count, so that products stay in 64 bits
+constexpr int64_t kMaxSize = int64_t(1) << 40;   // of a stride
 bool size_ok(int64_t n) { return n >= 0 && n <= kMaxSize; }
+
+// Whether n rows `stride` apart (both not negative) span at most 2^58 values:
+// no memory holds more, and sums of such products stay in 64 bits.
+bool span_ok(int64_t n, int64_t stride) { return n <= 1 || stride <= (int64_t(1) << 58) / (n - 1); }
 
 int fail_cuda(cudaError_t e) {
   record_cuda_error(e);
@@ -66,6 +70,9 @@ int check_cache(const tq_paged_kv* c) {
     return TQ_ERR_SHAPE;
   for (int64_t s : {c->page_stride, c->head_stride, c->slot_stride})
     if (s < 0 || s >= (int64_t(1) << 39) || s % 8 != 0) return TQ_ERR_SHAPE;
+  if (!span_ok(c->nseq, c->table_stride) || !span_ok(c->pages, c->page_stride) ||
+      !span_ok(c->heads, c->head_stride) || !span_ok(c->page_size, c->slot_stride))
+    return TQ_ERR_SHAPE;
   if (c->slot_stride < c->head_dim || (c->heads > 1 && c->head_stride < c->head_dim) ||
       (c->pages > 1 && c->page_stride < c->head_dim))
     return TQ_ERR_SHAPE;
@@ -221,7 +228,7 @@ int tq_qk_norm_rope(const void* Xq, int64_t xq_stride, const void* Xk, int64_t x
       k_heads > 65535 || head_dim < 2 || head_dim % 2 != 0 || head_dim > kMaxRopeDim)
     return TQ_ERR_SHAPE;
   for (int64_t s : {xq_stride, xk_stride, yq_stride, yk_stride})
-    if (!size_ok(s)) return TQ_ERR_SHAPE;
+    if (!size_ok(s) || !span_ok(ntok, s)) return TQ_ERR_SHAPE;
   if (!type_ok(x_type) || !type_ok(y_type)) return TQ_ERR_TYPE;
   if (ntok == 0 || q_heads + k_heads == 0) return TQ_OK;
   RopeCall c = {};
@@ -277,7 +284,7 @@ int tq_kv_append(const void* Xq, int64_t xq_stride, const void* Xk, int64_t xk_s
   if (rc != TQ_OK) return rc;
   if (ntok < 0 || ntok > 0x7fffffff || q_heads < 0 || q_heads > 65535) return TQ_ERR_SHAPE;
   for (int64_t s : {xq_stride, xk_stride, xv_stride, yq_stride})
-    if (!size_ok(s)) return TQ_ERR_SHAPE;
+    if (!size_ok(s) || !span_ok(ntok, s)) return TQ_ERR_SHAPE;
   if (!type_ok(x_type)) return TQ_ERR_TYPE;
   if (ntok == 0) return TQ_OK;
   const int64_t dim = kv->head_dim, xb = type_bytes(x_type);
@@ -368,7 +375,9 @@ int tq_paged_attention(const void* Q, int64_t q_stride, const tq_paged_kv* kv,
   const int64_t dim = kv->head_dim, row = q_heads * dim;
   rc = check_sizes(kv->nseq, ntok, q_heads, kv->heads, dim, max_q, max_kv, window);
   if (rc != TQ_OK) return rc;
-  if (!size_ok(q_stride) || !size_ok(o_stride) || !std::isfinite(scale)) return TQ_ERR_SHAPE;
+  if (!size_ok(q_stride) || !size_ok(o_stride) || !span_ok(ntok, q_stride) ||
+      !span_ok(ntok, o_stride) || !std::isfinite(scale))
+    return TQ_ERR_SHAPE;
   if (ntok > 1 && (q_stride < row || o_stride < row || q_stride % 8 != 0)) return TQ_ERR_SHAPE;
   if (!type_ok(o_type)) return TQ_ERR_TYPE;
   if (ntok == 0 || kv->nseq == 0) return TQ_OK;

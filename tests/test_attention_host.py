@@ -272,3 +272,18 @@ def test_ramp_ends(tq, rot, base, length, low, high, what):
         assert got == pytest.approx([x / factor for x in f], rel=1e-14)
     else:
         assert got == pytest.approx(ramp_rule(rot, base, factor, length, low, high), rel=1e-13)
+
+
+def test_spans_past_64_bits_refused(tq):
+    """Counts and strides that are each allowed, and buffers of more than 2^58 values that their product
+    would be (which the tests for overlap could not compute)."""
+    most = 1 << 40
+    assert qk(tq, n=(1 << 31) - 1, xqs=most) == tq.TQ_ERR_SHAPE
+    assert qk(tq, n=(1 << 31) - 1, yks=most) == tq.TQ_ERR_SHAPE
+    assert append(tq, n=(1 << 31) - 1, xvs=most) == tq.TQ_ERR_SHAPE
+    assert attend(tq, n=1 << 28, qs=most) == tq.TQ_ERR_SHAPE
+    assert attend(tq, n=1 << 28, os=most) == tq.TQ_ERR_SHAPE
+    for over in (dict(nseq=1 << 30, tstride=most), dict(pages=0x7ffffffe, ps=(1 << 39) - 8),
+                 dict(page=1 << 24, ss=(1 << 39) - 8)):
+        assert append(tq, kv=cache(tq, **over)) == tq.TQ_ERR_SHAPE
+        assert attend(tq, kv=cache(tq, **over)) == tq.TQ_ERR_SHAPE
