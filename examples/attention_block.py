@@ -23,9 +23,10 @@ I32 = torch.int32
 
 
 class AttentionBlock:
-    """y = x + Wo attention(Wqkv x), with the weights laid out once and the workspaces kept."""
+    """y = x + Wo attention(Wqkv x), with the weights laid out once and the workspaces kept. shapes:
+    the (tokens, most tokens of a sequence) of the calls to come."""
 
-    def __init__(self, width, q_heads, kv_heads, head_dim, max_tokens, max_kv, nseq, device="cuda"):
+    def __init__(self, width, q_heads, kv_heads, head_dim, shapes, max_kv, nseq, device="cuda"):
         self.width, self.hq, self.hk, self.dim = width, q_heads, kv_heads, head_dim
         self.rows = (q_heads + 2 * kv_heads) * head_dim
         self.out_cols = q_heads * head_dim
@@ -37,16 +38,16 @@ class AttentionBlock:
         # a context four times as long as the 4096 positions the rotation was made for
         turns, amplitude = tq.tq_rope_turns(head_dim, 1e6, tq.ROPE_RAMP, 4.0, 4096.0, 1.0, 32.0)
         self.rope = tq.Rope(turns.to(device), False, amplitude)
-        # buffers for up to max_tokens tokens
-        n = max_tokens
+        # buffers for the largest call, and one workspace for all of them (fewer tokens may need more)
+        n = max(t for t, _ in shapes)
         empty = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=device)  # noqa: E731
         self.qkv, self.att = empty(n, self.rows), empty(n, self.out_cols)
         self.q, self.y = empty(n, q_heads, head_dim, dtype=torch.bfloat16), empty(n, width)
         self.xq, self.aq = tq.q8K_empty(n, width, device), tq.q8K_empty(n, self.out_cols, device)
         need = max([tq.tq_paged_attention_workspace_bytes(nseq, t, q_heads, kv_heads, head_dim, m, max_kv)
-                    for t, m in ((n, n), (nseq, 1))] +
+                    for t, m in shapes] +
                    [tq.tq_matmul_workspace_bytes(r, c, t) for r, c in
-                    ((self.rows, width), (width, self.out_cols)) for t in (nseq, n)])
+                    ((self.rows, width), (width, self.out_cols)) for t, _ in shapes])
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
     def _weights(self, rows, cols, seed):
@@ -105,7 +106,8 @@ def run(seqs=4, prompt=300, steps=16, width=5120, q_heads=40, kv_heads=8, head_d
     g = torch.Generator(device=dev)
     g.manual_seed(seed)
     x = [torch.randn(n, width, generator=g, device=dev) for n in total]
-    block = AttentionBlock(width, q_heads, kv_heads, head_dim, sum(total), max(total), seqs)
+    shapes = [(sum(prompts), max(prompts)), (seqs, 1), (sum(total), max(total))]
+    block = AttentionBlock(width, q_heads, kv_heads, head_dim, shapes, max(total), seqs)
     table, pages = page_table(total, page_size, seed, dev)
 
     # the prompts, then a token of every sequence at a time

@@ -28,3 +28,12 @@ def test_steps_equal_whole_chunks(kw):
     # magnitude at most), and a value that lands on the other side of an int8 step moves by 1/127
     # of its block's largest: errors of a few percent of the rms of a sum over such values.
     assert off < 0.1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(seqs=5, prompt=300, steps=64, width=1024, q_heads=8, kv_heads=2),
+                                dict(seqs=3, prompt=600, steps=16, width=512, q_heads=4, kv_heads=4),
+                                dict(seqs=8, prompt=2, steps=3, width=512, q_heads=4, kv_heads=4)], ids=str)
+def test_workspace_of_every_call(kw):
+    """Batches whose prompts, or steps, need a larger workspace than all their tokens at once do."""
+    test_steps_equal_whole_chunks(kw)
