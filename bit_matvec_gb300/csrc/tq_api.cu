@@ -670,7 +670,7 @@ const char* tq_strerror(int code) {
     case TQ_ERR_CUDA: return "CUDA error (see tq_last_cuda_error)";
     case TQ_ERR_TIMEOUT: return "a kernel gave up a bounded wait";
     case TQ_ERR_ALIAS: return "output buffer overlaps an input";
-    case TQ_ERR_WORKSPACE: return "workspace smaller than tq_matmul_workspace_bytes";
+    case TQ_ERR_WORKSPACE: return "workspace smaller than the call needs (its ..._workspace_bytes function)";
     case TQ_ERR_INDEX: return "a kernel met a page, sequence or length out of range";
     case TQ_ERR_TYPE: return "element type not taken by this call";
     default: return "unknown error";

@@ -40,13 +40,13 @@ extern "C" {
 #endif
 
 #define TQ_OK            0
-#define TQ_ERR_SHAPE    -1  /* cols % 256 != 0, or a negative size */
+#define TQ_ERR_SHAPE    -1  /* a size is negative or not what the call asks for (cols % 256 != 0) */
 #define TQ_ERR_NULL     -2  /* a required pointer is NULL */
 #define TQ_ERR_ALIGN    -3  /* a buffer breaks its alignment rule */
 #define TQ_ERR_CUDA     -4  /* a CUDA launch or runtime call failed */
 #define TQ_ERR_TIMEOUT  -5  /* a kernel gave up a bounded wait (tq_device_status) */
 #define TQ_ERR_ALIAS    -6  /* an output buffer overlaps an input buffer */
-#define TQ_ERR_WORKSPACE -7 /* workspace smaller than tq_matmul_workspace_bytes */
+#define TQ_ERR_WORKSPACE -7 /* workspace smaller than the call needs (its ..._workspace_bytes) */
 #define TQ_ERR_INDEX    -8  /* a kernel met a page, sequence or length out of range */
 #define TQ_ERR_TYPE     -9  /* an element type this call does not take */
 

@@ -287,3 +287,8 @@ def test_spans_past_64_bits_refused(tq):
                  dict(page=1 << 24, ss=(1 << 39) - 8)):
         assert append(tq, kv=cache(tq, **over)) == tq.TQ_ERR_SHAPE
         assert attend(tq, kv=cache(tq, **over)) == tq.TQ_ERR_SHAPE
+
+
+def test_workspace_error_names_no_other_call(tq):
+    with_call = str(tq.TQError(tq.TQ_ERR_WORKSPACE, "tq_paged_attention"))
+    assert "workspace" in with_call and "matmul" not in with_call
