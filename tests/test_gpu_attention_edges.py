@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from attn_util import U, assert_within, attention, gather
-from test_gpu_attention import BF16, F16, F32, call, check, many_rows, problem
+from test_gpu_attention import BF16, BOTH, F16, F32, call, many_rows, problem
 
 pytestmark = pytest.mark.gpu
 BOTH_KERNELS = pytest.mark.parametrize("max_kv", [1, 10**8])
@@ -224,3 +224,31 @@ def test_first_cuda_call_of_a_host_thread(tq, max_kv):
     torch.cuda.synchronize()
     assert not errors, errors
     assert torch.equal(O, want) and torch.equal(L, want_lse)
+
+
+@pytest.mark.parametrize("nseq,max_kv", [(1, 1), (5, 1), (1, 10**8), (5, 10**8), (60, 10**8)])
+def test_no_new_tokens_in_any_sequence(tq, nseq, max_kv):
+    """Tokens of no sequence beside sequences of no new tokens: nothing is written, nothing reported."""
+    prob = list(problem([(20 * b, 0) for b in range(nseq)], 16, 1, 64, 16, F16))
+    prob[0] = torch.randn(300, 16, 64).to(F16)
+    assert many_rows(tq, prob[:4] + [torch.tensor([0, 300])] + prob[5:], max_kv) == (max_kv > 1)
+    O, L = call(tq, tuple(prob), F32, max_q=300, max_kv=max_kv)
+    assert torch.isnan(O).all() and torch.isnan(L).all()
+    assert tq.tq_device_status() == tq.TQ_OK
+
+
+@pytest.mark.parametrize("case", BOTH, ids=str)
+def test_both_kernels_give_the_same(tq, case):
+    """The same call planned for the kernel for few rows and for that for many: within the sum of their
+    bounds of one another, and the same rows see nothing."""
+    lens, hq, hk, dim, page, dtype, out, order = case
+    prob = problem(lens, hq, hk, dim, page, dtype, order=order)
+    assert not many_rows(tq, prob, 1) and many_rows(tq, prob, 10**8)
+    _, _, tol, tol_lse = attention(*prob[:6], dim ** -0.5, 0, out)
+    a, la = call(tq, prob, out, max_kv=1)
+    b, lb = call(tq, prob, out, max_kv=10**8)
+    assert ((a - b).double().abs().cpu() <= 2 * tol).all()
+    none = torch.isinf(la)
+    assert torch.equal(none, torch.isinf(lb))
+    assert ((la - lb).double().abs().cpu() <= 2 * tol_lse)[~none.cpu()].all()
+    assert tq.tq_device_status() == tq.TQ_OK
