@@ -242,7 +242,12 @@ attn_chunk_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
   extern __shared__ __align__(1024) uint8_t basep[];
   const uint32_t base = smem_u32(basep);
   if (base & 1023u) {   // the swizzled tiles need it, and there is no room to align
-    if (threadIdx.x == 0) *p.status = kDevTimeout;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+      *p.status = kDevTimeout;
+      static_cast<CutTile*>(p.cuts)[blockIdx.x] = {};   // nothing to join
+    }
     return;
   }
   // queries of the two softmaxes, then the ring, then the barriers
