@@ -189,7 +189,10 @@ AttnPlan attn_plan(int64_t nseq, int64_t ntok, int64_t q_heads, int64_t kv_heads
   // 163 and 89; 274 tokens of 8 heads on one over 521 positions 12 and 24; 8
   // ragged sequences of 16 heads on 4 and up to 1000 positions, 64 new tokens
   // 23 and 30, 200 new tokens 42 and 39; 200 single tokens and 2 x 16 over up to
-  // 500 positions 49 and 82.
+  // 500 positions 49 and 82. Of 105 shapes around the border, heads of 80 and 128
+  // lose at most 3.4% to the other kernel, heads of 64, whose times these are not,
+  // 27% and 13% in two of 35 (8 ragged sequences of 200 new tokens, 32 heads on
+  // 4, up to 1000 positions: 46 us where the few-row kernel takes 36).
   const double row_tiles = row_tiles_of(256);
   const double many_ns = 18500 + (rows > 128 ? 7500 : 0) +
                          row_tiles * ceil_div(span_of(256), 128) * (rows > 128 ? 1600 : 1300) / kPlanSms +

@@ -27,8 +27,9 @@ constexpr int kHalf = 128;            // rows of a softmax
 constexpr int kRows = 2 * kHalf;      // rows of a tile
 constexpr int kKeys = 128;            // keys of a tile
 // The cost of work, in units of about 0.4 us: a key tile of two halves, one of
-// up to 128 rows, starting and ending a row tile (1.6, 1.2 and 8 us measured at
-// dim 128), and the least work worth a block of its own.
+// up to 128 rows, starting and ending a row tile (1.6, 1.2 and about 7 us
+// measured at heads of 128, and taken for all), and the least work worth a block
+// of its own.
 constexpr int kCostTwo = 4, kCostAlt = 3, kTileCost = 18, kLeastWork = 12;
 
 TQ_HD int least(int a, int b) { return a < b ? a : b; }

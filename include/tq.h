@@ -512,7 +512,8 @@ int tq_kv_append(const void *Xq, int64_t xq_stride, const void *Xk, int64_t xk_s
  *   o = sum_j exp(s_j) v_j / sum_j exp(s_j),  s_j = scale * q . k_j
  * A token that sees nothing (p < 0), or whose every score is minus infinity,
  * gets zeros, and minus infinity as its lse. A query with a NaN gives NaN in its
- * row and its lse, an infinite one too unless all its scores are minus infinity.
+ * row and its lse, an infinite one too unless all its scores are minus infinity;
+ * with a scale of 0 every score is 0, whatever the query.
  *   Q   typed kv->type, head h of token t at Q + t * q_stride + h * head_dim;
  *       16-byte aligned, q_stride a multiple of 8.
  *   q_start int32 [nseq + 1], from 0, non-decreasing, at most ntok; kv_len int32 [nseq].
