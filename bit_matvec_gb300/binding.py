@@ -114,6 +114,9 @@ def _load():
             "tq_paged_attention": ([P, I64, P, P, P, P, I64, I, P, I64, I64, I64, I64, F, I64, P,
                                     I64, P], I),
             "tq_paged_attention_workspace_bytes": ([I64] * 8, I64),
+            "tq_lora_add": ([P, I64, I, P, P, P, I64, P, I64, I, I64, P, I64, P], I),
+            "tq_lora_add_workspace_bytes": ([I64, I64], I64),
+            "tq_sample": ([P, I64, I, I64, I64, P, P, P, P, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -330,7 +333,8 @@ def _calls():
         module.setup((torch.float32, torch.float16, torch.bfloat16, torch.int32),
                      torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                      tuple(ctypes.cast(f, ctypes.c_void_p).value for f in
-                           (lib.tq_qk_norm_rope, lib.tq_kv_append, lib.tq_paged_attention)))
+                           (lib.tq_qk_norm_rope, lib.tq_kv_append, lib.tq_paged_attention,
+                            lib.tq_lora_add, lib.tq_sample)))
         _call_module = module
     return _call_module
 
@@ -459,6 +463,74 @@ def tq_paged_attention(Q, kv: PagedKV, q_start, kv_len, O, max_q: int, max_kv: i
     rc = fn(*args)
     if rc:
         _finish(rc, "tq_paged_attention", Q, fn, args)
+
+
+# ---------------------------------------------------------------- adapters, sampling
+
+class Lora:
+    """Low-rank adapters of one matrix [rows][cols]: a [adapters][max_rank][cols] and
+    b [adapters][rows][max_rank], f16 or bf16, of any strides but unit last ones; rank int32 and
+    scale f32 [adapters], or None (all max_rank; 1). The tensors are used in place: write an
+    adapter's slot, its rank and its scale freely between calls."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [(n, ctypes.c_void_p) for n in ("a", "b", "rank", "scale")] + [
+            (n, ctypes.c_int64) for n in ("adapters", "max_rank", "rows", "cols", "a_stride",
+                                          "a_row_stride", "b_stride", "b_row_stride")] + [
+            ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, rank=None, scale=None):
+        if a.dim() != 3 or b.dim() != 3 or a.dtype != b.dtype or a.shape[0] != b.shape[0] or (
+                a.shape[1] != b.shape[2]):
+            raise ValueError("a must be [adapters][max_rank][cols] and b [adapters][rows][max_rank]")
+        if not (a.is_cuda and b.is_cuda):
+            raise ValueError("tensor must live on a CUDA device")
+        if any(t.shape[2] > 1 and t.stride(2) != 1 for t in (a, b)):
+            raise ValueError("the last dimension must be contiguous")
+        if rank is not None and (rank.dtype != torch.int32 or rank.numel() != a.shape[0]):
+            raise ValueError("rank must be int32 [adapters]")
+        if scale is not None and (scale.dtype != torch.float32 or scale.numel() != a.shape[0]):
+            raise ValueError("scale must be float32 [adapters]")
+        if any(t.device != a.device for t in (b, rank, scale) if t is not None):
+            raise ValueError("the tensors must be on one device")
+        self.a, self.b, self.rank, self.scale = a, b, rank, scale   # kept alive
+        count, top, cols = a.shape
+        rows = b.shape[1]
+
+        def stride(t, dim, least):   # of a dimension of one entry: any that is accepted
+            return t.stride(dim) if t.shape[dim] > 1 else least
+        self.struct = Lora._Struct(
+            a.data_ptr(), b.data_ptr(), _ptr(rank), _ptr(scale), count, top, rows, cols,
+            stride(a, 0, 0), stride(a, 1, 0), stride(b, 0, 0), stride(b, 1, 0), _type(a), 0)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def tq_lora_add_workspace_bytes(ntok: int, adapters: int) -> int:
+    n = _load().tq_lora_add_workspace_bytes(ntok, adapters)
+    if n < 0:
+        raise TQError(TQ_ERR_SHAPE, "tq_lora_add_workspace_bytes")
+    return int(n)
+
+
+def tq_lora_add(X, lora: Lora, ids, Y, Z=None, workspace=None, stream=None):
+    """Y[t] = Z[t] + the part of token t's adapter ids[t] (none if negative) in the product with
+    X[t]; Z may be Y, or None for zeros. X [tokens][cols], Y and Z [tokens][rows]."""
+    fn = (_call_module or _calls()).lora_add
+    args = (X, lora.ref, ids, Y, Z, workspace, stream)
+    rc = fn(*args)
+    if rc:
+        _finish(rc, "tq_lora_add", X, fn, args)
+
+
+def tq_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logp=None,
+              stream=None):
+    """tokens[t]: one token of each row of logits [tokens][vocab], drawn with the uniform number u[t]
+    after temperature, top-k, top-p and min-p of the row; logp[t]: the log of its probability."""
+    fn = (_call_module or _calls()).sample
+    args = (logits, u, tokens, temperature, top_k, top_p, min_p, logp, stream)
+    rc = fn(*args)
+    if rc:
+        _finish(rc, "tq_sample", logits, fn, args)
 
 
 def tq_strerror(code: int) -> str:

@@ -1,7 +1,8 @@
 /*
- * tq_call.c -- argument marshalling of the norm/rotation, append and attention
- * calls for Python, in C: for a few tokens these calls run for 2 to 8 us on the
- * GPU, and the same look at the tensors written in Python took 9.
+ * tq_call.c -- argument marshalling of the norm/rotation, append, attention,
+ * adapter and sampling calls for Python, in C: for a few tokens these calls run
+ * for 2 to 8 us on the GPU, and the same look at the tensors written in Python
+ * took 9.
  *
  * Each function takes the objects of the Python call, checks shapes, types and
  * placement, and calls the C ABI through the address setup() was given. It
@@ -30,9 +31,15 @@ typedef int (*append_fn)(const void *, int64_t, const void *, int64_t, const voi
 typedef int (*attend_fn)(const void *, int64_t, const tq_paged_kv *, const int32_t *,
                          const int32_t *, void *, int64_t, int, float *, int64_t, int64_t, int64_t,
                          int64_t, float, int64_t, void *, int64_t, void *);
+typedef int (*lora_fn)(const void *, int64_t, int, const tq_lora *, const int32_t *, const void *,
+                       int64_t, void *, int64_t, int, int64_t, void *, int64_t, void *);
+typedef int (*sample_fn)(const void *, int64_t, int, int64_t, int64_t, const float *, const float *,
+                         const int32_t *, const float *, const float *, int32_t *, float *, void *);
 static qk_fn call_qk;
 static append_fn call_append;
 static attend_fn call_attend;
+static lora_fn call_lora;
+static sample_fn call_sample;
 
 /* A [tokens][heads][head_dim] tensor. */
 typedef struct {
@@ -49,16 +56,18 @@ static int raise_value(const char *what) {
   return kRaised;
 }
 
-static int read_dims(PyObject *size, int64_t out[3]) {
+static int read_dims_of(PyObject *size, int64_t *out, int n) {
   if (!size) return kRaised;
-  if (!PyTuple_Check(size) || PyTuple_GET_SIZE(size) != 3) {
+  if (!PyTuple_Check(size) || PyTuple_GET_SIZE(size) != n) {
     Py_DECREF(size);
     return TQ_ERR_SHAPE;
   }
-  for (int i = 0; i < 3; ++i) out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(size, i));
+  for (int i = 0; i < n; ++i) out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(size, i));
   Py_DECREF(size);
   return PyErr_Occurred() ? kRaised : 0;
 }
+
+static int read_dims(PyObject *size, int64_t out[3]) { return read_dims_of(size, out, 3); }
 
 static int read_shape(PyObject *t, rows_t *r) {
   int64_t d[3] = {0, 0, 0};
@@ -110,6 +119,22 @@ static int read_rows(PyObject *t, rows_t *r) {
   return address(t, &r->p);
 }
 
+/* A [rows][values] tensor whose rows are contiguous: h is 1. */
+static int read_matrix(PyObject *t, rows_t *r) {
+  int64_t d[2], s[2];
+  int rc = read_dims_of(PyObject_GetAttr(t, n_shape), d, 2);
+  if (rc) return rc;
+  r->n = d[0];
+  r->h = 1;
+  r->d = d[1];
+  if ((rc = type_of(t, &r->type))) return rc;
+  if ((rc = on_cuda(t))) return rc;
+  if ((rc = read_dims_of(PyObject_CallMethodNoArgs(t, n_stride), s, 2))) return rc;
+  if (r->d > 1 && s[1] != 1) return raise_value("the values of a row must be contiguous");
+  r->stride = r->n > 1 ? s[0] : r->d;
+  return address(t, &r->p);
+}
+
 /* A contiguous vector of n values of a type, or None. */
 static int read_vector(PyObject *t, PyObject *dtype, int64_t n, void **p) {
   *p = NULL;
@@ -152,6 +177,26 @@ static int read_stream(PyObject *t, PyObject *stream, void **s) {
   if (!h) return kRaised;
   *s = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
+  return PyErr_Occurred() ? kRaised : 0;
+}
+
+/* A contiguous buffer of any type, or None, and its bytes. */
+static int read_workspace(PyObject *t, void **p, int64_t *bytes) {
+  *p = NULL;
+  *bytes = 0;
+  if (t == Py_None) return 0;
+  int rc = on_cuda(t);
+  if (rc) return rc;
+  PyObject *b = PyObject_CallMethodNoArgs(t, n_is_contiguous);
+  if (!b) return kRaised;
+  Py_DECREF(b);
+  if (b != Py_True) return raise_value("tensor must be contiguous");
+  if ((rc = address(t, p))) return rc;
+  PyObject *n = PyObject_CallMethodNoArgs(t, n_numel);
+  PyObject *e = n ? PyObject_CallMethodNoArgs(t, n_element_size) : NULL;
+  if (e) *bytes = PyLong_AsLongLong(n) * PyLong_AsLongLong(e);
+  Py_XDECREF(n);
+  Py_XDECREF(e);
   return PyErr_Occurred() ? kRaised : 0;
 }
 
@@ -261,7 +306,7 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
   TRY(read_rows(a[0], &q));
   TRY(read_rows(a[4], &o));
   CHECK(q.type == kv->type, TQ_ERR_TYPE);
-  void *start, *len, *ws = NULL, *lse, *stream;
+  void *start, *len, *ws, *lse, *stream;
   TRY(read_vector(a[2], dtype_i32, kv->nseq + 1, &start));
   TRY(read_vector(a[3], dtype_i32, kv->nseq, &len));
   TRY(read_vector(a[10], dtypes[0], q.n * q.h, &lse));
@@ -269,33 +314,65 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
   const double scale = PyFloat_AsDouble(a[7]);
   const int64_t window = PyLong_AsLongLong(a[9]);
   if (PyErr_Occurred()) return NULL;
-  int64_t ws_bytes = 0;
-  if (a[8] != Py_None) {
-    TRY(on_cuda(a[8]));
-    PyObject *b = PyObject_CallMethodNoArgs(a[8], n_is_contiguous);
-    if (!b) return NULL;
-    Py_DECREF(b);
-    if (b != Py_True) return result(raise_value("tensor must be contiguous"));
-    TRY(address(a[8], &ws));
-    PyObject *n = PyObject_CallMethodNoArgs(a[8], n_numel);
-    PyObject *e = n ? PyObject_CallMethodNoArgs(a[8], n_element_size) : NULL;
-    if (e) ws_bytes = PyLong_AsLongLong(n) * PyLong_AsLongLong(e);
-    Py_XDECREF(n);
-    Py_XDECREF(e);
-    if (PyErr_Occurred()) return NULL;
-  }
+  int64_t ws_bytes;
+  TRY(read_workspace(a[8], &ws, &ws_bytes));
   TRY(read_stream(a[0], a[11], &stream));
   return result(call_attend(q.p, q.stride, kv, start, len, o.p, o.stride, o.type, lse, q.n, q.h, max_q,
                             max_kv, (float)scale, window, ws, ws_bytes, stream));
 }
 
-/* ((float32, float16, bfloat16, int32), get_device, current_stream, (three addresses)) */
+/* (X, lora, ids, Y, Z, workspace, stream) */
+static PyObject *lora_add(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+  (void)self;
+  if (nargs != 7) return PyErr_Format(PyExc_TypeError, "7 arguments expected");
+  rows_t x = {0}, y = {0}, z = {0};
+  void *lp;
+  TRY(read_address(a[1], &lp));
+  const tq_lora *l = lp;
+  const int base = a[4] != Py_None;
+  TRY(read_matrix(a[0], &x));
+  TRY(read_matrix(a[3], &y));
+  CHECK(x.n == y.n && x.d == l->cols && y.d == l->rows, TQ_ERR_SHAPE);
+  if (base) {
+    TRY(read_matrix(a[4], &z));
+    CHECK(same_shape(&z, &y), TQ_ERR_SHAPE);
+    CHECK(z.type == y.type, TQ_ERR_TYPE);
+  }
+  void *ids, *ws, *stream;
+  int64_t ws_bytes;
+  TRY(read_vector(a[2], dtype_i32, x.n, &ids));
+  TRY(read_workspace(a[5], &ws, &ws_bytes));
+  TRY(read_stream(a[0], a[6], &stream));
+  return result(call_lora(x.p, x.stride, x.type, l, ids, z.p, z.stride, y.p, y.stride, y.type, x.n, ws,
+                          ws_bytes, stream));
+}
+
+/* (logits, u, tokens, temperature, top_k, top_p, min_p, logp, stream) */
+static PyObject *sample(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+  (void)self;
+  if (nargs != 9) return PyErr_Format(PyExc_TypeError, "9 arguments expected");
+  rows_t x = {0};
+  TRY(read_matrix(a[0], &x));
+  void *u, *tokens, *temperature, *top_k, *top_p, *min_p, *logp, *stream;
+  TRY(read_vector(a[1], dtypes[0], x.n, &u));
+  TRY(read_vector(a[2], dtype_i32, x.n, &tokens));
+  TRY(read_vector(a[3], dtypes[0], x.n, &temperature));
+  TRY(read_vector(a[4], dtype_i32, x.n, &top_k));
+  TRY(read_vector(a[5], dtypes[0], x.n, &top_p));
+  TRY(read_vector(a[6], dtypes[0], x.n, &min_p));
+  TRY(read_vector(a[7], dtypes[0], x.n, &logp));
+  TRY(read_stream(a[0], a[8], &stream));
+  return result(call_sample(x.p, x.stride, x.type, x.n, x.d, u, temperature, top_k, top_p, min_p, tokens,
+                            logp, stream));
+}
+
+/* ((float32, float16, bfloat16, int32), get_device, current_stream, (five addresses)) */
 static PyObject *setup(PyObject *self, PyObject *args) {
   (void)self;
   PyObject *types[4], *dev, *str;
-  unsigned long long fn[3];
-  if (!PyArg_ParseTuple(args, "(OOOO)OO(KKK)", &types[0], &types[1], &types[2], &types[3], &dev, &str,
-                        &fn[0], &fn[1], &fn[2]))
+  unsigned long long fn[5];
+  if (!PyArg_ParseTuple(args, "(OOOO)OO(KKKKK)", &types[0], &types[1], &types[2], &types[3], &dev, &str,
+                        &fn[0], &fn[1], &fn[2], &fn[3], &fn[4]))
     return NULL;
   for (int i = 0; i < 3; ++i) {
     Py_INCREF(types[i]);
@@ -310,6 +387,8 @@ static PyObject *setup(PyObject *self, PyObject *args) {
   call_qk = (qk_fn)(uintptr_t)fn[0];
   call_append = (append_fn)(uintptr_t)fn[1];
   call_attend = (attend_fn)(uintptr_t)fn[2];
+  call_lora = (lora_fn)(uintptr_t)fn[3];
+  call_sample = (sample_fn)(uintptr_t)fn[4];
   Py_RETURN_NONE;
 }
 
@@ -318,6 +397,8 @@ static PyMethodDef methods[] = {
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, NULL},
     {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, NULL},
+    {"lora_add", (PyCFunction)(void (*)(void))lora_add, METH_FASTCALL, NULL},
+    {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tq_call", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

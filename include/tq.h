@@ -555,6 +555,97 @@ int64_t tq_paged_attention_workspace_bytes(int64_t nseq, int64_t ntok, int64_t q
                                            int64_t kv_heads, int64_t head_dim, int64_t max_q,
                                            int64_t max_kv, int64_t window);
 
+/* ------------------------------------------------------------------------
+ * What differs from request to request beside the shared products: low-rank
+ * adapters, and the draw of the next token.
+ */
+
+/*
+ * Low-rank adapters of one matrix [rows][cols]: adapter i adds
+ * scale[i] * B_i A_i to it. Value k of row j of A_i is at
+ *   a + i * a_stride + j * a_row_stride + k,    j < rank[i], k < cols
+ * and value j of row n of B_i at
+ *   b + i * b_stride + n * b_row_stride + j,    n < rows, j < rank[i]
+ * (elements). What lies in a row of A or B past the adapter's rank may hold
+ * anything and is not used.
+ */
+typedef struct {
+    const void *a;         /* device, typed, 16-byte aligned */
+    const void *b;         /* device, typed, aligned to its element */
+    const int32_t *rank;   /* device, [adapters], 0 .. max_rank; NULL: all max_rank */
+    const float *scale;    /* device, [adapters]; NULL: 1 */
+    int64_t adapters;      /* 0 .. 32768 */
+    int64_t max_rank;      /* 0 .. 256 */
+    int64_t rows, cols;    /* cols a multiple of 8; both at most 2^24 */
+    int64_t a_stride, a_row_stride;   /* multiples of 8 */
+    int64_t b_stride, b_row_stride;
+    int32_t type;          /* TQ_F16 or TQ_BF16 */
+    int32_t reserved;      /* 0 */
+} tq_lora;
+
+/*
+ * tq_lora_add -- the adapters' part of a product of several requests' tokens:
+ *   Y[t] = Z[t] + scale[i] * B_i (A_i x[t]),  i = ids[t];  Y[t] = Z[t] if ids[t] < 0.
+ * Tokens of one adapter may stand anywhere; its weights are shared by them.
+ *   X    typed x_type, [ntok][cols] with stride x_stride, 16-byte aligned, a
+ *        row's bytes a multiple of 16: TQ_F32, or the adapters' type.
+ *   ids  int32 [ntok].
+ *   Z    typed y_type, [ntok][rows] with stride z_stride; may be Y (the same
+ *        pointer and stride: rows without adapter are then left as they are),
+ *        must not overlap it otherwise; NULL: zeros.
+ *   Y    typed y_type, [ntok][rows] with stride y_stride, aligned to its element.
+ *   workspace  tq_lora_add_workspace_bytes(ntok, adapters) bytes, 16-byte
+ *        aligned; contents overwritten and meaningless after the call; calls
+ *        that share it must be ordered.
+ * A token whose adapter, or its rank, is out of range gets Z alone, and
+ * tq_device_status() then returns TQ_ERR_INDEX.
+ * Products are good to 2^-21 of their value whatever the types, sums are
+ * 32-bit floats, and Y is rounded once.
+ * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
+ * TQ_ERR_WORKSPACE.
+ */
+int tq_lora_add(const void *X, int64_t x_stride, int x_type, const tq_lora *lora,
+                const int32_t *ids, const void *Z, int64_t z_stride, void *Y, int64_t y_stride,
+                int y_type, int64_t ntok, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Scratch of tq_lora_add: the tokens in the order of their adapters; 0 up to
+ * 256 tokens. Grows with both sizes. -1 for sizes it refuses. */
+int64_t tq_lora_add_workspace_bytes(int64_t ntok, int64_t adapters);
+
+/*
+ * tq_sample -- one token of each row of logits, drawn with one given uniform
+ * number a row. With m the row's largest logit, w_i = exp((l_i - m) / T), and
+ * the tokens in the order of falling logits, equal ones by rising index:
+ *   n_k = top_k, or all if top_k <= 0 or >= vocab
+ *   n_p = the least n whose first n weights sum to top_p times the sum of the
+ *         first n_k at least; all if not top_p < 1
+ *   n_m = the number of weights >= min_p; all if not min_p > 0
+ * the first min(n_k, n_p, n_m) tokens, at least one, are kept, and the token is
+ * the least i for which the kept weights up to index i sum to more than u times
+ * the sum of all of them. A temperature of 0 (or below 2^-100) takes the
+ * largest logit, the lowest index of equal ones.
+ *   logits       typed, [ntok][vocab] with row stride `stride` (elements),
+ *                aligned to its element; 1 <= vocab <= 262144.
+ *   u            f32 [ntok], in [0, 1); lower ones and NaN count as 0, higher
+ *                ones as the number just below 1.
+ *   temperature  f32 [ntok], NULL: 1.   top_k  int32 [ntok], NULL: off.
+ *   top_p        f32 [ntok], NULL: off. min_p  f32 [ntok], NULL: off.
+ *   tokens       int32 [ntok], written.
+ *   logp         f32 [ntok], the log of the probability that the token was
+ *                drawn with, w / (sum of the kept weights); 0 for a
+ *                temperature of 0. NULL: not written.
+ * Logits of minus infinity are never drawn; beside a plus infinity all others
+ * count as that. A row with a NaN or without any logit above minus infinity, or
+ * whose temperature is negative or not finite, gets token -1 and a NaN as logp.
+ * The weights are 2^-45 units in 64-bit sums, each good to 2^-36 of its value:
+ * sums do not depend on their order, and a border between two tokens is where
+ * the exact sums have it but for 2^-35 of the total.
+ * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS.
+ */
+int tq_sample(const void *logits, int64_t stride, int type, int64_t ntok, int64_t vocab,
+              const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, int32_t *tokens, float *logp, void *stream);
+
 /* Human-readable name of a TQ_* code. */
 const char *tq_strerror(int code);
 

@@ -1,0 +1,135 @@
+"""Host side of the adapter and sampling calls: workspace sizes and refusals, which return before any
+CUDA call (fake addresses are safe)."""
+import ctypes
+
+import pytest
+import torch
+
+A, B, C, D, E, G, H, W = (0x7F0000000000 + i * 0x10000000 for i in range(8))
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from bit_matvec_gb300 import build
+    build.build()
+    import bit_matvec_gb300
+    return bit_matvec_gb300
+
+
+def lora(tq, **over):
+    a = dict(a=A, b=B, rank=C, scale=C + 4096, adapters=4, top=16, rows=100, cols=64, as_=1024, ars=64,
+             bs=1600, brs=16, type=2)
+    a.update(over)
+    s = tq.Lora._Struct(a["a"], a["b"], a["rank"], a["scale"], a["adapters"], a["top"], a["rows"],
+                        a["cols"], a["as_"], a["ars"], a["bs"], a["brs"], a["type"], 0)
+    return s, ctypes.addressof(s)
+
+
+def add(tq, struct=None, **over):
+    a = dict(x=D, xs=64, xt=0, ids=E, z=G, zs=100, y=H, ys=100, yt=0, n=3, ws=W, wsb=1 << 20)
+    a.update(over)
+    keep, ref = struct or lora(tq)
+    return tq.library().tq_lora_add(a["x"], a["xs"], a["xt"], ref, a["ids"], a["z"], a["zs"], a["y"],
+                                    a["ys"], a["yt"], a["n"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(adapters=-1), "SHAPE"), (dict(adapters=32769), "SHAPE"), (dict(top=-1), "SHAPE"),
+    (dict(top=257, brs=257), "SHAPE"), (dict(rows=-1), "SHAPE"), (dict(rows=(1 << 24) + 1), "SHAPE"),
+    (dict(cols=60), "SHAPE"), (dict(cols=-8), "SHAPE"), (dict(cols=1 << 25), "SHAPE"),
+    (dict(as_=-8), "SHAPE"), (dict(as_=1028), "SHAPE"), (dict(ars=68), "SHAPE"), (dict(ars=56), "SHAPE"),
+    (dict(brs=15), "SHAPE"), (dict(bs=-1), "SHAPE"), (dict(as_=2 * BIG), "SHAPE"),
+    (dict(adapters=32768, bs=BIG), "OK"), (dict(rows=1 << 24, brs=BIG), "SHAPE"),
+    (dict(type=0), "TYPE"), (dict(type=3), "TYPE"), (dict(a=None), "NULL"), (dict(b=None), "NULL"),
+    (dict(a=A + 8), "ALIGN"), (dict(b=B + 1), "ALIGN"), (dict(rank=C + 2), "ALIGN"),
+    (dict(scale=C + 1), "ALIGN"),
+])
+def test_lora_description_refusals(tq, over, code):
+    # (no tokens: what is allowed enqueues nothing)
+    want = getattr(tq, "TQ_" + code if code == "OK" else "TQ_ERR_" + code)
+    assert add(tq, struct=lora(tq, **over), **(dict(n=0) if code == "OK" else {})) == want
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n=-1), "SHAPE"), (dict(n=1 << 31), "SHAPE"), (dict(xs=56), "SHAPE"), (dict(xs=66), "SHAPE"),
+    (dict(ys=99), "SHAPE"), (dict(zs=99), "SHAPE"), (dict(xs=-64), "SHAPE"), (dict(ys=2 * BIG), "SHAPE"),
+    (dict(n=(1 << 31) - 1, ys=BIG), "SHAPE"), (dict(xt=1), "TYPE"), (dict(xt=5), "TYPE"),
+    (dict(yt=3), "TYPE"), (dict(yt=-1), "TYPE"), (dict(x=None), "NULL"), (dict(ids=None), "NULL"),
+    (dict(y=None), "NULL"), (dict(x=D + 8), "ALIGN"), (dict(ids=E + 2), "ALIGN"), (dict(y=H + 2), "ALIGN"),
+    (dict(z=G + 1), "ALIGN"), (dict(y=D), "ALIAS"), (dict(y=A), "ALIAS"), (dict(y=B + 64), "ALIAS"),
+    (dict(y=C), "ALIAS"), (dict(y=C + 4096), "ALIAS"), (dict(y=E), "ALIAS"), (dict(y=G + 4), "ALIAS"),
+    (dict(y=G, ys=104), "ALIAS"), (dict(y=G + 100 * 4), "ALIAS"),
+])
+def test_lora_refusals(tq, over, code):
+    assert add(tq, **over) == getattr(tq, "TQ_ERR_" + code)
+
+
+def test_lora_nothing_to_do(tq):
+    assert add(tq, n=0, x=None, y=None, ids=None) == tq.TQ_OK
+    assert add(tq, struct=lora(tq, rows=0)) == tq.TQ_OK
+    assert tq.library().tq_lora_add(D, 64, 0, None, E, G, 100, H, 100, 0, 3, W, 1 << 20,
+                                    None) == tq.TQ_ERR_NULL
+
+
+def test_lora_workspace(tq):
+    assert tq.tq_lora_add_workspace_bytes(0, 0) == tq.tq_lora_add_workspace_bytes(256, 32768) == 0
+    sizes = [tq.tq_lora_add_workspace_bytes(n, 64) for n in (257, 1000, 8192, 1 << 20)]
+    assert sizes == sorted(sizes)
+    # some bytes a token and an adapter
+    assert tq.tq_lora_add_workspace_bytes(1 << 20, 32768) <= 32 * ((1 << 20) + 32768)
+    for bad in ((-1, 4), (5, -1), (1 << 31, 4), (5, 32769)):
+        with pytest.raises(tq.TQError):
+            tq.tq_lora_add_workspace_bytes(*bad)
+
+
+def test_lora_class(tq):
+    a, b = torch.zeros(2, 4, 8, dtype=torch.float16), torch.zeros(2, 5, 4, dtype=torch.float16)
+    for bad in ((a, b), (a[0], b), (a, b.bfloat16()), (a, b[:, :, :3]), (a[:1], b)):
+        with pytest.raises(ValueError):   # the first: not on a GPU
+            tq.Lora(*bad)
+
+
+def draw(tq, **over):
+    a = dict(x=A, stride=1000, type=0, n=3, vocab=1000, u=B, t=C, k=C + 4096, p=C + 8192, m=C + 12288,
+             tokens=D, logp=E)
+    a.update(over)
+    return tq.library().tq_sample(a["x"], a["stride"], a["type"], a["n"], a["vocab"], a["u"], a["t"],
+                                  a["k"], a["p"], a["m"], a["tokens"], a["logp"], None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n=-1), "SHAPE"), (dict(n=1 << 31), "SHAPE"), (dict(vocab=0), "SHAPE"),
+    (dict(vocab=262145, stride=262145), "SHAPE"), (dict(stride=999), "SHAPE"), (dict(stride=-1), "SHAPE"),
+    (dict(stride=2 * BIG), "SHAPE"), (dict(n=(1 << 31) - 1, stride=BIG), "SHAPE"), (dict(type=3), "TYPE"),
+    (dict(x=None), "NULL"), (dict(u=None), "NULL"), (dict(tokens=None), "NULL"), (dict(x=A + 2), "ALIGN"),
+    (dict(x=A + 1, type=1), "ALIGN"), (dict(u=B + 1), "ALIGN"), (dict(t=C + 2), "ALIGN"),
+    (dict(k=C + 2), "ALIGN"), (dict(p=C + 3), "ALIGN"), (dict(m=C + 1), "ALIGN"),
+    (dict(tokens=D + 2), "ALIGN"), (dict(logp=E + 2), "ALIGN"), (dict(tokens=A + 8), "ALIAS"),
+    (dict(logp=B), "ALIAS"), (dict(tokens=E), "ALIAS"), (dict(logp=C + 8196), "ALIAS"),
+])
+def test_sample_refusals(tq, over, code):
+    assert draw(tq, **over) == getattr(tq, "TQ_ERR_" + code)
+
+
+def test_sample_nothing_to_do(tq):
+    assert draw(tq, n=0, x=None, u=None, tokens=None) == tq.TQ_OK
+
+
+def test_marshalling(tq):
+    """What the C marshalling refuses before it looks for a GPU."""
+    calls = __import__("bit_matvec_gb300.binding", fromlist=["_calls"])._calls()
+    x = torch.zeros(3, 64)
+    for bad in ([], [x] * 3, [None] * 11):
+        with pytest.raises(TypeError):
+            calls.lora_add(*bad)
+        with pytest.raises(TypeError):
+            calls.sample(*bad)
+    with pytest.raises(ValueError):   # not on a GPU
+        tq.tq_sample(x, x, x)
+    with pytest.raises(tq.TQError) as e:
+        tq.tq_sample(torch.zeros(3, 2, 64), x, x)
+    assert e.value.code == tq.TQ_ERR_SHAPE
+    with pytest.raises(tq.TQError) as e:
+        tq.tq_sample(x.double(), x, x)
+    assert e.value.code == tq.TQ_ERR_TYPE
