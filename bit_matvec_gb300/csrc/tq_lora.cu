@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kTile = 32;          // tokens of a tile: two row blocks of 16
+constexpr int kChain = 4;          // chunks of 32 columns that are summed on the tensor cores
 constexpr int kInBlock = 256;      // tokens up to which every block finds its tile itself
 constexpr int kGroupThreads = 1024;
 static_assert(kInBlock == kThreads, "a thread a token");
@@ -44,7 +45,7 @@ struct Args {
   int b_vec;             // rows of B in 8-byte pieces
   // more than kInBlock tokens: the tiles, from the grouping kernel
   const int32_t* order;  // tokens by adapter
-  const int4* tiles;     // adapter, first of order, tokens
+  const int4* tiles;     // adapter, its rank, first of order, tokens
   const int* ntiles;
   int* status;
 };
@@ -110,30 +111,47 @@ __device__ __forceinline__ uint16_t down(float v, int type) {
   return type == TQ_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// n of eight consecutive values from `at` on (vec: the address is a multiple of 16 bytes).
-__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int n, bool vec, float (&v)[8]) {
+// n of eight consecutive values from `at` on, as they are (vec: the address is a multiple of 16
+// bytes), and as floats.
+struct Raw8 {
+  uint4 v[2];
+};
+__device__ __forceinline__ Raw8 load8(const void* p, int type, int64_t at, int n, bool vec) {
+  Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   if (type == TQ_F32) {
-    const float* f = static_cast<const float*>(p) + at;
+    const uint32_t* f = static_cast<const uint32_t*>(p) + at;
     if (vec && n == 8) {
-      const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      return;
-    }
+      r.v[0] = *reinterpret_cast<const uint4*>(f);
+      r.v[1] = *reinterpret_cast<const uint4*>(f + 4);
+    } else {
+      uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? f[e] : 0.0f;
-    return;
+      for (int e = 0; e < 8; ++e) w[e] = e < n ? f[e] : 0u;
+      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return r;
   }
   const uint16_t* h = static_cast<const uint16_t*>(p) + at;
-  uint16_t w[8];
   if (vec && n == 8) {
-    *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(h);
+    r.v[0] = *reinterpret_cast<const uint4*>(h);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = e < n ? h[e] : 0u;
+    r.v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  return r;
+}
+__device__ __forceinline__ void floats8(const Raw8& r, int type, float (&v)[8]) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+  if (type == TQ_F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = e < n ? h[e] : (uint16_t)0;
+    for (int e = 0; e < 8; ++e) v[e] = up((uint16_t)(w[e >> 1] >> (16 * (e & 1))), type);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = up(w[e], type);
 }
 __device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, bool vec, const float (&v)[8]) {
   if (type == TQ_F32) {
@@ -163,22 +181,22 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, boo
 
 // ---------------------------------------------------------------- tiles
 
-// The adapter that a token uses, -1 for none; `bad` if it is out of range.
-__device__ __forceinline__ int effective(const Args& p, int id, bool& bad) {
+// The adapter that a token uses, -1 for none, and its rank; `bad` if it is out of range.
+__device__ __forceinline__ int effective(const Args& p, int id, int& rank, bool& bad) {
   bad = false;
+  rank = 0;
   if (id < 0) return -1;
   if (id >= p.l.adapters) {
     bad = true;
     return -1;
   }
-  if (!p.l.rank) return p.l.max_rank > 0 ? id : -1;
-  const int r = __ldg(p.l.rank + id);
-  bad = r < 0 || r > p.l.max_rank;
-  return bad || r == 0 ? -1 : id;
+  rank = p.l.rank ? __ldg(p.l.rank + id) : (int)p.l.max_rank;
+  bad = rank < 0 || rank > p.l.max_rank;
+  return bad || rank == 0 ? -1 : id;
 }
 
 struct Tile {
-  int adapter, count;
+  int adapter, rank, count;
 };
 
 // Up to kInBlock tokens: tile number `want` of the call, its tokens into tok;
@@ -186,9 +204,9 @@ struct Tile {
 // token's place among those of its adapter is the number of them before it.
 __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, int* tok, int* ids, int* red) {
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  int id = -2;
+  int id = -2, rank = 0;
   bool bad = false;
-  if (i < p.ntok) id = effective(p, p.ids[i], bad);
+  if (i < p.ntok) id = effective(p, p.ids[i], rank, bad);
   if (bad && report) atomicMax(p.status, kDevIndex);
   ids[i] = id;
   __syncthreads();
@@ -208,19 +226,20 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, 
   if (first && number == want) {
     red[kWarps] = id;
     red[kWarps + 1] = before;
-    red[kWarps + 2] = 0;
+    red[kWarps + 2] = rank;
+    red[kWarps + 3] = 0;
   }
   __syncthreads();
   int total = 0;
   for (int w = 0; w < kWarps; ++w) total += red[w];
-  if (want >= total) return {-1, 0};
+  if (want >= total) return {-1, 0, 0};
   const int adapter = red[kWarps], from = red[kWarps + 1];
   const bool mine = id == adapter && before >= from && before < from + kTile;
   if (mine) tok[before - from] = i;
   const int n = __popc(__ballot_sync(0xffffffffu, mine));
-  if (lane == 0 && n) atomicAdd(&red[kWarps + 2], n);
+  if (lane == 0 && n) atomicAdd(&red[kWarps + 3], n);
   __syncthreads();
-  return {adapter, red[kWarps + 2]};
+  return {adapter, red[kWarps + 2], red[kWarps + 3]};
 }
 
 // More tokens: their order by adapter and the tiles, by one thread block.
@@ -241,7 +260,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
   pdl_launch_dependents();
   auto group_of = [&](int i, bool report) {
     bool bad;
-    const int id = effective(p, p.ids[i], bad);
+    int rank;
+    const int id = effective(p, p.ids[i], rank, bad);
     if (bad && report) atomicMax(p.status, kDevIndex);
     return id < 0 ? (p.copy ? groups - 1 : -1) : id;
   };
@@ -285,8 +305,10 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
     if (tid == 0) total = make_int2(base.x + sum.x, base.y + sum.y);
     if (g < groups) {
       counts[g] = at.x;
+      const int id = g == groups - 1 ? -1 : g;
+      const int rank = id < 0 || n == 0 ? 0 : p.l.rank ? __ldg(p.l.rank + id) : (int)p.l.max_rank;
       for (int k = 0; k * kTile < n; ++k)
-        tiles[at.y + k] = make_int4(g == groups - 1 ? -1 : g, at.x + k * kTile, min(kTile, n - k * kTile), 0);
+        tiles[at.y + k] = make_int4(id, rank, at.x + k * kTile, min(kTile, n - k * kTile));
     }
     __syncthreads();
   }
@@ -319,27 +341,71 @@ __device__ __forceinline__ float4 load_remote(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Shared memory (4-byte words) before the results, and for adapters of up to `top` rows of A, in blocks of
-// `block`: the partial h of this block's columns, and the eight warps' parts of
-// it, whose place the split h takes afterwards.
+// Shared memory in 4-byte words, for adapters of up to `top` rows of A in blocks of `block`: the
+// tile's description, the partial h of this block's columns, and the eight warps' parts of it, whose
+// place the split h takes afterwards.
 constexpr int kHeadInts = kThreads + kTile + 16;
 __host__ __device__ constexpr int rank16(int top) { return (top + 15) / 16 * 16; }
 __host__ __device__ constexpr int part_floats(int top) { return kTile * rank16(top); }
 __host__ __device__ constexpr int work_floats(int top, int block) {
-  const int warps = kWarps * kTile * block, h = 2 * kTile * rank16(top);
+  const int warps = kWarps * 16 * block, h = 2 * kTile * rank16(top);
   return warps > h ? warps : h;
 }
 
-// NT: row blocks of 8 of A that a warp takes at a time.
+// What a warp needs of 32 rows of B and Y for 16 tokens, beside h: a thread's values of B for up to
+// 16 KG values of h, and of Z for its two tokens and eight rows.
+template <typename TW, int KG> struct Unit {
+  uint2 w[KG][4];
+  Raw8 z[2];
+  int64_t out;    // the first of its eight rows of Y
+  int some;       // how many of them there are
+
+  // Column g of block i is row 8 (g / 2) + 2 i + g % 2, so that a thread's results are consecutive rows.
+  __device__ __forceinline__ void load_b(const Args& p, const TW* B, int64_t n0, int k0, int rank, int g, int t) {
+#pragma unroll
+    for (int q = 0; q < KG; ++q) {
+      const int k = k0 + 16 * q + 4 * t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+        const TW* const b = B + n * p.l.b_row_stride + k;
+        w[q][i] = make_uint2(0, 0);
+        if (p.b_vec && k + 4 <= rank && n < p.l.rows) {
+          w[q][i] = __ldg(reinterpret_cast<const uint2*>(b));
+        } else if (n < p.l.rows && k < rank) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
+          w[q][i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void load_z(const Args& p, int64_t n0, const int (&token)[2], int t) {
+    out = n0 + 8 * t;
+    some = (int)max((int64_t)0, min((int64_t)8, p.l.rows - out));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (p.z && token[h] >= 0 && some > 0) {
+        z[h] = load8(p.z, p.y_type, token[h] * p.z_stride + out, some, p.z_vec);
+      } else {
+        z[h].v[0] = z[h].v[1] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+};
+
+// NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns.
 template <typename TX, typename TW, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NT <= 4 ? 3 : 2)
 lora_kernel(const __grid_constant__ Args p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
-  constexpr int kBlock = 8 * NT;
+  constexpr int kBlock = 8 * NT, KG = NT / 2;
   extern __shared__ float4 shared4[];
   int* const s_ids = reinterpret_cast<int*>(shared4);                // [kThreads]
   int* const s_tok = s_ids + kThreads;                               // [kTile]
-  int* const s_red = s_tok + kTile;                                  // [kWarps + 3]
+  int* const s_red = s_tok + kTile;                                  // [kWarps + 4]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t crank = cluster_rank();
   const int unit = blockIdx.x / kCluster, want = unit / p.splits, part_of = unit % p.splits;
@@ -350,14 +416,14 @@ lora_kernel(const __grid_constant__ Args p) {
   if (p.tiles) {
     if (want >= *p.ntiles) return;
     const int4 q = p.tiles[want];
-    tile = {q.x, q.z};
-    if (tid < q.z) s_tok[tid] = p.order[q.y + tid];
+    tile = {q.x, q.y, q.w};
+    if (tid < q.w) s_tok[tid] = p.order[q.z + tid];
     __syncthreads();
   } else {
     tile = find_tile(p, want, blockIdx.x == 0, s_tok, s_ids, s_red);
     if (tile.count == 0) return;
   }
-  const int count = tile.count;
+  const int count = tile.count, rank = tile.rank;
   // rows of B and Y of this thread block, in units of 32
   const int64_t rows = p.l.rows, units = (rows + 31) / 32, shares = (int64_t)p.splits * kCluster;
   const int64_t share = (int64_t)part_of * kCluster + crank;
@@ -377,106 +443,113 @@ lora_kernel(const __grid_constant__ Args p) {
     }
     return;
   }
-  const int rank = p.l.rank ? __ldg(p.l.rank + tile.adapter) : (int)p.l.max_rank;
   const float scale = p.l.scale ? __ldg(p.l.scale + tile.adapter) : 1.0f;
   const int wide = rank16(rank);          // values of h a token, with zeros behind the rank
-  const int mblocks = count > 16 ? 2 : 1;
+  // up to 16 tokens: all warps take them; more: half of the warps each 16
+  const int mblocks = count > 16 ? 2 : 1, m = mblocks == 2 ? warp >> 2 : 0;
+  const int turn = mblocks == 2 ? warp & 3 : warp, turns = kWarps / mblocks;
   float* const part = reinterpret_cast<float*>(shared4) + kHeadInts; // [kTile][wide]
-  float* const work = part + part_floats((int)p.l.max_rank);         // [kWarps][kTile][kBlock], then h
+  float* const work = part + part_floats((int)p.l.max_rank);         // [kWarps][16][kBlock], then h
+  const int token[2] = {16 * m + g < count ? s_tok[16 * m + g] : -1,
+                        16 * m + 8 + g < count ? s_tok[16 * m + 8 + g] : -1};
 
   // ---- h = A x over this block's columns
   const TW* const A = static_cast<const TW*>(p.l.a) + tile.adapter * p.l.a_stride;
   const int cols = (int)p.l.cols, chunks = (cols + 31) / 32;
   const int chunk0 = (int)((int64_t)chunks * crank / kCluster), chunk1 = (int)((int64_t)chunks * (crank + 1) / kCluster);
-  const TX* x[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = 16 * m + 8 * h + g;
-      x[m][h] = j < count ? static_cast<const TX*>(p.x) + s_tok[j] * p.x_stride : nullptr;
-    }
+  const TX* const x0 = static_cast<const TX*>(p.x) + token[0] * p.x_stride;
+  const TX* const x1 = static_cast<const TX*>(p.x) + token[1] * p.x_stride;
   for (int r0 = 0; r0 < rank; r0 += kBlock) {
-    float acc[2][NT][4];
+    float acc[NT][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+    const TW* const Ar = A + (r0 + g) * p.l.a_row_stride;
+    if (r0 > 0) __syncthreads();
+    // The tensor cores cut their sums where 32-bit additions round, which leans
+    // one way: after a few chunks the sum goes to this thread's place in shared
+    // memory, by an addition that rounds (256 of 2176 columns a warp's chain
+    // long, rank 256: 2.2e-6 of the result; without, 3.3e-6).
+    float* const mine = work + (warp * 16 + g) * kBlock + 2 * t;
+    auto flush = [&](bool first) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+          float2* const at = reinterpret_cast<float2*>(mine + 8 * h * kBlock + 8 * j);
+          float2 sum = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+          if (!first) {
+            const float2 old = *at;
+            sum.x += old.x;
+            sum.y += old.y;
+          }
+          *at = sum;
+          acc[j][2 * h] = acc[j][2 * h + 1] = 0.0f;
+        }
+    };
+    int done = 0;
 #pragma unroll 2
-    for (int c = chunk0 + warp; c < chunk1; c += kWarps) {
+    for (int c = chunk0 + turn; c < chunk1; c += turns, ++done) {
+      if (done > 0 && done % kChain == 0) flush(done == kChain);
       const int k = c * 32 + 8 * t;
       const bool in = k < cols;       // (cols is a multiple of 8)
       uint4 w[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int r = r0 + 8 * j + g;
-        w[j] = in && r < rank ? __ldg(reinterpret_cast<const uint4*>(A + r * p.l.a_row_stride + k))
-                              : make_uint4(0, 0, 0, 0);
-      }
-      Acts<TX> v[2][2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (in && x[m][h]) v[m][h].load(x[m][h] + k);
-          else v[m][h].clear();
-        }
+      for (int j = 0; j < NT; ++j)
+        w[j] = in && r0 + 8 * j + g < rank
+                   ? __ldg(reinterpret_cast<const uint4*>(Ar + 8 * j * p.l.a_row_stride + k))
+                   : make_uint4(0, 0, 0, 0);
+      Acts<TX> v[2];
+      if (in && token[0] >= 0) v[0].load(x0 + k);
+      else v[0].clear();
+      if (in && token[1] >= 0) v[1].load(x1 + k);
+      else v[1].clear();
       __syncwarp();     // the products take a whole warp
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        uint32_t hi[2][4], lo[2][4];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a, b;
-            v[m][h].pair(s, a, b);
-            if constexpr (kSplit) {
-              split(__uint_as_float(a), hi[m][h], lo[m][h]);
-              split(__uint_as_float(b), hi[m][2 + h], lo[m][2 + h]);
-            } else {
-              hi[m][h] = a;
-              hi[m][2 + h] = b;
-            }
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a, b;
+          v[h].pair(s, a, b);
+          if constexpr (kSplit) {
+            split(__uint_as_float(a), hi[h], lo[h]);
+            split(__uint_as_float(b), hi[2 + h], lo[2 + h]);
+          } else {
+            hi[h] = a;
+            hi[2 + h] = b;
           }
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if (r0 + 8 * j >= rank) break;
           uint32_t b0, b1;
           widen<TW>(s == 0 ? w[j].x : s == 1 ? w[j].y : s == 2 ? w[j].z : w[j].w, b0, b1);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (m >= mblocks) break;
-            mma_tf32(acc[m][j], hi[m], b0, b1);
-            if constexpr (kSplit) mma_tf32(acc[m][j], lo[m], b0, b1);
-          }
+          mma_tf32(acc[j], hi, b0, b1);
+          if constexpr (kSplit) mma_tf32(acc[j], lo, b0, b1);
         }
       }
     }
-    // the eight warps' parts, summed in their order
-    if (r0 > 0) __syncthreads();
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if (m >= mblocks) break;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(work + (warp * kTile + 16 * m + 8 * h + g) * kBlock + 8 * j + 2 * t) =
-              make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-    }
+    // the warps' parts, summed in their order
+    flush(done <= kChain);
     __syncthreads();
     const int here = min(kBlock, wide - r0);
     for (int i = tid; i < mblocks * 16 * kBlock; i += kThreads) {
       const int j = i / kBlock, r = i % kBlock;
       if (r >= here) continue;
+      const int first = (j >> 4) * turns;
       float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += work[(w * kTile + j) * kBlock + r];
+      for (int w = 0; w < turns; ++w) sum += work[((first + w) * 16 + (j & 15)) * kBlock + r];
       part[j * wide + r0 + r] = sum;
     }
+  }
+  // what the second product starts with is on its way while the blocks wait for one another
+  const TW* const B = static_cast<const TW*>(p.l.b) + tile.adapter * p.l.b_stride;
+  Unit<TW, KG> in;
+  if (unit0 + turn < unit1) {
+    in.load_z(p, (unit0 + turn) * 32, token, t);
+    in.load_b(p, B, (unit0 + turn) * 32, 0, rank, g, t);
   }
   cluster_arrive();
   cluster_wait();
@@ -500,11 +573,11 @@ lora_kernel(const __grid_constant__ Args p) {
         h[2] += v[c].z;
         h[3] += v[c].w;
       }
-      const int m = j >> 4, half = (j >> 3) & 1, l = (j & 7) * 4 + (q & 3);
+      const int mb = j >> 4, half = (j >> 3) & 1, l = (j & 7) * 4 + (q & 3);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int step = 2 * (q >> 2) + (e >> 1);
-        const int at = ((step * mblocks + m) * 32 + l) * 4 + half + 2 * (e & 1);
+        const int at = ((step * mblocks + mb) * 32 + l) * 4 + half + 2 * (e & 1);
         // (past the rank an infinite activation has left a NaN)
         split(4 * q + e < rank ? h[e] * scale : 0.0f, hi[at], lo[at]);
       }
@@ -514,77 +587,52 @@ lora_kernel(const __grid_constant__ Args p) {
   cluster_arrive();     // this block's part has no reader left when all have arrived
 
   // ---- Y = Z + B h
-  const TW* const B = static_cast<const TW*>(p.l.b) + tile.adapter * p.l.b_stride;
   const int groups = wide / 16;
+  bool loaded = true;
 #pragma unroll 1
-  for (int64_t u = unit0 + warp; u < unit1; u += kWarps) {
+  for (int64_t u = unit0 + turn; u < unit1; u += turns) {
     const int64_t n0 = u * 32;
-    const int64_t out = n0 + 8 * t;           // this thread's eight rows of Y
-    const int some = (int)max((int64_t)0, min((int64_t)8, rows - out));
-    float acc[2][4][4];
+    if (!loaded) {
+      in.load_z(p, n0, token, t);
+      in.load_b(p, B, n0, 0, rank, g, t);
+    }
+    loaded = false;
+    float acc[4][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 #pragma unroll 1
-    for (int q = 0; q < groups; ++q) {
-      const int k = 16 * q + 4 * t;
-      uint2 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // column g of block i is row 8 (g / 2) + 2 i + g % 2, so that a thread's
-        // results are consecutive rows
-        const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-        w[i] = make_uint2(0, 0);
-        const TW* const b = B + n * p.l.b_row_stride + k;
-        if (p.b_vec && k + 4 <= rank && n < rows) {
-          w[i] = __ldg(reinterpret_cast<const uint2*>(b));
-        } else if (n < rows && k < rank) {
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
-          w[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-        }
-      }
+    for (int q0 = 0; q0 < groups; q0 += KG) {
+      if (q0 > 0) in.load_b(p, B, n0, 16 * q0, rank, g, t);
       __syncwarp();
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int q = 0; q < KG; ++q) {
+        if (q0 + q >= groups) break;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m >= mblocks) break;
-          const int at = (((2 * q + s) * mblocks + m) * 32 + lane) * 4;
+        for (int s = 0; s < 2; ++s) {
+          const int at = (((2 * (q0 + q) + s) * mblocks + m) * 32 + lane) * 4;
           const uint4 a = *reinterpret_cast<const uint4*>(hi + at), b = *reinterpret_cast<const uint4*>(lo + at);
           const uint32_t fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t b0, b1;
-            widen<TW>(s ? w[i].y : w[i].x, b0, b1);
-            mma_tf32(acc[m][i], fa, b0, b1);
-            mma_tf32(acc[m][i], fb, b0, b1);
+            widen<TW>(s ? in.w[q][i].y : in.w[q][i].x, b0, b1);
+            mma_tf32(acc[i], fa, b0, b1);
+            mma_tf32(acc[i], fb, b0, b1);
           }
         }
+      }
     }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int h = 0; h < 2; ++h) {
+      if (token[h] < 0 || in.some == 0) continue;
+      float v[8];
+      floats8(in.z[h], p.y_type, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 16 * m + 8 * h + g;
-        if (j >= count || some == 0) continue;
-        float v[8];
-        const int64_t token = s_tok[j];
-        if (p.z) {
-          load8(p.z, p.y_type, token * p.z_stride + out, some, p.z_vec, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += acc[m][e >> 1][2 * h + (e & 1)];
-        store8(p.y, p.y_type, token * p.y_stride + out, some, p.y_vec, v);
-      }
+      for (int e = 0; e < 8; ++e) v[e] += acc[e >> 1][2 * h + (e & 1)];
+      store8(p.y, p.y_type, token[h] * p.y_stride + in.out, in.some, p.y_vec, v);
+    }
   }
   cluster_wait();
 }
@@ -625,7 +673,9 @@ cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
 
 template <typename TX, typename TW>
 cudaError_t launch_for(const Args& a, int64_t tiles, cudaStream_t s) {
-  return a.l.max_rank <= 16 ? launch_as<TX, TW, 2>(a, tiles, s) : launch_as<TX, TW, 8>(a, tiles, s);
+  if (a.l.max_rank <= 16) return launch_as<TX, TW, 2>(a, tiles, s);
+  if (a.l.max_rank <= 32) return launch_as<TX, TW, 4>(a, tiles, s);
+  return launch_as<TX, TW, 8>(a, tiles, s);
 }
 
 }  // namespace
