@@ -7,7 +7,7 @@
 // The kept tokens are a beginning of the order (falling logit, rising index). A
 // token's place in it is an integer, its logit's bits above its complemented
 // index, so each filter is a least place, the cut. A cut is found by counting
-// (top-k) or weighing (top-p) the tokens in 1536 ranges, first 32 to an octave
+// (top-k) or weighing (top-p) the tokens in 768 ranges, first 16 to an octave
 // of weight, then, where a range holds too many tokens (equal logits), equal
 // parts of it, until the range around the cut holds few enough to be sorted. If
 // that range and all tokens above it fit in the list, which is the rule for the
@@ -33,10 +33,10 @@ constexpr int kIndexBits = 18;
 constexpr int kList = 1024;                 // tokens that are sorted
 constexpr int kBlock = 512;                 // tokens of a sum
 constexpr int kMaxSlice = 32768;            // tokens of a thread block: 2^15 times 2^16 fit in a bin
-constexpr int kMaxBlocks = kMaxSlice / kBlock;
+constexpr int kMaxBlocks = kMaxSlice / kBlock + 1;
 constexpr int kMaxCluster = 16;
 static_assert(kMaxVocab == 1 << kIndexBits, "an index below a logit's bits");
-static_assert(kBlock == kThreads, "a thread for each token of a block");
+static_assert(kBlock == kThreads && kList == 2 * kThreads, "one token, two entries a thread");
 static_assert(kWeightBins % 4 == 0 && kWeightBins / 4 <= kThreads, "four bins a thread");
 
 using u64 = unsigned long long;
@@ -59,19 +59,20 @@ struct Args {
 };
 
 // Shared memory before the slice.
-struct Shared {
-  float2 table[kExpSteps];
+struct alignas(16) Shared {
+  ExpTable table;
   u64 list[kList];            // places of the tokens at a cut
-  u64 weight[kList];          // (rank 0) their weights; while a window is narrowed, weights by bin
+  u64 weight[kList];          // (rank 0) their weights
   uint32_t bins[kWeightBins]; // tokens, or leading bits of weights
   u64 sums[kMaxBlocks];       // kept weights by block
   u64 scan[kWarps];
   u64 give[4];                // what the other blocks of the cluster read
+  u64 pick[6];
   int have;                   // entries of the list
   float top;
   int first;                  // lowest index of the largest logit
-  u64 pick[6];
 };
+static_assert(sizeof(Shared) % 16 == 0, "the slice behind it in 16-byte pieces");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -111,7 +112,7 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 }
 
 // floor(a * x) of a weight sum and a float in (0, 1), exactly; `up`: the ceiling.
-__device__ __forceinline__ u64 fraction_of(u64 a, float x, bool up) {
+__device__ __noinline__ u64 fraction_of(u64 a, float x, bool up) {
   const uint32_t b = __float_as_uint(x);
   const uint32_t mant = b >> 23 ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
   const int shift = 150 - (int)(b >> 23 ? b >> 23 : 1);     // x = mant / 2^shift, 24 <= shift <= 149
@@ -128,156 +129,266 @@ __device__ __forceinline__ u64 fraction_of(u64 a, float x, bool up) {
   return q + (up && left ? 1 : 0);
 }
 
+// ---------------------------------------------------------------- a thread block and its cluster
+// (Functions of their own, not inlined: the kernel runs once through most of its code, and for few
+// rows the time goes into fetching it.)
+
+__device__ __forceinline__ void meet(int cluster) {
+  if (cluster == 1) {
+    __syncthreads();
+    return;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+struct Sum {
+  u64 before, all;
+};
+// The sum of the threads' values before this thread, and of all.
+__device__ __noinline__ Sum scan(Shared* s, u64 v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 sum = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += o;
+  }
+  __syncthreads();      // (the last scan's readers are done)
+  if (lane == 31) s->scan[warp] = sum;
+  __syncthreads();
+  // every warp sums the warps' totals again
+  u64 w = lane < kWarps ? s->scan[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += o;
+  }
+  const u64 all = __shfl_sync(0xffffffffu, w, kWarps - 1);
+  const u64 before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return {(warp > 0 ? before : 0) + sum - v, all};
+}
+// The sum over the cluster of a value that all threads of a block have, by way
+// of give[at], and that of the blocks before this one.
+__device__ __noinline__ Sum over_cluster(Shared* s, u64 mine, int at, int cluster, int rank) {
+  if (cluster == 1) {
+    __syncthreads();
+    return {0, mine};
+  }
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) s->give[at] = mine;
+  meet(cluster);
+  u64 v = lane < cluster ? remote_u64(remote(&s->give[at], lane)) : 0;
+#pragma unroll
+  for (int d = 1; d < kMaxCluster; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  const u64 before = __shfl_sync(0xffffffffu, v, max(rank - 1, 0));
+  return {rank > 0 ? before : 0, __shfl_sync(0xffffffffu, v, kMaxCluster - 1)};
+}
+// The first n of kList values, falling; behind them are zeros up to the next
+// power of two. By as many warps as have pairs.
+__device__ __noinline__ void sort(u64* v, int n) {
+  int size = 2;
+  while (size < n) size *= 2;
+  const int threads = max(32, size / 2);
+  const int i = threadIdx.x;
+  if (i < threads) {
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        if (i < size / 2) {
+          const int a = 2 * i - (i & (j - 1)), b = a + j;
+          const u64 x = v[a], y = v[b];
+          if ((x < y) == ((a & k) == 0)) {
+            v[a] = y;
+            v[b] = x;
+          }
+        }
+        if (threads == 32) __syncwarp();
+        else named_barrier_sync(1, threads);
+      }
+  }
+  __syncthreads();
+}
+
+struct Window {
+  u64 lo, hi;       // places
+  u64 above;        // tokens above it (by count), their weight (by weight, where exact)
+  u64 inside;       // tokens in it, at most
+  u64 upto;         // tokens in it or above, at most
+};
+
+// Among the bins of all threads (n tokens at most; lo to hi of what counts, `above` before the first):
+// the first that may reach `target` in pick[0], what is before it in pick[2] and the tokens in pick[4];
+// the first that surely does in pick[1] (kWeightBins if none), the tokens up to it in pick[5].
+__device__ __forceinline__ void pick_bins(Shared* s, const u64 (&n)[4], const u64 (&lo)[4], const u64 (&hi)[4],
+                                          bool differ, u64 target, u64 above) {
+  const int tid = threadIdx.x;
+  u64 at_lo = above + scan(s, lo[0] + lo[1] + lo[2] + lo[3]).before;
+  u64 at_hi = differ ? above + scan(s, hi[0] + hi[1] + hi[2] + hi[3]).before : at_lo;
+  const Sum tokens = scan(s, n[0] + n[1] + n[2] + n[3]);
+  u64 at_n = tokens.before;
+  if (tid == 0) {
+    s->pick[0] = 0;
+    s->pick[1] = kWeightBins;
+    s->pick[2] = above;
+    s->pick[4] = 0;
+    s->pick[5] = tokens.all;
+  }
+  __syncthreads();
+  if (tid < kWeightBins / 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (at_hi < target && at_hi + hi[e] >= target) {
+        s->pick[0] = 4 * tid + e;
+        s->pick[2] = at_lo;
+        s->pick[4] = at_n;
+      }
+      if (at_lo < target && at_lo + lo[e] >= target) {
+        s->pick[1] = 4 * tid + e;
+        s->pick[5] = at_n + n[e];
+      }
+      at_lo += lo[e];
+      at_hi += hi[e];
+      at_n += n[e];
+    }
+  }
+  __syncthreads();
+}
+
 template <typename T> struct Row {
-  Shared& s;
-  const T* const xs;          // this block's slice
-  const Args& a;
-  const int tid, lane, warp, rank, cluster;
-  const int start, count, blocks;    // of the slice: its first token, tokens, blocks of 512
+  Shared* s;
+  const T* xs;                // this block's slice: values pad .. end - 1 of it
+  int cluster, rank;
+  int start;                  // the token of xs[0]
+  int pad, end, blocks;       // blocks of 512 values that hold some
   Weigher weigh;
 
-  // ---- the cluster and the block
-
-  __device__ __forceinline__ void meet() const {
-    if (cluster == 1) {
-      __syncthreads();
-      return;
-    }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  }
-  // The sum of the threads' values before this thread, and of all.
-  __device__ __forceinline__ u64 scan(u64 v, u64& total) const {
-    u64 sum = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const u64 o = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += o;
-    }
-    __syncthreads();      // (the last scan's readers are done)
-    if (lane == 31) s.scan[warp] = sum;
-    __syncthreads();
-    u64 before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const u64 o = s.scan[w];
-      if (w < warp) before += o;
-      total += o;
-    }
-    return before + sum - v;
-  }
-  // The sum over the cluster of a value that all threads of a block have, by
-  // way of give[at]; `before`: of the blocks before this one.
-  __device__ __forceinline__ u64 over_cluster(u64 mine, int at, u64& before) const {
-    if (tid == 0) s.give[at] = mine;
-    meet();
-    before = 0;
-    u64 all = 0;
-    for (int r = 0; r < cluster; ++r) {
-      const u64 v = cluster == 1 ? mine : remote_u64(remote(&s.give[at], r));
-      if (r < rank) before += v;
-      all += v;
-    }
-    return all;
-  }
-
-  // ---- tokens
-
-  __device__ __forceinline__ u64 place(float l, int i) const {   // i: within the slice
+  __device__ __forceinline__ u64 place(float l, int i) const {   // i: in xs
     return ((u64)order_key(l) << kIndexBits) | (unsigned)(kMaxVocab - 1 - (start + i));
   }
-  // Calls f(logit, index within the slice) for every token, four of a thread at
-  // a time; a warp's turn is a block of 512 tokens, after which `end(block)`.
-  template <typename F, typename E> __device__ __forceinline__ void each(F f, E end) const {
+  // Calls f(four logits, the index of the first in xs) for every token (NaN for
+  // what is none); a warp's turn is a block of 512, after which done(block).
+  template <typename F, typename D> __device__ __forceinline__ void each(F f, D done) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b = warp; b < blocks; b += kWarps) {
-      const int end_of = min(kBlock, count - b * kBlock);
-#pragma unroll
+      const int i0 = b * kBlock + lane * 4;
+      const bool whole = b * kBlock >= pad && (b + 1) * kBlock <= end;
+#pragma unroll 2
       for (int j = 0; j < kBlock / 128; ++j) {
-        const int o = j * 128 + lane * 4, i = b * kBlock + o;
+        const int i = i0 + j * 128;
         const Vec<T, 4> v = *reinterpret_cast<const Vec<T, 4>*>(xs + i);
+        float l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (o + e < end_of) f(Elem<T>::up(v.v[e]), i + e);
+        for (int e = 0; e < 4; ++e) l[e] = Elem<T>::up(v.v[e]);
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < pad || i + e >= end) l[e] = NAN;
+        }
+        f(l, i);
       }
-      end(b);
+      done(b);
     }
   }
   template <typename F> __device__ __forceinline__ void each(F f) const {
     each(f, [](int) {});
   }
+  // The sum of the weights of four tokens that fulfil `counts`.
+  template <typename C> __device__ __forceinline__ u64 weigh_if(const float (&l)[4], C counts) const {
+    bool in[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) in[e] = counts(e);
+    if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return 0;
+    uint64_t w[4];
+    int bits[4];
+    weigh(l, w, bits);
+    u64 sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += in[e] ? w[e] : 0;
+    return sum;
+  }
 
   // ---- finding a cut
 
-  struct Window {
-    u64 lo, hi;       // places
-    u64 above;        // by count: tokens above the window
-    u64 inside;       // tokens in it, at most
-  };
-
   // The least place of a weight's bin of at most b.
   __device__ __forceinline__ u64 bin_end(int b, uint32_t top_key) const {
+    const uint32_t lane = threadIdx.x & 31;
     // the least key whose bin is at most b: 32 candidates a step
     uint32_t lo = 0, hi = top_key + 1;     // (above all tokens, if none has such a bin)
     while (lo < hi) {
-      const uint32_t step = (hi - lo) / 32 + 1, at = lo + (uint32_t)lane * step;
-      const bool in = at < hi && at >= lo && weigh.bin(key_value(at)) <= b;
+      const uint32_t step = (hi - lo) / 32 + 1, at = lo + lane * step;
+      const bool in = at < hi && weigh.bin(key_value(at)) <= b;
       const unsigned m = __ballot_sync(0xffffffffu, in);
       if (m) {
-        const int l = __ffs(m) - 1;
-        hi = lo + (uint32_t)l * step;
-        if (l > 0) lo = lo + (uint32_t)(l - 1) * step + 1;
-        else lo = hi;
+        const uint32_t l = __ffs(m) - 1;
+        hi = lo + l * step;
+        lo = l > 0 ? lo + (l - 1) * step + 1 : hi;
       } else {
-        const uint32_t l = min(31u, (hi - 1 - lo) / step);    // the last candidate below hi
-        lo = lo + l * step + 1;
+        lo += min(31u, (hi - 1 - lo) / step) * step + 1;    // behind the last candidate below hi
       }
     }
     return (u64)lo << kIndexBits;
   }
 
-  // The range around the cut: by count, the least place such that `target`
-  // tokens are at it or above; by weight, such that they weigh the share `share`
-  // of all at least, whose sum goes to *all. Tokens from `from` on only.
-  // Narrowed until at most kList tokens are inside.
-  __device__ __forceinline__ Window search(bool by_weight, u64 target, u64 from, uint32_t top_key, u64* all,
-                                           float share) {
-    Window w = {from, ((u64)top_key << kIndexBits) | kIndexMask, 0, ~u64(0)};
+  // The range around the cut, of tokens from `from` on: by count, the least
+  // place such that `target` tokens are at it or above; by weight, such that
+  // they weigh `target` at least, the share `share` of all, whose sum is
+  // returned in *all.
+  __device__ __forceinline__ Window search(bool by_weight, u64& target, u64 from, uint32_t top_key, u64* all,
+                                           float share) const {
+    const int tid = threadIdx.x;
+    Window w = {from, ((u64)top_key << kIndexBits) | kIndexMask, 0, 0, 0};
     // (tokens that weigh nothing do not help to reach a weight)
     if (by_weight) w.lo = max(from, (u64)order_key(weigh.least) << kIndexBits);
-    // ---- 32 ranges to an octave of weight
-    meet();                              // (the last reading of the bins is over)
-    for (int j = tid; j < kWeightBins; j += kThreads) s.bins[j] = 0;
+    meet(cluster);                       // (the last reading of the bins is over)
+    for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
     __syncthreads();
-    u64 mine = 0;
-    each([&](float l, int i) {
-      if (from != kNoCut && place(l, i) < from) return;
-      if (!by_weight) {
-        atomicAdd(&s.bins[weigh.bin(l)], 1u);
-      } else if (l >= weigh.least) {
-        uint32_t top16;
-        mine += weigh(l, &top16);
-        atomicAdd(&s.bins[weigh.bin(l)], top16);
-      }
-    });
-    u64 ignored;
     if (by_weight) {
-      u64 sum;
-      scan(mine, sum);
-      *all = over_cluster(sum, 0, ignored);
+      u64 mine = 0;
+      const float lo = fmaxf(weigh.least, key_value(max((uint32_t)(from >> kIndexBits), order_key(-INFINITY))));
+      each([&](const float (&l)[4], int i) {
+        bool in[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = l[e] >= lo && (l[e] > lo || place(l[e], i + e) >= from);
+        if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
+        uint64_t wt[4];
+        int bits[4];
+        uint32_t top16[4];
+        weigh(l, wt, bits, top16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (in[e]) {
+            mine += wt[e];
+            atomicAdd(&s->bins[Weigher::bin_of(bits[e])], top16[e]);
+          }
+      });
+      *all = over_cluster(s, scan(s, mine).all, 0, cluster, rank).all;
       target = share > 0.0f ? max(u64(1), fraction_of(*all, share, true)) : 1;
     } else {
-      meet();
+      each([&](const float (&l)[4], int) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (l[e] == l[e]) atomicAdd(&s->bins[weigh.bin(l[e])], 1u);
+      });
+      meet(cluster);
     }
     // this thread's four bins, of all blocks: tokens (at most), and what counts, at least and at most
     u64 n[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
     if (tid < kWeightBins / 4) {
-      for (int r = 0; r < cluster; ++r) {
-        const uint4 v = remote_u128(remote(&s.bins[4 * tid], r));
-        n[0] += v.x;
-        n[1] += v.y;
-        n[2] += v.z;
-        n[3] += v.w;
+      for (int r0 = 0; r0 < cluster; r0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = r0 + r < cluster ? remote_u128(remote(&s->bins[4 * tid], r0 + r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          n[0] += v[r].x;
+          n[1] += v[r].y;
+          n[2] += v[r].z;
+          n[3] += v[r].w;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -285,7 +396,7 @@ template <typename T> struct Row {
           // Sums of weights' first 16 bits, 2^15 - 8 at least (just below a
           // power of two the table's entry is that power's): a token for each of
           // these in the sum, at most, each cut by less than one and off by a unit.
-          const int octave = (4 * tid + e + 31) / 32;
+          const int octave = Weigher::octave_of(4 * tid + e);
           const u64 tokens = (n[e] + (n[e] >> 11)) >> 15, v = (n[e] << 31) >> octave;
           lo[e] = v - min(v, tokens);
           hi[e] = tokens ? (((n[e] + tokens) << 31) >> octave) + tokens + 1 : 0;
@@ -295,331 +406,304 @@ template <typename T> struct Row {
         }
       }
     }
-    pick_bins(n, lo, hi, target, 0);
-    {
-      const int first = (int)s.pick[0], last = (int)s.pick[1];
-      const u64 low = last < kWeightBins ? bin_end(last, top_key) : 0;
-      if (first > 0) w.hi = bin_end(first - 1, top_key) - 1;
-      w.lo = max(w.lo, low);
-      w.inside = s.pick[5] - s.pick[4];
-      w.above = s.pick[2];
-    }
-    // ---- equal parts of the window, sums exact
-    u64* const sums = s.list;
-    static_assert(sizeof(s.list) + sizeof(s.weight) >= kWeightBins * sizeof(u64), "");
-    static_assert(offsetof(Shared, weight) == offsetof(Shared, list) + sizeof(s.list), "one after the other");
-    for (int level = 1; w.inside > kList; ++level) {
+    pick_bins(s, n, lo, hi, by_weight, target, 0);
+    const int first = (int)s->pick[0], last = (int)s->pick[1];
+    if (first > 0) w.hi = bin_end(first - 1, top_key) - 1;
+    w.lo = max(w.lo, last < kWeightBins ? bin_end(last, top_key) : 0);
+    w.inside = s->pick[5] - s->pick[4];
+    w.upto = s->pick[5];
+    w.above = s->pick[2];
+    return w;
+  }
+
+  // Narrows a window until at most kList tokens are inside: equal parts of it,
+  // with exact sums. (Not inlined, and given a copy of the row: it is for many
+  // equal logits, and for many tokens that weigh next to nothing.)
+  static __device__ __noinline__ Window narrow(Row row, Window w, bool by_weight, u64 target) {
+    Shared* const s = row.s;
+    const int tid = threadIdx.x;
+    u64* const sums = s->list;
+    static_assert(sizeof(s->list) + sizeof(s->weight) >= kWeightBins * sizeof(u64), "");
+    static_assert(offsetof(Shared, weight) == offsetof(Shared, list) + sizeof(s->list), "one after the other");
+    while (w.inside > kList) {
       int shift = 0;
       while (((w.hi - w.lo) >> shift) >= kWeightBins) ++shift;
-      meet();
+      meet(row.cluster);
       for (int j = tid; j < kWeightBins; j += kThreads) {
-        s.bins[j] = 0;
+        s->bins[j] = 0;
         sums[j] = 0;
       }
       __syncthreads();
       u64 above = 0;
-      each([&](float l, int i) {
-        const u64 q = place(l, i);
-        const bool weighs = by_weight && l >= weigh.least;
-        if (q > w.hi) {
-          if (weighs) above += weigh(l);
-        } else if (q >= w.lo) {
-          const int j = (int)((w.hi - q) >> shift);
-          atomicAdd(&s.bins[j], 1u);
-          if (weighs) atomicAdd(&sums[j], (u64)weigh(l));
+      row.each([&](const float (&l)[4], int i) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const float x = e == 0 ? l[0] : e == 1 ? l[1] : e == 2 ? l[2] : l[3];
+          if (!(x == x)) continue;
+          const u64 q = row.place(x, i + e);
+          const bool weighs = by_weight && x >= row.weigh.least;
+          if (q > w.hi) {
+            if (weighs) above += row.weigh.one(x);
+          } else if (q >= w.lo) {
+            const int j = (int)((w.hi - q) >> shift);
+            atomicAdd(&s->bins[j], 1u);
+            if (weighs) atomicAdd(&sums[j], (u64)row.weigh.one(x));
+          }
         }
       });
-      if (by_weight) {
-        u64 sum;
-        scan(above, sum);
-        w.above = over_cluster(sum, 0, ignored);
-      } else {
-        meet();
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) n[e] = lo[e] = 0;
+      if (by_weight) w.above = over_cluster(s, scan(s, above).all, 0, row.cluster, row.rank).all;
+      else meet(row.cluster);
+      u64 n[4] = {0, 0, 0, 0}, v[4] = {0, 0, 0, 0};
       if (tid < kWeightBins / 4) {
-        for (int r = 0; r < cluster; ++r) {
+        for (int r = 0; r < row.cluster; ++r) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            n[e] += remote_u32(remote(&s.bins[4 * tid + e], r));
-            if (by_weight) lo[e] += remote_u64(remote(&sums[4 * tid + e], r));
+            n[e] += remote_u32(remote(&s->bins[4 * tid + e], r));
+            if (by_weight) v[e] += remote_u64(remote(&sums[4 * tid + e], r));
           }
         }
       }
-      pick_bins(n, by_weight ? lo : n, by_weight ? lo : n, target, w.above);
-      const u64 end = w.hi, first = s.pick[0], last = s.pick[1];
-      w.hi = end - (first << shift);
-      w.lo = max(w.lo, end - min(end, ((last + 1) << shift) - 1));
-      w.inside = s.pick[5] - s.pick[4];
-      w.above = s.pick[2];
-      if (w.inside <= kList) meet();     // (the last reading of the sums, where the list is, is over)
+      pick_bins(s, n, by_weight ? v : n, by_weight ? v : n, false, target, w.above);
+      const u64 top = w.hi, first = s->pick[0], last = s->pick[1];
+      w.hi = top - (first << shift);
+      w.lo = max(w.lo, top - min(top, ((last + 1) << shift) - 1));
+      w.inside = s->pick[5] - s->pick[4];
+      w.above = s->pick[2];
     }
+    meet(row.cluster);     // the last reading of the sums, where the list is, is over
     return w;
   }
 
-  // Among the bins of all threads (n tokens at most; lo to hi of what counts, `above` before the
-  // first): the first that may reach `target` in pick[0], what is before it in pick[2] and the tokens
-  // in pick[4]; the first that surely does in pick[1] (kWeightBins if none), the tokens up to it in pick[5].
-  __device__ __forceinline__ void pick_bins(const u64 (&n)[4], const u64 (&lo)[4], const u64 (&hi)[4], u64 target,
-                                            u64 above) {
-    u64 total, all_n;
-    u64 at_lo = above + scan(lo[0] + lo[1] + lo[2] + lo[3], total);
-    u64 at_hi = above + scan(hi[0] + hi[1] + hi[2] + hi[3], total);
-    u64 at_n = scan(n[0] + n[1] + n[2] + n[3], all_n);
-    if (tid == 0) {
-      s.pick[0] = 0;
-      s.pick[1] = kWeightBins;
-      s.pick[2] = above;
-      s.pick[4] = 0;
-      s.pick[5] = all_n;
-    }
+  // The tokens of the window in this block's list. `weights`: the sum of the
+  // weights of those above it is returned, and by block in s->sums.
+  __device__ __forceinline__ u64 gather(const Window& w, bool weights) const {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) s->have = 0;
     __syncthreads();
-    if (tid < kWeightBins / 4) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (at_hi < target && at_hi + hi[e] >= target) {
-          s.pick[0] = 4 * tid + e;
-          s.pick[2] = at_lo;
-          s.pick[4] = at_n;
-        }
-        if (at_lo < target && at_lo + lo[e] >= target) {
-          s.pick[1] = 4 * tid + e;
-          s.pick[5] = at_n + n[e];
-        }
-        at_lo += lo[e];
-        at_hi += hi[e];
-        at_n += n[e];
-      }
-    }
-    __syncthreads();
-  }
-
-  // The tokens of the window in this block's list, and the weights of those
-  // above it.
-  __device__ __forceinline__ u64 gather(const Window& w, bool weights) {
-    if (tid == 0) s.have = 0;
-    __syncthreads();
-    u64 above = 0;
     const float lo = key_value(max((uint32_t)(w.lo >> kIndexBits), order_key(-INFINITY)));
-    each([&](float l, int i) {
-      if (!(l >= lo)) return;
+    const float hi = key_value((uint32_t)(w.hi >> kIndexBits));
+    auto collect = [&](float l, int i) {
       const u64 q = place(l, i);
-      if (q < w.lo) return;
-      if (q > w.hi) {
-        if (weights && l >= weigh.least) above += weigh(l);
-        return;
+      if (q < w.lo || q > w.hi) return;
+      const int at = atomicAdd(&s->have, 1);
+      if (at < kList) s->list[at] = q;
+    };
+    if (!weights) {
+      each([&](const float (&l)[4], int i) {
+        if (fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= lo) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (l[e] >= lo) collect(l[e], i + e);
+        }
+      });
+      __syncthreads();
+      return 0;
+    }
+    u64 mine = 0, all = 0;
+    each([&](const float (&l)[4], int i) {
+      bool at_window = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) at_window |= l[e] >= lo && l[e] <= hi;
+      if (at_window) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (l[e] >= lo && l[e] <= hi) collect(l[e], i + e);
       }
-      const int at = atomicAdd(&s.have, 1);
-      if (at < kList) s.list[at] = q;
+      __syncwarp();
+      mine += weigh_if(l, [&](int e) { return l[e] >= hi && (l[e] > hi || place(l[e], i + e) > w.hi); });
+    }, [&](int b) {
+      all += mine;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+      if (lane == 0) s->sums[b] = mine;
+      mine = 0;
     });
-    u64 sum;
-    scan(above, sum);
-    return sum;
+    return scan(s, all).all;
   }
 
   // (rank 0) All blocks' lists in this one's, sorted, the highest first; returns
-  // their number. The weights are in s.weight.
-  __device__ __forceinline__ int join() {
-    int have[kMaxCluster], n = 0, mine = 0;
-    if (cluster > 1) {
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) have[r] = r < cluster ? (int)remote_u32(remote(&s.have, r)) : 0;
-      mine = have[0];
-      u64 got[kList / kThreads];
-#pragma unroll
-      for (int j = 0; j < kList / kThreads; ++j) {
-        const int want = mine + j * kThreads + tid;
-        int at = want - mine;
-        got[j] = 0;
-        bool done = false;
-#pragma unroll
-        for (int r = 1; r < kMaxCluster; ++r) {
-          if (!done && at < have[r]) {
-            got[j] = remote_u64(remote(&s.list[at], r));
-            done = true;
-          }
-          if (!done) at -= have[r];
-        }
-        if (want < kList) s.list[want] = got[j];
-      }
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) n += have[r];
-    } else {
-      __syncthreads();
-      n = mine = s.have;
-      for (int i = mine + tid; i < kList; i += kThreads) s.list[i] = 0;
-    }
-    n = min(n, kList);
+  // their number. The weights are in s->weight.
+  __device__ __forceinline__ int join() const {
+    const int tid = threadIdx.x, lane = tid & 31;
     __syncthreads();
-    sort(s.list, n);
-    for (int i = tid; i < kList; i += kThreads) {
-      const float l = key_value((uint32_t)(s.list[i] >> kIndexBits));
-      s.weight[i] = i < n && l >= weigh.least ? weigh(l) : 0;
+    int have = lane < cluster ? (int)remote_u32(remote(&s->have, lane)) : 0;
+    const int mine = __shfl_sync(0xffffffffu, have, 0);
+    int upto = have;      // entries of the blocks up to the lane's
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const int n = min(__shfl_sync(0xffffffffu, upto, kMaxCluster - 1), kList);
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      const int at = mine + j * kThreads + tid;
+      // the block that has entry `at`: the first whose entries reach beyond it
+      int r = 0, base = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        const int e = __shfl_sync(0xffffffffu, upto, c);
+        if (e <= at) {
+          r = c + 1;
+          base = e;
+        }
+      }
+      if (at < kList) s->list[at] = at < n ? remote_u64(remote(&s->list[at - base], r)) : 0;
+    }
+    __syncthreads();
+    sort(s->list, n);
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      const int i = tid + j * kThreads;
+      const float l = key_value((uint32_t)(s->list[i] >> kIndexBits));
+      s->weight[i] = i < n && l >= weigh.least ? weigh.one(l) : 0;
     }
     __syncthreads();
     return n;
   }
-  // The first n of kList values, falling; what lies behind them is 0 up to the
-  // next power of two.
-  __device__ __forceinline__ void sort(u64* v, int n) const {
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int k = 2; k <= size; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < size / 2; i += kThreads) {
-          const int a = 2 * i - (i & (j - 1)), b = a + j;
-          const u64 x = v[a], y = v[b];
-          if ((x < y) == ((a & k) == 0)) {
-            v[a] = y;
-            v[b] = x;
-          }
-        }
-        __syncthreads();
-      }
-  }
-  // (rank 0) The number of sorted entries, at least 1, that are needed for the
-  // weights to sum to `target`; `before`: the weights before each thread's two.
-  __device__ __forceinline__ int needed(int n, u64 target) {
-    static_assert(kList == 2 * kThreads, "two entries a thread");
-    const u64 x = s.weight[2 * tid], y = s.weight[2 * tid + 1];
-    u64 total;
-    const u64 at = scan(x + y, total);
-    const int less = (at + x < target ? 1 : 0) + (at + x + y < target ? 1 : 0);
-    u64 all;
-    scan((u64)less, all);
-    return max(1, min(n, (int)all + 1));
+  // (rank 0) The number of sorted entries, at least 1, whose weights sum to
+  // `target`.
+  __device__ __forceinline__ int needed(int n, u64 target) const {
+    const u64 x = s->weight[2 * threadIdx.x], y = s->weight[2 * threadIdx.x + 1];
+    const u64 at = scan(s, x + y).before;
+    const u64 less = (at + x < target ? 1 : 0) + (at + x + y < target ? 1 : 0);
+    return max(1, min(n, (int)scan(s, less).all + 1));
   }
   // (rank 0) The sum of the first n entries' weights.
-  __device__ __forceinline__ u64 weight_of(int n) {
-    u64 total;
-    scan((2 * tid < n ? s.weight[2 * tid] : 0) + (2 * tid + 1 < n ? s.weight[2 * tid + 1] : 0), total);
-    return total;
-  }
-
-  __device__ __forceinline__ void answer(int64_t row, int token, float l, double temp, u64 total) const {
-    a.tokens[row] = token;
-    if (!a.logp) return;
-    // ln(w / total) = l / T - R ln 2 - ln(total / 2^46)
-    const double c = 1.4426950408889634074 / temp, r = 6144.0 - (double)weigh.k;
-    const double e = weigh.far ? ((double)l - (double)weigh.m) * c : (double)l * c;
-    a.logp[row] = (float)((e - r) * 0.69314718055994530942 - log((double)total * 0x1p-46));
-  }
-
-  // (rank 0) The draw from a sorted list that holds all kept tokens.
-  __device__ __forceinline__ void draw_from_list(int64_t row, int kept, double temp, float u) {
-    const u64 total = weight_of(kept);
-    const u64 goal = u > 0.0f ? (u < 1.0f ? min(fraction_of(total, u, false), total - 1) : total - 1) : 0;
-    // by rising index: the complemented index, then the entry
-    u64 again[kList / kThreads];
-#pragma unroll
-    for (int j = 0; j < kList / kThreads; ++j) {
-      const int i = tid + j * kThreads;
-      again[j] = i < kept ? u64(1) << 63 | (s.list[i] & kIndexMask) << 10 | (u64)i : 0;
-    }
-    static_assert(kList == 1 << 10, "an entry below an index");
-    __syncthreads();
-    u64* const by_index = reinterpret_cast<u64*>(s.table);     // (the weights are all computed)
-    static_assert(sizeof(s.table) >= kList * sizeof(u64), "");
-#pragma unroll
-    for (int j = 0; j < kList / kThreads; ++j) by_index[tid + j * kThreads] = again[j];
-    __syncthreads();
-    sort(by_index, kept);
-    const u64 p = by_index[2 * tid], q = by_index[2 * tid + 1];
-    const u64 x = p ? s.weight[p & (kList - 1)] : 0, y = q ? s.weight[q & (kList - 1)] : 0;
-    u64 sum;
-    const u64 at = scan(x + y, sum);
-    if (at <= goal && goal < at + x + y) {
-      const int i = (int)((goal < at + x ? p : q) & (kList - 1));
-      const u64 e = s.list[i];
-      answer(row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), temp, total);
-    }
+  __device__ __forceinline__ u64 weight_of(int n) const {
+    const int i = 2 * threadIdx.x;
+    return scan(s, (i < n ? s->weight[i] : 0) + (i + 1 < n ? s->weight[i + 1] : 0)).all;
   }
 };
+
+// The place of the draw among weights that sum to `total`.
+__device__ __forceinline__ u64 goal_of(u64 total, float u) {
+  return u > 0.0f ? (u < 1.0f ? min(fraction_of(total, u, false), total - 1) : total - 1) : 0;
+}
+
+__device__ __noinline__ void answer(const Args& a, Weigher weigh, int64_t row, int token, float l, double temp,
+                                    u64 total) {
+  a.tokens[row] = token;
+  // ln(w / total), both as parts of 2^46
+  if (a.logp)
+    a.logp[row] = (float)(weigh.log2_of(l, temp) * 0.69314718055994530942 - log((double)total * 0x1p-46));
+}
+
+// (rank 0) The draw from a sorted list that holds all kept tokens.
+__device__ __noinline__ void draw_from_list(Shared* s, const Args& a, Weigher weigh, int64_t row, int kept,
+                                            u64 total, double temp, float u) {
+  const int tid = threadIdx.x;
+  const u64 goal = goal_of(total, u);
+  // by rising index: the complemented index, then the entry; in the table's
+  // place (the weights are all computed)
+  u64* const by_index = reinterpret_cast<u64*>(&s->table);
+  static_assert(sizeof(s->table) >= kList * sizeof(u64) && kList == 1 << 10, "an entry below an index");
+  for (int i = tid; i < kList; i += kThreads)
+    by_index[i] = i < kept ? u64(1) << 63 | (s->list[i] & kIndexMask) << 10 | (u64)i : 0;
+  __syncthreads();
+  sort(by_index, kept);
+  const u64 p = by_index[2 * tid], q = by_index[2 * tid + 1];
+  const u64 x = p ? s->weight[p & (kList - 1)] : 0, y = q ? s->weight[q & (kList - 1)] : 0;
+  const u64 at = scan(s, x + y).before;
+  if (at <= goal && goal < at + x + y) {
+    const u64 e = s->list[(goal < at + x ? p : q) & (kList - 1)];
+    answer(a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), temp, total);
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) unsigned char raw[];
-  Shared& s = *reinterpret_cast<Shared*>(raw);
+  Shared* const s = reinterpret_cast<Shared*>(raw);
   T* const xs = reinterpret_cast<T*>(raw + sizeof(Shared));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
   const int64_t row = blockIdx.x / a.cluster;
-  const int start = rank * a.slice, count = max(0, min(a.slice, a.vocab - start));
-  const int blocks = (count + kBlock - 1) / kBlock;
-  for (int j = tid; j < kExpSteps; j += kThreads) s.table[j] = g_exp_table.v[j];
-  if (tid == 0) s.first = 0x7fffffff;
+  for (int j = tid; j < (int)(sizeof(ExpTable) / 16); j += kThreads)
+    reinterpret_cast<uint4*>(&s->table)[j] = reinterpret_cast<const uint4*>(&g_exp_table)[j];
+  if (tid == 0) s->first = 0x7fffffff;
   pdl_wait_primary();
   pdl_launch_dependents();
-  Row<T> r = {s, xs, a, tid, lane, warp, rank, a.cluster, start, count, blocks, {}};
 
   // ---- the slice, its largest logit, and whether there is a NaN
   const float temp = a.temperature ? a.temperature[row] : 1.0f;
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
-  const T* const x = static_cast<const T*>(a.logits) + row * a.stride + start;
+  const int from = rank * a.slice, count = max(0, min(a.slice, a.vocab - from));
+  const T* const x = static_cast<const T*>(a.logits) + row * a.stride + from;
+  // in shared memory as it lies in memory within 16 bytes, so that whole pieces are copied
+  constexpr int kPiece = 16 / (int)sizeof(T);
+  const int pad = (int)((uintptr_t)x % 16 / sizeof(T)), end = pad + count;
   float top = -INFINITY;
   {
-    constexpr int kPiece = 16 / (int)sizeof(T);
-    const int pieces = (uintptr_t)x % 16 == 0 ? count / kPiece : 0;
+    const uint4* const from16 = reinterpret_cast<const uint4*>(x - pad);
+    const int first = pad ? 1 : 0, last = end / kPiece;        // whole pieces
 #pragma unroll 4
-    for (int i = tid; i < pieces; i += kThreads) {
-      const uint4 q = ldg_stream_v4(reinterpret_cast<const uint4*>(x) + i);
+    for (int i = first + tid; i < last; i += kThreads) {
+      const uint4 q = ldg_stream_v4(from16 + i);
       reinterpret_cast<uint4*>(xs)[i] = q;
       const Vec<T, kPiece> v = *reinterpret_cast<const Vec<T, kPiece>*>(&q);
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) top = max_or_nan(top, Elem<T>::up(v.v[e]));
     }
-#pragma unroll 8
-    for (int i = pieces * kPiece + tid; i < count; i += kThreads) {
-      const T v = x[i];
+    // the ends: before the first whole piece, behind the last one
+    const int head = min(end, first * kPiece), tail = max(head, last * kPiece);
+    const int i = tid < kPiece ? pad + tid : tail + tid - kPiece;
+    if (tid < 2 * kPiece && (tid < kPiece ? i < head : i < end)) {
+      const T v = x[i - pad];
       xs[i] = v;
       top = max_or_nan(top, Elem<T>::up(v));
     }
-    for (int i = count + tid; i < blocks * kBlock; i += kThreads) xs[i] = Elem<T>::down(-INFINITY);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float* const tops = reinterpret_cast<float*>(s.scan);
+  float* const tops = reinterpret_cast<float*>(s->scan);
   if (lane == 0) tops[warp] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = max_or_nan(top, tops[w]);
   if (a.cluster > 1) {
-    if (tid == 0) s.top = top;
-    r.meet();
-    for (int c = 0; c < a.cluster; ++c) top = max_or_nan(top, __uint_as_float(remote_u32(remote(&s.top, c))));
+    if (tid == 0) s->top = top;
+    meet(a.cluster);
+    top = lane < a.cluster ? __uint_as_float(remote_u32(remote(&s->top, lane))) : top;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
   }
-  const bool none = top != top || top == -INFINITY || !(temp >= 0.0f) || temp == INFINITY;
-  if (none) {
+  Row<T> r = {s, xs, a.cluster, rank, from - pad, pad, end, (end + kBlock - 1) / kBlock, {}};
+  if (count == 0) r.blocks = 0;
+  if (top != top || top == -INFINITY || !(temp >= 0.0f) || temp == INFINITY) {
     if (rank == 0 && tid == 0) {
       a.tokens[row] = -1;
       if (a.logp) a.logp[row] = NAN;
     }
   } else if (temp < 0x1p-100f) {
     int first = 0x7fffffff;
-    r.each([&](float l, int i) {
-      if (l == top) first = min(first, start + i);
+    r.each([&](const float (&l)[4], int i) {
+#pragma unroll
+      for (int e = 3; e >= 0; --e)
+        if (l[e] == top) first = min(first, r.start + i + e);
     });
     first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0) atomicMin(&s.first, first);
-    r.meet();
-    if (rank == 0 && tid == 0) {
-      first = s.first;
-      for (int c = 1; c < a.cluster; ++c) first = min(first, (int)remote_u32(remote(&s.first, c)));
-      a.tokens[row] = first;
-      if (a.logp) a.logp[row] = 0.0f;
+    if (lane == 0) atomicMin(&s->first, first);
+    meet(a.cluster);
+    if (rank == 0 && warp == 0) {
+      first = lane < a.cluster ? (int)remote_u32(remote(&s->first, lane)) : 0x7fffffff;
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) {
+        a.tokens[row] = first;
+        if (a.logp) a.logp[row] = 0.0f;
+      }
     }
   } else {
     if (top == INFINITY) {
       // beside it every other logit is minus infinity
-      for (int i = tid; i < blocks * kBlock; i += kThreads)
+      for (int i = pad + tid; i < end; i += kThreads)
         xs[i] = Elem<T>::down(Elem<T>::up(xs[i]) == INFINITY ? 0.0f : -INFINITY);
       top = 0.0f;
       __syncthreads();
     }
     const double t = fmin((double)temp, 0x1p100);
-    r.weigh.set(top, (float)t, s.table);
+    r.weigh.set(top, t, &s->table);
     const uint32_t top_key = order_key(top);
     u64 floor = kNoCut;       // of min-p
     if (mp > 0.0f) {
@@ -627,83 +711,95 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       floor = (u64)order_key(least) << kIndexBits;
     }
     const bool by_count = k > 0 && k < a.vocab, by_weight = p < 1.0f;
-    // 0: not decided, 1: the list holds all kept tokens (rank 0 draws), 2: a cut
-    bool drawn = false;
+    bool drawn = false;       // by rank 0, from the list
+    bool summed = false;      // s->sums holds the kept weights
     u64 cut = kNoCut;
-    for (int which = 0; which < 2 && !drawn; ++which) {
-      if (which == 0 ? !by_count : !by_weight) continue;
-      u64 target = (u64)k, sum = 0, before;
-      const auto w = r.search(which == 1, target, cut, top_key, which == 1 ? &sum : nullptr, p);
-      if (which == 1) target = p > 0.0f ? max(u64(1), fraction_of(sum, p, true)) : 1;
-      // top-k with all tokens above it in the list: nothing else is kept
-      const bool whole = which == 0 && w.above + w.inside <= kList;
-      const auto range = whole ? typename Row<T>::Window{w.lo, ((u64)top_key << kIndexBits) | kIndexMask, 0, 0} : w;
-      const u64 mine = r.gather(range, which == 1);
-      const u64 above = r.over_cluster(mine, 1, before);
+#pragma unroll 1
+    for (int which = by_count ? 0 : 1; which < (by_weight ? 2 : 1) && !drawn; ++which) {
+      const bool weights = which == 1;
+      u64 target = (u64)k, all = 0;
+      Window w = r.search(weights, target, cut, top_key, &all, p);
+      // all tokens that may be kept fit in the list
+      const bool whole = w.upto <= kList;
+      if (whole) w.hi = ((u64)top_key << kIndexBits) | kIndexMask;
+      else if (w.inside > kList) w = Row<T>::narrow(r, w, weights, target);
+      const u64 above = over_cluster(s, r.gather(w, weights && !whole), 1, a.cluster, rank).all;
+      int n = s->have;        // entries of the list
+      u64 found = 0;
       if (rank == 0) {
-        const int n = r.join();
+        n = r.join();
         if (whole) {
-          int kept = min(n, k);
-          if (by_weight) {
+          int kept = weights ? r.needed(n, target) : min(n, k);
+          if (!weights && by_weight) {
             const u64 goal = p > 0.0f ? max(u64(1), fraction_of(r.weight_of(kept), p, true)) : 1;
             kept = min(kept, r.needed(kept, goal));
           }
           if (floor != kNoCut) {
-            u64 over;
-            r.scan((2 * tid < kept && s.list[2 * tid] >= floor ? 1 : 0) +
-                       (2 * tid + 1 < kept && s.list[2 * tid + 1] >= floor ? 1 : 0), over);
-            kept = max(1, (int)over);
+            const int i = 2 * tid;
+            const u64 over = (i < kept && s->list[i] >= floor ? 1 : 0) +
+                             (i + 1 < kept && s->list[i + 1] >= floor ? 1 : 0);
+            kept = max(1, (int)scan(s, over).all);
           }
-          r.draw_from_list(row, kept, t, u);
+          draw_from_list(s, a, r.weigh, row, kept, r.weight_of(kept), t, u);
         } else {
-          const int need = which == 0 ? min(n, (int)(target - w.above)) : target > above ? r.needed(n, target - above) : 1;
-          const u64 found = s.list[max(0, need - 1)];
-          if (tid < a.cluster) remote_put(remote(&s.give[2], tid), found);
+          const int need = !weights ? min(n, (int)(target - w.above)) : target > above ? r.needed(n, target - above) : 1;
+          found = s->list[max(0, need - 1)];
+          if (tid < a.cluster) remote_put(remote(&s->give[2], tid), found);
         }
       }
       if (whole) {
         drawn = true;
-      } else {
-        r.meet();
-        cut = max(cut, s.give[2]);
+        break;
+      }
+      meet(a.cluster);
+      cut = max(cut, s->give[2]);
+      if (weights && floor <= cut) {
+        // the kept tokens of the window, on top of those above it
+        const u64 lowest = (u64)(kMaxVocab - (r.start + end)), highest = (u64)(kMaxVocab - 1 - (r.start + pad));
+        for (int i = tid; i < n; i += kThreads) {
+          const u64 q = s->list[i], at = q & kIndexMask;
+          const float l = key_value((uint32_t)(q >> kIndexBits));
+          if (q >= cut && at >= lowest && at <= highest && l >= r.weigh.least)
+            atomicAdd(&s->sums[(kMaxVocab - 1 - (int)at - r.start) / kBlock], (u64)r.weigh.one(l));
+        }
+        summed = true;
       }
     }
     if (!drawn) {
-      cut = max(cut, floor);
       // ---- the kept weights by block, and the draw
-      const float lo = cut == kNoCut ? r.weigh.least : fmaxf(key_value((uint32_t)(cut >> kIndexBits)), r.weigh.least);
-      u64 mine = 0;
-      r.each([&](float l, int i) {
-        if (l >= lo && (cut == kNoCut || r.place(l, i) >= cut)) mine += r.weigh(l);
-      }, [&](int b) {
+      cut = max(cut, floor);
+      const float lo = fmaxf(key_value(max((uint32_t)(cut >> kIndexBits), order_key(-INFINITY))), r.weigh.least);
+      auto kept = [&](float l, int i) { return l >= lo && (l > lo || r.place(l, i) >= cut); };
+      if (!summed) {
+        u64 mine = 0;
+        r.each([&](const float (&l)[4], int i) { mine += r.weigh_if(l, [&](int e) { return kept(l[e], i + e); }); },
+               [&](int b) {
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-        if (lane == 0) s.sums[b] = mine;
-        mine = 0;
-      });
+                 for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+                 if (lane == 0) s->sums[b] = mine;
+                 mine = 0;
+               });
+      }
       __syncthreads();
-      u64 sum, before;
-      const u64 to_block = r.scan(tid < blocks ? s.sums[tid] : 0, sum);
-      const u64 total = r.over_cluster(sum, 3, before);
-      const u64 goal = u > 0.0f ? (u < 1.0f ? min(fraction_of(total, u, false), total - 1) : total - 1) : 0;
-      if (before <= goal && goal < before + sum) {       // (the same for all threads of a block)
-        const u64 at = before + to_block;
-        if (tid < blocks && at <= goal && goal < at + s.sums[tid]) {
-          s.pick[0] = tid;
-          s.pick[1] = at;
+      const Sum block = scan(s, tid < r.blocks ? s->sums[tid] : 0);
+      const Sum slices = over_cluster(s, block.all, 3, a.cluster, rank);
+      const u64 goal = goal_of(slices.all, u);
+      if (slices.before <= goal && goal < slices.before + block.all) {       // (the same for all threads of a block)
+        const u64 at = slices.before + block.before;
+        if (tid < r.blocks && at <= goal && goal < at + s->sums[tid]) {
+          s->pick[0] = tid;
+          s->pick[1] = at;
         }
         __syncthreads();
-        const int i = (int)s.pick[0] * kBlock + tid;
-        const u64 base = s.pick[1];
-        const float l = Elem<T>::up(xs[i]);
-        const u64 mine = l >= lo && (cut == kNoCut || r.place(l, i) >= cut) ? r.weigh(l) : 0;
-        u64 all;
-        const u64 from = base + r.scan(mine, all);
-        if (from <= goal && goal < from + mine) r.answer(row, start + i, l, t, total);
+        const int i = (int)s->pick[0] * kBlock + tid;
+        const float l = i >= pad && i < end ? Elem<T>::up(xs[i]) : NAN;
+        const u64 mine = kept(l, i) ? r.weigh.one(l) : 0;
+        const u64 before = s->pick[1] + scan(s, mine).before;
+        if (before <= goal && goal < before + mine) answer(a, r.weigh, row, r.start + i, l, t, slices.all);
       }
     }
   }
-  if (a.cluster > 1) r.meet();     // nothing of this block is read any more
+  if (a.cluster > 1) meet(a.cluster);     // nothing of this block is read any more
 }
 
 template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s) {
@@ -717,7 +813,7 @@ template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s)
   a.slice = ((c.vocab + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
   if (c.ntok * a.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const auto kernel = sample_kernel<T>;
-  const int smem = (int)sizeof(Shared) + a.slice * (int)sizeof(T);
+  const int smem = (int)sizeof(Shared) + (a.slice + kBlock) * (int)sizeof(T);
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e == cudaSuccess && a.cluster > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

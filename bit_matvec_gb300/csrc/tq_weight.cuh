@@ -7,7 +7,8 @@
 // any order. 64-bit floats would do too, but run at 1/64 of the rate.
 //
 // With c = log2(e) / T, the weight is 2^(l c - R), R a multiple of 2^-11 just above the largest l c,
-// plus one. l c is the sum of two floats (a product and its error), and its distance q from the
+// plus one. (Where that passes 2000, l is replaced by its difference from the largest, which is exact
+// for every logit that weighs anything: the two are within a factor of two.) l c is the sum of two floats (a product and its error), and its distance q from the
 // nearest multiple of 2^-11 is exact in the first of them: adding K = 6144 - R rounds to such
 // multiples, since 4096 <= l c + K < 8192, and leaves -e + j / 2048 in the sum's bits. The weight is
 // then 2^-e T[j] 2^q with |q| <= 2^-12; T is a table of 2^(j / 2048) as the sum of two floats, and
@@ -18,14 +19,14 @@
 // operation.
 #pragma once
 
-#include "tq_internal.cuh"
+#include "tq_tcgen05.cuh"
 
 namespace tq {
 
 constexpr int kExpSteps = 2048;      // entries of the table
 
 struct ExpTable {
-  float2 v[kExpSteps];               // 2^(40 + j / kExpSteps) as a sum
+  float hi[kExpSteps], lo[kExpSteps];   // 2^(40 + j / kExpSteps) as a sum
 };
 
 // 2^x for 0 <= x < 1 in 64 bits, by the series of exp.
@@ -39,73 +40,91 @@ constexpr ExpTable make_exp_table() {
   ExpTable t = {};
   for (int j = 0; j < kExpSteps; ++j) {
     const double x = exp2_series((double)j / kExpSteps) * 1099511627776.0;
-    t.v[j].x = (float)x;
-    t.v[j].y = (float)(x - (double)t.v[j].x);
+    t.hi[j] = (float)x;
+    t.lo[j] = (float)(x - (double)t.hi[j]);
   }
   return t;
 }
 
+constexpr int kWeightBins = 768;     // 16 to an octave, 47 octaves and a little
+
 struct Weigher {
   float c_hi, c_lo;    // log2(e) / T
   float k;             // 6144 - R
-  float m;             // the largest logit
+  float shift;         // taken from every logit: 0, or the largest one
   float least;         // logits below weigh nothing
-  int far;             // l c passes 2000: differences from m in its place
-  const float2* table;
+  const ExpTable* table;
 
   static constexpr int kMagic = 0x45c00000;   // the bits of 6144.0f
+  static constexpr int kBinShift = 7;         // 2048 / 16 steps a bin
 
   // For the row's largest logit (finite) and temperature.
-  __device__ __forceinline__ void set(float top, float temp, const float2* t) {
-    const double c = 1.4426950408889634074 / (double)temp;
+  __device__ __forceinline__ void set(float top, double temp, const ExpTable* t) {
+    const double c = 1.4426950408889634074 / temp;
     c_hi = (float)c;
     c_lo = (float)(c - (double)c_hi);
-    m = top;
     table = t;
     const double e = (double)top * c;
-    far = !(fabs(e) < 2000.0);
+    const bool far = !(fabs(e) < 2000.0);
+    shift = far ? top : 0.0f;
     const double r = far ? 1.0 : ceil(e * 2048.0) * (1.0 / 2048.0) + 1.0;
     k = (float)(6144.0 - r);
     least = fminf((float)(far ? (double)top - 46.0 / c : (r - 47.0) / c), top);
   }
-  // The argument of the exponential as a float and what it lacks. (Operations by
-  // name: a token has the same weight and bin wherever they are computed, which
-  // a multiplication and addition that the compiler may join would not give.)
-  __device__ __forceinline__ float exponent(float l, float& rest) const {
-    if (!far) {
-      const float p = __fmul_rn(l, c_hi);
-      rest = __fmaf_rn(l, c_lo, __fmaf_rn(l, c_hi, -p));
-      return p;
-    }
-    const float d = __fsub_rn(l, m), b = __fsub_rn(d, l);
-    const float dl = __fsub_rn(__fsub_rn(l, __fsub_rn(d, b)), __fadd_rn(m, b));   // d + dl = l - m exactly
-    const float p = __fmul_rn(d, c_hi);
-    rest = __fmaf_rn(dl, c_hi, __fmaf_rn(d, c_lo, __fmaf_rn(d, c_hi, -p)));
-    return p;
+  // The logarithm of a weight as a part of 2^46, to base 2.
+  __device__ __forceinline__ double log2_of(float l, double temp) const {
+    return ((double)l - (double)shift) * (1.4426950408889634074 / temp) - (6144.0 - (double)k);
   }
-  // l >= least. `top16`: the weight's leading 16 bits, its power of two apart.
-  __device__ __forceinline__ uint64_t operator()(float l, uint32_t* top16 = nullptr) const {
-    float rest;
-    const float p = exponent(l, rest), nm = __fadd_rn(p, k);
-    const float q = __fadd_rn(__fsub_rn(p, __fsub_rn(nm, k)), rest);
-    const int bits = __float_as_int(nm);
-    const float2 t = table[bits & (kExpSteps - 1)];
+
+  // N (even) weights, for logits of at least `least` (others give anything), and their bits: the
+  // exponent in steps of 2^-11. Two at a time, an operation for both.
+  template <int N> __device__ __forceinline__ void operator()(const float (&l)[N], uint64_t (&w)[N], int (&bits)[N],
+                                                              uint32_t* top16 = nullptr) const {
+    using namespace tc;
+    const uint64_t ch = f2_packf(c_hi, c_hi), minus_ch = f2_packf(-c_hi, -c_hi), minus_cl = f2_packf(-c_lo, -c_lo);
+    const uint64_t kk = f2_packf(k, k), sh = f2_packf(shift, shift);
     constexpr float kLn2 = 0.693147180559945f, kHalfSquare = 0.240226506959101f;
-    const int low = __float2int_rn(__fmaf_rn(__fmul_rn(t.x, q), __fmaf_rn(q, kHalfSquare, kLn2), t.y));
-    const uint32_t mant = (__float_as_uint(t.x) & 0x7fffffu) | 0x800000u;
-    const uint64_t w = ((uint64_t)mant << 17) + (int64_t)low;      // about 2^40 .. 2^41
-    if (top16) *top16 = (uint32_t)(w >> 25);
-    const int e = (kMagic >> 11) - (bits >> 11);                   // at least 1
-    return ((w << 6) >> e) | (e > 6 ? 1u : 0u);
+    const uint64_t ln2 = f2_packf(kLn2, kLn2), half_square = f2_packf(kHalfSquare, kHalfSquare);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t x = f2_sub(f2_packf(l[i], l[i + 1]), sh);
+      const uint64_t p = f2_mul(x, ch);
+      const uint64_t over = f2_fma(x, minus_cl, f2_fma(x, minus_ch, p));    // p - x c
+      const uint64_t nm = f2_add(p, kk);
+      const uint64_t q = f2_sub(f2_sub(p, f2_sub(nm, kk)), over);
+      bits[i] = (int)(uint32_t)nm;
+      bits[i + 1] = (int)(uint32_t)(nm >> 32);
+      const int j0 = bits[i] & (kExpSteps - 1), j1 = bits[i + 1] & (kExpSteps - 1);
+      const float t0 = table->hi[j0], t1 = table->hi[j1];
+      const float2 low = f2_unpack(f2_fma(f2_mul(f2_packf(t0, t1), q), f2_fma(q, half_square, ln2),
+                                          f2_packf(table->lo[j0], table->lo[j1])));
+      finish(t0, low.x, bits[i], w[i], top16 ? top16 + i : nullptr);
+      finish(t1, low.y, bits[i + 1], w[i + 1], top16 ? top16 + i + 1 : nullptr);
+    }
   }
-  // The weight's place among 32 to an octave, falling; a rising logit never rises in it.
+  // T[j] as a 24-bit integer with what is to be added: about 2^40 .. 2^41, then 2^6 times that, cut to
+  // its place.
+  static __device__ __forceinline__ void finish(float t, float low, int bits, uint64_t& w, uint32_t* top16) {
+    const uint32_t mant = (__float_as_uint(t) & 0x7fffffu) | 0x800000u;
+    const uint64_t v = ((uint64_t)mant << 23) + (int64_t)__float2int_rn(low) * 64;
+    if (top16) *top16 = (uint32_t)(v >> 31);
+    w = (v >> ((kMagic >> 11) - (bits >> 11))) | 1u;
+  }
+  __device__ __forceinline__ uint64_t one(float l) const {
+    const float two[2] = {l, l};
+    uint64_t w[2];
+    int bits[2];
+    (*this)(two, w, bits);
+    return w[0];
+  }
+  // The weight's place among 16 to an octave, falling; a rising logit never rises in it. The same
+  // operations as above: a token has the same bin wherever it is computed.
   __device__ __forceinline__ int bin(float l) const {
-    float rest;
-    const float nm = __fadd_rn(exponent(fmaxf(l, least), rest), k);
-    return (kMagic >> 6) - (__float_as_int(nm) >> 6);
+    return bin_of(__float_as_int(__fadd_rn(__fmul_rn(__fsub_rn(fmaxf(l, least), shift), c_hi), k)));
   }
+  static __device__ __forceinline__ int bin_of(int bits) { return (kMagic >> kBinShift) - (bits >> kBinShift); }
+  static __device__ __forceinline__ int octave_of(int bin) { return (bin + 15) / 16; }
 };
-constexpr int kWeightBins = 1536;    // 47 octaves and a little
 
 // Floats as integers of the same order (both zeros alike), and back.
 __device__ __forceinline__ uint32_t order_key(float l) {
