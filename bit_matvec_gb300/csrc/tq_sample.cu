@@ -68,6 +68,8 @@ struct alignas(16) Shared {
   u64 scan[kWarps];
   u64 give[4];                // what the other blocks of the cluster read
   u64 pick[6];
+  double log_total;           // ln of the kept weights' sum over 2^46
+  float min_p[2];             // T ln(min-p) as a sum
   int have;                   // entries of the list
   float top;
   int first;                  // lowest index of the largest logit
@@ -187,27 +189,50 @@ __device__ __noinline__ Sum over_cluster(Shared* s, u64 mine, int at, int cluste
   const u64 before = __shfl_sync(0xffffffffu, v, max(rank - 1, 0));
   return {rank > 0 ? before : 0, __shfl_sync(0xffffffffu, v, kMaxCluster - 1)};
 }
-// The first n of kList values, falling; behind them are zeros up to the next
-// power of two. By as many warps as have pairs.
-__device__ __noinline__ void sort(u64* v, int n) {
-  int size = 2;
+// Sorts the first n of kList values, falling; behind them are zeros up to the
+// next power of two. A value a thread (two above 512), exchanged by shuffles
+// within a warp, else through `v` and `spare` in turn, by the warps that have
+// values.
+__device__ __noinline__ void sort(u64* v, u64* spare, int n) {
+  int size = 32;
   while (size < n) size *= 2;
-  const int threads = max(32, size / 2);
-  const int i = threadIdx.x;
+  const int threads = min(size, kThreads), i = threadIdx.x;
+  const bool two = size > kThreads;
   if (i < threads) {
+    u64 x = v[i], y = two ? v[i + kThreads] : 0;
+    u64* from = spare;
+    u64* next = v;
+#pragma unroll 1
     for (int k = 2; k <= size; k *= 2)
+#pragma unroll 1
       for (int j = k / 2; j > 0; j /= 2) {
-        if (i < size / 2) {
-          const int a = 2 * i - (i & (j - 1)), b = a + j;
-          const u64 x = v[a], y = v[b];
-          if ((x < y) == ((a & k) == 0)) {
-            v[a] = y;
-            v[b] = x;
-          }
+        if (j == kThreads) {               // the whole, falling: a thread's two
+          const u64 a = max(x, y);
+          y = min(x, y);
+          x = a;
+          continue;
         }
-        if (threads == 32) __syncwarp();
-        else named_barrier_sync(1, threads);
+        u64 p, q = 0;
+        if (j < 32) {
+          p = __shfl_xor_sync(0xffffffffu, x, j);
+          if (two) q = __shfl_xor_sync(0xffffffffu, y, j);
+        } else {
+          from[i] = x;
+          if (two) from[i + kThreads] = y;
+          named_barrier_sync(1, threads);
+          p = from[i ^ j];
+          if (two) q = from[(i ^ j) + kThreads];
+          u64* const t = from;
+          from = next;
+          next = t;
+        }
+        const bool low = (i & j) == 0;
+        x = low == ((i & k) == 0) ? max(x, p) : min(x, p);
+        if (two) y = low == (((i + kThreads) & k) == 0) ? max(y, q) : min(y, q);
       }
+    named_barrier_sync(1, threads);        // (the last exchange through memory is read)
+    v[i] = x;
+    if (two) v[i + kThreads] = y;
   }
   __syncthreads();
 }
@@ -551,7 +576,7 @@ template <typename T> struct Row {
       if (at < kList) s->list[at] = at < n ? remote_u64(remote(&s->list[at - base], r)) : 0;
     }
     __syncthreads();
-    sort(s->list, n);
+    sort(s->list, s->weight, n);
 #pragma unroll
     for (int j = 0; j < kList / kThreads; ++j) {
       const int i = tid + j * kThreads;
@@ -561,53 +586,56 @@ template <typename T> struct Row {
     __syncthreads();
     return n;
   }
-  // (rank 0) The number of sorted entries, at least 1, whose weights sum to
-  // `target`.
-  __device__ __forceinline__ int needed(int n, u64 target) const {
-    const u64 x = s->weight[2 * threadIdx.x], y = s->weight[2 * threadIdx.x + 1];
-    const u64 at = scan(s, x + y).before;
-    const u64 less = (at + x < target ? 1 : 0) + (at + x + y < target ? 1 : 0);
-    return max(1, min(n, (int)scan(s, less).all + 1));
-  }
-  // (rank 0) The sum of the first n entries' weights.
-  __device__ __forceinline__ u64 weight_of(int n) const {
+  // (rank 0) The sums of the sorted weights up to each entry, in `sums`.
+  __device__ __forceinline__ void sum_up(u64* sums) const {
     const int i = 2 * threadIdx.x;
-    return scan(s, (i < n ? s->weight[i] : 0) + (i + 1 < n ? s->weight[i + 1] : 0)).all;
+    const u64 x = s->weight[i], y = s->weight[i + 1], at = scan(s, x + y).before;
+    sums[i] = at + x;
+    sums[i + 1] = at + x + y;
+    __syncthreads();
   }
 };
+
+// (rank 0) The number of entries for which `counts` holds.
+template <typename C> __device__ __forceinline__ int count_of(C counts) {
+  const int i = threadIdx.x;
+  return __syncthreads_count(counts(i)) + __syncthreads_count(counts(i + kThreads));
+}
 
 // The place of the draw among weights that sum to `total`.
 __device__ __forceinline__ u64 goal_of(u64 total, float u) {
   return u > 0.0f ? (u < 1.0f ? min(fraction_of(total, u, false), total - 1) : total - 1) : 0;
 }
 
-__device__ __noinline__ void answer(const Args& a, Weigher weigh, int64_t row, int token, float l, double temp,
-                                    u64 total) {
+// ln(total / 2^46), for `answer`: by a thread that has nothing else to do.
+__device__ __noinline__ void take_log(Shared* s, u64 total) { s->log_total = log((double)total * 0x1p-46); }
+
+__device__ __noinline__ void answer(Shared* s, const Args& a, Weigher weigh, int64_t row, int token, float l, double temp) {
   a.tokens[row] = token;
   // ln(w / total), both as parts of 2^46
-  if (a.logp)
-    a.logp[row] = (float)(weigh.log2_of(l, temp) * 0.69314718055994530942 - log((double)total * 0x1p-46));
+  if (a.logp) a.logp[row] = (float)(weigh.log2_of(l, temp) * 0.69314718055994530942 - s->log_total);
 }
 
-// (rank 0) The draw from a sorted list that holds all kept tokens.
-__device__ __noinline__ void draw_from_list(Shared* s, const Args& a, Weigher weigh, int64_t row, int kept,
-                                            u64 total, double temp, float u) {
+// (rank 0) The draw from a sorted list whose first `kept` entries are the kept
+// tokens; by_index and spare: room for kList values each.
+__device__ __noinline__ void draw_from_list(Shared* s, u64* by_index, u64* spare, const Args& a, Weigher weigh,
+                                            int64_t row, int kept, u64 total, double temp, float u) {
   const int tid = threadIdx.x;
   const u64 goal = goal_of(total, u);
-  // by rising index: the complemented index, then the entry; in the table's
-  // place (the weights are all computed)
-  u64* const by_index = reinterpret_cast<u64*>(&s->table);
-  static_assert(sizeof(s->table) >= kList * sizeof(u64) && kList == 1 << 10, "an entry below an index");
+  // by rising index: the complemented index, then the entry
+  static_assert(kList == 1 << 10, "an entry below an index");
   for (int i = tid; i < kList; i += kThreads)
     by_index[i] = i < kept ? u64(1) << 63 | (s->list[i] & kIndexMask) << 10 | (u64)i : 0;
   __syncthreads();
-  sort(by_index, kept);
+  if (tid == kThreads - 1) take_log(s, total);
+  __syncwarp();
+  sort(by_index, spare, kept);
   const u64 p = by_index[2 * tid], q = by_index[2 * tid + 1];
   const u64 x = p ? s->weight[p & (kList - 1)] : 0, y = q ? s->weight[q & (kList - 1)] : 0;
   const u64 at = scan(s, x + y).before;
   if (at <= goal && goal < at + x + y) {
     const u64 e = s->list[(goal < at + x ? p : q) & (kList - 1)];
-    answer(a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), temp, total);
+    answer(s, a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), temp);
   }
 }
 
@@ -629,6 +657,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float temp = a.temperature ? a.temperature[row] : 1.0f;
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
+  const float t = fminf(temp, 0x1p100f);
+  if (tid == kThreads - 1 && mp > 0.0f) {      // one thread, while the slice comes
+    const double d = (double)t * log((double)mp);
+    s->min_p[0] = (float)d;
+    s->min_p[1] = (float)(d - (double)s->min_p[0]);
+  }
   const int from = rank * a.slice, count = max(0, min(a.slice, a.vocab - from));
   const T* const x = static_cast<const T*>(a.logits) + row * a.stride + from;
   // in shared memory as it lies in memory within 16 bytes, so that whole pieces are copied
@@ -702,13 +736,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       top = 0.0f;
       __syncthreads();
     }
-    const double t = fmin((double)temp, 0x1p100);
-    r.weigh.set(top, t, &s->table);
+    r.weigh.set_temperature(t);
+    r.weigh.set_top(top, t, &s->table);
     const uint32_t top_key = order_key(top);
     u64 floor = kNoCut;       // of min-p
     if (mp > 0.0f) {
-      const float least = fminf(__double2float_ru((double)top + t * log((double)mp)), top);
-      floor = (u64)order_key(least) << kIndexBits;
+      // the least float that is top + T ln(min-p) or above: the sum, and one up if it was rounded down
+      const float hi = s->min_p[0], lo = s->min_p[1];
+      const float sum = __fadd_rn(top, hi), b = __fsub_rn(sum, top);
+      const float off = __fadd_rn(__fadd_rn(__fsub_rn(top, __fsub_rn(sum, b)), __fsub_rn(hi, b)), lo);
+      const float least = hi < 0.0f ? sum : top;
+      const uint32_t key = order_key(least) + (hi < 0.0f && off > 0.0f ? 1u : 0u);
+      floor = (u64)min(key, top_key) << kIndexBits;
     }
     const bool by_count = k > 0 && k < a.vocab, by_weight = p < 1.0f;
     bool drawn = false;       // by rank 0, from the list
@@ -728,21 +767,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       u64 found = 0;
       if (rank == 0) {
         n = r.join();
+        u64* const sums = reinterpret_cast<u64*>(&s->table);     // (the weights are all computed)
+        static_assert(sizeof(s->table) >= 2 * kList * sizeof(u64), "");
         if (whole) {
-          int kept = weights ? r.needed(n, target) : min(n, k);
-          if (!weights && by_weight) {
-            const u64 goal = p > 0.0f ? max(u64(1), fraction_of(r.weight_of(kept), p, true)) : 1;
-            kept = min(kept, r.needed(kept, goal));
+          r.sum_up(sums);
+          int kept = weights ? n : min(n, k);
+          if (by_weight) {
+            const u64 goal = weights ? target : p > 0.0f ? max(u64(1), fraction_of(sums[kept - 1], p, true)) : 1;
+            kept = min(kept, count_of([&](int i) { return sums[i] < goal; }) + 1);
           }
-          if (floor != kNoCut) {
-            const int i = 2 * tid;
-            const u64 over = (i < kept && s->list[i] >= floor ? 1 : 0) +
-                             (i + 1 < kept && s->list[i + 1] >= floor ? 1 : 0);
-            kept = max(1, (int)scan(s, over).all);
-          }
-          draw_from_list(s, a, r.weigh, row, kept, r.weight_of(kept), t, u);
+          if (floor != kNoCut) kept = max(1, min(kept, count_of([&](int i) { return s->list[i] >= floor; })));
+          const u64 total = sums[kept - 1];
+          draw_from_list(s, sums + kList, sums, a, r.weigh, row, kept, total, (double)t, u);
         } else {
-          const int need = !weights ? min(n, (int)(target - w.above)) : target > above ? r.needed(n, target - above) : 1;
+          int need = min(n, (int)(target - w.above));
+          if (weights) {
+            // (the table stays: there are weights to come)
+            need = 1;
+            if (target > above) {
+              r.sum_up(s->weight);
+              need = min(n, count_of([&](int i) { return s->weight[i] < target - above; }) + 1);
+            }
+          }
           found = s->list[max(0, need - 1)];
           if (tid < a.cluster) remote_put(remote(&s->give[2], tid), found);
         }
@@ -784,6 +830,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const Sum block = scan(s, tid < r.blocks ? s->sums[tid] : 0);
       const Sum slices = over_cluster(s, block.all, 3, a.cluster, rank);
       const u64 goal = goal_of(slices.all, u);
+      if (tid == kThreads - 1) take_log(s, slices.all);
+      __syncwarp();
       if (slices.before <= goal && goal < slices.before + block.all) {       // (the same for all threads of a block)
         const u64 at = slices.before + block.before;
         if (tid < r.blocks && at <= goal && goal < at + s->sums[tid]) {
@@ -795,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const float l = i >= pad && i < end ? Elem<T>::up(xs[i]) : NAN;
         const u64 mine = kept(l, i) ? r.weigh.one(l) : 0;
         const u64 before = s->pick[1] + scan(s, mine).before;
-        if (before <= goal && goal < before + mine) answer(a, r.weigh, row, r.start + i, l, t, slices.all);
+        if (before <= goal && goal < before + mine) answer(s, a, r.weigh, row, r.start + i, l, (double)t);
       }
     }
   }

@@ -25,7 +25,7 @@ namespace tq {
 
 constexpr int kExpSteps = 2048;      // entries of the table
 
-struct ExpTable {
+struct alignas(16) ExpTable {
   float hi[kExpSteps], lo[kExpSteps];   // 2^(40 + j / kExpSteps) as a sum
 };
 
@@ -58,18 +58,24 @@ struct Weigher {
   static constexpr int kMagic = 0x45c00000;   // the bits of 6144.0f
   static constexpr int kBinShift = 7;         // 2048 / 16 steps a bin
 
-  // For the row's largest logit (finite) and temperature.
-  __device__ __forceinline__ void set(float top, double temp, const ExpTable* t) {
-    const double c = 1.4426950408889634074 / temp;
-    c_hi = (float)c;
-    c_lo = (float)(c - (double)c_hi);
-    table = t;
-    const double e = (double)top * c;
-    const bool far = !(fabs(e) < 2000.0);
+  // log2(e) / T as a sum, for a temperature of 2^-100 .. 2^100. (By 32-bit
+  // operations, here and below: a block's 512 threads wait ten microseconds for
+  // the same few in 64 bits.)
+  __device__ __forceinline__ void set_temperature(float t) {
+    constexpr float kHi = 1.44269504088896341f, kLo = (float)(1.44269504088896341 - (double)kHi);
+    c_hi = __fdiv_rn(kHi, t);
+    c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c_hi, t, kHi), kLo), t);
+  }
+  // For the row's largest logit (finite).
+  __device__ __forceinline__ void set_top(float top, float t, const ExpTable* from) {
+    table = from;
+    const float p = __fmul_rn(top, c_hi), octave = __fmul_rn(t, 0.693147180559945f);
+    const bool far = !(fabsf(p) < 2000.0f);
     shift = far ? top : 0.0f;
-    const double r = far ? 1.0 : ceil(e * 2048.0) * (1.0 / 2048.0) + 1.0;
-    k = (float)(6144.0 - r);
-    least = fminf((float)(far ? (double)top - 46.0 / c : (r - 47.0) / c), top);
+    // (one step more for what c_lo adds)
+    const float r = far ? 1.0f : ceilf(p * 2048.0f) * (1.0f / 2048.0f) + (1.0f + 1.0f / 2048.0f);
+    k = 6144.0f - r;
+    least = fminf(far ? top - 46.0f * octave : (r - 47.0f) * octave, top);
   }
   // The logarithm of a weight as a part of 2^46, to base 2.
   __device__ __forceinline__ double log2_of(float l, double temp) const {
