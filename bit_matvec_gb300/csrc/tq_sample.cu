@@ -19,7 +19,6 @@
 // in which threads add.
 #include <algorithm>
 #include <cmath>
-#include <cstddef>
 
 #include "tq_requests.cuh"
 #include "tq_weight.cuh"
@@ -61,18 +60,27 @@ struct Args {
 // Shared memory before the slice.
 struct alignas(16) Shared {
   ExpTable table;
-  u64 list[kList];            // places of the tokens at a cut
-  u64 weight[kList];          // (rank 0) their weights
+  union {
+    struct {
+      u64 list[kList];        // places of the tokens at a cut
+      u64 weight[kList];      // (rank 0) their weights
+    };
+    struct {                  // before there is a list
+      u64 first[kWeightBins]; // (rank 0) sums of a bin at most; (narrowing, every block) sums of its own
+      u64 sums[kWeightBins];  // (rank 0) sums of a bin
+      uint32_t tokens[kWeightBins];
+    } by_bin;
+  };
   uint32_t bins[kWeightBins]; // tokens, or leading bits of weights
   u64 sums[kMaxBlocks];       // kept weights by block
+  int octaves[kMaxBlocks];    // of a row without filters: what they are relative to
   u64 scan[kWarps];
-  u64 give[4];                // what the other blocks of the cluster read
-  u64 pick[6];
-  double log_total;           // ln of the kept weights' sum over 2^46
-  float min_p[2];             // T ln(min-p) as a sum
+  u64 give[6];                // what the other blocks of the cluster read
+  u64 window[8];              // what rank 0 found
   int have;                   // entries of the list
-  float top;
   int first;                  // lowest index of the largest logit
+  u64 pick[2];
+  uint32_t least_top[kWarps];
 };
 static_assert(sizeof(Shared) % 16 == 0, "the slice behind it in 16-byte pieces");
 
@@ -239,47 +247,51 @@ __device__ __noinline__ void sort(u64* v, u64* spare, int n) {
 
 struct Window {
   u64 lo, hi;       // places
-  u64 above;        // tokens above it (by count), their weight (by weight, where exact)
+  u64 above;        // tokens above it (a narrowed one by weight: what they weigh)
   u64 inside;       // tokens in it, at most
   u64 upto;         // tokens in it or above, at most
 };
 
-// Among the bins of all threads (n tokens at most; lo to hi of what counts, `above` before the first):
-// the first that may reach `target` in pick[0], what is before it in pick[2] and the tokens in pick[4];
-// the first that surely does in pick[1] (kWeightBins if none), the tokens up to it in pick[5].
-__device__ __forceinline__ void pick_bins(Shared* s, const u64 (&n)[4], const u64 (&lo)[4], const u64 (&hi)[4],
-                                          bool differ, u64 target, u64 above) {
-  const int tid = threadIdx.x;
-  u64 at_lo = above + scan(s, lo[0] + lo[1] + lo[2] + lo[3]).before;
-  u64 at_hi = differ ? above + scan(s, hi[0] + hi[1] + hi[2] + hi[3]).before : at_lo;
-  const Sum tokens = scan(s, n[0] + n[1] + n[2] + n[3]);
-  u64 at_n = tokens.before;
-  if (tid == 0) {
-    s->pick[0] = 0;
-    s->pick[1] = kWeightBins;
-    s->pick[2] = above;
-    s->pick[4] = 0;
-    s->pick[5] = tokens.all;
-  }
-  __syncthreads();
-  if (tid < kWeightBins / 4) {
+// By one warp: the first of kWeightBins values v for which above + the sum up to
+// it reaches `target` (kWeightBins if none does), and what is before it.
+struct Found {
+  int bin;
+  u64 before;
+};
+__device__ __noinline__ Found first_reaching(const u64* v, u64 target, u64 above) {
+  constexpr int kEach = kWeightBins / 32;
+  static_assert(kEach <= 32, "a bin of a lane's share a lane");
+  const int lane = threadIdx.x & 31;
+  u64 sum = 0;
+#pragma unroll 8
+  for (int e = 0; e < kEach; ++e) sum += v[lane * kEach + (e + lane) % kEach];   // (no two lanes in one bank)
+  u64 upto = sum;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (at_hi < target && at_hi + hi[e] >= target) {
-        s->pick[0] = 4 * tid + e;
-        s->pick[2] = at_lo;
-        s->pick[4] = at_n;
-      }
-      if (at_lo < target && at_lo + lo[e] >= target) {
-        s->pick[1] = 4 * tid + e;
-        s->pick[5] = at_n + n[e];
-      }
-      at_lo += lo[e];
-      at_hi += hi[e];
-      at_n += n[e];
-    }
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
   }
-  __syncthreads();
+  const unsigned m = __ballot_sync(0xffffffffu, above + upto >= target);
+  if (m == 0) return {kWeightBins, above + __shfl_sync(0xffffffffu, upto, 31)};
+  const int share = __ffs(m) - 1;
+  const u64 base = above + __shfl_sync(0xffffffffu, upto - sum, share);
+  const u64 x = lane < kEach ? v[share * kEach + lane] : 0;
+  upto = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const int at = __ffs(__ballot_sync(0xffffffffu, base + upto >= target)) - 1;
+  return {share * kEach + at, base + __shfl_sync(0xffffffffu, upto - x, at)};
+}
+// By one warp: the sum of the first n of kWeightBins values.
+__device__ __noinline__ u64 sum_before(const uint32_t* v, int n) {
+  u64 sum = 0;
+  for (int i = threadIdx.x & 31; i < n; i += 32) sum += v[i];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
 }
 
 template <typename T> struct Row {
@@ -337,11 +349,22 @@ template <typename T> struct Row {
 
   // ---- finding a cut
 
-  // The least place of a weight's bin of at most b.
+  // By one warp: the least place of a weight's bin of at most b.
   __device__ __forceinline__ u64 bin_end(int b, uint32_t top_key) const {
     const uint32_t lane = threadIdx.x & 31;
-    // the least key whose bin is at most b: 32 candidates a step
-    uint32_t lo = 0, hi = top_key + 1;     // (above all tokens, if none has such a bin)
+    // Where the exponent passes the bin's end, to a few steps of a float: half a
+    // step of 2^-11 below the multiple that begins it.
+    const float edge = __int_as_float(((Weigher::kMagic >> Weigher::kBinShift) - b) << Weigher::kBinShift);
+    const float guess = __fdiv_rn((edge - 0x1p-12f) - weigh.k, weigh.c_hi) + weigh.shift;
+    if (weigh.bin(key_value(top_key)) > b) return (u64)(top_key + 1) << kIndexBits;   // above all tokens
+    uint32_t lo = 0, hi = top_key;         // (whose bin is at most b)
+    const uint32_t near = order_key(guess);
+    if (top_key > 31) {
+      const uint32_t base = min(near - min(near, 16u), top_key - 31);
+      const unsigned m = __ballot_sync(0xffffffffu, weigh.bin(key_value(base + lane)) <= b);
+      if (m != 0 && !(m & 1u)) lo = hi = base + (__ffs(m) - 1);
+    }
+    // otherwise the least key whose bin is at most b, 32 candidates a step
     while (lo < hi) {
       const uint32_t step = (hi - lo) / 32 + 1, at = lo + lane * step;
       const bool in = at < hi && weigh.bin(key_value(at)) <= b;
@@ -357,19 +380,35 @@ template <typename T> struct Row {
     return (u64)lo << kIndexBits;
   }
 
+  // What rank 0 found, for all blocks.
+  __device__ __forceinline__ void publish(const Window& w, u64 target) const {
+    const int lane = threadIdx.x & 31;
+    if (lane < cluster) {
+      const uint32_t to = remote(s->window, lane);
+      remote_put(to, w.lo);
+      remote_put(to + 8, w.hi);
+      remote_put(to + 16, w.above);
+      remote_put(to + 24, w.inside);
+      remote_put(to + 32, w.upto);
+      remote_put(to + 40, target);
+    }
+  }
+  __device__ __forceinline__ Window published(u64& target) const {
+    meet(cluster);
+    target = s->window[5];
+    return {s->window[0], s->window[1], s->window[2], s->window[3], s->window[4]};
+  }
+
   // The range around the cut, of tokens from `from` on: by count, the least
-  // place such that `target` tokens are at it or above; by weight, such that
-  // they weigh `target` at least, the share `share` of all, whose sum is
-  // returned in *all.
-  __device__ __forceinline__ Window search(bool by_weight, u64& target, u64 from, uint32_t top_key, u64* all,
-                                           float share) const {
+  // place such that `target` tokens are at it or above, none of which is below
+  // `least_top`; by weight, such that they weigh the share `share` of all at
+  // least. The bins are zeros.
+  __device__ __forceinline__ Window search(bool by_weight, u64& target, u64 from, uint32_t top_key, float share,
+                                           float least_top) const {
     const int tid = threadIdx.x;
-    Window w = {from, ((u64)top_key << kIndexBits) | kIndexMask, 0, 0, 0};
     // (tokens that weigh nothing do not help to reach a weight)
-    if (by_weight) w.lo = max(from, (u64)order_key(weigh.least) << kIndexBits);
-    meet(cluster);                       // (the last reading of the bins is over)
-    for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
-    __syncthreads();
+    Window w = {max(from, (u64)order_key(by_weight ? weigh.least : least_top) << kIndexBits),
+                ((u64)top_key << kIndexBits) | kIndexMask, 0, 0, 0};
     if (by_weight) {
       u64 mine = 0;
       const float lo = fmaxf(weigh.least, key_value(max((uint32_t)(from >> kIndexBits), order_key(-INFINITY))));
@@ -389,56 +428,76 @@ template <typename T> struct Row {
             atomicAdd(&s->bins[Weigher::bin_of(bits[e])], top16[e]);
           }
       });
-      *all = over_cluster(s, scan(s, mine).all, 0, cluster, rank).all;
-      target = share > 0.0f ? max(u64(1), fraction_of(*all, share, true)) : 1;
+      const u64 sum = scan(s, mine).all;
+      if (tid == 0) s->give[0] = sum;
     } else {
       each([&](const float (&l)[4], int) {
+        if (fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= least_top) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (l[e] == l[e]) atomicAdd(&s->bins[weigh.bin(l[e])], 1u);
+          for (int e = 0; e < 4; ++e)
+            if (l[e] >= least_top) atomicAdd(&s->bins[weigh.bin(l[e])], 1u);
+        }
       });
-      meet(cluster);
     }
-    // this thread's four bins, of all blocks: tokens (at most), and what counts, at least and at most
-    u64 n[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
-    if (tid < kWeightBins / 4) {
-      for (int r0 = 0; r0 < cluster; r0 += 8) {
-        uint4 v[8];
+    meet(cluster);
+    if (rank == 0) {
+      // all blocks' bins: tokens (at most), and what counts, at least and at most
+      u64* const lo = s->by_bin.sums;
+      u64* const hi = by_weight ? s->by_bin.first : lo;
+      uint32_t* const tokens = s->by_bin.tokens;
+      if (tid < kWeightBins / 4) {
+        u64 n[4] = {0, 0, 0, 0};
+        for (int r0 = 0; r0 < cluster; r0 += 8) {
+          uint4 v[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          v[r] = r0 + r < cluster ? remote_u128(remote(&s->bins[4 * tid], r0 + r)) : make_uint4(0, 0, 0, 0);
+          for (int r = 0; r < 8; ++r)
+            v[r] = r0 + r < cluster ? remote_u128(remote(&s->bins[4 * tid], r0 + r)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          n[0] += v[r].x;
-          n[1] += v[r].y;
-          n[2] += v[r].z;
-          n[3] += v[r].w;
+          for (int r = 0; r < 8; ++r) {
+            n[0] += v[r].x;
+            n[1] += v[r].y;
+            n[2] += v[r].z;
+            n[3] += v[r].w;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = 4 * tid + e;
+          if (by_weight) {
+            // Sums of weights' first 16 bits, 2^15 - 8 at least (just below a
+            // power of two the table's entry is that power's): a token for each of
+            // these in the sum, at most, each cut by less than one and off by a unit.
+            const int octave = Weigher::octave_of(b);
+            const u64 most = (n[e] + (n[e] >> 11)) >> 15, v = (n[e] << 31) >> octave;
+            lo[b] = v - min(v, most);
+            hi[b] = most ? (((n[e] + most) << 31) >> octave) + most + 1 : 0;
+            tokens[b] = (uint32_t)most;
+          } else {
+            lo[b] = n[e];
+            tokens[b] = (uint32_t)n[e];
+          }
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      __syncthreads();
+      if (tid < 32) {
         if (by_weight) {
-          // Sums of weights' first 16 bits, 2^15 - 8 at least (just below a
-          // power of two the table's entry is that power's): a token for each of
-          // these in the sum, at most, each cut by less than one and off by a unit.
-          const int octave = Weigher::octave_of(4 * tid + e);
-          const u64 tokens = (n[e] + (n[e] >> 11)) >> 15, v = (n[e] << 31) >> octave;
-          lo[e] = v - min(v, tokens);
-          hi[e] = tokens ? (((n[e] + tokens) << 31) >> octave) + tokens + 1 : 0;
-          n[e] = tokens;
-        } else {
-          lo[e] = hi[e] = n[e];
+          u64 all = tid < cluster ? remote_u64(remote(&s->give[0], tid)) : 0;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+          target = share > 0.0f ? max(u64(1), fraction_of(all, share, true)) : 1;
         }
+        const Found first = first_reaching(hi, target, 0);       // may reach the target
+        const Found last = by_weight ? first_reaching(lo, target, 0) : first;   // surely does
+        const u64 before = sum_before(tokens, first.bin);
+        w.upto = sum_before(tokens, min(last.bin + 1, kWeightBins));
+        w.inside = w.upto - before;
+        w.above = before;
+        if (first.bin > 0) w.hi = min(w.hi, bin_end(first.bin - 1, top_key) - 1);
+        w.lo = max(w.lo, last.bin < kWeightBins ? bin_end(last.bin, top_key) : 0);
+        publish(w, target);
       }
     }
-    pick_bins(s, n, lo, hi, by_weight, target, 0);
-    const int first = (int)s->pick[0], last = (int)s->pick[1];
-    if (first > 0) w.hi = bin_end(first - 1, top_key) - 1;
-    w.lo = max(w.lo, last < kWeightBins ? bin_end(last, top_key) : 0);
-    w.inside = s->pick[5] - s->pick[4];
-    w.upto = s->pick[5];
-    w.above = s->pick[2];
-    return w;
+    return published(target);
   }
 
   // Narrows a window until at most kList tokens are inside: equal parts of it,
@@ -447,9 +506,9 @@ template <typename T> struct Row {
   static __device__ __noinline__ Window narrow(Row row, Window w, bool by_weight, u64 target) {
     Shared* const s = row.s;
     const int tid = threadIdx.x;
-    u64* const sums = s->list;
-    static_assert(sizeof(s->list) + sizeof(s->weight) >= kWeightBins * sizeof(u64), "");
-    static_assert(offsetof(Shared, weight) == offsetof(Shared, list) + sizeof(s->list), "one after the other");
+    u64* const sums = s->by_bin.first;
+    u64* const all = s->by_bin.sums;
+    uint32_t* const tokens = s->by_bin.tokens;
     while (w.inside > kList) {
       int shift = 0;
       while (((w.hi - w.lo) >> shift) >= kWeightBins) ++shift;
@@ -468,7 +527,7 @@ template <typename T> struct Row {
           const u64 q = row.place(x, i + e);
           const bool weighs = by_weight && x >= row.weigh.least;
           if (q > w.hi) {
-            if (weighs) above += row.weigh.one(x);
+            above += by_weight ? (weighs ? row.weigh.one(x) : 0) : 1;
           } else if (q >= w.lo) {
             const int j = (int)((w.hi - q) >> shift);
             atomicAdd(&s->bins[j], 1u);
@@ -476,26 +535,32 @@ template <typename T> struct Row {
           }
         }
       });
-      if (by_weight) w.above = over_cluster(s, scan(s, above).all, 0, row.cluster, row.rank).all;
-      else meet(row.cluster);
-      u64 n[4] = {0, 0, 0, 0}, v[4] = {0, 0, 0, 0};
-      if (tid < kWeightBins / 4) {
-        for (int r = 0; r < row.cluster; ++r) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            n[e] += remote_u32(remote(&s->bins[4 * tid + e], r));
-            if (by_weight) v[e] += remote_u64(remote(&sums[4 * tid + e], r));
+      above = over_cluster(s, scan(s, above).all, 1, row.cluster, row.rank).all;
+      if (row.rank == 0) {
+        for (int j = tid; j < kWeightBins; j += kThreads) {
+          uint32_t n = 0;
+          u64 v = 0;
+          for (int r = 0; r < row.cluster; ++r) {
+            n += remote_u32(remote(&s->bins[j], r));
+            if (by_weight) v += remote_u64(remote(&sums[j], r));
           }
+          tokens[j] = n;
+          all[j] = by_weight ? v : n;
+        }
+        __syncthreads();
+        if (tid < 32) {
+          const Found at = first_reaching(all, target, above);
+          const int bin = min(at.bin, kWeightBins - 1);
+          const u64 top = w.hi;
+          w.hi = top - ((u64)bin << shift);
+          w.lo = max(w.lo, top - min(top, ((u64)(bin + 1) << shift) - 1));
+          w.above = at.before;
+          w.inside = tokens[bin];
+          row.publish(w, target);
         }
       }
-      pick_bins(s, n, by_weight ? v : n, by_weight ? v : n, false, target, w.above);
-      const u64 top = w.hi, first = s->pick[0], last = s->pick[1];
-      w.hi = top - (first << shift);
-      w.lo = max(w.lo, top - min(top, ((last + 1) << shift) - 1));
-      w.inside = s->pick[5] - s->pick[4];
-      w.above = s->pick[2];
+      w = row.published(target);
     }
-    meet(row.cluster);     // the last reading of the sums, where the list is, is over
     return w;
   }
 
@@ -607,19 +672,16 @@ __device__ __forceinline__ u64 goal_of(u64 total, float u) {
   return u > 0.0f ? (u < 1.0f ? min(fraction_of(total, u, false), total - 1) : total - 1) : 0;
 }
 
-// ln(total / 2^46), for `answer`: by a thread that has nothing else to do.
-__device__ __noinline__ void take_log(Shared* s, u64 total) { s->log_total = log((double)total * 0x1p-46); }
-
-__device__ __noinline__ void answer(Shared* s, const Args& a, Weigher weigh, int64_t row, int token, float l, double temp) {
+__device__ __noinline__ void answer(const Args& a, Weigher weigh, int64_t row, int token, float l, u64 total,
+                                    bool alone) {
   a.tokens[row] = token;
-  // ln(w / total), both as parts of 2^46
-  if (a.logp) a.logp[row] = (float)(weigh.log2_of(l, temp) * 0.69314718055994530942 - s->log_total);
+  if (a.logp) a.logp[row] = alone ? 0.0f : weigh.log_share(l, total);
 }
 
 // (rank 0) The draw from a sorted list whose first `kept` entries are the kept
 // tokens; by_index and spare: room for kList values each.
 __device__ __noinline__ void draw_from_list(Shared* s, u64* by_index, u64* spare, const Args& a, Weigher weigh,
-                                            int64_t row, int kept, u64 total, double temp, float u) {
+                                            int64_t row, int kept, u64 total, float u) {
   const int tid = threadIdx.x;
   const u64 goal = goal_of(total, u);
   // by rising index: the complemented index, then the entry
@@ -627,16 +689,143 @@ __device__ __noinline__ void draw_from_list(Shared* s, u64* by_index, u64* spare
   for (int i = tid; i < kList; i += kThreads)
     by_index[i] = i < kept ? u64(1) << 63 | (s->list[i] & kIndexMask) << 10 | (u64)i : 0;
   __syncthreads();
-  if (tid == kThreads - 1) take_log(s, total);
-  __syncwarp();
   sort(by_index, spare, kept);
   const u64 p = by_index[2 * tid], q = by_index[2 * tid + 1];
   const u64 x = p ? s->weight[p & (kList - 1)] : 0, y = q ? s->weight[q & (kList - 1)] : 0;
   const u64 at = scan(s, x + y).before;
   if (at <= goal && goal < at + x + y) {
     const u64 e = s->list[(goal < at + x ? p : q) & (kList - 1)];
-    answer(s, a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), temp);
+    answer(a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), total,
+           x + y == total && (x == 0 || y == 0));
   }
+}
+
+// A row without filters, in one pass over its logits as they come from memory:
+// the weights of a block of 512 tokens are relative to its own largest logit, in
+// whole octaves, so that sums join by shifts. False if the row needs the other
+// way: an infinite logit, or a temperature so low that exponents pass 2000.
+template <typename T>
+__device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* from16, Row<T> r, int64_t row, float t,
+                                             float u) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kNone = -(1 << 20);         // octave of a block without a logit above minus infinity
+  enum { kNan = 1, kOther = 2 };
+  r.weigh.set_temperature(t);
+  r.weigh.set_octave(0.0f, &s->table);      // (a warp may have no block of its own)
+  int flags = 0;
+#pragma unroll 1
+  for (int b = warp; b < r.blocks; b += kWarps) {
+    float l[16];
+    const int i0 = b * kBlock + lane * 4;
+    if (b * kBlock >= r.pad && (b + 1) * kBlock <= r.end) {
+      Vec<T, 4> v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const Vec<T, 4>*>(from16 + i0 + j * 128);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) l[e] = Elem<T>::up(v[e >> 2].v[e & 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int i = i0 + (e >> 2) * 128 + (e & 3);
+        l[e] = i >= r.pad && i < r.end ? Elem<T>::up(from16[i]) : -INFINITY;
+      }
+    }
+    float top = l[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) top = max_or_nan(top, l[e]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    u64 sum = 0;
+    int octave = kNone;
+    if (top != top) {
+      flags |= kNan;
+    } else if (top != -INFINITY) {
+      if (top == INFINITY || !(fabsf(top * r.weigh.c_hi) < 1900.0f)) {
+        flags |= kOther;
+      } else {
+        octave = r.weigh.set_octave(top, &s->table);
+        const float least = (float)(octave - 47) / r.weigh.c_hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x[4] = {l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
+          uint64_t w[4];
+          int bits[4];
+          r.weigh(x, w, bits);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += x[e] >= least ? w[e] : 0;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      }
+    }
+    if (lane == 0) {
+      s->sums[b] = sum;
+      s->octaves[b] = octave;
+    }
+  }
+  // ---- this block's sum, and the cluster's
+  if (tid == 0) s->have = 0;
+  __syncthreads();
+  if (flags && lane == 0) atomicOr(&s->have, flags);
+  int top = tid < r.blocks ? s->octaves[tid] : kNone;
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s->least_top[warp] = (uint32_t)top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, (int)s->least_top[w]);
+  auto shifted = [](u64 v, int by) { return by < 64 ? v >> by : 0; };
+  const u64 block = tid < r.blocks ? shifted(s->sums[tid], top - s->octaves[tid]) : 0;
+  const Sum blocks = scan(s, block);
+  if (tid == 0) {
+    s->give[4] = blocks.all;
+    s->give[5] = (u64)(uint32_t)top << 32 | (uint32_t)s->have;
+  }
+  meet(r.cluster);
+  u64 v = 0, what = (u64)(uint32_t)kNone << 32;
+  if (lane < r.cluster) {
+    v = remote_u64(remote(&s->give[4], lane));
+    what = remote_u64(remote(&s->give[5], lane));
+  }
+  const int octave = (int)(what >> 32);
+  const int highest = __reduce_max_sync(0xffffffffu, octave);
+  flags = (int)__reduce_or_sync(0xffffffffu, (uint32_t)what);
+  if (flags & kNan) flags = kNan;
+  if (flags == kOther) return false;
+  if (flags == kNan || highest == kNone) {
+    if (r.rank == 0 && tid == 0) {
+      a.tokens[row] = -1;
+      if (a.logp) a.logp[row] = NAN;
+    }
+    return true;
+  }
+  v = shifted(v, highest - octave);
+  u64 upto = v;
+#pragma unroll
+  for (int d = 1; d < kMaxCluster; d <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const u64 total = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
+  const u64 before = __shfl_sync(0xffffffffu, upto - v, r.rank), mine = __shfl_sync(0xffffffffu, v, r.rank);
+  const u64 goal = goal_of(total, u);
+  if (!(before <= goal && goal < before + mine)) return true;       // (the same for all threads of a block)
+  // ---- the goal in this block's units, then in those of the 512 tokens it falls into
+  const u64 here = min((goal - before) << (highest - top), blocks.all - 1);
+  if (blocks.before <= here && here < blocks.before + block) {
+    s->pick[0] = tid;
+    s->pick[1] = min((here - blocks.before) << (top - s->octaves[tid]), s->sums[tid] - 1);
+  }
+  __syncthreads();
+  const int b = (int)s->pick[0], i = b * kBlock + tid;
+  r.weigh.k = 6144.0f - (float)s->octaves[b];
+  const float l = i >= r.pad && i < r.end ? Elem<T>::up(from16[i]) : -INFINITY;
+  const u64 w = l >= (float)(s->octaves[b] - 47) / r.weigh.c_hi ? r.weigh.one(l) : 0;
+  const u64 at = scan(s, w).before;
+  if (at <= s->pick[1] && s->pick[1] < at + w) {
+    r.weigh.k = 6144.0f - (float)highest;      // what the total is relative to
+    answer(a, r.weigh, row, r.start + i, l, total, shifted(w, highest - s->octaves[b]) == total);
+  }
+  return true;
 }
 
 template <typename T>
@@ -649,25 +838,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int64_t row = blockIdx.x / a.cluster;
   for (int j = tid; j < (int)(sizeof(ExpTable) / 16); j += kThreads)
     reinterpret_cast<uint4*>(&s->table)[j] = reinterpret_cast<const uint4*>(&g_exp_table)[j];
+  for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
   if (tid == 0) s->first = 0x7fffffff;
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  // ---- the slice, its largest logit, and whether there is a NaN
   const float temp = a.temperature ? a.temperature[row] : 1.0f;
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
   const float t = fminf(temp, 0x1p100f);
-  if (tid == kThreads - 1 && mp > 0.0f) {      // one thread, while the slice comes
-    const double d = (double)t * log((double)mp);
-    s->min_p[0] = (float)d;
-    s->min_p[1] = (float)(d - (double)s->min_p[0]);
-  }
+  const bool by_count = k > 0 && k < a.vocab, by_weight = p < 1.0f;
   const int from = rank * a.slice, count = max(0, min(a.slice, a.vocab - from));
   const T* const x = static_cast<const T*>(a.logits) + row * a.stride + from;
   // in shared memory as it lies in memory within 16 bytes, so that whole pieces are copied
   constexpr int kPiece = 16 / (int)sizeof(T);
   const int pad = (int)((uintptr_t)x % 16 / sizeof(T)), end = pad + count;
+  Row<T> r = {s, xs, a.cluster, rank, from - pad, pad, end, count > 0 ? (end + kBlock - 1) / kBlock : 0, {}};
+  if (temp >= 0x1p-100f && temp < INFINITY && !by_count && !by_weight && !(mp > 0.0f)) {
+    __syncthreads();
+    const bool done = draw_unfiltered<T>(s, a, x - pad, r, row, t, u);
+    meet(a.cluster);          // what the other blocks read is read
+    if (done) return;
+  }
+
+  // ---- the slice, its largest logit, and whether there is a NaN
   float top = -INFINITY;
   {
     const uint4* const from16 = reinterpret_cast<const uint4*>(x - pad);
@@ -689,22 +883,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       top = max_or_nan(top, Elem<T>::up(v));
     }
   }
+  // The largest logits of groups of four threads: as many tokens as there are
+  // groups are at least the least of these, so no cut by such a count is below it.
+  uint32_t least_top = 0;
+  {
+    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    least_top = __reduce_min_sync(0xffffffffu, order_key(top));
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float* const tops = reinterpret_cast<float*>(s->scan);
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
+    for (int d = 16; d > 2; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float* const tops = reinterpret_cast<float*>(s->scan);
+    if (lane == 0) {
+      tops[warp] = top;
+      s->least_top[warp] = least_top;
+    }
+    __syncthreads();
+    top = tops[lane & (kWarps - 1)];
+    least_top = __reduce_min_sync(0xffffffffu, s->least_top[lane & (kWarps - 1)]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max_or_nan(top, tops[w]);
-  if (a.cluster > 1) {
-    if (tid == 0) s->top = top;
-    meet(a.cluster);
-    top = lane < a.cluster ? __uint_as_float(remote_u32(remote(&s->top, lane))) : top;
+    for (int d = kWarps / 2; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (a.cluster > 1) {
+      if (tid == 0) s->give[3] = (u64)least_top << 32 | __float_as_uint(top);
+      meet(a.cluster);
+      const u64 v = remote_u64(remote(&s->give[3], min(lane, a.cluster - 1)));
+      top = __uint_as_float((uint32_t)v);
+      least_top = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
   }
-  Row<T> r = {s, xs, a.cluster, rank, from - pad, pad, end, (end + kBlock - 1) / kBlock, {}};
-  if (count == 0) r.blocks = 0;
   if (top != top || top == -INFINITY || !(temp >= 0.0f) || temp == INFINITY) {
     if (rank == 0 && tid == 0) {
       a.tokens[row] = -1;
@@ -729,7 +936,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   } else {
-    if (top == INFINITY) {
+    const bool infinite = top == INFINITY;
+    if (infinite) {
       // beside it every other logit is minus infinity
       for (int i = pad + tid; i < end; i += kThreads)
         xs[i] = Elem<T>::down(Elem<T>::up(xs[i]) == INFINITY ? 0.0f : -INFINITY);
@@ -742,33 +950,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 floor = kNoCut;       // of min-p
     if (mp > 0.0f) {
       // the least float that is top + T ln(min-p) or above: the sum, and one up if it was rounded down
-      const float hi = s->min_p[0], lo = s->min_p[1];
+      float hi, lo;
+      scaled_log(mp, t, s->table, hi, lo);
       const float sum = __fadd_rn(top, hi), b = __fsub_rn(sum, top);
       const float off = __fadd_rn(__fadd_rn(__fsub_rn(top, __fsub_rn(sum, b)), __fsub_rn(hi, b)), lo);
-      const float least = hi < 0.0f ? sum : top;
-      const uint32_t key = order_key(least) + (hi < 0.0f && off > 0.0f ? 1u : 0u);
+      const uint32_t key = hi < 0.0f ? order_key(sum) + (off > 0.0f ? 1u : 0u) : top_key;
       floor = (u64)min(key, top_key) << kIndexBits;
     }
-    const bool by_count = k > 0 && k < a.vocab, by_weight = p < 1.0f;
     bool drawn = false;       // by rank 0, from the list
     bool summed = false;      // s->sums holds the kept weights
     u64 cut = kNoCut;
 #pragma unroll 1
     for (int which = by_count ? 0 : 1; which < (by_weight ? 2 : 1) && !drawn; ++which) {
       const bool weights = which == 1;
-      u64 target = (u64)k, all = 0;
-      Window w = r.search(weights, target, cut, top_key, &all, p);
+      if (weights && by_count) {      // the bins are in use no more, and zeros again
+        meet(a.cluster);
+        for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
+        __syncthreads();
+      }
+      u64 target = (u64)k;
+      const bool bounded = !infinite && k <= a.cluster * (kThreads / 4);
+      Window w = r.search(weights, target, cut, top_key, p, bounded ? key_value(least_top) : -INFINITY);
       // all tokens that may be kept fit in the list
       const bool whole = w.upto <= kList;
       if (whole) w.hi = ((u64)top_key << kIndexBits) | kIndexMask;
       else if (w.inside > kList) w = Row<T>::narrow(r, w, weights, target);
-      const u64 above = over_cluster(s, r.gather(w, weights && !whole), 1, a.cluster, rank).all;
+      const u64 mine = r.gather(w, weights && !whole);
+      u64 above = 0;
+      if (weights && !whole) above = over_cluster(s, mine, 1, a.cluster, rank).all;
+      else meet(a.cluster);
       int n = s->have;        // entries of the list
-      u64 found = 0;
       if (rank == 0) {
         n = r.join();
-        u64* const sums = reinterpret_cast<u64*>(&s->table);     // (the weights are all computed)
-        static_assert(sizeof(s->table) >= 2 * kList * sizeof(u64), "");
+        // room for the sums, where this block's slice was
+        u64* const sums = reinterpret_cast<u64*>(xs);
         if (whole) {
           r.sum_up(sums);
           int kept = weights ? n : min(n, k);
@@ -777,19 +992,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             kept = min(kept, count_of([&](int i) { return sums[i] < goal; }) + 1);
           }
           if (floor != kNoCut) kept = max(1, min(kept, count_of([&](int i) { return s->list[i] >= floor; })));
-          const u64 total = sums[kept - 1];
-          draw_from_list(s, sums + kList, sums, a, r.weigh, row, kept, total, (double)t, u);
+          draw_from_list(s, sums + kList, sums, a, r.weigh, row, kept, sums[kept - 1], u);
         } else {
           int need = min(n, (int)(target - w.above));
           if (weights) {
-            // (the table stays: there are weights to come)
             need = 1;
             if (target > above) {
               r.sum_up(s->weight);
               need = min(n, count_of([&](int i) { return s->weight[i] < target - above; }) + 1);
             }
           }
-          found = s->list[max(0, need - 1)];
+          const u64 found = s->list[max(0, need - 1)];
           if (tid < a.cluster) remote_put(remote(&s->give[2], tid), found);
         }
       }
@@ -828,10 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       __syncthreads();
       const Sum block = scan(s, tid < r.blocks ? s->sums[tid] : 0);
-      const Sum slices = over_cluster(s, block.all, 3, a.cluster, rank);
+      const Sum slices = over_cluster(s, block.all, 4, a.cluster, rank);
       const u64 goal = goal_of(slices.all, u);
-      if (tid == kThreads - 1) take_log(s, slices.all);
-      __syncwarp();
       if (slices.before <= goal && goal < slices.before + block.all) {       // (the same for all threads of a block)
         const u64 at = slices.before + block.before;
         if (tid < r.blocks && at <= goal && goal < at + s->sums[tid]) {
@@ -843,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const float l = i >= pad && i < end ? Elem<T>::up(xs[i]) : NAN;
         const u64 mine = kept(l, i) ? r.weigh.one(l) : 0;
         const u64 before = s->pick[1] + scan(s, mine).before;
-        if (before <= goal && goal < before + mine) answer(s, a, r.weigh, row, r.start + i, l, (double)t);
+        if (before <= goal && goal < before + mine) answer(a, r.weigh, row, r.start + i, l, slices.all, mine == slices.all);
       }
     }
   }
@@ -861,7 +1072,7 @@ template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s)
   a.slice = ((c.vocab + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
   if (c.ntok * a.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const auto kernel = sample_kernel<T>;
-  const int smem = (int)sizeof(Shared) + (a.slice + kBlock) * (int)sizeof(T);
+  const int smem = (int)sizeof(Shared) + std::max((a.slice + kBlock) * (int)sizeof(T), 2 * kList * (int)sizeof(u64));
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e == cudaSuccess && a.cluster > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

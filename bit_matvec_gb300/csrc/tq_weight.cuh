@@ -77,11 +77,43 @@ struct Weigher {
     k = 6144.0f - r;
     least = fminf(far ? top - 46.0f * octave : (r - 47.0f) * octave, top);
   }
-  // The logarithm of a weight as a part of 2^46, to base 2.
-  __device__ __forceinline__ double log2_of(float l, double temp) const {
-    return ((double)l - (double)shift) * (1.4426950408889634074 / temp) - (6144.0 - (double)k);
+  // The same with whole octaves: sums relative to other logits' are shifts
+  // apart. Returns R; not for logits whose exponent passes 2000.
+  __device__ __forceinline__ int set_octave(float top, const ExpTable* from) {
+    table = from;
+    shift = 0.0f;
+    const float r = ceilf(__fmul_rn(top, c_hi)) + 2.0f;
+    k = 6144.0f - r;
+    least = -INFINITY;
+    return (int)r;
   }
-
+  // ln(w / total) for the weight of l and a sum in units of 2^-46 of 2^(6144 - k).
+  __device__ __forceinline__ float log_share(float l, uint64_t total) const {
+    const float x = __fsub_rn(l, shift), p = __fmul_rn(x, c_hi);
+    const float rest = __fmaf_rn(x, c_lo, __fmaf_rn(x, c_hi, -p));       // x c - p
+    float whole, part;
+    log2_of(total, *table, whole, part);
+    // x c - R + 46 - log2(total): p and a multiple of 2^-11, and what they lack
+    const float b = (6144.0f - k) - 46.0f + whole;
+    const float a = __fsub_rn(p, b), t = __fsub_rn(a, p);
+    const float lack = __fadd_rn(__fsub_rn(p, __fsub_rn(a, t)), -__fadd_rn(b, t));
+    const float low = __fadd_rn(__fadd_rn(lack, rest), -part);
+    constexpr float kLn2 = 0.69314718055994531f, kLn2Low = (float)(0.69314718055994531 - (double)kLn2);
+    const float h = __fmul_rn(a, kLn2);
+    return __fadd_rn(h, __fadd_rn(__fmaf_rn(a, kLn2, -h), __fmaf_rn(a, kLn2Low, __fmul_rn(low, kLn2))));
+  }
+  // log2 of a positive integer, as a multiple of 2^-11 and the rest,
+  // good to 2^-34: the leading bits m over the table's entry below are 1 + d, d < 2^-10.
+  static __device__ __forceinline__ void log2_of(uint64_t n, const ExpTable& t, float& whole, float& part) {
+    const int zeros = __clzll((long long)n);
+    const uint64_t m = n << zeros;
+    const float hi = (float)(uint32_t)(m >> 40) * 0x1p17f;                     // 2^40 .. 2^41
+    const float lo = (float)(uint32_t)((m >> 16) & 0xffffffu) * 0x1p-7f;
+    const int j = max(0, min(kExpSteps - 1, (int)(__log2f(hi * 0x1p-40f) * kExpSteps)));
+    const float d = __fdiv_rn(__fadd_rn(__fsub_rn(hi, t.hi[j]), __fsub_rn(lo, t.lo[j])), t.hi[j]);
+    part = __fmul_rn(1.44269504088896341f, __fmaf_rn(__fmul_rn(d, d), __fmaf_rn(d, 1.0f / 3.0f, -0.5f), d));
+    whole = (float)(63 - zeros) + (float)j * (1.0f / kExpSteps);
+  }
   // N (even) weights, for logits of at least `least` (others give anything), and their bits: the
   // exponent in steps of 2^-11. Two at a time, an operation for both.
   template <int N> __device__ __forceinline__ void operator()(const float (&l)[N], uint64_t (&w)[N], int (&bits)[N],
@@ -131,6 +163,26 @@ struct Weigher {
   static __device__ __forceinline__ int bin_of(int bits) { return (kMagic >> kBinShift) - (bits >> kBinShift); }
   static __device__ __forceinline__ int octave_of(int bin) { return (bin + 15) / 16; }
 };
+
+// t ln(x) as a sum of two floats, for x > 0 (infinity gives infinity).
+__device__ __forceinline__ void scaled_log(float x, float t, const ExpTable& table, float& hi, float& lo) {
+  const uint32_t b = __float_as_uint(x);
+  if (b >= 0x7f800000u) {
+    hi = INFINITY;
+    lo = 0.0f;
+    return;
+  }
+  const uint32_t mant = b >> 23 ? (b & 0x7fffffu) | 0x800000u : b;
+  float whole, part;
+  Weigher::log2_of(mant, table, whole, part);
+  whole += (float)((b >> 23 ? (int)(b >> 23) : 1) - 150);
+  constexpr float kLn2 = 0.69314718055994531f, kLn2Low = (float)(0.69314718055994531 - (double)kLn2);
+  const float h = __fmul_rn(kLn2, t), l = __fmaf_rn(kLn2, t, -h) + __fmul_rn(kLn2Low, t);    // ln 2 * t
+  const float p = __fmul_rn(whole, h);
+  const float q = __fadd_rn(__fmaf_rn(whole, h, -p), __fmaf_rn(whole, l, __fmul_rn(part, h)));
+  hi = __fadd_rn(p, q);
+  lo = __fsub_rn(q, __fsub_rn(hi, p));
+}
 
 // Floats as integers of the same order (both zeros alike), and back.
 __device__ __forceinline__ uint32_t order_key(float l) {
