@@ -1,8 +1,10 @@
 // tq_sample.cu -- the draw of the next token: temperature, top-k, top-p, min-p
 // and one given uniform number a row.
 //
-// A cluster of thread blocks takes a row, each a slice of it that stays in its
-// shared memory: logits are read from memory once, whatever the filters need.
+// A cluster of thread blocks takes a row, each a slice of it: one block where rows
+// are many, sixteen where there is one. The slice stays in shared memory, or, where
+// it is too large for that, in L2: logits are read from memory once, whatever the
+// filters need.
 //
 // The kept tokens are a beginning of the order (falling logit, rising index). A
 // token's place in it is an integer, its logit's bits above its complemented
@@ -31,12 +33,14 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kIndexBits = 18;
 constexpr int kList = 1024;                 // tokens that are sorted
 constexpr int kBlock = 512;                 // tokens of a sum
-constexpr int kMaxSlice = 32768;            // tokens of a thread block: 2^15 times 2^16 fit in a bin
-constexpr int kMaxBlocks = kMaxSlice / kBlock + 1;
+constexpr int kMaxBlocks = kMaxVocab / kBlock + 1;
 constexpr int kMaxCluster = 16;
+constexpr int kSlots = 304;                 // thread blocks at once: two on each of 152 SMs
+constexpr int kMaxResident = 65536;         // bytes of a slice in shared memory
 static_assert(kMaxVocab == 1 << kIndexBits, "an index below a logit's bits");
 static_assert(kBlock == kThreads && kList == 2 * kThreads, "one token, two entries a thread");
-static_assert(kWeightBins % 4 == 0 && kWeightBins / 4 <= kThreads, "four bins a thread");
+static_assert(kWeightBins % 128 == 0 && kWeightBins / 4 <= kThreads, "four bins a thread, in whole warps");
+static_assert(kMaxBlocks <= 2 * kThreads, "two sums a thread");
 
 using u64 = unsigned long long;
 constexpr u64 kNoCut = 0;
@@ -65,9 +69,8 @@ struct alignas(16) Shared {
       u64 list[kList];        // places of the tokens at a cut
       u64 weight[kList];      // (rank 0) their weights
     };
-    struct {                  // before there is a list
-      u64 first[kWeightBins]; // (rank 0) sums of a bin at most; (narrowing, every block) sums of its own
-      u64 sums[kWeightBins];  // (rank 0) sums of a bin
+    struct {                  // while a window is narrowed: weights by bin, this block's and (rank 0) all
+      u64 mine[kWeightBins], all[kWeightBins];
       uint32_t tokens[kWeightBins];
     } by_bin;
   };
@@ -77,9 +80,11 @@ struct alignas(16) Shared {
   u64 scan[kWarps];
   u64 give[6];                // what the other blocks of the cluster read
   u64 window[8];              // what rank 0 found
+  int entry[kBlock];          // of the list, by the low bits of their indexes
   int have;                   // entries of the list
   int first;                  // lowest index of the largest logit
-  u64 pick[2];
+  u64 pick[4];
+  u64 warps[3][kWeightBins / 128];
   uint32_t least_top[kWarps];
 };
 static_assert(sizeof(Shared) % 16 == 0, "the slice behind it in 16-byte pieces");
@@ -285,46 +290,55 @@ __device__ __noinline__ Found first_reaching(const u64* v, u64 target, u64 above
   const int at = __ffs(__ballot_sync(0xffffffffu, base + upto >= target)) - 1;
   return {share * kEach + at, base + __shfl_sync(0xffffffffu, upto - x, at)};
 }
-// By one warp: the sum of the first n of kWeightBins values.
-__device__ __noinline__ u64 sum_before(const uint32_t* v, int n) {
-  u64 sum = 0;
-  for (int i = threadIdx.x & 31; i < n; i += 32) sum += v[i];
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return sum;
-}
-
 template <typename T> struct Row {
   Shared* s;
-  const T* xs;                // this block's slice: values pad .. end - 1 of it
+  const T* xs;                // this block's slice: values pad .. end - 1 from here
   int cluster, rank;
   int start;                  // the token of xs[0]
   int pad, end, blocks;       // blocks of 512 values that hold some
+  bool infinite;              // a plus infinity: every other logit is minus infinity beside it
   Weigher weigh;
 
   __device__ __forceinline__ u64 place(float l, int i) const {   // i: in xs
     return ((u64)order_key(l) << kIndexBits) | (unsigned)(kMaxVocab - 1 - (start + i));
   }
+  __device__ __forceinline__ float beside_infinity(float l) const { return l == INFINITY ? 0.0f : -INFINITY; }
+  // One logit, NaN outside the slice.
+  __device__ __forceinline__ float value(int i) const {
+    if (i < pad || i >= end) return NAN;
+    const float l = Elem<T>::up(xs[i]);
+    return infinite ? beside_infinity(l) : l;
+  }
   // Calls f(four logits, the index of the first in xs) for every token (NaN for
   // what is none); a warp's turn is a block of 512, after which done(block).
   template <typename F, typename D> __device__ __forceinline__ void each(F f, D done) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
     for (int b = warp; b < blocks; b += kWarps) {
       const int i0 = b * kBlock + lane * 4;
+      Vec<T, 4> v[4];
       const bool whole = b * kBlock >= pad && (b + 1) * kBlock <= end;
-#pragma unroll 2
-      for (int j = 0; j < kBlock / 128; ++j) {
-        const int i = i0 + j * 128;
-        const Vec<T, 4> v = *reinterpret_cast<const Vec<T, 4>*>(xs + i);
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const Vec<T, 4>*>(xs + i0 + j * 128);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = i0 + (e >> 2) * 128 + (e & 3);
+          v[e >> 2].v[e & 3] = i >= pad && i < end ? xs[i] : Elem<T>::down(NAN);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         float l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l[e] = Elem<T>::up(v.v[e]);
-        if (!whole) {
+        for (int e = 0; e < 4; ++e) l[e] = Elem<T>::up(v[j].v[e]);
+        if (infinite) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (i + e < pad || i + e >= end) l[e] = NAN;
+            if (l[e] == l[e]) l[e] = beside_infinity(l[e]);
         }
-        f(l, i);
+        f(l, i0 + j * 128);
       }
       done(b);
     }
@@ -380,18 +394,10 @@ template <typename T> struct Row {
     return (u64)lo << kIndexBits;
   }
 
-  // What rank 0 found, for all blocks.
-  __device__ __forceinline__ void publish(const Window& w, u64 target) const {
+  // A word of what rank 0 found, for all blocks: by one warp.
+  __device__ __forceinline__ void publish(int word, u64 v) const {
     const int lane = threadIdx.x & 31;
-    if (lane < cluster) {
-      const uint32_t to = remote(s->window, lane);
-      remote_put(to, w.lo);
-      remote_put(to + 8, w.hi);
-      remote_put(to + 16, w.above);
-      remote_put(to + 24, w.inside);
-      remote_put(to + 32, w.upto);
-      remote_put(to + 40, target);
-    }
+    if (lane < cluster) remote_put(remote(&s->window[word], lane), v);
   }
   __device__ __forceinline__ Window published(u64& target) const {
     meet(cluster);
@@ -419,13 +425,13 @@ template <typename T> struct Row {
         if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
         uint64_t wt[4];
         int bits[4];
-        uint32_t top16[4];
-        weigh(l, wt, bits, top16);
+        uint32_t lead[4];
+        weigh(l, wt, bits, lead);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (in[e]) {
             mine += wt[e];
-            atomicAdd(&s->bins[Weigher::bin_of(bits[e])], top16[e]);
+            atomicAdd(&s->bins[Weigher::bin_of(bits[e])], lead[e]);
           }
       });
       const u64 sum = scan(s, mine).all;
@@ -441,12 +447,18 @@ template <typename T> struct Row {
     }
     meet(cluster);
     if (rank == 0) {
-      // all blocks' bins: tokens (at most), and what counts, at least and at most
-      u64* const lo = s->by_bin.sums;
-      u64* const hi = by_weight ? s->by_bin.first : lo;
-      uint32_t* const tokens = s->by_bin.tokens;
+      const int lane = tid & 31, warp = tid >> 5;
+      if (by_weight) {
+        u64 all = lane < cluster ? remote_u64(remote(&s->give[0], lane)) : 0;
+#pragma unroll
+        for (int d = kMaxCluster / 2; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+        all = __shfl_sync(0xffffffffu, all, 0);
+        target = share > 0.0f ? max(u64(1), fraction_of(all, share, true)) : 1;
+      }
+      // This thread's four bins, of all blocks: tokens (at most), and what
+      // counts, at least and at most; and the sums before them.
+      u64 n[4] = {0, 0, 0, 0}, lo[4], hi[4], at_lo = 0, at_hi = 0, at_n = 0;
       if (tid < kWeightBins / 4) {
-        u64 n[4] = {0, 0, 0, 0};
         for (int r0 = 0; r0 < cluster; r0 += 8) {
           uint4 v[8];
 #pragma unroll
@@ -462,39 +474,91 @@ template <typename T> struct Row {
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int b = 4 * tid + e;
+          lo[e] = hi[e] = n[e];
           if (by_weight) {
-            // Sums of weights' first 16 bits, 2^15 - 8 at least (just below a
+            // Sums of weights' first 13 bits, 2^12 - 1 at least (just below a
             // power of two the table's entry is that power's): a token for each of
             // these in the sum, at most, each cut by less than one and off by a unit.
-            const int octave = Weigher::octave_of(b);
-            const u64 most = (n[e] + (n[e] >> 11)) >> 15, v = (n[e] << 31) >> octave;
-            lo[b] = v - min(v, most);
-            hi[b] = most ? (((n[e] + most) << 31) >> octave) + most + 1 : 0;
-            tokens[b] = (uint32_t)most;
-          } else {
-            lo[b] = n[e];
-            tokens[b] = (uint32_t)n[e];
+            const int shift = 34 - Weigher::octave_of(4 * tid + e);
+            auto shifted = [&](u64 v) { return shift >= 0 ? v << shift : v >> -shift; };
+            const u64 most = (n[e] + (n[e] >> 11)) >> 12, v = shifted(n[e]);
+            lo[e] = v - min(v, most);
+            hi[e] = most ? shifted(n[e] + most) + most + 1 : 0;
+            n[e] = most;
           }
+        }
+        const u64 sum_lo = lo[0] + lo[1] + lo[2] + lo[3], sum_hi = hi[0] + hi[1] + hi[2] + hi[3];
+        const u64 sum_n = n[0] + n[1] + n[2] + n[3];
+        at_lo = sum_lo;
+        at_hi = sum_hi;
+        at_n = sum_n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const u64 x = __shfl_up_sync(0xffffffffu, at_lo, d);
+          if (lane >= d) at_lo += x;
+          if (by_weight) {
+            const u64 y = __shfl_up_sync(0xffffffffu, at_hi, d), z = __shfl_up_sync(0xffffffffu, at_n, d);
+            if (lane >= d) {
+              at_hi += y;
+              at_n += z;
+            }
+          }
+        }
+        if (!by_weight) at_hi = at_n = at_lo;
+        if (lane == 31) {
+          s->warps[0][warp] = at_lo;
+          s->warps[1][warp] = at_hi;
+          s->warps[2][warp] = at_n;
+        }
+        at_lo -= sum_lo;
+        at_hi -= sum_hi;
+        at_n -= sum_n;
+      }
+      if (tid == kThreads - 1) {
+        s->pick[0] = 0;
+        s->pick[1] = kWeightBins;
+        s->pick[2] = 0;
+      }
+      __syncthreads();
+      u64 tokens = 0;
+      if (tid < kWeightBins / 4) {
+        for (int w = 0; w < kWeightBins / 128; ++w) {
+          tokens += s->warps[2][w];
+          if (w >= warp) continue;
+          at_lo += s->warps[0][w];
+          at_hi += s->warps[1][w];
+          at_n += s->warps[2][w];
+        }
+        if (tid == 0) s->pick[3] = tokens;
+      }
+      __syncthreads();
+      if (tid < kWeightBins / 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (at_hi < target && at_hi + hi[e] >= target) {      // the first that may reach the target
+            s->pick[0] = 4 * tid + e;
+            s->pick[2] = at_n;
+          }
+          if (at_lo < target && at_lo + lo[e] >= target) {      // the first that surely does
+            s->pick[1] = 4 * tid + e;
+            s->pick[3] = at_n + n[e];
+          }
+          at_lo += lo[e];
+          at_hi += hi[e];
+          at_n += n[e];
         }
       }
       __syncthreads();
-      if (tid < 32) {
-        if (by_weight) {
-          u64 all = tid < cluster ? remote_u64(remote(&s->give[0], tid)) : 0;
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-          target = share > 0.0f ? max(u64(1), fraction_of(all, share, true)) : 1;
-        }
-        const Found first = first_reaching(hi, target, 0);       // may reach the target
-        const Found last = by_weight ? first_reaching(lo, target, 0) : first;   // surely does
-        const u64 before = sum_before(tokens, first.bin);
-        w.upto = sum_before(tokens, min(last.bin + 1, kWeightBins));
-        w.inside = w.upto - before;
-        w.above = before;
-        if (first.bin > 0) w.hi = min(w.hi, bin_end(first.bin - 1, top_key) - 1);
-        w.lo = max(w.lo, last.bin < kWeightBins ? bin_end(last.bin, top_key) : 0);
-        publish(w, target);
+      if (warp == 0) {
+        const int last = (int)s->pick[1];
+        publish(0, max(w.lo, last < kWeightBins ? bin_end(last, top_key) : 0));
+        publish(2, s->pick[2]);
+        publish(3, s->pick[3] - s->pick[2]);
+      } else if (warp == 1) {
+        const int first = (int)s->pick[0];
+        publish(1, first > 0 ? min(w.hi, bin_end(first - 1, top_key) - 1) : w.hi);
+        publish(4, s->pick[3]);
+        publish(5, target);
       }
     }
     return published(target);
@@ -506,8 +570,8 @@ template <typename T> struct Row {
   static __device__ __noinline__ Window narrow(Row row, Window w, bool by_weight, u64 target) {
     Shared* const s = row.s;
     const int tid = threadIdx.x;
-    u64* const sums = s->by_bin.first;
-    u64* const all = s->by_bin.sums;
+    u64* const sums = s->by_bin.mine;
+    u64* const all = s->by_bin.all;
     uint32_t* const tokens = s->by_bin.tokens;
     while (w.inside > kList) {
       int shift = 0;
@@ -556,7 +620,10 @@ template <typename T> struct Row {
           w.lo = max(w.lo, top - min(top, ((u64)(bin + 1) << shift) - 1));
           w.above = at.before;
           w.inside = tokens[bin];
-          row.publish(w, target);
+          row.publish(0, w.lo);
+          row.publish(1, w.hi);
+          row.publish(2, w.above);
+          row.publish(3, w.inside);
         }
       }
       w = row.published(target);
@@ -679,24 +746,44 @@ __device__ __noinline__ void answer(const Args& a, Weigher weigh, int64_t row, i
 }
 
 // (rank 0) The draw from a sorted list whose first `kept` entries are the kept
-// tokens; by_index and spare: room for kList values each.
-__device__ __noinline__ void draw_from_list(Shared* s, u64* by_index, u64* spare, const Args& a, Weigher weigh,
-                                            int64_t row, int kept, u64 total, float u) {
+// tokens: the sums of their weights by the upper half of their indexes, then, for
+// the part that the draw falls into, by index. bins: room for 512 values.
+__device__ __noinline__ void draw_from_list(Shared* s, u64* bins, const Args& a, Weigher weigh, int64_t row, int kept,
+                                            u64 total, float u) {
   const int tid = threadIdx.x;
-  const u64 goal = goal_of(total, u);
-  // by rising index: the complemented index, then the entry
-  static_assert(kList == 1 << 10, "an entry below an index");
-  for (int i = tid; i < kList; i += kThreads)
-    by_index[i] = i < kept ? u64(1) << 63 | (s->list[i] & kIndexMask) << 10 | (u64)i : 0;
-  __syncthreads();
-  sort(by_index, spare, kept);
-  const u64 p = by_index[2 * tid], q = by_index[2 * tid + 1];
-  const u64 x = p ? s->weight[p & (kList - 1)] : 0, y = q ? s->weight[q & (kList - 1)] : 0;
-  const u64 at = scan(s, x + y).before;
-  if (at <= goal && goal < at + x + y) {
-    const u64 e = s->list[(goal < at + x ? p : q) & (kList - 1)];
-    answer(a, weigh, row, kMaxVocab - 1 - (int)(e & kIndexMask), key_value((uint32_t)(e >> kIndexBits)), total,
-           x + y == total && (x == 0 || y == 0));
+  static_assert(kIndexBits == 18 && kThreads == 512 && kBlock == 512, "two halves of 9 bits");
+  u64 goal = goal_of(total, u);
+  int part = 0;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    bins[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+      const int i = tid + j * kThreads;
+      if (i >= kept) continue;
+      const int index = kMaxVocab - 1 - (int)(s->list[i] & kIndexMask);
+      if (half == 0) {
+        atomicAdd(&bins[index >> 9], s->weight[i]);
+      } else if (index >> 9 == part) {
+        bins[index & 511] = s->weight[i];
+        s->entry[index & 511] = i;
+      }
+    }
+    __syncthreads();
+    const u64 mine = bins[tid], at = scan(s, mine).before;
+    if (at <= goal && goal < at + mine) {
+      if (half == 0) {
+        s->pick[0] = tid;
+        s->pick[1] = at;
+      } else {
+        const u64 e = s->list[s->entry[tid]];
+        answer(a, weigh, row, part << 9 | tid, key_value((uint32_t)(e >> kIndexBits)), total, mine == total);
+      }
+    }
+    __syncthreads();
+    part = (int)s->pick[0];
+    goal -= s->pick[1];
   }
 }
 
@@ -767,15 +854,16 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
   if (tid == 0) s->have = 0;
   __syncthreads();
   if (flags && lane == 0) atomicOr(&s->have, flags);
-  int top = tid < r.blocks ? s->octaves[tid] : kNone;
+  const int b0 = 2 * tid, b1 = b0 + 1;
+  int top = max(b0 < r.blocks ? s->octaves[b0] : kNone, b1 < r.blocks ? s->octaves[b1] : kNone);
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) s->least_top[warp] = (uint32_t)top;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max(top, (int)s->least_top[w]);
+  top = __reduce_max_sync(0xffffffffu, (int)s->least_top[lane & (kWarps - 1)]);
   auto shifted = [](u64 v, int by) { return by < 64 ? v >> by : 0; };
-  const u64 block = tid < r.blocks ? shifted(s->sums[tid], top - s->octaves[tid]) : 0;
-  const Sum blocks = scan(s, block);
+  const u64 block0 = b0 < r.blocks ? shifted(s->sums[b0], top - s->octaves[b0]) : 0;
+  const u64 block1 = b1 < r.blocks ? shifted(s->sums[b1], top - s->octaves[b1]) : 0;
+  const Sum blocks = scan(s, block0 + block1);
   if (tid == 0) {
     s->give[4] = blocks.all;
     s->give[5] = (u64)(uint32_t)top << 32 | (uint32_t)s->have;
@@ -811,9 +899,11 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
   if (!(before <= goal && goal < before + mine)) return true;       // (the same for all threads of a block)
   // ---- the goal in this block's units, then in those of the 512 tokens it falls into
   const u64 here = min((goal - before) << (highest - top), blocks.all - 1);
-  if (blocks.before <= here && here < blocks.before + block) {
-    s->pick[0] = tid;
-    s->pick[1] = min((here - blocks.before) << (top - s->octaves[tid]), s->sums[tid] - 1);
+  if (blocks.before <= here && here < blocks.before + block0 + block1) {
+    const bool second = here >= blocks.before + block0;
+    const int b = second ? b1 : b0;
+    s->pick[0] = b;
+    s->pick[1] = min((here - blocks.before - (second ? block0 : 0)) << (top - s->octaves[b]), s->sums[b] - 1);
   }
   __syncthreads();
   const int b = (int)s->pick[0], i = b * kBlock + tid;
@@ -828,11 +918,11 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
   return true;
 }
 
-template <typename T>
+template <typename T, bool kResident>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) unsigned char raw[];
   Shared* const s = reinterpret_cast<Shared*>(raw);
-  T* const xs = reinterpret_cast<T*>(raw + sizeof(Shared));
+  unsigned char* const room = raw + sizeof(Shared);     // the slice, or 16 KB
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
   const int64_t row = blockIdx.x / a.cluster;
@@ -853,7 +943,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // in shared memory as it lies in memory within 16 bytes, so that whole pieces are copied
   constexpr int kPiece = 16 / (int)sizeof(T);
   const int pad = (int)((uintptr_t)x % 16 / sizeof(T)), end = pad + count;
-  Row<T> r = {s, xs, a.cluster, rank, from - pad, pad, end, count > 0 ? (end + kBlock - 1) / kBlock : 0, {}};
+  Row<T> r = {s, kResident ? reinterpret_cast<const T*>(room) : x - pad, a.cluster, rank, from - pad, pad, end,
+              count > 0 ? (end + kBlock - 1) / kBlock : 0, false, {}};
   if (temp >= 0x1p-100f && temp < INFINITY && !by_count && !by_weight && !(mp > 0.0f)) {
     __syncthreads();
     const bool done = draw_unfiltered<T>(s, a, x - pad, r, row, t, u);
@@ -869,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll 4
     for (int i = first + tid; i < last; i += kThreads) {
       const uint4 q = ldg_stream_v4(from16 + i);
-      reinterpret_cast<uint4*>(xs)[i] = q;
+      if (kResident) reinterpret_cast<uint4*>(room)[i] = q;
       const Vec<T, kPiece> v = *reinterpret_cast<const Vec<T, kPiece>*>(&q);
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) top = max_or_nan(top, Elem<T>::up(v.v[e]));
@@ -879,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int i = tid < kPiece ? pad + tid : tail + tid - kPiece;
     if (tid < 2 * kPiece && (tid < kPiece ? i < head : i < end)) {
       const T v = x[i - pad];
-      xs[i] = v;
+      if (kResident) reinterpret_cast<T*>(room)[i] = v;
       top = max_or_nan(top, Elem<T>::up(v));
     }
   }
@@ -936,14 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   } else {
-    const bool infinite = top == INFINITY;
-    if (infinite) {
-      // beside it every other logit is minus infinity
-      for (int i = pad + tid; i < end; i += kThreads)
-        xs[i] = Elem<T>::down(Elem<T>::up(xs[i]) == INFINITY ? 0.0f : -INFINITY);
-      top = 0.0f;
-      __syncthreads();
-    }
+    r.infinite = top == INFINITY;
+    if (r.infinite) top = 0.0f;
     r.weigh.set_temperature(t);
     r.weigh.set_top(top, t, &s->table);
     const uint32_t top_key = order_key(top);
@@ -969,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
       }
       u64 target = (u64)k;
-      const bool bounded = !infinite && k <= a.cluster * (kThreads / 4);
+      const bool bounded = !r.infinite && k <= a.cluster * (kThreads / 4);
       Window w = r.search(weights, target, cut, top_key, p, bounded ? key_value(least_top) : -INFINITY);
       // all tokens that may be kept fit in the list
       const bool whole = w.upto <= kList;
@@ -983,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (rank == 0) {
         n = r.join();
         // room for the sums, where this block's slice was
-        u64* const sums = reinterpret_cast<u64*>(xs);
+        u64* const sums = reinterpret_cast<u64*>(room);
         if (whole) {
           r.sum_up(sums);
           int kept = weights ? n : min(n, k);
@@ -992,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             kept = min(kept, count_of([&](int i) { return sums[i] < goal; }) + 1);
           }
           if (floor != kNoCut) kept = max(1, min(kept, count_of([&](int i) { return s->list[i] >= floor; })));
-          draw_from_list(s, sums + kList, sums, a, r.weigh, row, kept, sums[kept - 1], u);
+          draw_from_list(s, sums + kList, a, r.weigh, row, kept, sums[kept - 1], u);
         } else {
           int need = min(n, (int)(target - w.above));
           if (weights) {
@@ -1040,45 +1125,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                });
       }
       __syncthreads();
-      const Sum block = scan(s, tid < r.blocks ? s->sums[tid] : 0);
+      const int b0 = 2 * tid, b1 = b0 + 1;
+      const u64 sum0 = b0 < r.blocks ? s->sums[b0] : 0, sum1 = b1 < r.blocks ? s->sums[b1] : 0;
+      const Sum block = scan(s, sum0 + sum1);
       const Sum slices = over_cluster(s, block.all, 4, a.cluster, rank);
       const u64 goal = goal_of(slices.all, u);
       if (slices.before <= goal && goal < slices.before + block.all) {       // (the same for all threads of a block)
         const u64 at = slices.before + block.before;
-        if (tid < r.blocks && at <= goal && goal < at + s->sums[tid]) {
-          s->pick[0] = tid;
-          s->pick[1] = at;
+        if (at <= goal && goal < at + sum0 + sum1) {
+          const bool second = goal >= at + sum0;
+          s->pick[0] = second ? b1 : b0;
+          s->pick[1] = second ? at + sum0 : at;
         }
         __syncthreads();
         const int i = (int)s->pick[0] * kBlock + tid;
-        const float l = i >= pad && i < end ? Elem<T>::up(xs[i]) : NAN;
+        const float l = r.value(i);
         const u64 mine = kept(l, i) ? r.weigh.one(l) : 0;
         const u64 before = s->pick[1] + scan(s, mine).before;
-        if (before <= goal && goal < before + mine) answer(a, r.weigh, row, r.start + i, l, slices.all, mine == slices.all);
+        if (before <= goal && goal < before + mine)
+          answer(a, r.weigh, row, r.start + i, l, slices.all, mine == slices.all);
       }
     }
   }
   if (a.cluster > 1) meet(a.cluster);     // nothing of this block is read any more
 }
 
-template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s) {
-  Args a = {c.logits, c.stride, c.vocab, 0, 1, c.u, c.temperature, c.top_k, c.top_p, c.min_p, c.tokens, c.logp};
-  // Thread blocks a row: slices of at most 64 KB, two blocks an SM; more while
-  // SMs are free and slices have 2048 tokens.
-  constexpr int kSlice = std::min(kMaxSlice, 65536 / (int)sizeof(T));
-  while (a.cluster < kMaxCluster &&
-         (c.vocab > a.cluster * kSlice || (c.ntok * a.cluster < 152 && c.vocab > a.cluster * 2048)))
-    a.cluster *= 2;
-  a.slice = ((c.vocab + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
-  if (c.ntok * a.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const auto kernel = sample_kernel<T>;
-  const int smem = (int)sizeof(Shared) + std::max((a.slice + kBlock) * (int)sizeof(T), 2 * kList * (int)sizeof(u64));
+template <typename T, bool kResident> cudaError_t launch_kernel(const Args& a, int64_t ntok, cudaStream_t s) {
+  const auto kernel = sample_kernel<T, kResident>;
+  const int slice = kResident ? (a.slice + kBlock) * (int)sizeof(T) : 0;
+  const int smem = (int)sizeof(Shared) + std::max(slice, 2 * kList * (int)sizeof(u64));
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e == cudaSuccess && a.cluster > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(c.ntok * a.cluster));
+  cfg.gridDim = dim3((unsigned)(ntok * a.cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -1091,6 +1172,18 @@ template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s)
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s) {
+  Args a = {c.logits, c.stride, c.vocab, 0, 1, c.u, c.temperature, c.top_k, c.top_p, c.min_p, c.tokens, c.logp};
+  // Thread blocks a row: as many as run at once (two an SM), where slices have
+  // 2048 tokens at least.
+  while (a.cluster < kMaxCluster && 2 * c.ntok * a.cluster <= kSlots && c.vocab > a.cluster * 2048) a.cluster *= 2;
+  a.slice = ((c.vocab + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
+  if (c.ntok * a.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // In shared memory where two slices fit into an SM's, else read again from L2.
+  return a.slice * (int)sizeof(T) <= kMaxResident ? launch_kernel<T, true>(a, c.ntok, s)
+                                                  : launch_kernel<T, false>(a, c.ntok, s);
 }
 
 }  // namespace

@@ -117,7 +117,7 @@ struct Weigher {
   // N (even) weights, for logits of at least `least` (others give anything), and their bits: the
   // exponent in steps of 2^-11. Two at a time, an operation for both.
   template <int N> __device__ __forceinline__ void operator()(const float (&l)[N], uint64_t (&w)[N], int (&bits)[N],
-                                                              uint32_t* top16 = nullptr) const {
+                                                              uint32_t* lead = nullptr) const {
     using namespace tc;
     const uint64_t ch = f2_packf(c_hi, c_hi), minus_ch = f2_packf(-c_hi, -c_hi), minus_cl = f2_packf(-c_lo, -c_lo);
     const uint64_t kk = f2_packf(k, k), sh = f2_packf(shift, shift);
@@ -136,16 +136,16 @@ struct Weigher {
       const float t0 = table->hi[j0], t1 = table->hi[j1];
       const float2 low = f2_unpack(f2_fma(f2_mul(f2_packf(t0, t1), q), f2_fma(q, half_square, ln2),
                                           f2_packf(table->lo[j0], table->lo[j1])));
-      finish(t0, low.x, bits[i], w[i], top16 ? top16 + i : nullptr);
-      finish(t1, low.y, bits[i + 1], w[i + 1], top16 ? top16 + i + 1 : nullptr);
+      finish(t0, low.x, bits[i], w[i], lead ? lead + i : nullptr);
+      finish(t1, low.y, bits[i + 1], w[i + 1], lead ? lead + i + 1 : nullptr);
     }
   }
   // T[j] as a 24-bit integer with what is to be added: about 2^40 .. 2^41, then 2^6 times that, cut to
   // its place.
-  static __device__ __forceinline__ void finish(float t, float low, int bits, uint64_t& w, uint32_t* top16) {
+  static __device__ __forceinline__ void finish(float t, float low, int bits, uint64_t& w, uint32_t* lead) {
     const uint32_t mant = (__float_as_uint(t) & 0x7fffffu) | 0x800000u;
     const uint64_t v = ((uint64_t)mant << 23) + (int64_t)__float2int_rn(low) * 64;
-    if (top16) *top16 = (uint32_t)(v >> 31);
+    if (lead) *lead = (uint32_t)(v >> 34);
     w = (v >> ((kMagic >> 11) - (bits >> 11))) | 1u;
   }
   __device__ __forceinline__ uint64_t one(float l) const {
