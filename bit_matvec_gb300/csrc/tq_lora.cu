@@ -24,7 +24,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kTile = 32;          // tokens of a tile: two row blocks of 16
+constexpr int kTile = 32;          // tokens of a tile at most: two row blocks of 16
+constexpr int kSmallTile = 8;      // or so many, where adapters have few tokens each
+constexpr int kParts = 8;          // shares of a block's columns, a warp's each, summed apart
 constexpr int kChain = 4;          // chunks of 32 columns that are summed on the tensor cores
 constexpr int kInBlock = 256;      // tokens up to which every block finds its tile itself
 constexpr int kGroupThreads = 1024;
@@ -39,6 +41,7 @@ struct Args {
   int64_t x_stride, z_stride, y_stride;
   int y_type;
   int ntok;
+  int tile;              // tokens of a tile
   int splits;            // clusters that share the rows of a tile
   int copy;              // tokens without adapter are copied (Z is not Y)
   int y_vec, z_vec;      // rows of Y, of Z in 16-byte pieces
@@ -111,72 +114,39 @@ __device__ __forceinline__ uint16_t down(float v, int type) {
   return type == TQ_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// n of eight consecutive values from `at` on, as they are (vec: the address is a multiple of 16
-// bytes), and as floats.
-struct Raw8 {
-  uint4 v[2];
-};
-__device__ __forceinline__ Raw8 load8(const void* p, int type, int64_t at, int n, bool vec) {
-  Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+// Eight consecutive values from `at` on, at an address of a multiple of 16 bytes, as they are (w[0..7],
+// or w[0..3]), and back from floats.
+__device__ __forceinline__ void load8(const void* p, int type, int64_t at, uint32_t* w) {
+  const uint4* q = type == TQ_F32 ? reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + at)
+                                  : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+  const uint4 a = q[0];
+  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   if (type == TQ_F32) {
-    const uint32_t* f = static_cast<const uint32_t*>(p) + at;
-    if (vec && n == 8) {
-      r.v[0] = *reinterpret_cast<const uint4*>(f);
-      r.v[1] = *reinterpret_cast<const uint4*>(f + 4);
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = e < n ? f[e] : 0u;
-      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-    return r;
-  }
-  const uint16_t* h = static_cast<const uint16_t*>(p) + at;
-  if (vec && n == 8) {
-    r.v[0] = *reinterpret_cast<const uint4*>(h);
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = e < n ? h[e] : 0u;
-    r.v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-  }
-  return r;
-}
-__device__ __forceinline__ void floats8(const Raw8& r, int type, float (&v)[8]) {
-  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-  if (type == TQ_F32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = up((uint16_t)(w[e >> 1] >> (16 * (e & 1))), type);
+    const uint4 b = q[1];
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
 }
-__device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, const float (&v)[8]) {
   if (type == TQ_F32) {
-    float* f = static_cast<float*>(p) + at;
-    if (vec && n == 8) {
-      *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(f + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) f[e] = v[e];
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    f[0] = make_float4(v[0], v[1], v[2], v[3]);
+    f[1] = make_float4(v[4], v[5], v[6], v[7]);
     return;
   }
-  uint16_t* h = static_cast<uint16_t*>(p) + at;
-  uint16_t w[8];
+  uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = down(v[e], type);
-  if (vec && n == 8) {
-    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(w);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) h[e] = w[e];
+  for (int e = 0; e < 4; ++e) w[e] = (uint32_t)down(v[2 * e], type) | (uint32_t)down(v[2 * e + 1], type) << 16;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t load1(const void* p, int type, int64_t at) {
+  return type == TQ_F32 ? static_cast<const uint32_t*>(p)[at] : (uint32_t)static_cast<const uint16_t*>(p)[at];
+}
+__device__ __forceinline__ float up1(uint32_t w, int type) {
+  return type == TQ_F32 ? __uint_as_float(w) : up((uint16_t)w, type);
+}
+__device__ __forceinline__ void store1(void* p, int type, int64_t at, float v) {
+  if (type == TQ_F32) static_cast<float*>(p)[at] = v;
+  else static_cast<uint16_t*>(p)[at] = down(v, type);
 }
 
 // ---------------------------------------------------------------- tiles
@@ -217,7 +187,7 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, 
     before += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
   }
   before += __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1));
-  const bool first = id != -2 && (id >= 0 || p.copy) && before % kTile == 0;
+  const bool first = id != -2 && (id >= 0 || p.copy) && before % p.tile == 0;
   const unsigned firsts = __ballot_sync(0xffffffffu, first);
   if (lane == 0) red[warp] = __popc(firsts);
   __syncthreads();
@@ -234,7 +204,7 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, 
   for (int w = 0; w < kWarps; ++w) total += red[w];
   if (want >= total) return {-1, 0, 0};
   const int adapter = red[kWarps], from = red[kWarps + 1];
-  const bool mine = id == adapter && before >= from && before < from + kTile;
+  const bool mine = id == adapter && before >= from && before < from + p.tile;
   if (mine) tok[before - from] = i;
   const int n = __popc(__ballot_sync(0xffffffffu, mine));
   if (lane == 0 && n) atomicAdd(&red[kWarps + 3], n);
@@ -244,8 +214,8 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, 
 
 // More tokens: their order by adapter and the tiles, by one thread block.
 // Counters of the adapters (the last one: no adapter) in shared memory. Which of
-// an adapter's tokens come first is left to chance: a token's result does not
-// depend on its place.
+// an adapter's tokens come first is left to chance: a token's result depends
+// neither on its place nor on the other tokens of its tile.
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_constant__ Args p, int32_t* order,
                                                               int4* tiles, int* ntiles) {
   extern __shared__ int2 part[];                       // [32], their sum
@@ -279,7 +249,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
   // where each group's tokens and tiles start
   for (int g0 = 0; g0 < groups; g0 += kGroupThreads) {
     const int g = g0 + tid, n = g < groups ? counts[g] : 0;
-    int2 s = make_int2(n, (n + kTile - 1) / kTile);
+    int2 s = make_int2(n, (n + p.tile - 1) / p.tile);
     for (int d = 1; d < 32; d <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, s.x, d), b = __shfl_up_sync(0xffffffffu, s.y, d);
       if (lane >= d) {
@@ -290,7 +260,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
     if (lane == 31) part[warp] = s;
     __syncthreads();
     const int2 base = total;
-    int2 at = make_int2(base.x + s.x - n, base.y + s.y - (n + kTile - 1) / kTile);
+    int2 at = make_int2(base.x + s.x - n, base.y + s.y - (n + p.tile - 1) / p.tile);
     int2 sum = make_int2(0, 0);
     for (int w = 0; w < 32; ++w) {
       const int2 q = part[w];
@@ -307,8 +277,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
       counts[g] = at.x;
       const int id = g == groups - 1 ? -1 : g;
       const int rank = id < 0 || n == 0 ? 0 : p.l.rank ? __ldg(p.l.rank + id) : (int)p.l.max_rank;
-      for (int k = 0; k * kTile < n; ++k)
-        tiles[at.y + k] = make_int4(id, rank, at.x + k * kTile, min(kTile, n - k * kTile));
+      for (int k = 0; k * p.tile < n; ++k)
+        tiles[at.y + k] = make_int4(id, rank, at.x + k * p.tile, min(p.tile, n - k * p.tile));
     }
     __syncthreads();
   }
@@ -341,64 +311,48 @@ __device__ __forceinline__ float4 load_remote(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Shared memory in 4-byte words, for adapters of up to `top` rows of A in blocks of `block`: the
-// tile's description, the partial h of this block's columns, and the eight warps' parts of it, whose
-// place the split h takes afterwards.
+// Asynchronous copies of 16 and 8 bytes into this thread's own slots of shared memory: what a thread
+// copies it reads itself, so it waits for nobody. `have`: false gives zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(have ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 slot16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 slot8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put8(uint32_t a, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+
+constexpr int kStages = 4;       // of weights under way, a warp
+constexpr int kPitch = 33;       // floats of a row of results on their way to rows of Y at any address
+// Shared memory in 4-byte words, for adapters of up to `top` rows of A, NT row blocks at a time: the
+// tile's description, the partial h of this block's columns, the split h, the warps' stages of weights
+// (the first of which also takes the warp's part of h).
 constexpr int kHeadInts = kThreads + kTile + 16;
 __host__ __device__ constexpr int rank16(int top) { return (top + 15) / 16 * 16; }
 __host__ __device__ constexpr int part_floats(int top) { return kTile * rank16(top); }
-__host__ __device__ constexpr int work_floats(int top, int block) {
-  const int warps = kWarps * 16 * block, h = 2 * kTile * rank16(top);
-  return warps > h ? warps : h;
-}
-
-// What a warp needs of 32 rows of B and Y for 16 tokens, beside h: a thread's values of B for up to
-// 16 KG values of h, and of Z for its two tokens and eight rows.
-template <typename TW, int KG> struct Unit {
-  uint2 w[KG][4];
-  Raw8 z[2];
-  int64_t out;    // the first of its eight rows of Y
-  int some;       // how many of them there are
-
-  // Column g of block i is row 8 (g / 2) + 2 i + g % 2, so that a thread's results are consecutive rows.
-  __device__ __forceinline__ void load_b(const Args& p, const TW* B, int64_t n0, int k0, int rank, int g, int t) {
-#pragma unroll
-    for (int q = 0; q < KG; ++q) {
-      const int k = k0 + 16 * q + 4 * t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-        const TW* const b = B + n * p.l.b_row_stride + k;
-        w[q][i] = make_uint2(0, 0);
-        if (p.b_vec && k + 4 <= rank && n < p.l.rows) {
-          w[q][i] = __ldg(reinterpret_cast<const uint2*>(b));
-        } else if (n < p.l.rows && k < rank) {
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
-          w[q][i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void load_z(const Args& p, int64_t n0, const int (&token)[2], int t) {
-    out = n0 + 8 * t;
-    some = (int)max((int64_t)0, min((int64_t)8, p.l.rows - out));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (p.z && token[h] >= 0 && some > 0) {
-        z[h] = load8(p.z, p.y_type, token[h] * p.z_stride + out, some, p.z_vec);
-      } else {
-        z[h].v[0] = z[h].v[1] = make_uint4(0, 0, 0, 0);
-      }
-    }
-  }
-};
+__host__ __device__ constexpr int split_floats(int top) { return 2 * kTile * rank16(top); }
+__host__ __device__ constexpr int stage_floats(int nt) { return nt * 128; }
+__host__ __device__ constexpr int ring_floats(int nt) { return kWarps * kStages * stage_floats(nt); }
+constexpr int kPitchFloats = kWarps * 16 * kPitch;
 
 // NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns.
 template <typename TX, typename TW, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ Args p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
   constexpr int kBlock = 8 * NT, KG = NT / 2;
@@ -425,31 +379,50 @@ lora_kernel(const __grid_constant__ Args p) {
   }
   const int count = tile.count, rank = tile.rank;
   // rows of B and Y of this thread block, in units of 32
-  const int64_t rows = p.l.rows, units = (rows + 31) / 32, shares = (int64_t)p.splits * kCluster;
-  const int64_t share = (int64_t)part_of * kCluster + crank;
-  const int64_t unit0 = units * share / shares, unit1 = units * (share + 1) / shares;
+  const int rows = (int)p.l.rows, units = (rows + 31) / 32, shares = p.splits * kCluster;
+  const int share = part_of * kCluster + (int)crank;
+  const int unit0 = (int)((int64_t)units * share / shares), unit1 = (int)((int64_t)units * (share + 1) / shares);
 
   if (tile.adapter < 0) {   // Z as it is, to the bit
-    for (int j = 0; j < count; ++j) {
-      const int64_t to = s_tok[j] * p.y_stride, from = s_tok[j] * p.z_stride;
-      const int64_t end = min(rows, unit1 * 32);
-      if (p.y_type == TQ_F32) {
-        for (int64_t n = unit0 * 32 + tid; n < end; n += kThreads)
-          static_cast<uint32_t*>(p.y)[to + n] = p.z ? static_cast<const uint32_t*>(p.z)[from + n] : 0u;
+    const int begin = unit0 * 32, n = max(0, min(rows, unit1 * 32) - begin);
+    const int bytes = p.y_type == TQ_F32 ? 4 : 2, piece = p.y_vec && p.z_vec ? 16 / bytes : 1;
+    const int pieces = n / piece, left = n - pieces * piece;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int i = tid; i < count * pieces; i += kThreads) {
+      const int j = i / pieces, at = begin + (i - j * pieces) * piece;
+      const int64_t to = s_tok[j] * p.y_stride + at, from = s_tok[j] * p.z_stride + at;
+      if (piece > 1) {
+        reinterpret_cast<uint4*>(static_cast<char*>(p.y) + to * bytes)[0] =
+            p.z ? reinterpret_cast<const uint4*>(static_cast<const char*>(p.z) + from * bytes)[0] : zero;
+      } else if (bytes == 4) {
+        static_cast<uint32_t*>(p.y)[to] = p.z ? static_cast<const uint32_t*>(p.z)[from] : 0u;
       } else {
-        for (int64_t n = unit0 * 32 + tid; n < end; n += kThreads)
-          static_cast<uint16_t*>(p.y)[to + n] = p.z ? static_cast<const uint16_t*>(p.z)[from + n] : (uint16_t)0;
+        static_cast<uint16_t*>(p.y)[to] = p.z ? static_cast<const uint16_t*>(p.z)[from] : (uint16_t)0;
       }
+    }
+    for (int i = tid; i < count * left; i += kThreads) {
+      const int j = i / left, at = begin + pieces * piece + i - j * left;
+      const int64_t to = s_tok[j] * p.y_stride + at, from = s_tok[j] * p.z_stride + at;
+      if (bytes == 4) static_cast<uint32_t*>(p.y)[to] = p.z ? static_cast<const uint32_t*>(p.z)[from] : 0u;
+      else static_cast<uint16_t*>(p.y)[to] = p.z ? static_cast<const uint16_t*>(p.z)[from] : (uint16_t)0;
     }
     return;
   }
   const float scale = p.l.scale ? __ldg(p.l.scale + tile.adapter) : 1.0f;
   const int wide = rank16(rank);          // values of h a token, with zeros behind the rank
-  // up to 16 tokens: all warps take them; more: half of the warps each 16
+  // Small tiles: the two parts of a value are rows g and g + 8 of one product.
+  // Others: up to 16 tokens, all warps take the 16 rows; more: half of the warps each 16.
+  const bool packed = p.tile == kSmallTile;
   const int mblocks = count > 16 ? 2 : 1, m = mblocks == 2 ? warp >> 2 : 0;
   const int turn = mblocks == 2 ? warp & 3 : warp, turns = kWarps / mblocks;
   float* const part = reinterpret_cast<float*>(shared4) + kHeadInts; // [kTile][wide]
-  float* const work = part + part_floats((int)p.l.max_rank);         // [kWarps][16][kBlock], then h
+  uint32_t* const hi = reinterpret_cast<uint32_t*>(part + part_floats((int)p.l.max_rank));
+  uint32_t* const lo = hi + mblocks * 16 * wide;
+  float* const ring = reinterpret_cast<float*>(hi + split_floats((int)p.l.max_rank));
+  float* const own_ring = ring + warp * kStages * stage_floats(NT);
+  const uint32_t slots = smem_u32(own_ring);                          // [kStages][NT][32] pieces of 16 bytes
+  float* const pitched = ring + ring_floats(NT) + warp * 16 * kPitch;
   const int token[2] = {16 * m + g < count ? s_tok[16 * m + g] : -1,
                         16 * m + 8 + g < count ? s_tok[16 * m + 8 + g] : -1};
 
@@ -457,111 +430,197 @@ lora_kernel(const __grid_constant__ Args p) {
   const TW* const A = static_cast<const TW*>(p.l.a) + tile.adapter * p.l.a_stride;
   const int cols = (int)p.l.cols, chunks = (cols + 31) / 32;
   const int chunk0 = (int)((int64_t)chunks * crank / kCluster), chunk1 = (int)((int64_t)chunks * (crank + 1) / kCluster);
-  const TX* const x0 = static_cast<const TX*>(p.x) + token[0] * p.x_stride;
-  const TX* const x1 = static_cast<const TX*>(p.x) + token[1] * p.x_stride;
+  const TX* const x0 = static_cast<const TX*>(p.x) + token[0] * p.x_stride + 8 * t;
+  const TX* const x1 = static_cast<const TX*>(p.x) + token[1] * p.x_stride + 8 * t;
+  // A share is every eighth chunk of 32 columns; a warp has one, or two with 16 rows for each half of
+  // the warps: the sums are the same ones either way.
   for (int r0 = 0; r0 < rank; r0 += kBlock) {
-    float acc[NT][4];
+#pragma unroll 1
+   for (int share_of = turn; share_of < kParts; share_of += turns) {
+    const int mine = max(0, (chunk1 - chunk0 - share_of + kParts - 1) / kParts);     // its chunks
+    // The tensor cores cut their sums where 32-bit additions round, which leans
+    // one way: every kChain chunks the sum is added to another, by additions that
+    // round (without, 2176 columns a warp at rank 256 were 3.3e-6 off, with 2.2e-6).
+    float acc[NT][4], sum[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-    const TW* const Ar = A + (r0 + g) * p.l.a_row_stride;
-    if (r0 > 0) __syncthreads();
-    // The tensor cores cut their sums where 32-bit additions round, which leans
-    // one way: after a few chunks the sum goes to this thread's place in shared
-    // memory, by an addition that rounds (256 of 2176 columns a warp's chain
-    // long, rank 256: 2.2e-6 of the result; without, 3.3e-6).
-    float* const mine = work + (warp * 16 + g) * kBlock + 2 * t;
-    auto flush = [&](bool first) {
+      for (int e = 0; e < 4; ++e) acc[j][e] = sum[j][e] = 0.0f;
+    const TW* const Ar = A + (r0 + g) * p.l.a_row_stride + 8 * t;
+    auto issue = [&](int i) {
+      if (i < mine) {
+        const int k = (chunk0 + share_of + i * kParts) * 32;
+        const uint32_t at = slots + (i & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 16;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2* const at = reinterpret_cast<float2*>(mine + 8 * h * kBlock + 8 * j);
-          float2 sum = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
-          if (!first) {
-            const float2 old = *at;
-            sum.x += old.x;
-            sum.y += old.y;
-          }
-          *at = sum;
-          acc[j][2 * h] = acc[j][2 * h + 1] = 0.0f;
+        for (int j = 0; j < NT; ++j) {
+          const bool have = k + 8 * t < cols && r0 + 8 * j + g < rank;    // (cols is a multiple of 8)
+          copy16(at + j * 512, have ? Ar + 8 * j * p.l.a_row_stride + k : A, have);
         }
+      }
+      copies_issued();
     };
-    int done = 0;
-#pragma unroll 2
-    for (int c = chunk0 + turn; c < chunk1; c += turns, ++done) {
-      if (done > 0 && done % kChain == 0) flush(done == kChain);
-      const int k = c * 32 + 8 * t;
-      const bool in = k < cols;       // (cols is a multiple of 8)
-      uint4 w[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        w[j] = in && r0 + 8 * j + g < rank
-                   ? __ldg(reinterpret_cast<const uint4*>(Ar + 8 * j * p.l.a_row_stride + k))
-                   : make_uint4(0, 0, 0, 0);
-      Acts<TX> v[2];
+    auto load_x = [&](int i, Acts<TX> (&v)[2]) {
+      const int k = (chunk0 + share_of + i * kParts) * 32;
+      const bool in = i < mine && k + 8 * t < cols;
       if (in && token[0] >= 0) v[0].load(x0 + k);
       else v[0].clear();
       if (in && token[1] >= 0) v[1].load(x1 + k);
       else v[1].clear();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    Acts<TX> next[2];
+    load_x(0, next);
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      issue(i + kStages - 1);
+      Acts<TX> v[2] = {next[0], next[1]};
+      load_x(i + 1, next);
+      copies_but<kStages - 1>();
+      uint4 w[NT];
+      const uint32_t at = slots + (i & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) w[j] = slot16(at + j * 512);
       __syncwarp();     // the products take a whole warp
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        uint32_t hi[4], lo[4];
+        uint32_t fa[4], fb[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a, b;
           v[h].pair(s, a, b);
           if constexpr (kSplit) {
-            split(__uint_as_float(a), hi[h], lo[h]);
-            split(__uint_as_float(b), hi[2 + h], lo[2 + h]);
+            split(__uint_as_float(a), fa[h], fb[h]);
+            split(__uint_as_float(b), fa[2 + h], fb[2 + h]);
           } else {
-            hi[h] = a;
-            hi[2 + h] = b;
+            fa[h] = a;
+            fa[2 + h] = b;
           }
+        }
+        if (kSplit && packed) {
+          fa[1] = fb[0];
+          fa[3] = fb[2];
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if (r0 + 8 * j >= rank) break;
           uint32_t b0, b1;
           widen<TW>(s == 0 ? w[j].x : s == 1 ? w[j].y : s == 2 ? w[j].z : w[j].w, b0, b1);
-          mma_tf32(acc[j], hi, b0, b1);
-          if constexpr (kSplit) mma_tf32(acc[j], lo, b0, b1);
+          mma_tf32(acc[j], fa, b0, b1);
+          if (kSplit && !packed) mma_tf32(acc[j], fb, b0, b1);
         }
       }
+      if (i % kChain == kChain - 1 || i == mine - 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[j][e] += acc[j][e];
+            acc[j][e] = 0.0f;
+          }
+      }
     }
-    // the warps' parts, summed in their order
-    flush(done <= kChain);
+    // to where the shares are summed: a warp's last one in its first stage
+    copies_but<0>();
+    float* const place = share_of + turns < kParts ? pitched : own_ring;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float* const to = place + g * kBlock + 8 * j + 2 * t;
+      if (packed) {
+        *reinterpret_cast<float2*>(to) = make_float2(sum[j][0] + sum[j][2], sum[j][1] + sum[j][3]);
+        *reinterpret_cast<float2*>(to + 8 * kBlock) = make_float2(0.0f, 0.0f);
+      } else {
+        *reinterpret_cast<float2*>(to) = make_float2(sum[j][0], sum[j][1]);
+        *reinterpret_cast<float2*>(to + 8 * kBlock) = make_float2(sum[j][2], sum[j][3]);
+      }
+    }
+   }
     __syncthreads();
     const int here = min(kBlock, wide - r0);
     for (int i = tid; i < mblocks * 16 * kBlock; i += kThreads) {
-      const int j = i / kBlock, r = i % kBlock;
+      const int j = i / kBlock, r = i % kBlock, first = (j >> 4) * turns, at = (j & 15) * kBlock + r;
       if (r >= here) continue;
-      const int first = (j >> 4) * turns;
-      float sum = 0.0f;
-      for (int w = 0; w < turns; ++w) sum += work[((first + w) * 16 + (j & 15)) * kBlock + r];
-      part[j * wide + r0 + r] = sum;
+      float total = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        const int w = first + (q & (turns - 1));
+        total += (q + turns < kParts ? ring + ring_floats(NT) + w * 16 * kPitch : ring + w * kStages * stage_floats(NT))[at];
+      }
+      part[j * wide + r0 + r] = total;
     }
+    __syncthreads();
   }
-  // what the second product starts with is on its way while the blocks wait for one another
+
+  // ---- Y = Z + B h: what it starts with is on its way while the blocks wait for one another
   const TW* const B = static_cast<const TW*>(p.l.b) + tile.adapter * p.l.b_stride;
-  Unit<TW, KG> in;
-  if (unit0 + turn < unit1) {
-    in.load_z(p, (unit0 + turn) * 32, token, t);
-    in.load_b(p, B, (unit0 + turn) * 32, 0, rank, g, t);
-  }
+  const int groups = wide / 16, turns_b = (groups + KG - 1) / KG;      // turns of 16 KG values of h a unit
+  const int items = max(0, (unit1 - unit0 - turn + turns - 1) / turns) * turns_b;
+  // Column g of block i is row 8 (g / 2) + 2 i + g % 2, so that a thread's results are consecutive rows.
+  const int row_of = 8 * (g >> 1) + (g & 1);
+  int unit_ahead = unit0 + turn, turn_ahead = 0;
+  auto issue = [&](int item) {
+    if (item < items) {
+      const uint32_t at = slots + (item & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 8;
+#pragma unroll
+      for (int q = 0; q < KG; ++q) {
+        const int k = 16 * (turn_ahead * KG + q) + 4 * t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = unit_ahead * 32 + row_of + 2 * i;
+          const bool have = n < rows && k < rank;
+          const TW* const b = have ? B + n * p.l.b_row_stride + k : B;
+          const uint32_t to = at + (q * 4 + i) * 256;
+          if (p.b_vec && (k + 4 <= rank || !have)) {
+            copy8(to, have ? b : reinterpret_cast<const TW*>(p.l.b), have);
+          } else {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = have && k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
+            put8(to, make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16));
+          }
+        }
+      }
+      if (++turn_ahead == turns_b) {
+        turn_ahead = 0;
+        unit_ahead += turns;
+      }
+    }
+    copies_issued();
+  };
+  const bool vec = p.y_vec && p.z_vec;
+  // Z of 16 tokens and 32 rows: the eight rows of this thread's two tokens, or
+  // (rows of Y or Z at any address, or the last of them) a row of each of the 16
+  auto load_z = [&](int u, uint32_t (&z)[16]) {
+    if (u >= unit1 || !p.z) return;
+    const int n0 = u * 32;
+    if (vec && n0 + 32 <= rows) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (token[h] >= 0) load8(p.z, p.y_type, token[h] * p.z_stride + n0 + 8 * t, z + 8 * h);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (16 * m + j < count && n0 + lane < rows)
+          z[j] = load1(p.z, p.y_type, s_tok[16 * m + j] * p.z_stride + n0 + lane);
+    }
+  };
+  uint32_t z_next[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z_next[e] = 0;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  load_z(unit0 + turn, z_next);
   cluster_arrive();
   cluster_wait();
 
   // ---- h of all columns, split, in the order of the fragments: for each 8 values
   // of h and 16 tokens, a lane's four values
-  uint32_t* const hi = reinterpret_cast<uint32_t*>(work);
-  uint32_t* const lo = hi + mblocks * 16 * wide;
   {
     const uint32_t base = smem_u32(part);
-    for (int i = tid; i < mblocks * 16 * wide / 4; i += kThreads) {
-      const int j = i / (wide / 4), q = i % (wide / 4);     // values 4 q .. 4 q + 3 of token j
+    const int quads = wide / 4, tokens = packed ? 8 : mblocks * 16;
+    for (int i = tid; i < tokens * quads; i += kThreads) {
+      const int j = i / quads, q = i % quads;     // values 4 q .. 4 q + 3 of token j
       float4 v[kCluster];
 #pragma unroll
       for (int c = 0; c < kCluster; ++c) v[c] = load_remote(base + (j * wide + 4 * q) * 4, c);
@@ -579,32 +638,39 @@ lora_kernel(const __grid_constant__ Args p) {
         const int step = 2 * (q >> 2) + (e >> 1);
         const int at = ((step * mblocks + mb) * 32 + l) * 4 + half + 2 * (e & 1);
         // (past the rank an infinite activation has left a NaN)
-        split(4 * q + e < rank ? h[e] * scale : 0.0f, hi[at], lo[at]);
+        uint32_t a, b;
+        split(4 * q + e < rank ? h[e] * scale : 0.0f, a, b);
+        hi[at] = a;
+        (packed ? hi + 1 : lo)[at] = b;
       }
     }
   }
   __syncthreads();
   cluster_arrive();     // this block's part has no reader left when all have arrived
 
-  // ---- Y = Z + B h
-  const int groups = wide / 16;
-  bool loaded = true;
+  int item = 0;
 #pragma unroll 1
-  for (int64_t u = unit0 + turn; u < unit1; u += turns) {
-    const int64_t n0 = u * 32;
-    if (!loaded) {
-      in.load_z(p, n0, token, t);
-      in.load_b(p, B, n0, 0, rank, g, t);
-    }
-    loaded = false;
+  for (int u = unit0 + turn; u < unit1; u += turns) {
+    const int n0 = u * 32;
+    uint32_t z[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = z_next[e];
+    load_z(u + turns, z_next);
     float acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 #pragma unroll 1
-    for (int q0 = 0; q0 < groups; q0 += KG) {
-      if (q0 > 0) in.load_b(p, B, n0, 16 * q0, rank, g, t);
+    for (int q0 = 0; q0 < groups; q0 += KG, ++item) {
+      issue(item + kStages - 1);
+      copies_but<kStages - 1>();
+      const uint32_t from = slots + (item & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 8;
+      uint2 w[KG][4];
+#pragma unroll
+      for (int q = 0; q < KG; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[q][i] = slot8(from + (q * 4 + i) * 256);
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < KG; ++q) {
@@ -612,34 +678,67 @@ lora_kernel(const __grid_constant__ Args p) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int at = (((2 * (q0 + q) + s) * mblocks + m) * 32 + lane) * 4;
-          const uint4 a = *reinterpret_cast<const uint4*>(hi + at), b = *reinterpret_cast<const uint4*>(lo + at);
-          const uint32_t fa[4] = {a.x, a.y, a.z, a.w}, fb[4] = {b.x, b.y, b.z, b.w};
+          const uint4 a = *reinterpret_cast<const uint4*>(hi + at);
+          const uint32_t fa[4] = {a.x, a.y, a.z, a.w};
+          uint4 b = make_uint4(0, 0, 0, 0);
+          if (!packed) b = *reinterpret_cast<const uint4*>(lo + at);
+          const uint32_t fb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t b0, b1;
-            widen<TW>(s ? in.w[q][i].y : in.w[q][i].x, b0, b1);
+            widen<TW>(s ? w[q][i].y : w[q][i].x, b0, b1);
             mma_tf32(acc[i], fa, b0, b1);
-            mma_tf32(acc[i], fb, b0, b1);
+            if (!packed) mma_tf32(acc[i], fb, b0, b1);
           }
         }
       }
     }
+    if (packed) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (token[h] < 0 || in.some == 0) continue;
-      float v[8];
-      floats8(in.z[h], p.y_type, v);
+      for (int i = 0; i < 4; ++i) {
+        acc[i][0] += acc[i][2];
+        acc[i][1] += acc[i][3];
+      }
+    }
+    if (vec && n0 + 32 <= rows) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += acc[e >> 1][2 * h + (e & 1)];
-      store8(p.y, p.y_type, token[h] * p.y_stride + in.out, in.some, p.y_vec, v);
+      for (int h = 0; h < 2; ++h) {
+        if (token[h] < 0) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = p.y_type == TQ_F32 ? __uint_as_float(z[8 * h + e])
+                                    : up((uint16_t)(z[8 * h + (e >> 1)] >> (16 * (e & 1))), p.y_type);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += acc[e >> 1][2 * h + (e & 1)];
+        store8(p.y, p.y_type, token[h] * p.y_stride + n0 + 8 * t, v);
+      }
+    } else {
+      // rows of Y at any address: through shared memory, so that a warp stores
+      // 32 rows of a token
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pitched[(8 * h + g) * kPitch + 8 * t + e] = acc[e >> 1][2 * h + (e & 1)];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (16 * m + j < count && n0 + lane < rows)
+          store1(p.y, p.y_type, s_tok[16 * m + j] * p.y_stride + n0 + lane,
+                 up1(z[j], p.y_type) + pitched[j * kPitch + lane]);
+      __syncwarp();
     }
   }
+  copies_but<0>();
   cluster_wait();
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Tiles of 8 tokens where adapters have no more than that each on average. (A function of the call's
+// sizes alone: so is the order of every sum.)
+int64_t tile_of(int64_t ntok, int64_t adapters) { return ntok <= kSmallTile * adapters ? kSmallTile : kTile; }
 int64_t max_tiles(int64_t ntok, int64_t adapters) {
-  return std::min(ntok, ntok / kTile + std::min(adapters, ntok) + 1);
+  return std::min(ntok, ntok / tile_of(ntok, adapters) + std::min(adapters, ntok) + 1);
 }
 
 bool in_pieces(const void* p, int64_t stride, int64_t bytes, int64_t piece) {
@@ -650,7 +749,7 @@ template <typename TX, typename TW, int NT>
 cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
   const auto kernel = lora_kernel<TX, TW, NT>;
   const int top = (int)a.l.max_rank;
-  const int smem = (kHeadInts + part_floats(top) + work_floats(top, 8 * NT)) * (int)sizeof(float);
+  const int smem = (kHeadInts + part_floats(top) + split_floats(top) + ring_floats(NT) + kPitchFloats) * (int)sizeof(float);
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -673,9 +772,7 @@ cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
 
 template <typename TX, typename TW>
 cudaError_t launch_for(const Args& a, int64_t tiles, cudaStream_t s) {
-  if (a.l.max_rank <= 16) return launch_as<TX, TW, 2>(a, tiles, s);
-  if (a.l.max_rank <= 32) return launch_as<TX, TW, 4>(a, tiles, s);
-  return launch_as<TX, TW, 8>(a, tiles, s);
+  return a.l.max_rank <= 16 ? launch_as<TX, TW, 2>(a, tiles, s) : launch_as<TX, TW, 4>(a, tiles, s);
 }
 
 }  // namespace
@@ -699,6 +796,7 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
   a.y_type = c.y_type;
   a.ntok = (int)c.ntok;
   a.copy = c.z != c.y;
+  a.tile = (int)tile_of(c.ntok, c.lora.adapters);
   a.status = c.status;
   const int64_t yb = c.y_type == TQ_F32 ? 4 : 2;
   a.y_vec = in_pieces(c.y, c.ntok > 1 ? c.y_stride : 0, yb, 16);
