@@ -35,7 +35,9 @@ constexpr int kList = 1024;                 // tokens that are sorted
 constexpr int kBlock = 512;                 // tokens of a sum
 constexpr int kMaxBlocks = kMaxVocab / kBlock + 1;
 constexpr int kMaxCluster = 16;
-constexpr int kSlots = 304;                 // thread blocks at once: two on each of 152 SMs
+constexpr int kSlots = 608;                 // thread blocks of a call at most: twice as many as run at once
+                                            // (200 rows of 128001 f16, top-k: 135 us with 304, 73 with 608, 84
+                                            // with 1216; 64 rows of 131072: 51, 48, 80)
 constexpr int kMaxResident = 65536;         // bytes of a slice in shared memory
 static_assert(kMaxVocab == 1 << kIndexBits, "an index below a logit's bits");
 static_assert(kBlock == kThreads && kList == 2 * kThreads, "one token, two entries a thread");
@@ -85,7 +87,8 @@ struct alignas(16) Shared {
   int first;                  // lowest index of the largest logit
   u64 pick[4];
   u64 warps[3][kWeightBins / 128];
-  uint32_t least_top[kWarps];
+  uint32_t least_top[kWarps], tops[kThreads];   // tops: counts of threads by their largest logit
+  uint32_t bound;             // a logit that so many tokens are at or above
 };
 static_assert(sizeof(Shared) % 16 == 0, "the slice behind it in 16-byte pieces");
 
@@ -678,6 +681,38 @@ template <typename T> struct Row {
     return scan(s, all).all;
   }
 
+  // The tokens at `lo` or above in this block's list: each warp's in a part of
+  // s->weight first. s->have is more than kList if they do not fit there.
+  __device__ __forceinline__ void gather_from(float lo) const {
+    constexpr int kEach = kList / kWarps;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
+    each([&](const float (&l)[4], int i) {
+      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= lo)) return;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned m = __ballot_sync(0xffffffffu, l[e] >= lo);
+        const int at = n + __popc(m & ((1u << lane) - 1));
+        if (l[e] >= lo && at < kEach) s->weight[warp * kEach + at] = place(l[e], i + e);
+        n += __popc(m);
+      }
+    });
+    if (lane == 0) s->least_top[warp] = (uint32_t)n;
+    __syncthreads();
+    const uint32_t of = lane < kWarps ? s->least_top[lane] : 0;
+    const bool fits = __all_sync(0xffffffffu, of <= kEach);
+    const int all = (int)__reduce_add_sync(0xffffffffu, of);
+    const int before = (int)__reduce_add_sync(0xffffffffu, lane < warp ? of : 0);
+    if (fits)
+      for (int i = lane; i < n; i += 32) s->list[before + i] = s->weight[warp * kEach + i];
+    if (threadIdx.x == 0) s->have = fits ? all : kList + 1;
+  }
+  // Entries of all blocks' lists (after the cluster has met).
+  __device__ __forceinline__ int listed() const {
+    const int lane = threadIdx.x & 31;
+    return (int)__reduce_add_sync(0xffffffffu, lane < cluster ? remote_u32(remote(&s->have, lane)) : 0);
+  }
+
   // (rank 0) All blocks' lists in this one's, sorted, the highest first; returns
   // their number. The weights are in s->weight.
   __device__ __forceinline__ int join() const {
@@ -929,7 +964,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   for (int j = tid; j < (int)(sizeof(ExpTable) / 16); j += kThreads)
     reinterpret_cast<uint4*>(&s->table)[j] = reinterpret_cast<const uint4*>(&g_exp_table)[j];
   for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
-  if (tid == 0) s->first = 0x7fffffff;
+  s->tops[tid] = 0;
+  if (tid == 0) {
+    s->first = 0x7fffffff;
+    s->bound = 0xffffffffu;
+  }
   pdl_wait_primary();
   pdl_launch_dependents();
 
@@ -974,31 +1013,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       top = max_or_nan(top, Elem<T>::up(v));
     }
   }
-  // The largest logits of groups of four threads: as many tokens as there are
-  // groups are at least the least of these, so no cut by such a count is below it.
-  uint32_t least_top = 0;
+  // `top` is each thread's largest logit now. As many threads as have theirs at
+  // or above some value, so many tokens are there; the `share`-th largest of them
+  // bounds a cut by count from below (and few tokens are above it that do not
+  // belong). It is found among 512 equal parts of their range.
+  uint32_t bound = 0;
+  const int share = (k + a.cluster - 1) / a.cluster;
+  const bool bounded = by_count && share <= kThreads;
   {
-    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    least_top = __reduce_min_sync(0xffffffffu, order_key(top));
+    const float own = top;
+    uint32_t least = __reduce_min_sync(0xffffffffu, order_key(top));
 #pragma unroll
-    for (int d = 16; d > 2; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
     float* const tops = reinterpret_cast<float*>(s->scan);
     if (lane == 0) {
       tops[warp] = top;
-      s->least_top[warp] = least_top;
+      s->least_top[warp] = least;
     }
     __syncthreads();
     top = tops[lane & (kWarps - 1)];
-    least_top = __reduce_min_sync(0xffffffffu, s->least_top[lane & (kWarps - 1)]);
+    least = __reduce_min_sync(0xffffffffu, s->least_top[lane & (kWarps - 1)]);
 #pragma unroll
     for (int d = kWarps / 2; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (bounded) {
+      const float low = key_value(least);
+      const float steps = (float)(kThreads - 1) / (top - low);      // (no number where the range is infinite or nothing)
+      const int part = min(kThreads - 1, max(0, (int)((own - low) * steps)));
+      atomicAdd(&s->tops[part], 1u);
+      __syncthreads();
+      // every warp: 16 parts a lane, the highest first
+      uint32_t n = 0;
+      constexpr int kEach = kThreads / 32;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) n += s->tops[kThreads - 1 - (lane * kEach + e)];
+      uint32_t upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const int lane_of = __ffs(__ballot_sync(0xffffffffu, upto >= (uint32_t)share)) - 1;
+      uint32_t before = __shfl_sync(0xffffffffu, upto - n, lane_of);
+      int at = kThreads - 1 - lane_of * kEach;
+      for (; (before += s->tops[at]) < (uint32_t)share; --at) {
+      }
+      // the least of the threads' values in that part or above
+      const uint32_t mine = __reduce_min_sync(0xffffffffu, part >= at ? order_key(own) : 0xffffffffu);
+      if (lane == 0) atomicMin(&s->bound, mine);
+      __syncthreads();
+      bound = s->bound;
+    }
     if (a.cluster > 1) {
-      if (tid == 0) s->give[3] = (u64)least_top << 32 | __float_as_uint(top);
+      if (tid == 0) s->give[3] = (u64)bound << 32 | __float_as_uint(top);
       meet(a.cluster);
       const u64 v = remote_u64(remote(&s->give[3], min(lane, a.cluster - 1)));
       top = __uint_as_float((uint32_t)v);
-      least_top = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
+      bound = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
     }
@@ -1053,17 +1123,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int j = tid; j < kWeightBins; j += kThreads) s->bins[j] = 0;
         __syncthreads();
       }
-      u64 target = (u64)k;
-      const bool bounded = !r.infinite && k <= a.cluster * (kThreads / 4);
-      Window w = r.search(weights, target, cut, top_key, p, bounded ? key_value(least_top) : -INFINITY);
-      // all tokens that may be kept fit in the list
-      const bool whole = w.upto <= kList;
-      if (whole) w.hi = ((u64)top_key << kIndexBits) | kIndexMask;
-      else if (w.inside > kList) w = Row<T>::narrow(r, w, weights, target);
-      const u64 mine = r.gather(w, weights && !whole);
-      u64 above = 0;
-      if (weights && !whole) above = over_cluster(s, mine, 1, a.cluster, rank).all;
-      else meet(a.cluster);
+      u64 target = (u64)k, above = 0;
+      Window w = {0, ((u64)top_key << kIndexBits) | kIndexMask, 0, 0, 0};
+      bool whole = false;       // all tokens that may be kept are in the list
+      const bool usable = bounded && !r.infinite && bound > order_key(-INFINITY);
+      if (!weights && usable) {
+        r.gather_from(key_value(bound));
+        meet(a.cluster);
+        whole = r.listed() <= kList;
+        if (!whole) meet(a.cluster);       // the last reading of the counts is over
+      }
+      if (!whole) {
+        w = r.search(weights, target, cut, top_key, p, usable ? key_value(bound) : -INFINITY);
+        whole = w.upto <= kList;
+        if (whole) w.hi = ((u64)top_key << kIndexBits) | kIndexMask;
+        else if (w.inside > kList) w = Row<T>::narrow(r, w, weights, target);
+        const u64 mine = r.gather(w, weights && !whole);
+        if (weights && !whole) above = over_cluster(s, mine, 1, a.cluster, rank).all;
+        else meet(a.cluster);
+      }
       int n = s->have;        // entries of the list
       if (rank == 0) {
         n = r.join();
@@ -1179,7 +1257,7 @@ template <typename T> cudaError_t launch_as(const SampleCall& c, cudaStream_t s)
   // Thread blocks a row: as many as run at once (two an SM), where slices have
   // 2048 tokens at least.
   while (a.cluster < kMaxCluster && 2 * c.ntok * a.cluster <= kSlots && c.vocab > a.cluster * 2048) a.cluster *= 2;
-  a.slice = ((c.vocab + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
+  a.slice = ((c.vocab + a.cluster - 1) / a.cluster + 31) / 32 * 32;
   if (c.ntok * a.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // In shared memory where two slices fit into an SM's, else read again from L2.
   return a.slice * (int)sizeof(T) <= kMaxResident ? launch_kernel<T, true>(a, c.ntok, s)
