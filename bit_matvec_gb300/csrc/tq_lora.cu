@@ -337,22 +337,23 @@ __device__ __forceinline__ void put8(uint32_t a, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
-constexpr int kStages = 4;       // of weights under way, a warp
+constexpr int kStages = 3;       // of weights under way, a warp
 constexpr int kPitch = 33;       // floats of a row of results on their way to rows of Y at any address
 // Shared memory in 4-byte words, for adapters of up to `top` rows of A, NT row blocks at a time: the
 // tile's description, the partial h of this block's columns, the split h, the warps' stages of weights
 // (the first of which also takes the warp's part of h).
 constexpr int kHeadInts = kThreads + kTile + 16;
 __host__ __device__ constexpr int rank16(int top) { return (top + 15) / 16 * 16; }
-__host__ __device__ constexpr int part_floats(int top) { return kTile * rank16(top); }
-__host__ __device__ constexpr int split_floats(int top) { return 2 * kTile * rank16(top); }
+__host__ __device__ constexpr int part_floats(int top, bool packed) { return (packed ? 16 : kTile) * rank16(top); }
+__host__ __device__ constexpr int split_floats(int top, bool packed) { return (packed ? 16 : 2 * kTile) * rank16(top); }
 __host__ __device__ constexpr int stage_floats(int nt) { return nt * 128; }
 __host__ __device__ constexpr int ring_floats(int nt) { return kWarps * kStages * stage_floats(nt); }
-constexpr int kPitchFloats = kWarps * 16 * kPitch;
+__host__ __device__ constexpr int pitch_floats(bool packed) { return kWarps * (packed ? 8 : 16) * kPitch; }
 
-// NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns.
-template <typename TX, typename TW, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+// NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns. kPacked:
+// small tiles, the two parts of a value as rows g and g + 8 of one product.
+template <typename TX, typename TW, int NT, bool kPacked>
+__global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2)
 lora_kernel(const __grid_constant__ Args p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
   constexpr int kBlock = 8 * NT, KG = NT / 2;
@@ -411,20 +412,18 @@ lora_kernel(const __grid_constant__ Args p) {
   }
   const float scale = p.l.scale ? __ldg(p.l.scale + tile.adapter) : 1.0f;
   const int wide = rank16(rank);          // values of h a token, with zeros behind the rank
-  // Small tiles: the two parts of a value are rows g and g + 8 of one product.
-  // Others: up to 16 tokens, all warps take the 16 rows; more: half of the warps each 16.
-  const bool packed = p.tile == kSmallTile;
-  const int mblocks = count > 16 ? 2 : 1, m = mblocks == 2 ? warp >> 2 : 0;
+  // Up to 16 tokens: all warps take them; more: half of the warps each 16.
+  const int mblocks = !kPacked && count > 16 ? 2 : 1, m = mblocks == 2 ? warp >> 2 : 0;
   const int turn = mblocks == 2 ? warp & 3 : warp, turns = kWarps / mblocks;
   float* const part = reinterpret_cast<float*>(shared4) + kHeadInts; // [kTile][wide]
-  uint32_t* const hi = reinterpret_cast<uint32_t*>(part + part_floats((int)p.l.max_rank));
+  uint32_t* const hi = reinterpret_cast<uint32_t*>(part + part_floats((int)p.l.max_rank, kPacked));
   uint32_t* const lo = hi + mblocks * 16 * wide;
-  float* const ring = reinterpret_cast<float*>(hi + split_floats((int)p.l.max_rank));
+  float* const ring = reinterpret_cast<float*>(hi + split_floats((int)p.l.max_rank, kPacked));
   float* const own_ring = ring + warp * kStages * stage_floats(NT);
   const uint32_t slots = smem_u32(own_ring);                          // [kStages][NT][32] pieces of 16 bytes
-  float* const pitched = ring + ring_floats(NT) + warp * 16 * kPitch;
+  float* const pitched = ring + ring_floats(NT) + warp * (kPacked ? 8 : 16) * kPitch;
   const int token[2] = {16 * m + g < count ? s_tok[16 * m + g] : -1,
-                        16 * m + 8 + g < count ? s_tok[16 * m + 8 + g] : -1};
+                        !kPacked && 16 * m + 8 + g < count ? s_tok[16 * m + 8 + g] : -1};
 
   // ---- h = A x over this block's columns
   const TW* const A = static_cast<const TW*>(p.l.a) + tile.adapter * p.l.a_stride;
@@ -450,7 +449,7 @@ lora_kernel(const __grid_constant__ Args p) {
     auto issue = [&](int i) {
       if (i < mine) {
         const int k = (chunk0 + share_of + i * kParts) * 32;
-        const uint32_t at = slots + (i & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 16;
+        const uint32_t at = slots + (i % kStages) * (stage_floats(NT) * 4) + lane * 16;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const bool have = k + 8 * t < cols && r0 + 8 * j + g < rank;    // (cols is a multiple of 8)
@@ -464,7 +463,7 @@ lora_kernel(const __grid_constant__ Args p) {
       const bool in = i < mine && k + 8 * t < cols;
       if (in && token[0] >= 0) v[0].load(x0 + k);
       else v[0].clear();
-      if (in && token[1] >= 0) v[1].load(x1 + k);
+      if (!kPacked && in && token[1] >= 0) v[1].load(x1 + k);
       else v[1].clear();
     };
 #pragma unroll
@@ -478,7 +477,7 @@ lora_kernel(const __grid_constant__ Args p) {
       load_x(i + 1, next);
       copies_but<kStages - 1>();
       uint4 w[NT];
-      const uint32_t at = slots + (i & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 16;
+      const uint32_t at = slots + (i % kStages) * (stage_floats(NT) * 4) + lane * 16;
 #pragma unroll
       for (int j = 0; j < NT; ++j) w[j] = slot16(at + j * 512);
       __syncwarp();     // the products take a whole warp
@@ -487,8 +486,8 @@ lora_kernel(const __grid_constant__ Args p) {
         uint32_t fa[4], fb[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t a, b;
-          v[h].pair(s, a, b);
+          uint32_t a = 0, b = 0;
+          if (!kPacked || h == 0) v[h].pair(s, a, b);
           if constexpr (kSplit) {
             split(__uint_as_float(a), fa[h], fb[h]);
             split(__uint_as_float(b), fa[2 + h], fb[2 + h]);
@@ -497,7 +496,7 @@ lora_kernel(const __grid_constant__ Args p) {
             fa[2 + h] = b;
           }
         }
-        if (kSplit && packed) {
+        if (kSplit && kPacked) {
           fa[1] = fb[0];
           fa[3] = fb[2];
         }
@@ -507,7 +506,7 @@ lora_kernel(const __grid_constant__ Args p) {
           uint32_t b0, b1;
           widen<TW>(s == 0 ? w[j].x : s == 1 ? w[j].y : s == 2 ? w[j].z : w[j].w, b0, b1);
           mma_tf32(acc[j], fa, b0, b1);
-          if (kSplit && !packed) mma_tf32(acc[j], fb, b0, b1);
+          if (kSplit && !kPacked) mma_tf32(acc[j], fb, b0, b1);
         }
       }
       if (i % kChain == kChain - 1 || i == mine - 1) {
@@ -526,7 +525,7 @@ lora_kernel(const __grid_constant__ Args p) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float* const to = place + g * kBlock + 8 * j + 2 * t;
-      if (packed) {
+      if (kPacked) {
         *reinterpret_cast<float2*>(to) = make_float2(sum[j][0] + sum[j][2], sum[j][1] + sum[j][3]);
         *reinterpret_cast<float2*>(to + 8 * kBlock) = make_float2(0.0f, 0.0f);
       } else {
@@ -560,7 +559,7 @@ lora_kernel(const __grid_constant__ Args p) {
   int unit_ahead = unit0 + turn, turn_ahead = 0;
   auto issue = [&](int item) {
     if (item < items) {
-      const uint32_t at = slots + (item & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 8;
+      const uint32_t at = slots + (item % kStages) * (stage_floats(NT) * 4) + lane * 8;
 #pragma unroll
       for (int q = 0; q < KG; ++q) {
         const int k = 16 * (turn_ahead * KG + q) + 4 * t;
@@ -596,11 +595,11 @@ lora_kernel(const __grid_constant__ Args p) {
     const int n0 = u * 32;
     if (vec && n0 + 32 <= rows) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < (kPacked ? 1 : 2); ++h)
         if (token[h] >= 0) load8(p.z, p.y_type, token[h] * p.z_stride + n0 + 8 * t, z + 8 * h);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < (kPacked ? 8 : 16); ++j)
         if (16 * m + j < count && n0 + lane < rows)
           z[j] = load1(p.z, p.y_type, s_tok[16 * m + j] * p.z_stride + n0 + lane);
     }
@@ -618,7 +617,7 @@ lora_kernel(const __grid_constant__ Args p) {
   // of h and 16 tokens, a lane's four values
   {
     const uint32_t base = smem_u32(part);
-    const int quads = wide / 4, tokens = packed ? 8 : mblocks * 16;
+    const int quads = wide / 4, tokens = kPacked ? 8 : mblocks * 16;
     for (int i = tid; i < tokens * quads; i += kThreads) {
       const int j = i / quads, q = i % quads;     // values 4 q .. 4 q + 3 of token j
       float4 v[kCluster];
@@ -641,7 +640,7 @@ lora_kernel(const __grid_constant__ Args p) {
         uint32_t a, b;
         split(4 * q + e < rank ? h[e] * scale : 0.0f, a, b);
         hi[at] = a;
-        (packed ? hi + 1 : lo)[at] = b;
+        (kPacked ? hi + 1 : lo)[at] = b;
       }
     }
   }
@@ -665,7 +664,7 @@ lora_kernel(const __grid_constant__ Args p) {
     for (int q0 = 0; q0 < groups; q0 += KG, ++item) {
       issue(item + kStages - 1);
       copies_but<kStages - 1>();
-      const uint32_t from = slots + (item & (kStages - 1)) * (stage_floats(NT) * 4) + lane * 8;
+      const uint32_t from = slots + (item % kStages) * (stage_floats(NT) * 4) + lane * 8;
       uint2 w[KG][4];
 #pragma unroll
       for (int q = 0; q < KG; ++q)
@@ -681,19 +680,19 @@ lora_kernel(const __grid_constant__ Args p) {
           const uint4 a = *reinterpret_cast<const uint4*>(hi + at);
           const uint32_t fa[4] = {a.x, a.y, a.z, a.w};
           uint4 b = make_uint4(0, 0, 0, 0);
-          if (!packed) b = *reinterpret_cast<const uint4*>(lo + at);
+          if (!kPacked) b = *reinterpret_cast<const uint4*>(lo + at);
           const uint32_t fb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t b0, b1;
             widen<TW>(s ? w[q][i].y : w[q][i].x, b0, b1);
             mma_tf32(acc[i], fa, b0, b1);
-            if (!packed) mma_tf32(acc[i], fb, b0, b1);
+            if (!kPacked) mma_tf32(acc[i], fb, b0, b1);
           }
         }
       }
     }
-    if (packed) {
+    if (kPacked) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[i][0] += acc[i][2];
@@ -702,7 +701,7 @@ lora_kernel(const __grid_constant__ Args p) {
     }
     if (vec && n0 + 32 <= rows) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < (kPacked ? 1 : 2); ++h) {
         if (token[h] < 0) continue;
         float v[8];
 #pragma unroll
@@ -717,12 +716,12 @@ lora_kernel(const __grid_constant__ Args p) {
       // rows of Y at any address: through shared memory, so that a warp stores
       // 32 rows of a token
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < (kPacked ? 1 : 2); ++h)
 #pragma unroll
         for (int e = 0; e < 8; ++e) pitched[(8 * h + g) * kPitch + 8 * t + e] = acc[e >> 1][2 * h + (e & 1)];
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < (kPacked ? 8 : 16); ++j)
         if (16 * m + j < count && n0 + lane < rows)
           store1(p.y, p.y_type, s_tok[16 * m + j] * p.y_stride + n0 + lane,
                  up1(z[j], p.y_type) + pitched[j * kPitch + lane]);
@@ -745,11 +744,11 @@ bool in_pieces(const void* p, int64_t stride, int64_t bytes, int64_t piece) {
   return (uintptr_t)p % piece == 0 && stride * bytes % piece == 0;
 }
 
-template <typename TX, typename TW, int NT>
+template <typename TX, typename TW, int NT, bool kPacked>
 cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
-  const auto kernel = lora_kernel<TX, TW, NT>;
+  const auto kernel = lora_kernel<TX, TW, NT, kPacked>;
   const int top = (int)a.l.max_rank;
-  const int smem = (kHeadInts + part_floats(top) + split_floats(top) + ring_floats(NT) + kPitchFloats) * (int)sizeof(float);
+  const int smem = (kHeadInts + part_floats(top, kPacked) + split_floats(top, kPacked) + ring_floats(NT) + pitch_floats(kPacked)) * (int)sizeof(float);
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -772,7 +771,9 @@ cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
 
 template <typename TX, typename TW>
 cudaError_t launch_for(const Args& a, int64_t tiles, cudaStream_t s) {
-  return a.l.max_rank <= 16 ? launch_as<TX, TW, 2>(a, tiles, s) : launch_as<TX, TW, 4>(a, tiles, s);
+  if (a.tile == kSmallTile)
+    return a.l.max_rank <= 16 ? launch_as<TX, TW, 2, true>(a, tiles, s) : launch_as<TX, TW, 4, true>(a, tiles, s);
+  return a.l.max_rank <= 16 ? launch_as<TX, TW, 2, false>(a, tiles, s) : launch_as<TX, TW, 4, false>(a, tiles, s);
 }
 
 }  // namespace
@@ -805,11 +806,11 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
             in_pieces(nullptr, c.lora.adapters > 1 ? c.lora.b_stride : 0, 2, 8);
   const int64_t tiles = max_tiles(c.ntok, c.lora.adapters);
   // Few tiles: several clusters share the rows of one, each with the whole of h
-  // for itself, up to two thread blocks an SM, and while a block's share of B and
+  // for itself, up to as many thread blocks as run at once, and while a block's share of B and
   // Y is no less than half its share of A and x.
   const int64_t r = std::max<int64_t>(c.lora.max_rank, 1);
   const int64_t most = std::max<int64_t>(1, 2 * c.lora.rows * (r + 4) / std::max<int64_t>(1, c.lora.cols * (r + 2)));
-  a.splits = (int)std::max<int64_t>(1, std::min(most, 304 / (tiles * kCluster)));
+  a.splits = (int)std::max<int64_t>(1, std::min(most, (a.tile == kSmallTile ? 456 : 304) / (tiles * kCluster)));
   if (c.ntok > kInBlock) {
     char* at = static_cast<char*>(c.ws);
     int* ntiles = reinterpret_cast<int*>(at);
