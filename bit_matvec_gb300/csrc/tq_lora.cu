@@ -337,7 +337,8 @@ __device__ __forceinline__ void put8(uint32_t a, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
-constexpr int kStages = 3;       // of weights under way, a warp
+// Stages of weights under way, a warp: 6 KB.
+__host__ __device__ constexpr int stages(int nt) { return 12 / nt; }
 constexpr int kPitch = 33;       // floats of a row of results on their way to rows of Y at any address
 // Shared memory in 4-byte words, for adapters of up to `top` rows of A, NT row blocks at a time: the
 // tile's description, the partial h of this block's columns, the split h, the warps' stages of weights
@@ -347,7 +348,7 @@ __host__ __device__ constexpr int rank16(int top) { return (top + 15) / 16 * 16;
 __host__ __device__ constexpr int part_floats(int top, bool packed) { return (packed ? 16 : kTile) * rank16(top); }
 __host__ __device__ constexpr int split_floats(int top, bool packed) { return (packed ? 16 : 2 * kTile) * rank16(top); }
 __host__ __device__ constexpr int stage_floats(int nt) { return nt * 128; }
-__host__ __device__ constexpr int ring_floats(int nt) { return kWarps * kStages * stage_floats(nt); }
+__host__ __device__ constexpr int ring_floats(int nt) { return kWarps * stages(nt) * stage_floats(nt); }
 __host__ __device__ constexpr int pitch_floats(bool packed) { return kWarps * (packed ? 8 : 16) * kPitch; }
 
 // NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns. kPacked:
@@ -356,7 +357,7 @@ template <typename TX, typename TW, int NT, bool kPacked>
 __global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2)
 lora_kernel(const __grid_constant__ Args p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
-  constexpr int kBlock = 8 * NT, KG = NT / 2;
+  constexpr int kBlock = 8 * NT, KG = NT / 2, kStages = stages(NT);
   extern __shared__ float4 shared4[];
   int* const s_ids = reinterpret_cast<int*>(shared4);                // [kThreads]
   int* const s_tok = s_ids + kThreads;                               // [kTile]
@@ -429,8 +430,8 @@ lora_kernel(const __grid_constant__ Args p) {
   const TW* const A = static_cast<const TW*>(p.l.a) + tile.adapter * p.l.a_stride;
   const int cols = (int)p.l.cols, chunks = (cols + 31) / 32;
   const int chunk0 = (int)((int64_t)chunks * crank / kCluster), chunk1 = (int)((int64_t)chunks * (crank + 1) / kCluster);
-  const TX* const x0 = static_cast<const TX*>(p.x) + token[0] * p.x_stride + 8 * t;
-  const TX* const x1 = static_cast<const TX*>(p.x) + token[1] * p.x_stride + 8 * t;
+  const TX* const x0 = static_cast<const TX*>(p.x) + max(token[0], 0) * p.x_stride;
+  const TX* const x1 = static_cast<const TX*>(p.x) + max(token[1], 0) * p.x_stride;
   // A share is every eighth chunk of 32 columns; a warp has one, or two with 16 rows for each half of
   // the warps: the sums are the same ones either way.
   for (int r0 = 0; r0 < rank; r0 += kBlock) {
@@ -445,39 +446,59 @@ lora_kernel(const __grid_constant__ Args p) {
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = sum[j][e] = 0.0f;
-    const TW* const Ar = A + (r0 + g) * p.l.a_row_stride + 8 * t;
-    auto issue = [&](int i) {
-      if (i < mine) {
-        const int k = (chunk0 + share_of + i * kParts) * 32;
-        const uint32_t at = slots + (i % kStages) * (stage_floats(NT) * 4) + lane * 16;
+    // Where this thread's pieces come from: addresses that step from chunk to
+    // chunk. Columns past the last are behind every chunk but the last one's.
+    constexpr int kStep = kParts * 32;
+    const int k0 = (chunk0 + share_of) * 32 + 8 * t;
+    const TW* from_a = A + (r0 + g) * p.l.a_row_stride + k0;
+    const int64_t block_step = 8 * p.l.a_row_stride;
+    const TX* from_x0 = x0 + k0;
+    const TX* from_x1 = x1 + k0;
+    uint32_t has = 0;               // blocks whose row of this thread there is
+#pragma unroll
+    for (int j = 0; j < NT; ++j) has |= (r0 + 8 * j + g < rank ? 1u : 0u) << j;
+    int ahead = 0, stage_to = 0, stage_from = 0;
+    auto issue = [&]() {
+      if (ahead < mine) {
+        const uint32_t at = slots + stage_to * (stage_floats(NT) * 4) + lane * 16;
+        const bool in = k0 + ahead * kStep < cols;    // (cols is a multiple of 8)
+        const TW* f = from_a;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const bool have = k + 8 * t < cols && r0 + 8 * j + g < rank;    // (cols is a multiple of 8)
-          copy16(at + j * 512, have ? Ar + 8 * j * p.l.a_row_stride + k : A, have);
+          const bool have = in && (has >> j & 1u);
+          copy16(at + j * 512, have ? f : A, have);
+          f += block_step;
         }
+        from_a += kStep;
+        ++ahead;
+        stage_to = stage_to == kStages - 1 ? 0 : stage_to + 1;
       }
       copies_issued();
     };
     auto load_x = [&](int i, Acts<TX> (&v)[2]) {
-      const int k = (chunk0 + share_of + i * kParts) * 32;
-      const bool in = i < mine && k + 8 * t < cols;
-      if (in && token[0] >= 0) v[0].load(x0 + k);
+      const bool in = i < mine && k0 + i * kStep < cols;
+      if (in && token[0] >= 0) v[0].load(from_x0);
       else v[0].clear();
-      if (!kPacked && in && token[1] >= 0) v[1].load(x1 + k);
-      else v[1].clear();
+      if (!kPacked) {
+        if (in && token[1] >= 0) v[1].load(from_x1);
+        else v[1].clear();
+        from_x1 += kStep;
+      }
+      from_x0 += kStep;
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) issue();
     Acts<TX> next[2];
     load_x(0, next);
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-      issue(i + kStages - 1);
+      issue();
       Acts<TX> v[2] = {next[0], next[1]};
       load_x(i + 1, next);
       copies_but<kStages - 1>();
       uint4 w[NT];
-      const uint32_t at = slots + (i % kStages) * (stage_floats(NT) * 4) + lane * 16;
+      const uint32_t at = slots + stage_from * (stage_floats(NT) * 4) + lane * 16;
+      stage_from = stage_from == kStages - 1 ? 0 : stage_from + 1;
 #pragma unroll
       for (int j = 0; j < NT; ++j) w[j] = slot16(at + j * 512);
       __syncwarp();     // the products take a whole warp
@@ -556,59 +577,85 @@ lora_kernel(const __grid_constant__ Args p) {
   const int items = max(0, (unit1 - unit0 - turn + turns - 1) / turns) * turns_b;
   // Column g of block i is row 8 (g / 2) + 2 i + g % 2, so that a thread's results are consecutive rows.
   const int row_of = 8 * (g >> 1) + (g & 1);
-  int unit_ahead = unit0 + turn, turn_ahead = 0;
-  auto issue = [&](int item) {
-    if (item < items) {
-      const uint32_t at = slots + (item % kStages) * (stage_floats(NT) * 4) + lane * 8;
-#pragma unroll
-      for (int q = 0; q < KG; ++q) {
-        const int k = 16 * (turn_ahead * KG + q) + 4 * t;
+  int unit_ahead = unit0 + turn, turn_ahead = 0, ahead = 0, stage_to = 0, stage_from = 0;
+  const int64_t pair_step = 2 * p.l.b_row_stride;
+  const TW* from_b = B + (unit_ahead * 32 + row_of) * p.l.b_row_stride + 4 * t;   // of the unit ahead
+  const bool whole_b = p.b_vec && rank % 4 == 0;     // a thread's four values all there, or none
+  auto issue = [&]() {
+    if (ahead < items) {
+      const uint32_t at = slots + stage_to * (stage_floats(NT) * 4) + lane * 8;
+      const int k0 = 16 * KG * turn_ahead;
+      if (whole_b && unit_ahead * 32 + 32 <= rows) {
+        const TW* f = from_b + k0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int q = 0; q < KG; ++q) {
+            const bool have = k0 + 16 * q + 4 * t < rank;
+            copy8(at + (q * 4 + i) * 256, have ? f + 16 * q : B, have);
+          }
+          f += pair_step;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
           const int n = unit_ahead * 32 + row_of + 2 * i;
-          const bool have = n < rows && k < rank;
-          const TW* const b = have ? B + n * p.l.b_row_stride + k : B;
-          const uint32_t to = at + (q * 4 + i) * 256;
-          if (p.b_vec && (k + 4 <= rank || !have)) {
-            copy8(to, have ? b : reinterpret_cast<const TW*>(p.l.b), have);
-          } else {
+#pragma unroll 1
+          for (int q = 0; q < KG; ++q) {
+            const int k = k0 + 16 * q + 4 * t;
             uint32_t v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              v[e] = have && k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
-            put8(to, make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16));
+              v[e] = n < rows && k + e < rank
+                         ? __ldg(reinterpret_cast<const unsigned short*>(B + n * p.l.b_row_stride + k) + e) : 0u;
+            put8(at + (q * 4 + i) * 256, make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16));
           }
         }
       }
       if (++turn_ahead == turns_b) {
         turn_ahead = 0;
         unit_ahead += turns;
+        from_b += 32 * turns * p.l.b_row_stride;
       }
+      ++ahead;
+      stage_to = stage_to == kStages - 1 ? 0 : stage_to + 1;
     }
     copies_issued();
   };
   const bool vec = p.y_vec && p.z_vec;
+  const int bytes = p.y_type == TQ_F32 ? 4 : 2;
+  const char* from_z[2];
+  char* to_y[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t at = (unit0 + turn) * 32 + 8 * t, j = max(token[h], 0);
+    from_z[h] = static_cast<const char*>(p.z) + (j * p.z_stride + at) * bytes;
+    to_y[h] = static_cast<char*>(p.y) + (j * p.y_stride + at) * bytes;
+  }
   // Z of 16 tokens and 32 rows: the eight rows of this thread's two tokens, or
   // (rows of Y or Z at any address, or the last of them) a row of each of the 16
   auto load_z = [&](int u, uint32_t (&z)[16]) {
-    if (u >= unit1 || !p.z) return;
-    const int n0 = u * 32;
-    if (vec && n0 + 32 <= rows) {
+    if (p.z && u < unit1) {
+      const int n0 = u * 32;
+      if (vec && n0 + 32 <= rows) {
 #pragma unroll
-      for (int h = 0; h < (kPacked ? 1 : 2); ++h)
-        if (token[h] >= 0) load8(p.z, p.y_type, token[h] * p.z_stride + n0 + 8 * t, z + 8 * h);
-    } else {
+        for (int h = 0; h < (kPacked ? 1 : 2); ++h)
+          if (token[h] >= 0) load8(from_z[h], p.y_type, 0, z + 8 * h);
+      } else {
 #pragma unroll
-      for (int j = 0; j < (kPacked ? 8 : 16); ++j)
-        if (16 * m + j < count && n0 + lane < rows)
-          z[j] = load1(p.z, p.y_type, s_tok[16 * m + j] * p.z_stride + n0 + lane);
+        for (int j = 0; j < (kPacked ? 8 : 16); ++j)
+          if (16 * m + j < count && n0 + lane < rows)
+            z[j] = load1(p.z, p.y_type, s_tok[16 * m + j] * p.z_stride + n0 + lane);
+      }
     }
+    from_z[0] += 32 * turns * bytes;
+    if (!kPacked) from_z[1] += 32 * turns * bytes;
   };
   uint32_t z_next[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) z_next[e] = 0;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) issue();
   load_z(unit0 + turn, z_next);
   cluster_arrive();
   cluster_wait();
@@ -647,7 +694,6 @@ lora_kernel(const __grid_constant__ Args p) {
   __syncthreads();
   cluster_arrive();     // this block's part has no reader left when all have arrived
 
-  int item = 0;
 #pragma unroll 1
   for (int u = unit0 + turn; u < unit1; u += turns) {
     const int n0 = u * 32;
@@ -661,10 +707,11 @@ lora_kernel(const __grid_constant__ Args p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 #pragma unroll 1
-    for (int q0 = 0; q0 < groups; q0 += KG, ++item) {
-      issue(item + kStages - 1);
+    for (int q0 = 0; q0 < groups; q0 += KG) {
+      issue();
       copies_but<kStages - 1>();
-      const uint32_t from = slots + (item % kStages) * (stage_floats(NT) * 4) + lane * 8;
+      const uint32_t from = slots + stage_from * (stage_floats(NT) * 4) + lane * 8;
+      stage_from = stage_from == kStages - 1 ? 0 : stage_from + 1;
       uint2 w[KG][4];
 #pragma unroll
       for (int q = 0; q < KG; ++q)
@@ -710,7 +757,7 @@ lora_kernel(const __grid_constant__ Args p) {
                                     : up((uint16_t)(z[8 * h + (e >> 1)] >> (16 * (e & 1))), p.y_type);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += acc[e >> 1][2 * h + (e & 1)];
-        store8(p.y, p.y_type, token[h] * p.y_stride + n0 + 8 * t, v);
+        store8(to_y[h], p.y_type, 0, v);
       }
     } else {
       // rows of Y at any address: through shared memory, so that a warp stores
@@ -727,6 +774,8 @@ lora_kernel(const __grid_constant__ Args p) {
                  up1(z[j], p.y_type) + pitched[j * kPitch + lane]);
       __syncwarp();
     }
+    to_y[0] += 32 * turns * bytes;
+    if (!kPacked) to_y[1] += 32 * turns * bytes;
   }
   copies_but<0>();
   cluster_wait();
