@@ -16,14 +16,14 @@
 // (t, t + 4) that the fragment wants.
 #include <algorithm>
 
-#include "tq_requests.cuh"
+#include "tq_lora.cuh"
 
 namespace tq {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kCluster = kLoraCluster;
 constexpr int kTile = 32;          // tokens of a tile at most: two row blocks of 16
 constexpr int kSmallTile = 8;      // or so many, where adapters have few tokens each
 constexpr int kParts = 8;          // shares of a block's columns, a warp's each, summed apart
@@ -32,27 +32,6 @@ constexpr int kInBlock = 256;      // tokens up to which every block finds its t
 constexpr int kGroupThreads = 1024;
 static_assert(kInBlock == kThreads, "a thread a token");
 
-struct Args {
-  const void* x;
-  const void* z;
-  void* y;
-  const int32_t* ids;
-  tq_lora l;
-  int64_t x_stride, z_stride, y_stride;
-  int y_type;
-  int ntok;
-  int tile;              // tokens of a tile
-  int splits;            // clusters that share the rows of a tile
-  int copy;              // tokens without adapter are copied (Z is not Y)
-  int y_vec, z_vec;      // rows of Y, of Z in 16-byte pieces
-  int b_vec;             // rows of B in 8-byte pieces
-  // more than kInBlock tokens: the tiles, from the grouping kernel
-  const int32_t* order;  // tokens by adapter
-  const int4* tiles;     // adapter, its rank, first of order, tokens
-  const int* ntiles;
-  int* status;
-};
-
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -60,99 +39,10 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x as a tf32 value and the rest of it, rounded to tf32: good to 2^-21. The
-// first part is cut, not rounded, so that it does not overflow; an infinity
-// leaves no rest.
-__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  const float h = __uint_as_float(hi), rest = x == h ? 0.0f : x - h;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
-}
-
-// The two 16-bit values of a word as 32-bit ones.
-template <typename T> __device__ __forceinline__ void widen(uint32_t w, uint32_t& a, uint32_t& b);
-template <> __device__ __forceinline__ void widen<__nv_bfloat16>(uint32_t w, uint32_t& a, uint32_t& b) {
-  a = w << 16;
-  b = w & 0xffff0000u;
-}
-template <> __device__ __forceinline__ void widen<__half>(uint32_t w, uint32_t& a, uint32_t& b) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  a = __float_as_uint(f.x);
-  b = __float_as_uint(f.y);
-}
-
-// Eight activations from p on: 32 or 16 bytes.
-template <typename TX> struct Acts {
-  uint4 v[sizeof(TX) == 4 ? 2 : 1];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (auto& q : v) q = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void load(const TX* p) {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(v) / sizeof(v[0])); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-  }
-  // values 2 s and 2 s + 1
-  __device__ __forceinline__ void pair(int s, uint32_t& a, uint32_t& b) const {
-    if constexpr (sizeof(TX) == 4) {
-      const uint4 q = v[s >> 1];
-      a = s & 1 ? q.z : q.x;
-      b = s & 1 ? q.w : q.y;
-    } else {
-      const uint4 q = v[0];
-      widen<TX>(s == 0 ? q.x : s == 1 ? q.y : s == 2 ? q.z : q.w, a, b);
-    }
-  }
-};
-
-// ---------------------------------------------------------------- Y and Z
-
-__device__ __forceinline__ float up(uint16_t v, int type) {
-  return type == TQ_F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
-}
-__device__ __forceinline__ uint16_t down(float v, int type) {
-  return type == TQ_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-// Eight consecutive values from `at` on, at an address of a multiple of 16 bytes, as they are (w[0..7],
-// or w[0..3]), and back from floats.
-__device__ __forceinline__ void load8(const void* p, int type, int64_t at, uint32_t* w) {
-  const uint4* q = type == TQ_F32 ? reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + at)
-                                  : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-  const uint4 a = q[0];
-  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  if (type == TQ_F32) {
-    const uint4 b = q[1];
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-}
-__device__ __forceinline__ void store8(void* p, int type, int64_t at, const float (&v)[8]) {
-  if (type == TQ_F32) {
-    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    f[0] = make_float4(v[0], v[1], v[2], v[3]);
-    f[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = (uint32_t)down(v[2 * e], type) | (uint32_t)down(v[2 * e + 1], type) << 16;
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint32_t load1(const void* p, int type, int64_t at) {
-  return type == TQ_F32 ? static_cast<const uint32_t*>(p)[at] : (uint32_t)static_cast<const uint16_t*>(p)[at];
-}
-__device__ __forceinline__ float up1(uint32_t w, int type) {
-  return type == TQ_F32 ? __uint_as_float(w) : up((uint16_t)w, type);
-}
-__device__ __forceinline__ void store1(void* p, int type, int64_t at, float v) {
-  if (type == TQ_F32) static_cast<float*>(p)[at] = v;
-  else static_cast<uint16_t*>(p)[at] = down(v, type);
-}
-
 // ---------------------------------------------------------------- tiles
 
 // The adapter that a token uses, -1 for none, and its rank; `bad` if it is out of range.
-__device__ __forceinline__ int effective(const Args& p, int id, int& rank, bool& bad) {
+__device__ __forceinline__ int effective(const LoraArgs& p, int id, int& rank, bool& bad) {
   bad = false;
   rank = 0;
   if (id < 0) return -1;
@@ -172,7 +62,7 @@ struct Tile {
 // Up to kInBlock tokens: tile number `want` of the call, its tokens into tok;
 // count 0 if there are fewer tiles. Tiles are numbered by their first tokens; a
 // token's place among those of its adapter is the number of them before it.
-__device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, int* tok, int* ids, int* red) {
+__device__ __forceinline__ Tile find_tile(const LoraArgs& p, int want, bool report, int* tok, int* ids, int* red) {
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   int id = -2, rank = 0;
   bool bad = false;
@@ -216,7 +106,7 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int want, bool report, 
 // Counters of the adapters (the last one: no adapter) in shared memory. Which of
 // an adapter's tokens come first is left to chance: a token's result depends
 // neither on its place nor on the other tokens of its tile.
-__global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_constant__ Args p, int32_t* order,
+__global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_constant__ LoraArgs p, int32_t* order,
                                                               int4* tiles, int* ntiles) {
   extern __shared__ int2 part[];                       // [32], their sum
   int2& total = part[32];
@@ -249,7 +139,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
   // where each group's tokens and tiles start
   for (int g0 = 0; g0 < groups; g0 += kGroupThreads) {
     const int g = g0 + tid, n = g < groups ? counts[g] : 0;
-    int2 s = make_int2(n, (n + p.tile - 1) / p.tile);
+    const int tile = g == groups - 1 ? p.copy_tile : p.tile, ntile = (n + tile - 1) / tile;
+    int2 s = make_int2(n, ntile);
     for (int d = 1; d < 32; d <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, s.x, d), b = __shfl_up_sync(0xffffffffu, s.y, d);
       if (lane >= d) {
@@ -260,7 +151,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
     if (lane == 31) part[warp] = s;
     __syncthreads();
     const int2 base = total;
-    int2 at = make_int2(base.x + s.x - n, base.y + s.y - (n + p.tile - 1) / p.tile);
+    int2 at = make_int2(base.x + s.x - n, base.y + s.y - ntile);
     int2 sum = make_int2(0, 0);
     for (int w = 0; w < 32; ++w) {
       const int2 q = part[w];
@@ -277,8 +168,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
       counts[g] = at.x;
       const int id = g == groups - 1 ? -1 : g;
       const int rank = id < 0 || n == 0 ? 0 : p.l.rank ? __ldg(p.l.rank + id) : (int)p.l.max_rank;
-      for (int k = 0; k * p.tile < n; ++k)
-        tiles[at.y + k] = make_int4(id, rank, at.x + k * p.tile, min(p.tile, n - k * p.tile));
+      for (int k = 0; k < ntile; ++k)
+        tiles[at.y + k] = make_int4(id, rank, at.x + k * tile, min(tile, n - k * tile));
     }
     __syncthreads();
   }
@@ -290,26 +181,6 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------- the products
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ float4 load_remote(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
 
 // Asynchronous copies of 16 and 8 bytes into this thread's own slots of shared memory: what a thread
 // copies it reads itself, so it waits for nobody. `have`: false gives zeros.
@@ -355,7 +226,7 @@ __host__ __device__ constexpr int pitch_floats(bool packed) { return kWarps * (p
 // small tiles, the two parts of a value as rows g and g + 8 of one product.
 template <typename TX, typename TW, int NT, bool kPacked>
 __global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2)
-lora_kernel(const __grid_constant__ Args p) {
+lora_kernel(const __grid_constant__ LoraArgs p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
   constexpr int kBlock = 8 * NT, KG = NT / 2, kStages = stages(NT);
   extern __shared__ float4 shared4[];
@@ -386,29 +257,7 @@ lora_kernel(const __grid_constant__ Args p) {
   const int unit0 = (int)((int64_t)units * share / shares), unit1 = (int)((int64_t)units * (share + 1) / shares);
 
   if (tile.adapter < 0) {   // Z as it is, to the bit
-    const int begin = unit0 * 32, n = max(0, min(rows, unit1 * 32) - begin);
-    const int bytes = p.y_type == TQ_F32 ? 4 : 2, piece = p.y_vec && p.z_vec ? 16 / bytes : 1;
-    const int pieces = n / piece, left = n - pieces * piece;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int i = tid; i < count * pieces; i += kThreads) {
-      const int j = i / pieces, at = begin + (i - j * pieces) * piece;
-      const int64_t to = s_tok[j] * p.y_stride + at, from = s_tok[j] * p.z_stride + at;
-      if (piece > 1) {
-        reinterpret_cast<uint4*>(static_cast<char*>(p.y) + to * bytes)[0] =
-            p.z ? reinterpret_cast<const uint4*>(static_cast<const char*>(p.z) + from * bytes)[0] : zero;
-      } else if (bytes == 4) {
-        static_cast<uint32_t*>(p.y)[to] = p.z ? static_cast<const uint32_t*>(p.z)[from] : 0u;
-      } else {
-        static_cast<uint16_t*>(p.y)[to] = p.z ? static_cast<const uint16_t*>(p.z)[from] : (uint16_t)0;
-      }
-    }
-    for (int i = tid; i < count * left; i += kThreads) {
-      const int j = i / left, at = begin + pieces * piece + i - j * left;
-      const int64_t to = s_tok[j] * p.y_stride + at, from = s_tok[j] * p.z_stride + at;
-      if (bytes == 4) static_cast<uint32_t*>(p.y)[to] = p.z ? static_cast<const uint32_t*>(p.z)[from] : 0u;
-      else static_cast<uint16_t*>(p.y)[to] = p.z ? static_cast<const uint16_t*>(p.z)[from] : (uint16_t)0;
-    }
+    copy_rows(p, s_tok, count, unit0 * 32, max(0, min(rows, unit1 * 32) - unit0 * 32), kThreads);
     return;
   }
   const float scale = p.l.scale ? __ldg(p.l.scale + tile.adapter) : 1.0f;
@@ -785,8 +634,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tiles of 8 tokens where adapters have no more than that each on average. (A function of the call's
 // sizes alone: so is the order of every sum.)
 int64_t tile_of(int64_t ntok, int64_t adapters) { return ntok <= kSmallTile * adapters ? kSmallTile : kTile; }
-int64_t max_tiles(int64_t ntok, int64_t adapters) {
-  return std::min(ntok, ntok / tile_of(ntok, adapters) + std::min(adapters, ntok) + 1);
+int64_t max_tiles(int64_t ntok, int64_t adapters, int64_t tile) {
+  return std::min(ntok, ntok / tile + std::min(adapters, ntok) + 1);
 }
 
 bool in_pieces(const void* p, int64_t stride, int64_t bytes, int64_t piece) {
@@ -794,7 +643,7 @@ bool in_pieces(const void* p, int64_t stride, int64_t bytes, int64_t piece) {
 }
 
 template <typename TX, typename TW, int NT, bool kPacked>
-cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_as(const LoraArgs& a, int64_t tiles, cudaStream_t s) {
   const auto kernel = lora_kernel<TX, TW, NT, kPacked>;
   const int top = (int)a.l.max_rank;
   const int smem = (kHeadInts + part_floats(top, kPacked) + split_floats(top, kPacked) + ring_floats(NT) + pitch_floats(kPacked)) * (int)sizeof(float);
@@ -819,7 +668,7 @@ cudaError_t launch_as(const Args& a, int64_t tiles, cudaStream_t s) {
 }
 
 template <typename TX, typename TW>
-cudaError_t launch_for(const Args& a, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_for(const LoraArgs& a, int64_t tiles, cudaStream_t s) {
   if (a.tile == kSmallTile)
     return a.l.max_rank <= 16 ? launch_as<TX, TW, 2, true>(a, tiles, s) : launch_as<TX, TW, 4, true>(a, tiles, s);
   return a.l.max_rank <= 16 ? launch_as<TX, TW, 2, false>(a, tiles, s) : launch_as<TX, TW, 4, false>(a, tiles, s);
@@ -830,11 +679,11 @@ cudaError_t launch_for(const Args& a, int64_t tiles, cudaStream_t s) {
 // The order of the tokens, the tiles and their number.
 int64_t lora_workspace_bytes(int64_t ntok, int64_t adapters) {
   if (ntok <= kInBlock) return 0;
-  return 16 + max_tiles(ntok, adapters) * 16 + ceil_div(ntok, 4) * 16;
+  return 16 + max_tiles(ntok, adapters, tile_of(ntok, adapters)) * 16 + ceil_div(ntok, 4) * 16;
 }
 
 cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
-  Args a = {};
+  LoraArgs a = {};
   a.x = c.x;
   a.z = c.z;
   a.y = c.y;
@@ -846,20 +695,23 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
   a.y_type = c.y_type;
   a.ntok = (int)c.ntok;
   a.copy = c.z != c.y;
-  a.tile = (int)tile_of(c.ntok, c.lora.adapters);
   a.status = c.status;
   const int64_t yb = c.y_type == TQ_F32 ? 4 : 2;
   a.y_vec = in_pieces(c.y, c.ntok > 1 ? c.y_stride : 0, yb, 16);
   a.z_vec = in_pieces(c.z, c.ntok > 1 ? c.z_stride : 0, yb, 16);
   a.b_vec = in_pieces(c.lora.b, c.lora.rows > 1 ? c.lora.b_row_stride : 0, 2, 8) &&
             in_pieces(nullptr, c.lora.adapters > 1 ? c.lora.b_stride : 0, 2, 8);
-  const int64_t tiles = max_tiles(c.ntok, c.lora.adapters);
+  const bool large = lora_large_fits(a, c.ntok);
+  a.tile = large ? kLargeTile : (int)tile_of(c.ntok, c.lora.adapters);
+  // (tokens without adapter are copied, 32 to a tile, which is quick)
+  a.copy_tile = (int)std::min<int64_t>(a.tile, kTile);
+  const int64_t tiles = max_tiles(c.ntok, c.lora.adapters, a.copy ? a.copy_tile : a.tile);
   // Few tiles: several clusters share the rows of one, each with the whole of h
   // for itself, up to as many thread blocks as run at once, and while a block's share of B and
   // Y is no less than half its share of A and x.
-  const int64_t r = std::max<int64_t>(c.lora.max_rank, 1);
+  const int64_t r = std::max<int64_t>(c.lora.max_rank, 1), blocks = a.tile == kSmallTile ? 456 : 304;
   const int64_t most = std::max<int64_t>(1, 2 * c.lora.rows * (r + 4) / std::max<int64_t>(1, c.lora.cols * (r + 2)));
-  a.splits = (int)std::max<int64_t>(1, std::min(most, (a.tile == kSmallTile ? 456 : 304) / (tiles * kCluster)));
+  a.splits = (int)std::max<int64_t>(1, std::min(most, blocks / (tiles * kCluster)));
   if (c.ntok > kInBlock) {
     char* at = static_cast<char*>(c.ws);
     int* ntiles = reinterpret_cast<int*>(at);
@@ -874,6 +726,7 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
     a.tiles = list;
     a.ntiles = ntiles;
   }
+  if (large) return launch_lora_large(a, tiles, c.x_type, s);
   if (c.lora.type == TQ_F16)
     return c.x_type == TQ_F32 ? launch_for<float, __half>(a, tiles, s) : launch_for<__half, __half>(a, tiles, s);
   return c.x_type == TQ_F32 ? launch_for<float, __nv_bfloat16>(a, tiles, s)

@@ -1,0 +1,524 @@
+// tq_lora_large.cu -- low-rank adapters for many tokens each: tiles of 128 tokens on the 5th-generation
+// tensor cores.
+//
+// A cluster of four thread blocks takes a tile: each block a quarter of A's columns for h = A x, the four
+// parts summed through distributed shared memory, then each block a quarter of the rows of Y = Z + B h.
+// With 128 tokens a tile, A and B are read from L2 a quarter as often as with the 32 of tq_lora.cu, and a
+// quarter of the blocks' time goes to them; what is left for the threads is the traffic itself: x in, Z in, Y
+// out. (Clusters of eight: 273 us where four take 183; the GPU holds 15 of them with a block an SM, and 36
+// of four.)
+//
+// Taken for ranks above 32, at least 4096 tokens and 512 an adapter. Matrices of 5120 x 15360, f32, one to
+// sixteen adapters, us, this kernel and that of tq_lora.cu: rank 64, 4096 tokens of four 185 and 277; 8192 of
+// sixteen 360 and 522; 2048 of one 178 and 149; 4096 of sixteen 296 and 278. Rank 32: 163 and 172 at 4096,
+// and ranks of several sizes up to 32 395 and 327. Rank 16: 149 both.
+//
+// Products are tcgen05 kind::tf32 with 128 tokens as rows of A, operands in shared memory without a
+// swizzle: 16-byte columns (four values of the contraction index), 128 rows of each one after another,
+// columns 16 bytes further apart than that, so that threads that write neighbouring columns meet no bank
+// twice. x and h are the sum of two tf32 parts, multiplied one after the other into the same accumulator.
+// The first product's columns go to eight accumulators one after the other, which are added in 32 bits: the
+// tensor cores cut their sums, which leans one way over many steps.
+//
+// A warp takes its 32 tokens' sums of 32 rows from tensor memory, a token a lane, and turns them through
+// shared memory into rows of 128 bytes of four tokens at a time, as it has loaded them of Z a tile ahead and
+// stores them to Y. (With a token a lane to the end every load and store met 32 lines of the cache.)
+//
+// What bounds it: at 4096 tokens, 5120 columns, 15360 rows, rank 64, f32, 183 us or 3.2 TB/s. The 36 clusters
+// leave eight SMs out; the first product takes a sixth of the time, and the second's tile of 128 x 128 about
+// 8,700 cycles, of which memory would take 5,300: the eight warps' own loads, turns and stores take turns.
+// (Sixteen warps: 229 us, with the registers of a thread halved.)
+#include <algorithm>
+
+#include "tq_lora.cuh"
+#include "tq_ring.cuh"
+#include "tq_tcgen05.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = 256;              // eight warps that load, convert and store,
+constexpr int kAll = kThreads + 32;        // and one that issues the products
+constexpr int kM = kLargeTile;
+constexpr int kCluster = 4;                // thread blocks that share a tile
+constexpr int N = 64;                      // values of h a token: the largest rank
+constexpr int kLeastRank = 33, kLeastTokens = 4096, kLeastTokensEach = 512;
+constexpr int kStages = 3;                 // of 32 columns of x and A in shared memory
+constexpr int kRows = 128;                 // rows of Y of a tile of the second product
+constexpr int kColumn = kM * 16 + 16;      // bytes of a 16-byte column of 128 rows
+constexpr int kAhead = 4;                  // chunks of 32 columns of x and A under way
+constexpr int kAccs = 8;                   // accumulators of the first product: 64 columns of TMEM each
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+constexpr int kXStage = 2 * 8 * kColumn;                   // both parts of 32 columns of x
+constexpr int kWStage = 8 * (N * 16 + 16);             // 32 columns of A
+constexpr int kHBytes = 2 * (N / 4) * kColumn;         // both parts of h
+constexpr int kBBytes = (N / 4) * kColumn;             // 128 rows of B
+constexpr int kHead = 1024;
+constexpr int kUnion = std::max(kStages * (kXStage + kWStage), kHBytes + 2 * kBBytes);
+constexpr int kPartPitch = N + 4;                      // floats
+constexpr int kTurnPitch = 36;                             // floats of a token's 32 sums on their way to rows
+constexpr int kTurn = kThreads * kTurnPitch * 4;
+constexpr int kPart = std::max(kM * kPartPitch * 4, kTurn);    // (the parts of h make room for them)
+constexpr int kSlice = kM / kCluster * kPartPitch * 4;
+constexpr int kSmem = kHead + kUnion + kPart + kSlice;
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+
+// kind::tf32: D f32, A and B tf32 (format 2), both K-major.
+__device__ __forceinline__ uint32_t idesc_tf32(int m, int n) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_tf32_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void put16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void split4(const uint4& v, uint4& hi, uint4& lo) {
+  split(__uint_as_float(v.x), hi.x, lo.x);
+  split(__uint_as_float(v.y), hi.y, lo.y);
+  split(__uint_as_float(v.z), hi.z, lo.z);
+  split(__uint_as_float(v.w), hi.w, lo.w);
+}
+
+template <typename TX, typename TW>
+__global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_constant__ LoraArgs p) {
+  constexpr bool kSplit = sizeof(TX) == 4;
+  constexpr int kXPieces = kSplit ? 4 : 2;          // 16-byte pieces of a chunk of x a thread
+  constexpr int kWColumn = N * 16 + 16;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  int* const s_tok = reinterpret_cast<int*>(smem);                    // [kM]
+  // stages filled and read of the first product; B's buffers filled, and products done, of the second
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + 512);     // [kStages]
+  uint64_t* const read = full + kStages;                              // [kStages]
+  uint64_t* const b_full = read + kStages;                            // [2]
+  uint64_t* const done = b_full + 2;                                  // [2]
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 640);
+  const uint32_t base = smem_u32(smem + kHead);
+  float* const part = reinterpret_cast<float*>(smem + kHead + kUnion);
+  float* const slice = reinterpret_cast<float*>(smem + kHead + kUnion + kPart);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t crank = cluster_rank();
+  const int want = blockIdx.x / kCluster;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (want >= *p.ntiles) return;
+  const int4 tile = p.tiles[want];        // adapter, rank, first of order, tokens
+  const int count = tile.w, rank = tile.y;
+  if (tid < count) s_tok[tid] = p.order[tile.z + tid];
+  // rows of B and Y of this thread block, from a multiple of 32 on
+  const int rows = (int)p.l.rows, units = (rows + 31) / 32, share = (int)crank;
+  const int begin = (int)((int64_t)units * share / kCluster) * 32;
+  const int end = min(rows, (int)((int64_t)units * (share + 1) / kCluster) * 32);
+  if (tile.x < 0) {
+    __syncthreads();
+    copy_rows(p, s_tok, count, begin, max(0, end - begin), kAll);
+    return;
+  }
+  const bool issuer = warp == kThreads / 32;
+  if (issuer) {
+    tc::tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
+    tc::tmem_relinquish<1>();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbarrier_init(smem_u32(full + i), kThreads / 32);
+      mbarrier_init(smem_u32(read + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbarrier_init(smem_u32(b_full + i), kThreads / 32);
+      mbarrier_init(smem_u32(done + i), 1);
+    }
+    mbarrier_init_fence();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool failed = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!failed && !mbarrier_wait_bounded(smem_u32(bar), parity, kWaitLimitNs)) failed = true;
+  };
+  // what this warp's threads have stored to shared memory, for the tensor cores
+  auto hand_over = [&](uint64_t* bar) {
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbarrier_arrive(smem_u32(bar));
+  };
+
+  // ---- h = A x over this block's columns, 32 at a time
+  const int cols = (int)p.l.cols, chunks = (cols + 31) / 32;
+  const int chunk0 = (int)((int64_t)chunks * crank / kCluster), chunk1 = (int)((int64_t)chunks * (crank + 1) / kCluster);
+  const int nk = chunk1 - chunk0;
+  const int tiles = max(0, (end - begin + kRows - 1) / kRows);
+  const uint32_t hs = base, bs = base + kHBytes;
+  constexpr int kQuads = N / 4;
+  if (issuer) {
+    // ---- the products, by one thread
+    if (lane == 0) {
+      const uint32_t idesc1 = idesc_tf32(kM, N), idesc2 = idesc_tf32(kM, kRows);
+      for (int k = 0, stage = 0, phase = 0; k < nk; ++k) {
+        wait(full + stage, phase);
+        tc::tc_fence_after();
+        const uint32_t xs = base + stage * (kXStage + kWStage), ws = xs + kXStage;
+        const int acc = k * kAccs / max(nk, kAccs);
+        const uint32_t d = tmem + acc * N;
+        const bool fresh = k == 0 || (k - 1) * kAccs / max(nk, kAccs) != acc;
+        if (!failed) {
+#pragma unroll
+          for (int h = 0; h < (kSplit ? 2 : 1); ++h)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_tf32_ss(d, tc::smem_desc(xs + (8 * h + 2 * kk) * kColumn, kColumn, 128),
+                          tc::smem_desc(ws + 2 * kk * kWColumn, kWColumn, 128), idesc1,
+                          fresh && h == 0 && kk == 0 ? 0u : 1u);
+        }
+        tc::mma_commit(smem_u32(read + stage));     // (also on failure: it keeps the others' phases moving)
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    if (lane == 0) {
+      const uint32_t idesc2 = idesc_tf32(kM, kRows);
+      for (int i = 0; i < tiles; ++i) {
+        wait(b_full + (i & 1), (i >> 1) & 1);
+        tc::tc_fence_after();
+        const uint32_t d = tmem + (i & 1) * kRows, b = bs + (i & 1) * kBBytes;
+        if (!failed) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int kk = 0; kk < N / 8; ++kk)
+              mma_tf32_ss(d, tc::smem_desc(hs + (h * kQuads + 2 * kk) * kColumn, kColumn, 128),
+                          tc::smem_desc(b + 2 * kk * kColumn, kColumn, 128), idesc2, h == 0 && kk == 0 ? 0u : 1u);
+        }
+        tc::mma_commit(smem_u32(done + (i & 1)));
+      }
+    }
+    __syncwarp();
+  } else {
+  // x: a row's pieces of 16 bytes are neighbouring lanes'; A: a row a quad
+  constexpr int kLanes = kSplit ? 8 : 4, kRowsAtOnce = 32 / kLanes;
+  const int xc = lane % kLanes, xr = warp * 16 + lane / kLanes;
+  const int wr = tid >> 2, wt = tid & 3;
+  const TX* from_x[kXPieces];
+#pragma unroll
+  for (int i = 0; i < kXPieces; ++i) {
+    const int row = xr + i * kRowsAtOnce;
+    from_x[i] = row < count ? static_cast<const TX*>(p.x) + s_tok[row] * p.x_stride + chunk0 * 32 + xc * (16 / (int)sizeof(TX))
+                            : nullptr;
+  }
+  const TW* const from_w = static_cast<const TW*>(p.l.a) + tile.x * p.l.a_stride + wr * p.l.a_row_stride + chunk0 * 32 + 8 * wt;
+  uint4 xv[kAhead][kXPieces], wv[kAhead];
+  auto load = [&](int k, uint4 (&x)[kXPieces], uint4& w) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int at = (chunk0 + k) * 32;
+#pragma unroll
+    for (int i = 0; i < kXPieces; ++i)
+      x[i] = k < nk && from_x[i] && at + xc * (16 / (int)sizeof(TX)) < cols
+                 ? ldg_stream_v4(from_x[i] + k * 32) : zero;
+    w = k < nk && wr < rank && at + 8 * wt < cols ? __ldg(reinterpret_cast<const uint4*>(from_w + k * 32)) : zero;
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, xv[u], wv[u]);
+  int stage = 0;
+  uint32_t phase = 1;           // of the last reading of a stage: none yet
+#pragma unroll 1
+  for (int k0 = 0; k0 < nk; k0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= nk) break;
+      const uint32_t xs = base + stage * (kXStage + kWStage), ws = xs + kXStage;
+      if (k >= kStages) wait(read + stage, phase);
+#pragma unroll
+      for (int i = 0; i < kXPieces; ++i) {
+        const uint32_t at = xs + (xr + i * kRowsAtOnce) * 16;
+        if constexpr (kSplit) {
+          uint4 hi, lo;
+          split4(xv[u][i], hi, lo);
+          put16(at + xc * kColumn, hi);
+          put16(at + (8 + xc) * kColumn, lo);
+        } else {
+          const uint4 v = xv[u][i];
+          uint4 a, b;
+          widen<TX>(v.x, a.x, a.y);
+          widen<TX>(v.y, a.z, a.w);
+          widen<TX>(v.z, b.x, b.y);
+          widen<TX>(v.w, b.z, b.w);
+          put16(at + 2 * xc * kColumn, a);
+          put16(at + (2 * xc + 1) * kColumn, b);
+        }
+      }
+      if (wr < N) {
+        const uint4 v = wv[u];
+        uint4 a, b;
+        widen<TW>(v.x, a.x, a.y);
+        widen<TW>(v.y, a.z, a.w);
+        widen<TW>(v.z, b.x, b.y);
+        widen<TW>(v.w, b.z, b.w);
+        put16(ws + 2 * wt * kWColumn + wr * 16, a);
+        put16(ws + (2 * wt + 1) * kWColumn + wr * 16, b);
+      }
+      load(k + kAhead, xv[u], wv[u]);
+      hand_over(full + stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+
+  // ---- what the second product starts with, on its way from here on
+  constexpr int kRowStep = kThreads / kQuads, kBPieces = kRows / kRowStep;
+  const int bq = tid % kQuads, br = tid / kQuads;
+  const TW* const B = static_cast<const TW*>(p.l.b) + tile.x * p.l.b_stride;
+  uint2 bv[kBPieces];
+  auto load_b = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < kBPieces; ++i) {
+      const int n = n0 + br + i * kRowStep, k = 4 * bq;
+      const TW* const b = B + n * p.l.b_row_stride + k;
+      bv[i] = make_uint2(0, 0);
+      if (n < end && k + 4 <= rank) {
+        bv[i] = __ldg(reinterpret_cast<const uint2*>(b));
+      } else if (n < end && k < rank) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
+        bv[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      }
+    }
+  };
+  // A warp's tokens and half of a tile's rows of Y. Pieces of 16 bytes: of 32 rows a token has 8 (or 4, of
+  // 16-bit types), neighbouring lanes'; a lane's pieces are of every fourth (eighth) token.
+  const int first = (warp & 3) * 32, half = warp >> 2, row = first + lane;
+  const bool f32 = p.y_type == TQ_F32;
+  const int bytes = f32 ? 4 : 2, in_row = f32 ? lane & 7 : lane & 3, of_token = f32 ? lane >> 3 : lane >> 2;
+  const int step = f32 ? 4 : 8, turns = f32 ? 8 : 4, values = 16 / bytes;
+  int64_t at_z[8], at_y[8];        // bytes from Z and Y to the pieces' first row; -1: no such token
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int j = first + of_token + i * step;
+    const bool have = i < turns && j < count;
+    const int64_t token = have ? s_tok[j] : 0, n = begin + half * 64 + in_row * values;
+    at_z[i] = have ? (token * p.z_stride + n) * bytes : -1;
+    at_y[i] = have ? (token * p.y_stride + n) * bytes : -1;
+  }
+  const char* const Z = static_cast<const char*>(p.z);
+  char* const Y = static_cast<char*>(p.y);
+  uint4 zv[2][8];
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) zv[g][i] = make_uint4(0, 0, 0, 0);
+  // of 32 rows: g of the two of this warp's half, in the tile that starts `ahead` rows from begin
+  auto load_z = [&](int ahead, int g, uint4 (&z)[8]) {
+    if (!Z || begin + ahead + half * 64 + g * 32 + in_row * values >= end) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at_z[i] >= 0) z[i] = *reinterpret_cast<const uint4*>(Z + at_z[i] + (ahead + g * 32) * bytes);
+  };
+  load_b(begin);
+  load_z(0, 0, zv[0]);
+  load_z(0, 1, zv[1]);
+
+  // ---- this block's part of h
+  // the last products are done, and with them those before
+  if (nk > 0) wait(read + (nk - 1) % kStages, ((nk - 1) / kStages) & 1);
+  failed = __any_sync(0xffffffffu, failed);        // (tcgen05.ld takes a whole warp)
+  tc::tc_fence_after();
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  for (int g = half; g < N / 16; g += 2) {
+    float sum[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
+    if (!failed)
+#pragma unroll 1
+      for (int a = 0; a < min(nk, kAccs); ++a) {
+        uint32_t v[16];
+        tc::tmem_ld16_nowait(tmem + lanes + a * N + g * 16, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
+      }
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+      *reinterpret_cast<float4*>(part + row * kPartPitch + g * 16 + e) =
+          make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+  }
+  tc::tc_fence_before();
+  // ---- of the whole: a quarter of the tokens summed by each block, then all of them taken
+  cluster_arrive();
+  cluster_wait();
+  const float scale = p.l.scale ? __ldg(p.l.scale + tile.x) : 1.0f;
+  for (int i = tid; i < kM / kCluster * kQuads; i += kThreads) {
+    const int j = i / kQuads, q = i % kQuads;
+    const uint32_t from = smem_u32(part + ((int)crank * (kM / kCluster) + j) * kPartPitch + 4 * q);
+    float4 v[kCluster];
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) v[c] = load_remote(from, c);
+    float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      h.x += v[c].x;
+      h.y += v[c].y;
+      h.z += v[c].z;
+      h.w += v[c].w;
+    }
+    *reinterpret_cast<float4*>(slice + j * kPartPitch + 4 * q) =
+        make_float4(h.x * scale, h.y * scale, h.z * scale, h.w * scale);
+  }
+  cluster_arrive();
+  cluster_wait();
+#pragma unroll 4
+  for (int i = tid; i < kM * kQuads; i += kThreads) {
+    const int j = i % kM, q = i / kM;
+    const float4 v = load_remote(smem_u32(slice + (j % (kM / kCluster)) * kPartPitch + 4 * q), j / (kM / kCluster));
+    // (past the rank an infinite activation has left a NaN)
+    const uint4 w = make_uint4(4 * q < rank ? __float_as_uint(v.x) : 0u, 4 * q + 1 < rank ? __float_as_uint(v.y) : 0u,
+                               4 * q + 2 < rank ? __float_as_uint(v.z) : 0u, 4 * q + 3 < rank ? __float_as_uint(v.w) : 0u);
+    uint4 hi, lo;
+    split4(w, hi, lo);
+    put16(hs + q * kColumn + j * 16, hi);
+    put16(hs + (kQuads + q) * kColumn + j * 16, lo);
+  }
+  cluster_arrive();       // this block's slice has no reader left when all have arrived
+
+  // ---- Y = Z + B h, 128 rows at a time: the products of a tile run while the one before is stored
+  auto put_b = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kBPieces; ++i) {
+      uint4 v;
+      widen<TW>(bv[i].x, v.x, v.y);
+      widen<TW>(bv[i].y, v.z, v.w);
+      put16(bs + buf * kBBytes + bq * kColumn + (br + i * kRowStep) * 16, v);
+    }
+  };
+  // all of h is in place before any of the products (a warp's share of it is handed over with its B)
+  named_barrier_sync(1, kThreads);
+  if (tiles > 0) {
+    put_b(0);
+    hand_over(b_full);
+    load_b(begin + kRows);
+  }
+#pragma unroll 1
+  for (int i = 0; i < tiles; ++i) {
+    if (i + 1 < tiles) {
+      put_b((i + 1) & 1);
+      tc::tc_fence_before();       // (the accumulator of two tiles ago is read)
+      hand_over(b_full + ((i + 1) & 1));
+      load_b(begin + (i + 2) * kRows);
+    }
+    wait(done + (i & 1), (i >> 1) & 1);
+    failed = __any_sync(0xffffffffu, failed);
+    tc::tc_fence_after();
+    float* const turn = part + warp * 32 * kTurnPitch;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t acc[32];
+      if (!failed) tc::tmem_ld32(tmem + lanes + (i & 1) * kRows + half * 64 + g * 32, acc);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<uint4*>(turn + lane * kTurnPitch + e) = make_uint4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      __syncwarp();
+      const int ahead = i * kRows;
+      if (!failed && begin + ahead + half * 64 + g * 32 + in_row * values < end) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (at_y[u] < 0) continue;
+          const float* const from = turn + (of_token + u * step) * kTurnPitch + in_row * values;
+          const float4 a = *reinterpret_cast<const float4*>(from);
+          const uint4 z = zv[g][u];
+          uint4* const to = reinterpret_cast<uint4*>(Y + at_y[u] + (ahead + g * 32) * bytes);
+          if (f32) {
+            *to = make_uint4(__float_as_uint(a.x + __uint_as_float(z.x)), __float_as_uint(a.y + __uint_as_float(z.y)),
+                             __float_as_uint(a.z + __uint_as_float(z.z)), __float_as_uint(a.w + __uint_as_float(z.w)));
+          } else {
+            const float4 b = *reinterpret_cast<const float4*>(from + 4);
+            auto sum = [&](float x, float y, uint32_t w) {
+              return (uint32_t)down(x + up((uint16_t)w, p.y_type), p.y_type) |
+                     (uint32_t)down(y + up((uint16_t)(w >> 16), p.y_type), p.y_type) << 16;
+            };
+            *to = make_uint4(sum(a.x, a.y, z.x), sum(a.z, a.w, z.y), sum(b.x, b.y, z.z), sum(b.z, b.w, z.w));
+          }
+        }
+      }
+      __syncwarp();
+      load_z(ahead + kRows, g, zv[g]);
+    }
+  }
+  }
+  // A wait that ran out: products that were issued still write tensor memory, so each last phase is waited
+  // for once more.
+  if (failed) {
+    atomicExch(p.status, kDevTimeout);
+    for (int i = 0; i < kStages; ++i) {
+      const int last = last_phase(nk, i, kStages);
+      if (last >= 0) mbarrier_wait_bounded(smem_u32(read + i), (uint32_t)last, kWaitLimitNs);
+    }
+    for (int i = 0; i < 2; ++i) {
+      const int last = last_phase(tiles, i, 2);
+      if (last >= 0) mbarrier_wait_bounded(smem_u32(done + i), (uint32_t)last, kWaitLimitNs);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (issuer) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc<1>(tmem, kTmemCols);
+  }
+  cluster_wait();
+}
+
+template <typename TX, typename TW> cudaError_t launch_as(const LoraArgs& a, int64_t tiles, cudaStream_t s) {
+  const auto kernel = lora_large_kernel<TX, TW>;
+  cudaError_t e = ensure_dynamic_smem((const void*)kernel, kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = tiles * kCluster;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kAll);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+bool lora_large_fits(const LoraArgs& a, int64_t ntok) {
+  return a.l.max_rank >= kLeastRank && a.l.max_rank <= N && ntok >= kLeastTokens &&
+         ntok >= kLeastTokensEach * a.l.adapters && a.l.rows % 8 == 0 && a.y_vec && a.z_vec && a.b_vec;
+}
+
+cudaError_t launch_lora_large(const LoraArgs& a, int64_t tiles, int x_type, cudaStream_t s) {
+  if (a.l.type == TQ_F16)
+    return x_type == TQ_F32 ? launch_as<float, __half>(a, tiles, s) : launch_as<__half, __half>(a, tiles, s);
+  return x_type == TQ_F32 ? launch_as<float, __nv_bfloat16>(a, tiles, s)
+                          : launch_as<__nv_bfloat16, __nv_bfloat16>(a, tiles, s);
+}
+
+}  // namespace tq

@@ -66,12 +66,13 @@ def check(d, got, z=True):
     want, mag, part = reference(d, z)
     got64 = got.double()
     assert torch.isfinite(got64).all()
-    # Rounding Y to its type: half a step. Products: 2^-21 of each (three operations of it, doubled
+    # Rounding Y to its type: half a step, which is the same for all values below the least normal one
+    # (f16: 2^-25 below 2^-14). Products: 2^-21 of each (three operations of it, doubled
     # for their second order). Sums in 32 bits: at most cols / 16 + rank + 32 additions one after
     # another, each off by 2^-24 of a partial sum, which the sum of the magnitudes bounds.
     cols, top = d["a"].shape[2], d["a"].shape[1]
     step = torch.finfo(got.dtype).eps / 2
-    bound = want.abs() * step + mag * (2.0**-19 + (cols / 16 + top + 32) * 2.0**-24) + 1e-30
+    bound = want.abs().clamp(min=torch.finfo(got.dtype).tiny) * step + mag * (2.0**-19 + (cols / 16 + top + 32) * 2.0**-24) + 1e-30
     worst = ((got64 - want).abs() / bound).max().item()
     assert worst <= 1.0, worst
     # The same errors as independent ones: rms of a product 2^-21, of a sum of n steps sqrt(n) 2^-24
@@ -109,14 +110,73 @@ def test_against_64_bits(tq, shape, types):
     check(d, run(tq, d))
 
 
-@pytest.mark.parametrize("ntok", [1, 16, 40, 300])
+# many tokens an adapter. From 4096 tokens, 512 an adapter and rank 33 to 64 on, tiles of 128, their last ones
+# short; rows that are a multiple of 8 (others go the way of few tokens), fewer columns than thread blocks share
+MANY = [(600, 640, 512, 2, 64), (513, 96, 8, 3, 5), (900, 17408, 256, 2, 48),
+        (4096, 256, 136, 1, 64), (4100, 640, 512, 8, 33), (5000, 264, 40, 5, 48), (4096, 96, 8, 3, 64),
+        (4200, 1288, 2048, 4, 40), (4097, 17408, 72, 2, 64), (6000, 8, 1032, 2, 64), (4500, 520, 777, 2, 50),
+        (4096, 256, 136, 9, 64), (4096, 256, 136, 4, 65)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=str)
+@pytest.mark.parametrize("types", [(F32, BF16, F32), (F32, F16, F32), (BF16, BF16, BF16), (F16, F16, F32),
+                                   (F32, BF16, F16)], ids=str)
+def test_many_tokens_of_few_adapters(tq, shape, types):
+    ntok, cols, rows, adapters, top = shape
+    xt, wt, yt = types
+    d = make(ntok, cols, rows, adapters, top, xt, wt, yt, seed=ntok + rows)
+    got = run(tq, d)
+    check(d, got)
+    lora, ws = tq.Lora(d["a"], d["b"], d["rank"], d["scale"]), scratch(tq, ntok, adapters)
+    y = d["z"].clone()
+    tq.tq_lora_add(d["x"], lora, d["ids"], y, y, ws)
+    assert torch.equal(y, got)
+    none = torch.full_like(y, float("nan"))
+    tq.tq_lora_add(d["x"], lora, d["ids"], none, workspace=ws)
+    check(d, none, z=False)
+
+
+def test_many_tokens_order_and_strides(tq):
+    """Tokens in another order, and rows of wider tensors, give the same bits."""
+    d = make(4500, 520, 264, 6, 40, seed=50)
+    want = run(tq, d)
+    p = torch.randperm(4500, generator=torch.Generator().manual_seed(1)).cuda()
+    e = dict(d, x=d["x"][p].contiguous(), z=d["z"][p].contiguous(), ids=d["ids"][p].contiguous())
+    assert torch.equal(run(tq, e), want[p])
+    wide = torch.full((4500, 1000), float("nan"), device="cuda")
+    x, y, z = wide[:, 4:524], wide[:, 528:792], torch.full((4500, 272), float("nan"), device="cuda")[:, 4:268]
+    x.copy_(d["x"])
+    z.copy_(d["z"])
+    before = wide.clone()
+    tq.tq_lora_add(x, tq.Lora(d["a"], d["b"], d["rank"], d["scale"]), d["ids"], y, z, scratch(tq, 4500, 6))
+    assert torch.equal(y, want)
+    left = torch.ones_like(wide, dtype=torch.bool)
+    left[:, 528:792] = False
+    assert torch.equal(wide.view(I32)[left], before.view(I32)[left])
+
+
+def test_many_tokens_not_finite_and_bad(tq):
+    d = make(4300, 256, 64, 2, 48, seed=51, bare=0.0, ragged=False)
+    clean = run(tq, d)
+    d["x"][3, 5], d["x"][4200, 9] = float("inf"), float("nan")
+    got = run(tq, d)
+    touched = torch.zeros(4300, dtype=torch.bool, device="cuda")
+    touched[[3, 4200]] = True
+    assert torch.equal(got[~touched], clean[~touched]) and not torch.isfinite(got[touched]).any()
+    d["ids"][::3] = 9
+    got = run(tq, d)
+    assert tq.tq_device_status() == tq.TQ_ERR_INDEX
+    assert torch.equal(got[::3], d["z"][::3])
+
+
+@pytest.mark.parametrize("ntok", [1, 16, 40, 300, 700, 5000])
 def test_exact_on_small_integers(tq, ntok):
     """Sums of integers below 2^24 have no rounding in any order: the result is equal to the bit."""
     g = torch.Generator().manual_seed(ntok)
 
     def ints(hi, *shape):
         return torch.randint(-hi, hi + 1, shape, generator=g).float()
-    for top, cols, rows in ((5, 72, 31), (16, 512, 300), (64, 1024, 130)):
+    for top, cols, rows in ((5, 72, 31), (16, 512, 300), (64, 1024, 136)):
         d = {"a": ints(2, 3, top, cols).bfloat16().cuda(), "b": ints(2, 3, rows, top).bfloat16().cuda(),
              "x": ints(3, ntok, cols).cuda(), "z": ints(100, ntok, rows).cuda(),
              "ids": torch.randint(-1, 3, (ntok,), generator=g, dtype=I32).cuda(),
