@@ -183,12 +183,12 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
 // ---------------------------------------------------------------- the products
 
 // Asynchronous copies of 16 and 8 bytes into this thread's own slots of shared memory: what a thread
-// copies it reads itself, so it waits for nobody. `have`: false gives zeros.
+// copies it reads itself, so it waits for nobody. `have`: false gives zeros; `bytes`: zeros behind them.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(have ? 8 : 0) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_but() {
@@ -241,8 +241,9 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
 
   Tile tile;
   if (p.tiles) {
-    if (want >= *p.ntiles) return;
-    const int4 q = p.tiles[want];
+    const int n = *p.ntiles;
+    const int4 q = p.tiles[want];       // (what is there behind the last one is not used)
+    if (want >= n) return;
     tile = {q.x, q.y, q.w};
     if (tid < q.w) s_tok[tid] = p.order[q.z + tid];
     __syncthreads();
@@ -441,12 +442,24 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
 #pragma unroll
           for (int q = 0; q < KG; ++q) {
             const bool have = k0 + 16 * q + 4 * t < rank;
+            copy8(at + (q * 4 + i) * 256, have ? f + 16 * q : B, have ? 8 : 0);
+          }
+          f += pair_step;
+        }
+      } else if (p.b_vec) {
+        const TW* f = from_b + k0;
+        const int rows_left = rows - unit_ahead * 32 - row_of, left = rank - k0 - 4 * t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int q = 0; q < KG; ++q) {
+            const int have = 2 * i < rows_left ? min(8, max(0, 2 * left - 32 * q)) : 0;
             copy8(at + (q * 4 + i) * 256, have ? f + 16 * q : B, have);
           }
           f += pair_step;
         }
       } else {
-#pragma unroll 1
+#pragma unroll 2
         for (int i = 0; i < 4; ++i) {
           const int n = unit_ahead * 32 + row_of + 2 * i;
 #pragma unroll 1
@@ -491,10 +504,21 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
         for (int h = 0; h < (kPacked ? 1 : 2); ++h)
           if (token[h] >= 0) load8(from_z[h], p.y_type, 0, z + 8 * h);
       } else {
+        const int have = n0 + lane < rows ? count - 16 * m : 0;
 #pragma unroll
-        for (int j = 0; j < (kPacked ? 8 : 16); ++j)
-          if (16 * m + j < count && n0 + lane < rows)
-            z[j] = load1(p.z, p.y_type, s_tok[16 * m + j] * p.z_stride + n0 + lane);
+        for (int j0 = 0; j0 < (kPacked ? 8 : 16); j0 += 4) {
+          const int4 q = *reinterpret_cast<const int4*>(s_tok + 16 * m + j0);
+          const int tok[4] = {q.x, q.y, q.z, q.w};
+          if (p.y_type == TQ_F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j0 + e < have) z[j0 + e] = (static_cast<const uint32_t*>(p.z) + n0 + lane)[tok[e] * p.z_stride];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j0 + e < have) z[j0 + e] = (static_cast<const uint16_t*>(p.z) + n0 + lane)[tok[e] * p.z_stride];
+          }
+        }
       }
     }
     from_z[0] += 32 * turns * bytes;
@@ -616,11 +640,28 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) pitched[(8 * h + g) * kPitch + 8 * t + e] = acc[e >> 1][2 * h + (e & 1)];
       __syncwarp();
+      // (four tokens at a time, no branch between them: 170 cycles each otherwise)
+      const int have = n0 + lane < rows ? count - 16 * m : 0;
 #pragma unroll
-      for (int j = 0; j < (kPacked ? 8 : 16); ++j)
-        if (16 * m + j < count && n0 + lane < rows)
-          store1(p.y, p.y_type, s_tok[16 * m + j] * p.y_stride + n0 + lane,
-                 up1(z[j], p.y_type) + pitched[j * kPitch + lane]);
+      for (int j0 = 0; j0 < (kPacked ? 8 : 16); j0 += 4) {
+        const int4 q = *reinterpret_cast<const int4*>(s_tok + 16 * m + j0);
+        const int tok[4] = {q.x, q.y, q.z, q.w};
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = up1(z[j0 + e], p.y_type) + pitched[(j0 + e) * kPitch + lane];
+        if (p.y_type == TQ_F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j0 + e < have) (static_cast<float*>(p.y) + n0 + lane)[tok[e] * p.y_stride] = v[e];
+        } else {
+          uint16_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = down(v[e], p.y_type);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j0 + e < have) (static_cast<uint16_t*>(p.y) + n0 + lane)[tok[e] * p.y_stride] = w[e];
+        }
+      }
       __syncwarp();
     }
     to_y[0] += 32 * turns * bytes;

@@ -110,15 +110,8 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t at, const floa
   for (int e = 0; e < 4; ++e) w[e] = (uint32_t)down(v[2 * e], type) | (uint32_t)down(v[2 * e + 1], type) << 16;
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint32_t load1(const void* p, int type, int64_t at) {
-  return type == TQ_F32 ? static_cast<const uint32_t*>(p)[at] : (uint32_t)static_cast<const uint16_t*>(p)[at];
-}
 __device__ __forceinline__ float up1(uint32_t w, int type) {
   return type == TQ_F32 ? __uint_as_float(w) : up((uint16_t)w, type);
-}
-__device__ __forceinline__ void store1(void* p, int type, int64_t at, float v) {
-  if (type == TQ_F32) static_cast<float*>(p)[at] = v;
-  else static_cast<uint16_t*>(p)[at] = down(v, type);
 }
 
 // The rows of Z of tokens without adapter as they are, to the bit: rows begin .. begin + n - 1 of `count`

@@ -108,8 +108,9 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   const int want = blockIdx.x / kCluster;
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (want >= *p.ntiles) return;
+  const int ntiles = *p.ntiles;
   const int4 tile = p.tiles[want];        // adapter, rank, first of order, tokens
+  if (want >= ntiles) return;
   const int count = tile.w, rank = tile.y;
   if (tid < count) s_tok[tid] = p.order[tile.z + tid];
   // rows of B and Y of this thread block, from a multiple of 32 on
