@@ -14,6 +14,19 @@
 // parts whose sum is good to 2^-21. The order of the contraction index is free,
 // so a thread loads consecutive values of a row and feeds them as the pairs
 // (t, t + 4) that the fragment wants.
+//
+// Tiles are of 8 tokens where adapters have no more than that each on average: both parts of a value
+// are rows of one product then. (Tiles of 32 for 256 tokens of 100 adapters, rank 64, 17408 x 5120: 102 us
+// where those of 8 take 69.) Long batches of high rank have a kernel of their own, in
+// tq_lora_large.cu. A warp's weights come through a ring of asynchronous copies that only it reads, 6 KB
+// under way, so the products wait for no barrier; two thread blocks an SM, 96 KB.
+//
+// What bounds it: one token, 5120 x 5120, rank 16: 8 us of latency (one launch, the token's adapter, A, the
+// cluster's sum, B, one after the other). 256 tokens of 100 adapters, ranks 16 to 64: 197 MB in 69 us or
+// 2.8 TB/s: some 740 thread blocks of which 304 run at once, each with the same wait for its tile, its first
+// weights and the cluster. 8192
+// tokens of 16 adapters, ranks up to 32, 5120 x 17408: 1.3 GB in 327 us or 4 TB/s; conversions and products
+// of the x and Z that pass take as long as the memory does.
 #include <algorithm>
 
 #include "tq_lora.cuh"
@@ -225,9 +238,12 @@ __host__ __device__ constexpr int pitch_floats(bool packed) { return kWarps * (p
 // NT: row blocks of 8 of A that a warp takes at a time; ranks above 8 NT take several turns. kPacked:
 // small tiles, the two parts of a value as rows g and g + 8 of one product.
 template <typename TX, typename TW, int NT, bool kPacked>
-__global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 lora_kernel(const __grid_constant__ LoraArgs p) {
   constexpr bool kSplit = sizeof(TX) == 4;    // 16-bit activations are exact in tf32
+  // Chunks of x under way: with one, each chunk waited for the next one's activations. (Small tiles, 256
+  // tokens of 100 adapters: 97 us; two 85; three and two thread blocks an SM instead of three 69; six 80.)
+  constexpr int kAheadX = kPacked ? 3 : 1;
   constexpr int kBlock = 8 * NT, KG = NT / 2, kStages = stages(NT);
   extern __shared__ float4 shared4[];
   int* const s_ids = reinterpret_cast<int*>(shared4);                // [kThreads]
@@ -338,13 +354,18 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
     };
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue();
-    Acts<TX> next[2];
-    load_x(0, next);
+    Acts<TX> next[kAheadX][2];
+#pragma unroll
+    for (int i = 0; i < kAheadX; ++i) load_x(i, next[i]);
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
       issue();
-      Acts<TX> v[2] = {next[0], next[1]};
-      load_x(i + 1, next);
+      Acts<TX> v[2] = {next[0][0], next[0][1]};
+#pragma unroll
+      for (int u = 0; u + 1 < kAheadX; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) next[u][h] = next[u + 1][h];
+      load_x(i + kAheadX, next[kAheadX - 1]);
       copies_but<kStages - 1>();
       uint4 w[NT];
       const uint32_t at = slots + stage_from * (stage_floats(NT) * 4) + lane * 16;
@@ -750,9 +771,9 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
   // Few tiles: several clusters share the rows of one, each with the whole of h
   // for itself, up to as many thread blocks as run at once, and while a block's share of B and
   // Y is no less than half its share of A and x.
-  const int64_t r = std::max<int64_t>(c.lora.max_rank, 1), blocks = a.tile == kSmallTile ? 456 : 304;
+  const int64_t r = std::max<int64_t>(c.lora.max_rank, 1);
   const int64_t most = std::max<int64_t>(1, 2 * c.lora.rows * (r + 4) / std::max<int64_t>(1, c.lora.cols * (r + 2)));
-  a.splits = (int)std::max<int64_t>(1, std::min(most, blocks / (tiles * kCluster)));
+  a.splits = (int)std::max<int64_t>(1, std::min(most, 304 / (tiles * kCluster)));
   if (c.ntok > kInBlock) {
     char* at = static_cast<char*>(c.ws);
     int* ntiles = reinterpret_cast<int*>(at);
