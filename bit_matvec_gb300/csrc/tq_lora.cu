@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
   __syncthreads();
   pdl_wait_primary();
   pdl_launch_dependents();
-  auto group_of = [&](int i, bool report) {
+  auto group_of = [&](int64_t i, bool report) {
     bool bad;
     int rank;
     const int id = effective(p, p.ids[i], rank, bad);
@@ -146,13 +146,13 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
     if (lane == leader && g >= 0) at = atomicAdd(&counts[g], __popc(same));
     return __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
   };
-  const int whole = (p.ntok + 31) & ~31;
-  for (int i = tid; i < whole; i += kGroupThreads) take(i < p.ntok ? group_of(i, true) : -1);
+  const int64_t whole = ((int64_t)p.ntok + 31) / 32 * 32;
+  for (int64_t i = tid; i < whole; i += kGroupThreads) take(i < p.ntok ? group_of(i, true) : -1);
   __syncthreads();
   // where each group's tokens and tiles start
   for (int g0 = 0; g0 < groups; g0 += kGroupThreads) {
     const int g = g0 + tid, n = g < groups ? counts[g] : 0;
-    const int tile = g == groups - 1 ? p.copy_tile : p.tile, ntile = (n + tile - 1) / tile;
+    const int tile = g == groups - 1 ? p.copy_tile : p.tile, ntile = n / tile + (n % tile != 0);
     int2 s = make_int2(n, ntile);
     for (int d = 1; d < 32; d <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, s.x, d), b = __shfl_up_sync(0xffffffffu, s.y, d);
@@ -187,9 +187,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const __grid_const
     __syncthreads();
   }
   if (tid == 0) *ntiles = total.y;
-  for (int i = tid; i < whole; i += kGroupThreads) {
+  for (int64_t i = tid; i < whole; i += kGroupThreads) {
     const int g = i < p.ntok ? group_of(i, false) : -1, at = take(g);
-    if (g >= 0) order[at] = i;
+    if (g >= 0) order[at] = (int)i;
   }
 }
 
