@@ -973,8 +973,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   pdl_launch_dependents();
 
   const float temp = a.temperature ? a.temperature[row] : 1.0f;
-  const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
+  const int k = mp > 1.0f ? 1 : a.top_k ? a.top_k[row] : 0;     // (no weight is above 1: one token, the first)
   const float t = fminf(temp, 0x1p100f);
   const bool by_count = k > 0 && k < a.vocab, by_weight = p < 1.0f;
   const int from = rank * a.slice, count = max(0, min(a.slice, a.vocab - from));

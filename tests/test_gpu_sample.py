@@ -133,6 +133,18 @@ def test_equal_logits(tq, vocab):
     check(tq, x, [0.9] * 6, t=[0.0] * 6)
 
 
+@pytest.mark.parametrize("vocab", [1, 40, 3000, 70000])
+def test_min_p_above_one(tq, vocab):
+    """No weight is that large: one token is kept, the first of the order, also of equal largest ones."""
+    g = torch.Generator().manual_seed(vocab)
+    l = torch.randint(0, 5, (6, vocab), generator=g).float().cuda()
+    l[5] = INF
+    m = [1.0000001, 1.5, INF, 2.0, 1.0, 3.0]
+    check(tq, l, [0.0, 0.5, 0.99, 0.7, 0.9, 0.6], [1.0, 0.5, 2.0, 1.0, 1.0, 1.0], m=m)
+    check(tq, l, [0.0, 0.5, 0.99, 0.7, 0.9, 0.6], [1.0, 0.5, 2.0, 1.0, 1.0, 1.0], [3, 0, 9, 2, 5, 1],
+          [0.5, 0.9, 1.0, 0.3, 0.8, 0.5], m)
+
+
 def test_masked(tq):
     """Minus infinity and the type's lowest value are never drawn beside others, whatever u is."""
     for dtype in (F32, F16, BF16):
