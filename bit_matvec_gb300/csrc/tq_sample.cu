@@ -21,6 +21,7 @@
 // in which threads add.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "tq_requests.cuh"
 #include "tq_weight.cuh"
@@ -127,6 +128,17 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
+}
+
+// The larger ones of two pairs of 16-bit values, NaN if one of the two is; a pair of minus infinities.
+template <typename T> __device__ __forceinline__ uint32_t max_of_pairs(uint32_t a, uint32_t b) {
+  uint32_t m;
+  if (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+template <typename T> __device__ __forceinline__ uint32_t none_of_pairs() {
+  return std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 }
 
 // floor(a * x) of a weight sum and a float in (0, 1), exactly; `up`: the ceiling.
@@ -996,13 +1008,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   {
     const uint4* const from16 = reinterpret_cast<const uint4*>(x - pad);
     const int first = pad ? 1 : 0, last = end / kPiece;        // whole pieces
+    uint32_t pairs = none_of_pairs<T>();                       // 16-bit types: two maxima in one operation
 #pragma unroll 4
     for (int i = first + tid; i < last; i += kThreads) {
       const uint4 q = ldg_stream_v4(from16 + i);
       if (kResident) reinterpret_cast<uint4*>(room)[i] = q;
-      const Vec<T, kPiece> v = *reinterpret_cast<const Vec<T, kPiece>*>(&q);
-#pragma unroll
-      for (int e = 0; e < kPiece; ++e) top = max_or_nan(top, Elem<T>::up(v.v[e]));
+      if constexpr (sizeof(T) == 2) {
+        pairs = max_of_pairs<T>(pairs, max_of_pairs<T>(max_of_pairs<T>(q.x, q.y), max_of_pairs<T>(q.z, q.w)));
+      } else {
+        top = max_or_nan(max_or_nan(top, max_or_nan(__uint_as_float(q.x), __uint_as_float(q.y))),
+                         max_or_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+      }
+    }
+    if constexpr (sizeof(T) == 2) {
+      const Vec<T, 2> v = *reinterpret_cast<const Vec<T, 2>*>(&pairs);
+      top = max_or_nan(Elem<T>::up(v.v[0]), Elem<T>::up(v.v[1]));
     }
     // the ends: before the first whole piece, behind the last one
     const int head = min(end, first * kPiece), tail = max(head, last * kPiece);
