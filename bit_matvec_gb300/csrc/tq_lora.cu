@@ -203,6 +203,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have)
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_but() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -467,7 +470,7 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
           }
           f += pair_step;
         }
-      } else if (p.b_vec) {
+      } else if (p.b_pairs) {
         const TW* f = from_b + k0;
         const int rows_left = rows - unit_ahead * 32 - row_of, left = rank - k0 - 4 * t;
 #pragma unroll
@@ -475,24 +478,33 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
 #pragma unroll
           for (int q = 0; q < KG; ++q) {
             const int have = 2 * i < rows_left ? min(8, max(0, 2 * left - 32 * q)) : 0;
-            copy8(at + (q * 4 + i) * 256, have ? f + 16 * q : B, have);
+            const uint32_t to = at + (q * 4 + i) * 256;
+            const TW* const from = have ? f + 16 * q : B;
+            if (p.b_vec) {
+              copy8(to, from, have);
+            } else {
+              copy4(to, from, min(have, 4));
+              copy4(to + 4, have > 4 ? from + 2 : B, max(have - 4, 0));
+            }
           }
           f += pair_step;
         }
       } else {
-#pragma unroll 2
-        for (int i = 0; i < 4; ++i) {
-          const int n = unit_ahead * 32 + row_of + 2 * i;
 #pragma unroll 1
-          for (int q = 0; q < KG; ++q) {
-            const int k = k0 + 16 * q + 4 * t;
-            uint32_t v[4];
+        for (int q = 0; q < KG; ++q) {
+          const int k = k0 + 16 * q + 4 * t;
+          uint32_t v[4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = n < rows && k + e < rank
-                         ? __ldg(reinterpret_cast<const unsigned short*>(B + n * p.l.b_row_stride + k) + e) : 0u;
-            put8(at + (q * 4 + i) * 256, make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16));
-          }
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int n = unit_ahead * 32 + row_of + 2 * i;
+              v[i][e] = n < rows && k + e < rank
+                            ? __ldg(reinterpret_cast<const unsigned short*>(B + n * p.l.b_row_stride + k) + e) : 0u;
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            put8(at + (q * 4 + i) * 256, make_uint2(v[i][0] | v[i][1] << 16, v[i][2] | v[i][3] << 16));
         }
       }
       if (++turn_ahead == turns_b) {
@@ -763,6 +775,8 @@ cudaError_t launch_lora_add(const LoraCall& c, cudaStream_t s) {
   a.z_vec = in_pieces(c.z, c.ntok > 1 ? c.z_stride : 0, yb, 16);
   a.b_vec = in_pieces(c.lora.b, c.lora.rows > 1 ? c.lora.b_row_stride : 0, 2, 8) &&
             in_pieces(nullptr, c.lora.adapters > 1 ? c.lora.b_stride : 0, 2, 8);
+  a.b_pairs = in_pieces(c.lora.b, c.lora.rows > 1 ? c.lora.b_row_stride : 0, 2, 4) &&
+              in_pieces(nullptr, c.lora.adapters > 1 ? c.lora.b_stride : 0, 2, 4);
   const bool large = lora_large_fits(a, c.ntok);
   a.tile = large ? kLargeTile : (int)tile_of(c.ntok, c.lora.adapters);
   // (tokens without adapter are copied, 32 to a tile, which is quick)

@@ -24,7 +24,7 @@ struct LoraArgs {
   int splits;            // clusters that share the rows of a tile
   int copy;              // tokens without adapter are copied (Z is not Y)
   int y_vec, z_vec;      // rows of Y, of Z in 16-byte pieces
-  int b_vec;             // rows of B in 8-byte pieces
+  int b_vec, b_pairs;    // rows of B in 8-byte pieces, in 4-byte pieces
   // more than kInBlock tokens: the tiles, from the grouping kernel
   const int32_t* order;  // tokens by adapter
   const int4* tiles;     // adapter, its rank, first of order, tokens
