@@ -22,6 +22,7 @@ struct LoraArgs {
   int tile;              // tokens of a tile,
   int copy_tile;         // and of one that is only copied
   int splits;            // clusters that share the rows of a tile
+  int rank_from;         // (the kernel for many tokens) ranks below are done
   int copy;              // tokens without adapter are copied (Z is not Y)
   int y_vec, z_vec;      // rows of Y, of Z in 16-byte pieces
   int b_vec, b_pairs;    // rows of B in 8-byte pieces, in 4-byte pieces

@@ -8,10 +8,16 @@
 // out. (Clusters of eight: 273 us where four take 183; the GPU holds 15 of them with a block an SM, and 36
 // of four.)
 //
-// Taken for ranks above 32, at least 4096 tokens and 512 an adapter. Matrices of 5120 x 15360, f32, one to
-// sixteen adapters, us, this kernel and that of tq_lora.cu: rank 64, 4096 tokens of four 185 and 277; 8192 of
-// sixteen 360 and 522; 2048 of one 178 and 149; 4096 of sixteen 296 and 278. Rank 32: 163 and 172 at 4096,
-// and ranks of several sizes up to 32 395 and 327. Rank 16: 149 both.
+// Ranks above 64 take several passes of 64 over Y, of 32-bit values: a pass adds to what the one before
+// has stored, which is the same 32-bit sum. (16-bit Y would be rounded twice: such calls take tq_lora.cu.)
+//
+// Taken for ranks above 32, at least 4096 tokens and 512 an adapter; from 2048 tokens on above rank 112, where
+// tq_lora.cu has room for one thread block an SM. us, this kernel and that of tq_lora.cu, f32: matrices of
+// 5120 x 15360, rank 64, 4096 tokens of four adapters 185 and 277, of sixteen 296 and 278; 8192 of sixteen 360
+// and 522; 2048 of one 178 and 149; rank 32, 4096 tokens 163 and 172, ranks of several sizes up to 32 395 and
+// 327; rank 16 149 both. Matrices of 5120 x 5120, 4096 tokens: rank 45 119 and 206, 100 180 and 287, 128 178
+// and 421, 256 339 and 759; 2048 tokens: rank 64 83 and 91, 100 152 and 151, 128 152 and 236; 1024 tokens,
+// rank 128: 143 and 139.
 //
 // Products are tcgen05 kind::tf32 with 128 tokens as rows of A, operands in shared memory without a
 // swizzle: 16-byte columns (four values of the contraction index), 128 rows of each one after another,
@@ -41,8 +47,9 @@ constexpr int kThreads = 256;              // eight warps that load, convert and
 constexpr int kAll = kThreads + 32;        // and one that issues the products
 constexpr int kM = kLargeTile;
 constexpr int kCluster = 4;                // thread blocks that share a tile
-constexpr int N = 64;                      // values of h a token: the largest rank
+constexpr int N = 64;                      // values of h a token; larger ranks take several passes
 constexpr int kLeastRank = 33, kLeastTokens = 4096, kLeastTokensEach = 512;
+constexpr int kHighRank = 113, kLeastTokensHigh = 2048;
 constexpr int kStages = 3;                 // of 32 columns of x and A in shared memory
 constexpr int kRows = 128;                 // rows of Y of a tile of the second product
 constexpr int kColumn = kM * 16 + 16;      // bytes of a 16-byte column of 128 rows
@@ -111,7 +118,8 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   const int ntiles = *p.ntiles;
   const int4 tile = p.tiles[want];        // adapter, rank, first of order, tokens
   if (want >= ntiles) return;
-  const int count = tile.w, rank = tile.y;
+  const int count = tile.w, rank = min(N, max(0, tile.y - p.rank_from));
+  if (p.rank_from > 0 && rank == 0) return;
   if (tid < count) s_tok[tid] = p.order[tile.z + tid];
   // rows of B and Y of this thread block, from a multiple of 32 on
   const int rows = (int)p.l.rows, units = (rows + 31) / 32, share = (int)crank;
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
     from_x[i] = row < count ? static_cast<const TX*>(p.x) + s_tok[row] * p.x_stride + chunk0 * 32 + xc * (16 / (int)sizeof(TX))
                             : nullptr;
   }
-  const TW* const from_w = static_cast<const TW*>(p.l.a) + tile.x * p.l.a_stride + wr * p.l.a_row_stride + chunk0 * 32 + 8 * wt;
+  const TW* const from_w = static_cast<const TW*>(p.l.a) + tile.x * p.l.a_stride + (p.rank_from + wr) * p.l.a_row_stride + chunk0 * 32 + 8 * wt;
   uint4 xv[kAhead][kXPieces], wv[kAhead];
   auto load = [&](int k, uint4 (&x)[kXPieces], uint4& w) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   // ---- what the second product starts with, on its way from here on
   constexpr int kRowStep = kThreads / kQuads, kBPieces = kRows / kRowStep;
   const int bq = tid % kQuads, br = tid / kQuads;
-  const TW* const B = static_cast<const TW*>(p.l.b) + tile.x * p.l.b_stride;
+  const TW* const B = static_cast<const TW*>(p.l.b) + tile.x * p.l.b_stride + p.rank_from;
   uint2 bv[kBPieces];
   auto load_b = [&](int n0) {
 #pragma unroll
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
       const int n = n0 + br + i * kRowStep, k = 4 * bq;
       const TW* const b = B + n * p.l.b_row_stride + k;
       bv[i] = make_uint2(0, 0);
-      if (n < end && k + 4 <= rank) {
+      if (n < end && p.b_vec && k + 4 <= rank) {
         bv[i] = __ldg(reinterpret_cast<const uint2*>(b));
       } else if (n < end && k < rank) {
         uint32_t v[4];
@@ -511,15 +519,24 @@ template <typename TX, typename TW> cudaError_t launch_as(const LoraArgs& a, int
 }  // namespace
 
 bool lora_large_fits(const LoraArgs& a, int64_t ntok) {
-  return a.l.max_rank >= kLeastRank && a.l.max_rank <= N && ntok >= kLeastTokens &&
-         ntok >= kLeastTokensEach * a.l.adapters && a.l.rows % 8 == 0 && a.y_vec && a.z_vec && a.b_vec;
+  return a.l.max_rank >= kLeastRank && (a.l.max_rank <= N || a.y_type == TQ_F32) && ntok >= (a.l.max_rank >= kHighRank ? kLeastTokensHigh : kLeastTokens) &&
+         ntok >= kLeastTokensEach * a.l.adapters && a.l.rows % (a.y_type == TQ_F32 ? 4 : 8) == 0 && a.y_vec && a.z_vec;
 }
 
-cudaError_t launch_lora_large(const LoraArgs& a, int64_t tiles, int x_type, cudaStream_t s) {
-  if (a.l.type == TQ_F16)
-    return x_type == TQ_F32 ? launch_as<float, __half>(a, tiles, s) : launch_as<__half, __half>(a, tiles, s);
-  return x_type == TQ_F32 ? launch_as<float, __nv_bfloat16>(a, tiles, s)
-                          : launch_as<__nv_bfloat16, __nv_bfloat16>(a, tiles, s);
+cudaError_t launch_lora_large(const LoraArgs& call, int64_t tiles, int x_type, cudaStream_t s) {
+  LoraArgs a = call;
+  cudaError_t e = cudaSuccess;
+  for (; a.rank_from < std::max<int64_t>(1, a.l.max_rank) && e == cudaSuccess; a.rank_from += N) {
+    if (a.l.type == TQ_F16)
+      e = x_type == TQ_F32 ? launch_as<float, __half>(a, tiles, s) : launch_as<__half, __half>(a, tiles, s);
+    else
+      e = x_type == TQ_F32 ? launch_as<float, __nv_bfloat16>(a, tiles, s)
+                           : launch_as<__nv_bfloat16, __nv_bfloat16>(a, tiles, s);
+    // the next 64 ranks, on top of these (sums of 32-bit values, as within a pass)
+    a.z = a.y;
+    a.z_stride = a.y_stride;
+  }
+  return e;
 }
 
 }  // namespace tq

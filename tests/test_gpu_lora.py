@@ -110,12 +110,14 @@ def test_against_64_bits(tq, shape, types):
     check(d, run(tq, d))
 
 
-# many tokens an adapter. From 4096 tokens, 512 an adapter and rank 33 to 64 on, tiles of 128, their last ones
-# short; rows that are a multiple of 8 (others go the way of few tokens), fewer columns than thread blocks share
+# many tokens an adapter. From 4096 tokens (2048 above rank 112), 512 an adapter and rank 33 on, tiles of 128,
+# their last ones short, in passes of 64 ranks; rows in 16-byte pieces (others go the way of few tokens), and
+# fewer columns than thread blocks share
 MANY = [(600, 640, 512, 2, 64), (513, 96, 8, 3, 5), (900, 17408, 256, 2, 48),
         (4096, 256, 136, 1, 64), (4100, 640, 512, 8, 33), (5000, 264, 40, 5, 48), (4096, 96, 8, 3, 64),
         (4200, 1288, 2048, 4, 40), (4097, 17408, 72, 2, 64), (6000, 8, 1032, 2, 64), (4500, 520, 777, 2, 50),
-        (4096, 256, 136, 9, 64), (4096, 256, 136, 4, 65)]
+        (4096, 256, 136, 9, 64), (4096, 256, 136, 4, 65), (4200, 520, 264, 3, 130), (4100, 1032, 520, 2, 200),
+        (4300, 264, 128, 1, 51), (4100, 264, 132, 1, 40), (2048, 136, 264, 4, 113), (2060, 136, 264, 1, 112)]
 
 
 @pytest.mark.parametrize("shape", MANY, ids=str)
