@@ -33,7 +33,7 @@
 // What bounds it: at 4096 tokens, 5120 columns, 15360 rows, rank 64, f32, 183 us or 3.2 TB/s. The 36 clusters
 // leave eight SMs out; the first product takes a sixth of the time, and the second's tile of 128 x 128 about
 // 8,700 cycles, of which memory would take 5,300: the eight warps' own loads, turns and stores take turns.
-// (Sixteen warps: 229 us, with the registers of a thread halved.)
+// (Sixteen warps: 229 us, with 96 registers a thread for 168.)
 #include <algorithm>
 
 #include "tq_lora.cuh"
@@ -297,20 +297,26 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   const int bq = tid % kQuads, br = tid / kQuads;
   const TW* const B = static_cast<const TW*>(p.l.b) + tile.x * p.l.b_stride + p.rank_from;
   uint2 bv[kBPieces];
+  const bool whole_b = p.b_vec && rank % 4 == 0;      // a thread's four values all there, or none
   auto load_b = [&](int n0) {
+    const int k = 4 * bq;
+    if (whole_b) {
+#pragma unroll
+      for (int i = 0; i < kBPieces; ++i) {
+        const int n = n0 + br + i * kRowStep;
+        bv[i] = n < end && k < rank ? __ldg(reinterpret_cast<const uint2*>(B + n * p.l.b_row_stride + k)) : make_uint2(0, 0);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kBPieces; ++i) {
-      const int n = n0 + br + i * kRowStep, k = 4 * bq;
-      const TW* const b = B + n * p.l.b_row_stride + k;
-      bv[i] = make_uint2(0, 0);
-      if (n < end && p.b_vec && k + 4 <= rank) {
-        bv[i] = __ldg(reinterpret_cast<const uint2*>(b));
-      } else if (n < end && k < rank) {
-        uint32_t v[4];
+      const int n = n0 + br + i * kRowStep;
+      uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = k + e < rank ? __ldg(reinterpret_cast<const unsigned short*>(b) + e) : 0u;
-        bv[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-      }
+      for (int e = 0; e < 4; ++e)
+        v[e] = n < end && k + e < rank
+                   ? __ldg(reinterpret_cast<const unsigned short*>(B + n * p.l.b_row_stride + k) + e) : 0u;
+      bv[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
     }
   };
   // A warp's tokens and half of a tile's rows of Y. Pieces of 16 bytes: of 32 rows a token has 8 (or 4, of

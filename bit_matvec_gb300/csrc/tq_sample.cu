@@ -19,6 +19,13 @@
 //
 // Weights are integers (tq_weight.cuh): their sums do not depend on the order
 // in which threads add.
+//
+// What bounds it: the weights' instructions, 36 a token for a row without filters. 256 rows of 262144
+// take 113 us (2.4 TB/s, 2.4 instructions a cycle), 512 rows of 32768 with filters of their own 63, 64 of
+// 131072 50, where top-p weighs the tokens twice and a row waits for its slowest block. Top-k alone weighs
+// only the list: 200 rows of 128001 f16 58 us, in two rounds of thread blocks that each read their slice,
+// wait, read it again and wait. One row of 131072 takes 15 us: five meetings of its sixteen blocks, a sort
+// and the code's way into the caches.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
