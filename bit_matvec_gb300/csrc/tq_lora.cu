@@ -22,11 +22,10 @@
 // under way, so the products wait for no barrier; two thread blocks an SM, 96 KB.
 //
 // What bounds it: one token, 5120 x 5120, rank 16: 8 us of latency (one launch, the token's adapter, A, the
-// cluster's sum, B, one after the other). 256 tokens of 100 adapters, ranks 16 to 64: 197 MB in 69 us or
+// cluster's sum, B, one after the other). 256 tokens of 100 adapters, ranks 16 to 64: 190 MB in 69 us or
 // 2.8 TB/s: some 740 thread blocks of which 304 run at once, each with the same wait for its tile, its first
-// weights and the cluster. 8192
-// tokens of 16 adapters, ranks up to 32, 5120 x 17408: 1.3 GB in 327 us or 4 TB/s; conversions and products
-// of the x and Z that pass take as long as the memory does.
+// weights and the cluster. 8192 tokens of 16 adapters, ranks up to 32, 5120 x 17408: 1.3 GB in 327 us or
+// 4 TB/s at 1.5 instructions a cycle, conversions and products of the x and Z that pass.
 #include <algorithm>
 
 #include "tq_lora.cuh"
@@ -36,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = kLoraCluster;
+constexpr int kCluster = 8;        // thread blocks that share a tile
 constexpr int kTile = 32;          // tokens of a tile at most: two row blocks of 16
 constexpr int kSmallTile = 8;      // or so many, where adapters have few tokens each
 constexpr int kParts = 8;          // shares of a block's columns, a warp's each, summed apart

@@ -6,7 +6,6 @@
 
 namespace tq {
 
-constexpr int kLoraCluster = 8;    // thread blocks that share a tile of tokens
 constexpr int kLargeTile = 128;    // tokens of a tile of the kernel for many tokens
 
 // A call's arguments, for the kernels.

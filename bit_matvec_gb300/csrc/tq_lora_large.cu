@@ -3,9 +3,8 @@
 //
 // A cluster of four thread blocks takes a tile: each block a quarter of A's columns for h = A x, the four
 // parts summed through distributed shared memory, then each block a quarter of the rows of Y = Z + B h.
-// With 128 tokens a tile, A and B are read from L2 a quarter as often as with the 32 of tq_lora.cu, and a
-// quarter of the blocks' time goes to them; what is left for the threads is the traffic itself: x in, Z in, Y
-// out. (Clusters of eight: 273 us where four take 183; the GPU holds 15 of them with a block an SM, and 36
+// With 128 tokens a tile, A and B are read from L2 a quarter as often as with the 32 of tq_lora.cu; what is left
+// for the threads is the traffic itself: x in, Z in, Y out. (Clusters of eight: 273 us where four take 183; the GPU holds 15 of them with a block an SM, and 36
 // of four.)
 //
 // Ranks above 64 take several passes of 64 over Y, of 32-bit values: a pass adds to what the one before

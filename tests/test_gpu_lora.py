@@ -157,6 +157,50 @@ def test_many_tokens_order_and_strides(tq):
     assert torch.equal(wide.view(I32)[left], before.view(I32)[left])
 
 
+@pytest.mark.parametrize("top", [40, 100])
+def test_many_tokens_graph_and_streams(tq, top):
+    """From a graph with other adapters each time, and on two streams at once; in one pass and in two."""
+    ntok, cols, rows, adapters = 4200, 264, 136, 4
+    ds = [make(ntok, cols, rows, adapters, top, seed=60 + s, bare=0.3 * s) for s in range(3)]
+    want = [run(tq, d) for d in ds]
+    for d, y in zip(ds, want):
+        check(d, y)
+        assert torch.equal(y[d["ids"] < 0], d["z"][d["ids"] < 0])
+    e = {n: t.clone() for n, t in ds[0].items()}
+    lora = tq.Lora(e["a"], e["b"], e["rank"], e["scale"])
+    y, ws = torch.empty_like(e["z"]), scratch(tq, ntok, adapters)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        tq.tq_lora_add(e["x"], lora, e["ids"], y, e["z"], ws)
+    torch.cuda.synchronize()
+    for d, w in list(zip(ds, want))[::-1]:
+        for n in e:
+            e[n].copy_(d[n])
+        y.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(y, w)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ds], [[], [], []]
+    for _ in range(4):
+        for i, (d, s) in enumerate(zip(ds, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run(tq, d))
+    torch.cuda.synchronize()
+    for i in range(3):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("top", [40, 51, 100])
+def test_many_tokens_weights_at_any_address(tq, top):
+    """Rows of B 2 bytes off, and of an odd stride, give the bits of those at 8-byte addresses."""
+    d = make(4100, 264, 136, 3, top, seed=70, pad=-top % 4)
+    want = run(tq, d)
+    b = torch.full((3, 140, top + 3 - top % 2), float("nan"), device="cuda", dtype=BF16)[:, 3:139, 1:top + 1]
+    b.copy_(d["b"])
+    assert torch.equal(run(tq, dict(d, b=b)), want)
+
+
 def test_many_tokens_not_finite_and_bad(tq):
     d = make(4300, 256, 64, 2, 48, seed=51, bare=0.0, ragged=False)
     clean = run(tq, d)
