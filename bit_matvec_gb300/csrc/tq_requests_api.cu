@@ -95,8 +95,9 @@ int tq_lora_add(const void* X, int64_t x_stride, int x_type, const tq_lora* lora
                    (Z && z_stride < l.rows)))
     return TQ_ERR_SHAPE;
   if (ntok == 0 || l.rows == 0) return TQ_OK;
-  const bool work = l.adapters > 0 && l.max_rank > 0 && l.cols > 0;
-  if (!ids || !Y || (work && (!X || !l.a || !l.b))) return TQ_ERR_NULL;
+  // (without columns h is zeros, and B is multiplied by them all the same)
+  const bool work = l.adapters > 0 && l.max_rank > 0;
+  if (!ids || !Y || (work && (!l.b || (l.cols > 0 && (!X || !l.a))))) return TQ_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(Y, yb) || !aligned(Z, yb) || !aligned(X, 16) || !aligned(l.a, 16) ||
       !aligned(l.b, 2) || !aligned(l.rank, 4) || !aligned(l.scale, 4))
     return TQ_ERR_ALIGN;

@@ -439,3 +439,19 @@ def test_workspace_refused(tq):
         with pytest.raises(tq.TQError) as e:
             tq.tq_lora_add(**args)
         assert e.value.code == tq.TQ_ERR_SHAPE
+
+
+@pytest.mark.parametrize("ntok,top", [(3, 8), (40, 20), (300, 20), (4200, 40)])
+def test_without_columns(tq, ntok, top):
+    """A product over nothing is zero: Y is Z, X and A may be missing."""
+    d = make(ntok, 8, 264, 2, top, seed=80, ragged=False)
+    lora = tq.Lora(d["a"], d["b"], None, d["scale"])
+    s = lora.struct
+    s.a, s.cols, s.a_stride, s.a_row_stride = None, 0, 0, 0
+    y = torch.full_like(d["z"], float("nan"))
+    ws = scratch(tq, ntok, 2)
+    rc = tq.library().tq_lora_add(None, 0, tq.TQ_F32, lora.ref, d["ids"].data_ptr(), d["z"].data_ptr(), 264,
+                                  y.data_ptr(), 264, tq.TQ_F32, ntok, ws.data_ptr() if ws is not None else None,
+                                  ws.numel() if ws is not None else 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == tq.TQ_OK
+    assert torch.equal(y, d["z"])

@@ -72,6 +72,13 @@ def test_lora_nothing_to_do(tq):
                                     None) == tq.TQ_ERR_NULL
 
 
+def test_lora_without_columns(tq):
+    """h is zeros then, and B is read all the same: it may not be missing where there is a rank."""
+    without = dict(cols=0, a=None, as_=0, ars=0)
+    for over in ({}, dict(top=1, brs=1), dict(adapters=1)):
+        assert add(tq, struct=lora(tq, b=None, **without, **over), x=None, xs=0) == tq.TQ_ERR_NULL
+
+
 def test_lora_workspace(tq):
     assert tq.tq_lora_add_workspace_bytes(0, 0) == tq.tq_lora_add_workspace_bytes(256, 32768) == 0
     sizes = [tq.tq_lora_add_workspace_bytes(n, 64) for n in (257, 1000, 8192, 1 << 20)]
