@@ -470,8 +470,8 @@ def tq_paged_attention(Q, kv: PagedKV, q_start, kv_len, O, max_q: int, max_kv: i
 class Lora:
     """Low-rank adapters of one matrix [rows][cols]: a [adapters][max_rank][cols] and
     b [adapters][rows][max_rank], f16 or bf16, of any strides but unit last ones; rank int32 and
-    scale f32 [adapters], or None (all max_rank; 1). The tensors are used in place: write an
-    adapter's slot, its rank and its scale freely between calls."""
+    scale f32 [adapters], contiguous, or None (all max_rank; 1). The tensors are used in place:
+    write an adapter's slot, its rank and its scale freely between calls."""
 
     class _Struct(ctypes.Structure):
         _fields_ = [(n, ctypes.c_void_p) for n in ("a", "b", "rank", "scale")] + [
@@ -483,14 +483,16 @@ class Lora:
         if a.dim() != 3 or b.dim() != 3 or a.dtype != b.dtype or a.shape[0] != b.shape[0] or (
                 a.shape[1] != b.shape[2]):
             raise ValueError("a must be [adapters][max_rank][cols] and b [adapters][rows][max_rank]")
-        if not (a.is_cuda and b.is_cuda):
-            raise ValueError("tensor must live on a CUDA device")
         if any(t.shape[2] > 1 and t.stride(2) != 1 for t in (a, b)):
             raise ValueError("the last dimension must be contiguous")
         if rank is not None and (rank.dtype != torch.int32 or rank.numel() != a.shape[0]):
             raise ValueError("rank must be int32 [adapters]")
         if scale is not None and (scale.dtype != torch.float32 or scale.numel() != a.shape[0]):
             raise ValueError("scale must be float32 [adapters]")
+        if any(t is not None and not t.is_contiguous() for t in (rank, scale)):
+            raise ValueError("rank and scale must be contiguous")
+        if not (a.is_cuda and b.is_cuda):
+            raise ValueError("tensor must live on a CUDA device")
         if any(t.device != a.device for t in (b, rank, scale) if t is not None):
             raise ValueError("the tensors must be on one device")
         self.a, self.b, self.rank, self.scale = a, b, rank, scale   # kept alive

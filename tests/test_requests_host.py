@@ -97,6 +97,19 @@ def test_lora_class(tq):
             tq.Lora(*bad)
 
 
+def test_lora_rank_and_scale_in_one_piece(tq):
+    """Their addresses alone are kept: views with gaps, or of one value for all, would be read
+    beside what they show."""
+    a, b = torch.zeros(2, 4, 8, dtype=torch.float16), torch.zeros(2, 5, 4, dtype=torch.float16)
+    rank, scale = torch.zeros(4, dtype=torch.int32), torch.zeros(2, 2)
+    for kw in (dict(rank=rank[::2]), dict(rank=rank[:1].expand(2)), dict(scale=scale[:, 1]),
+               dict(scale=torch.ones(1).expand(2)), dict(rank=rank[:2], scale=scale[:, 0])):
+        with pytest.raises(ValueError, match="contiguous"):
+            tq.Lora(a, b, **kw)
+    with pytest.raises(ValueError, match="CUDA"):   # what is left to refuse here
+        tq.Lora(a, b, rank[2:], scale[1])
+
+
 def draw(tq, **over):
     a = dict(x=A, stride=1000, type=0, n=3, vocab=1000, u=B, t=C, k=C + 4096, p=C + 8192, m=C + 12288,
              tokens=D, logp=E)
