@@ -361,14 +361,15 @@ class Rope:
 
     class _Struct(ctypes.Structure):
         _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int64),
-                    ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+                    ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                    ("device", ctypes.c_int64)]   # of the tensors, for csrc/tq_call.c
 
     def __init__(self, turns: torch.Tensor, interleaved: bool = False, amplitude: float = 1.0):
         self.turns = turns   # kept alive: the struct holds its address
         if turns.dtype != torch.int64:
             raise ValueError("turns must be torch.int64")
         self.struct = Rope._Struct(_ptr(turns), 2 * turns.numel(), 1 if interleaved else 0,
-                                   amplitude)
+                                   amplitude, turns.get_device())
         self.ref = ctypes.addressof(self.struct)
 
 
@@ -385,7 +386,8 @@ class PagedKV:
                         (n, ctypes.c_int64) for n in
                         ("nseq", "table_width", "table_stride", "pages", "page_size", "heads",
                          "head_dim", "page_stride", "head_stride", "slot_stride")] + [
-                        ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                        ("type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                        ("device", ctypes.c_int64)]   # of the tensors, for csrc/tq_call.c
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor):
         if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
@@ -397,13 +399,15 @@ class PagedKV:
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or (
                 block_table.shape[1] > 1 and block_table.stride(1) != 1):
             raise ValueError("block_table must be int32 [sequences][pages] with contiguous rows")
+        if not k.device == v.device == block_table.device:
+            raise ValueError("the tensors must be on one device")
         self.k, self.v, self.block_table = k, v, block_table
         nseq, width = block_table.shape
         pages, heads, page_size, dim = k.shape
         self.struct = PagedKV._Struct(
             k.data_ptr(), v.data_ptr(), block_table.data_ptr(), nseq, width,
             block_table.stride(0) if nseq > 1 else width, pages, page_size, heads, dim,
-            k.stride(0), k.stride(1), k.stride(2), _type(k), 0)
+            k.stride(0), k.stride(1), k.stride(2), _type(k), 0, k.get_device())
         self.ref = ctypes.addressof(self.struct)
 
 
@@ -477,7 +481,8 @@ class Lora:
         _fields_ = [(n, ctypes.c_void_p) for n in ("a", "b", "rank", "scale")] + [
             (n, ctypes.c_int64) for n in ("adapters", "max_rank", "rows", "cols", "a_stride",
                                           "a_row_stride", "b_stride", "b_row_stride")] + [
-            ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+            ("type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+            ("device", ctypes.c_int64)]   # of the tensors, for csrc/tq_call.c
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, rank=None, scale=None):
         if a.dim() != 3 or b.dim() != 3 or a.dtype != b.dtype or a.shape[0] != b.shape[0] or (
@@ -503,7 +508,8 @@ class Lora:
             return t.stride(dim) if t.shape[dim] > 1 else least
         self.struct = Lora._Struct(
             a.data_ptr(), b.data_ptr(), _ptr(rank), _ptr(scale), count, top, rows, cols,
-            stride(a, 0, 0), stride(a, 1, 0), stride(b, 0, 0), stride(b, 1, 0), _type(a), 0)
+            stride(a, 0, 0), stride(a, 1, 0), stride(b, 0, 0), stride(b, 1, 0), _type(a), 0,
+            a.get_device())
         self.ref = ctypes.addressof(self.struct)
 
 

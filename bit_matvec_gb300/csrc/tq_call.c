@@ -16,7 +16,7 @@
 
 enum { kOtherDevice = 1 };
 
-static PyObject *n_shape, *n_stride, *n_dtype, *n_is_cuda, *n_data_ptr, *n_get_device, *n_numel,
+static PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr, *n_get_device, *n_numel,
     *n_is_contiguous, *n_cuda_stream, *n_element_size;
 static PyObject *dtypes[3], *dtype_i32;          /* torch.float32, float16, bfloat16; int32 */
 static PyObject *get_device, *current_stream;    /* of the current device; of a device */
@@ -90,12 +90,20 @@ static int type_of(PyObject *t, int *type) {
   return TQ_ERR_TYPE;
 }
 
-static int on_cuda(PyObject *t) {
-  PyObject *b = PyObject_GetAttr(t, n_is_cuda);
-  if (!b) return kRaised;
-  const int yes = b == Py_True;
-  Py_DECREF(b);
-  return yes ? 0 : raise_value("tensor must live on a CUDA device");
+/* The device of a call's tensors so far, -1 before the first: one more of them. */
+static int same_device(int64_t d, int64_t *dev) {
+  if (d < 0) return raise_value("tensor must live on a CUDA device");
+  if (*dev >= 0 && d != *dev) return raise_value("the tensors must be on one device");
+  *dev = d;
+  return 0;
+}
+
+static int on_device(PyObject *t, int64_t *dev) {
+  PyObject *i = PyObject_CallMethodNoArgs(t, n_get_device);
+  if (!i) return kRaised;
+  const int64_t d = PyLong_AsLongLong(i);
+  Py_DECREF(i);
+  return PyErr_Occurred() ? kRaised : same_device(d, dev);
 }
 
 static int address(PyObject *t, void **p) {
@@ -107,10 +115,10 @@ static int address(PyObject *t, void **p) {
 }
 
 /* Type, placement, strides and address of a tensor whose shape was read. */
-static int read_rows(PyObject *t, rows_t *r) {
+static int read_rows(PyObject *t, rows_t *r, int64_t *dev) {
   int rc = type_of(t, &r->type);
   if (rc) return rc;
-  if ((rc = on_cuda(t))) return rc;
+  if ((rc = on_device(t, dev))) return rc;
   int64_t s[3];
   if ((rc = read_dims(PyObject_CallMethodNoArgs(t, n_stride), s))) return rc;
   if ((r->d > 1 && s[2] != 1) || (r->h > 1 && s[1] != r->d))
@@ -120,7 +128,7 @@ static int read_rows(PyObject *t, rows_t *r) {
 }
 
 /* A [rows][values] tensor whose rows are contiguous: h is 1. */
-static int read_matrix(PyObject *t, rows_t *r) {
+static int read_matrix(PyObject *t, rows_t *r, int64_t *dev) {
   int64_t d[2], s[2];
   int rc = read_dims_of(PyObject_GetAttr(t, n_shape), d, 2);
   if (rc) return rc;
@@ -128,7 +136,7 @@ static int read_matrix(PyObject *t, rows_t *r) {
   r->h = 1;
   r->d = d[1];
   if ((rc = type_of(t, &r->type))) return rc;
-  if ((rc = on_cuda(t))) return rc;
+  if ((rc = on_device(t, dev))) return rc;
   if ((rc = read_dims_of(PyObject_CallMethodNoArgs(t, n_stride), s, 2))) return rc;
   if (r->d > 1 && s[1] != 1) return raise_value("the values of a row must be contiguous");
   r->stride = r->n > 1 ? s[0] : r->d;
@@ -136,7 +144,7 @@ static int read_matrix(PyObject *t, rows_t *r) {
 }
 
 /* A contiguous vector of n values of a type, or None. */
-static int read_vector(PyObject *t, PyObject *dtype, int64_t n, void **p) {
+static int read_vector(PyObject *t, PyObject *dtype, int64_t n, void **p, int64_t *dev) {
   *p = NULL;
   if (t == Py_None) return 0;
   PyObject *d = PyObject_GetAttr(t, n_dtype);
@@ -148,7 +156,7 @@ static int read_vector(PyObject *t, PyObject *dtype, int64_t n, void **p) {
   const int64_t count = PyLong_AsLongLong(c);
   Py_DECREF(c);
   if (count != n) return TQ_ERR_SHAPE;
-  const int rc = on_cuda(t);
+  const int rc = on_device(t, dev);
   if (rc) return rc;
   PyObject *b = PyObject_CallMethodNoArgs(t, n_is_contiguous);
   if (!b) return kRaised;
@@ -157,23 +165,17 @@ static int read_vector(PyObject *t, PyObject *dtype, int64_t n, void **p) {
   return address(t, p);
 }
 
-/* The stream's handle: the given one's, or the current one's of the tensor's
+/* The stream's handle: the given one's, or the current one's of the tensors'
  * device, which has to be the current device. */
-static int read_stream(PyObject *t, PyObject *stream, void **s) {
-  PyObject *dev = PyObject_CallMethodNoArgs(t, n_get_device);
-  if (!dev) return kRaised;
+static int read_stream(int64_t dev, PyObject *stream, void **s) {
   PyObject *cur = PyObject_CallNoArgs(get_device);
-  if (!cur) {
-    Py_DECREF(dev);
-    return kRaised;
-  }
-  const int64_t here = PyLong_AsLongLong(cur), want = PyLong_AsLongLong(dev);
-  Py_DECREF(cur);
+  if (!cur) return kRaised;
+  const int64_t here = PyLong_AsLongLong(cur);
   PyObject *h = NULL;
-  if (here == want)
-    h = stream == Py_None ? PyObject_CallOneArg(current_stream, dev) : PyObject_GetAttr(stream, n_cuda_stream);
-  Py_DECREF(dev);
-  if (here != want) return PyErr_Occurred() ? kRaised : kOtherDevice;
+  if (here == dev)
+    h = stream == Py_None ? PyObject_CallOneArg(current_stream, cur) : PyObject_GetAttr(stream, n_cuda_stream);
+  Py_DECREF(cur);
+  if (here != dev) return PyErr_Occurred() ? kRaised : kOtherDevice;
   if (!h) return kRaised;
   *s = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
@@ -181,11 +183,11 @@ static int read_stream(PyObject *t, PyObject *stream, void **s) {
 }
 
 /* A contiguous buffer of any type, or None, and its bytes. */
-static int read_workspace(PyObject *t, void **p, int64_t *bytes) {
+static int read_workspace(PyObject *t, void **p, int64_t *bytes, int64_t *dev) {
   *p = NULL;
   *bytes = 0;
   if (t == Py_None) return 0;
-  int rc = on_cuda(t);
+  int rc = on_device(t, dev);
   if (rc) return rc;
   PyObject *b = PyObject_CallMethodNoArgs(t, n_is_contiguous);
   if (!b) return kRaised;
@@ -209,6 +211,20 @@ static int read_address(PyObject *o, void **p) {
   return PyErr_Occurred() ? kRaised : 0;
 }
 
+/* What the binding's objects point to: the C struct and the device of its tensors. */
+typedef struct {
+  tq_rope c;
+  int64_t device;
+} placed_rope;
+typedef struct {
+  tq_paged_kv c;
+  int64_t device;
+} placed_kv;
+typedef struct {
+  tq_lora c;
+  int64_t device;
+} placed_lora;
+
 static PyObject *result(int rc) { return rc == kRaised ? NULL : PyLong_FromLong(rc); }
 
 #define TRY(x)                        \
@@ -226,6 +242,7 @@ static PyObject *qk_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t nar
   (void)self;
   if (nargs != 10) return PyErr_Format(PyExc_TypeError, "10 arguments expected");
   rows_t xq = {0}, xk = {0}, yq = {0}, yk = {0};
+  int64_t dev = -1;
   const int keys = a[1] != Py_None;
   TRY(read_shape(a[0], &xq));
   TRY(read_shape(a[2], &yq));
@@ -235,21 +252,22 @@ static PyObject *qk_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t nar
     TRY(read_shape(a[3], &yk));
     CHECK(same_shape(&xk, &yk) && xk.n == xq.n && xk.d == xq.d, TQ_ERR_SHAPE);
   }
-  TRY(read_rows(a[0], &xq));
-  TRY(read_rows(a[2], &yq));
+  TRY(read_rows(a[0], &xq, &dev));
+  TRY(read_rows(a[2], &yq, &dev));
   if (keys) {
-    TRY(read_rows(a[1], &xk));
-    TRY(read_rows(a[3], &yk));
+    TRY(read_rows(a[1], &xk, &dev));
+    TRY(read_rows(a[3], &yk, &dev));
     CHECK(xk.type == xq.type && yk.type == yq.type, TQ_ERR_TYPE);
   }
   void *pos, *rope, *qw, *kw, *stream;
-  TRY(read_vector(a[4], dtype_i32, xq.n, &pos));
+  TRY(read_vector(a[4], dtype_i32, xq.n, &pos, &dev));
   TRY(read_address(a[5], &rope));
-  TRY(read_vector(a[6], dtypes[0], xq.d, &qw));
-  TRY(read_vector(a[7], dtypes[0], xq.d, &kw));
+  if (rope) TRY(same_device(((const placed_rope *)rope)->device, &dev));
+  TRY(read_vector(a[6], dtypes[0], xq.d, &qw, &dev));
+  TRY(read_vector(a[7], dtypes[0], xq.d, &kw, &dev));
   const double eps = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) return NULL;
-  TRY(read_stream(a[0], a[9], &stream));
+  TRY(read_stream(dev, a[9], &stream));
   return result(call_qk(xq.p, xq.stride, xk.p, xk.stride, xq.type, yq.p, yq.stride, yk.p, yk.stride,
                         yq.type, xq.n, xq.h, xk.h, xq.d, qw, kw, (float)eps, rope, pos, stream));
 }
@@ -259,6 +277,7 @@ static PyObject *kv_append(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
   (void)self;
   if (nargs != 12) return PyErr_Format(PyExc_TypeError, "12 arguments expected");
   rows_t xq = {0}, xk = {0}, xv = {0}, yq = {0};
+  int64_t dev = -1;
   const int queries = a[0] != Py_None;
   void *kvp;
   TRY(read_address(a[4], &kvp));
@@ -271,23 +290,25 @@ static PyObject *kv_append(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     TRY(read_shape(a[3], &yq));
     CHECK(same_shape(&xq, &yq) && xq.n == xk.n && xq.d == xk.d, TQ_ERR_SHAPE);
   }
-  TRY(read_rows(a[1], &xk));
-  TRY(read_rows(a[2], &xv));
+  TRY(read_rows(a[1], &xk, &dev));
+  TRY(read_rows(a[2], &xv, &dev));
   CHECK(xv.type == xk.type, TQ_ERR_TYPE);
   if (queries) {
-    TRY(read_rows(a[0], &xq));
-    TRY(read_rows(a[3], &yq));
+    TRY(read_rows(a[0], &xq, &dev));
+    TRY(read_rows(a[3], &yq, &dev));
     CHECK(xq.type == xk.type && yq.type == kv->type, TQ_ERR_TYPE);
   }
+  TRY(same_device(((const placed_kv *)kvp)->device, &dev));
   void *seq, *pos, *rope, *qw, *kw, *stream;
-  TRY(read_vector(a[5], dtype_i32, xk.n, &seq));
-  TRY(read_vector(a[6], dtype_i32, xk.n, &pos));
+  TRY(read_vector(a[5], dtype_i32, xk.n, &seq, &dev));
+  TRY(read_vector(a[6], dtype_i32, xk.n, &pos, &dev));
   TRY(read_address(a[7], &rope));
-  TRY(read_vector(a[8], dtypes[0], xk.d, &qw));
-  TRY(read_vector(a[9], dtypes[0], xk.d, &kw));
+  if (rope) TRY(same_device(((const placed_rope *)rope)->device, &dev));
+  TRY(read_vector(a[8], dtypes[0], xk.d, &qw, &dev));
+  TRY(read_vector(a[9], dtypes[0], xk.d, &kw, &dev));
   const double eps = PyFloat_AsDouble(a[10]);
   if (PyErr_Occurred()) return NULL;
-  TRY(read_stream(a[1], a[11], &stream));
+  TRY(read_stream(dev, a[11], &stream));
   return result(call_append(xq.p, xq.stride, xk.p, xk.stride, xv.p, xv.stride, xk.type, yq.p, yq.stride,
                             kv, seq, pos, xk.n, xq.h, qw, kw, (float)eps, rope, stream));
 }
@@ -297,26 +318,28 @@ static PyObject *paged_attention(PyObject *self, PyObject *const *a, Py_ssize_t 
   (void)self;
   if (nargs != 12) return PyErr_Format(PyExc_TypeError, "12 arguments expected");
   rows_t q = {0}, o = {0};
+  int64_t dev = -1;
   void *kvp;
   TRY(read_address(a[1], &kvp));
   const tq_paged_kv *kv = kvp;
   TRY(read_shape(a[0], &q));
   TRY(read_shape(a[4], &o));
   CHECK(same_shape(&q, &o) && q.d == kv->head_dim, TQ_ERR_SHAPE);
-  TRY(read_rows(a[0], &q));
-  TRY(read_rows(a[4], &o));
+  TRY(read_rows(a[0], &q, &dev));
+  TRY(read_rows(a[4], &o, &dev));
   CHECK(q.type == kv->type, TQ_ERR_TYPE);
+  TRY(same_device(((const placed_kv *)kvp)->device, &dev));
   void *start, *len, *ws, *lse, *stream;
-  TRY(read_vector(a[2], dtype_i32, kv->nseq + 1, &start));
-  TRY(read_vector(a[3], dtype_i32, kv->nseq, &len));
-  TRY(read_vector(a[10], dtypes[0], q.n * q.h, &lse));
+  TRY(read_vector(a[2], dtype_i32, kv->nseq + 1, &start, &dev));
+  TRY(read_vector(a[3], dtype_i32, kv->nseq, &len, &dev));
+  TRY(read_vector(a[10], dtypes[0], q.n * q.h, &lse, &dev));
   const int64_t max_q = PyLong_AsLongLong(a[5]), max_kv = PyLong_AsLongLong(a[6]);
   const double scale = PyFloat_AsDouble(a[7]);
   const int64_t window = PyLong_AsLongLong(a[9]);
   if (PyErr_Occurred()) return NULL;
   int64_t ws_bytes;
-  TRY(read_workspace(a[8], &ws, &ws_bytes));
-  TRY(read_stream(a[0], a[11], &stream));
+  TRY(read_workspace(a[8], &ws, &ws_bytes, &dev));
+  TRY(read_stream(dev, a[11], &stream));
   return result(call_attend(q.p, q.stride, kv, start, len, o.p, o.stride, o.type, lse, q.n, q.h, max_q,
                             max_kv, (float)scale, window, ws, ws_bytes, stream));
 }
@@ -326,23 +349,25 @@ static PyObject *lora_add(PyObject *self, PyObject *const *a, Py_ssize_t nargs) 
   (void)self;
   if (nargs != 7) return PyErr_Format(PyExc_TypeError, "7 arguments expected");
   rows_t x = {0}, y = {0}, z = {0};
+  int64_t dev = -1;
   void *lp;
   TRY(read_address(a[1], &lp));
   const tq_lora *l = lp;
   const int base = a[4] != Py_None;
-  TRY(read_matrix(a[0], &x));
-  TRY(read_matrix(a[3], &y));
+  TRY(read_matrix(a[0], &x, &dev));
+  TRY(read_matrix(a[3], &y, &dev));
   CHECK(x.n == y.n && x.d == l->cols && y.d == l->rows, TQ_ERR_SHAPE);
   if (base) {
-    TRY(read_matrix(a[4], &z));
+    TRY(read_matrix(a[4], &z, &dev));
     CHECK(same_shape(&z, &y), TQ_ERR_SHAPE);
     CHECK(z.type == y.type, TQ_ERR_TYPE);
   }
+  TRY(same_device(((const placed_lora *)lp)->device, &dev));
   void *ids, *ws, *stream;
   int64_t ws_bytes;
-  TRY(read_vector(a[2], dtype_i32, x.n, &ids));
-  TRY(read_workspace(a[5], &ws, &ws_bytes));
-  TRY(read_stream(a[0], a[6], &stream));
+  TRY(read_vector(a[2], dtype_i32, x.n, &ids, &dev));
+  TRY(read_workspace(a[5], &ws, &ws_bytes, &dev));
+  TRY(read_stream(dev, a[6], &stream));
   return result(call_lora(x.p, x.stride, x.type, l, ids, z.p, z.stride, y.p, y.stride, y.type, x.n, ws,
                           ws_bytes, stream));
 }
@@ -352,16 +377,17 @@ static PyObject *sample(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
   (void)self;
   if (nargs != 9) return PyErr_Format(PyExc_TypeError, "9 arguments expected");
   rows_t x = {0};
-  TRY(read_matrix(a[0], &x));
+  int64_t dev = -1;
+  TRY(read_matrix(a[0], &x, &dev));
   void *u, *tokens, *temperature, *top_k, *top_p, *min_p, *logp, *stream;
-  TRY(read_vector(a[1], dtypes[0], x.n, &u));
-  TRY(read_vector(a[2], dtype_i32, x.n, &tokens));
-  TRY(read_vector(a[3], dtypes[0], x.n, &temperature));
-  TRY(read_vector(a[4], dtype_i32, x.n, &top_k));
-  TRY(read_vector(a[5], dtypes[0], x.n, &top_p));
-  TRY(read_vector(a[6], dtypes[0], x.n, &min_p));
-  TRY(read_vector(a[7], dtypes[0], x.n, &logp));
-  TRY(read_stream(a[0], a[8], &stream));
+  TRY(read_vector(a[1], dtypes[0], x.n, &u, &dev));
+  TRY(read_vector(a[2], dtype_i32, x.n, &tokens, &dev));
+  TRY(read_vector(a[3], dtypes[0], x.n, &temperature, &dev));
+  TRY(read_vector(a[4], dtype_i32, x.n, &top_k, &dev));
+  TRY(read_vector(a[5], dtypes[0], x.n, &top_p, &dev));
+  TRY(read_vector(a[6], dtypes[0], x.n, &min_p, &dev));
+  TRY(read_vector(a[7], dtypes[0], x.n, &logp, &dev));
+  TRY(read_stream(dev, a[8], &stream));
   return result(call_sample(x.p, x.stride, x.type, x.n, x.d, u, temperature, top_k, top_p, min_p, tokens,
                             logp, stream));
 }
@@ -408,7 +434,7 @@ PyMODINIT_FUNC PyInit__tq_call(void) {
     PyObject **at;
     const char *name;
   } names[] = {{&n_shape, "shape"}, {&n_stride, "stride"}, {&n_dtype, "dtype"},
-               {&n_is_cuda, "is_cuda"}, {&n_data_ptr, "data_ptr"}, {&n_get_device, "get_device"},
+               {&n_data_ptr, "data_ptr"}, {&n_get_device, "get_device"},
                {&n_numel, "numel"}, {&n_is_contiguous, "is_contiguous"},
                {&n_cuda_stream, "cuda_stream"}, {&n_element_size, "element_size"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)

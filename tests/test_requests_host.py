@@ -1,6 +1,7 @@
 """Host side of the adapter and sampling calls: workspace sizes and refusals, which return before any
 CUDA call (fake addresses are safe)."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -153,3 +154,65 @@ def test_marshalling(tq):
     with pytest.raises(tq.TQError) as e:
         tq.tq_sample(x.double(), x, x)
     assert e.value.code == tq.TQ_ERR_TYPE
+
+
+class Placed:
+    """What the marshalling asks a tensor for, of one that would lie on GPU `device`."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device=0, at=A):
+        self.shape, self.dtype, self.device, self.at = torch.Size(shape), dtype, device, at
+
+    def stride(self):
+        return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+def test_tensors_of_several_devices(tq):
+    """Each tensor of a call in turn on another GPU than the others, and the description's: refused
+    before anything is asked of a GPU."""
+    calls = __import__("bit_matvec_gb300.binding", fromlist=["_calls"])._calls()
+    f32, i32, bf16 = torch.float32, torch.int32, torch.bfloat16
+    rope = tq.Rope._Struct(A, 32, 0, 1.0)
+    cache = tq.PagedKV._Struct(A, B, C, 2, 8, 8, 16, 16, 2, 64, 2048, 1024, 64, 2, 0)
+    low = tq.Lora._Struct(A, B, None, None, 4, 16, 100, 64, 1024, 64, 1600, 16, 2, 0)
+    every = {
+        "lora_add": ((3, 64), low, ("i", 3), (3, 100), (3, 100), ("b", 64), None),
+        "sample": ((3, 50), ("f", 3), ("i", 3), ("f", 3), ("i", 3), ("f", 3), ("f", 3), ("f", 3), None),
+        "paged_attention": (("q", 3, 4, 64), cache, ("i", 3), ("i", 2), ("q", 3, 4, 64), 2, 100, 0.125, ("b", 64),
+                            0, ("f", 12), None),
+        "kv_append": ((3, 4, 64), (3, 2, 64), (3, 2, 64), ("q", 3, 4, 64), cache, ("i", 3), ("i", 3), rope,
+                      ("f", 64), ("f", 64), 1e-6, None),
+        "qk_norm_rope": ((3, 4, 64), (3, 2, 64), (3, 4, 64), (3, 2, 64), ("i", 3), rope, ("f", 64), ("f", 64),
+                         1e-6, None),
+    }
+    for name, form in every.items():
+        movable = [i for i, f in enumerate(form) if isinstance(f, (tuple, ctypes.Structure))]
+        for away in movable:
+            args = []
+            for i, f in enumerate(form):
+                device = 1 if i == away else 0
+                if isinstance(f, ctypes.Structure):
+                    f.device = device
+                    f = ctypes.addressof(f)
+                elif isinstance(f, tuple):
+                    kind = f[0] if isinstance(f[0], str) else "f"
+                    dtype = {"f": f32, "i": i32, "b": torch.uint8, "q": bf16}[kind]
+                    f = Placed(f[1:] if isinstance(f[0], str) else f, dtype, device)
+                args.append(f)
+            with pytest.raises(ValueError, match="one device"):
+                getattr(calls, name)(*args)
