@@ -30,6 +30,8 @@ struct LoraArgs {
   const int4* tiles;     // adapter, its rank, first of order, tokens
   const int* ntiles;
   int* status;
+  uint64_t stall_ns;     // (the kernel for many tokens) test facility, if not 0: the first block issues no
+                         // products, its waits expire after this (tq_debug_stall_next_launch)
 };
 
 // x as a tf32 value and the rest of it, rounded to tf32: good to 2^-21. The

@@ -692,9 +692,9 @@ int tq_probe_read_sum(const void *buf, int64_t bytes, uint32_t *out, int early, 
  * it did request before it exits, so no copy outlives it. Nothing faults and
  * nothing waits without bound. Kernels that take it: the GEMV (ntok <= 16, or <= 8
  * in the workspace forms),
- * the tensor-core kernel of the workspace forms and the kernels of
- * tq_paged_attention (their usual limit is 1 s). wait_limit_ns = 0 cancels a
- * pending stall.
+ * the tensor-core kernel of the workspace forms, the kernels of
+ * tq_paged_attention and the one of tq_lora_add for long batches of high rank
+ * (the usual limit of these is 1 s). wait_limit_ns = 0 cancels a pending stall.
  * Errors: TQ_ERR_SHAPE if wait_limit_ns < 0.
  */
 int tq_debug_stall_next_launch(int64_t wait_limit_ns);

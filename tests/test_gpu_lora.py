@@ -1,5 +1,7 @@
 """Low-rank adapters beside a product, on the GPU against the 64-bit form: types, ranks, odd sizes,
 strides, tokens in any order, padding that holds anything, bad indexes, streams and graphs."""
+import time
+
 import pytest
 import torch
 
@@ -455,3 +457,28 @@ def test_without_columns(tq, ntok, top):
                                   ws.numel() if ws is not None else 0, torch.cuda.current_stream().cuda_stream)
     assert rc == tq.TQ_OK
     assert torch.equal(y, d["z"])
+
+
+@pytest.mark.parametrize("shape", [(4200, 264, 136, 1, 40), (6000, 8, 1032, 2, 64), (4097, 5120, 2048, 2, 64),
+                                   (4200, 520, 264, 3, 130)], ids=str)
+def test_timeout_reported_then_cleared(tq, shape):
+    """A first block of the kernel for long batches that hands nothing to the tensor cores (columns of x, or,
+    where it has none, rows of B): its waits run out, once, the other tiles are right, the next call is. In
+    one pass of ranks and in three."""
+    ntok, cols, rows, adapters, top = shape
+    d = make(ntok, cols, rows, adapters, top, seed=90)
+    want = run(tq, d)
+    assert tq.tq_device_status() == tq.TQ_OK
+    torch.cuda.synchronize()
+    tq.tq_debug_stall_next_launch(200_000)
+    try:
+        t = time.perf_counter()
+        got = run(tq, d)
+        torch.cuda.synchronize()
+        t = time.perf_counter() - t
+    finally:
+        tq.tq_debug_stall_next_launch(0)
+    assert tq.tq_device_status() == tq.TQ_ERR_TIMEOUT
+    assert t < 0.8 and tq.tq_device_status() == tq.TQ_OK
+    assert ((got != want).any(dim=1).sum() <= 128)      # the tokens of one tile
+    assert torch.equal(run(tq, d), want)
