@@ -9,7 +9,7 @@
 // The kept tokens are a beginning of the order (falling logit, rising index). A
 // token's place in it is an integer, its logit's bits above its complemented
 // index, so each filter is a least place, the cut. A cut is found by counting
-// (top-k) or weighing (top-p) the tokens in 768 ranges, first 16 to an octave
+// (top-k) or weighing (top-p) the tokens in 896 ranges, first 16 to an octave
 // of weight, then, where a range holds too many tokens (equal logits), equal
 // parts of it, until the range around the cut holds few enough to be sorted. If
 // that range and all tokens above it fit in the list, which is the rule for the
@@ -18,7 +18,8 @@
 // draw falls into is looked through.
 //
 // Weights are integers (tq_weight.cuh): their sums do not depend on the order
-// in which threads add.
+// in which threads add. What a thread, a block of 512 tokens or the list sums up is
+// in units of a weight; where such sums meet they are cut to coarse units.
 //
 // What bounds it: the weights' instructions, 36 a token for a row without filters. 256 rows of 262144
 // take 113 us (2.4 TB/s, 2.4 instructions a cycle), 512 rows of 32768 with filters of their own 63, 64 of
@@ -79,13 +80,13 @@ struct alignas(16) Shared {
       u64 list[kList];        // places of the tokens at a cut
       u64 weight[kList];      // (rank 0) their weights
     };
-    struct {                  // while a window is narrowed: weights by bin, this block's and (rank 0) all
-      u64 mine[kWeightBins], all[kWeightBins];
-      uint32_t tokens[kWeightBins];
+    struct {                  // while a window is narrowed: weights by bin, this block's, then (rank 0) all
+      u64 mine[kWeightBins];      // coarse units, and what they lack
+      uint32_t low[kWeightBins], tokens[kWeightBins];
     } by_bin;
   };
   uint32_t bins[kWeightBins]; // tokens, or leading bits of weights
-  u64 sums[kMaxBlocks];       // kept weights by block
+  u64 sums[kMaxBlocks];       // kept weights by block, in units of a weight
   int octaves[kMaxBlocks];    // of a row without filters: what they are relative to
   u64 scan[kWarps];
   u64 give[6];                // what the other blocks of the cluster read
@@ -205,6 +206,12 @@ __device__ __noinline__ Sum scan(Shared* s, u64 v) {
   const u64 before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   return {(warp > 0 ? before : 0) + sum - v, all};
 }
+// This thread's part of its warp's sum of weights, in coarse units: the warp's sum
+// is cut, not each thread's.
+__device__ __forceinline__ u64 coarse(u64 units) {
+  const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)units & ((1u << kCoarse) - 1));
+  return (units >> kCoarse) + ((threadIdx.x & 31) == 0 ? low >> kCoarse : 0);
+}
 // The sum over the cluster of a value that all threads of a block have, by way
 // of give[at], and that of the blocks before this one.
 __device__ __noinline__ Sum over_cluster(Shared* s, u64 mine, int at, int cluster, int rank) {
@@ -274,7 +281,7 @@ __device__ __noinline__ void sort(u64* v, u64* spare, int n) {
 
 struct Window {
   u64 lo, hi;       // places
-  u64 above;        // tokens above it (a narrowed one by weight: what they weigh)
+  u64 above;        // tokens above it (a narrowed one by weight: what they weigh, in coarse units)
   u64 inside;       // tokens in it, at most
   u64 upto;         // tokens in it or above, at most
 };
@@ -430,7 +437,7 @@ template <typename T> struct Row {
   // The range around the cut, of tokens from `from` on: by count, the least
   // place such that `target` tokens are at it or above, none of which is below
   // `least_top`; by weight, such that they weigh the share `share` of all at
-  // least. The bins are zeros.
+  // least (`target` becomes that, in coarse units). The bins are zeros.
   __device__ __forceinline__ Window search(bool by_weight, u64& target, u64 from, uint32_t top_key, float share,
                                            float least_top) const {
     const int tid = threadIdx.x;
@@ -456,7 +463,7 @@ template <typename T> struct Row {
             atomicAdd(&s->bins[Weigher::bin_of(bits[e])], lead[e]);
           }
       });
-      const u64 sum = scan(s, mine).all;
+      const u64 sum = scan(s, coarse(mine)).all;
       if (tid == 0) s->give[0] = sum;
     } else {
       each([&](const float (&l)[4], int) {
@@ -500,7 +507,7 @@ template <typename T> struct Row {
           if (by_weight) {
             // Sums of weights' first 13 bits, 2^12 - 1 at least (just below a
             // power of two the table's entry is that power's): a token for each of
-            // these in the sum, at most, each cut by less than one and off by a unit.
+            // these in the sum, at most, each cut by less than one, and to a unit.
             const int shift = 34 - Weigher::octave_of(4 * tid + e);
             auto shifted = [&](u64 v) { return shift >= 0 ? v << shift : v >> -shift; };
             const u64 most = (n[e] + (n[e] >> 11)) >> 12, v = shifted(n[e]);
@@ -593,7 +600,7 @@ template <typename T> struct Row {
     Shared* const s = row.s;
     const int tid = threadIdx.x;
     u64* const sums = s->by_bin.mine;
-    u64* const all = s->by_bin.all;
+    uint32_t* const low = s->by_bin.low;
     uint32_t* const tokens = s->by_bin.tokens;
     while (w.inside > kList) {
       int shift = 0;
@@ -602,6 +609,7 @@ template <typename T> struct Row {
       for (int j = tid; j < kWeightBins; j += kThreads) {
         s->bins[j] = 0;
         sums[j] = 0;
+        low[j] = 0;
       }
       __syncthreads();
       u64 above = 0;
@@ -617,25 +625,33 @@ template <typename T> struct Row {
           } else if (q >= w.lo) {
             const int j = (int)((w.hi - q) >> shift);
             atomicAdd(&s->bins[j], 1u);
-            if (weighs) atomicAdd(&sums[j], (u64)row.weigh.one(x));
+            if (weighs) {
+              const u64 units = row.weigh.one(x);
+              atomicAdd(&sums[j], units >> kCoarse);
+              atomicAdd(&low[j], (uint32_t)units & ((1u << kCoarse) - 1));
+            }
           }
         }
       });
-      above = over_cluster(s, scan(s, above).all, 1, row.cluster, row.rank).all;
+      __syncwarp();
+      above = over_cluster(s, scan(s, by_weight ? coarse(above) : above).all, 1, row.cluster, row.rank).all;
       if (row.rank == 0) {
         for (int j = tid; j < kWeightBins; j += kThreads) {
-          uint32_t n = 0;
+          uint32_t n = 0, lack = 0;
           u64 v = 0;
           for (int r = 0; r < row.cluster; ++r) {
             n += remote_u32(remote(&s->bins[j], r));
-            if (by_weight) v += remote_u64(remote(&sums[j], r));
+            if (by_weight) {
+              v += remote_u64(remote(&sums[j], r));
+              lack += remote_u32(remote(&low[j], r));
+            }
           }
           tokens[j] = n;
-          all[j] = by_weight ? v : n;
+          sums[j] = by_weight ? v + (lack >> kCoarse) : n;
         }
         __syncthreads();
         if (tid < 32) {
-          const Found at = first_reaching(all, target, above);
+          const Found at = first_reaching(sums, target, above);
           const int bin = min(at.bin, kWeightBins - 1);
           const u64 top = w.hi;
           w.hi = top - ((u64)bin << shift);
@@ -654,7 +670,7 @@ template <typename T> struct Row {
   }
 
   // The tokens of the window in this block's list. `weights`: the sum of the
-  // weights of those above it is returned, and by block in s->sums.
+  // weights of those above it is returned, in coarse units, and by block in s->sums.
   __device__ __forceinline__ u64 gather(const Window& w, bool weights) const {
     const int tid = threadIdx.x, lane = tid & 31;
     if (tid == 0) s->have = 0;
@@ -697,7 +713,7 @@ template <typename T> struct Row {
       if (lane == 0) s->sums[b] = mine;
       mine = 0;
     });
-    return scan(s, all).all;
+    return scan(s, coarse(all)).all;
   }
 
   // The tokens at `lo` or above in this block's list: each warp's in a part of
@@ -832,7 +848,7 @@ __device__ __noinline__ void draw_from_list(Shared* s, u64* bins, const Args& a,
         s->pick[1] = at;
       } else {
         const u64 e = s->list[s->entry[tid]];
-        answer(a, weigh, row, part << 9 | tid, key_value((uint32_t)(e >> kIndexBits)), total, mine == total);
+        answer(a, weigh, row, part << 9 | tid, key_value((uint32_t)(e >> kIndexBits)), total >> kCoarse, mine == total);
       }
     }
     __syncthreads();
@@ -885,7 +901,7 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
         flags |= kOther;
       } else {
         octave = r.weigh.set_octave(top, &s->table);
-        const float least = (float)(octave - 47) / r.weigh.c_hi;
+        const float least = (float)(octave - kOctaves) / r.weigh.c_hi;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float x[4] = {l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
@@ -915,8 +931,8 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
   __syncthreads();
   top = __reduce_max_sync(0xffffffffu, (int)s->least_top[lane & (kWarps - 1)]);
   auto shifted = [](u64 v, int by) { return by < 64 ? v >> by : 0; };
-  const u64 block0 = b0 < r.blocks ? shifted(s->sums[b0], top - s->octaves[b0]) : 0;
-  const u64 block1 = b1 < r.blocks ? shifted(s->sums[b1], top - s->octaves[b1]) : 0;
+  const u64 block0 = b0 < r.blocks ? shifted(s->sums[b0], top - s->octaves[b0] + kCoarse) : 0;
+  const u64 block1 = b1 < r.blocks ? shifted(s->sums[b1], top - s->octaves[b1] + kCoarse) : 0;
   const Sum blocks = scan(s, block0 + block1);
   if (tid == 0) {
     s->give[4] = blocks.all;
@@ -957,17 +973,17 @@ __device__ __noinline__ bool draw_unfiltered(Shared* s, const Args& a, const T* 
     const bool second = here >= blocks.before + block0;
     const int b = second ? b1 : b0;
     s->pick[0] = b;
-    s->pick[1] = min((here - blocks.before - (second ? block0 : 0)) << (top - s->octaves[b]), s->sums[b] - 1);
+    s->pick[1] = min((here - blocks.before - (second ? block0 : 0)) << (top - s->octaves[b] + kCoarse), s->sums[b] - 1);
   }
   __syncthreads();
   const int b = (int)s->pick[0], i = b * kBlock + tid;
   r.weigh.k = 6144.0f - (float)s->octaves[b];
   const float l = i >= r.pad && i < r.end ? Elem<T>::up(from16[i]) : -INFINITY;
-  const u64 w = l >= (float)(s->octaves[b] - 47) / r.weigh.c_hi ? r.weigh.one(l) : 0;
+  const u64 w = l >= (float)(s->octaves[b] - kOctaves) / r.weigh.c_hi ? r.weigh.one(l) : 0;
   const u64 at = scan(s, w).before;
   if (at <= s->pick[1] && s->pick[1] < at + w) {
     r.weigh.k = 6144.0f - (float)highest;      // what the total is relative to
-    answer(a, r.weigh, row, r.start + i, l, total, shifted(w, highest - s->octaves[b]) == total);
+    answer(a, r.weigh, row, r.start + i, l, total, shifted(w, highest - s->octaves[b] + kCoarse) == total);
   }
   return true;
 }
@@ -1179,7 +1195,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           int kept = weights ? n : min(n, k);
           if (by_weight) {
             const u64 goal = weights ? target : p > 0.0f ? max(u64(1), fraction_of(sums[kept - 1], p, true)) : 1;
-            kept = min(kept, count_of([&](int i) { return sums[i] < goal; }) + 1);
+            const int unit = weights ? kCoarse : 0;
+            kept = min(kept, count_of([&](int i) { return sums[i] >> unit < goal; }) + 1);
           }
           if (floor != kNoCut) kept = max(1, min(kept, count_of([&](int i) { return s->list[i] >= floor; })));
           draw_from_list(s, sums + kList, a, r.weigh, row, kept, sums[kept - 1], u);
@@ -1189,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             need = 1;
             if (target > above) {
               r.sum_up(s->weight);
-              need = min(n, count_of([&](int i) { return s->weight[i] < target - above; }) + 1);
+              need = min(n, count_of([&](int i) { return s->weight[i] >> kCoarse < target - above; }) + 1);
             }
           }
           const u64 found = s->list[max(0, need - 1)];
@@ -1231,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       __syncthreads();
       const int b0 = 2 * tid, b1 = b0 + 1;
-      const u64 sum0 = b0 < r.blocks ? s->sums[b0] : 0, sum1 = b1 < r.blocks ? s->sums[b1] : 0;
+      const u64 sum0 = b0 < r.blocks ? s->sums[b0] >> kCoarse : 0, sum1 = b1 < r.blocks ? s->sums[b1] >> kCoarse : 0;
       const Sum block = scan(s, sum0 + sum1);
       const Sum slices = over_cluster(s, block.all, 4, a.cluster, rank);
       const u64 goal = goal_of(slices.all, u);
@@ -1239,16 +1256,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const u64 at = slices.before + block.before;
         if (at <= goal && goal < at + sum0 + sum1) {
           const bool second = goal >= at + sum0;
-          s->pick[0] = second ? b1 : b0;
-          s->pick[1] = second ? at + sum0 : at;
+          const int b = second ? b1 : b0;
+          s->pick[0] = b;
+          s->pick[1] = min((goal - at - (second ? sum0 : 0)) << kCoarse, s->sums[b] - 1);
         }
         __syncthreads();
         const int i = (int)s->pick[0] * kBlock + tid;
         const float l = r.value(i);
         const u64 mine = kept(l, i) ? r.weigh.one(l) : 0;
-        const u64 before = s->pick[1] + scan(s, mine).before;
-        if (before <= goal && goal < before + mine)
-          answer(a, r.weigh, row, r.start + i, l, slices.all, mine == slices.all);
+        const u64 before = scan(s, mine).before, place = s->pick[1];
+        if (before <= place && place < before + mine)
+          answer(a, r.weigh, row, r.start + i, l, slices.all, mine >> kCoarse == slices.all);
       }
     }
   }

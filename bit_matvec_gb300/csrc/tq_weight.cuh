@@ -1,5 +1,5 @@
 // tq_weight.cuh -- exp(l / T) relative to a row's largest as a 64-bit integer, good to 2^-35 of its
-// value and half a unit.
+// value and a unit.
 //
 // A draw compares sums of up to 2^18 weights with a border. In 32 bits a sum is off by some 2^-24 of
 // the total and a border is as near as the smallest weights, so one row in a hundred would draw a
@@ -14,9 +14,11 @@
 // then 2^-e T[j] 2^q with |q| <= 2^-12; T is a table of 2^(j / 2048) as the sum of two floats, and
 // 2^q - 1 = q ln 2 + (q ln 2)^2 / 2, short by (q ln 2)^3 / 6 <= 2^-40.
 //
-// The unit is 2^-46 of 2^R, so a weight is at most 2^45 and 2^18 of them fit in 64 bits. Where bits
-// fall off at the low end the last bit is set: off by at most one unit, to both sides alike, in one
-// operation.
+// The unit is 2^-54 of 2^R, so a weight is at most 2^53 and 2^10 of them fit in 64 bits: those of a list, of
+// a block of 512, of a thread. Sums of more are in units of 2^-46, which 2^18 fit in. (With that unit for the
+// weights as well, a quarter million of them a few units each were off by 2^-25 of the total together.)
+// A weight is cut to its unit, so those of 2^-14 of 2^R and more lose nothing; those of 2^-6 and more are
+// whole coarse units: where a share of equal logits is a whole number of them, it is met exactly.
 #pragma once
 
 #include "tq_tcgen05.cuh"
@@ -46,7 +48,9 @@ constexpr ExpTable make_exp_table() {
   return t;
 }
 
-constexpr int kWeightBins = 768;     // 16 to an octave, 47 octaves and a little
+constexpr int kWeightBins = 896;     // 16 to an octave, 54 octaves and more
+constexpr int kOctaves = 54;         // a weight below 2^R by more is less than a unit
+constexpr int kCoarse = 8;           // a coarse unit is 2^8 units
 
 struct Weigher {
   float c_hi, c_lo;    // log2(e) / T
@@ -75,7 +79,7 @@ struct Weigher {
     // (one step more for what c_lo adds)
     const float r = far ? 1.0f : ceilf(p * 2048.0f) * (1.0f / 2048.0f) + (1.0f + 1.0f / 2048.0f);
     k = 6144.0f - r;
-    least = fminf(far ? top - 46.0f * octave : (r - 47.0f) * octave, top);
+    least = fminf(far ? top - (kOctaves - 1) * octave : (r - kOctaves) * octave, top);
   }
   // The same with whole octaves: sums relative to other logits' are shifts
   // apart. Returns R; not for logits whose exponent passes 2000.
@@ -87,7 +91,7 @@ struct Weigher {
     least = -INFINITY;
     return (int)r;
   }
-  // ln(w / total) for the weight of l and a sum in units of 2^-46 of 2^(6144 - k).
+  // ln(w / total) for the weight of l and a sum in coarse units, 2^-46 of 2^(6144 - k).
   __device__ __forceinline__ float log_share(float l, uint64_t total) const {
     const float x = __fsub_rn(l, shift), p = __fmul_rn(x, c_hi);
     const float rest = __fmaf_rn(x, c_lo, __fmaf_rn(x, c_hi, -p));       // x c - p
@@ -140,13 +144,13 @@ struct Weigher {
       finish(t1, low.y, bits[i + 1], w[i + 1], lead ? lead + i + 1 : nullptr);
     }
   }
-  // T[j] as a 24-bit integer with what is to be added: about 2^40 .. 2^41, then 2^6 times that, cut to
+  // T[j] as a 24-bit integer with what is to be added: about 2^40 .. 2^41, then 2^14 times that, cut to
   // its place.
   static __device__ __forceinline__ void finish(float t, float low, int bits, uint64_t& w, uint32_t* lead) {
     const uint32_t mant = (__float_as_uint(t) & 0x7fffffu) | 0x800000u;
-    const uint64_t v = ((uint64_t)mant << 23) + (int64_t)__float2int_rn(low) * 64;
-    if (lead) *lead = (uint32_t)(v >> 34);
-    w = (v >> ((kMagic >> 11) - (bits >> 11))) | 1u;
+    const uint64_t v = ((uint64_t)mant << 31) + (int64_t)__float2int_rn(low) * 16384;
+    if (lead) *lead = (uint32_t)(v >> 42);
+    w = v >> ((kMagic >> 11) - (bits >> 11));
   }
   __device__ __forceinline__ uint64_t one(float l) const {
     const float two[2] = {l, l};

@@ -638,10 +638,10 @@ int64_t tq_lora_add_workspace_bytes(int64_t ntok, int64_t adapters);
  * count as that. A row with a NaN or without any logit above minus infinity, or
  * whose temperature is negative or not finite, gets token -1 and a NaN as logp.
  * A temperature above 2^100 counts as that.
- * Weights are integers in units of 2^-43 of the largest or less, each good to
- * 2^-35 of its value and a unit, in 64-bit sums: these do not depend on their order, and
- * a border between two tokens is where the exact sums have it but for 2^-34 of
- * the total.
+ * Weights are integers, each good to 2^-35 of its value and 2^-52 of the largest,
+ * in 64-bit sums: these do not depend on their order, and a border between two
+ * tokens is where the exact sums have it but for 2^-32 of the total, however many
+ * light tokens there are.
  * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS.
  */
 int tq_sample(const void *logits, int64_t stride, int type, int64_t ntok, int64_t vocab,

@@ -319,3 +319,65 @@ def test_shapes_refused(tq):
         assert e.value.code == code
     with pytest.raises(ValueError):
         tq.tq_sample(torch.zeros(3, 20, device="cuda")[:, ::2], u, tokens)
+
+
+def span(l, u, t, k, p, m, delta):
+    """The lowest and the highest token of a row's draw in 64 bits, if the borders of the nucleus and of the
+    draw lie up to delta of the total beside the exact ones."""
+    l = l.double().cpu().numpy()
+    w = np.exp((l - l.max()) / t)
+    order = np.argsort(-l, kind="stable")
+    nk = k if 0 < k < len(l) else len(l)
+    cum = np.cumsum(w[order][:nk])
+    found = []
+    for near in (-delta, 0.0, delta):
+        n = min(nk, int((cum < (p + near) * cum[-1]).sum()) + 1) if p < 1 else nk
+        if m > 0:
+            n = min(n, int((w >= m).sum()))
+        kept = np.zeros(len(l), bool)
+        kept[order[:max(n, 1)]] = True
+        c = np.cumsum(np.where(kept, w, 0.0))
+        for close in (-delta, 0.0, delta):
+            at = int((c <= max(u + close, 0.0) * c[-1]).sum())
+            found.append(min(at, int(np.nonzero(kept)[0][-1])))
+    return min(found) - 1, max(found) + 1
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("vocab", [262144, 70001])
+def test_light_tokens_weigh_together(tq, rows, vocab):
+    """A leader and many tokens whose weights are a few units of 2^-45 of its own, or less: what one of them
+    is off by counts that many times. The header's 2^-32 of the total is up to 50,000 of them here."""
+    x = torch.empty(rows, vocab)
+    f = lambda v: float(np.float32(v))   # noqa: E731
+    wrong = []
+    for drop, lead, base, u, k, p, m in [
+            # below the leader; where that is; what both are above; then, as parts of all light tokens' share:
+            # u from 0 on (or from 1 down), top-k, top-p from 1 down; min-p
+            (30.49, -1, 0.0, 0.7, 0.0, 0.0, 1e-14), (32.0, -1, 0.0, 0.6, 0.0, 0.0, 1e-16),
+            (30.49, vocab // 2, 0.0, 0.3, 0.0, 0.0, 1e-14), (22.0, 0, 0.0, -0.2, 0.0, 0.6, 0.0),
+            (21.5, 0, -1.0, -0.3, 0.0, 0.3, 0.0), (28.0, -1, 0.0, 0.4, 0.99, 0.0, 0.0),
+            (26.0, -1, 2.0, 0.2, 0.75, 0.5, 1e-13), (20.0, 5, 0.0, -0.1, 0.0, 0.25, 0.0),
+            (30.5, -1, 9000.0, 0.7, 0.0, 0.0, 1e-14), (30.49, -1, 0.0, 0.7, 0.0, 0.0, 0.0)]:
+        x.fill_(base - drop)
+        x[:, lead] = base
+        share = (vocab - 1) * math.exp(-drop)
+        u, k, p = f(u * share if u > 0 else 1 + u * share), int(k * vocab), f(1 - p * share)
+        kw = dict(k=[k] * rows, p=[p] * rows, m=[m] * rows) if (k, p, m) != (0, 1.0, 0.0) else {}
+        tokens, _ = draw(tq, x.cuda(), [u] * rows, **kw)
+        lo, hi = span(x[0], u, 1.0, k, p, f(m), 2.0**-32)
+        assert 0 < lo and hi < vocab - 1 and hi - lo < 0.6 * vocab      # (the case says something)
+        wrong += [(drop, lead, u, k, p, m, a, lo, hi) for a in tokens.tolist() if not lo <= a <= hi]
+    assert not wrong, wrong
+
+
+@pytest.mark.parametrize("vocab", [2, 6, 256, 512, 1000, 4096, 262144])
+@pytest.mark.parametrize("value", [0.0, -3.25, 7.7, 5000.0])
+def test_shares_of_equal_logits_are_exact(tq, vocab, value):
+    """A half and a quarter of equal weights are met by just that many of them, whatever a weight is in units:
+    u just below 1 draws the last of them."""
+    x = torch.full((4, vocab), value)
+    x[2:, vocab // 2:] = -INF
+    tokens, _ = draw(tq, x.cuda(), [BELOW_ONE] * 4, p=[0.5, 0.25, 0.5, 0.25])
+    halves = [vocab] * 2 + [vocab // 2] * 2
+    assert tokens.tolist() == [max(1, math.ceil(n * p)) - 1 for n, p in zip(halves, [0.5, 0.25] * 2)]
