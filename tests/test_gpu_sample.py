@@ -381,3 +381,81 @@ def test_shares_of_equal_logits_are_exact(tq, vocab, value):
     tokens, _ = draw(tq, x.cuda(), [BELOW_ONE] * 4, p=[0.5, 0.25, 0.5, 0.25])
     halves = [vocab] * 2 + [vocab // 2] * 2
     assert tokens.tolist() == [max(1, math.ceil(n * p)) - 1 for n, p in zip(halves, [0.5, 0.25] * 2)]
+
+
+def blocks_of(rows, vocab, size):
+    """What the call takes for these sizes: thread blocks a row (twice as many as before while at most 608 are
+    in the call and a block has more than 2048 tokens), and whether their slices stay in shared memory (up to
+    64 KB)."""
+    cluster = 1
+    while cluster < 16 and 2 * rows * cluster <= 608 and vocab > cluster * 2048:
+        cluster *= 2
+    return cluster, ((vocab + cluster - 1) // cluster + 31) // 32 * 32 * size <= 65536
+
+
+def check_rows(tq, x, u, t, k, p, m, rows):
+    """Some rows of a draw of many against the definition; every row's draw is made."""
+    tokens, logp = draw(tq, x, u, t, k, p, m)
+    f = lambda v: float(np.float32(v))   # noqa: E731
+    for i in rows:
+        want = reference(x[i], f(u[i]), f(t[i]), int(k[i]), f(p[i]), f(m[i]))
+        a, got = tokens[i].item(), logp[i].item()
+        assert a in want, (i, a, want, u[i], t[i], k[i], p[i], m[i])
+        assert math.isnan(got) if a == -1 else any(abs(got - v) <= abs(v) * 2.0**-24 + 2.0**-30 for v in want[a]), i
+
+
+@pytest.mark.parametrize("n,vocab,dtype,blocks,pad,offset", [
+    (320, 32771, F32, 1, 5, 0), (320, 40001, F16, 1, 0, 3), (320, 40001, BF16, 1, 6, 1), (305, 16400, F32, 1, 0, 1),
+    (200, 128001, F16, 2, 7, 0), (150, 131073, F32, 4, 2, 2), (76, 140001, F32, 8, 0, 0), (310, 262144, BF16, 1, 0, 0)],
+    ids=str)
+def test_slices_that_stay_in_memory(tq, n, vocab, dtype, blocks, pad, offset):
+    """Rows whose slices are too large for shared memory: filters of their own, at any address."""
+    assert blocks_of(n, vocab, dtype.itemsize) == (blocks, False)
+    stride = vocab + pad
+    flat = torch.full((n * stride + 16,), NAN, dtype=dtype, device="cuda")
+    x = flat.as_strided((n, vocab), (stride, 1), offset)
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x.copy_(torch.randn(n, vocab, generator=g, device="cuda") * 2.5)
+    x[1::7].masked_fill_(torch.rand(x[1::7].shape, generator=g, device="cuda") < 0.9, -INF)
+    x[2, vocab // 2], x[3, 7], x[4] = INF, NAN, -INF
+    r = np.random.RandomState(n)
+    t = r.choice([0.0, 0.3, 0.7, 1.0, 1.5, 8.0], n).tolist()
+    k = r.choice([0, 0, 1, 5, 40, 700, 1000, vocab // 2, vocab], n).tolist()
+    p = r.choice([1.0, 1.0, 1e-6, 0.3, 0.9, 0.999], n).tolist()
+    m = r.choice([0.0, 0.0, 1e-4, 0.05, 0.5, 3.0], n).tolist()
+    check_rows(tq, x, rand_u(n, vocab + 1), t, k, p, m, list(range(14)) + list(range(20, n, max(1, n // 24))))
+    assert torch.isnan(flat[offset + n * stride:]).all()
+
+
+@pytest.mark.parametrize("n,vocab,dtype,blocks", [(320, 32800, F32, 1), (320, 262144, F32, 1), (200, 128001, F16, 2)],
+                         ids=str)
+def test_equal_logits_that_stay_in_memory(tq, n, vocab, dtype, blocks):
+    """One value, two and four in such rows: cuts among equal logits, the sums of all of them."""
+    assert blocks_of(n, vocab, dtype.itemsize) == (blocks, False)
+    x = torch.full((n, vocab), -3.25, dtype=dtype, device="cuda")
+    x[3::6, ::2] = 1.5
+    x[4::6] = (torch.arange(vocab, device="cuda") % 4).to(dtype)
+    x[5::6, 1:] = -12.5
+    t = [1.0, 0.7, 2.0, 1.0, 0.5, 1.0] * n
+    k = [vocab // 2 + 1, 0, vocab - 1, 0, vocab // 3, 0] * n
+    p = [0.5, 0.999, 1.0, 0.25, 0.75, 0.99] * n
+    m = [0.0, 0.5, 0.0, 0.001, 0.0, 1e-9] * n
+    check_rows(tq, x, rand_u(n, 21), t[:n], k[:n], p[:n], m[:n], range(12))
+    check_rows(tq, x, [BELOW_ONE, 0.0] * (n // 2), t[1:n + 1], [0] * n, p[:n], m[2:n + 2], range(n - 12, n))
+    check_rows(tq, x, [0.5] * n, [0.0] * n, [0] * n, [1.0] * n, [0.0] * n, range(6))
+
+
+def test_light_tokens_that_stay_in_memory(tq):
+    """The sums of many light tokens in rows of one thread block each."""
+    n, vocab, drop = 320, 262144, 30.49
+    assert blocks_of(n, vocab, 4) == (1, False)
+    x = torch.full((n, vocab), -drop, device="cuda")
+    x[:, -1] = 0.0
+    share = (vocab - 1) * math.exp(-drop)
+    parts = [0.1, 0.35, 0.7, 0.9]
+    us = [float(np.float32(v * share)) for v in parts] * (n // 4)
+    for m in (1e-14, 0.0):
+        tokens, _ = draw(tq, x, us, m=[m] * n)
+        for j in range(4):
+            lo, hi = span(x[0], us[j], 1.0, 0, 1.0, float(np.float32(m)), 2.0**-32)
+            assert lo <= tokens[j::4].min() and tokens[j::4].max() <= hi, (m, us[j], tokens[j].item(), lo, hi)
