@@ -23,7 +23,9 @@
 // columns 16 bytes further apart than that, so that threads that write neighbouring columns meet no bank
 // twice. x and h are the sum of two tf32 parts, multiplied one after the other into the same accumulator.
 // The first product's columns go to eight accumulators one after the other, which are added in 32 bits: the
-// tensor cores cut their sums, which leans one way over many steps.
+// tensor cores cut their sums, which leans one way over many steps. After 16 chunks of 32 columns in each (16384
+// columns of the matrix) they are read and begun again. (2^20 columns of one sign, divided among the eight
+// however many there are, were 4.0e-4 off; now 6.0e-6.)
 //
 // A warp takes its 32 tokens' sums of 32 rows from tensor memory, a token a lane, and turns them through
 // shared memory into rows of 128 bytes of four tokens at a time, as it has loaded them of Z a tile ahead and
@@ -53,7 +55,9 @@ constexpr int kStages = 3;                 // of 32 columns of x and A in shared
 constexpr int kRows = 128;                 // rows of Y of a tile of the second product
 constexpr int kColumn = kM * 16 + 16;      // bytes of a 16-byte column of 128 rows
 constexpr int kAhead = 4;                  // chunks of 32 columns of x and A under way
-constexpr int kAccs = 8;                   // accumulators of the first product: 64 columns of TMEM each
+constexpr int kAccs = 8;                   // accumulators of the first product: 64 columns of TMEM each,
+constexpr int kChain = 16;                 // chunks that one of them sums up at most,
+constexpr int kRound = kAccs * kChain;     // and all of them until they are read
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
@@ -70,6 +74,7 @@ constexpr int kPart = std::max(kM * kPartPitch * 4, kTurn);    // (the parts of 
 constexpr int kSlice = kM / kCluster * kPartPitch * 4;
 constexpr int kSmem = kHead + kUnion + kPart + kSlice;
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+static_assert(kRound % kAhead == 0, "rounds of whole turns");
 
 // kind::tf32: D f32, A and B tf32 (format 2), both K-major.
 __device__ __forceinline__ uint32_t idesc_tf32(int m, int n) {
@@ -183,9 +188,10 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
         wait(stalled ? never : full + stage, stalled ? 0 : phase);
         tc::tc_fence_after();
         const uint32_t xs = base + stage * (kXStage + kWStage), ws = xs + kXStage;
-        const int acc = k * kAccs / max(nk, kAccs);
+        const int in_round = k % kRound, round = max(min(nk - (k - in_round), kRound), kAccs);
+        const int acc = in_round * kAccs / round;
         const uint32_t d = tmem + acc * N;
-        const bool fresh = k == 0 || (k - 1) * kAccs / max(nk, kAccs) != acc;
+        const bool fresh = in_round == 0 || (in_round - 1) * kAccs / round != acc;
         if (!failed) {
 #pragma unroll
           for (int h = 0; h < (kSplit ? 2 : 1); ++h)
@@ -251,50 +257,86 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   };
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load(u, xv[u], wv[u]);
+  // The accumulators of the products of `upto` chunks, and of the rounds before, as this block's part of h: a
+  // warp's 32 tokens, a token a lane.
+  const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  auto read_accs = [&](int upto) {
+    // the last products are done, and with them those before
+    if (upto > 0) wait(read + (upto - 1) % kStages, ((upto - 1) / kStages) & 1);
+    failed = __any_sync(0xffffffffu, failed);        // (tcgen05.ld takes a whole warp)
+    tc::tc_fence_after();
+    const int accs = upto > 0 ? min((upto - 1) % kRound + 1, kAccs) : 0;
+#pragma unroll 1
+    for (int g = half; g < N / 16; g += 2) {
+      float* const to = part + row * kPartPitch + g * 16;
+      float sum[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[e] = upto > kRound ? to[e] : 0.0f;
+      if (!failed)
+#pragma unroll 1
+        for (int a = 0; a < accs; ++a) {
+          uint32_t v[16];
+          tc::tmem_ld16_nowait(tmem + lanes + a * N + g * 16, v);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
+        }
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(to + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+    }
+    tc::tc_fence_before();
+  };
   int stage = 0;
   uint32_t phase = 1;           // of the last reading of a stage: none yet
 #pragma unroll 1
-  for (int k0 = 0; k0 < nk; k0 += kAhead) {
+  for (int r0 = 0; r0 < nk; r0 += kRound) {
+    if (r0 > 0) read_accs(r0);       // (what is handed over next says that it is done)
+    const int r1 = min(nk, r0 + kRound);
+#pragma unroll 1
+    for (int k0 = r0; k0 < r1; k0 += kAhead) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int k = k0 + u;
-      if (k >= nk) break;
-      const uint32_t xs = base + stage * (kXStage + kWStage), ws = xs + kXStage;
-      if (k >= kStages) wait(read + stage, phase);
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u;
+        if (k >= nk) break;
+        const uint32_t xs = base + stage * (kXStage + kWStage), ws = xs + kXStage;
+        if (k >= kStages) wait(read + stage, phase);
 #pragma unroll
-      for (int i = 0; i < kXPieces; ++i) {
-        const uint32_t at = xs + (xr + i * kRowsAtOnce) * 16;
-        if constexpr (kSplit) {
-          uint4 hi, lo;
-          split4(xv[u][i], hi, lo);
-          put16(at + xc * kColumn, hi);
-          put16(at + (8 + xc) * kColumn, lo);
-        } else {
-          const uint4 v = xv[u][i];
-          uint4 a, b;
-          widen<TX>(v.x, a.x, a.y);
-          widen<TX>(v.y, a.z, a.w);
-          widen<TX>(v.z, b.x, b.y);
-          widen<TX>(v.w, b.z, b.w);
-          put16(at + 2 * xc * kColumn, a);
-          put16(at + (2 * xc + 1) * kColumn, b);
+        for (int i = 0; i < kXPieces; ++i) {
+          const uint32_t at = xs + (xr + i * kRowsAtOnce) * 16;
+          if constexpr (kSplit) {
+            uint4 hi, lo;
+            split4(xv[u][i], hi, lo);
+            put16(at + xc * kColumn, hi);
+            put16(at + (8 + xc) * kColumn, lo);
+          } else {
+            const uint4 v = xv[u][i];
+            uint4 a, b;
+            widen<TX>(v.x, a.x, a.y);
+            widen<TX>(v.y, a.z, a.w);
+            widen<TX>(v.z, b.x, b.y);
+            widen<TX>(v.w, b.z, b.w);
+            put16(at + 2 * xc * kColumn, a);
+            put16(at + (2 * xc + 1) * kColumn, b);
+          }
         }
-      }
-      if (wr < N) {
-        const uint4 v = wv[u];
-        uint4 a, b;
-        widen<TW>(v.x, a.x, a.y);
-        widen<TW>(v.y, a.z, a.w);
-        widen<TW>(v.z, b.x, b.y);
-        widen<TW>(v.w, b.z, b.w);
-        put16(ws + 2 * wt * kWColumn + wr * 16, a);
-        put16(ws + (2 * wt + 1) * kWColumn + wr * 16, b);
-      }
-      load(k + kAhead, xv[u], wv[u]);
-      hand_over(full + stage);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
+        if (wr < N) {
+          const uint4 v = wv[u];
+          uint4 a, b;
+          widen<TW>(v.x, a.x, a.y);
+          widen<TW>(v.y, a.z, a.w);
+          widen<TW>(v.z, b.x, b.y);
+          widen<TW>(v.w, b.z, b.w);
+          put16(ws + 2 * wt * kWColumn + wr * 16, a);
+          put16(ws + (2 * wt + 1) * kWColumn + wr * 16, b);
+        }
+        load(k + kAhead, xv[u], wv[u]);
+        hand_over(full + stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
   }
@@ -328,7 +370,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   };
   // A warp's tokens and half of a tile's rows of Y. Pieces of 16 bytes: of 32 rows a token has 8 (or 4, of
   // 16-bit types), neighbouring lanes'; a lane's pieces are of every fourth (eighth) token.
-  const int first = (warp & 3) * 32, half = warp >> 2, row = first + lane;
+  const int first = (warp & 3) * 32;
   const bool f32 = p.y_type == TQ_F32;
   const int bytes = f32 ? 4 : 2, in_row = f32 ? lane & 7 : lane & 3, of_token = f32 ? lane >> 3 : lane >> 2;
   const int step = f32 ? 4 : 8, turns = f32 ? 8 : 4, values = 16 / bytes;
@@ -360,30 +402,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   load_z(0, 1, zv[1]);
 
   // ---- this block's part of h
-  // the last products are done, and with them those before
-  if (nk > 0) wait(read + (nk - 1) % kStages, ((nk - 1) / kStages) & 1);
-  failed = __any_sync(0xffffffffu, failed);        // (tcgen05.ld takes a whole warp)
-  tc::tc_fence_after();
-  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-  for (int g = half; g < N / 16; g += 2) {
-    float sum[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
-    if (!failed)
-#pragma unroll 1
-      for (int a = 0; a < min(nk, kAccs); ++a) {
-        uint32_t v[16];
-        tc::tmem_ld16_nowait(tmem + lanes + a * N + g * 16, v);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
-      }
-#pragma unroll
-    for (int e = 0; e < 16; e += 4)
-      *reinterpret_cast<float4*>(part + row * kPartPitch + g * 16 + e) =
-          make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-  }
-  tc::tc_fence_before();
+  read_accs(nk);
   // ---- of the whole: a quarter of the tokens summed by each block, then all of them taken
   cluster_arrive();
   cluster_wait();

@@ -600,7 +600,8 @@ typedef struct {
  * A token whose adapter, or its rank, is out of range gets Z alone, and
  * tq_device_status() then returns TQ_ERR_INDEX.
  * Products are good to 2^-21 of their value whatever the types, sums are
- * 32-bit floats, and Y is rounded once.
+ * 32-bit floats, joined from sums of at most 512 terms that the tensor cores
+ * cut, and Y is rounded once.
  * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
  * TQ_ERR_WORKSPACE.
  */

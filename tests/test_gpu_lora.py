@@ -482,3 +482,28 @@ def test_timeout_reported_then_cleared(tq, shape):
     assert t < 0.8 and tq.tq_device_status() == tq.TQ_OK
     assert ((got != want).any(dim=1).sum() <= 128)      # the tokens of one tile
     assert torch.equal(run(tq, d), want)
+
+
+@pytest.mark.parametrize("ntok", [4096, 300])
+def test_many_columns_of_one_sign(tq, ntok):
+    """Sums on the tensor cores are cut, which leans one way: they may not grow with the columns. 2^20 columns of
+    positive values, far more than any chain of them."""
+    cols, rows, top = 1 << 20, 8, 40
+    g = torch.Generator(device="cuda").manual_seed(ntok)
+    x = torch.rand(ntok, cols, generator=g, device="cuda")
+    a = (torch.rand(1, top, cols, generator=g, device="cuda") + 0.5).to(BF16)
+    b = torch.zeros(1, rows, top, device="cuda", dtype=BF16)
+    pick = torch.arange(rows) * 5
+    b[0, torch.arange(rows), pick] = 1.0                       # Y's rows are values of h
+    y = torch.empty(ntok, rows, device="cuda")
+    tq.tq_lora_add(x, tq.Lora(a, b), torch.zeros(ntok, dtype=I32, device="cuda"), y, None, scratch(tq, ntok, 1))
+    at = torch.arange(0, ntok, ntok // 48, device="cuda")
+    want = x[at].double() @ a[0, pick.cuda()].double().T
+    # A step on the tensor cores adds eight products to a sum, each of the nine cut by less than a unit of 2^-23
+    # of it, and a chain of 128 steps (16 chunks, four steps of both parts) grows evenly, so half of that on
+    # average: 128 / 2 * 9 * 2^-23. These are joined by at most 64 * 8 + 4 additions, growing too: 258 * 2^-24.
+    # Products: 2^-21.
+    bound = 64 * 9 * 2.0**-23 + 258 * 2.0**-24 + 2.0**-21
+    worst = ((y[at].double() - want).abs() / want).max().item()
+    print("off by", worst)
+    assert worst <= bound, (worst, bound)
