@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "tq_lora.cuh"
+#include "tq_tcgen05.cuh"
 
 namespace tq {
 namespace {
@@ -420,7 +421,9 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
     for (int j = 0; j < NT; ++j) {
       float* const to = place + g * kBlock + 8 * j + 2 * t;
       if (kPacked) {
-        *reinterpret_cast<float2*>(to) = make_float2(sum[j][0] + sum[j][2], sum[j][1] + sum[j][3]);
+        // (16-bit activations have no second part: its sums are zeros, or NaN of infinite weights)
+        *reinterpret_cast<float2*>(to) = kSplit ? make_float2(sum[j][0] + sum[j][2], sum[j][1] + sum[j][3])
+                                                : make_float2(sum[j][0], sum[j][1]);
         *reinterpret_cast<float2*>(to + 8 * kBlock) = make_float2(0.0f, 0.0f);
       } else {
         *reinterpret_cast<float2*>(to) = make_float2(sum[j][0], sum[j][1]);
@@ -584,6 +587,15 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
         h[3] += v[c].w;
       }
       const int mb = j >> 4, half = (j >> 3) & 1, l = (j & 7) * 4 + (q & 3);
+      const float sum = (h[0] + h[1]) + (h[2] + h[3]);      // (NaN if one of them is)
+      if (kSplit && sum != sum && j < count) {
+        const float4 again = dots_again(make_float4(h[0], h[1], h[2], h[3]), static_cast<const TX*>(p.x) + s_tok[j] * p.x_stride,
+                                        A, p.l.a_row_stride, 4 * q, rank, cols);
+        h[0] = again.x;
+        h[1] = again.y;
+        h[2] = again.z;
+        h[3] = again.w;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int step = 2 * (q >> 2) + (e >> 1);
@@ -647,8 +659,40 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
     if (kPacked) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[i][0] += acc[i][2];
-        acc[i][1] += acc[i][3];
+        acc[i][0] = joined(acc[i][0], acc[i][2]);
+        acc[i][1] = joined(acc[i][1], acc[i][3]);
+      }
+    } else {
+      // A NaN among this thread's sums (or infinities of both signs) is one in their sum.
+      uint64_t some[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) some[h] = tc::f2_add(some[h], tc::f2_packf(acc[i][2 * h], acc[i][2 * h + 1]));
+      const float2 two = tc::f2_unpack(tc::f2_add(some[0], some[1]));
+      const float all = two.x + two.y;
+      if (__any_sync(0xffffffffu, all != all)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pitched[(8 * h + g) * kPitch + 8 * t + e] = acc[e >> 1][2 * h + (e & 1)];
+        __syncwarp();
+        // a row of B a lane, one token after the other
+#pragma unroll 1
+        for (int j = 16 * m; n0 + lane < rows && j < min(count, 16 * m + 16); ++j) {
+          float& y = pitched[(j - 16 * m) * kPitch + lane];
+          if (y == y) continue;
+          y = row_again(reinterpret_cast<const float*>(hi), reinterpret_cast<const float*>(lo), [&](int r) {
+            const int step = 2 * (r >> 4) + ((r >> 1) & 1), l = (j & 7) * 4 + ((r >> 2) & 3);
+            return ((step * mblocks + (j >> 4)) * 32 + l) * 4 + ((j >> 3) & 1) + 2 * (r & 1);
+          }, B + (n0 + lane) * p.l.b_row_stride, rank);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e >> 1][2 * h + (e & 1)] = pitched[(8 * h + g) * kPitch + 8 * t + e];
+        __syncwarp();
       }
     }
     if (vec && n0 + 32 <= rows) {

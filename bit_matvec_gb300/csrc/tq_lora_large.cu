@@ -21,7 +21,8 @@
 // Products are tcgen05 kind::tf32 with 128 tokens as rows of A, operands in shared memory without a
 // swizzle: 16-byte columns (four values of the contraction index), 128 rows of each one after another,
 // columns 16 bytes further apart than that, so that threads that write neighbouring columns meet no bank
-// twice. x and h are the sum of two tf32 parts, multiplied one after the other into the same accumulator.
+// twice. x and h are the sum of two tf32 parts, those of x multiplied one after the other into the same accumulator,
+// those of h into two that are added by the threads (tq_lora.cuh: infinite weights).
 // The first product's columns go to eight accumulators one after the other, which are added in 32 bits: the
 // tensor cores cut their sums, which leans one way over many steps. After 16 chunks of 32 columns in each (16384
 // columns of the matrix) they are read and begun again. (2^20 columns of one sign, divided among the eight
@@ -65,7 +66,8 @@ constexpr int kXStage = 2 * 8 * kColumn;                   // both parts of 32 c
 constexpr int kWStage = 8 * (N * 16 + 16);             // 32 columns of A
 constexpr int kHBytes = 2 * (N / 4) * kColumn;         // both parts of h
 constexpr int kBBytes = (N / 4) * kColumn;             // 128 rows of B
-constexpr int kHead = 1024;
+constexpr int kOffsets = 1024;                         // bytes from Y and Z to the tokens' rows
+constexpr int kHead = kOffsets + 2 * kM * 8;
 constexpr int kUnion = std::max(kStages * (kXStage + kWStage), kHBytes + 2 * kBBytes);
 constexpr int kPartPitch = N + 4;                      // floats
 constexpr int kTurnPitch = 36;                             // floats of a token's 32 sums on their way to rows
@@ -98,6 +100,14 @@ __device__ __forceinline__ void split4(const uint4& v, uint4& hi, uint4& lo) {
   split(__uint_as_float(v.w), hi.w, lo.w);
 }
 
+// Loads from tensor memory are over; their values are named, so that none is used before.
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
+
 template <typename TX, typename TW>
 __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_constant__ LoraArgs p) {
   constexpr bool kSplit = sizeof(TX) == 4;
@@ -112,6 +122,8 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   uint64_t* const done = b_full + 2;                                  // [2]
   uint64_t* const never = done + 2;          // test facility: nothing arrives here
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 640);
+  int64_t* const s_y = reinterpret_cast<int64_t*>(smem + kOffsets);   // [kM], -1: no such token
+  int64_t* const s_z = s_y + kM;                                      // [kM]
   const uint32_t base = smem_u32(smem + kHead);
   float* const part = reinterpret_cast<float*>(smem + kHead + kUnion);
   float* const slice = reinterpret_cast<float*>(smem + kHead + kUnion + kPart);
@@ -125,7 +137,13 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   if (want >= ntiles) return;
   const int count = tile.w, rank = min(N, max(0, tile.y - p.rank_from));
   if (p.rank_from > 0 && rank == 0) return;
-  if (tid < count) s_tok[tid] = p.order[tile.z + tid];
+  const int bytes = p.y_type == TQ_F32 ? 4 : 2;
+  if (tid < kM) {
+    const int64_t token = tid < count ? p.order[tile.z + tid] : 0;
+    s_tok[tid] = (int)token;
+    s_y[tid] = tid < count ? token * p.y_stride * bytes : -1;
+    s_z[tid] = tid < count ? token * p.z_stride * bytes : -1;
+  }
   // rows of B and Y of this thread block, from a multiple of 32 on
   const int rows = (int)p.l.rows, units = (rows + 31) / 32, share = (int)crank;
   const int begin = (int)((int64_t)units * share / kCluster) * 32;
@@ -219,14 +237,14 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
       for (int i = 0; i < tiles; ++i) {
         wait(stalled ? never : b_full + (i & 1), stalled ? 0 : (i >> 1) & 1);
         tc::tc_fence_after();
-        const uint32_t d = tmem + (i & 1) * kRows, b = bs + (i & 1) * kBBytes;
+        const uint32_t d = tmem + (i & 1) * 2 * kRows, b = bs + (i & 1) * kBBytes;
         if (!failed) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int kk = 0; kk < N / 8; ++kk)
-              mma_tf32_ss(d, tc::smem_desc(hs + (h * kQuads + 2 * kk) * kColumn, kColumn, 128),
-                          tc::smem_desc(b + 2 * kk * kColumn, kColumn, 128), idesc2, h == 0 && kk == 0 ? 0u : 1u);
+              mma_tf32_ss(d + h * kRows, tc::smem_desc(hs + (h * kQuads + 2 * kk) * kColumn, kColumn, 128),
+                          tc::smem_desc(b + 2 * kk * kColumn, kColumn, 128), idesc2, kk == 0 ? 0u : 1u);
         }
         tc::mma_commit(smem_u32(done + (i & 1)));
       }
@@ -278,7 +296,7 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
         for (int a = 0; a < accs; ++a) {
           uint32_t v[16];
           tc::tmem_ld16_nowait(tmem + lanes + a * N + g * 16, v);
-          tc::tmem_wait_ld();
+          wait_loads(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
         }
@@ -372,17 +390,8 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
   // 16-bit types), neighbouring lanes'; a lane's pieces are of every fourth (eighth) token.
   const int first = (warp & 3) * 32;
   const bool f32 = p.y_type == TQ_F32;
-  const int bytes = f32 ? 4 : 2, in_row = f32 ? lane & 7 : lane & 3, of_token = f32 ? lane >> 3 : lane >> 2;
+  const int in_row = f32 ? lane & 7 : lane & 3, of_token = f32 ? lane >> 3 : lane >> 2;
   const int step = f32 ? 4 : 8, turns = f32 ? 8 : 4, values = 16 / bytes;
-  int64_t at_z[8], at_y[8];        // bytes from Z and Y to the pieces' first row; -1: no such token
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = first + of_token + i * step;
-    const bool have = i < turns && j < count;
-    const int64_t token = have ? s_tok[j] : 0, n = begin + half * 64 + in_row * values;
-    at_z[i] = have ? (token * p.z_stride + n) * bytes : -1;
-    at_y[i] = have ? (token * p.y_stride + n) * bytes : -1;
-  }
   const char* const Z = static_cast<const char*>(p.z);
   char* const Y = static_cast<char*>(p.y);
   uint4 zv[2][8];
@@ -392,10 +401,14 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
     for (int i = 0; i < 8; ++i) zv[g][i] = make_uint4(0, 0, 0, 0);
   // of 32 rows: g of the two of this warp's half, in the tile that starts `ahead` rows from begin
   auto load_z = [&](int ahead, int g, uint4 (&z)[8]) {
-    if (!Z || begin + ahead + half * 64 + g * 32 + in_row * values >= end) return;
+    const int64_t n = begin + ahead + half * 64 + g * 32 + in_row * values;
+    if (!Z || n >= end) return;
+    const char* const from = Z + n * bytes;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (at_z[i] >= 0) z[i] = *reinterpret_cast<const uint4*>(Z + at_z[i] + (ahead + g * 32) * bytes);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = i < turns ? s_z[first + of_token + i * step] : -1;
+      if (at >= 0) z[i] = *reinterpret_cast<const uint4*>(from + at);
+    }
   };
   load_b(begin);
   load_z(0, 0, zv[0]);
@@ -421,6 +434,12 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
       h.z += v[c].z;
       h.w += v[c].w;
     }
+    const int of = (int)crank * (kM / kCluster) + j;      // among the tile's tokens
+    const float sum = (h.x + h.y) + (h.z + h.w);            // (NaN if one of them is)
+    if (kSplit && sum != sum && of < count)
+      h = dots_again(h, static_cast<const TX*>(p.x) + s_tok[of] * p.x_stride,
+                     static_cast<const TW*>(p.l.a) + tile.x * p.l.a_stride + p.rank_from * p.l.a_row_stride,
+                     p.l.a_row_stride, 4 * q, rank, cols);
     *reinterpret_cast<float4*>(slice + j * kPartPitch + 4 * q) =
         make_float4(h.x * scale, h.y * scale, h.z * scale, h.w * scale);
   }
@@ -471,21 +490,34 @@ __global__ void __launch_bounds__(kAll, 1) lora_large_kernel(const __grid_consta
     float* const turn = part + warp * 32 * kTurnPitch;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      uint32_t acc[32];
-      if (!failed) tc::tmem_ld32(tmem + lanes + (i & 1) * kRows + half * 64 + g * 32, acc);
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        *reinterpret_cast<uint4*>(turn + lane * kTurnPitch + e) = make_uint4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-      __syncwarp();
+      for (int c = 0; c < 32; c += 16) {
+        uint32_t hi[16], lo[16];
+        const uint32_t at = tmem + lanes + (i & 1) * 2 * kRows + half * 64 + g * 32 + c;
+        if (!failed) {
+          tc::tmem_ld16_nowait(at, hi);
+          tc::tmem_ld16_nowait(at + kRows, lo);
+          wait_loads(hi);
+          wait_loads(lo);
+        }
+        auto sum = [&](int e) { return joined(__uint_as_float(hi[e]), __uint_as_float(lo[e])); };
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(turn + lane * kTurnPitch + c + e) =
+              make_float4(sum(e), sum(e + 1), sum(e + 2), sum(e + 3));
+      }
       const int ahead = i * kRows;
-      if (!failed && begin + ahead + half * 64 + g * 32 + in_row * values < end) {
+      __syncwarp();
+      const int64_t n = begin + ahead + half * 64 + g * 32 + in_row * values;
+      if (!failed && n < end) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          if (at_y[u] < 0) continue;
+          const int64_t at = u < turns ? s_y[first + of_token + u * step] : -1;
+          if (at < 0) continue;
           const float* const from = turn + (of_token + u * step) * kTurnPitch + in_row * values;
           const float4 a = *reinterpret_cast<const float4*>(from);
           const uint4 z = zv[g][u];
-          uint4* const to = reinterpret_cast<uint4*>(Y + at_y[u] + (ahead + g * 32) * bytes);
+          uint4* const to = reinterpret_cast<uint4*>(Y + n * bytes + at);
           if (f32) {
             *to = make_uint4(__float_as_uint(a.x + __uint_as_float(z.x)), __float_as_uint(a.y + __uint_as_float(z.y)),
                              __float_as_uint(a.z + __uint_as_float(z.z)), __float_as_uint(a.w + __uint_as_float(z.w)));

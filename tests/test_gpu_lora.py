@@ -8,6 +8,7 @@ import torch
 pytestmark = pytest.mark.gpu
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 I32 = torch.int32
+INF = float("inf")
 
 
 @pytest.fixture(scope="module")
@@ -507,3 +508,34 @@ def test_many_columns_of_one_sign(tq, ntok):
     worst = ((y[at].double() - want).abs() / want).max().item()
     print("off by", worst)
     assert worst <= bound, (worst, bound)
+
+
+@pytest.mark.parametrize("types", [(F32, BF16, F32), (F32, F16, F32), (BF16, BF16, F32), (F32, BF16, BF16)], ids=str)
+@pytest.mark.parametrize("ntok,top,rows", [(5, 5, 31), (9, 40, 136), (40, 16, 136), (40, 64, 31), (300, 20, 136),
+                                           (300, 100, 33), (5000, 40, 136), (4200, 130, 136)])
+def test_infinite_weights(tq, ntok, top, rows, types):
+    """What the formula gives: infinity, and NaN where zero meets it or two of them. Small integers, whose
+    second part is zero in every split, also beside each infinity."""
+    xt, wt, yt = types
+    g = torch.Generator().manual_seed(ntok + top)
+    cols = 72
+
+    def ints(hi, *shape):
+        return torch.randint(-hi, hi + 1, shape, generator=g).float()
+    a, b = ints(2, 3, top, cols), ints(2, 3, rows, top)
+    a[0, 3, 7], a[0, top - 1, 71], b[1, 4, 2], b[1, rows - 1, top - 1] = INF, -INF, -INF, INF
+    a[2, 0, 0], b[2, 5, 1], b[2, 6, 0] = INF, INF, float("nan")
+    d = {"a": a.to(wt).cuda(), "b": b.to(wt).cuda(), "x": ints(3, ntok, cols).to(xt).cuda(),
+         "z": ints(100, ntok, rows).to(yt).cuda(), "ids": torch.randint(-1, 3, (ntok,), generator=g, dtype=I32).cuda(),
+         "rank": torch.full((3,), top, dtype=I32).cuda(), "scale": torch.tensor([1.0, 2.0, -1.0]).cuda()}
+    d["x"][::5, 3] = INF
+    want = d["z"].double()
+    for i in range(3):
+        at = (d["ids"] == i).nonzero()[:, 0]
+        for t in at.split(256):      # (products term by term: no library's way with infinities)
+            h = (d["x"][t].double()[:, None] * d["a"][i].double()).sum(2) * d["scale"][i].double()
+            want[t] += (h[:, None] * d["b"][i].double()).sum(2)
+    got, want = run(tq, d), want.to(yt)
+    assert torch.isnan(want).any() and torch.isinf(want).any() and torch.isfinite(want).any()
+    wrong = ~((got == want) | (torch.isnan(got) & torch.isnan(want)))
+    assert not wrong.any(), (wrong.sum().item(), got[wrong][:8], want[wrong][:8], wrong.nonzero()[:8])
