@@ -15,17 +15,18 @@
 // so a thread loads consecutive values of a row and feeds them as the pairs
 // (t, t + 4) that the fragment wants.
 //
-// Tiles are of 8 tokens where adapters have no more than that each on average: both parts of a value
-// are rows of one product then. (Tiles of 32 for 256 tokens of 100 adapters, rank 64, 17408 x 5120: 102 us
-// where those of 8 take 69.) Long batches of high rank have a kernel of their own, in
+// Tiles are of 8 tokens where there are no more than that for each slot of an adapter on average, used or not: both
+// parts of a value are rows of one product then. (Tiles of 32 for 256 tokens of 100 adapters, rank 64, 17408 x
+// 5120: 102 us where those of 8 take 69. But 2048 tokens of one adapter in a pool of 256 slots, rank 16, 5120 x 5120,
+// take 78 us, and 49 with a description of that slot alone.) Long batches of high rank have a kernel of their own, in
 // tq_lora_large.cu. A warp's weights come through a ring of asynchronous copies that only it reads, 6 KB
 // under way, so the products wait for no barrier; two thread blocks an SM, 96 KB.
 //
-// What bounds it: one token, 5120 x 5120, rank 16: 8 us of latency (one launch, the token's adapter, A, the
+// What bounds it: one token, 5120 x 5120, rank 16: 7.1 us of latency (one launch, the token's adapter, A, the
 // cluster's sum, B, one after the other). 256 tokens of 100 adapters, ranks 16 to 64: 190 MB in 69 us or
 // 2.8 TB/s: some 740 thread blocks of which 304 run at once, each with the same wait for its tile, its first
-// weights and the cluster. 8192 tokens of 16 adapters, ranks up to 32, 5120 x 17408: 1.3 GB in 327 us or
-// 4 TB/s at 1.5 instructions a cycle, conversions and products of the x and Z that pass.
+// weights and the cluster. 8192 tokens of 16 adapters, ranks up to 32, 5120 x 17408: 1.3 GB in 333 us or
+// 3.9 TB/s at 1.5 instructions a cycle, conversions and products of the x and Z that pass.
 #include <algorithm>
 
 #include "tq_lora.cuh"
@@ -748,7 +749,7 @@ lora_kernel(const __grid_constant__ LoraArgs p) {
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// Tiles of 8 tokens where adapters have no more than that each on average. (A function of the call's
+// Tiles of 8 tokens where slots have no more than that each on average. (A function of the call's
 // sizes alone: so is the order of every sum.)
 int64_t tile_of(int64_t ntok, int64_t adapters) { return ntok <= kSmallTile * adapters ? kSmallTile : kTile; }
 int64_t max_tiles(int64_t ntok, int64_t adapters, int64_t tile) {

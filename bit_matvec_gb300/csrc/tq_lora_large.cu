@@ -4,19 +4,20 @@
 // A cluster of four thread blocks takes a tile: each block a quarter of A's columns for h = A x, the four
 // parts summed through distributed shared memory, then each block a quarter of the rows of Y = Z + B h.
 // With 128 tokens a tile, A and B are read from L2 a quarter as often as with the 32 of tq_lora.cu; what is left
-// for the threads is the traffic itself: x in, Z in, Y out. (Clusters of eight: 273 us where four take 183; the GPU holds 15 of them with a block an SM, and 36
-// of four.)
+// for the threads is the traffic itself: x in, Z in, Y out. (Clusters of eight: 273 us where four took 183; the GPU
+// holds 15 of them with a block an SM, and 36 of four.)
 //
 // Ranks above 64 take several passes of 64 over Y, of 32-bit values: a pass adds to what the one before
 // has stored, which is the same 32-bit sum. (16-bit Y would be rounded twice: such calls take tq_lora.cu.)
 //
-// Taken for ranks above 32, at least 4096 tokens and 512 an adapter; from 2048 tokens on above rank 112, where
-// tq_lora.cu has room for one thread block an SM. us, this kernel and that of tq_lora.cu, f32: matrices of
-// 5120 x 15360, rank 64, 4096 tokens of four adapters 185 and 277, of sixteen 296 and 278; 8192 of sixteen 360
-// and 522; 2048 of one 178 and 149; rank 32, 4096 tokens 163 and 172, ranks of several sizes up to 32 395 and
-// 327; rank 16 149 both. Matrices of 5120 x 5120, 4096 tokens: rank 45 119 and 206, 100 180 and 287, 128 178
-// and 421, 256 339 and 759; 2048 tokens: rank 64 83 and 91, 100 152 and 151, 128 152 and 236; 1024 tokens,
-// rank 128: 143 and 139.
+// Taken for ranks above 32, at least 4096 tokens and 512 an adapter (a slot, used or not); from 2048 tokens on above
+// rank 112, where tq_lora.cu has room for one thread block an SM. us, this kernel and that of tq_lora.cu, f32:
+// matrices of 5120 x 15360, rank 64, 4096 tokens of four adapters 158 and 277, of sixteen 251 and 282; 8192 of
+// sixteen 348 and 530; 2048 of one 143 and 149; 4096 of two, rank 32, 158 and 177, rank 16 159 and 149; 8192 of
+// sixteen, ranks of several sizes up to 32, 17408 rows: 329 and 345. Matrices of 5120 x 5120, 4096 tokens of two:
+// rank 45 106 and 200, 100 165 and 279, 128 165 and 417, 256 311 and 751; 2048 tokens of one: rank 64 76 and 90, 100
+// 143 and 149, 128 143 and 234; 1024 of one, rank 128: 138 and 137. (The limits are from when this kernel took a
+// sixth more: calls of 2048 tokens, or of rank 32, that would be a little faster here still go the other way.)
 //
 // Products are tcgen05 kind::tf32 with 128 tokens as rows of A, operands in shared memory without a
 // swizzle: 16-byte columns (four values of the contraction index), 128 rows of each one after another,
@@ -32,10 +33,12 @@
 // shared memory into rows of 128 bytes of four tokens at a time, as it has loaded them of Z a tile ahead and
 // stores them to Y. (With a token a lane to the end every load and store met 32 lines of the cache.)
 //
-// What bounds it: at 4096 tokens, 5120 columns, 15360 rows, rank 64, f32, 183 us or 3.2 TB/s. The 36 clusters
-// leave eight SMs out; the first product takes a sixth of the time, and the second's tile of 128 x 128 about
-// 8,700 cycles, of which memory would take 5,300: the eight warps' own loads, turns and stores take turns.
-// (Sixteen warps: 229 us, with 96 registers a thread for 168.)
+// What bounds it: at 4096 tokens, 5120 columns, 15360 rows, rank 64, f32, 159 us or 3.7 TB/s. (The offsets of the
+// tokens' rows of Y and Z stand in shared memory: in registers 52 bytes a thread were spilled, loads of Z under way
+// among them, and it took 183 us, 194 with the parts of h summed apart.) The time goes by whole waves of 36
+// clusters: of two adapters these are 33 tiles or so, which leaves some 20 SMs without work; sixteen have about 40
+// tiles, a second wave (251 us). Within a tile the eight warps' own loads, turns and stores take turns; the first
+// product is a fifth of it. (Sixteen warps, with 96 registers a thread for 168: 229 us where eight took 184.)
 #include <algorithm>
 
 #include "tq_lora.cuh"

@@ -21,9 +21,9 @@
 // in which threads add. What a thread, a block of 512 tokens or the list sums up is
 // in units of a weight; where such sums meet they are cut to coarse units.
 //
-// What bounds it: the weights' instructions, 36 a token for a row without filters. 256 rows of 262144
-// take 113 us (2.4 TB/s, 2.4 instructions a cycle), 512 rows of 32768 with filters of their own 63, 64 of
-// 131072 50, where top-p weighs the tokens twice and a row waits for its slowest block. Top-k alone weighs
+// What bounds it: the weights' instructions, 35 a token for a row without filters. 256 rows of 262144
+// take 110 us (2.4 TB/s, 2.4 instructions a cycle), 512 rows of 32768 with filters of their own 58 to 65, 64 of
+// 131072 44 to 55, where top-p weighs the tokens twice and a row waits for its slowest block. Top-k alone weighs
 // only the list: 200 rows of 128001 f16 58 us, in two rounds of thread blocks that each read their slice,
 // wait, read it again and wait. One row of 131072 takes 15 us: five meetings of its sixteen blocks, a sort
 // and the code's way into the caches.
@@ -45,8 +45,9 @@ constexpr int kBlock = 512;                 // tokens of a sum
 constexpr int kMaxBlocks = kMaxVocab / kBlock + 1;
 constexpr int kMaxCluster = 16;
 constexpr int kSlots = 608;                 // thread blocks of a call at most: twice as many as run at once
-                                            // (200 rows of 128001 f16, top-k: 135 us with 304, 73 with 608, 84
-                                            // with 1216; 64 rows of 131072: 51, 48, 80)
+                                            // (200 rows of 128001 f16, top-k: 46 us with 304, 58 with 608, 66
+                                            // with 1216; 64 rows of 131072: 47, 55, 84. Chosen when a block's look
+                                            // through its slice took longer and 200 rows took 135, 73 and 84.)
 constexpr int kMaxResident = 65536;         // bytes of a slice in shared memory
 static_assert(kMaxVocab == 1 << kIndexBits, "an index below a logit's bits");
 static_assert(kBlock == kThreads && kList == 2 * kThreads, "one token, two entries a thread");

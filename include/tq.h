@@ -574,7 +574,7 @@ typedef struct {
     const void *b;         /* device, typed, aligned to its element */
     const int32_t *rank;   /* device, [adapters], 0 .. max_rank; NULL: all max_rank */
     const float *scale;    /* device, [adapters]; NULL: 1 */
-    int64_t adapters;      /* 0 .. 32768 */
+    int64_t adapters;      /* 0 .. 32768 slots */
     int64_t max_rank;      /* 0 .. 256 */
     int64_t rows, cols;    /* cols a multiple of 8; both at most 2^24 */
     int64_t a_stride, a_row_stride;   /* multiples of 8 */
@@ -586,7 +586,11 @@ typedef struct {
 /*
  * tq_lora_add -- the adapters' part of a product of several requests' tokens:
  *   Y[t] = Z[t] + scale[i] * B_i (A_i x[t]),  i = ids[t];  Y[t] = Z[t] if ids[t] < 0.
- * Tokens of one adapter may stand anywhere; its weights are shared by them.
+ * Tokens of one adapter may stand anywhere; its weights are shared by them. How
+ * many tokens share a reading of them goes by ntok / adapters, so a call whose
+ * tokens use few slots of a large pool is faster (up to twice as fast) with a
+ * description that starts at the first of these and ends with the last (ids
+ * count from its start).
  *   X    typed x_type, [ntok][cols] with stride x_stride, 16-byte aligned, a
  *        row's bytes a multiple of 16: TQ_F32, or the adapters' type.
  *   ids  int32 [ntok].
@@ -601,7 +605,8 @@ typedef struct {
  * tq_device_status() then returns TQ_ERR_INDEX.
  * Products are good to 2^-21 of their value whatever the types, sums are
  * 32-bit floats, joined from sums of at most 512 terms that the tensor cores
- * cut, and Y is rounded once.
+ * cut, and Y is rounded once. Infinities, of weights as well, and NaN give what
+ * the formula gives.
  * Errors: TQ_ERR_SHAPE, TQ_ERR_TYPE, TQ_ERR_NULL, TQ_ERR_ALIGN, TQ_ERR_ALIAS,
  * TQ_ERR_WORKSPACE.
  */
